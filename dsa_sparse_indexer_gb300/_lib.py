@@ -17,7 +17,7 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "dsa.h")
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA = 0, 1, 2, 3
 DSA_FLAG_BOUNDS, DSA_FLAG_TIMEOUT = 1, 2
 
-_p, _i, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+_p, _i, _i64, _d = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_double
 
 # Argument types, in the order include/dsa.h declares them.
 SIGNATURES = {
@@ -39,6 +39,12 @@ SIGNATURES = {
     "dsa_fused_norm_rope": ([_p, _p, _p, _p, ctypes.c_float, _p, _i, _i, _p, _p, _p, _p, _i64,
                              _p, _p], _i),
     "dsa_kv_cache_insert": ([_p, _p, _p, _i, _p, _i64, _p, _p], _i),
+    "dsa_rope_table": ([_i, _i, _d, _i, _d, _i, _d, _d, ctypes.c_float, _p, _p], _i),
+    "dsa_rotary_embed": ([_p, _i64, _i64, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _p, _i64,
+                          _i64, _p, _p], _i),
+    "dsa_kv_cache_insert_fp8": ([_p, _p, _p, _i, _p, _p, _i64, _i, _p, _p, _p], _i),
+    "dsa_sparse_mla_decode_fp8": ([_p, _p, _p, _i64, _i, _p, _p, _i, _i, _i, _i, ctypes.c_float,
+                                   _p, _p, _p, _p], _i),
     "dsa_indexer_steps_noalloc": ([_p, _i64, _i, _i, _i, _i, _p, _p, _p, _i, _i, _i, _p, _p, _p,
                                    _p, _p, _p], _i),
 }

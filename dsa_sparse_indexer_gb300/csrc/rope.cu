@@ -1,0 +1,312 @@
+// Rotary positions (sm_103a): tables of cosines and sines, scaled for contexts
+// longer than the trained one, and the rotation of queries, keys or their
+// gradients by such a table.  The table's layout is the one fused_norm_rope
+// reads: per position, rot_dim / 2 cosines, then as many sines.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+#include "common.cuh"
+
+namespace dsa {
+namespace {
+
+// ---- the table ---------------------------------------------------------------
+//
+// Entry (p, i) is the angle p w_i.  A far position's angle loses its fraction
+// of a turn in fp32, and fp64 arithmetic is slow here, so the angle is an
+// integer: w_i / 2 pi as a 64-bit fraction of a turn (rounded once, on the
+// host), p times that modulo 2^64, the whole turns falling off the top.  Its
+// upper 32 bits, as a signed number, are the angle within half a turn to
+// 2^-32 turns, whatever p.  A thread keeps its pair i and steps its phase by
+// whole positions (one 64-bit addition each).
+constexpr int kMaxPairs = 128;
+constexpr int kTableThreads = 256;
+constexpr int kTablePositions = 64;            // positions per block
+
+struct TableArgs {
+  uint64_t step[kMaxPairs];                    // 2^64 w_i / (2 pi)
+  float* table;
+  float amplitude;
+  int max_pos, half, group;                    // group: positions side by side in a block
+};
+
+__global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const TableArgs a) {
+  __shared__ uint64_t step[kMaxPairs];
+  if (threadIdx.x < a.half) step[threadIdx.x] = a.step[threadIdx.x];
+  __syncthreads();
+  const int q = threadIdx.x / a.half, i = threadIdx.x - q * a.half;
+  if (q >= a.group) return;
+  const int end = min(a.max_pos - (int)blockIdx.x * kTablePositions, kTablePositions);
+  const int64_t p0 = (int64_t)blockIdx.x * kTablePositions;
+  uint64_t phase = step[i] * (uint64_t)(p0 + q);
+  const uint64_t stride = step[i] * (uint64_t)a.group;
+  float* row = a.table + (p0 + q) * (2 * a.half) + i;
+  for (int p = q; p < end; p += a.group) {
+    float s, c;
+    sincospif((float)(int32_t)(uint32_t)(phase >> 32) * 0x1p-31f, &s, &c);
+    row[0] = c * a.amplitude;
+    row[a.half] = s * a.amplitude;
+    row += (int64_t)a.group * (2 * a.half);
+    phase += stride;
+  }
+}
+
+// ---- the rotation --------------------------------------------------------------
+//
+// A row is one head of one token: D values, of which [first, first + rot) turn
+// in pairs and the rest is carried.  Memory-bound: 16-byte accesses wherever
+// the layout allows them.  A unit is what one thread takes of a row: a vector
+// (interleaved pairs lie within it), or the two vectors at i and i + rot / 2 of
+// the half layout.  A thread takes the same unit of kRows consecutive rows:
+// their loads are all in flight at once, and heads of one token share one read
+// of the table.
+
+enum { kInterleaved = DSA_ROPE_INTERLEAVED, kHalf = DSA_ROPE_HALF };
+constexpr int kMaxWidth = 1024;               // values of a row
+
+struct RotArgs {
+  const void* x;
+  void* out;
+  int64_t x_token, x_head, out_token, out_head;   // strides in elements
+  const int32_t* positions;
+  const float* table;
+  uint32_t* flags;
+  int max_pos, rot, first, D, T, H;
+  int units, turning;       // units of a row (the rotating ones first)
+  int per_block;            // groups of rows side by side in a block
+  float sign;               // -1 for the inverse rotation
+  int64_t rows;
+  FastDiv fH;
+};
+
+template <typename E> __device__ __forceinline__ float to_float(E v);
+template <> __device__ __forceinline__ float to_float(float v) { return v; }
+template <> __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename E> __device__ __forceinline__ E from_float(float v);
+template <> __device__ __forceinline__ float from_float(float v) { return v; }
+template <> __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
+
+template <typename E, int V>
+struct alignas(sizeof(E) * V) Vec {
+  E e[V];
+};
+
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float x = a, y = b;
+  a = fmaf(x, c, -y * s);
+  b = fmaf(y, c, x * s);
+}
+
+// V elements per vector: 16 bytes, or 1 where a row's layout has no 16-byte
+// alignment (then an interleaved unit is the two elements of a pair).
+template <typename E, int LAYOUT, int V, int kRows>
+__global__ void __launch_bounds__(V == 1 ? kMaxWidth : 256) rotary_kernel(const RotArgs a) {
+  constexpr int kVecs = LAYOUT == kHalf || V == 1 ? 2 : 1;   // vectors of a rotating unit
+  constexpr int kPairs = kVecs * V / 2;
+  using VecT = Vec<E, V>;
+  const int g = threadIdx.x / a.units, u = threadIdx.x - g * a.units;
+  if (g >= a.per_block) return;
+  const int64_t row0 = ((int64_t)blockIdx.x * a.per_block + g) * kRows;
+  const bool turning = u < a.turning;
+  // Element offsets of the unit's vectors, and its first pair.
+  int at0, at1 = 0, pair = 0;
+  if (turning) {
+    pair = u * kPairs;
+    at0 = a.first + (LAYOUT == kHalf ? pair : 2 * pair);
+    at1 = LAYOUT == kHalf ? at0 + a.rot / 2 : at0 + 1;
+  } else {
+    at0 = (u - a.turning) * V;
+    if (at0 >= a.first) at0 += a.rot;
+  }
+  VecT v[kRows][kVecs];
+  uint32_t tok[kRows], head[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    if (row0 + k >= a.rows) break;
+    tok[k] = fdivmod((uint32_t)(row0 + k), a.fH, &head[k]);
+    const E* src = static_cast<const E*>(a.x) + tok[k] * a.x_token + head[k] * a.x_head;
+    v[k][0] = *reinterpret_cast<const VecT*>(src + at0);
+    if (kVecs == 2 && turning) v[k][kVecs - 1] = *reinterpret_cast<const VecT*>(src + at1);
+  }
+  float c[kPairs], s[kPairs];
+  uint32_t held = ~0u;
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    if (row0 + k >= a.rows) break;
+    if (turning) {
+      if (tok[k] != held) {
+        held = tok[k];
+        const int pos = __ldg(a.positions + held);
+        const bool in = pos >= 0 && pos < a.max_pos;
+        if (!in && u == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);   // identity for this token
+        using VecP = Vec<float, (kPairs > 4 ? 4 : kPairs)>;
+        constexpr int kP = kPairs > 4 ? 4 : kPairs;
+        const float* row = a.table + (int64_t)(in ? pos : 0) * a.rot + pair;
+#pragma unroll
+        for (int j = 0; j < kPairs; j += kP) {
+          const VecP cv = *reinterpret_cast<const VecP*>(row + j);
+          const VecP sv = *reinterpret_cast<const VecP*>(row + a.rot / 2 + j);
+#pragma unroll
+          for (int i = 0; i < kP; ++i) {
+            c[j + i] = in ? cv.e[i] : 1.f;
+            s[j + i] = in ? sv.e[i] * a.sign : 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        E& ea = kVecs == 2 ? v[k][0].e[j] : v[k][0].e[2 * j];
+        E& eb = kVecs == 2 ? v[k][kVecs - 1].e[j] : v[k][0].e[(2 * j + 1) % V];
+        float fa = to_float(ea), fb = to_float(eb);
+        turn(fa, fb, c[j], s[j]);
+        ea = from_float<E>(fa);
+        eb = from_float<E>(fb);
+      }
+    }
+    E* dst = static_cast<E*>(a.out) + tok[k] * a.out_token + head[k] * a.out_head;
+    *reinterpret_cast<VecT*>(dst + at0) = v[k][0];
+    if (kVecs == 2 && turning) *reinterpret_cast<VecT*>(dst + at1) = v[k][kVecs - 1];
+  }
+}
+
+template <typename E, int LAYOUT>
+cudaError_t launch_rotary(RotArgs& a, bool in_place, cudaStream_t stream) {
+  constexpr int V = 16 / (int)sizeof(E);
+  auto lined = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  // 16-byte vectors: both tensors' rows, the turning part's ends (and middle,
+  // in the half layout) and the table's pairs on their boundaries.
+  const bool wide = lined(a.x) && lined(a.out) && lined(a.table) && a.x_token % V == 0 &&
+                    a.x_head % V == 0 && a.out_token % V == 0 && a.out_head % V == 0 &&
+                    a.D % V == 0 && a.first % V == 0 &&
+                    a.rot % (LAYOUT == kHalf ? 2 * V : V) == 0;
+  const int v = wide ? V : 1;
+  const int vecs = LAYOUT == kHalf || !wide ? 2 : 1;
+  a.turning = a.rot / (vecs * v);
+  a.units = a.turning + (in_place ? 0 : (a.D - a.rot) / v);
+  // A block holds whole rows: at most kMaxWidth units (256 when wide).
+  const int threads = a.units > 256 ? (a.units + 31) / 32 * 32 : 256;
+  a.per_block = threads / a.units;
+  auto go = [&](auto kernel, int rows_each) {
+    const int64_t groups = (a.rows + rows_each - 1) / rows_each;
+    const int64_t blocks = (groups + a.per_block - 1) / a.per_block;
+    return launch_kernel(kernel, dim3((unsigned)blocks), dim3((unsigned)threads), 0, stream, 0u,
+                         a);
+  };
+  // Four rows a thread once that still fills the GPU's 152 SMs twice over;
+  // below that the call is latency, and a row a thread spreads it widest.
+  const bool many = a.rows * a.units >= (int64_t)152 * 2 * 256 * 4;
+  if (wide) return many ? go(rotary_kernel<E, LAYOUT, V, 4>, 4) : go(rotary_kernel<E, LAYOUT, V, 1>, 1);
+  return many ? go(rotary_kernel<E, LAYOUT, 1, 4>, 4) : go(rotary_kernel<E, LAYOUT, 1, 1>, 1);
+}
+
+template <typename E>
+cudaError_t launch_rotary(RotArgs& a, int layout, bool in_place, cudaStream_t stream) {
+  return layout == kHalf ? launch_rotary<E, kHalf>(a, in_place, stream)
+                         : launch_rotary<E, kInterleaved>(a, in_place, stream);
+}
+
+}  // namespace
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" dsa_status dsa_rope_table(int max_pos, int rot_dim, double base, int scaling,
+                                     double factor, int orig_max_pos, double beta_fast,
+                                     double beta_slow, float amplitude, float* table,
+                                     cudaStream_t stream) {
+  if (max_pos < 0 || rot_dim < 2 || rot_dim % 2 || !(base > 1.0) || !std::isfinite(base) ||
+      !(factor >= 1.0) || !std::isfinite(factor) || !std::isfinite(amplitude))
+    return DSA_ERR_INVALID_ARG;
+  if (scaling < DSA_ROPE_NONE || scaling > DSA_ROPE_YARN) return DSA_ERR_INVALID_ARG;
+  if (scaling == DSA_ROPE_YARN &&
+      (orig_max_pos < 1 || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) ||
+       !std::isfinite(beta_fast)))
+    return DSA_ERR_INVALID_ARG;
+  if (rot_dim > 2 * kMaxPairs) return DSA_ERR_UNSUPPORTED;
+  if (max_pos == 0) return DSA_OK;
+  if (!table || (reinterpret_cast<uintptr_t>(table) & 3u)) return DSA_ERR_INVALID_ARG;
+  const double pi = 3.14159265358979323846, d = rot_dim;
+  const double b = scaling == DSA_ROPE_NTK && rot_dim > 2 ? base * std::pow(factor, d / (d - 2.0))
+                                                          : base;
+  // The pair whose wavelength turns `r` times within the trained context.
+  auto pair_of = [&](double r) {
+    return d * std::log(orig_max_pos / (2.0 * pi * r)) / (2.0 * std::log(base));
+  };
+  double low = 0.0, high = 0.0;
+  if (scaling == DSA_ROPE_YARN) {
+    low = std::fmax(std::floor(pair_of(beta_fast)), 0.0);
+    high = std::fmin(std::ceil(pair_of(beta_slow)), d - 1.0);
+  }
+  TableArgs a{};
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double w = std::pow(b, -2.0 * i / d);
+    if (scaling == DSA_ROPE_LINEAR) w /= factor;
+    if (scaling == DSA_ROPE_YARN) {
+      const double ramp = std::fmin(std::fmax((i - low) / std::fmax(high - low, 0.001), 0.0), 1.0);
+      w = w * (1.0 - ramp) + w / factor * ramp;
+    }
+    a.step[i] = (uint64_t)(w / (2.0 * pi) * 0x1p64 + 0.5);
+  }
+  a.table = table;
+  a.amplitude = amplitude;
+  a.max_pos = max_pos;
+  a.half = rot_dim / 2;
+  a.group = kTableThreads / a.half;
+  const unsigned grid = (unsigned)(((int64_t)max_pos + kTablePositions - 1) / kTablePositions);
+  const cudaError_t e =
+      launch_kernel(rope_table_kernel, dim3(grid), dim3(kTableThreads), 0, stream, 0u, a);
+  return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+extern "C" dsa_status dsa_rotary_embed(const void* x, int64_t x_token, int64_t x_head,
+                                       const int32_t* positions, const float* cos_sin_cache,
+                                       int max_pos, int rot_dim, int first, int T, int H, int D,
+                                       int dtype, int layout, int inverse, void* out,
+                                       int64_t out_token, int64_t out_head, uint32_t* err_flags,
+                                       cudaStream_t stream) {
+  if (T < 0 || H < 0 || D < 1 || max_pos < 1 || rot_dim < 2 || rot_dim % 2 || first < 0 ||
+      first > D - rot_dim || x_token < 0 || x_head < 0 || out_token < 0 || out_head < 0)
+    return DSA_ERR_INVALID_ARG;
+  if (dtype < DSA_BF16 || dtype > DSA_FP32 || layout < DSA_ROPE_INTERLEAVED ||
+      layout > DSA_ROPE_HALF)
+    return DSA_ERR_INVALID_ARG;
+  if (D > kMaxWidth || (int64_t)T * H > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (T == 0 || H == 0) return DSA_OK;
+  if (!x || !out || !positions || !cos_sin_cache) return DSA_ERR_INVALID_ARG;
+  // Rows of the output may not land on one another.
+  if ((T > 1 && out_token == 0) || (H > 1 && out_head == 0)) return DSA_ERR_INVALID_ARG;
+  const uintptr_t es = dtype == DSA_FP32 ? 3u : 1u;
+  if ((reinterpret_cast<uintptr_t>(x) & es) || (reinterpret_cast<uintptr_t>(out) & es) ||
+      (reinterpret_cast<uintptr_t>(cos_sin_cache) & 3u))
+    return DSA_ERR_INVALID_ARG;
+  RotArgs a{};
+  a.x = x;
+  a.out = out;
+  a.x_token = x_token;
+  a.x_head = x_head;
+  a.out_token = out_token;
+  a.out_head = out_head;
+  a.positions = positions;
+  a.table = cos_sin_cache;
+  a.flags = err_flags;
+  a.max_pos = max_pos;
+  a.rot = rot_dim;
+  a.first = first;
+  a.D = D;
+  a.T = T;
+  a.H = H;
+  a.sign = inverse ? -1.f : 1.f;
+  a.rows = (int64_t)T * H;
+  a.fH = FastDiv((uint32_t)H);
+  const bool in_place = x == out && (T == 1 || x_token == out_token) && (H == 1 || x_head == out_head);
+  if (x == out && !in_place) return DSA_ERR_INVALID_ARG;
+  cudaError_t e;
+  if (dtype == DSA_BF16) e = launch_rotary<__nv_bfloat16>(a, layout, in_place, stream);
+  else if (dtype == DSA_FP16) e = launch_rotary<__half>(a, layout, in_place, stream);
+  else e = launch_rotary<float>(a, layout, in_place, stream);
+  return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}

@@ -13,7 +13,8 @@ from . import _lib
 
 __all__ = ["shard_topk", "pack_candidates", "shard_topk_pack", "merge_topk_stable",
            "convert_index_compact", "indexer_fused", "lse_combine", "slot_mapping",
-           "sparse_mla_decode", "new_error_flags", "SUPPORTED_K", "MLA_DQK", "MLA_DV"]
+           "sparse_mla_decode", "rope_table", "rotary_embed", "kv_cache_insert_fp8",
+           "sparse_mla_decode_fp8", "new_error_flags", "SUPPORTED_K", "MLA_DQK", "MLA_DV"]
 
 SUPPORTED_K = (512, 1024, 2048)
 MLA_DQK, MLA_DV = 576, 512       # DSA_MLA_DQK, DSA_MLA_DV of include/dsa.h
@@ -339,3 +340,193 @@ def kv_cache_insert(kv_rows, kpe_rows, slot_mapping, kv_cache, err_flags=None):
     _lib.call("dsa_kv_cache_insert", _ptr(kv_rows), _ptr(kpe_rows), _ptr(slot_mapping), T,
               _ptr(kv_cache), kv_cache.shape[0], _ptr(err_flags), _stream(kv_rows))
     return kv_cache
+
+
+# ---- rotary positions, and the MLA cache in 8 bits -------------------------
+ROPE_SCALINGS = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+INSERT_FP8_SMALL = 512           # DSA_INSERT_FP8_SMALL of include/dsa.h
+
+
+def _together(first: torch.Tensor, *others):
+    """Every tensor on the first one's device, which becomes the current one
+    for the launch (the returned context; None when it already is)."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
+    return None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _launch(context, name: str, *args) -> None:
+    if context is None:
+        _lib.call(name, *args)
+    else:
+        with context:
+            _lib.call(name, *args)
+
+
+def _flags(err_flags):
+    if err_flags is not None:
+        _need(err_flags, "err_flags", torch.int32, 1)
+
+
+def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, scaling: str | None = None,
+               factor: float = 1.0, orig_max_pos: int = 4096, beta_fast: float = 32.0,
+               beta_slow: float = 1.0, amplitude: float = 1.0, device="cuda", out=None):
+    """Cosines and sines for rotary_embed and fused_norm_rope: [max_pos, rot_dim]
+    fp32, rot_dim / 2 cosines then as many sines per position, times amplitude.
+
+    scaling: None, "linear" (positions divided by factor), "ntk" (the base
+    raised for factor) or "yarn" (pairs that turn fewer than beta_slow times in
+    orig_max_pos positions interpolated by factor, those above beta_fast left,
+    a ramp between)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {list(ROPE_SCALINGS)}, got {scaling!r}")
+    if out is None:
+        if max_pos < 0 or rot_dim < 0:
+            raise ValueError("max_pos and rot_dim must not be negative")
+        out = torch.empty((max_pos, rot_dim), dtype=torch.float32, device=device)
+    _need(out, "out", torch.float32, 2)
+    if tuple(out.shape) != (max_pos, rot_dim):
+        raise ValueError("out must be [max_pos, rot_dim]")
+    _launch(_together(out), "dsa_rope_table", max_pos, rot_dim, float(base),
+            ROPE_SCALINGS[scaling], float(factor), orig_max_pos, float(beta_fast),
+            float(beta_slow), float(amplitude), _ptr(out), _stream(out))
+    return out
+
+
+def _rows_of(t: torch.Tensor, name: str, dtype: torch.dtype):
+    """(token stride, head stride) of a [T, H, D] or [T, D] tensor whose values
+    are contiguous; heads and tokens may be strided."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [T, H, D] or [T, D]")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.stride(0), (t.stride(1) if t.dim() == 3 else 0)
+
+
+def rotary_embed(x, positions, cos_sin_cache, layout: str = "interleaved", first: int = 0,
+                 inverse: bool = False, out=None, err_flags=None):
+    """Rotary positions: of each row of x ([T, H, D] or [T, D]; bf16, fp16 or
+    fp32; tokens and heads may be strided) the values [first, first + rot_dim)
+    turn by the table's row of positions [T] int32, the others are carried;
+    cos_sin_cache [max_pos, rot_dim] fp32 (rope_table).
+
+    layout "interleaved" pairs neighbours, "half" pairs value i with value
+    i + rot_dim / 2.  inverse turns back (the rotation's gradient).  out may be
+    x itself (in place), else it must not overlap it."""
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {list(ROPE_LAYOUTS)}, got {layout!r}")
+    dtype = x.dtype if isinstance(x, torch.Tensor) else None
+    if dtype is not None and dtype not in ROPE_DTYPES:
+        raise TypeError(f"x must be bf16, fp16 or fp32, got {dtype}")
+    x_token, x_head = _rows_of(x, "x", dtype)
+    _need(positions, "positions", torch.int32, 1)
+    _need(cos_sin_cache, "cos_sin_cache", torch.float32, 2)
+    _flags(err_flags)
+    T, D = x.shape[0], x.shape[-1]
+    H = x.shape[1] if x.dim() == 3 else 1
+    if positions.shape[0] != T:
+        raise ValueError("positions must have one entry per token")
+    if out is None:
+        out = torch.empty(x.shape, dtype=dtype, device=x.device)
+    out_token, out_head = _rows_of(out, "out", dtype)
+    if out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    context = _together(x, positions, cos_sin_cache, out, err_flags)
+    _launch(context, "dsa_rotary_embed", _ptr(x), x_token, x_head, _ptr(positions),
+            _ptr(cos_sin_cache), cos_sin_cache.shape[0], cos_sin_cache.shape[1], first, T, H, D,
+            ROPE_DTYPES[dtype], ROPE_LAYOUTS[layout], int(bool(inverse)), _ptr(out), out_token,
+            out_head, _ptr(err_flags), _stream(x))
+    return out
+
+
+def _block_tokens(n_slots: int, n_blocks: int) -> int:
+    if n_blocks < 1 or n_slots % n_blocks:
+        raise ValueError("kv_cache must hold a whole number of slots per block scale")
+    return n_slots // n_blocks
+
+
+def kv_cache_insert_fp8(kv_rows, kpe_rows, slot_mapping, kv_cache, block_scales, work=None,
+                        err_flags=None):
+    """New rows (kv_rows [T, 512], kpe_rows [T, 64] bf16) into an 8-bit cache
+    at slot_mapping [T] int32 (-1: skipped; of several tokens with one slot the
+    last): kv_cache [n_slots, 576] uint8 (e4m3 codes), block_scales [n_blocks]
+    fp32, one for each n_slots / n_blocks slots.
+
+    A block whose scale is 0 holds nothing: zero the scales of blocks handed to
+    a new sequence.  Scales only grow otherwise, and the rows already in a
+    block move with them.  work: [n_slots + n_blocks] int32 for calls of more
+    than 512 tokens (allocated when not given)."""
+    _need(kv_rows, "kv_rows", torch.bfloat16, 2)
+    _need(kpe_rows, "kpe_rows", torch.bfloat16, 2)
+    _need(slot_mapping, "slot_mapping", torch.int32, 1)
+    _need(kv_cache, "kv_cache", torch.uint8, 2)
+    _need(block_scales, "block_scales", torch.float32, 1)
+    _flags(err_flags)
+    T = slot_mapping.shape[0]
+    if tuple(kv_rows.shape) != (T, MLA_DV) or tuple(kpe_rows.shape) != (T, MLA_DQK - MLA_DV):
+        raise ValueError("kv_rows must be [T, 512] and kpe_rows [T, 64], T slots")
+    n_slots, width = kv_cache.shape
+    n_blocks = block_scales.shape[0]
+    if width != MLA_DQK:
+        raise ValueError(f"kv_cache must be [n_slots, {MLA_DQK}]")
+    block = _block_tokens(n_slots, n_blocks)
+    if work is None and T > INSERT_FP8_SMALL:
+        work = torch.empty(n_slots + n_blocks, dtype=torch.int32, device=kv_cache.device)
+    if work is not None:
+        _need(work, "work", torch.int32, 1)
+        if work.shape[0] < n_slots + n_blocks:
+            raise ValueError("work must have n_slots + n_blocks entries")
+    context = _together(kv_cache, kv_rows, kpe_rows, slot_mapping, block_scales, work, err_flags)
+    _launch(context, "dsa_kv_cache_insert_fp8", _ptr(kv_rows), _ptr(kpe_rows),
+            _ptr(slot_mapping), T, _ptr(kv_cache), _ptr(block_scales), n_slots, block, _ptr(work),
+            _ptr(err_flags), _stream(kv_cache))
+    return kv_cache, block_scales
+
+
+def sparse_mla_decode_fp8(q, kv_cache, block_scales, slots, counts, scale: float, out=None,
+                          lse2=None, err_flags=None):
+    """sparse_mla_decode over an 8-bit cache (kv_cache_insert_fp8).
+
+    q [rows, H, 576] bf16, kv_cache [S, n_slots, 576] uint8 (e4m3 codes),
+    block_scales [S, n_blocks] fp32 (one for each n_slots / n_blocks slots),
+    slots [S, rows, K] int32, counts [S, rows] int32 -> (out [S, rows, H, 512]
+    bf16, lse2 [S, rows, H] fp32, base 2)."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(kv_cache, "kv_cache", torch.uint8, 3)
+    _need(block_scales, "block_scales", torch.float32, 2)
+    _need(slots, "slots", torch.int32, 3)
+    _need(counts, "counts", torch.int32, 2)
+    _flags(err_flags)
+    rows, H, dqk = q.shape
+    S, n_slots, dqk2 = kv_cache.shape
+    if dqk != MLA_DQK or dqk2 != MLA_DQK:
+        raise ValueError(f"q and kv_cache rows must have {MLA_DQK} entries")
+    if block_scales.shape[0] != S:
+        raise ValueError("block_scales must be [S, n_blocks]")
+    block = _block_tokens(n_slots, block_scales.shape[1])
+    if slots.shape[:2] != (S, rows) or tuple(counts.shape) != (S, rows):
+        raise ValueError("slots must be [S, rows, K] and counts [S, rows]")
+    K = slots.shape[2]
+    if out is None:
+        out = torch.empty((S, rows, H, MLA_DV), dtype=torch.bfloat16, device=q.device)
+    _need(out, "out", torch.bfloat16, 4)
+    if lse2 is None:
+        lse2 = torch.empty((S, rows, H), dtype=torch.float32, device=q.device)
+    _need(lse2, "lse2", torch.float32, 3)
+    if tuple(out.shape) != (S, rows, H, MLA_DV) or tuple(lse2.shape) != (S, rows, H):
+        raise ValueError("out must be [S, rows, H, 512] and lse2 [S, rows, H]")
+    context = _together(q, kv_cache, block_scales, slots, counts, out, lse2, err_flags)
+    _launch(context, "dsa_sparse_mla_decode_fp8", _ptr(q), _ptr(kv_cache), _ptr(block_scales),
+            n_slots, block, _ptr(slots), _ptr(counts), rows, S, H, K, float(scale), _ptr(out),
+            _ptr(lse2), _ptr(err_flags), _stream(q))
+    return out, lse2

@@ -40,7 +40,8 @@
  *     one exception, dsa_indexer_steps_noalloc, uses a static device array
  *     that exists while the library is loaded).
  *   - Every call is asynchronous on `stream` (0 = legacy default stream) and
- *     enqueues one kernel (dsa_indexer_steps_noalloc: three); results are
+ *     enqueues one kernel (dsa_indexer_steps_noalloc: three;
+ *     dsa_kv_cache_insert_fp8: one or two); results are
  *     ready when the stream reaches it.
  *   - Arguments are checked on the host before anything is enqueued.  A bad
  *     argument returns DSA_ERR_INVALID_ARG or DSA_ERR_UNSUPPORTED and touches
@@ -412,6 +413,120 @@ dsa_status dsa_fused_norm_rope(const uint16_t* kv_c, const uint16_t* k_pe,
 dsa_status dsa_kv_cache_insert(const uint16_t* kv_rows, const uint16_t* kpe_rows,
                                const int32_t* slot_mapping, int T, uint16_t* kv_cache,
                                int64_t n_slots, uint32_t* err_flags, cudaStream_t stream);
+
+/*
+ * dsa_rope_table - cosines and sines of every position's rotation angles, for
+ * dsa_rotary_embed and dsa_fused_norm_rope, with the angles scaled for
+ * contexts longer than the trained one.
+ *
+ *   table   [max_pos][rot_dim] fp32 out: row p holds amplitude * cos(p w_i),
+ *           i < rot_dim / 2, then amplitude * sin(p w_i).  4-byte aligned.
+ * With w_i = base^(-2 i / rot_dim):
+ *   DSA_ROPE_NONE    w_i (factor unused)
+ *   DSA_ROPE_LINEAR  w_i / factor (positions interpolated)
+ *   DSA_ROPE_NTK     base replaced by base * factor^(rot_dim / (rot_dim - 2))
+ *   DSA_ROPE_YARN    w_i (1 - r_i) + w_i / factor r_i, r_i rising linearly
+ *                    from 0 at i = low to 1 at i = high, low and high the pairs
+ *                    that turn beta_fast and beta_slow times in orig_max_pos
+ *                    positions (floor and ceil of rot_dim ln(orig_max_pos /
+ *                    (2 pi beta)) / (2 ln base), kept in [0, rot_dim - 1])
+ * Each angle is reduced exactly (modulo a turn, in 64-bit integers), so far
+ * positions are as exact as near ones.
+ * Errors: max_pos < 0, rot_dim odd or < 2, base <= 1, factor < 1, values not
+ *         finite, an unknown scaling, YARN with orig_max_pos < 1, beta_slow <= 0
+ *         or beta_fast < beta_slow, null or misaligned table -> INVALID_ARG;
+ *         rot_dim > 256 -> UNSUPPORTED.
+ */
+enum { DSA_ROPE_NONE = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_NTK = 2, DSA_ROPE_YARN = 3 };
+dsa_status dsa_rope_table(int max_pos, int rot_dim, double base, int scaling, double factor,
+                          int orig_max_pos, double beta_fast, double beta_slow, float amplitude,
+                          float* table, cudaStream_t stream);
+
+/*
+ * dsa_rotary_embed - rotary positions of queries, keys or their gradients.
+ * Of each head's D values, [first, first + rot_dim) turn in pairs by the
+ * table's row of the token's position; the others are carried.
+ *   DSA_ROPE_INTERLEAVED  pair i = (first + 2 i, first + 2 i + 1)
+ *   DSA_ROPE_HALF         pair i = (first + i, first + rot_dim / 2 + i)
+ *   (a, b) -> (a c - b s, b c + a s); inverse != 0 turns back (s -> -s: the
+ *   gradient of the rotation).  fp32 arithmetic, one rounding at the store.
+ *
+ *   x, out     [T][H][D] of dtype, values contiguous, token and head strides in
+ *              elements (x's may be 0, out's only for a single token or head).
+ *              out == x with the same strides turns in place (the carried
+ *              values are not touched); otherwise they must not overlap.
+ *   positions  [T] int32; cos_sin_cache [max_pos][rot_dim] fp32
+ *   err_flags  DSA_FLAG_BOUNDS if a position is outside [0, max_pos) (that
+ *              token is carried unturned).
+ * Errors: negative sizes or strides, D < 1, max_pos < 1, rot_dim odd or < 2,
+ *         the turning part outside [0, D), an unknown dtype or layout, null
+ *         or misaligned pointers, output rows on one another, out == x with
+ *         other strides -> INVALID_ARG; D > 1024, T * H >= 2^31 -> UNSUPPORTED.
+ */
+enum { DSA_BF16 = 0, DSA_FP16 = 1, DSA_FP32 = 2 };
+enum { DSA_ROPE_INTERLEAVED = 0, DSA_ROPE_HALF = 1 };
+dsa_status dsa_rotary_embed(const void* x, int64_t x_token, int64_t x_head,
+                            const int32_t* positions, const float* cos_sin_cache, int max_pos,
+                            int rot_dim, int first, int T, int H, int D, int dtype, int layout,
+                            int inverse, void* out, int64_t out_token, int64_t out_head,
+                            uint32_t* err_flags, cudaStream_t stream);
+
+/*
+ * dsa_kv_cache_insert_fp8 - new rows into a paged MLA cache held in 8 bits.
+ * The cache stores e4m3 codes; a row's values are its codes times the scale of
+ * its block of block_tokens consecutive slots (one latent head: one scale for
+ * a block).  For every block that receives rows of this call:
+ *   scale' = max(scale, the smallest power of two s >= 2^-126 with
+ *            amax <= 448 s), amax over the call's finite values in the block
+ *   its other rows, if 0 < scale < scale':  code = e4m3(code * (scale / scale'))
+ *   its new rows:  code = e4m3(value / scale')
+ * with round to nearest even, saturating at +-448 (an infinity too; a NaN
+ * becomes the format's NaN).  A scale of 0 (or less, or NaN) means that the
+ * block holds nothing yet: zero the scales of blocks handed to a new sequence.
+ * A row of a slot that several tokens name is the last one's.
+ *
+ *   kv_rows [T][DSA_MLA_DV] bf16, kpe_rows [T][64] bf16: 16-byte aligned
+ *   slot_mapping [T] int32; a slot < 0 writes nothing
+ *   kv_cache [n_slots][DSA_MLA_DQK] e4m3 codes, 16-byte aligned
+ *   block_scales [n_slots / block_tokens] fp32
+ *   work       [n_slots + n_slots / block_tokens] int32, contents arbitrary;
+ *              needed when T > DSA_INSERT_FP8_SMALL, else may be NULL.  Calls
+ *              that may run at the same time need their own.
+ *   err_flags  DSA_FLAG_BOUNDS if a slot is >= n_slots (skipped)
+ * Enqueues two kernels when T > DSA_INSERT_FP8_SMALL, else one.
+ * Errors: T < 0, n_slots < 1, block_tokens < 1, n_slots % block_tokens, null
+ *         pointers, misalignment -> INVALID_ARG; block_tokens > 1024, n_slots
+ *         > 2^31 - 1 -> UNSUPPORTED.
+ */
+#define DSA_INSERT_FP8_SMALL 512
+dsa_status dsa_kv_cache_insert_fp8(const uint16_t* kv_rows, const uint16_t* kpe_rows,
+                                   const int32_t* slot_mapping, int T, uint8_t* kv_cache,
+                                   float* block_scales, int64_t n_slots, int block_tokens,
+                                   int32_t* work, uint32_t* err_flags, cudaStream_t stream);
+
+/*
+ * dsa_sparse_mla_decode_fp8 - dsa_sparse_mla_decode over an 8-bit cache
+ * (dsa_kv_cache_insert_fp8): cache row j is its e4m3 codes times the scale of
+ * its block of block_tokens slots, as key (all DSA_MLA_DQK values) and as
+ * value (the first DSA_MLA_DV).
+ *
+ *   q            [rows][H][DSA_MLA_DQK] bf16, 16-byte aligned
+ *   kv_cache     [S][n_slots][DSA_MLA_DQK] e4m3 codes, 16-byte aligned
+ *   block_scales [S][n_slots / block_tokens] fp32
+ *   slots, counts, out, lse2, err_flags, scale: as dsa_sparse_mla_decode
+ * A slot outside [0, n_slots) is left out and raises DSA_FLAG_BOUNDS; what
+ * the cache holds there or elsewhere cannot reach the result.
+ * Errors: rows < 0, K < 1, H < 1, n_slots < 1, block_tokens < 1, n_slots %
+ *         block_tokens, scale not finite, null pointers, misalignment ->
+ *         INVALID_ARG; S not in [1, 64], n_slots > 2^31 - 1, too many CTAs ->
+ *         UNSUPPORTED.
+ */
+dsa_status dsa_sparse_mla_decode_fp8(const uint16_t* q, const uint8_t* kv_cache,
+                                     const float* block_scales, int64_t n_slots,
+                                     int block_tokens, const int32_t* slots,
+                                     const int32_t* counts, int rows, int S, int H, int K,
+                                     float scale, uint16_t* out, float* lse2,
+                                     uint32_t* err_flags, cudaStream_t stream);
 
 /*
  * dsa_indexer_steps_noalloc - dsa_shard_topk_pack, dsa_merge_topk_stable and
