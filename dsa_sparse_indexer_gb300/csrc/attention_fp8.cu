@@ -28,20 +28,25 @@
 // stages of a tile (72 KB each), the query 72 KB, and 8 KB of weights; the
 // other 8 KB of weights take the tile's rope block, which only the scores read.
 //
-//  warps 0-7   the query's two parts, then the softmax: a token and 32 heads a
-//              thread, the running reference of a head moving only when a
-//              tile's maximum is 2^5.75 above the last, and the outputs
-//  warps 8-11  gather the selected rows, two warps a stage, 16-byte cp.async
-//              into the swizzled layouts; a stage is filled and freed in two
-//              parts (dimensions 0-255, the rest), as the value products that
-//              read them end
-//  warp 12     one thread issues the MMAs, whichever is ready first
+//  warps 0-15  the softmax: a token and 16 heads a thread, the running
+//              reference of a head moving only when a weight would pass its
+//              bound; the outputs; and a row's query in its two parts, the next
+//              one's while this one's last value products run
+//  warps 16-19 gather the selected rows, 32 of each tile a warp, 16-byte
+//              cp.async into the swizzled layouts; a stage is filled and freed
+//              in two parts (dimensions 0-255, the rest), as the value products
+//              that read them end
+//  warps 20-21 a thread each issues the scores and the value products
+// The kernel is persistent: one CTA an SM, each with a run of (row, shard)
+// pairs in row order, so that a row's shards share the query on chip and a
+// pair's start and end overlap its neighbours' tiles.
 // Every wait is bounded; one that runs out raises DSA_FLAG_TIMEOUT and stops
 // the CTA's roles, which drain their copies and MMAs in flight.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -58,11 +63,19 @@ constexpr int kKvBlock = kTile * 128;        // bytes of a tile's block
 constexpr int kKvRope = kTile * 64;          // and of its rope block
 constexpr int kQBlock = 2 * kHeads * 128;    // bytes of a query block, both parts
 constexpr int kQRope = 2 * kHeads * 64;
-constexpr int kSoftmaxWarps = 8, kGatherWarps = 4;
+constexpr int kSoftmaxWarps = 16, kGatherWarps = 4;
+constexpr int kGroups = kSoftmaxWarps / 4;   // of four warps, 16 heads each
+constexpr int kGroupHeads = kHeads / kGroups;
 constexpr int kGather0 = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + kGatherWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kThreads = 768;                // six warpgroups; warps 22-23 only make up the last
+// Registers a thread of the softmax's four warpgroups, the gathering one and
+// the MMA's: 128 (4 x 88 + 64 + 64) = the 768 x 80 the CTA is launched with.
+constexpr int kRegsSoftmax = 88, kRegsGather = 64, kRegsMma = 64;
+static_assert(128 * (4 * kRegsSoftmax + kRegsGather + kRegsMma) <= kThreads * 80, "registers");
 // Tensor-memory columns.
 constexpr int kOCol = 0, kSCol = 256, kTmemCols = 512;
+constexpr int kCounts = 20;                  // pairs whose counts are kept on chip
+constexpr int kSms = 152;                     // of a GB300
 constexpr float kLog2e = 1.4426950408889634f;
 // A head's weights, with their token's scale, are t 2^(x - ref): a new reference
 // puts the largest at 2^3, and they may grow to 2^8.75 (448 is the largest
@@ -77,12 +90,13 @@ struct alignas(1024) Smem {
   uint8_t rope[kStages][kKvRope];            // 16384; then the weights' first parts
   uint8_t qrope[kQRope];                     // 8192
   uint8_t plo[kKvRope];                      // 8192: the weights' second parts
-  float part[2][4][kHeads];                  // per 32 tokens: a tile's maxima, then the sums
+  float part[4][kHeads];                     // per 32 tokens: a tile's maxima
   float ref[2][kHeads];                      // a tile's references
-  float fq[kHeads];                          // scale log2(e) / the query's power of two; at the
-                                             // end the outputs' factors
-  uint64_t group[2], final, qfull, fullA[kStages], fullB[kStages], emptyA[kStages], emptyB[kStages];
-  uint64_t sfull[2], sfree[2], pfull, pvdone, drain;
+  float fq[kHeads];                          // scale log2(e) / the query's power of two
+  float tok[kStages][kTile];                 // the tokens' scales; -1: left out
+  int counts[kCounts];                       // of the CTA's first pairs
+  uint64_t qfull, fullA[kStages], fullB[kStages], emptyA[kStages], emptyB[kStages];
+  uint64_t sfull[2], sfree[2], pfull, pvdone, drain[2];
   uint32_t tmem;
   int abort;
 };
@@ -95,12 +109,46 @@ struct MlaFp8Args {
   const int32_t* slots;          // [S][rows][K]
   const int32_t* counts;         // [S][rows]
   int64_t n_slots, n_blocks;
-  int rows, H, K, hgroups;
+  int rows, S, H, K, hgroups;
   float c2;                      // scale * log2(e)
   __nv_bfloat16* out;            // [S][rows][H][kDv]
   float* lse2;                   // [S][rows][H]
   uint32_t* flags;
-  FastDiv fblock;
+  FastDiv fblock, fS;
+};
+
+// Pair p = row * S + shard.
+__device__ __forceinline__ int row_of(const MlaFp8Args& a, int p) { return (int)fdiv((uint32_t)p, a.fS); }
+__device__ __forceinline__ int64_t list_of(const MlaFp8Args& a, int p, int* shard) {
+  uint32_t s;
+  const int row = (int)fdivmod((uint32_t)p, a.fS, &s);
+  *shard = (int)s;
+  return (int64_t)s * a.rows + row;          // index of the pair's list, count and outputs
+}
+
+// Steps over the tiles of the CTA's pairs [p0, p1), those with no token left out.
+struct Cursor {
+  int p, t, count;
+  __device__ __forceinline__ bool valid(int p1) const { return p < p1; }
+  // The first pair with tokens from p on.
+  __device__ __forceinline__ void settle(const MlaFp8Args& a, const Smem& sm, int p0, int p1) {
+    for (t = 0, count = 0; p < p1; ++p) {
+      int s;
+      count = p - p0 < kCounts ? sm.counts[p - p0]
+                               : min(max(__ldg(a.counts + list_of(a, p, &s)), 0), a.K);
+      if (count > 0) break;
+    }
+  }
+  __device__ __forceinline__ Cursor(const MlaFp8Args& a, const Smem& sm, int p0, int p1) : p(p0) {
+    settle(a, sm, p0, p1);
+  }
+  __device__ __forceinline__ void next_pair(const MlaFp8Args& a, const Smem& sm, int p0, int p1) {
+    ++p;
+    settle(a, sm, p0, p1);
+  }
+  __device__ __forceinline__ void advance(const MlaFp8Args& a, const Smem& sm, int p0, int p1) {
+    if (++t * kTile >= count) next_pair(a, sm, p0, p1);
+  }
 };
 
 // Shared-memory matrix descriptor: start address >> 4 (bits 0-13), leading
@@ -172,16 +220,46 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return done != 0;
 }
 
+// Named hardware barriers of the softmax's warps, which run the same sequence
+// of them whatever happens: a failed wait does not end their loops, so that no
+// warp is left behind.
+__device__ __forceinline__ bool barrier_or(int id, int threads, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"((uint32_t)mine)
+      : "memory");
+  return any != 0;
+}
+__device__ __forceinline__ void barrier(int id, int threads) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 __device__ __forceinline__ bool aborted(const Smem& sm) {
   return *reinterpret_cast<const volatile int*>(&sm.abort) != 0;
 }
 
-// Bounded wait that also gives up once another role of the CTA has aborted.
+// Bounded wait that also gives up once another role of the CTA has aborted.  A
+// try suspends the thread for up to kSuspendNs (or until the phase ends), so
+// that waiting warps leave the issue slots to the softmax: polling without it
+// took three quarters of all instructions issued.
+constexpr uint32_t kSuspendNs = 20000, kWaitTries = kWaitPolls >> 6;
 __device__ __forceinline__ bool wait_or_abort(Smem& sm, uint64_t* bar, uint32_t parity) {
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
+  for (uint32_t i = 0; i < kWaitTries; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    if (done) return true;
     if (aborted(sm)) return false;
-    if (i > 64) __nanosleep(64);
   }
   return false;
 }
@@ -191,43 +269,72 @@ __device__ __forceinline__ void abort_cta(Smem& sm, uint32_t* flags) {
   *reinterpret_cast<volatile int*>(&sm.abort) = 1;
 }
 
-// 32 columns of this warp's 32 tensor-memory lanes; tmem_wait names the
-// registers so that no use of them is scheduled before it.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr));
+// 16 columns of this warp's 32 tensor-memory lanes; or 32 columns of 16 lanes,
+// a thread then holding of each 8 columns two of lane (id / 4) and two
+// of lane 8 + id / 4.  tmem_wait names the registers so that no use of them is
+// scheduled before it.
+#define DSA_R16(o)                                                                             \
+  "+r"(r[o + 0]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]),              \
+      "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7]), "+r"(r[o + 8]), "+r"(r[o + 9]),          \
+      "+r"(r[o + 10]), "+r"(r[o + 11]), "+r"(r[o + 12]), "+r"(r[o + 13]), "+r"(r[o + 14]),     \
+      "+r"(r[o + 15])
+#define DSA_W16(o)                                                                             \
+  "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]),              \
+      "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]),          \
+      "=r"(r[o + 10]), "=r"(r[o + 11]), "=r"(r[o + 12]), "=r"(r[o + 13]), "=r"(r[o + 14]),     \
+      "=r"(r[o + 15])
+#define DSA_L16 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {" DSA_L16 "}, [%16];"
+               : DSA_W16(0)
+               : "r"(addr));
 }
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld32_of16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {" DSA_L16 "}, [%16];"
+               : DSA_W16(0)
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32_of16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], {" DSA_L16 "};"
+               : DSA_R16(0)
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+  asm volatile("" : DSA_R16(0));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
-      "%29, %30, %31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31]), "r"(addr)
-      : "memory");
-}
+#undef DSA_R16
+#undef DSA_W16
+#undef DSA_L16
 
 // 2^x (ex2.approx.ftz.f32: relative error about 2^-22, 2^-inf = 0).
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two products, sums or fused multiply-adds in one instruction, each rounded as
+// the scalar operation would be.
+#define DSA_F32X2(name, op)                                                              \
+  __device__ __forceinline__ float2 name(float2 a, float2 b) {                           \
+    uint64_t r;                                                                          \
+    asm(op " %0, %1, %2;"                                                                \
+        : "=l"(r)                                                                        \
+        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b))); \
+    return *reinterpret_cast<float2*>(&r);                                               \
+  }
+DSA_F32X2(fmul2, "mul.rn.f32x2")
+DSA_F32X2(fadd2, "add.rn.f32x2")
+#undef DSA_F32X2
+__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+        "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
 }
 
 // The largest of the warp's values (a NaN loses to a number).
@@ -252,7 +359,9 @@ __device__ __forceinline__ __half2 of_e5m2x2(uint32_t c) {
 }
 
 // ---- gathering: the selected rows into the stages --------------------------
-// Warps g and g + 2 serve stage g, rows 0-63 and 64-127 of each tile.
+// Warp g takes rows 32 g .. + 31 of every tile.  Eight lanes copy a row's
+// 128-byte segment of a block, so lane l serves rows l / 8 + 4 i, and keeps
+// their offsets in registers: the copies of a part are issued back to back.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(in ? 16 : 0)
@@ -263,461 +372,575 @@ __device__ __forceinline__ void landed(uint64_t* bar) {   // this lane's copies,
   mbar_arrive1(bar);
 }
 
-__device__ __forceinline__ void gather_tiles(const MlaFp8Args& a, Smem& sm, int64_t shard_slots,
-                                             int count, int ntiles, const int32_t* list) {
-  const int lane = threadIdx.x & 31, g = (threadIdx.x >> 5) - kGather0;
-  const int st = g & 1, row0 = (g >> 1) * 64;
-  const uint8_t* cache = a.cache + shard_slots * kDqk;
-  const uint32_t kv = smem_u32(sm.kv[st][0]), rope = smem_u32(sm.rope[st]);
+__device__ __forceinline__ void gather_tiles(const MlaFp8Args& a, Smem& sm, int p0, int p1) {
+  const int lane = threadIdx.x & 31, row0 = ((threadIdx.x >> 5) - kGather0) * 32;
+  const int sub = lane >> 3, c = lane & 7;
+  // A row's chunk c lies at c ^ (row & 7): rows 4 i + sub alternate between
+  // two places.  The rope block's rows have four chunks, at c ^ (row / 2 & 3);
+  // lanes 0-3 of eight copy row 4 i + sub, lanes 4-7 the same plus 16.
+  const uint32_t kv0 = smem_u32(sm.kv[0][0]) + (uint32_t)(row0 + sub) * 128;
+  const uint32_t even = (uint32_t)(c ^ sub) << 4, odd = (uint32_t)(c ^ (sub + 4)) << 4;
+  const uint32_t rope0 = smem_u32(sm.rope[0]) + (uint32_t)(row0 + sub + (c >> 2) * 16) * 64;
   bool bad = false, ok = true;
-  for (int t = st, k = 0; t < ntiles; t += kStages, ++k) {
-    // Two tokens a lane; one left out, or past the list, becomes a zero row.
-    int y[2];
+  Cursor cur(a, sm, p0, p1);
+  int shard = 0;
+  int32_t slot[8];                           // of rows row0 + sub + 4 i, the next tile's
+  auto fetch = [&]() {
+    const int32_t* list = a.slots + list_of(a, cur.p, &shard) * a.K;
+    const int j0 = cur.t * kTile + row0 + sub;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = t * kTile + row0 + 32 * i + lane;
-      const int slot = j < count ? __ldg(list + j) : -1;
-      const bool in = slot >= 0 && slot < a.n_slots;
-      bad |= j < count && !in;
-      y[i] = in ? slot : -1;
-    }
-    // The value products read whole groups of 32 tokens; a group past the list
-    // is not read by any, and its scores are masked.
-    const int groups = min(2, (count - t * kTile - row0 + 31) / 32);
-    if (k >= 1) ok = wait_or_abort(sm, &sm.emptyA[st], (uint32_t)(k - 1) & 1u);
-    if (!__all_sync(kFull, ok)) break;
-    for (int i = 0; i < groups; ++i)
-#pragma unroll 2
-      for (int rq = 0; rq < 8; ++rq) {
-        const int jr = 4 * rq + (lane >> 3), c = lane & 7;
-        const int slot = __shfl_sync(kFull, i ? y[1] : y[0], jr);
-        const uint8_t* src = cache + (int64_t)max(slot, 0) * kDqk + c * 16;
-        const uint32_t dst = kv + (uint32_t)((row0 + 32 * i + jr) * 128 + ((c ^ (jr & 7)) << 4));
-        copy16(dst, src, slot >= 0);
-        copy16(dst + kKvBlock, src + 128, slot >= 0);
-      }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    // Part B at once where its stage is free already, so that both are in
-    // flight; else part A is handed over before the wait.
-    const bool both = k == 0 || __all_sync(kFull, mbar_test(&sm.emptyB[st], (uint32_t)(k - 1) & 1u));
-    if (!both) {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      landed(&sm.fullA[st]);
-      ok = wait_or_abort(sm, &sm.emptyB[st], (uint32_t)(k - 1) & 1u);
-      if (!__all_sync(kFull, ok)) break;
-    }
-    for (int i = 0; i < groups; ++i) {
-#pragma unroll 2
-      for (int rq = 0; rq < 8; ++rq) {
-        const int jr = 4 * rq + (lane >> 3), c = lane & 7;
-        const int slot = __shfl_sync(kFull, i ? y[1] : y[0], jr);
-        const uint8_t* src = cache + (int64_t)max(slot, 0) * kDqk + 256 + c * 16;
-        const uint32_t dst =
-            kv + 2 * kKvBlock + (uint32_t)((row0 + 32 * i + jr) * 128 + ((c ^ (jr & 7)) << 4));
-        copy16(dst, src, slot >= 0);
-        copy16(dst + kKvBlock, src + 128, slot >= 0);
-      }
-#pragma unroll 2
-      for (int rq = 0; rq < 4; ++rq) {
-        const int jr = 8 * rq + (lane >> 2), c = lane & 3;
-        const int slot = __shfl_sync(kFull, i ? y[1] : y[0], jr);
-        copy16(rope + (uint32_t)((row0 + 32 * i + jr) * 64 + ((c ^ ((jr >> 1) & 3)) << 4)),
-               cache + (int64_t)max(slot, 0) * kDqk + kDv + c * 16, slot >= 0);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    if (both) {
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      landed(&sm.fullA[st]);
-    }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    landed(&sm.fullB[st]);
+    for (int i = 0; i < 8; ++i) slot[i] = j0 + 4 * i < cur.count ? __ldg(list + j0 + 4 * i) : -1;
+  };
+  int32_t mine = -1;                         // the slot of row0 + lane, the next tile's
+  auto fetch_mine = [&]() {
+    const int j = cur.t * kTile + row0 + lane;
+    mine = j < cur.count ? __ldg(a.slots + list_of(a, cur.p, &shard) * a.K + j) : -1;
+  };
+  if (cur.valid(p1)) {
+    fetch();
+    fetch_mine();
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");   // none outlives the CTA
+  // Parts issued and not yet handed over, the older first: at most two.
+  uint64_t *older = nullptr, *newer = nullptr;
+  auto drain = [&]() {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (older) landed(older);
+    if (newer) landed(newer);
+    older = newer = nullptr;
+  };
+  // A part may be filled once the value products of its last tile are done;
+  // where that is still to come, what has been issued is handed over first.
+  auto room = [&](uint64_t* empty, int k) {
+    if (k >= 1 && !__all_sync(kFull, mbar_test(empty, (uint32_t)(k - 1) & 1u))) {
+      drain();
+      ok = wait_or_abort(sm, empty, (uint32_t)(k - 1) & 1u);
+    }
+    if (newer) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      landed(older);
+      older = newer;
+      newer = nullptr;
+    }
+    return __all_sync(kFull, ok) != 0;
+  };
+  auto issued = [&](uint64_t* full) {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (older) newer = full;
+    else older = full;
+  };
+  for (int n = 0; cur.valid(p1); ++n) {
+    const int st = n & 1, k = n >> 1, left = cur.count - cur.t * kTile - row0;
+    const uint8_t* cache = a.cache + (int64_t)shard * a.n_slots * kDqk + c * 16;
+    // One left out, or past the list, becomes a zero row.  The value products
+    // read whole groups of 32 tokens; a group past the list is not read by any,
+    // and its scores are masked: it is not filled.
+    int32_t y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool in = slot[i] >= 0 && slot[i] < a.n_slots;
+      y[i] = in ? slot[i] : -1;
+    }
+    // The scale of row0 + lane's token, for the softmax.
+    const bool in = mine >= 0 && mine < a.n_slots;
+    bad |= !in && lane < left;
+    float ts = -1.f;
+    if (in) ts = __ldg(a.scales + shard * a.n_blocks + fdiv((uint32_t)mine, a.fblock));
+    cur.advance(a, sm, p0, p1);
+    if (cur.valid(p1)) {
+      fetch();
+      fetch_mine();
+    }
+    const uint32_t kv = kv0 + (uint32_t)st * (kBlocks * kKvBlock);
+    auto copy_pair = [&](int block) {        // blocks `block` and block + 1
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint8_t* src = cache + (int64_t)max(y[i], 0) * kDqk + block * 128;
+        const uint32_t dst = kv + block * kKvBlock + i * 512 + ((i & 1) ? odd : even);
+        copy16(dst, src, y[i] >= 0);
+        copy16(dst + kKvBlock, src + 128, y[i] >= 0);
+      }
+    };
+    if (!room(&sm.emptyA[st], k)) break;
+    if (left > 0) copy_pair(0);
+    issued(&sm.fullA[st]);
+    if (!room(&sm.emptyB[st], k)) break;
+    bad |= in && !(ts == 0.f || (ts >= kMinScale && ts <= kMaxScale));
+    sm.tok[st][row0 + lane] = !in ? -1.f : ts > 0.f ? ts : 0.f;
+    if (left > 0) {
+      copy_pair(2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int32_t row = c < 4 ? y[i] : y[i + 4];
+        copy16(rope0 + (uint32_t)st * kKvRope + i * 256 + (((c & 3) ^ ((2 * i + (sub >> 1)) & 3)) << 4),
+               cache + (int64_t)max(row, 0) * kDqk + kDv - (c & 4) * 16, row >= 0);
+      }
+    }
+    issued(&sm.fullB[st]);
+  }
+  drain();                                   // none outlives the CTA
   if (!__all_sync(kFull, ok) && lane == 0 && !aborted(sm)) abort_cta(sm, a.flags);
   if (bad) raise_flag(a.flags, DSA_FLAG_BOUNDS);
 }
 
-// ---- one thread: the MMAs ----------------------------------------------------
-__device__ __forceinline__ void issue_mmas(const MlaFp8Args& a, Smem& sm, uint32_t tmem, int count,
-                                           int ntiles) {
-  constexpr uint32_t kIdS = idesc_f8(kTile, 2 * kHeads, 0, 0, 0);
-  constexpr uint32_t kIdHi = idesc_f8(kHeads, 256, 0, 1, 1), kIdLo = idesc_f8(kHeads, 256, 1, 1, 1);
-  bool ok = wait_or_abort(sm, &sm.qfull, 0);
-  tc_fence_after();
+// ---- the MMAs: a thread for the scores, a thread for the value products ------
+// Scores run up to two tiles ahead of the value products, across pairs; a new
+// row's wait for its query.
+__device__ __forceinline__ bool issue_scores(const MlaFp8Args& a, Smem& sm, uint32_t tmem, int p0,
+                                             int p1) {
+  constexpr uint32_t kId = idesc_f8(kTile, 2 * kHeads, 0, 0, 0);
   const uint64_t qd = smem_desc(smem_u32(sm.q[0]), 16, 1024, 2);
   const uint64_t qrd = smem_desc(smem_u32(sm.qrope), 16, 512, 4);
-  const uint64_t lod = smem_desc(smem_u32(sm.plo), 16, 512, 4);
-  int na = 0, nb = 0;                        // tiles whose score parts A and B are issued
-  uint32_t idle = 0;
-  for (int t = 0; ok && t < ntiles;) {
-    const int st = t & 1;
-    if (nb > t && mbar_test(&sm.pfull, (uint32_t)t & 1u)) {
-      tc_fence_after();
-      // Groups of 32 tokens that the tile has; the two halves of the
-      // dimensions one after the other, so that the first one's blocks free
-      // early.
-      const int steps = min(kTile / 32, (count - t * kTile + 31) / 32);
-      const uint64_t hid = smem_desc(smem_u32(sm.rope[st]), 16, 512, 4);
+  auto block = [&](uint32_t d, int st, int b) {
+    const uint64_t kd = smem_desc(smem_u32(sm.kv[st][b]), 16, 1024, 2);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint64_t vd = smem_desc(smem_u32(sm.kv[st][2 * half]), kKvBlock, 1024, 2);
-        const uint32_t d = tmem + kOCol + half * 128;
-        for (int k = 0; k < steps; ++k) {
-          const uint64_t v = vd + (uint64_t)(k * (4096 >> 4)), p = (uint64_t)(k * (2048 >> 4));
-          mma_f8_ws(d, lod + p, v, kIdLo, (t > 0 || k > 0) ? 1u : 0u);
-          mma_f8_ws(d, hid + p, v, kIdHi, 1u);
-        }
-        mma_commit(half == 0 ? &sm.emptyA[st] : &sm.emptyB[st]);
-      }
-      mma_commit(&sm.pvdone);
-      ++t;
-      idle = 0;
-      continue;
+    for (int k = 0; k < 4; ++k)
+      mma_f8(d, kd + k * 2, qd + (uint64_t)(b * (kQBlock >> 4) + k * 2), kId, b + k > 0 ? 1u : 0u);
+  };
+  Cursor cur(a, sm, p0, p1);
+  int row = -1, run = -1;                    // the row at hand; rows begun
+  for (int n = 0; cur.valid(p1); ++n) {
+    const int st = n & 1;
+    const uint32_t parity = (uint32_t)(n >> 1) & 1u, d = tmem + kSCol + st * 128;
+    if (row_of(a, cur.p) != row) {
+      row = row_of(a, cur.p);
+      if (!wait_or_abort(sm, &sm.qfull, (uint32_t)++run & 1u)) return false;
     }
-    const int sb = nb & 1;
-    if (na > nb && mbar_test(&sm.fullB[sb], (uint32_t)(nb >> 1) & 1u)) {
-      tc_fence_after();
-      const uint32_t d = tmem + kSCol + sb * 128;
+    if ((n >= 2 && !wait_or_abort(sm, &sm.sfree[st], parity ^ 1u)) ||
+        !wait_or_abort(sm, &sm.fullA[st], parity))
+      return false;
+    tc_fence_after();
+    block(d, st, 0);
+    block(d, st, 1);
+    if (!wait_or_abort(sm, &sm.fullB[st], parity)) return false;
+    tc_fence_after();
+    block(d, st, 2);
+    block(d, st, 3);
+    const uint64_t rd = smem_desc(smem_u32(sm.rope[st]), 16, 512, 4);
 #pragma unroll
-      for (int b = 2; b < kBlocks; ++b) {
-        const uint64_t kd = smem_desc(smem_u32(sm.kv[sb][b]), 16, 1024, 2);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_f8(d, kd + k * 2, qd + (uint64_t)(b * (kQBlock >> 4) + k * 2), kIdS, 1u);
-      }
-      const uint64_t rd = smem_desc(smem_u32(sm.rope[sb]), 16, 512, 4);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) mma_f8(d, rd + k * 2, qrd + k * 2, kIdS, 1u);
-      mma_commit(&sm.sfull[sb]);
-      ++nb;
-      idle = 0;
-      continue;
-    }
-    const int sa = na & 1;
-    if (na == nb && na < ntiles && mbar_test(&sm.fullA[sa], (uint32_t)(na >> 1) & 1u) &&
-        (na < 2 || mbar_test(&sm.sfree[sa], (uint32_t)((na >> 1) - 1) & 1u))) {
-      tc_fence_after();
-      const uint32_t d = tmem + kSCol + sa * 128;
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const uint64_t kd = smem_desc(smem_u32(sm.kv[sa][b]), 16, 1024, 2);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_f8(d, kd + k * 2, qd + (uint64_t)(b * (kQBlock >> 4) + k * 2), kIdS,
-                 (b > 0 || k > 0) ? 1u : 0u);
-      }
-      ++na;
-      idle = 0;
-      continue;
-    }
-    if (++idle >= 4 * kWaitPolls || aborted(sm)) {
-      ok = false;
-      break;
-    }
-    if (idle > 64) __nanosleep(32);
+    for (int k = 0; k < 2; ++k) mma_f8(d, rd + k * 2, qrd + k * 2, kId, 1u);
+    mma_commit(&sm.sfull[st]);
+    cur.advance(a, sm, p0, p1);
   }
+  return true;
+}
+
+__device__ __forceinline__ bool issue_values(const MlaFp8Args& a, Smem& sm, uint32_t tmem, int p0,
+                                             int p1) {
+  constexpr uint32_t kIdHi = idesc_f8(kHeads, 256, 0, 1, 1), kIdLo = idesc_f8(kHeads, 256, 1, 1, 1);
+  const uint64_t lod = smem_desc(smem_u32(sm.plo), 16, 512, 4);
+  Cursor cur(a, sm, p0, p1);
+  for (int n = 0; cur.valid(p1); ++n) {
+    // Groups of 32 tokens that the tile has; the two halves of the dimensions
+    // one after the other, so that the first one's blocks free early.
+    const int st = n & 1, steps = min(kTile / 32, (cur.count - cur.t * kTile + 31) / 32);
+    const uint64_t hid = smem_desc(smem_u32(sm.rope[st]), 16, 512, 4);
+    if (!wait_or_abort(sm, &sm.pfull, (uint32_t)n & 1u)) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const uint64_t vd = smem_desc(smem_u32(sm.kv[st][2 * half]), kKvBlock, 1024, 2);
+      const uint32_t d = tmem + kOCol + half * 128;
+      for (int k = 0; k < steps; ++k) {
+        const uint64_t v = vd + (uint64_t)(k * (4096 >> 4)), p = (uint64_t)(k * (2048 >> 4));
+        mma_f8_ws(d, lod + p, v, kIdLo, (cur.t > 0 || k > 0) ? 1u : 0u);
+        mma_f8_ws(d, hid + p, v, kIdHi, 1u);
+      }
+      mma_commit(half == 0 ? &sm.emptyA[st] : &sm.emptyB[st]);
+    }
+    mma_commit(&sm.pvdone);
+    cur.advance(a, sm, p0, p1);
+  }
+  return true;
+}
+
+// Every MMA issued ends before the tensor memory is freed.
+__device__ __forceinline__ void drain_mmas(const MlaFp8Args& a, Smem& sm, uint64_t* bar, bool ok) {
   if (!ok && !aborted(sm)) abort_cta(sm, a.flags);
-  mma_commit(&sm.drain);                     // every MMA issued ends before the memory is freed
-  if (!mbar_wait(&sm.drain, 0)) abort_cta(sm, a.flags);
+  mma_commit(bar);
+  if (!mbar_wait(bar, 0)) abort_cta(sm, a.flags);
 }
 
 // ---- the query's two parts -----------------------------------------------------
-// A warp takes eight heads; a head's 576 values are 72 chunks of 8, lanes
-// 0-31 three times (the last for eight lanes).
-__device__ __forceinline__ void split_query(const MlaFp8Args& a, Smem& sm, int r, int hg) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll 2
-  for (int i = 0; i < kHeads / kSoftmaxWarps; ++i) {
-    const int h = warp * (kHeads / kSoftmaxWarps) + i, gh = hg * kHeads + h;
-    const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)r * a.H + gh) * kDqk);
-    uint4 v[3];
+// Warp w takes heads 4 w .. + 3.  A head's 512 latent values are 64 chunks of 8,
+// two a lane; the four rope parts, 32 chunks, one a lane.  Returns the factor of
+// head 4 w + lane (lanes 0-3).
+__device__ __forceinline__ void split_chunk(const uint4& v, float f, uint8_t* hi_at, uint8_t* lo_at) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int c = 0; c < 3; ++c)
-      v[c] = gh < a.H && (c < 2 || lane < 8) ? __ldg(src + c * 32 + lane) : make_uint4(0, 0, 0, 0);
-    uint32_t m = 0;
+  for (int k = 0; k < 4; ++k) {
+    const float2 y = fmul2(make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)),
+                           make_float2(f, f));
+    const __half2 x = __floats2half2_rn(y.x, y.y);
+    hi[k] = to_e4m3x2(x);
+    lo[k] = to_e4m3x2(__hsub2(x, of_e4m3x2(hi[k])));
+  }
+  *reinterpret_cast<uint2*>(hi_at) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+  *reinterpret_cast<uint2*>(lo_at) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+}
+__device__ __forceinline__ uint32_t chunk_amax(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0;
 #pragma unroll
-    for (int c = 0; c < 3; ++c) {
-      const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+  for (int k = 0; k < 4; ++k) m = max(m, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+  return m;
+}
+// 2^up brings a head's largest value (bf16 bits m) to [2^7, 2^8).
+__device__ __forceinline__ int query_up(uint32_t m) {
+  return m ? min(7 - ((int)(m >> 7) - 127), 120) : 0;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+__device__ __forceinline__ float split_query(const MlaFp8Args& a, Smem& sm, int r, int hg) {
+  constexpr int kEach = kHeads / kSoftmaxWarps;
+  const int lane = threadIdx.x & 31, h0 = (threadIdx.x >> 5) * kEach, gh0 = hg * kHeads + h0;
+  const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)r * a.H + gh0) * kDqk);
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  uint4 v[kEach][2];
+  const int ri = lane >> 3;                  // this lane's rope chunk: its head, and place
+  const uint4 rope = gh0 + ri < a.H ? __ldg(src + ri * (kDqk / 8) + kDv / 8 + (lane & 7)) : none;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) m = max(m, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-    }
-    m = __reduce_max_sync(kFull, m);
-    // 2^up brings the largest value to [2^7, 2^8).
-    const int up = m ? min(7 - ((int)(m >> 7) - 127), 120) : 0;
-    const float f = __uint_as_float((uint32_t)(up + 127) << 23);
-    if (lane == 0)
-      sm.fq[h] = m >= 0x7F80u ? __uint_as_float(0x7FC00000u)
-                              : a.c2 * __uint_as_float((uint32_t)(127 - up) << 23);
+  for (int i = 0; i < kEach; ++i)
 #pragma unroll
-    for (int c = 0; c < 3; ++c) {
-      const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-      uint32_t hi[4], lo[4];
+    for (int c = 0; c < 2; ++c)
+      v[i][c] = gh0 + i < a.H ? __ldg(src + i * (kDqk / 8) + c * 32 + lane) : none;
+  uint32_t mr = chunk_amax(rope);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 x = make_float2(__uint_as_float(w[k] << 16) * f,
-                                     __uint_as_float(w[k] & 0xFFFF0000u) * f);
-        const __half2 xh = __float22half2_rn(x);
-        hi[k] = to_e4m3x2(xh);
-        lo[k] = to_e4m3x2(__hsub2(xh, of_e4m3x2(hi[k])));
-      }
-      const uint2 ph = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-      const uint2 pl = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-      const int d = (c * 32 + lane) * 8;     // first dimension of the chunk
-      if (d < kDv) {
-        uint8_t* blk = sm.q[d >> 7] + (d & 8);
-        const int at = (((d & 127) >> 4) ^ (h & 7)) << 4;      // heads and 64 + heads alike
-        *reinterpret_cast<uint2*>(blk + h * 128 + at) = ph;
-        *reinterpret_cast<uint2*>(blk + (kHeads + h) * 128 + at) = pl;
-      } else if (d < kDqk) {
-        uint8_t* blk = sm.qrope + (d & 8);
-        const int at = (((d & 63) >> 4) ^ ((h >> 1) & 3)) << 4;
-        *reinterpret_cast<uint2*>(blk + h * 64 + at) = ph;
-        *reinterpret_cast<uint2*>(blk + (kHeads + h) * 64 + at) = pl;
-      }
+  for (int o = 1; o < 8; o <<= 1) mr = max(mr, __shfl_xor_sync(kFull, mr, o));
+  int rope_up = 0;
+  float factor = 0.f;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int h = h0 + i;
+    const uint32_t m = max(__reduce_max_sync(kFull, max(chunk_amax(v[i][0]), chunk_amax(v[i][1]))),
+                           __shfl_sync(kFull, mr, 8 * i));
+    const int up = query_up(m);
+    if (ri == i) rope_up = up;
+    if (lane == i) factor = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : a.c2 * pow2(-up);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      // Heads h and 64 + h (the second parts) share a swizzle phase.
+      const int chunk = c * 32 + lane;       // of 8 values; two make 16 codes
+      uint8_t* at = sm.q[chunk >> 4] + h * 128 + ((((chunk >> 1) & 7) ^ (h & 7)) << 4) + (chunk & 1) * 8;
+      split_chunk(v[i][c], pow2(up), at, at + kHeads * 128);
     }
   }
+  const int h = h0 + ri;
+  uint8_t* at = sm.qrope + h * 64 + ((((lane & 7) >> 1) ^ ((h >> 1) & 3)) << 4) + (lane & 1) * 8;
+  split_chunk(rope, pow2(rope_up), at, at + kHeads * 64);
   proxy_fence();
   __syncwarp();
   if (lane == 0) mbar_arrive1(&sm.qfull);
+  return factor;
 }
 
-// Sums of 32 registers over the warp: lane h gets register h's.
-__device__ __forceinline__ float transpose_sum(float (&v)[32]) {
+// Sums of 16 values over the warp: lanes i and 16 + i get value i's.
+__device__ __forceinline__ float transpose_sum(const float2 (&v2)[8]) {
   const int lane = threadIdx.x & 31;
+  float v[16];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int i = 0; i < 16; ++i) v[i] = i & 1 ? v2[i / 2].y : v2[i / 2].x;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
       if (i < o) {
         const bool up = lane & o;
         const float mine = up ? v[i + o] : v[i], other = up ? v[i] : v[i + o];
         v[i] = mine + __shfl_xor_sync(kFull, other, o);
       }
-  return v[0];
+  return v[0] + __shfl_xor_sync(kFull, v[0], 16);
 }
 
 // ---- the softmax and the outputs ---------------------------------------------------
-// Warp w reads the scores of tokens 32 (w % 4) .. + 31 (its tensor-memory
-// lanes) for 32 of the 64 heads: half `hh`, chosen so that warps 0-3 handle the
-// heads whose outputs lie in their lanes (head h with dimensions 0-127 of each
-// 256 in lane h, with dimensions 128-255 in lane 64 + h).  The four warps of a
-// half exchange their maxima and take the same decisions from them.
+// Warp 4 g + q reads the scores of tokens 32 q .. + 31 (its tensor-memory lanes)
+// for the 16 heads of group g.  The four warps of a group exchange what they
+// need and take the same decisions from it.  O holds head h with dimensions
+// 0-127 of each 256 in lane h, with dimensions 128-255 in lane 64 + h.
 __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm, uint32_t tmem,
-                                                  int s, int count, int ntiles,
-                                                  const int32_t* list, int64_t head0, int nheads) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3;
-  const int hh = warp < 4 ? (quad & 1) : ((quad & 1) ^ 1);
-  const int token = quad * 32 + lane, col = hh * 32 + lane;
+                                                  int hg, int p0, int p1) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3, grp = warp >> 2;
+  const int token = quad * 32 + lane, col0 = grp * kGroupHeads, col = col0 + (lane & 15);
+  const int nheads = min(kHeads, a.H - hg * kHeads);
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-  const float* scales = a.scales + (int64_t)s * a.n_blocks;
-  // The scale of this thread's token of tile t; `in` false for one left out.
-  auto token_scale = [&](int t, bool* in) {
-    const int j = t * kTile + token;
-    const int slot = j < count ? __ldg(list + j) : -1;
-    *in = slot >= 0 && slot < a.n_slots;
-    return *in ? __ldg(scales + fdiv((uint32_t)slot, a.fblock)) : 0.f;
+  bool ok = true;
+  // A wait that fails leaves `ok` false; nothing is written out then.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!wait_or_abort(sm, bar, parity)) ok = false;
+    __syncwarp();
   };
-  bool in_next, odd = false;
-  float ts_next = token_scale(0, &in_next);
-  float ref = -INFINITY;                     // of head `col`
-  float l[32], gone[32];                     // weights; weights less their two parts
-#pragma unroll
-  for (int i = 0; i < 32; ++i) l[i] = gone[i] = 0.f;
-  bool ok = wait_or_abort(sm, &sm.qfull, 0);   // fq is there
-  for (int t = 0; __all_sync(kFull, ok) && t < ntiles; ++t) {
-    const int sb = t & 1;
-    const float ts = ts_next;
-    const bool in = in_next;
-    if (t + 1 < ntiles) ts_next = token_scale(t + 1, &in_next);
-    odd |= in && !(ts == 0.f || (ts >= kMinScale && ts <= kMaxScale));
-    const float rts = ts > 0.f ? __frcp_rn(ts) : 0.f;
-    const float lt = ts > 0.f ? __log2f(ts) : 0.f;
-    ok = wait_or_abort(sm, &sm.sfull[sb], (uint32_t)(t >> 1) & 1u);
-    if (!__all_sync(kFull, ok)) break;
-    tc_fence_after();
-    float y[32];
-    {
-      uint32_t hi[32], lo[32];
-      tmem_ld32(lanes + kSCol + sb * 128 + hh * 32, hi);
-      tmem_ld32(lanes + kSCol + sb * 128 + kHeads + hh * 32, lo);
-      tmem_wait(hi);
-      tmem_wait(lo);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive1(&sm.sfree[sb]);
-      const float4* fq = reinterpret_cast<const float4*>(sm.fq + hh * 32);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 f = fq[i];
-        const float ff[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float x = (__uint_as_float(hi[4 * i + k]) + __uint_as_float(lo[4 * i + k])) * ts;
-          y[4 * i + k] = in ? x * ff[k] : -INFINITY;
-        }
-      }
-    }
-    float mine = 0.f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float m = warp_max(y[i] + lt);
-      if (lane == i) mine = m;
-    }
-    sm.part[sb][quad][col] = mine;
+  auto arrive = [&](uint64_t* bar) {
     __syncwarp();
-    if (lane == 0) mbar_arrive1(&sm.group[hh]);
-    ok = wait_or_abort(sm, &sm.group[hh], (uint32_t)t & 1u);
-    if (!__all_sync(kFull, ok)) break;
-    const float mx = fmaxf(fmaxf(sm.part[sb][0][col], sm.part[sb][1][col]),
-                           fmaxf(sm.part[sb][2][col], sm.part[sb][3][col]));
-    const bool move = mx > ref + kGap || (ref == -INFINITY && mx > -INFINITY);
-    const float now = move ? mx - kTop : ref;
-    const float alpha = move && ref > -INFINITY ? fast_exp2(ref - now) : 1.f;
-    const unsigned moved = __ballot_sync(kFull, alpha != 1.f);
-    ref = now;
-    sm.ref[sb][col] = now == -INFINITY ? 0.f : now;   // the half's four warps alike
-    __syncwarp();
-    if (moved) {
+    if (lane == 0) mbar_arrive1(bar);
+  };
+  // Nothing selected on a shard: O = 0, lse2 = -inf.
+  for (int p = p0 + warp; p < p1; p += kSoftmaxWarps) {
+    int shard;
+    const int64_t at = list_of(a, p, &shard);
+    if (__ldg(a.counts + at) > 0) continue;
+    const int64_t head0 = at * a.H + hg * kHeads;
+    for (int i = lane; i < nheads * (kDv / 8); i += 32)
+      reinterpret_cast<uint4*>(a.out + head0 * kDv)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = lane; i < nheads; i += 32) a.lse2[head0 + i] = -INFINITY;
+  }
+  Cursor cur(a, sm, p0, p1);
+  if (cur.valid(p1)) {
+    const float f = split_query(a, sm, row_of(a, cur.p), hg);
+    if (lane < 4) sm.fq[4 * warp + lane] = f;
+    barrier(1 + kGroups, kSoftmaxWarps * 32);
+  }
+  int n = 0;                                 // tiles done
+#pragma unroll 1
+  while (cur.valid(p1)) {
+    const int p = cur.p, ntiles = (cur.count + kTile - 1) / kTile;
+    cur.next_pair(a, sm, p0, p1);
+    const bool first = cur.valid(p1) && row_of(a, cur.p) != row_of(a, p);   // of its row
+    // The last pair's sums have been read, and a new row's factors are there.
+    if (n > 0) barrier(1 + kGroups, kSoftmaxWarps * 32);
+    const float4* fq = reinterpret_cast<const float4*>(sm.fq + col0);
+    float ref = 0.f;                         // of head `col`
+    bool fresh = true;                       // every token so far left out: no reference yet
+    float2 l[8], gone[8];                    // weights; weights less their two parts
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float f = __shfl_sync(kFull, alpha, i);
-        l[i] *= f;
-        gone[i] *= f;
+    for (int i = 0; i < 8; ++i) l[i] = gone[i] = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int t = 0; t < ntiles; ++t, ++n) {
+      const int sb = n & 1;
+      if (first && t + 1 == ntiles) {
+        // The next row's query on its way to L2, 128 bytes a thread.
+        const char* q = reinterpret_cast<const char*>(
+            a.q + ((int64_t)row_of(a, cur.p) * a.H + hg * kHeads) * kDqk);
+        for (int i = threadIdx.x; i < nheads * kDqk / 64; i += kSoftmaxWarps * 32)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i * 128));
       }
-    }
-    uint32_t phi[8], plo[8];
-    const float4* rf = reinterpret_cast<const float4*>(sm.ref[sb] + hh * 32);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 r = rf[i];
-      const float rr[4] = {r.x, r.y, r.z, r.w};
-      uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int e = 4 * i + 2 * k;
-        const float p0 = fast_exp2(y[e] - rr[2 * k]), p1 = fast_exp2(y[e + 1] - rr[2 * k + 1]);
-        l[e] += p0;
-        l[e + 1] += p1;
-        const __half2 p = __floats2half2_rn(p0 * ts, p1 * ts);
-        hi[k] = to_e4m3x2(p);
-        const __half2 rest = __hsub2(p, of_e4m3x2(hi[k]));
-        lo[k] = to_e5m2x2(rest);
-        const float2 lost = __half22float2(__hsub2(rest, of_e5m2x2(lo[k])));
-        gone[e] = fmaf(lost.x, rts, gone[e]);
-        gone[e + 1] = fmaf(lost.y, rts, gone[e + 1]);
-      }
-      phi[i] = hi[0] | (hi[1] << 16);
-      plo[i] = lo[0] | (lo[1] << 16);
-    }
-    // The last tile's value products are done: its weights' space is free and
-    // O holds every earlier tile.
-    if (t > 0) ok = wait_or_abort(sm, &sm.pvdone, (uint32_t)(t - 1) & 1u);
-    if (!__all_sync(kFull, ok)) break;
-    if (moved && warp < 4 && t > 0) {
+      wait(&sm.fullB[sb], (uint32_t)(n >> 1) & 1u);   // the token's scale is there
+      const float held = sm.tok[sb][token], ts = fmaxf(held, 0.f);
+      const bool in = held >= 0.f;
+      const float lt = ts > 0.f ? __log2f(ts) : 0.f;
+      wait(&sm.sfull[sb], (uint32_t)(n >> 1) & 1u);
       tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(lanes + kOCol + c, o);
-        tmem_wait(o);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-        tmem_st32(lanes + kOCol + c, o);
-      }
-      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-    }
-    uint8_t* dh = sm.rope[sb] + token * 64;
-    uint8_t* dl = sm.plo + token * 64;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int at = ((2 * hh + c) ^ ((token >> 1) & 3)) << 4;
-      *reinterpret_cast<uint4*>(dh + at) =
-          make_uint4(phi[4 * c], phi[4 * c + 1], phi[4 * c + 2], phi[4 * c + 3]);
-      *reinterpret_cast<uint4*>(dl + at) =
-          make_uint4(plo[4 * c], plo[4 * c + 1], plo[4 * c + 2], plo[4 * c + 3]);
-    }
-    proxy_fence();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive1(&sm.pfull);
-  }
-  if (odd) raise_flag(a.flags, DSA_FLAG_BOUNDS);
-  // The sums over all tokens: 32 lanes, then the half's four warps.
-  auto half_sum = [&](float mine, int phase) {
-    sm.part[phase & 1][quad][col] = mine;
-    __syncwarp();
-    if (lane == 0) mbar_arrive1(&sm.group[hh]);
-    ok = wait_or_abort(sm, &sm.group[hh], (uint32_t)phase & 1u);
-    const float(*p)[kHeads] = sm.part[phase & 1];
-    return (p[0][col] + p[1][col]) + (p[2][col] + p[3][col]);
-  };
-  if (__all_sync(kFull, ok)) {
-    const float sum = half_sum(transpose_sum(l), ntiles);
-    const float less = __all_sync(kFull, ok) ? half_sum(transpose_sum(gone), ntiles + 1) : 0.f;
-    if (warp < 2) {                          // warp = hh
-      sm.fq[col] = sum == 0.f ? 0.f : 1.f / (sum - less);
-      if (__all_sync(kFull, ok) && col < nheads)
-        a.lse2[head0 + col] = sum == 0.f ? -INFINITY : ref + log2f(sum);
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive1(&sm.final);
-    ok = __all_sync(kFull, ok) && wait_or_abort(sm, &sm.final, 0) &&
-         wait_or_abort(sm, &sm.pvdone, (uint32_t)(ntiles - 1) & 1u);
-  }
-  if (!__all_sync(kFull, ok)) {
-    if (lane == 0 && !aborted(sm)) abort_cta(sm, a.flags);
-    return;
-  }
-  tc_fence_after();
-  const int h = (quad & 1) * 32 + lane, group = warp >> 2;
-  const float inv = sm.fq[h];
-  __nv_bfloat16* orow = a.out + (head0 + h) * kDv + group * 256 + (quad >> 1) * 128;
-#pragma unroll 1
-  for (int c = 0; c < 128; c += 32) {
-    uint32_t o[32];
-    tmem_ld32(lanes + kOCol + group * 128 + c, o);
-    tmem_wait(o);
-    if (h < nheads) {
-      uint4* dst = reinterpret_cast<uint4*>(orow + c);
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        uint32_t b[4];
+      // Exponents of 16 heads relative to their references: the query's parts
+      // added, times the token's scale and the head's factor.
+      float2 x[8];
+      {
+        uint32_t hi[16], lo[16];
+        tmem_ld16(lanes + kSCol + sb * 128 + col0, hi);
+        tmem_ld16(lanes + kSCol + sb * 128 + kHeads + col0, lo);
+        const float4* rf = reinterpret_cast<const float4*>(sm.ref[sb ^ 1] + col0);
+        const float2 t2 = make_float2(ts, ts);
+        tmem_wait(hi);
+        tmem_wait(lo);
+        tc_fence_before();
+        arrive(&sm.sfree[sb]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 x =
-              __floats2bfloat162_rn(__uint_as_float(o[8 * v + 2 * i]) * inv,
-                                    __uint_as_float(o[8 * v + 2 * i + 1]) * inv);
-          b[i] = *reinterpret_cast<const uint32_t*>(&x);
+          const float4 f = fq[i], r = t > 0 ? rf[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float2 u = fadd2(
+              make_float2(__uint_as_float(hi[4 * i]), __uint_as_float(hi[4 * i + 1])),
+              make_float2(__uint_as_float(lo[4 * i]), __uint_as_float(lo[4 * i + 1])));
+          const float2 v = fadd2(
+              make_float2(__uint_as_float(hi[4 * i + 2]), __uint_as_float(hi[4 * i + 3])),
+              make_float2(__uint_as_float(lo[4 * i + 2]), __uint_as_float(lo[4 * i + 3])));
+          x[2 * i] = ffma2(fmul2(u, t2), make_float2(f.x, f.y), make_float2(-r.x, -r.y));
+          x[2 * i + 1] = ffma2(fmul2(v, t2), make_float2(f.z, f.w), make_float2(-r.z, -r.w));
         }
-        dst[v] = make_uint4(b[0], b[1], b[2], b[3]);
+      }
+      if (!__all_sync(kFull, in)) {          // a last tile, or a token left out
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (!in) x[i] = make_float2(-INFINITY, -INFINITY);
+      }
+      // The references stay unless some weight of the group's heads would pass
+      // its bound: then, as for a pair's first tile, the heads' maxima decide
+      // the new ones.
+      bool moves = fresh;
+      if (!fresh) {
+        float2 top = x[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+          top.x = fmaxf(top.x, x[i].x);
+          top.y = fmaxf(top.y, x[i].y);
+        }
+        moves = barrier_or(1 + grp, 128, fmaxf(top.x, top.y) + lt > kGap);
+      }
+      float alpha = 1.f;
+      if (moves) {
+        float mine = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float m = warp_max((i & 1 ? x[i / 2].y : x[i / 2].x) + lt);
+          if ((lane & 15) == i) mine = m;
+        }
+        sm.part[quad][col] = mine;
+        barrier(1 + grp, 128);
+        // Relative to `ref`; -inf where the tile has no token.
+        const float mx = fmaxf(fmaxf(sm.part[0][col], sm.part[1][col]),
+                               fmaxf(sm.part[2][col], sm.part[3][col]));
+        const bool move = fresh ? mx > -INFINITY : mx > kGap;
+        const float up = move ? mx - kTop : 0.f;
+        if (!fresh) alpha = fast_exp2(-up);
+        fresh = fresh && !__any_sync(kFull, move);
+        ref += up;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 d = make_float2(__shfl_sync(kFull, up, 2 * i), __shfl_sync(kFull, up, 2 * i + 1));
+          x[i] = fadd2(x[i], make_float2(-d.x, -d.y));
+          const float2 f = make_float2(__shfl_sync(kFull, alpha, 2 * i),
+                                       __shfl_sync(kFull, alpha, 2 * i + 1));
+          l[i] = fmul2(l[i], f);
+          gone[i] = fmul2(gone[i], f);
+        }
+        // The maxima have been read before another tile's are written.
+        barrier(1 + grp, 128);
+      }
+      sm.ref[sb][col] = ref;                 // the group's four warps alike
+      const float rts = ts > 0.f ? __frcp_rn(ts) : 0.f;
+      uint32_t phi[4], plo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int e = 2 * i + k;
+          const float2 w = make_float2(fast_exp2(x[e].x), fast_exp2(x[e].y));
+          l[e] = fadd2(l[e], w);
+          // The token's scale goes with its weight into the value product.
+          const float2 wt = fmul2(w, make_float2(ts, ts));
+          const __half2 pw = __floats2half2_rn(wt.x, wt.y);
+          hi[k] = to_e4m3x2(pw);
+          const __half2 rest = __hsub2(pw, of_e4m3x2(hi[k]));
+          lo[k] = to_e5m2x2(rest);
+          const float2 lost = __half22float2(__hsub2(rest, of_e5m2x2(lo[k])));
+          gone[e] = ffma2(lost, make_float2(rts, rts), gone[e]);
+        }
+        phi[i] = hi[0] | (hi[1] << 16);
+        plo[i] = lo[0] | (lo[1] << 16);
+      }
+      // The last tile's value products are done (its weights' space is free and
+      // O holds every earlier tile).
+      if (n > 0) wait(&sm.pvdone, (uint32_t)(n - 1) & 1u);
+      // A reference has moved: the group's heads of O, 16 lanes of two quads.
+      if (__any_sync(kFull, alpha != 1.f) && (quad & 1) == (grp >> 1)) {
+        tc_fence_after();
+        const float up = __shfl_sync(kFull, alpha, lane >> 2);
+        const float down = __shfl_sync(kFull, alpha, 8 + (lane >> 2));
+        const uint32_t o16 = lanes + ((uint32_t)(grp & 1) << 20) + kOCol;
+#pragma unroll 1
+        for (int c = 0; c < 256; c += 32) {
+          uint32_t o[16];
+          tmem_ld32_of16(o16 + c, o);
+          tmem_wait(o);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * (i & 2 ? down : up));
+          tmem_st32_of16(o16 + c, o);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      }
+      const int at = token * 64 + ((grp ^ ((token >> 1) & 3)) << 4);
+      *reinterpret_cast<uint4*>(sm.rope[sb] + at) = make_uint4(phi[0], phi[1], phi[2], phi[3]);
+      *reinterpret_cast<uint4*>(sm.plo + at) = make_uint4(plo[0], plo[1], plo[2], plo[3]);
+      proxy_fence();
+      tc_fence_before();
+      arrive(&sm.pfull);
+    }
+    // The sums over all tokens: 32 lanes, then the group's four warps, exchanged
+    // in the weights' space once the value products have read it.
+    const float all = transpose_sum(l), less = transpose_sum(gone);
+    // This row's scores are done: the next row's query takes the place of this
+    // one's while the last value products run.
+    float factor = 0.f;
+    if (first) factor = split_query(a, sm, row_of(a, cur.p), hg);
+    wait(&sm.pvdone, (uint32_t)(n - 1) & 1u);
+    float* w = reinterpret_cast<float*>(sm.plo);
+    w[quad * kHeads + col] = all;
+    w[(4 + quad) * kHeads + col] = less;
+    if (quad == 0) w[8 * kHeads + col] = ref;
+    barrier(1 + kGroups, kSoftmaxWarps * 32);
+    if (first && lane < 4) sm.fq[4 * warp + lane] = factor;   // read after the next such barrier
+    tc_fence_after();
+    const bool good = __all_sync(kFull, ok);
+    int shard;
+    const int64_t head0 = list_of(a, p, &shard) * a.H + hg * kHeads;   // first head of the CTA's
+    auto sum_of = [&](int h, float* off) {
+      const float* y = w + h;
+      *off = (y[4 * kHeads] + y[5 * kHeads]) + (y[6 * kHeads] + y[7 * kHeads]);
+      return (y[0] + y[kHeads]) + (y[2 * kHeads] + y[3 * kHeads]);
+    };
+    if (warp < 2 && good) {
+      const int h = warp * 32 + lane;
+      float off;
+      const float sum = sum_of(h, &off);
+      if (h < nheads)
+        a.lse2[head0 + h] = sum == 0.f ? -INFINITY : w[8 * kHeads + h] + log2f(sum);
+    }
+    // The warp's 32 tensor-memory lanes hold heads (quad & 1) 32 + lane with 64
+    // of their dimensions.  16 lanes and 32 columns at a time; four threads hold
+    // 8 columns of a head two by two and exchange them, so that each stores 16
+    // bytes and the four 64 contiguous ones.
+    float inv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float off;
+      const float sum = sum_of((quad & 1) * 32 + 8 * i + (lane >> 2), &off);
+      inv[i] = sum == 0.f ? 0.f : 1.f / (sum - off);
+    }
+    const int j = lane & 3;
+    __nv_bfloat16* orow = a.out + (head0 + (quad & 1) * 32 + (lane >> 2)) * kDv + (grp >> 1) * 256 +
+                          (quad >> 1) * 128 + (grp & 1) * 64 + j * 8;
+#pragma unroll
+    for (int part = 0; part < 4; ++part) {
+      const int up16 = part >> 1, c = (part & 1) * 32;
+      uint32_t o[16];
+      tmem_ld32_of16(lanes + ((uint32_t)up16 << 20) + kOCol + grp * 64 + c, o);
+      tmem_wait(o);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) { // heads lane / 4, then 8 + lane / 4
+        const float f = inv[2 * up16 + half];
+        uint32_t b[4];                       // word j of the 16 bytes of columns 8 i ..
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 y =
+              __floats2bfloat162_rn(__uint_as_float(o[4 * i + 2 * half]) * f,
+                                    __uint_as_float(o[4 * i + 2 * half + 1]) * f);
+          b[i] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+#pragma unroll
+        for (int x = 1; x < 4; x <<= 1)      // a 4 by 4 transposition over the threads
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(i & x)) {
+              const bool high = j & x;
+              const uint32_t give = high ? b[i] : b[i + x];
+              const uint32_t got = __shfl_xor_sync(kFull, give, x);
+              if (high) b[i] = got;
+              else b[i + x] = got;
+            }
+        const int h = up16 * 16 + half * 8;
+        if (good && (quad & 1) * 32 + h + (lane >> 2) < nheads)
+          *reinterpret_cast<uint4*>(orow + (int64_t)h * kDv + c) = make_uint4(b[0], b[1], b[2], b[3]);
       }
     }
   }
+  if (!__all_sync(kFull, ok) && lane == 0 && !aborted(sm)) abort_cta(sm, a.flags);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(const MlaFp8Args a) {
   extern __shared__ __align__(1024) unsigned char mla_fp8_smem[];
   Smem& sm = *reinterpret_cast<Smem*>(mla_fp8_smem);
   const int tid = threadIdx.x, warp = tid >> 5;
-  const int hg = blockIdx.x % a.hgroups, pair = blockIdx.x / a.hgroups;
-  const int s = pair / a.rows, r = pair - s * a.rows;
-  int count = __ldg(a.counts + pair);
-  if ((count < 0 || count > a.K) && tid == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);
-  count = min(max(count, 0), a.K);
-  const int ntiles = (count + kTile - 1) / kTile;
-  const int64_t head0 = (int64_t)pair * a.H + hg * kHeads;   // first head of the group
-  const int nheads = min(kHeads, a.H - hg * kHeads);
-  const int32_t* list = a.slots + (int64_t)pair * a.K;
+  // Neighbouring CTAs take the head groups of the same pairs, whose rows the
+  // second finds in L2.
+  const int hg = blockIdx.x % a.hgroups, g = blockIdx.x / a.hgroups, groups = gridDim.x / a.hgroups;
+  const int64_t pairs = (int64_t)a.rows * a.S;
+  const int p0 = (int)(pairs * g / groups), p1 = (int)(pairs * (g + 1) / groups);
 
-  if (count == 0) {
-    // Nothing selected on this shard: O = 0, lse2 = -inf.
-    for (int i = tid; i < nheads * (kDv / 8); i += kThreads)
-      reinterpret_cast<uint4*>(a.out + head0 * kDv)[i] = make_uint4(0, 0, 0, 0);
-    if (tid < nheads) a.lse2[head0 + tid] = -INFINITY;
-    return;
+  for (int p = p0 + tid; p < p1; p += kThreads) {
+    int shard;
+    const int count = __ldg(a.counts + list_of(a, p, &shard));
+    if (count < 0 || count > a.K) raise_flag(a.flags, DSA_FLAG_BOUNDS);
+    if (p - p0 < kCounts) sm.counts[p - p0] = min(max(count, 0), a.K);
   }
-
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&sm.tmem)),
@@ -727,9 +950,8 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.group[i], 4);
-      mbar_init(&sm.fullA[i], 64);           // every lane of the stage's two gathering warps
-      mbar_init(&sm.fullB[i], 64);
+      mbar_init(&sm.fullA[i], 32 * kGatherWarps);   // every gathering lane
+      mbar_init(&sm.fullB[i], 32 * kGatherWarps);
       mbar_init(&sm.emptyA[i], 1);
       mbar_init(&sm.emptyB[i], 1);
       mbar_init(&sm.sfull[i], 1);
@@ -737,9 +959,9 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
     }
     mbar_init(&sm.qfull, kSoftmaxWarps);
     mbar_init(&sm.pfull, kSoftmaxWarps);
-    mbar_init(&sm.final, kSoftmaxWarps);
     mbar_init(&sm.pvdone, 1);
-    mbar_init(&sm.drain, 1);
+    mbar_init(&sm.drain[0], 1);
+    mbar_init(&sm.drain[1], 1);
     sm.abort = 0;
     mbar_init_fence();
   }
@@ -749,12 +971,17 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
   const uint32_t tmem = sm.tmem;
 
   if (warp < kSoftmaxWarps) {
-    split_query(a, sm, r, hg);
-    softmax_and_store(a, sm, tmem, s, count, ntiles, list, head0, nheads);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    softmax_and_store(a, sm, tmem, hg, p0, p1);
   } else if (warp < kMmaWarp) {
-    gather_tiles(a, sm, (int64_t)s * a.n_slots, count, ntiles, list);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsGather));
+    gather_tiles(a, sm, p0, p1);
   } else {
-    if ((tid & 31) == 0) issue_mmas(a, sm, tmem, count, ntiles);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
+    if (tid == kMmaWarp * 32)
+      drain_mmas(a, sm, &sm.drain[0], issue_scores(a, sm, tmem, p0, p1));
+    else if (tid == (kMmaWarp + 1) * 32)
+      drain_mmas(a, sm, &sm.drain[1], issue_values(a, sm, tmem, p0, p1));
     __syncwarp();
   }
   tc_fence_before();
@@ -788,9 +1015,10 @@ extern "C" dsa_status dsa_sparse_mla_decode_fp8(const uint16_t* q, const uint8_t
   if (!q || !kv_cache || !block_scales || !slots || !counts || !out || !lse2)
     return DSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
-  const int hgroups = (H + kHeads - 1) / kHeads;
-  const int64_t blocks = (int64_t)rows * S * hgroups;
-  if (blocks > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  const int64_t hgroups = (H + kHeads - 1) / kHeads, pairs = (int64_t)rows * S;
+  if (pairs > INT32_MAX || hgroups > INT32_MAX / kSms) return DSA_ERR_UNSUPPORTED;
+  // One CTA an SM: as many groups of pairs as all SMs hold with each head group.
+  const int64_t groups = std::min<int64_t>(pairs, std::max<int64_t>(1, kSms / hgroups));
   const int smem = (int)sizeof(Smem);
   if (cudaFuncSetAttribute(sparse_mla_decode_fp8_kernel,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -803,15 +1031,18 @@ extern "C" dsa_status dsa_sparse_mla_decode_fp8(const uint16_t* q, const uint8_t
                      n_slots,
                      n_slots / block_tokens,
                      rows,
+                     S,
                      H,
                      K,
-                     hgroups,
+                     (int)hgroups,
                      scale * kLog2e,
                      reinterpret_cast<__nv_bfloat16*>(out),
                      lse2,
                      err_flags,
-                     FastDiv((uint32_t)block_tokens)};
-  const cudaError_t e = launch_kernel(sparse_mla_decode_fp8_kernel, dim3((unsigned)blocks),
-                                      dim3(kThreads), (size_t)smem, stream, 0u, a);
+                     FastDiv((uint32_t)block_tokens),
+                     FastDiv((uint32_t)S)};
+  const cudaError_t e =
+      launch_kernel(sparse_mla_decode_fp8_kernel, dim3((unsigned)(groups * hgroups)),
+                    dim3(kThreads), (size_t)smem, stream, 0u, a);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
