@@ -95,6 +95,7 @@ struct alignas(1024) Smem {
   float fq[kHeads];                          // scale log2(e) / the query's power of two
   float tok[kStages][kTile];                 // the tokens' scales; -1: left out
   int counts[kCounts];                       // of the CTA's first pairs
+  int first;                                 // the CTA's first token of its pair (split pairs)
   uint64_t qfull, fullA[kStages], fullB[kStages], emptyA[kStages], emptyB[kStages];
   uint64_t sfull[2], sfree[2], pfull, pvdone, drain[2];
   uint32_t tmem;
@@ -237,6 +238,39 @@ __device__ __forceinline__ bool barrier_or(int id, int threads, bool mine) {
 }
 __device__ __forceinline__ void barrier(int id, int threads) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// ---- clusters: a pair split over several CTAs ------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of the cluster's CTAs that has not exited.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this CTA's shared-memory location in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster16(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y),
+               "f"(v.z), "f"(v.w)
+               : "memory");
 }
 
 __device__ __forceinline__ bool aborted(const Smem& sm) {
@@ -383,10 +417,11 @@ __device__ __forceinline__ void gather_tiles(const MlaFp8Args& a, Smem& sm, int 
   const uint32_t rope0 = smem_u32(sm.rope[0]) + (uint32_t)(row0 + sub + (c >> 2) * 16) * 64;
   bool bad = false, ok = true;
   Cursor cur(a, sm, p0, p1);
+  const int32_t* slots = a.slots + sm.first;
   int shard = 0;
   int32_t slot[8];                           // of rows row0 + sub + 4 i, the next tile's
   auto fetch = [&]() {
-    const int32_t* list = a.slots + list_of(a, cur.p, &shard) * a.K;
+    const int32_t* list = slots + list_of(a, cur.p, &shard) * a.K;
     const int j0 = cur.t * kTile + row0 + sub;
 #pragma unroll
     for (int i = 0; i < 8; ++i) slot[i] = j0 + 4 * i < cur.count ? __ldg(list + j0 + 4 * i) : -1;
@@ -394,7 +429,7 @@ __device__ __forceinline__ void gather_tiles(const MlaFp8Args& a, Smem& sm, int 
   int32_t mine = -1;                         // the slot of row0 + lane, the next tile's
   auto fetch_mine = [&]() {
     const int j = cur.t * kTile + row0 + lane;
-    mine = j < cur.count ? __ldg(a.slots + list_of(a, cur.p, &shard) * a.K + j) : -1;
+    mine = j < cur.count ? __ldg(slots + list_of(a, cur.p, &shard) * a.K + j) : -1;
   };
   if (cur.valid(p1)) {
     fetch();
@@ -657,6 +692,16 @@ __device__ __forceinline__ float transpose_sum(const float2 (&v2)[8]) {
 // for the 16 heads of group g.  The four warps of a group exchange what they
 // need and take the same decisions from it.  O holds head h with dimensions
 // 0-127 of each 256 in lane h, with dimensions 128-255 in lane 64 + h.
+// The sums of a pair, in the weights' space: of each head 4 partial sums of the
+// weights, 4 of what rounding took from them, and the reference.
+constexpr int kSumRows = 9;
+__device__ __forceinline__ float head_sum(const float* w, int h, float* off) {
+  const float* y = w + h;
+  *off = (y[4 * kHeads] + y[5 * kHeads]) + (y[6 * kHeads] + y[7 * kHeads]);
+  return (y[0] + y[kHeads]) + (y[2 * kHeads] + y[3 * kHeads]);
+}
+
+template <bool kSplit>
 __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm, uint32_t tmem,
                                                   int hg, int p0, int p1) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3, grp = warp >> 2;
@@ -674,7 +719,7 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
     if (lane == 0) mbar_arrive1(bar);
   };
   // Nothing selected on a shard: O = 0, lse2 = -inf.
-  for (int p = p0 + warp; p < p1; p += kSoftmaxWarps) {
+  for (int p = p0 + warp; !kSplit && p < p1; p += kSoftmaxWarps) {
     int shard;
     const int64_t at = list_of(a, p, &shard);
     if (__ldg(a.counts + at) > 0) continue;
@@ -860,17 +905,13 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
     if (first && lane < 4) sm.fq[4 * warp + lane] = factor;   // read after the next such barrier
     tc_fence_after();
     const bool good = __all_sync(kFull, ok);
+    if (kSplit) break;                       // merged with the cluster's other parts
     int shard;
     const int64_t head0 = list_of(a, p, &shard) * a.H + hg * kHeads;   // first head of the CTA's
-    auto sum_of = [&](int h, float* off) {
-      const float* y = w + h;
-      *off = (y[4 * kHeads] + y[5 * kHeads]) + (y[6 * kHeads] + y[7 * kHeads]);
-      return (y[0] + y[kHeads]) + (y[2 * kHeads] + y[3 * kHeads]);
-    };
     if (warp < 2 && good) {
       const int h = warp * 32 + lane;
       float off;
-      const float sum = sum_of(h, &off);
+      const float sum = head_sum(w, h, &off);
       if (h < nheads)
         a.lse2[head0 + h] = sum == 0.f ? -INFINITY : w[8 * kHeads + h] + log2f(sum);
     }
@@ -882,7 +923,7 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float off;
-      const float sum = sum_of((quad & 1) * 32 + 8 * i + (lane >> 2), &off);
+      const float sum = head_sum(w, (quad & 1) * 32 + 8 * i + (lane >> 2), &off);
       inv[i] = sum == 0.f ? 0.f : 1.f / (sum - off);
     }
     const int j = lane & 3;
@@ -925,22 +966,144 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
   if (!__all_sync(kFull, ok) && lane == 0 && !aborted(sm)) abort_cta(sm, a.flags);
 }
 
+// ---- a split pair's parts together ---------------------------------------------
+// Every CTA of the cluster holds O and the sums of its part of the list.  Each
+// scales its O to the common reference and normaliser and writes it to the
+// CTA that owns the dimensions (512 / C of them a CTA, in the stages' space:
+// C parts of 64 heads, 16-byte chunks swizzled by the head), which adds the
+// parts in rank order.
+__device__ __forceinline__ void merge_parts(const MlaFp8Args& a, Smem& sm, uint32_t tmem, int hg, int p,
+                                            bool mine) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3, grp = warp >> 2;
+  const uint32_t rank = cluster_rank(), parts = cluster_size();
+  const int nheads = min(kHeads, a.H - hg * kHeads), dims = kDv / (int)parts;
+  int shard;
+  const int64_t head0 = list_of(a, p, &shard) * a.H + hg * kHeads;
+  float* w = reinterpret_cast<float*>(sm.plo);
+  if (!mine)
+    for (int i = threadIdx.x; i < kSumRows * kHeads; i += kThreads) w[i] = 0.f;
+  if (threadIdx.x == 0) sm.first = aborted(sm);
+  cluster_sync();
+  bool good = true;
+  for (uint32_t c = 0; c < parts; ++c) {
+    int bad;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                 : "=r"(bad)
+                 : "r"(in_cta(smem_u32(&sm.first), c))
+                 : "memory");
+    good = good && !bad;
+  }
+  if (warp < kSoftmaxWarps) {
+    const int h = (quad & 1) * 32 + lane;    // this thread's head, 64 of its dimensions
+    float top = -INFINITY, sum = 0.f, less = 0.f, own = 0.f;
+    auto part = [&](uint32_t c, float* off, float* ref) {
+      const uint32_t at = in_cta(smem_u32(w + h), c);
+      float y[kSumRows];
+#pragma unroll
+      for (int i = 0; i < kSumRows; ++i) y[i] = ld_cluster(at + i * kHeads * 4);
+      *off = (y[4] + y[5]) + (y[6] + y[7]);
+      *ref = y[8];
+      return (y[0] + y[1]) + (y[2] + y[3]);
+    };
+    for (uint32_t c = 0; c < parts; ++c) {
+      float off, ref;
+      if (part(c, &off, &ref) != 0.f) top = fmaxf(top, ref);
+    }
+    for (uint32_t c = 0; c < parts; ++c) {
+      float off, ref;
+      const float s = part(c, &off, &ref), f = s != 0.f ? fast_exp2(ref - top) : 0.f;
+      sum = fmaf(s, f, sum);
+      less = fmaf(off, f, less);
+      if (c == rank) own = f;
+    }
+    const float inv = sum == 0.f ? 0.f : own / (sum - less);
+    if (rank == 0 && warp < 2 && h < nheads && good)
+      a.lse2[head0 + h] = sum == 0.f ? -INFINITY : top + log2f(sum);
+    const int d0 = (grp >> 1) * 256 + (quad >> 1) * 128 + (grp & 1) * 64;
+    const uint32_t to = in_cta(smem_u32(sm.kv[0][0]), (uint32_t)(d0 / dims)) +
+                        (rank * kHeads + h) * (uint32_t)(dims * 4);
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    tc_fence_after();
+#pragma unroll
+    for (int c = 0; c < 64; c += 16) {
+      uint32_t o[16];
+      if (mine) {
+        tmem_ld16(lanes + kOCol + grp * 64 + c, o);
+        tmem_wait(o);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (mine)
+          v = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                          __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+        const int chunk = (d0 % dims + c) / 4 + i;
+        st_cluster16(to + (uint32_t)((chunk ^ (h & 7)) << 4), v);
+      }
+    }
+  }
+  cluster_sync();
+  const float4* in = reinterpret_cast<const float4*>(sm.kv[0][0]);
+  const int chunks = dims / 8;               // 8 dimensions, 16 bytes out
+  for (int i = threadIdx.x; i < nheads * chunks; i += kThreads) {
+    const int h = i / chunks, k = i - h * chunks;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    for (uint32_t c = 0; c < parts; ++c) {
+      const float4* row = in + (c * kHeads + h) * (dims / 4);
+      const float4 u = row[(2 * k) ^ (h & 7)], v = row[(2 * k + 1) ^ (h & 7)];
+      x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
+      y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+    }
+    const __nv_bfloat162 b[4] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w),
+                                 __floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
+    if (good)
+      *reinterpret_cast<uint4*>(a.out + (head0 + h) * kDv + rank * dims + k * 8) =
+          *reinterpret_cast<const uint4*>(b);
+  }
+}
+
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(const MlaFp8Args a) {
   extern __shared__ __align__(1024) unsigned char mla_fp8_smem[];
   Smem& sm = *reinterpret_cast<Smem*>(mla_fp8_smem);
   const int tid = threadIdx.x, warp = tid >> 5;
-  // Neighbouring CTAs take the head groups of the same pairs, whose rows the
-  // second finds in L2.
-  const int hg = blockIdx.x % a.hgroups, g = blockIdx.x / a.hgroups, groups = gridDim.x / a.hgroups;
+  // Neighbouring CTAs (clusters) take the head groups of the same pairs, whose
+  // rows the second finds in L2.
+  const int parts = kSplit ? (int)cluster_size() : 1;
+  const int unit = blockIdx.x / parts, units = gridDim.x / parts;
+  const int hg = unit % a.hgroups, g = unit / a.hgroups, groups = units / a.hgroups;
   const int64_t pairs = (int64_t)a.rows * a.S;
   const int p0 = (int)(pairs * g / groups), p1 = (int)(pairs * (g + 1) / groups);
 
-  for (int p = p0 + tid; p < p1; p += kThreads) {
+  int total = 0;                             // tokens of a split pair, over the cluster
+  for (int p = p0 + (kSplit ? 0 : tid); p < p1; p += kThreads) {
     int shard;
-    const int count = __ldg(a.counts + list_of(a, p, &shard));
-    if (count < 0 || count > a.K) raise_flag(a.flags, DSA_FLAG_BOUNDS);
-    if (p - p0 < kCounts) sm.counts[p - p0] = min(max(count, 0), a.K);
+    int count = __ldg(a.counts + list_of(a, p, &shard));
+    if ((count < 0 || count > a.K) && (!kSplit || tid == 0)) raise_flag(a.flags, DSA_FLAG_BOUNDS);
+    count = min(max(count, 0), a.K);
+    if (kSplit) {                            // the one pair: this CTA's tiles of it
+      total = count;
+      const int tiles = (count + kTile - 1) / kTile, rank = (int)cluster_rank();
+      const int lo = tiles * rank / parts * kTile, hi = tiles * (rank + 1) / parts * kTile;
+      if (tid == 0) {
+        sm.first = lo;
+        sm.counts[0] = min(count, hi) - min(count, lo);
+      }
+    } else if (p - p0 < kCounts) {
+      sm.counts[p - p0] = count;
+    }
   }
+  if (kSplit && total == 0) {
+    // Nothing selected on this shard: O = 0, lse2 = -inf.
+    int shard;
+    const int64_t head0 = list_of(a, p0, &shard) * a.H + hg * kHeads;
+    const int nheads = min(kHeads, a.H - hg * kHeads);
+    for (int i = tid; i < nheads * (kDv / 8) && cluster_rank() == 0; i += kThreads)
+      reinterpret_cast<uint4*>(a.out + head0 * kDv)[i] = make_uint4(0, 0, 0, 0);
+    if (cluster_rank() == 0 && tid < nheads) a.lse2[head0 + tid] = -INFINITY;
+    return;                                  // the whole cluster alike
+  }
+  if (!kSplit && tid == 0) sm.first = 0;
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&sm.tmem)),
@@ -972,7 +1135,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
 
   if (warp < kSoftmaxWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    softmax_and_store(a, sm, tmem, hg, p0, p1);
+    softmax_and_store<kSplit>(a, sm, tmem, hg, p0, p1);
   } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsGather));
     gather_tiles(a, sm, p0, p1);
@@ -986,6 +1149,11 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
   }
   tc_fence_before();
   __syncthreads();
+  if (kSplit) {
+    merge_parts(a, sm, tmem, hg, p0, sm.counts[0] > 0);
+    tc_fence_before();
+    __syncthreads();
+  }
   if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
@@ -1019,9 +1187,15 @@ extern "C" dsa_status dsa_sparse_mla_decode_fp8(const uint16_t* q, const uint8_t
   if (pairs > INT32_MAX || hgroups > INT32_MAX / kSms) return DSA_ERR_UNSUPPORTED;
   // One CTA an SM: as many groups of pairs as all SMs hold with each head group.
   const int64_t groups = std::min<int64_t>(pairs, std::max<int64_t>(1, kSms / hgroups));
+  // Few pairs: each over a cluster of as many CTAs as keep the SMs busy, two
+  // tiles or more a CTA (the merge costs about one).
+  const int tiles = (K + kTile - 1) / kTile;
+  unsigned parts = 1;
+  while (parts < 8 && pairs * hgroups * parts * 2 <= kSms && (int)parts * 4 <= tiles) parts *= 2;
   const int smem = (int)sizeof(Smem);
-  if (cudaFuncSetAttribute(sparse_mla_decode_fp8_kernel,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  const auto kernel =
+      parts > 1 ? sparse_mla_decode_fp8_kernel<true> : sparse_mla_decode_fp8_kernel<false>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return DSA_ERR_CUDA;
   const MlaFp8Args a{reinterpret_cast<const __nv_bfloat16*>(q),
                      kv_cache,
@@ -1042,7 +1216,7 @@ extern "C" dsa_status dsa_sparse_mla_decode_fp8(const uint16_t* q, const uint8_t
                      FastDiv((uint32_t)block_tokens),
                      FastDiv((uint32_t)S)};
   const cudaError_t e =
-      launch_kernel(sparse_mla_decode_fp8_kernel, dim3((unsigned)(groups * hgroups)),
-                    dim3(kThreads), (size_t)smem, stream, 0u, a);
+      launch_kernel(kernel, dim3((unsigned)(groups * hgroups * parts)), dim3(kThreads),
+                    (size_t)smem, stream, parts > 1 ? parts : 0u, a);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
