@@ -44,7 +44,8 @@ SIGNATURES = {
                           _i64, _p, _p], _i),
     "dsa_kv_cache_insert_fp8": ([_p, _p, _p, _i, _p, _p, _i64, _i, _p, _p, _p], _i),
     "dsa_sparse_mla_decode_fp8": ([_p, _p, _p, _i64, _i, _p, _p, _i, _i, _i, _i, ctypes.c_float,
-                                   _p, _p, _p, _p], _i),
+                                   _p, _p, _p, _p, _p], _i),
+    "dsa_sparse_mla_decode_fp8_work": ([_i, _i, _i, _i], _i64),
     "dsa_indexer_steps_noalloc": ([_p, _i64, _i, _i, _i, _i, _p, _p, _p, _i, _i, _i, _p, _p, _p,
                                    _p, _p, _p], _i),
 }

@@ -114,6 +114,7 @@ struct MlaFp8Args {
   float c2;                      // scale * log2(e)
   __nv_bfloat16* out;            // [S][rows][H][kDv]
   float* lse2;                   // [S][rows][H]
+  float* work;                   // a slot for every CTA of split pairs
   uint32_t* flags;
   FastDiv fblock, fS;
 };
@@ -256,23 +257,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The address of this CTA's shared-memory location in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void st_cluster16(uint32_t addr, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y),
-               "f"(v.z), "f"(v.w)
-               : "memory");
-}
-
 __device__ __forceinline__ bool aborted(const Smem& sm) {
   return *reinterpret_cast<const volatile int*>(&sm.abort) != 0;
 }
@@ -615,10 +599,10 @@ __device__ __forceinline__ void split_chunk(const uint4& v, float f, uint8_t* hi
 }
 __device__ __forceinline__ uint32_t chunk_amax(const uint4& v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t m = 0;
+  uint32_t m = 0;                            // two at a time: bits order magnitudes
 #pragma unroll
-  for (int k = 0; k < 4; ++k) m = max(m, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-  return m;
+  for (int k = 0; k < 4; ++k) m = __vmaxu2(m, w[k] & 0x7FFF7FFFu);
+  return max(m & 0xFFFFu, m >> 16);
 }
 // 2^up brings a head's largest value (bf16 bits m) to [2^7, 2^8).
 __device__ __forceinline__ int query_up(uint32_t m) {
@@ -694,7 +678,6 @@ __device__ __forceinline__ float transpose_sum(const float2 (&v2)[8]) {
 // 0-127 of each 256 in lane h, with dimensions 128-255 in lane 64 + h.
 // The sums of a pair, in the weights' space: of each head 4 partial sums of the
 // weights, 4 of what rounding took from them, and the reference.
-constexpr int kSumRows = 9;
 __device__ __forceinline__ float head_sum(const float* w, int h, float* off) {
   const float* y = w + h;
   *off = (y[4 * kHeads] + y[5 * kHeads]) + (y[6 * kHeads] + y[7 * kHeads]);
@@ -967,98 +950,127 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
 }
 
 // ---- a split pair's parts together ---------------------------------------------
-// Every CTA of the cluster holds O and the sums of its part of the list.  Each
-// scales its O to the common reference and normaliser and writes it to the
-// CTA that owns the dimensions (512 / C of them a CTA, in the stages' space:
-// C parts of 64 heads, 16-byte chunks swizzled by the head), which adds the
-// parts in rank order.
+// Every CTA of the cluster writes the O of its part of the list, unscaled, and
+// its sums to its slot of the workspace: through shared memory (rows of 512
+// fp32, 16-byte chunks swizzled by the head against bank conflicts, and so they
+// stay) and bulk copies.  After one cluster barrier each reads all parts of the
+// 512 / C dimensions that are its own, from L2, and adds them in rank order.
+// (The same exchange through distributed shared memory, written or read 16
+// bytes a lane, moved about 5 bytes a cycle: 13 us of a 26 us call.)
+constexpr int kSlotFloats = kHeads * kDv + 4 * kHeads;   // O; sum, loss, reference, failed
+
 __device__ __forceinline__ void merge_parts(const MlaFp8Args& a, Smem& sm, uint32_t tmem, int hg, int p,
                                             bool mine) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3, grp = warp >> 2;
   const uint32_t rank = cluster_rank(), parts = cluster_size();
-  const int nheads = min(kHeads, a.H - hg * kHeads), dims = kDv / (int)parts;
-  int shard;
-  const int64_t head0 = list_of(a, p, &shard) * a.H + hg * kHeads;
-  float* w = reinterpret_cast<float*>(sm.plo);
-  if (!mine)
-    for (int i = threadIdx.x; i < kSumRows * kHeads; i += kThreads) w[i] = 0.f;
-  if (threadIdx.x == 0) sm.first = aborted(sm);
-  cluster_sync();
-  bool good = true;
-  for (uint32_t c = 0; c < parts; ++c) {
-    int bad;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                 : "=r"(bad)
-                 : "r"(in_cta(smem_u32(&sm.first), c))
-                 : "memory");
-    good = good && !bad;
+  const int nheads = min(kHeads, a.H - hg * kHeads);
+  float* slots = a.work + (int64_t)(blockIdx.x - rank) * kSlotFloats;   // of the cluster's CTAs
+  float* slot = slots + (int64_t)rank * kSlotFloats;
+  if (threadIdx.x < kHeads) {
+    const int h = threadIdx.x;
+    const float* w = reinterpret_cast<const float*>(sm.plo);
+    float off = 0.f;
+    float* to = slot + kHeads * kDv + h;
+    to[0] = mine ? head_sum(w, h, &off) : 0.f;
+    to[kHeads] = off;
+    to[2 * kHeads] = mine ? w[8 * kHeads + h] : 0.f;
+    to[3 * kHeads] = aborted(sm) ? 1.f : 0.f;
   }
-  if (warp < kSoftmaxWarps) {
+  if (mine) {
     const int h = (quad & 1) * 32 + lane;    // this thread's head, 64 of its dimensions
-    float top = -INFINITY, sum = 0.f, less = 0.f, own = 0.f;
-    auto part = [&](uint32_t c, float* off, float* ref) {
-      const uint32_t at = in_cta(smem_u32(w + h), c);
-      float y[kSumRows];
-#pragma unroll
-      for (int i = 0; i < kSumRows; ++i) y[i] = ld_cluster(at + i * kHeads * 4);
-      *off = (y[4] + y[5]) + (y[6] + y[7]);
-      *ref = y[8];
-      return (y[0] + y[1]) + (y[2] + y[3]);
-    };
-    for (uint32_t c = 0; c < parts; ++c) {
-      float off, ref;
-      if (part(c, &off, &ref) != 0.f) top = fmaxf(top, ref);
-    }
-    for (uint32_t c = 0; c < parts; ++c) {
-      float off, ref;
-      const float s = part(c, &off, &ref), f = s != 0.f ? fast_exp2(ref - top) : 0.f;
-      sum = fmaf(s, f, sum);
-      less = fmaf(off, f, less);
-      if (c == rank) own = f;
-    }
-    const float inv = sum == 0.f ? 0.f : own / (sum - less);
-    if (rank == 0 && warp < 2 && h < nheads && good)
-      a.lse2[head0 + h] = sum == 0.f ? -INFINITY : top + log2f(sum);
     const int d0 = (grp >> 1) * 256 + (quad >> 1) * 128 + (grp & 1) * 64;
-    const uint32_t to = in_cta(smem_u32(sm.kv[0][0]), (uint32_t)(d0 / dims)) +
-                        (rank * kHeads + h) * (uint32_t)(dims * 4);
+    float4* row = reinterpret_cast<float4*>(sm.kv[0][0]) + h * (kDv / 4);
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     tc_fence_after();
 #pragma unroll
     for (int c = 0; c < 64; c += 16) {
       uint32_t o[16];
-      if (mine) {
-        tmem_ld16(lanes + kOCol + grp * 64 + c, o);
-        tmem_wait(o);
-      }
+      tmem_ld16(lanes + kOCol + grp * 64 + c, o);
+      tmem_wait(o);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (mine)
-          v = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                          __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
-        const int chunk = (d0 % dims + c) / 4 + i;
-        st_cluster16(to + (uint32_t)((chunk ^ (h & 7)) << 4), v);
+      for (int i = 0; i < 4; ++i)
+        row[((d0 + c) / 4 + i) ^ (h & 7)] =
+            make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                        __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+    }
+    proxy_fence();
+    barrier(1 + kGroups, kSoftmaxWarps * 32);
+    if (lane == 0) {
+      constexpr int kBytes = kHeads * kDv * 4 / kSoftmaxWarps;
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                       reinterpret_cast<char*>(slot) + warp * kBytes),
+                   "r"(smem_u32(sm.kv[0][0]) + warp * kBytes), "r"(kBytes)
+                   : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+    }
+    __syncwarp();
+  }
+  __threadfence();
+  cluster_sync();
+  int shard;
+  const int64_t head0 = list_of(a, p, &shard) * a.H + hg * kHeads;
+  float* factor = reinterpret_cast<float*>(sm.plo);   // [C][64]
+  bool good = true;
+  if (threadIdx.x < kHeads) {
+    const int h = threadIdx.x;
+    float sum[8], off[8], ref[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      sum[c] = off[c] = ref[c] = 0.f;
+      if (c < (int)parts) {
+        const float* at = slots + (int64_t)c * kSlotFloats + kHeads * kDv + h;
+        sum[c] = __ldcg(at);
+        off[c] = __ldcg(at + kHeads);
+        ref[c] = __ldcg(at + 2 * kHeads);
+        good &= __ldcg(at + 3 * kHeads) == 0.f;
       }
     }
-  }
-  cluster_sync();
-  const float4* in = reinterpret_cast<const float4*>(sm.kv[0][0]);
-  const int chunks = dims / 8;               // 8 dimensions, 16 bytes out
-  for (int i = threadIdx.x; i < nheads * chunks; i += kThreads) {
-    const int h = i / chunks, k = i - h * chunks;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-    for (uint32_t c = 0; c < parts; ++c) {
-      const float4* row = in + (c * kHeads + h) * (dims / 4);
-      const float4 u = row[(2 * k) ^ (h & 7)], v = row[(2 * k + 1) ^ (h & 7)];
-      x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
-      y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+    float top = -INFINITY, all = 0.f, less = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (sum[c] != 0.f) top = fmaxf(top, ref[c]);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      ref[c] = sum[c] != 0.f ? fast_exp2(ref[c] - top) : 0.f;
+      all = fmaf(sum[c], ref[c], all);
+      less = fmaf(off[c], ref[c], less);
     }
-    const __nv_bfloat162 b[4] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w),
-                                 __floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
+    const float inv = all == 0.f ? 0.f : 1.f / (all - less);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < (int)parts) factor[c * kHeads + h] = ref[c] * inv;
+    if (rank == 0 && h < nheads && good)
+      a.lse2[head0 + h] = all == 0.f ? -INFINITY : top + log2f(all);
+  }
+  good = !barrier_or(1 + kGroups, kSoftmaxWarps * 32, !good);
+  const int chunks = kDv / 8 / (int)parts;   // of 8 dimensions, 16 bytes out
+  for (int i = threadIdx.x; i < nheads * chunks; i += kSoftmaxWarps * 32) {
+    const int h = i / chunks, k = 2 * ((int)rank * chunks + i - h * chunks);
+    uint32_t b[4];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const float4* at = reinterpret_cast<const float4*>(slots + h * kDv) + ((k + half) ^ (h & 7));
+      float4 u[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < (int)parts) u[c] = __ldcg(at + (int64_t)c * (kSlotFloats / 4));
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float f = c < (int)parts ? factor[c * kHeads + h] : 0.f;
+        if (f != 0.f)                        // a part without tokens has written nothing
+          x = make_float4(fmaf(u[c].x, f, x.x), fmaf(u[c].y, f, x.y), fmaf(u[c].z, f, x.z),
+                          fmaf(u[c].w, f, x.w));
+      }
+      const __nv_bfloat162 y0 = __floats2bfloat162_rn(x.x, x.y), y1 = __floats2bfloat162_rn(x.z, x.w);
+      b[2 * half] = *reinterpret_cast<const uint32_t*>(&y0);
+      b[2 * half + 1] = *reinterpret_cast<const uint32_t*>(&y1);
+    }
     if (good)
-      *reinterpret_cast<uint4*>(a.out + (head0 + h) * kDv + rank * dims + k * 8) =
-          *reinterpret_cast<const uint4*>(b);
+      *reinterpret_cast<uint4*>(a.out + (head0 + h) * kDv + k * 4) =
+          make_uint4(b[0], b[1], b[2], b[3]);
   }
 }
 
@@ -1136,9 +1148,11 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
   if (warp < kSoftmaxWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     softmax_and_store<kSplit>(a, sm, tmem, hg, p0, p1);
+    if (kSplit) merge_parts(a, sm, tmem, hg, p0, sm.counts[0] > 0);
   } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsGather));
     gather_tiles(a, sm, p0, p1);
+    if (kSplit) cluster_sync();              // the merge's barrier
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
     if (tid == kMmaWarp * 32)
@@ -1146,14 +1160,10 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
     else if (tid == (kMmaWarp + 1) * 32)
       drain_mmas(a, sm, &sm.drain[1], issue_values(a, sm, tmem, p0, p1));
     __syncwarp();
+    if (kSplit) cluster_sync();
   }
   tc_fence_before();
   __syncthreads();
-  if (kSplit) {
-    merge_parts(a, sm, tmem, hg, p0, sm.counts[0] > 0);
-    tc_fence_before();
-    __syncthreads();
-  }
   if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
@@ -1169,12 +1179,31 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 using namespace dsa;
 
+// Few pairs are split, each over a cluster of as many CTAs (at most 8) as keep
+// the SMs busy with four tiles or more a CTA before the last doubling: two
+// tiles cost about what the merge does.
+static int split_parts(int64_t pairs, int64_t hgroups, int K) {
+  const int tiles = (K + kTile - 1) / kTile;
+  int parts = 1;
+  if (pairs > kSms || hgroups > kSms) return parts;
+  while (parts < 8 && pairs * hgroups * parts * 2 <= kSms && parts * 4 <= tiles) parts *= 2;
+  return parts;
+}
+
+extern "C" int64_t dsa_sparse_mla_decode_fp8_work(int rows, int S, int H, int K) {
+  if (rows < 1 || S < 1 || S > DSA_MAX_SHARDS || H < 1 || K < 1) return 0;
+  const int64_t pairs = (int64_t)rows * S, hgroups = ((int64_t)H + kHeads - 1) / kHeads;
+  const int parts = split_parts(pairs, hgroups, K);
+  return parts > 1 ? pairs * hgroups * parts * kSlotFloats * 4 : 0;
+}
+
 extern "C" dsa_status dsa_sparse_mla_decode_fp8(const uint16_t* q, const uint8_t* kv_cache,
                                                 const float* block_scales, int64_t n_slots,
                                                 int block_tokens, const int32_t* slots,
                                                 const int32_t* counts, int rows, int S, int H,
                                                 int K, float scale, uint16_t* out, float* lse2,
-                                                uint32_t* err_flags, cudaStream_t stream) {
+                                                float* work, uint32_t* err_flags,
+                                                cudaStream_t stream) {
   if (rows < 0 || K < 1 || H < 1 || n_slots < 1 || block_tokens < 1 || n_slots % block_tokens ||
       !std::isfinite(scale))
     return DSA_ERR_INVALID_ARG;
@@ -1182,16 +1211,13 @@ extern "C" dsa_status dsa_sparse_mla_decode_fp8(const uint16_t* q, const uint8_t
   if (rows == 0) return DSA_OK;
   if (!q || !kv_cache || !block_scales || !slots || !counts || !out || !lse2)
     return DSA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
-  const int64_t hgroups = (H + kHeads - 1) / kHeads, pairs = (int64_t)rows * S;
+  if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(out) || !aligned16(work))
+    return DSA_ERR_INVALID_ARG;
+  const int64_t hgroups = ((int64_t)H + kHeads - 1) / kHeads, pairs = (int64_t)rows * S;
   if (pairs > INT32_MAX || hgroups > INT32_MAX / kSms) return DSA_ERR_UNSUPPORTED;
   // One CTA an SM: as many groups of pairs as all SMs hold with each head group.
   const int64_t groups = std::min<int64_t>(pairs, std::max<int64_t>(1, kSms / hgroups));
-  // Few pairs: each over a cluster of as many CTAs as keep the SMs busy, two
-  // tiles or more a CTA (the merge costs about one).
-  const int tiles = (K + kTile - 1) / kTile;
-  unsigned parts = 1;
-  while (parts < 8 && pairs * hgroups * parts * 2 <= kSms && (int)parts * 4 <= tiles) parts *= 2;
+  const unsigned parts = work ? (unsigned)split_parts(pairs, hgroups, K) : 1u;
   const int smem = (int)sizeof(Smem);
   const auto kernel =
       parts > 1 ? sparse_mla_decode_fp8_kernel<true> : sparse_mla_decode_fp8_kernel<false>;
@@ -1212,6 +1238,7 @@ extern "C" dsa_status dsa_sparse_mla_decode_fp8(const uint16_t* q, const uint8_t
                      scale * kLog2e,
                      reinterpret_cast<__nv_bfloat16*>(out),
                      lse2,
+                     work,
                      err_flags,
                      FastDiv((uint32_t)block_tokens),
                      FastDiv((uint32_t)S)};

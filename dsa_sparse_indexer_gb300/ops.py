@@ -7,6 +7,8 @@ CPU tensors are rejected.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _lib
@@ -352,11 +354,15 @@ INSERT_FP8_SMALL = 512           # DSA_INSERT_FP8_SMALL of include/dsa.h
 def _together(first: torch.Tensor, *others):
     """Every tensor on the first one's device, which becomes the current one
     for the launch (the returned context; None when it already is)."""
-    dev = first.device
+    dev = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
-    return None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"all tensors must be on {first.device}, got one on {t.device}")
+    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _raw_stream(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _launch(context, name: str, *args) -> None:
@@ -393,7 +399,7 @@ def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, scaling: str |
         raise ValueError("out must be [max_pos, rot_dim]")
     _launch(_together(out), "dsa_rope_table", max_pos, rot_dim, float(base),
             ROPE_SCALINGS[scaling], float(factor), orig_max_pos, float(beta_fast),
-            float(beta_slow), float(amplitude), _ptr(out), _stream(out))
+            float(beta_slow), float(amplitude), _ptr(out), _raw_stream(out))
     return out
 
 
@@ -445,7 +451,7 @@ def rotary_embed(x, positions, cos_sin_cache, layout: str = "interleaved", first
     _launch(context, "dsa_rotary_embed", _ptr(x), x_token, x_head, _ptr(positions),
             _ptr(cos_sin_cache), cos_sin_cache.shape[0], cos_sin_cache.shape[1], first, T, H, D,
             ROPE_DTYPES[dtype], ROPE_LAYOUTS[layout], int(bool(inverse)), _ptr(out), out_token,
-            out_head, _ptr(err_flags), _stream(x))
+            out_head, _ptr(err_flags), _raw_stream(x))
     return out
 
 
@@ -489,18 +495,25 @@ def kv_cache_insert_fp8(kv_rows, kpe_rows, slot_mapping, kv_cache, block_scales,
     context = _together(kv_cache, kv_rows, kpe_rows, slot_mapping, block_scales, work, err_flags)
     _launch(context, "dsa_kv_cache_insert_fp8", _ptr(kv_rows), _ptr(kpe_rows),
             _ptr(slot_mapping), T, _ptr(kv_cache), _ptr(block_scales), n_slots, block, _ptr(work),
-            _ptr(err_flags), _stream(kv_cache))
+            _ptr(err_flags), _raw_stream(kv_cache))
     return kv_cache, block_scales
 
 
+@functools.lru_cache(maxsize=None)
+def _mla_fp8_work(rows: int, S: int, H: int, K: int) -> int:
+    return _lib.load().dsa_sparse_mla_decode_fp8_work(rows, S, H, K) // 4
+
+
 def sparse_mla_decode_fp8(q, kv_cache, block_scales, slots, counts, scale: float, out=None,
-                          lse2=None, err_flags=None):
+                          lse2=None, work=None, err_flags=None):
     """sparse_mla_decode over an 8-bit cache (kv_cache_insert_fp8).
 
     q [rows, H, 576] bf16, kv_cache [S, n_slots, 576] uint8 (e4m3 codes),
     block_scales [S, n_blocks] fp32 (one for each n_slots / n_blocks slots),
     slots [S, rows, K] int32, counts [S, rows] int32 -> (out [S, rows, H, 512]
-    bf16, lse2 [S, rows, H] fp32, base 2)."""
+    bf16, lse2 [S, rows, H] fp32, base 2).  work: fp32 workspace of few-row
+    calls, dsa_sparse_mla_decode_fp8_work(rows, S, H, K) bytes (allocated when
+    not given)."""
     _need(q, "q", torch.bfloat16, 3)
     _need(kv_cache, "kv_cache", torch.uint8, 3)
     _need(block_scales, "block_scales", torch.float32, 2)
@@ -525,8 +538,15 @@ def sparse_mla_decode_fp8(q, kv_cache, block_scales, slots, counts, scale: float
     _need(lse2, "lse2", torch.float32, 3)
     if tuple(out.shape) != (S, rows, H, MLA_DV) or tuple(lse2.shape) != (S, rows, H):
         raise ValueError("out must be [S, rows, H, 512] and lse2 [S, rows, H]")
-    context = _together(q, kv_cache, block_scales, slots, counts, out, lse2, err_flags)
+    need = _mla_fp8_work(rows, S, H, K)
+    if work is None and need:
+        work = torch.empty(need, dtype=torch.float32, device=q.device)
+    if work is not None:
+        _need(work, "work", torch.float32, 1)
+        if work.shape[0] < need:
+            raise ValueError(f"work must have {need} entries")
+    context = _together(q, kv_cache, block_scales, slots, counts, out, lse2, work, err_flags)
     _launch(context, "dsa_sparse_mla_decode_fp8", _ptr(q), _ptr(kv_cache), _ptr(block_scales),
             n_slots, block, _ptr(slots), _ptr(counts), rows, S, H, K, float(scale), _ptr(out),
-            _ptr(lse2), _ptr(err_flags), _stream(q))
+            _ptr(lse2), _ptr(work), _ptr(err_flags), _raw_stream(q))
     return out, lse2

@@ -513,7 +513,17 @@ dsa_status dsa_kv_cache_insert_fp8(const uint16_t* kv_rows, const uint16_t* kpe_
  *   q            [rows][H][DSA_MLA_DQK] bf16, 16-byte aligned
  *   kv_cache     [S][n_slots][DSA_MLA_DQK] e4m3 codes, 16-byte aligned
  *   block_scales [S][n_slots / block_tokens] fp32
- *   slots, counts, out, lse2, err_flags, scale: as dsa_sparse_mla_decode
+ *   slots, counts, out, lse2, scale: as dsa_sparse_mla_decode
+ *   work         dsa_sparse_mla_decode_fp8_work(rows, S, H, K) bytes, contents
+ *                arbitrary, 16-byte aligned, or NULL: few (row, shard) pairs are
+ *                then not split over several CTAs.  Calls that may run at the
+ *                same time need their own.
+ *   err_flags    as dsa_sparse_mla_decode; DSA_FLAG_BOUNDS also if the scale of a
+ *                selected row's block is neither 0 nor in [2^-100, 2^100]
+ * Scores accumulate in fp32, from the query to 2^-18 of its head's largest
+ * value (exactly, above 2^-10 of it); a softmax weight enters the value product
+ * to 2^-7 of its size (2^-20 of the row's largest), which the normaliser
+ * follows.
  * A slot outside [0, n_slots) is left out and raises DSA_FLAG_BOUNDS; what
  * the cache holds there or elsewhere cannot reach the result.
  * Errors: rows < 0, K < 1, H < 1, n_slots < 1, block_tokens < 1, n_slots %
@@ -526,7 +536,10 @@ dsa_status dsa_sparse_mla_decode_fp8(const uint16_t* q, const uint8_t* kv_cache,
                                      int block_tokens, const int32_t* slots,
                                      const int32_t* counts, int rows, int S, int H, int K,
                                      float scale, uint16_t* out, float* lse2,
-                                     uint32_t* err_flags, cudaStream_t stream);
+                                     float* work, uint32_t* err_flags, cudaStream_t stream);
+
+/* Bytes of the workspace that dsa_sparse_mla_decode_fp8 uses for these sizes (0: none). */
+int64_t dsa_sparse_mla_decode_fp8_work(int rows, int S, int H, int K);
 
 /*
  * dsa_indexer_steps_noalloc - dsa_shard_topk_pack, dsa_merge_topk_stable and

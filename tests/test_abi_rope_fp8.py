@@ -78,14 +78,28 @@ def test_kv_cache_insert_fp8(lib):
 
 def test_sparse_mla_decode_fp8(lib):
     f = lib.dsa_sparse_mla_decode_fp8
-    #     q  cache scales n_slots block slots counts rows S H K scale out lse err stream
-    ok = (NULL, NULL, NULL, 128, 64, NULL, NULL, 0, 2, 16, 512, 0.1, NULL, NULL, NULL, NULL)
+    #     q  cache scales n_slots block slots counts rows S H K scale out lse work err stream
+    ok = (NULL, NULL, NULL, 128, 64, NULL, NULL, 0, 2, 16, 512, 0.1, NULL, NULL, NULL, NULL, NULL)
     assert f(*ok) == OK
-    some = (P, P, P, 128, 64, P, P, 3, 2, 16, 512, 0.1, P, P, NULL, NULL)
+    some = (P, P, P, 128, 64, P, P, 3, 2, 16, 512, 0.1, P, P, NULL, NULL, NULL)
     check(f, some, [(0, NULL), (1, NULL), (2, NULL), (5, NULL), (6, NULL), (12, NULL), (13, NULL),
-                    (0, P + 8), (1, P + 8), (12, P + 8), (3, 0), (3, 100), (4, 0), (7, -1),
+                    (0, P + 8), (1, P + 8), (12, P + 8), (14, P + 4), (3, 0), (3, 100), (4, 0),
+                    (7, -1),
                     (9, 0), (10, 0), (11, INF), (11, NAN)], INVALID)
     check(f, some, [(8, 0), (8, 65), (3, 2 ** 32), (7, 2 ** 30)], UNSUPPORTED)
+
+
+def test_sparse_mla_decode_fp8_work(lib):
+    f = lib.dsa_sparse_mla_decode_fp8_work
+    assert f(64, 4, 128, 2048) == 0                 # more pairs than SMs
+    one = f(1, 1, 128, 2048)
+    assert one == 2 * 8 * (64 * 512 + 256) * 4      # two head groups, eight parts
+    assert f(1, 1, 16, 2048) == one // 2
+    assert f(1, 1, 128, 300) == 0                   # three tiles: not worth a merge
+    for bad in ((0, 1, 128, 2048), (1, 0, 128, 2048), (1, 65, 128, 2048), (1, 1, 0, 2048),
+                (1, 1, 128, 0)):
+        assert f(*bad) == 0
+    assert f(2 ** 31 - 1, 64, 2 ** 31 - 1, 2 ** 31 - 1) == 0
 
 
 def test_binding_refusals():

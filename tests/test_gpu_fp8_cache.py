@@ -270,6 +270,35 @@ def test_few_and_many_rows(rows, S, K):
     _check(q, KF.values(codes, scales), slots, counts, SCALE, out, lse2, pairs)
 
 
+@pytest.mark.parametrize("rows,K", [(1, 2048), (3, 700)])
+def test_few_rows_without_a_workspace(rows, K):
+    """The C entry point with work = NULL does not split the lists; with it,
+    the parts' sum is within the same bounds, and any contents do."""
+    from dsa_sparse_indexer_gb300 import _lib
+    rng = np.random.default_rng(rows)
+    S, H, n_slots = 1, 100, 4096
+    codes, scales = _cache(rng, S, n_slots, 64, True)
+    q = W.mla_query(rows, H, seed=rows)
+    counts = np.full((S, rows), K)
+    counts[0, -1] = K // 2 + 5
+    slots = rng.integers(0, n_slots, (S, rows, K))
+    need = _lib.load().dsa_sparse_mla_decode_fp8_work(rows, S, H, K)
+    assert need > 0
+    args = [_bf(q), G.dev(codes), G.dev(scales), G.dev(slots.astype(np.int32)),
+            G.dev(counts.astype(np.int32))]
+    for work in (None, torch.full((need // 4,), float("nan"), device="cuda")):
+        g = G.Guards()
+        out, lse2 = g.empty((S, rows, H, 512), torch.bfloat16), g.empty((S, rows, H), torch.float32)
+        P = lambda t: None if t is None else t.data_ptr()      # noqa: E731
+        _lib.call("dsa_sparse_mla_decode_fp8", P(args[0]), P(args[1]), P(args[2]), n_slots, 64,
+                  P(args[3]), P(args[4]), rows, S, H, K, SCALE, P(out), P(lse2), P(work), None,
+                  torch.cuda.current_stream().cuda_stream)
+        g.check()
+        _check(q, KF.values(codes, scales), slots, counts, SCALE,
+               OC.bf16_to_f64(out.view(torch.int16).cpu().numpy().view(np.uint16)),
+               lse2.double().cpu().numpy())
+
+
 def _left_out_case():
     rng = np.random.default_rng(9)
     S, R, H, K, n_slots = 2, 3, 64, 512, 640
