@@ -56,12 +56,15 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const TableAr
 // ---- the rotation --------------------------------------------------------------
 //
 // A row is one head of one token: D values, of which [first, first + rot) turn
-// in pairs and the rest is carried.  Memory-bound: 16-byte accesses wherever
-// the layout allows them.  A unit is what one thread takes of a row: a vector
-// (interleaved pairs lie within it), or the two vectors at i and i + rot / 2 of
-// the half layout.  A thread takes the same unit of kRows consecutive rows:
-// their loads are all in flight at once, and heads of one token share one read
-// of the table.
+// in pairs and the rest is carried.  Memory-bound, and the arithmetic (unpacking,
+// four multiply-adds a pair, packing) close behind, so addresses and the
+// table's values are shared: a unit is what one thread takes of a row, a 16-byte
+// vector (interleaved pairs lie within it) or the two vectors at i and
+// i + rot / 2 of the half layout, and a thread takes the same unit of kRows
+// consecutive heads of a token, all loads in flight at once.
+// Measured: 4096 tokens of 128 heads of 64 (67 MB in, 67 MB out, strided) in
+// 37 us with every row's token, address and table read found anew, 28 us so; a
+// plain copy of as much takes 23.
 
 enum { kInterleaved = DSA_ROPE_INTERLEAVED, kHalf = DSA_ROPE_HALF };
 constexpr int kMaxWidth = 1024;               // values of a row
@@ -77,8 +80,8 @@ struct RotArgs {
   int units, turning;       // units of a row (the rotating ones first)
   int per_block;            // groups of rows side by side in a block
   float sign;               // -1 for the inverse rotation
-  int64_t rows;
-  FastDiv fH;
+  int64_t groups;           // of kRows heads
+  FastDiv fgroups;          // groups of a token
 };
 
 template <typename E> __device__ __forceinline__ float to_float(E v);
@@ -108,55 +111,62 @@ __global__ void __launch_bounds__(V == 1 ? kMaxWidth : 256) rotary_kernel(const 
   constexpr int kVecs = LAYOUT == kHalf || V == 1 ? 2 : 1;   // vectors of a rotating unit
   constexpr int kPairs = kVecs * V / 2;
   using VecT = Vec<E, V>;
-  const int g = threadIdx.x / a.units, u = threadIdx.x - g * a.units;
-  if (g >= a.per_block) return;
-  const int64_t row0 = ((int64_t)blockIdx.x * a.per_block + g) * kRows;
+  const int side = threadIdx.x / a.units, u = threadIdx.x - side * a.units;
+  const int64_t g = (int64_t)blockIdx.x * a.per_block + side;
+  if (side >= a.per_block || g >= a.groups) return;
+  uint32_t part;
+  const uint32_t tok = fdivmod((uint32_t)g, a.fgroups, &part);
+  const uint32_t head = part * kRows;
   const bool turning = u < a.turning;
-  // Element offsets of the unit's vectors, and its first pair.
-  int at0, at1 = 0, pair = 0;
+  // Element offsets of the unit's vectors, and its first pair.  A carried unit
+  // has as many vectors as a turning one, the last unit perhaps one less.
+  int at0, apart, pair = 0;
+  bool both = true;
   if (turning) {
     pair = u * kPairs;
     at0 = a.first + (LAYOUT == kHalf ? pair : 2 * pair);
-    at1 = LAYOUT == kHalf ? at0 + a.rot / 2 : at0 + 1;
+    apart = LAYOUT == kHalf ? a.rot / 2 : 1;
   } else {
-    at0 = (u - a.turning) * V;
+    at0 = (u - a.turning) * (kVecs * V);
+    both = at0 + V < a.D - a.rot;
+    apart = at0 < a.first && at0 + V >= a.first ? V + a.rot : V;
     if (at0 >= a.first) at0 += a.rot;
   }
+  const E* src = static_cast<const E*>(a.x) + tok * a.x_token + head * a.x_head + at0;
   VecT v[kRows][kVecs];
-  uint32_t tok[kRows], head[kRows];
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    if (row0 + k >= a.rows) break;
-    tok[k] = fdivmod((uint32_t)(row0 + k), a.fH, &head[k]);
-    const E* src = static_cast<const E*>(a.x) + tok[k] * a.x_token + head[k] * a.x_head;
-    v[k][0] = *reinterpret_cast<const VecT*>(src + at0);
-    if (kVecs == 2 && turning) v[k][kVecs - 1] = *reinterpret_cast<const VecT*>(src + at1);
+    v[k][0] = *reinterpret_cast<const VecT*>(src + k * a.x_head);
+    if (kVecs == 2 && both)
+      v[k][kVecs - 1] = *reinterpret_cast<const VecT*>(src + k * a.x_head + apart);
   }
-  float c[kPairs], s[kPairs];
-  uint32_t held = ~0u;
+  if (turning) {
+    constexpr int kP = kPairs > 4 ? 4 : kPairs;
+    using VecP = Vec<float, kP>;
+    float c[kPairs], s[kPairs];
+    const int pos = __ldg(a.positions + tok);
+    if (pos >= 0 && pos < a.max_pos) {
+      const float* row = a.table + (int64_t)pos * a.rot + pair;
 #pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    if (row0 + k >= a.rows) break;
-    if (turning) {
-      if (tok[k] != held) {
-        held = tok[k];
-        const int pos = __ldg(a.positions + held);
-        const bool in = pos >= 0 && pos < a.max_pos;
-        if (!in && u == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);   // identity for this token
-        using VecP = Vec<float, (kPairs > 4 ? 4 : kPairs)>;
-        constexpr int kP = kPairs > 4 ? 4 : kPairs;
-        const float* row = a.table + (int64_t)(in ? pos : 0) * a.rot + pair;
+      for (int j = 0; j < kPairs; j += kP) {
+        const VecP cv = *reinterpret_cast<const VecP*>(row + j);
+        const VecP sv = *reinterpret_cast<const VecP*>(row + a.rot / 2 + j);
 #pragma unroll
-        for (int j = 0; j < kPairs; j += kP) {
-          const VecP cv = *reinterpret_cast<const VecP*>(row + j);
-          const VecP sv = *reinterpret_cast<const VecP*>(row + a.rot / 2 + j);
-#pragma unroll
-          for (int i = 0; i < kP; ++i) {
-            c[j + i] = in ? cv.e[i] : 1.f;
-            s[j + i] = in ? sv.e[i] * a.sign : 0.f;
-          }
+        for (int i = 0; i < kP; ++i) {
+          c[j + i] = cv.e[i];
+          s[j + i] = sv.e[i] * a.sign;
         }
       }
+    } else {                                 // identity for this token
+      if (u == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        c[j] = 1.f;
+        s[j] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
         E& ea = kVecs == 2 ? v[k][0].e[j] : v[k][0].e[2 * j];
@@ -166,10 +176,13 @@ __global__ void __launch_bounds__(V == 1 ? kMaxWidth : 256) rotary_kernel(const 
         ea = from_float<E>(fa);
         eb = from_float<E>(fb);
       }
-    }
-    E* dst = static_cast<E*>(a.out) + tok[k] * a.out_token + head[k] * a.out_head;
-    *reinterpret_cast<VecT*>(dst + at0) = v[k][0];
-    if (kVecs == 2 && turning) *reinterpret_cast<VecT*>(dst + at1) = v[k][kVecs - 1];
+  }
+  E* dst = static_cast<E*>(a.out) + tok * a.out_token + head * a.out_head + at0;
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    *reinterpret_cast<VecT*>(dst + k * a.out_head) = v[k][0];
+    if (kVecs == 2 && both)
+      *reinterpret_cast<VecT*>(dst + k * a.out_head + apart) = v[k][kVecs - 1];
   }
 }
 
@@ -186,21 +199,28 @@ cudaError_t launch_rotary(RotArgs& a, bool in_place, cudaStream_t stream) {
   const int v = wide ? V : 1;
   const int vecs = LAYOUT == kHalf || !wide ? 2 : 1;
   a.turning = a.rot / (vecs * v);
-  a.units = a.turning + (in_place ? 0 : (a.D - a.rot) / v);
-  // A block holds whole rows: at most kMaxWidth units (256 when wide).
-  const int threads = a.units > 256 ? (a.units + 31) / 32 * 32 : 256;
+  const int carried = in_place ? 0 : (a.D - a.rot) / v;
+  a.units = a.turning + (carried + vecs - 1) / vecs;
+  // A block holds whole rows: at most kMaxWidth units (256 when wide).  Small
+  // blocks leave an SM sooner and take the next row's loads up earlier: 128
+  // threads measured 28 us where 256 took 31.
+  const int threads = a.units > 128 ? (a.units + 31) / 32 * 32 : 128;
   a.per_block = threads / a.units;
   auto go = [&](auto kernel, int rows_each) {
-    const int64_t groups = (a.rows + rows_each - 1) / rows_each;
-    const int64_t blocks = (groups + a.per_block - 1) / a.per_block;
+    a.groups = (int64_t)a.T * (a.H / rows_each);
+    a.fgroups = FastDiv((uint32_t)(a.H / rows_each));
+    const int64_t blocks = (a.groups + a.per_block - 1) / a.per_block;
     return launch_kernel(kernel, dim3((unsigned)blocks), dim3((unsigned)threads), 0, stream, 0u,
                          a);
   };
-  // Four rows a thread once that still fills the GPU's 152 SMs twice over;
-  // below that the call is latency, and a row a thread spreads it widest.
-  const bool many = a.rows * a.units >= (int64_t)152 * 2 * 256 * 4;
-  if (wide) return many ? go(rotary_kernel<E, LAYOUT, V, 4>, 4) : go(rotary_kernel<E, LAYOUT, V, 1>, 1);
-  return many ? go(rotary_kernel<E, LAYOUT, 1, 4>, 4) : go(rotary_kernel<E, LAYOUT, 1, 1>, 1);
+  // Several heads a thread (four of one vector, two of two) once that still
+  // fills the GPU's 152 SMs twice over; below that the call is latency, and a
+  // head a thread spreads it widest.
+  const bool many = (int64_t)a.T * a.H * a.units >= (int64_t)152 * 2 * 256 * 4;
+  if (!wide) return go(rotary_kernel<E, LAYOUT, 1, 1>, 1);
+  if (many && LAYOUT == kInterleaved && a.H % 4 == 0) return go(rotary_kernel<E, LAYOUT, V, 4>, 4);
+  if (many && a.H % 2 == 0) return go(rotary_kernel<E, LAYOUT, V, 2>, 2);
+  return go(rotary_kernel<E, LAYOUT, V, 1>, 1);
 }
 
 template <typename E>
@@ -300,8 +320,6 @@ extern "C" dsa_status dsa_rotary_embed(const void* x, int64_t x_token, int64_t x
   a.T = T;
   a.H = H;
   a.sign = inverse ? -1.f : 1.f;
-  a.rows = (int64_t)T * H;
-  a.fH = FastDiv((uint32_t)H);
   const bool in_place = x == out && (T == 1 || x_token == out_token) && (H == 1 || x_head == out_head);
   if (x == out && !in_place) return DSA_ERR_INVALID_ARG;
   cudaError_t e;
