@@ -25,10 +25,11 @@ namespace {
 constexpr int kDc = DSA_MLA_DV;                // 512 latent values
 constexpr int kRow = DSA_MLA_DQK;              // 576 codes of a row
 constexpr int kDr = kRow - kDc;                // 64 rope values
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kHeld = 8;                       // rows that a warp keeps in registers
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kHeld = 4;                       // rows that a warp keeps in registers
 constexpr int kMaxBlock = 1024;                // slots of a block
-constexpr int kTokensPerCta = 8;               // tokens whose blocks a CTA looks after
+constexpr int kTokensPerCta = 64;              // tokens whose blocks a CTA looks after
+constexpr int kAlone = 4;                      // new rows of a block that a warp takes alone
 
 struct InsertArgs {
   const uint16_t* kv;
@@ -58,19 +59,28 @@ __device__ __forceinline__ RowRegs load_row(const InsertArgs& a, int t, int lane
   return r;
 }
 
-// The larger magnitude of two packed bf16, as bits (the order of magnitudes);
-// infinities and NaN count as 0.
-__device__ __forceinline__ uint32_t pair_amax(uint32_t w) {
+// The row's largest magnitude in this lane, as bf16 bits (which order
+// magnitudes), two values at a time; infinities and NaN count as 0.
+__device__ __forceinline__ uint32_t finite(uint32_t w) {
   const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
   return max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u);
 }
-
-__device__ __forceinline__ uint32_t row_amax(const RowRegs& r) {
-  uint32_t m = pair_amax(r.p);
-  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+// Read again: the common path keeps its rows in registers.
+__device__ __noinline__ uint32_t row_amax_finite(const InsertArgs& a, int t, int lane) {
+  const RowRegs r = load_row(a, t, lane);
+  const uint32_t w[9] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w, r.p};
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, pair_amax(w[i]));
+  for (int i = 0; i < 9; ++i) m = max(m, finite(w[i]));
   return m;
+}
+__device__ __forceinline__ uint32_t row_amax(const InsertArgs& a, const RowRegs& r, int t, int lane) {
+  const uint32_t w[9] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w, r.p};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 9; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+  m = max(m & 0xFFFFu, m >> 16);
+  return m < 0x7F80u ? m : row_amax_finite(a, t, lane);
 }
 
 // The smallest power of two s >= 2^-126 with amax <= 448 s (448 = 1.75 2^8)
@@ -85,21 +95,33 @@ __device__ __forceinline__ uint32_t codes2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
-__device__ __forceinline__ uint32_t encode2(uint32_t w, float scale, float inv) {
-  const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xFFFF0000u);
-  return inv != 0.f ? codes2(lo * inv, hi * inv) : codes2(__fdiv_rn(lo, scale), __fdiv_rn(hi, scale));
+__device__ __forceinline__ uint32_t encode2(uint32_t w, float inv) {
+  return codes2(__uint_as_float(w << 16) * inv, __uint_as_float(w & 0xFFFF0000u) * inv);
 }
 
+// The row's codes, for a scale that is a power of two (the product with its
+// inverse is the quotient).
 __device__ __forceinline__ void store_row(const InsertArgs& a, int64_t slot, const RowRegs& r,
-                                          float scale, float inv, int lane) {
+                                          float inv, int lane) {
   const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c[i] = encode2(w[2 * i], scale, inv) | (encode2(w[2 * i + 1], scale, inv) << 16);
+  for (int i = 0; i < 4; ++i) c[i] = encode2(w[2 * i], inv) | (encode2(w[2 * i + 1], inv) << 16);
   uint8_t* dst = a.cache + slot * kRow;
   reinterpret_cast<uint4*>(dst)[lane] = make_uint4(c[0], c[1], c[2], c[3]);
-  reinterpret_cast<uint16_t*>(dst + kDc)[lane] = (uint16_t)encode2(r.p, scale, inv);
+  reinterpret_cast<uint16_t*>(dst + kDc)[lane] = (uint16_t)encode2(r.p, inv);
+}
+
+// Any other scale (another quantiser's): token t's row divided by it.
+__device__ __noinline__ void store_row_divided(const InsertArgs& a, int64_t slot, int t, float scale) {
+  uint8_t* dst = a.cache + slot * kRow;
+  for (int i = threadIdx.x & 31; i < kRow / 2; i += 32) {
+    const uint32_t w = i < kDc / 2
+                           ? __ldg(reinterpret_cast<const uint32_t*>(a.kv + (int64_t)t * kDc) + i)
+                           : __ldg(reinterpret_cast<const uint32_t*>(a.kpe + (int64_t)t * kDr) + i - kDc / 2);
+    reinterpret_cast<uint16_t*>(dst)[i] = (uint16_t)codes2(
+        __fdiv_rn(__uint_as_float(w << 16), scale), __fdiv_rn(__uint_as_float(w & 0xFFFF0000u), scale));
+  }
 }
 
 // Four codes times `ratio`, rounded once more.
@@ -115,7 +137,7 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t c, float ratio) {
   return out;
 }
 
-__device__ __forceinline__ void requantise_row(const InsertArgs& a, int64_t slot, float ratio,
+__device__ __noinline__ void requantise_row(const InsertArgs& a, int64_t slot, float ratio,
                                                int lane) {
   uint4* row = reinterpret_cast<uint4*>(a.cache + slot * kRow);
   for (int i = lane; i < kRow / 16; i += 32) {
@@ -128,6 +150,23 @@ __device__ __forceinline__ void requantise_row(const InsertArgs& a, int64_t slot
   }
 }
 
+// What a block's new rows make of its scale.
+struct BlockScale {
+  float div, inv, ratio;    // the divisor; 1 / div where exact (a power of two), else 0; old / div
+  bool grown;               // rows that stay are requantised
+};
+__device__ __forceinline__ BlockScale block_scale(const InsertArgs& a, int b, float held,
+                                                  uint32_t amax, bool writer) {
+  const float old = held > 0.f ? held : 0.f, scale = fmaxf(old, scale_for(amax));
+  if (writer && !(held == scale)) a.scales[b] = scale;
+  BlockScale s;
+  s.div = scale > 0.f ? scale : 1.f;
+  s.inv = (__float_as_uint(s.div) & 0x7FFFFFu) == 0 ? 1.f / s.div : 0.f;
+  s.ratio = __fdiv_rn(old, s.div);
+  s.grown = old > 0.f && scale > old;
+  return s;
+}
+
 // One cache block b: row_tok[r] = 1 + the token of its row r, 0 for a row that
 // stays.  Every thread of the CTA calls it.  Rows up to kHeld a warp are kept
 // in registers between the maximum and the store; a larger block's are read
@@ -137,7 +176,6 @@ __device__ __forceinline__ void write_block(const InsertArgs& a, int b, const in
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t slot0 = (int64_t)b * a.block;
   const float held = a.scales[b];
-  const float old = held > 0.f ? held : 0.f;
   RowRegs regs[kHeld];
   uint32_t m = 0;
 #pragma unroll
@@ -147,40 +185,98 @@ __device__ __forceinline__ void write_block(const InsertArgs& a, int b, const in
     else regs[k] = RowRegs{};
   }
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k) m = max(m, row_amax(regs[k]));
+  for (int k = 0; k < kHeld; ++k) {
+    const int r = warp + k * kWarps;
+    if (r < a.block && row_tok[r] != 0) m = max(m, row_amax(a, regs[k], row_tok[r] - 1, lane));
+  }
   for (int r = warp + kHeld * kWarps; r < a.block; r += kWarps)
-    if (row_tok[r] != 0) m = max(m, row_amax(load_row(a, row_tok[r] - 1, lane)));
+    if (row_tok[r] != 0)
+      m = max(m, row_amax(a, load_row(a, row_tok[r] - 1, lane), row_tok[r] - 1, lane));
   m = __reduce_max_sync(kFull, m);
   if (lane == 0) warp_max[warp] = m;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) m = max(m, warp_max[w]);
-  const float scale = fmaxf(old, scale_for(m));
-  if (threadIdx.x == 0 && !(held == scale)) a.scales[b] = scale;
-  // 1 / scale where that is exact (a power of two), else 0: divide.
-  const float div = scale > 0.f ? scale : 1.f;
-  const float inv = (__float_as_uint(div) & 0x7FFFFFu) == 0 ? 1.f / div : 0.f;
-  const bool grown = old > 0.f && scale > old;
-  const float ratio = __fdiv_rn(old, div);
+  const BlockScale sc = block_scale(a, b, held, m, threadIdx.x == 0);
 #pragma unroll
   for (int k = 0; k < kHeld; ++k) {
     const int r = warp + k * kWarps;
     if (r >= a.block) continue;
-    if (row_tok[r] != 0) store_row(a, slot0 + r, regs[k], div, inv, lane);
-    else if (grown) requantise_row(a, slot0 + r, ratio, lane);
+    if (row_tok[r] != 0 && sc.inv != 0.f) store_row(a, slot0 + r, regs[k], sc.inv, lane);
   }
-  for (int r = warp + kHeld * kWarps; r < a.block; r += kWarps) {
-    if (row_tok[r] != 0) store_row(a, slot0 + r, load_row(a, row_tok[r] - 1, lane), div, inv, lane);
-    else if (grown) requantise_row(a, slot0 + r, ratio, lane);
+  for (int r = warp + kHeld * kWarps; r < a.block; r += kWarps)
+    if (row_tok[r] != 0 && sc.inv != 0.f)
+      store_row(a, slot0 + r, load_row(a, row_tok[r] - 1, lane), sc.inv, lane);
+  if (sc.inv != 0.f && !sc.grown) return;
+  for (int r = warp; r < a.block; r += kWarps) {
+    if (row_tok[r] == 0 && sc.grown) requantise_row(a, slot0 + r, sc.ratio, lane);
+    if (row_tok[r] != 0 && sc.inv == 0.f) store_row_divided(a, slot0 + r, row_tok[r] - 1, sc.div);
   }
+}
+
+// The token that row `slot` gets from this call, plus 1; 0 for none (large calls).
+__device__ __forceinline__ int owner_of(const InsertArgs& a, int slot) {
+  const int o = a.owner[slot];
+  return o >= 1 && o <= a.T && __ldg(a.slots + o - 1) == slot ? o : 0;
+}
+
+// A block with up to kAlone new rows, by one warp: several at a time in a CTA
+// when the call's tokens are spread over many blocks.  False: more rows.
+__device__ __forceinline__ bool write_block_alone(const InsertArgs& a, int b) {
+  const int lane = threadIdx.x & 31;
+  const int64_t slot0 = (int64_t)b * a.block;
+  const float held = a.scales[b];
+  int rows[kAlone], toks[kAlone], n = 0;
+  for (int r0 = 0; r0 < a.block; r0 += 32) {
+    const int tok = r0 + lane < a.block ? owner_of(a, (int)slot0 + r0 + lane) : 0;
+    unsigned there = __ballot_sync(kFull, tok != 0);
+    if (n + __popc(there) > kAlone) return false;
+#pragma unroll
+    for (int i = 0; i < kAlone; ++i) {
+      if (i < n || !there) continue;
+      const int from = __ffs(there) - 1;
+      there &= there - 1;
+      rows[i] = r0 + from;
+      toks[i] = __shfl_sync(kFull, tok, from) - 1;
+      n = i + 1;
+    }
+  }
+  RowRegs regs[kAlone];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kAlone; ++i) regs[i] = i < n ? load_row(a, toks[i], lane) : RowRegs{};
+#pragma unroll
+  for (int i = 0; i < kAlone; ++i)
+    if (i < n) m = max(m, row_amax(a, regs[i], toks[i], lane));
+  const BlockScale sc = block_scale(a, b, held, __reduce_max_sync(kFull, m), lane == 0);
+#pragma unroll
+  for (int i = 0; i < kAlone; ++i)
+    if (i < n) {
+      if (sc.inv != 0.f) store_row(a, slot0 + rows[i], regs[i], sc.inv, lane);
+      else store_row_divided(a, slot0 + rows[i], toks[i], sc.div);
+    }
+  if (sc.grown)
+    for (int r = 0; r < a.block; ++r) {
+      bool stays = true;
+#pragma unroll
+      for (int i = 0; i < kAlone; ++i) stays = stays && !(i < n && rows[i] == r);
+      if (stays) requantise_row(a, slot0 + r, sc.ratio, lane);
+    }
+  return true;
 }
 
 // Few tokens: one kernel, no workspace.  CTA t looks through the call's slots
 // for the rows of its token's block; the block's first token does the work.
-__global__ void __launch_bounds__(kThreads) insert_few_kernel(const InsertArgs a) {
+__global__ void __launch_bounds__(kThreads) insert_few_kernel(const __grid_constant__ InsertArgs a) {
   __shared__ int row_tok[kMaxBlock];
   __shared__ uint32_t warp_max[kWarps];
   const int t = blockIdx.x;
+  // The row is on its way to L2 while its block is looked up.
+  if (threadIdx.x < 10) {
+    const char* row = threadIdx.x < 8 ? reinterpret_cast<const char*>(a.kv + (int64_t)t * kDc) + threadIdx.x * 128
+                                      : reinterpret_cast<const char*>(a.kpe + (int64_t)t * kDr) + (threadIdx.x - 8) * 64;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
+  }
   const int slot = __ldg(a.slots + t);
   if (slot < 0) return;
   if (slot >= a.n_slots) {
@@ -205,10 +301,9 @@ __global__ void __launch_bounds__(kThreads) insert_few_kernel(const InsertArgs a
 
 // Many tokens: the first kernel writes, for every slot, the last token that
 // names it, and for every block one token that looks after it.  The words may
-// hold anything before: one counts only if the token it names has that slot
-// (that block).
-__global__ void __launch_bounds__(kThreads) insert_claim_kernel(const InsertArgs a) {
-  const int t = blockIdx.x * kThreads + threadIdx.x;
+// hold anything before: one counts only if the token it names has that slot.
+__global__ void __launch_bounds__(kThreads) insert_claim_kernel(const __grid_constant__ InsertArgs a) {
+  int t = blockIdx.x * kThreads + threadIdx.x;
   if (t >= a.T) return;
   const int slot = __ldg(a.slots + t);
   if (slot < 0) return;
@@ -216,51 +311,62 @@ __global__ void __launch_bounds__(kThreads) insert_claim_kernel(const InsertArgs
     raise_flag(a.flags, DSA_FLAG_BOUNDS);
     return;
   }
-  auto names = [&](int word) { return word >= 1 && word <= a.T; };
-  int cur = *const_cast<volatile int32_t*>(a.owner + slot);
-  while (!(names(cur) && __ldg(a.slots + cur - 1) == slot && cur > t)) {
-    const int seen = atomicCAS(a.owner + slot, cur, t + 1);
-    if (seen == cur) break;
-    cur = seen;
-  }
-  const int b = (int)fdiv((uint32_t)slot, a.fblock);
-  const int base = b * a.block;
-  cur = *const_cast<volatile int32_t*>(a.leader + b);
-  for (;;) {
-    if (names(cur)) {
-      const int other = __ldg(a.slots + cur - 1);
-      if (other >= base && other - base < a.block) break;
-    }
-    const int seen = atomicCAS(a.leader + b, cur, t + 1);
-    if (seen == cur) break;
-    cur = seen;
+  a.leader[fdiv((uint32_t)slot, a.fblock)] = t + 1;   // whichever is left names the block
+  // The token's own number takes the slot's place; a later token's that it finds
+  // there, it puts back, unless a still later one has come.
+  int* owner = a.owner + slot;
+  auto later = [&](int word) {
+    return word > t + 1 && word <= a.T && __ldg(a.slots + word - 1) == slot;
+  };
+  int seen = atomicExch(owner, t + 1);
+  while (later(seen)) {
+    t = seen - 1;
+    seen = atomicExch(owner, t + 1);
   }
 }
 
 // The second writes the blocks: a CTA looks at kTokensPerCta tokens and takes
-// the blocks that they lead.
-__global__ void __launch_bounds__(kThreads) insert_many_kernel(const InsertArgs a) {
+// the blocks that they lead, first those of few rows, a warp each, then the
+// others together.
+__global__ void __launch_bounds__(kThreads, 2) insert_many_kernel(const __grid_constant__ InsertArgs a) {
   __shared__ int row_tok[kMaxBlock];
   __shared__ uint32_t warp_max[kWarps];
-  const int t0 = blockIdx.x * kTokensPerCta;
-  int lead[kTokensPerCta];
-#pragma unroll
-  for (int i = 0; i < kTokensPerCta; ++i) {
-    const int slot = t0 + i < a.T ? __ldg(a.slots + t0 + i) : -1;
-    lead[i] = slot >= 0 && slot < a.n_slots ? (int)fdiv((uint32_t)slot, a.fblock) : -1;
+  __shared__ int lead[kTokensPerCta], large[kTokensPerCta], n_lead, n_large;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) n_large = 0;
+  // Neighbouring tokens mostly share blocks: their rows are on their way to L2
+  // while the blocks are looked up.
+  const int t0 = blockIdx.x * kTokensPerCta, mine = min(kTokensPerCta, a.T - t0);
+  for (int i = threadIdx.x; i < mine * 9; i += kThreads) {
+    const char* row = i < mine * 8 ? reinterpret_cast<const char*>(a.kv + (int64_t)t0 * kDc) + i * 128
+                                   : reinterpret_cast<const char*>(a.kpe + (int64_t)t0 * kDr) + (i - mine * 8) * 128;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
   }
-#pragma unroll
-  for (int i = 0; i < kTokensPerCta; ++i)
-    if (lead[i] >= 0 && a.leader[lead[i]] != t0 + i + 1) lead[i] = -1;
-#pragma unroll 1
-  for (int i = 0; i < kTokensPerCta; ++i) {
-    const int b = lead[i];
-    if (b < 0) continue;
-    const int base = b * a.block;
-    for (int r = threadIdx.x; r < a.block; r += kThreads) {
-      const int o = a.owner[base + r];
-      row_tok[r] = o >= 1 && o <= a.T && __ldg(a.slots + o - 1) == base + r ? o : 0;
+  if (warp == 0) {
+    int n = 0;
+    for (int i = lane; i < kTokensPerCta; i += 32) {
+      const int t = t0 + i;
+      const int slot = t < a.T ? __ldg(a.slots + t) : -1;
+      const int b = slot >= 0 && slot < a.n_slots ? (int)fdiv((uint32_t)slot, a.fblock) : -1;
+      const bool leads = b >= 0 && a.leader[b] == t + 1;
+      const unsigned all = __ballot_sync(kFull, leads);
+      if (leads) lead[n + __popc(all & lanemask_lt())] = b;
+      n += __popc(all);
     }
+    if (lane == 0) n_lead = n;
+  }
+  __syncthreads();
+  // (One or two blocks hold many rows each, as in a prompt, or nothing is lost.)
+  if (n_lead > 2) {
+    for (int i = warp; i < n_lead; i += kWarps)
+      if (!write_block_alone(a, lead[i]) && lane == 0) large[atomicAdd(&n_large, 1)] = lead[i];
+  } else if (threadIdx.x == 0) {
+    for (n_large = 0; n_large < n_lead; ++n_large) large[n_large] = lead[n_large];
+  }
+  __syncthreads();
+  for (int i = 0; i < n_large; ++i) {
+    const int b = large[i], base = b * a.block;
+    for (int r = threadIdx.x; r < a.block; r += kThreads) row_tok[r] = owner_of(a, base + r);
     __syncthreads();
     write_block(a, b, row_tok, warp_max);
     __syncthreads();
