@@ -684,12 +684,19 @@ __device__ __forceinline__ float head_sum(const float* w, int h, float* off) {
   return (y[0] + y[kHeads]) + (y[2 * kHeads] + y[3 * kHeads]);
 }
 
+// Softmax warps with a head; the others leave, and what they would hold (scores,
+// weights and outputs of no head) stays as it is.
+__device__ __forceinline__ int active_warps(int nheads) {
+  return (nheads + kGroupHeads - 1) / kGroupHeads * 4;
+}
+
 template <bool kSplit>
 __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm, uint32_t tmem,
                                                   int hg, int p0, int p1) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3, grp = warp >> 2;
   const int token = quad * 32 + lane, col0 = grp * kGroupHeads, col = col0 + (lane & 15);
   const int nheads = min(kHeads, a.H - hg * kHeads);
+  const int active = active_warps(nheads);
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
   bool ok = true;
   // A wait that fails leaves `ok` false; nothing is written out then.
@@ -702,7 +709,7 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
     if (lane == 0) mbar_arrive1(bar);
   };
   // Nothing selected on a shard: O = 0, lse2 = -inf.
-  for (int p = p0 + warp; !kSplit && p < p1; p += kSoftmaxWarps) {
+  for (int p = p0 + warp; !kSplit && p < p1; p += active) {
     int shard;
     const int64_t at = list_of(a, p, &shard);
     if (__ldg(a.counts + at) > 0) continue;
@@ -715,7 +722,7 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
   if (cur.valid(p1)) {
     const float f = split_query(a, sm, row_of(a, cur.p), hg);
     if (lane < 4) sm.fq[4 * warp + lane] = f;
-    barrier(1 + kGroups, kSoftmaxWarps * 32);
+    barrier(1 + kGroups, active * 32);
   }
   int n = 0;                                 // tiles done
 #pragma unroll 1
@@ -724,7 +731,7 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
     cur.next_pair(a, sm, p0, p1);
     const bool first = cur.valid(p1) && row_of(a, cur.p) != row_of(a, p);   // of its row
     // The last pair's sums have been read, and a new row's factors are there.
-    if (n > 0) barrier(1 + kGroups, kSoftmaxWarps * 32);
+    if (n > 0) barrier(1 + kGroups, active * 32);
     const float4* fq = reinterpret_cast<const float4*>(sm.fq + col0);
     float ref = 0.f;                         // of head `col`
     bool fresh = true;                       // every token so far left out: no reference yet
@@ -738,7 +745,7 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
         // The next row's query on its way to L2, 128 bytes a thread.
         const char* q = reinterpret_cast<const char*>(
             a.q + ((int64_t)row_of(a, cur.p) * a.H + hg * kHeads) * kDqk);
-        for (int i = threadIdx.x; i < nheads * kDqk / 64; i += kSoftmaxWarps * 32)
+        for (int i = threadIdx.x; i < nheads * kDqk / 64; i += active * 32)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i * 128));
       }
       wait(&sm.fullB[sb], (uint32_t)(n >> 1) & 1u);   // the token's scale is there
@@ -807,16 +814,19 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
         const bool move = fresh ? mx > -INFINITY : mx > kGap;
         const float up = move ? mx - kTop : 0.f;
         if (!fresh) alpha = fast_exp2(-up);
+        const bool first_tile = fresh;
         fresh = fresh && !__any_sync(kFull, move);
         ref += up;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float2 d = make_float2(__shfl_sync(kFull, up, 2 * i), __shfl_sync(kFull, up, 2 * i + 1));
           x[i] = fadd2(x[i], make_float2(-d.x, -d.y));
-          const float2 f = make_float2(__shfl_sync(kFull, alpha, 2 * i),
-                                       __shfl_sync(kFull, alpha, 2 * i + 1));
-          l[i] = fmul2(l[i], f);
-          gone[i] = fmul2(gone[i], f);
+          if (!first_tile) {
+            const float2 f = make_float2(__shfl_sync(kFull, alpha, 2 * i),
+                                         __shfl_sync(kFull, alpha, 2 * i + 1));
+            l[i] = fmul2(l[i], f);
+            gone[i] = fmul2(gone[i], f);
+          }
         }
         // The maxima have been read before another tile's are written.
         barrier(1 + grp, 128);
@@ -884,65 +894,66 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
     w[quad * kHeads + col] = all;
     w[(4 + quad) * kHeads + col] = less;
     if (quad == 0) w[8 * kHeads + col] = ref;
-    barrier(1 + kGroups, kSoftmaxWarps * 32);
+    barrier(1 + kGroups, active * 32);
     if (first && lane < 4) sm.fq[4 * warp + lane] = factor;   // read after the next such barrier
     tc_fence_after();
     const bool good = __all_sync(kFull, ok);
     if (kSplit) break;                       // merged with the cluster's other parts
     int shard;
     const int64_t head0 = list_of(a, p, &shard) * a.H + hg * kHeads;   // first head of the CTA's
-    if (warp < 2 && good) {
+    if (warp < 2) {
       const int h = warp * 32 + lane;
       float off;
       const float sum = head_sum(w, h, &off);
-      if (h < nheads)
+      sm.part[0][h] = sum == 0.f ? 0.f : 1.f / (sum - off);
+      if (h < nheads && good)
         a.lse2[head0 + h] = sum == 0.f ? -INFINITY : w[8 * kHeads + h] + log2f(sum);
     }
-    // The warp's 32 tensor-memory lanes hold heads (quad & 1) 32 + lane with 64
-    // of their dimensions.  16 lanes and 32 columns at a time; four threads hold
-    // 8 columns of a head two by two and exchange them, so that each stores 16
-    // bytes and the four 64 contiguous ones.
+    barrier(1 + kGroups, active * 32);
+    // The warp's 32 tensor-memory lanes hold heads (quad & 1) 32 + lane, 64
+    // columns a group.  16 lanes and 32 columns at a time; a thread holds two
+    // columns of each 8 of two heads, and swaps with its neighbour so that four
+    // threads store 32 contiguous bytes of a head, a whole sector.  (Measured a
+    // pair: 3.7 us with 64 bytes and twice the swaps, 5.5 through shared memory,
+    // 5 with a head a thread and 32-byte stores.)
     float inv[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float off;
-      const float sum = head_sum(w, (quad & 1) * 32 + 8 * i + (lane >> 2), &off);
-      inv[i] = sum == 0.f ? 0.f : 1.f / (sum - off);
-    }
+    for (int i = 0; i < 4; ++i) inv[i] = sm.part[0][(quad & 1) * 32 + 8 * i + (lane >> 2)];
     const int j = lane & 3;
-    __nv_bfloat16* orow = a.out + (head0 + (quad & 1) * 32 + (lane >> 2)) * kDv + (grp >> 1) * 256 +
-                          (quad >> 1) * 128 + (grp & 1) * 64 + j * 8;
+    for (int cg = grp; cg < 4; cg += active / 4) {
+      __nv_bfloat16* orow = a.out + (head0 + (quad & 1) * 32 + (lane >> 2)) * kDv + (cg >> 1) * 256 +
+                            (quad >> 1) * 128 + (cg & 1) * 64 + (j & 1) * 8 + (j >> 1) * 4;
 #pragma unroll
-    for (int part = 0; part < 4; ++part) {
-      const int up16 = part >> 1, c = (part & 1) * 32;
-      uint32_t o[16];
-      tmem_ld32_of16(lanes + ((uint32_t)up16 << 20) + kOCol + grp * 64 + c, o);
-      tmem_wait(o);
+      for (int up16 = 0; up16 < 2; ++up16) {
+        if ((quad & 1) * 32 + up16 * 16 >= nheads) break;
+        uint32_t o0[16], o1[16];             // columns 0-31 and 32-63
+        tmem_ld32_of16(lanes + ((uint32_t)up16 << 20) + kOCol + cg * 64, o0);
+        tmem_ld32_of16(lanes + ((uint32_t)up16 << 20) + kOCol + cg * 64 + 32, o1);
+        tmem_wait(o0);
+        tmem_wait(o1);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) { // heads lane / 4, then 8 + lane / 4
-        const float f = inv[2 * up16 + half];
-        uint32_t b[4];                       // word j of the 16 bytes of columns 8 i ..
+        for (int q = 0; q < 4; ++q) {        // 32 columns; heads lane / 4, then 8 + lane / 4
+          const int c = (q >> 1) * 32, half = q & 1;
+          const uint32_t(&o)[16] = q < 2 ? o0 : o1;
+          const float f = inv[2 * up16 + half];
+          uint32_t b[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 y =
-              __floats2bfloat162_rn(__uint_as_float(o[4 * i + 2 * half]) * f,
-                                    __uint_as_float(o[4 * i + 2 * half + 1]) * f);
-          b[i] = *reinterpret_cast<const uint32_t*>(&y);
+          for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 y =
+                __floats2bfloat162_rn(__uint_as_float(o[4 * i + 2 * half]) * f,
+                                      __uint_as_float(o[4 * i + 2 * half + 1]) * f);
+            b[i] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          const int h = up16 * 16 + half * 8;
+          const bool there = good && (quad & 1) * 32 + h + (lane >> 2) < nheads;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {      // columns 16 k .. + 15: 8-column groups 2 k, 2 k + 1
+            const uint32_t give = j & 1 ? b[2 * k] : b[2 * k + 1];
+            const uint32_t got = __shfl_xor_sync(kFull, give, 1);
+            const uint2 v = j & 1 ? make_uint2(got, b[2 * k + 1]) : make_uint2(b[2 * k], got);
+            if (there) *reinterpret_cast<uint2*>(orow + (int64_t)h * kDv + c + 16 * k) = v;
+          }
         }
-#pragma unroll
-        for (int x = 1; x < 4; x <<= 1)      // a 4 by 4 transposition over the threads
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!(i & x)) {
-              const bool high = j & x;
-              const uint32_t give = high ? b[i] : b[i + x];
-              const uint32_t got = __shfl_xor_sync(kFull, give, x);
-              if (high) b[i] = got;
-              else b[i + x] = got;
-            }
-        const int h = up16 * 16 + half * 8;
-        if (good && (quad & 1) * 32 + h + (lane >> 2) < nheads)
-          *reinterpret_cast<uint4*>(orow + (int64_t)h * kDv + c) = make_uint4(b[0], b[1], b[2], b[3]);
       }
     }
   }
@@ -963,11 +974,10 @@ __device__ __forceinline__ void merge_parts(const MlaFp8Args& a, Smem& sm, uint3
                                             bool mine) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3, grp = warp >> 2;
   const uint32_t rank = cluster_rank(), parts = cluster_size();
-  const int nheads = min(kHeads, a.H - hg * kHeads);
+  const int nheads = min(kHeads, a.H - hg * kHeads), active = active_warps(nheads);
   float* slots = a.work + (int64_t)(blockIdx.x - rank) * kSlotFloats;   // of the cluster's CTAs
   float* slot = slots + (int64_t)rank * kSlotFloats;
-  if (threadIdx.x < kHeads) {
-    const int h = threadIdx.x;
+  for (int h = threadIdx.x; h < nheads; h += active * 32) {
     const float* w = reinterpret_cast<const float*>(sm.plo);
     float off = 0.f;
     float* to = slot + kHeads * kDv + h;
@@ -977,24 +987,27 @@ __device__ __forceinline__ void merge_parts(const MlaFp8Args& a, Smem& sm, uint3
     to[3 * kHeads] = aborted(sm) ? 1.f : 0.f;
   }
   if (mine) {
-    const int h = (quad & 1) * 32 + lane;    // this thread's head, 64 of its dimensions
-    const int d0 = (grp >> 1) * 256 + (quad >> 1) * 128 + (grp & 1) * 64;
+    const int h = (quad & 1) * 32 + lane;    // this thread's head, 64 columns a group
     float4* row = reinterpret_cast<float4*>(sm.kv[0][0]) + h * (kDv / 4);
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     tc_fence_after();
+    for (int cg = grp; cg < 4 && (quad & 1) * 32 < nheads; cg += active / 4) {
+      const int d0 = (cg >> 1) * 256 + (quad >> 1) * 128 + (cg & 1) * 64;
 #pragma unroll
-    for (int c = 0; c < 64; c += 16) {
-      uint32_t o[16];
-      tmem_ld16(lanes + kOCol + grp * 64 + c, o);
-      tmem_wait(o);
+      for (int c = 0; c < 64; c += 16) {
+        uint32_t o[16];
+        tmem_ld16(lanes + kOCol + cg * 64 + c, o);
+        tmem_wait(o);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        row[((d0 + c) / 4 + i) ^ (h & 7)] =
-            make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                        __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+        for (int i = 0; i < 4; ++i)
+          row[((d0 + c) / 4 + i) ^ (h & 7)] =
+              make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                          __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+      }
     }
     proxy_fence();
-    barrier(1 + kGroups, kSoftmaxWarps * 32);
+    barrier(1 + kGroups, active * 32);
+    // Four heads a warp.
     if (lane == 0) {
       constexpr int kBytes = kHeads * kDv * 4 / kSoftmaxWarps;
       asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
@@ -1013,7 +1026,7 @@ __device__ __forceinline__ void merge_parts(const MlaFp8Args& a, Smem& sm, uint3
   const int64_t head0 = list_of(a, p, &shard) * a.H + hg * kHeads;
   float* factor = reinterpret_cast<float*>(sm.plo);   // [C][64]
   bool good = true;
-  if (threadIdx.x < kHeads) {
+  if ((int)threadIdx.x < nheads) {
     const int h = threadIdx.x;
     float sum[8], off[8], ref[8];
 #pragma unroll
@@ -1041,12 +1054,12 @@ __device__ __forceinline__ void merge_parts(const MlaFp8Args& a, Smem& sm, uint3
 #pragma unroll
     for (int c = 0; c < 8; ++c)
       if (c < (int)parts) factor[c * kHeads + h] = ref[c] * inv;
-    if (rank == 0 && h < nheads && good)
+    if (rank == 0 && good)
       a.lse2[head0 + h] = all == 0.f ? -INFINITY : top + log2f(all);
   }
-  good = !barrier_or(1 + kGroups, kSoftmaxWarps * 32, !good);
+  good = !barrier_or(1 + kGroups, active * 32, !good);
   const int chunks = kDv / 8 / (int)parts;   // of 8 dimensions, 16 bytes out
-  for (int i = threadIdx.x; i < nheads * chunks; i += kSoftmaxWarps * 32) {
+  for (int i = threadIdx.x; i < nheads * chunks; i += active * 32) {
     const int h = i / chunks, k = 2 * ((int)rank * chunks + i - h * chunks);
     uint32_t b[4];
 #pragma unroll
@@ -1086,6 +1099,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
   const int hg = unit % a.hgroups, g = unit / a.hgroups, groups = units / a.hgroups;
   const int64_t pairs = (int64_t)a.rows * a.S;
   const int p0 = (int)(pairs * g / groups), p1 = (int)(pairs * (g + 1) / groups);
+  const int active = active_warps(min(kHeads, a.H - hg * kHeads));
 
   int total = 0;                             // tokens of a split pair, over the cluster
   for (int p = p0 + (kSplit ? 0 : tid); p < p1; p += kThreads) {
@@ -1130,10 +1144,10 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
       mbar_init(&sm.emptyA[i], 1);
       mbar_init(&sm.emptyB[i], 1);
       mbar_init(&sm.sfull[i], 1);
-      mbar_init(&sm.sfree[i], kSoftmaxWarps);
+      mbar_init(&sm.sfree[i], active);
     }
-    mbar_init(&sm.qfull, kSoftmaxWarps);
-    mbar_init(&sm.pfull, kSoftmaxWarps);
+    mbar_init(&sm.qfull, active);
+    mbar_init(&sm.pfull, active);
     mbar_init(&sm.pvdone, 1);
     mbar_init(&sm.drain[0], 1);
     mbar_init(&sm.drain[1], 1);
@@ -1147,12 +1161,16 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
 
   if (warp < kSoftmaxWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    softmax_and_store<kSplit>(a, sm, tmem, hg, p0, p1);
-    if (kSplit) merge_parts(a, sm, tmem, hg, p0, sm.counts[0] > 0);
+    if (warp < active) {
+      softmax_and_store<kSplit>(a, sm, tmem, hg, p0, p1);
+      if (kSplit) merge_parts(a, sm, tmem, hg, p0, sm.counts[0] > 0);
+    } else if (kSplit) {
+      cluster_sync();                        // the merge's barrier
+    }
   } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsGather));
     gather_tiles(a, sm, p0, p1);
-    if (kSplit) cluster_sync();              // the merge's barrier
+    if (kSplit) cluster_sync();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
     if (tid == kMmaWarp * 32)
