@@ -913,9 +913,11 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
     // The warp's 32 tensor-memory lanes hold heads (quad & 1) 32 + lane, 64
     // columns a group.  16 lanes and 32 columns at a time; a thread holds two
     // columns of each 8 of two heads, and swaps with its neighbour so that four
-    // threads store 32 contiguous bytes of a head, a whole sector.  (Measured a
-    // pair: 3.7 us with 64 bytes and twice the swaps, 5.5 through shared memory,
-    // 5 with a head a thread and 32-byte stores.)
+    // threads store 32 contiguous bytes of a head, a whole sector: 3.8 thousand
+    // cycles a pair, beside the next pair's scores.  (5.0 with a head a thread and
+    // 32-byte stores.  From the last stage's space by bulk copies it is 1.3, but
+    // the stage then comes back later: the same time in all, and 12 % more where
+    // pairs have two tiles.)
     float inv[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) inv[i] = sm.part[0][(quad & 1) * 32 + 8 * i + (lane >> 2)];
@@ -1099,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
   const int hg = unit % a.hgroups, g = unit / a.hgroups, groups = units / a.hgroups;
   const int64_t pairs = (int64_t)a.rows * a.S;
   const int p0 = (int)(pairs * g / groups), p1 = (int)(pairs * (g + 1) / groups);
-  const int active = active_warps(min(kHeads, a.H - hg * kHeads));
+  const int nheads = min(kHeads, a.H - hg * kHeads), active = active_warps(nheads);
 
   int total = 0;                             // tokens of a split pair, over the cluster
   for (int p = p0 + (kSplit ? 0 : tid); p < p1; p += kThreads) {
@@ -1123,7 +1125,6 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
     // Nothing selected on this shard: O = 0, lse2 = -inf.
     int shard;
     const int64_t head0 = list_of(a, p0, &shard) * a.H + hg * kHeads;
-    const int nheads = min(kHeads, a.H - hg * kHeads);
     for (int i = tid; i < nheads * (kDv / 8) && cluster_rank() == 0; i += kThreads)
       reinterpret_cast<uint4*>(a.out + head0 * kDv)[i] = make_uint4(0, 0, 0, 0);
     if (cluster_rank() == 0 && tid < nheads) a.lse2[head0 + tid] = -INFINITY;
