@@ -76,11 +76,20 @@ static_assert(128 * (4 * kRegsSoftmax + kRegsGather + kRegsMma) <= kThreads * 80
 constexpr int kOCol = 0, kSCol = 256, kTmemCols = 512;
 constexpr int kCounts = 20;                  // pairs whose counts are kept on chip
 constexpr int kSms = 152;                     // of a GB300
+constexpr int kMaxList = 1 << 30;            // tokens of a list
 constexpr float kLog2e = 1.4426950408889634f;
 // A head's weights, with their token's scale, are t 2^(x - ref): a new reference
 // puts the largest at 2^3, and they may grow to 2^8.75 (448 is the largest
 // e4m3) before the next.
 constexpr float kTop = 3.f, kGap = 8.75f;
+#ifdef DSA_TEST_STALLED_COPY
+// The test-only build (never libdsa.so): part A of every stage expects one
+// arrival that nothing makes, so the scores' wait runs out (every copy still
+// lands) and the kernel returns with DSA_FLAG_TIMEOUT.
+constexpr uint32_t kStalledArrivals = 1;
+#else
+constexpr uint32_t kStalledArrivals = 0;
+#endif
 // Scales for which neither the sums nor the weights leave fp32.
 constexpr float kMinScale = 0x1p-100f, kMaxScale = 0x1p100f;
 
@@ -262,12 +271,10 @@ __device__ __forceinline__ bool aborted(const Smem& sm) {
 }
 
 // Bounded wait that also gives up once another role of the CTA has aborted.  A
-// try suspends the thread for up to kSuspendNs (or until the phase ends), so
-// that waiting warps leave the issue slots to the softmax: polling without it
-// took three quarters of all instructions issued.
-constexpr uint32_t kSuspendNs = 20000, kWaitTries = kWaitPolls >> 6;
+// try may suspend the thread for up to kSuspendNs.
+constexpr uint32_t kSuspendNs = 1000;
 __device__ __forceinline__ bool wait_or_abort(Smem& sm, uint64_t* bar, uint32_t parity) {
-  for (uint32_t i = 0; i < kWaitTries; ++i) {
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -1140,7 +1147,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.fullA[i], 32 * kGatherWarps);   // every gathering lane
+      mbar_init(&sm.fullA[i], 32 * kGatherWarps + kStalledArrivals);   // every gathering lane
       mbar_init(&sm.fullB[i], 32 * kGatherWarps);
       mbar_init(&sm.emptyA[i], 1);
       mbar_init(&sm.emptyB[i], 1);
@@ -1210,7 +1217,7 @@ static int split_parts(int64_t pairs, int64_t hgroups, int K) {
 }
 
 extern "C" int64_t dsa_sparse_mla_decode_fp8_work(int rows, int S, int H, int K) {
-  if (rows < 1 || S < 1 || S > DSA_MAX_SHARDS || H < 1 || K < 1) return 0;
+  if (rows < 1 || S < 1 || S > DSA_MAX_SHARDS || H < 1 || K < 1 || K > kMaxList) return 0;
   const int64_t pairs = (int64_t)rows * S, hgroups = ((int64_t)H + kHeads - 1) / kHeads;
   const int parts = split_parts(pairs, hgroups, K);
   return parts > 1 ? pairs * hgroups * parts * kSlotFloats * 4 : 0;
@@ -1226,7 +1233,8 @@ extern "C" dsa_status dsa_sparse_mla_decode_fp8(const uint16_t* q, const uint8_t
   if (rows < 0 || K < 1 || H < 1 || n_slots < 1 || block_tokens < 1 || n_slots % block_tokens ||
       !std::isfinite(scale))
     return DSA_ERR_INVALID_ARG;
-  if (S < 1 || S > DSA_MAX_SHARDS || n_slots > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (S < 1 || S > DSA_MAX_SHARDS || n_slots > INT32_MAX || K > kMaxList)
+    return DSA_ERR_UNSUPPORTED;
   if (rows == 0) return DSA_OK;
   if (!q || !kv_cache || !block_scales || !slots || !counts || !out || !lse2)
     return DSA_ERR_INVALID_ARG;

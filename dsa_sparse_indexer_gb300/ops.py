@@ -499,7 +499,7 @@ def kv_cache_insert_fp8(kv_rows, kpe_rows, slot_mapping, kv_cache, block_scales,
     return kv_cache, block_scales
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=4096)
 def _mla_fp8_work(rows: int, S: int, H: int, K: int) -> int:
     return _lib.load().dsa_sparse_mla_decode_fp8_work(rows, S, H, K) // 4
 

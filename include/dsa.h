@@ -528,8 +528,8 @@ dsa_status dsa_kv_cache_insert_fp8(const uint16_t* kv_rows, const uint16_t* kpe_
  * the cache holds there or elsewhere cannot reach the result.
  * Errors: rows < 0, K < 1, H < 1, n_slots < 1, block_tokens < 1, n_slots %
  *         block_tokens, scale not finite, null pointers, misalignment ->
- *         INVALID_ARG; S not in [1, 64], n_slots > 2^31 - 1, too many CTAs ->
- *         UNSUPPORTED.
+ *         INVALID_ARG; S not in [1, 64], n_slots > 2^31 - 1, K > 2^30, too many
+ *         CTAs -> UNSUPPORTED.
  */
 dsa_status dsa_sparse_mla_decode_fp8(const uint16_t* q, const uint8_t* kv_cache,
                                      const float* block_scales, int64_t n_slots,

@@ -86,7 +86,7 @@ def test_sparse_mla_decode_fp8(lib):
                     (0, P + 8), (1, P + 8), (12, P + 8), (14, P + 4), (3, 0), (3, 100), (4, 0),
                     (7, -1),
                     (9, 0), (10, 0), (11, INF), (11, NAN)], INVALID)
-    check(f, some, [(8, 0), (8, 65), (3, 2 ** 32), (7, 2 ** 30)], UNSUPPORTED)
+    check(f, some, [(8, 0), (8, 65), (3, 2 ** 32), (7, 2 ** 30), (10, 2 ** 30 + 1)], UNSUPPORTED)
 
 
 def test_sparse_mla_decode_fp8_work(lib):

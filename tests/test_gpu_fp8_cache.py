@@ -336,6 +336,55 @@ def test_slots_left_out_do_not_reach_the_result():
     _check(q, values, keep, cnt, SCALE, out, lse2)
 
 
+def test_what_is_not_finite_stays_in_its_head_and_row():
+    """An infinity or NaN in a head of the query makes that head's outputs NaN,
+    a NaN code in a selected row that row's, and no others."""
+    rng = np.random.default_rng(19)
+    codes, scales = _cache(rng, 1, 512, 64, True)
+    q = W.mla_query(3, 70, seed=6)
+    q[0, 2, 7], q[0, 69, 575], q[1, 0, 0] = 0x7F80, 0xFF80, 0x7FC0
+    slots = rng.integers(0, 256, (1, 3, 200))
+    slots[0, 2, 150] = 300
+    codes[0, 300, 40] = 0x7F
+    counts = np.array([[200, 130, 200]])
+    out, lse2, err = _attend(q, codes, scales, slots, counts)
+    assert err == 0
+    hit = np.zeros((3, 70), bool)
+    hit[0, [2, 69]] = hit[1, 0] = hit[2] = True
+    assert np.array_equal(np.isnan(lse2[0]), hit)
+    assert np.array_equal(np.isnan(out[0]).any(-1), hit)
+    assert np.isnan(out[0][0, [2, 69]]).all() and np.isnan(out[0][1, 0]).all()
+    held = q.copy()
+    held[0, [2, 69]] = held[1, 0] = 0
+    want = [OA.sparse_mla_decode(OC.bf16_to_f64(held[r]), KF.values(codes, scales)[0, slots[0, r, :n]],
+                                 SCALE, 512) for r, n in ((0, 200), (1, 130))]
+    for r, (o, l) in enumerate(want):
+        rows = KF.values(codes, scales)[0, slots[0, r, :counts[0, r]]]
+        tol_o, tol_l = _tolerance(OC.bf16_to_f64(held[r]), rows, SCALE, o, l)
+        keep = ~hit[r]
+        assert (np.abs(out[0, r] - o) <= tol_o)[keep].all()
+        assert (np.abs(lse2[0, r] - l) <= tol_l)[keep].all()
+
+
+@pytest.mark.parametrize("value", [2.0 ** -100, 2.0 ** 100, 2.0 ** -101, 2.0 ** 101, -1.0])
+def test_block_scales_at_the_edges(value):
+    """Scales from 2^-100 to 2^100 are exact; others in a selected row's block
+    are flagged, 0 (an empty block's) is not."""
+    rng = np.random.default_rng(20)
+    codes, scales = _cache(rng, 1, 256, 64, True)
+    q = (rng.standard_normal((1, 16, 576)) / value if value > 0 else rng.standard_normal((1, 16, 576)))
+    bits = W.f32_to_bf16_bits(q.astype(np.float32) / 60)
+    slots = rng.integers(0, 256, (1, 1, 180))
+    out, lse2, err = _attend(bits, codes, np.full((1, 4), value, np.float32), slots, np.array([[180]]))
+    inside = 2.0 ** -100 <= value <= 2.0 ** 100
+    assert err == (0 if inside else 1)
+    if inside:
+        _check(bits, KF.values(codes, np.full((1, 4), value)), slots, np.array([[180]]), SCALE, out, lse2)
+    out, lse2, err = _attend(bits, codes, np.zeros((1, 4), np.float32), slots, np.array([[180]]))
+    assert err == 0 and (out == 0).all()
+    np.testing.assert_allclose(lse2, np.log2(180.0), rtol=1e-6)
+
+
 def test_counts_outside_the_list_are_clamped_and_flagged():
     rng = np.random.default_rng(10)
     codes, scales = _cache(rng, 1, 256, 64, True)
