@@ -13,9 +13,11 @@
 // rows had been inserted one after another.
 //
 // Bound by memory: 1152 + 576 bytes a token, and twice 576 for every row that
-// has to be requantised.
+// has to be requantised; small calls by a launch's latency (64 tokens 3.0 us).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 
@@ -28,7 +30,8 @@ constexpr int kDr = kRow - kDc;                // 64 rope values
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kHeld = 4;                       // rows that a warp keeps in registers
 constexpr int kMaxBlock = 1024;                // slots of a block
-constexpr int kTokensPerCta = 64;              // tokens whose blocks a CTA looks after
+constexpr int kTokensPerCta = 64;              // tokens whose blocks a CTA looks after, at most
+constexpr int kSms = 152;                      // of a GB300
 constexpr int kAlone = 4;                      // new rows of a block that a warp takes alone
 
 struct InsertArgs {
@@ -41,6 +44,7 @@ struct InsertArgs {
   int32_t* leader;          // [blocks] 1 + a token of the block
   uint32_t* flags;
   int T, n_slots, block;
+  int each;                 // tokens whose blocks a CTA looks after
   FastDiv fblock;
 };
 
@@ -325,9 +329,11 @@ __global__ void __launch_bounds__(kThreads) insert_claim_kernel(const __grid_con
   }
 }
 
-// The second writes the blocks: a CTA looks at kTokensPerCta tokens and takes
-// the blocks that they lead, first those of few rows, a warp each, then the
-// others together.
+// The second writes the blocks: a CTA looks at some tokens and takes the blocks
+// that they lead, first those of few rows, a warp each, then the others
+// together.  Their number gives every SM a CTA, from 16 on (2048 scattered
+// tokens: 25 us with 64 each, 13 with 16) up to 64 (16384 tokens of a prompt:
+// 13 us with 16 each, 9.2 with 64).
 __global__ void __launch_bounds__(kThreads, 2) insert_many_kernel(const __grid_constant__ InsertArgs a) {
   __shared__ int row_tok[kMaxBlock];
   __shared__ uint32_t warp_max[kWarps];
@@ -336,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 2) insert_many_kernel(const __grid_c
   if (threadIdx.x == 0) n_large = 0;
   // Neighbouring tokens mostly share blocks: their rows are on their way to L2
   // while the blocks are looked up.
-  const int t0 = blockIdx.x * kTokensPerCta, mine = min(kTokensPerCta, a.T - t0);
+  const int t0 = blockIdx.x * a.each, mine = min(a.each, a.T - t0);
   for (int i = threadIdx.x; i < mine * 9; i += kThreads) {
     const char* row = i < mine * 8 ? reinterpret_cast<const char*>(a.kv + (int64_t)t0 * kDc) + i * 128
                                    : reinterpret_cast<const char*>(a.kpe + (int64_t)t0 * kDr) + (i - mine * 8) * 128;
@@ -346,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 2) insert_many_kernel(const __grid_c
     int n = 0;
     for (int i = lane; i < kTokensPerCta; i += 32) {
       const int t = t0 + i;
-      const int slot = t < a.T ? __ldg(a.slots + t) : -1;
+      const int slot = i < mine ? __ldg(a.slots + t) : -1;
       const int b = slot >= 0 && slot < a.n_slots ? (int)fdiv((uint32_t)slot, a.fblock) : -1;
       const bool leads = b >= 0 && a.leader[b] == t + 1;
       const unsigned all = __ballot_sync(kFull, leads);
@@ -373,6 +379,28 @@ __global__ void __launch_bounds__(kThreads, 2) insert_many_kernel(const __grid_c
   }
 }
 
+// Or a CTA takes each block of the cache and looks whether it has a token: no
+// CTA has a block more than another, and of a CTA's few loads none waits for a
+// list.  For calls of at least a quarter of the cache's slots, whose untouched
+// blocks are few, and eight tokens a block (or about as many blocks as CTAs fit
+// at a time).  32768 tokens, a tenth left out, into 65536 slots of blocks of
+// 64 (56 MB): in a prompt's order 11.6 us (4.9 TB/s), by the tokens' CTAs
+// above 14.1; in any order 16.1 and 100 to 112.  Past those bounds it loses:
+// 8192 into 65536 of blocks of 128 11.1 us, above 9.6; 16384 into 65536 of
+// blocks of 16 17.7, above 13.7.
+__global__ void __launch_bounds__(kThreads, 2) insert_blocks_kernel(const __grid_constant__ InsertArgs a) {
+  __shared__ int row_tok[kMaxBlock];
+  __shared__ uint32_t warp_max[kWarps];
+  const int b = blockIdx.x, base = b * a.block;
+  const int o = a.leader[b];
+  for (int r = threadIdx.x; r < a.block; r += kThreads) row_tok[r] = owner_of(a, base + r);
+  if (o < 1 || o > a.T) return;
+  const int slot = __ldg(a.slots + o - 1);
+  if (slot < base || slot - base >= a.block) return;   // the CTA alike
+  __syncthreads();
+  write_block(a, b, row_tok, warp_max);
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
@@ -392,8 +420,21 @@ extern "C" dsa_status dsa_kv_cache_insert_fp8(const uint16_t* kv_rows, const uin
       (T > DSA_INSERT_FP8_SMALL && !work))
     return DSA_ERR_INVALID_ARG;
   if (!aligned16(kv_rows) || !aligned16(kpe_rows) || !aligned16(kv_cache)) return DSA_ERR_INVALID_ARG;
-  const InsertArgs a{kv_rows,  kpe_rows, slot_mapping, kv_cache, block_scales, work,
-                     work ? work + n_slots : nullptr, err_flags, T, (int)n_slots, block_tokens,
+  const int64_t n_blocks = n_slots / block_tokens;
+  int each = 16;
+  while (each < kTokensPerCta && (int64_t)each * kSms < T) each *= 2;
+  const InsertArgs a{kv_rows,
+                     kpe_rows,
+                     slot_mapping,
+                     kv_cache,
+                     block_scales,
+                     work,
+                     work ? work + n_slots : nullptr,
+                     err_flags,
+                     T,
+                     (int)n_slots,
+                     block_tokens,
+                     each,
                      FastDiv((uint32_t)block_tokens)};
   cudaError_t e;
   if (T <= DSA_INSERT_FP8_SMALL) {
@@ -401,10 +442,12 @@ extern "C" dsa_status dsa_kv_cache_insert_fp8(const uint16_t* kv_rows, const uin
   } else {
     e = launch_kernel(insert_claim_kernel, dim3((unsigned)((T + kThreads - 1) / kThreads)),
                       dim3(kThreads), 0, stream, 0u, a);
-    if (e == cudaSuccess)
-      e = launch_kernel(insert_many_kernel,
-                        dim3((unsigned)((T + kTokensPerCta - 1) / kTokensPerCta)), dim3(kThreads),
-                        0, stream, 0u, a);
+    if (e == cudaSuccess && n_slots / 4 <= T && n_blocks <= std::max(T / 8, 4 * kSms))
+      e = launch_kernel(insert_blocks_kernel, dim3((unsigned)n_blocks), dim3(kThreads), 0, stream,
+                        0u, a);
+    else if (e == cudaSuccess)
+      e = launch_kernel(insert_many_kernel, dim3((unsigned)((T + each - 1) / each)),
+                        dim3(kThreads), 0, stream, 0u, a);
   }
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

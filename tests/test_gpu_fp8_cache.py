@@ -90,6 +90,33 @@ def test_insert_matches_the_oracle(T, block, state):
     _same_codes(got_c, want_c)
 
 
+@pytest.mark.parametrize("T,n,block", [
+    (700, 4096, 16), (2433, 16384, 64), (3000, 16384, 16), (6000, 32768, 64), (2600, 20800, 1),
+    (6000, 16384, 16), (5000, 16384, 32), (4096, 16384, 27), (4095, 16384, 64), (2048, 2048, 1024)])
+@pytest.mark.parametrize("order", ["prompt", "any"])
+def test_insert_of_many_rows(T, n, block, order):
+    """Both ways of finding the blocks of a large call, on both sides of the
+    sizes that choose; tokens in the order of their slots, or in none."""
+    rng = np.random.default_rng(T + block)
+    n = n // block * block
+    bits, rows = _rows(rng, T)
+    if order == "prompt":
+        blocks = rng.permutation(n // block)
+        slots = (blocks[:, None] * block + np.arange(block)).reshape(-1)[:T].copy()
+    else:
+        slots = rng.integers(0, n, T)
+    slots[::13] = -1
+    slots[5] = slots[T - 2]
+    cache = W.e4m3_codes(rng, (n, 576))
+    scales = 2.0 ** rng.integers(-9, -3, n // block).astype(np.float32)
+    scales[rng.random(n // block) < 0.2] = 0.0
+    want_c, want_s = KF.insert(cache, scales, rows, slots)
+    got_c, got_s, err = _insert(bits, slots, cache, scales)
+    assert err == 0
+    np.testing.assert_array_equal(got_s, want_s)
+    _same_codes(got_c, want_c)
+
+
 @pytest.mark.parametrize("T", [40, 600])
 def test_insert_of_extreme_values(T):
     """Infinities, NaN, zero rows, the smallest and largest bf16, scales that
