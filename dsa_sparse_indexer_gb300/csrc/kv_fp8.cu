@@ -32,7 +32,7 @@ constexpr int kHeld = 4;                       // rows that a warp keeps in regi
 constexpr int kMaxBlock = 1024;                // slots of a block
 constexpr int kTokensPerCta = 64;              // tokens whose blocks a CTA looks after, at most
 constexpr int kSms = 152;                      // of a GB300
-constexpr int kAlone = 4;                      // new rows of a block that a warp takes alone
+constexpr int kAlone = 32;                     // new rows of a block that a warp takes alone
 
 struct InsertArgs {
   const uint16_t* kv;
@@ -225,47 +225,53 @@ __device__ __forceinline__ int owner_of(const InsertArgs& a, int slot) {
 }
 
 // A block with up to kAlone new rows, by one warp: several at a time in a CTA
-// when the call's tokens are spread over many blocks.  False: more rows.
-__device__ __forceinline__ bool write_block_alone(const InsertArgs& a, int b) {
+// when the call's tokens are spread over many blocks.  `list` is the warp's
+// space for the rows and their tokens.  Four rows are kept in registers, more
+// are read again for the store (from L2): 16384 scattered tokens into 131072
+// slots of blocks of 64 take 27 us, and 70 if all CTAs take blocks of more than
+// four rows together.  False: more rows.
+__device__ __forceinline__ bool write_block_alone(const InsertArgs& a, int b, int2* list) {
   const int lane = threadIdx.x & 31;
   const int64_t slot0 = (int64_t)b * a.block;
   const float held = a.scales[b];
-  int rows[kAlone], toks[kAlone], n = 0;
+  int n = 0;
   for (int r0 = 0; r0 < a.block; r0 += 32) {
     const int tok = r0 + lane < a.block ? owner_of(a, (int)slot0 + r0 + lane) : 0;
-    unsigned there = __ballot_sync(kFull, tok != 0);
+    const unsigned there = __ballot_sync(kFull, tok != 0);
     if (n + __popc(there) > kAlone) return false;
-#pragma unroll
-    for (int i = 0; i < kAlone; ++i) {
-      if (i < n || !there) continue;
-      const int from = __ffs(there) - 1;
-      there &= there - 1;
-      rows[i] = r0 + from;
-      toks[i] = __shfl_sync(kFull, tok, from) - 1;
-      n = i + 1;
-    }
+    if (tok != 0) list[n + __popc(there & lanemask_lt())] = make_int2(r0 + lane, tok - 1);
+    n += __popc(there);
   }
-  RowRegs regs[kAlone];
+  __syncwarp();
+  RowRegs regs[kHeld];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) regs[i] = i0 + i < n ? load_row(a, list[i0 + i].y, lane) : RowRegs{};
+  };
   uint32_t m = 0;
+  for (int i0 = 0; i0 < n; i0 += kHeld) {
+    load(i0);
 #pragma unroll
-  for (int i = 0; i < kAlone; ++i) regs[i] = i < n ? load_row(a, toks[i], lane) : RowRegs{};
-#pragma unroll
-  for (int i = 0; i < kAlone; ++i)
-    if (i < n) m = max(m, row_amax(a, regs[i], toks[i], lane));
+    for (int i = 0; i < kHeld; ++i)
+      if (i0 + i < n) m = max(m, row_amax(a, regs[i], list[i0 + i].y, lane));
+  }
   const BlockScale sc = block_scale(a, b, held, __reduce_max_sync(kFull, m), lane == 0);
+  for (int i0 = 0; i0 < n; i0 += kHeld) {
+    if (n > kHeld) load(i0);
 #pragma unroll
-  for (int i = 0; i < kAlone; ++i)
-    if (i < n) {
-      if (sc.inv != 0.f) store_row(a, slot0 + rows[i], regs[i], sc.inv, lane);
-      else store_row_divided(a, slot0 + rows[i], toks[i], sc.div);
-    }
-  if (sc.grown)
-    for (int r = 0; r < a.block; ++r) {
-      bool stays = true;
-#pragma unroll
-      for (int i = 0; i < kAlone; ++i) stays = stays && !(i < n && rows[i] == r);
-      if (stays) requantise_row(a, slot0 + r, sc.ratio, lane);
-    }
+    for (int i = 0; i < kHeld; ++i)
+      if (i0 + i < n) {
+        const int2 e = list[i0 + i];
+        if (sc.inv != 0.f) store_row(a, slot0 + e.x, regs[i], sc.inv, lane);
+        else store_row_divided(a, slot0 + e.x, e.y, sc.div);
+      }
+  }
+  if (sc.grown) {
+    const int mine = lane < n ? list[lane].x : -1;
+    for (int r = 0; r < a.block; ++r)
+      if (!__any_sync(kFull, mine == r)) requantise_row(a, slot0 + r, sc.ratio, lane);
+  }
+  __syncwarp();                              // the list is free
   return true;
 }
 
@@ -332,12 +338,13 @@ __global__ void __launch_bounds__(kThreads) insert_claim_kernel(const __grid_con
 // The second writes the blocks: a CTA looks at some tokens and takes the blocks
 // that they lead, first those of few rows, a warp each, then the others
 // together.  Their number gives every SM a CTA, from 16 on (2048 scattered
-// tokens: 25 us with 64 each, 13 with 16) up to 64 (16384 tokens of a prompt:
-// 13 us with 16 each, 9.2 with 64).
+// tokens: 17.5 us with 64 each, 9.3 with 16) up to 64 (16384 tokens of a
+// prompt: 13.7 us with 16 each, 9.4 with 64).
 __global__ void __launch_bounds__(kThreads, 2) insert_many_kernel(const __grid_constant__ InsertArgs a) {
   __shared__ int row_tok[kMaxBlock];
   __shared__ uint32_t warp_max[kWarps];
   __shared__ int lead[kTokensPerCta], large[kTokensPerCta], n_lead, n_large;
+  __shared__ int2 list[kWarps][kAlone];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) n_large = 0;
   // Neighbouring tokens mostly share blocks: their rows are on their way to L2
@@ -365,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 2) insert_many_kernel(const __grid_c
   // (One or two blocks hold many rows each, as in a prompt, or nothing is lost.)
   if (n_lead > 2) {
     for (int i = warp; i < n_lead; i += kWarps)
-      if (!write_block_alone(a, lead[i]) && lane == 0) large[atomicAdd(&n_large, 1)] = lead[i];
+      if (!write_block_alone(a, lead[i], list[warp]) && lane == 0) large[atomicAdd(&n_large, 1)] = lead[i];
   } else if (threadIdx.x == 0) {
     for (n_large = 0; n_large < n_lead; ++n_large) large[n_large] = lead[n_large];
   }
@@ -384,10 +391,10 @@ __global__ void __launch_bounds__(kThreads, 2) insert_many_kernel(const __grid_c
 // list.  For calls of at least a quarter of the cache's slots, whose untouched
 // blocks are few, and eight tokens a block (or about as many blocks as CTAs fit
 // at a time).  32768 tokens, a tenth left out, into 65536 slots of blocks of
-// 64 (56 MB): in a prompt's order 11.6 us (4.9 TB/s), by the tokens' CTAs
-// above 14.1; in any order 16.1 and 100 to 112.  Past those bounds it loses:
-// 8192 into 65536 of blocks of 128 11.1 us, above 9.6; 16384 into 65536 of
-// blocks of 16 17.7, above 13.7.
+// 64 (56 MB): in a prompt's order 11.7 us (4.8 TB/s), by the tokens' CTAs
+// above 14.5; in any order 16.3 and 55.  Past those bounds it loses: 8192
+// into 65536 of blocks of 128 11.1 us, above 9.8; 16384 into 65536 of blocks
+// of 16 17.7, above 12.4.
 __global__ void __launch_bounds__(kThreads, 2) insert_blocks_kernel(const __grid_constant__ InsertArgs a) {
   __shared__ int row_tok[kMaxBlock];
   __shared__ uint32_t warp_max[kWarps];

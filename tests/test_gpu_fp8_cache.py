@@ -92,7 +92,8 @@ def test_insert_matches_the_oracle(T, block, state):
 
 @pytest.mark.parametrize("T,n,block", [
     (700, 4096, 16), (2433, 16384, 64), (3000, 16384, 16), (6000, 32768, 64), (2600, 20800, 1),
-    (6000, 16384, 16), (5000, 16384, 32), (4096, 16384, 27), (4095, 16384, 64), (2048, 2048, 1024)])
+    (6000, 16384, 16), (5000, 16384, 32), (4096, 16384, 27), (4095, 16384, 64), (2048, 2048, 1024),
+    (4000, 24576, 256)])
 @pytest.mark.parametrize("order", ["prompt", "any"])
 def test_insert_of_many_rows(T, n, block, order):
     """Both ways of finding the blocks of a large call, on both sides of the
