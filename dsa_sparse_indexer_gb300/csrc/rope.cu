@@ -63,11 +63,14 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const TableAr
 // table's values are shared: a unit is what one thread takes of a row, a 16-byte
 // vector (interleaved pairs lie within it) or the two vectors at i and
 // i + rot / 2 of the half layout, and a thread takes the same unit of kRows
-// consecutive heads of a token, all loads in flight at once.
+// consecutive heads of a token, all loads in flight at once.  Rows that no
+// 16-byte vectors fit (odd widths, offsets) take vectors of two elements or one.
 // Measured: 4096 tokens of 128 heads of 64 (67 MB in, 67 MB out, strided) in
 // 37 us with every row's token, address and table read found anew, 27.5 so (25
-// in back-to-back replays, 5.3 TB/s); a plain copy of as much takes 23.  64 tokens take 2.0 us, a
-// launch's latency.
+// in back-to-back replays, 5.3 TB/s); a plain copy of as much takes 23.  64
+// tokens take 2.0 us, a launch's latency.  8192 tokens of 32 heads of 130 (136
+// MB) take 28 us, at odd offsets 36 to 41 for 125 values; a head and an element
+// a thread, 134 and 81.
 
 enum { kInterleaved = DSA_ROPE_INTERLEAVED, kHalf = DSA_ROPE_HALF };
 constexpr int kMaxWidth = 1024;               // values of a row
@@ -107,10 +110,11 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   b = fmaf(y, c, x * s);
 }
 
-// V elements per vector: 16 bytes, or 1 where a row's layout has no 16-byte
-// alignment (then an interleaved unit is the two elements of a pair).
-template <typename E, int LAYOUT, int V, int kRows>
-__global__ void __launch_bounds__(V == 1 ? kMaxWidth : 256) rotary_kernel(const RotArgs a) {
+// V elements per vector: 16 bytes, or less where a row's layout is not so
+// aligned (of one element, an interleaved unit is the two of a pair).
+// kTail: a token's last thread may have fewer than kRows heads.
+template <typename E, int LAYOUT, int V, int kRows, bool kTail>
+__global__ void __launch_bounds__(V * sizeof(E) == 16 ? 256 : kMaxWidth / 2) rotary_kernel(const RotArgs a) {
   constexpr int kVecs = LAYOUT == kHalf || V == 1 ? 2 : 1;   // vectors of a rotating unit
   constexpr int kPairs = kVecs * V / 2;
   using VecT = Vec<E, V>;
@@ -120,6 +124,7 @@ __global__ void __launch_bounds__(V == 1 ? kMaxWidth : 256) rotary_kernel(const 
   uint32_t part;
   const uint32_t tok = fdivmod((uint32_t)g, a.fgroups, &part);
   const uint32_t head = part * kRows;
+  const int rows = kTail ? min(kRows, a.H - (int)head) : kRows;
   const bool turning = u < a.turning;
   // Element offsets of the unit's vectors, and its first pair.  A carried unit
   // has as many vectors as a turning one, the last unit perhaps one less.
@@ -139,8 +144,8 @@ __global__ void __launch_bounds__(V == 1 ? kMaxWidth : 256) rotary_kernel(const 
   VecT v[kRows][kVecs];
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    v[k][0] = *reinterpret_cast<const VecT*>(src + k * a.x_head);
-    if (kVecs == 2 && both)
+    if (k < rows) v[k][0] = *reinterpret_cast<const VecT*>(src + k * a.x_head);
+    if (kVecs == 2 && both && k < rows)
       v[k][kVecs - 1] = *reinterpret_cast<const VecT*>(src + k * a.x_head + apart);
   }
   if (turning) {
@@ -183,51 +188,73 @@ __global__ void __launch_bounds__(V == 1 ? kMaxWidth : 256) rotary_kernel(const 
   E* dst = static_cast<E*>(a.out) + tok * a.out_token + head * a.out_head + at0;
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    *reinterpret_cast<VecT*>(dst + k * a.out_head) = v[k][0];
-    if (kVecs == 2 && both)
+    if (k < rows) *reinterpret_cast<VecT*>(dst + k * a.out_head) = v[k][0];
+    if (kVecs == 2 && both && k < rows)
       *reinterpret_cast<VecT*>(dst + k * a.out_head + apart) = v[k][kVecs - 1];
   }
 }
 
-template <typename E, int LAYOUT>
+template <typename E, int LAYOUT, int V>
 cudaError_t launch_rotary(RotArgs& a, bool in_place, cudaStream_t stream) {
-  constexpr int V = 16 / (int)sizeof(E);
-  auto lined = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
-  // 16-byte vectors: both tensors' rows, the turning part's ends (and middle,
-  // in the half layout) and the table's pairs on their boundaries.
-  const bool wide = lined(a.x) && lined(a.out) && lined(a.table) && a.x_token % V == 0 &&
-                    a.x_head % V == 0 && a.out_token % V == 0 && a.out_head % V == 0 &&
-                    a.D % V == 0 && a.first % V == 0 &&
-                    a.rot % (LAYOUT == kHalf ? 2 * V : V) == 0;
-  const int v = wide ? V : 1;
-  const int vecs = LAYOUT == kHalf || !wide ? 2 : 1;
-  a.turning = a.rot / (vecs * v);
-  const int carried = in_place ? 0 : (a.D - a.rot) / v;
-  a.units = a.turning + (carried + vecs - 1) / vecs;
-  // A block holds whole rows: at most kMaxWidth units (256 when wide).  Small
-  // blocks leave an SM sooner and take the next row's loads up earlier: 128
-  // threads measured 28 us where 256 took 31.
-  const int threads = a.units > 128 ? (a.units + 31) / 32 * 32 : 128;
-  a.per_block = threads / a.units;
+  constexpr int kVecs = LAYOUT == kHalf || V == 1 ? 2 : 1;
+  a.turning = a.rot / (kVecs * V);
+  const int carried = in_place ? 0 : (a.D - a.rot) / V;
+  a.units = a.turning + (carried + kVecs - 1) / kVecs;
+  // A block holds whole rows, at most kMaxWidth / 2 units; so many side by side
+  // as leave the fewest threads over, in about 128 threads: small blocks leave
+  // an SM sooner and take the next row's loads up earlier (128 threads measured
+  // 28 us where 256 took 31).
+  int threads = 0;
+  for (int n = (127 + a.units) / a.units; n * a.units <= 256 || threads == 0; ++n) {
+    const int all = (n * a.units + 31) / 32 * 32;
+    if (threads == 0 || n * a.units * threads > a.per_block * a.units * all) {
+      threads = all;
+      a.per_block = n;
+    }
+  }
   auto go = [&](auto kernel, int rows_each) {
-    a.groups = (int64_t)a.T * (a.H / rows_each);
-    a.fgroups = FastDiv((uint32_t)(a.H / rows_each));
+    const int parts = (a.H + rows_each - 1) / rows_each;
+    a.groups = (int64_t)a.T * parts;
+    a.fgroups = FastDiv((uint32_t)parts);
     const int64_t blocks = (a.groups + a.per_block - 1) / a.per_block;
     return launch_kernel(kernel, dim3((unsigned)blocks), dim3((unsigned)threads), 0, stream, 0u,
                          a);
   };
-  // Several heads a thread (four of one vector, two of two) once that still
-  // fills the GPU's 152 SMs twice over; below that the call is latency, and a
-  // head a thread spreads it widest.
-  const bool many = (int64_t)a.T * a.H * a.units >= (int64_t)152 * 2 * 256 * 4;
-  if (!wide) return go(rotary_kernel<E, LAYOUT, 1, 1>, 1);
-  if (many && LAYOUT == kInterleaved && a.H % 4 == 0) return go(rotary_kernel<E, LAYOUT, V, 4>, 4);
-  if (many && a.H % 2 == 0) return go(rotary_kernel<E, LAYOUT, V, 2>, 2);
-  return go(rotary_kernel<E, LAYOUT, V, 1>, 1);
+  // Several heads a thread, 32 or 64 bytes in flight, once that still fills the
+  // GPU's 152 SMs twice over; below that the call is latency, and a head a
+  // thread spreads it widest.  Narrow vectors take eight when they fill all
+  // threads and the heads divide (8192 tokens of 32 heads of 130, bf16: 27.6
+  // us, with four 35).
+  constexpr int kBytes = kVecs * V * (int)sizeof(E), kMany = kBytes > 16 ? 2 : 4;
+  const int64_t all = (int64_t)a.T * a.H * a.units;
+  const bool many = all >= (int64_t)152 * 2 * 256 * 4;
+  if constexpr (kBytes <= 8)
+    if (all >= (int64_t)152 * 2048 * 8 && a.H % 8 == 0)
+      return go(rotary_kernel<E, LAYOUT, V, 8, false>, 8);
+  if (many && a.H % kMany == 0) return go(rotary_kernel<E, LAYOUT, V, kMany, false>, kMany);
+  if (many && a.H > kMany) return go(rotary_kernel<E, LAYOUT, V, kMany, true>, kMany);
+  return go(rotary_kernel<E, LAYOUT, V, 1, false>, 1);
+}
+
+template <typename E, int LAYOUT>
+cudaError_t launch_rotary(RotArgs& a, bool in_place, cudaStream_t stream) {
+  // Vectors of V: both tensors' rows, the turning part's ends (and middle, in
+  // the half layout) and the table's pairs on their boundaries.
+  auto fits = [&](int V) {
+    auto lined = [](const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+    return lined(a.x, V * sizeof(E)) && lined(a.out, V * sizeof(E)) && lined(a.table, 16) &&
+           a.x_token % V == 0 && a.x_head % V == 0 && a.out_token % V == 0 &&
+           a.out_head % V == 0 && a.D % V == 0 && a.first % V == 0 &&
+           a.rot % (LAYOUT == kHalf ? 2 * V : V) == 0;
+  };
+  constexpr int kWide = 16 / (int)sizeof(E);
+  if (fits(kWide)) return launch_rotary<E, LAYOUT, kWide>(a, in_place, stream);
+  if (fits(2)) return launch_rotary<E, LAYOUT, 2>(a, in_place, stream);
+  return launch_rotary<E, LAYOUT, 1>(a, in_place, stream);
 }
 
 template <typename E>
-cudaError_t launch_rotary(RotArgs& a, int layout, bool in_place, cudaStream_t stream) {
+cudaError_t launch_rotary_of(RotArgs& a, int layout, bool in_place, cudaStream_t stream) {
   return layout == kHalf ? launch_rotary<E, kHalf>(a, in_place, stream)
                          : launch_rotary<E, kInterleaved>(a, in_place, stream);
 }
@@ -326,8 +353,8 @@ extern "C" dsa_status dsa_rotary_embed(const void* x, int64_t x_token, int64_t x
   const bool in_place = x == out && (T == 1 || x_token == out_token) && (H == 1 || x_head == out_head);
   if (x == out && !in_place) return DSA_ERR_INVALID_ARG;
   cudaError_t e;
-  if (dtype == DSA_BF16) e = launch_rotary<__nv_bfloat16>(a, layout, in_place, stream);
-  else if (dtype == DSA_FP16) e = launch_rotary<__half>(a, layout, in_place, stream);
-  else e = launch_rotary<float>(a, layout, in_place, stream);
+  if (dtype == DSA_BF16) e = launch_rotary_of<__nv_bfloat16>(a, layout, in_place, stream);
+  else if (dtype == DSA_FP16) e = launch_rotary_of<__half>(a, layout, in_place, stream);
+  else e = launch_rotary_of<float>(a, layout, in_place, stream);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

@@ -59,7 +59,11 @@ def _check(x, pos, cs, got, layout, first, inverse, dtype):
 @pytest.mark.parametrize("T,H,D,rot,first,inverse", [
     (1, 1, 2, 2, 0, False), (1, 128, 64, 64, 0, False), (3, 5, 7, 4, 1, True),
     (37, 3, 192, 64, 128, False), (130, 64, 128, 64, 0, True), (9, 2, 576, 64, 512, False),
-    (2, 3, 1024, 256, 512, True), (2, 1, 1023, 6, 1017, False), (700, 33, 96, 96, 0, False)])
+    (2, 3, 1024, 256, 512, True), (2, 1, 1023, 6, 1017, False), (700, 33, 96, 96, 0, False),
+    # several heads a thread, vectors of every width, heads left over
+    (1000, 7, 130, 98, 0, False), (1200, 8, 132, 100, 32, True), (1100, 5, 125, 90, 3, False),
+    (5000, 8, 130, 66, 2, False), (2600, 16, 127, 126, 1, True), (2500, 3, 200, 40, 8, False),
+    (90, 9, 1022, 256, 6, False)])
 def test_rotation(layout, name, T, H, D, rot, first, inverse):
     import dsa_sparse_indexer_gb300 as dsa
     dtype = DTYPES[name]
