@@ -362,13 +362,6 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   return *reinterpret_cast<float2*>(&r);
 }
 
-// The largest of the warp's values (a NaN loses to a number).
-__device__ __forceinline__ float warp_max(float x) {
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Two values as e4m3 codes, and as the half floats that those stand for.
 __device__ __forceinline__ uint32_t to_e4m3x2(__half2 v) {
   return __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(v), __NV_SATFINITE, __NV_E4M3);
@@ -660,8 +653,10 @@ __device__ __forceinline__ float split_query(const MlaFp8Args& a, Smem& sm, int 
   return factor;
 }
 
-// Sums of 16 values over the warp: lanes i and 16 + i get value i's.
-__device__ __forceinline__ float transpose_sum(const float2 (&v2)[8]) {
+// 16 values of every lane joined over the warp, by halves: lanes i and 16 + i get
+// value i's.  16 shuffles, where one value after another takes 80.
+template <typename Join>
+__device__ __forceinline__ float transpose_join(const float2 (&v2)[8], Join join) {
   const int lane = threadIdx.x & 31;
   float v[16];
 #pragma unroll
@@ -673,9 +668,15 @@ __device__ __forceinline__ float transpose_sum(const float2 (&v2)[8]) {
       if (i < o) {
         const bool up = lane & o;
         const float mine = up ? v[i + o] : v[i], other = up ? v[i] : v[i + o];
-        v[i] = mine + __shfl_xor_sync(kFull, other, o);
+        v[i] = join(mine, __shfl_xor_sync(kFull, other, o));
       }
-  return v[0] + __shfl_xor_sync(kFull, v[0], 16);
+  return join(v[0], __shfl_xor_sync(kFull, v[0], 16));
+}
+__device__ __forceinline__ float transpose_sum(const float2 (&v)[8]) {
+  return transpose_join(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float transpose_max(const float2 (&v)[8]) {
+  return transpose_join(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // ---- the softmax and the outputs ---------------------------------------------------
@@ -807,13 +808,10 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
       }
       float alpha = 1.f;
       if (moves) {
-        float mine = 0.f;
+        float2 xt[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float m = warp_max((i & 1 ? x[i / 2].y : x[i / 2].x) + lt);
-          if ((lane & 15) == i) mine = m;
-        }
-        sm.part[quad][col] = mine;
+        for (int i = 0; i < 8; ++i) xt[i] = fadd2(x[i], make_float2(lt, lt));
+        sm.part[quad][col] = transpose_max(xt);
         barrier(1 + grp, 128);
         // Relative to `ref`; -inf where the tile has no token.
         const float mx = fmaxf(fmaxf(sm.part[0][col], sm.part[1][col]),
