@@ -969,10 +969,11 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
 
 // ---- a split pair's parts together ---------------------------------------------
 // Every CTA of the cluster writes the O of its part of the list, unscaled, and
-// its sums to its slot of the workspace: through shared memory (rows of 512
-// fp32, 16-byte chunks swizzled by the head against bank conflicts, and so they
-// stay) and bulk copies.  After one cluster barrier each reads all parts of the
-// 512 / C dimensions that are its own, from L2, and adds them in rank order.
+// its sums to its slot of the workspace: through shared memory and bulk copies,
+// 16 dimensions of 32 heads at a time ([dims / 16][head][16] fp32, the 16-byte
+// chunks of a head swizzled by it against bank conflicts, and so they stay).
+// After one cluster barrier each reads all parts of the 512 / C dimensions that
+// are its own, from L2, and adds them in rank order.
 // (The same exchange through distributed shared memory, written or read 16
 // bytes a lane, moved about 5 bytes a cycle: 13 us of a 26 us call.)
 constexpr int kSlotFloats = kHeads * kDv + 4 * kHeads;   // O; sum, loss, reference, failed
@@ -995,7 +996,7 @@ __device__ __forceinline__ void merge_parts(const MlaFp8Args& a, Smem& sm, uint3
   }
   if (mine) {
     const int h = (quad & 1) * 32 + lane;    // this thread's head, 64 columns a group
-    float4* row = reinterpret_cast<float4*>(sm.kv[0][0]) + h * (kDv / 4);
+    float4* space = reinterpret_cast<float4*>(sm.kv[0][0]);
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     tc_fence_after();
     for (int cg = grp; cg < 4 && (quad & 1) * 32 < nheads; cg += active / 4) {
@@ -1005,30 +1006,29 @@ __device__ __forceinline__ void merge_parts(const MlaFp8Args& a, Smem& sm, uint3
         uint32_t o[16];
         tmem_ld16(lanes + kOCol + cg * 64 + c, o);
         tmem_wait(o);
+        const int at = ((d0 + c) / 16 * kHeads + h) * 4;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          row[((d0 + c) / 4 + i) ^ (h & 7)] =
+          space[at + (i ^ ((h >> 1) & 3))] =
               make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                           __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                           reinterpret_cast<float4*>(slot) + at),
+                       "r"(smem_u32(space + at)), "r"(32 * 64)
+                       : "memory");
       }
     }
-    proxy_fence();
-    barrier(1 + kGroups, active * 32);
-    // Four heads a warp.
     if (lane == 0) {
-      constexpr int kBytes = kHeads * kDv * 4 / kSoftmaxWarps;
-      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                       reinterpret_cast<char*>(slot) + warp * kBytes),
-                   "r"(smem_u32(sm.kv[0][0]) + warp * kBytes), "r"(kBytes)
-                   : "memory");
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       asm volatile("fence.proxy.async.global;" ::: "memory");
     }
     __syncwarp();
   }
-  __threadfence();
-  cluster_sync();
+  cluster_sync();                            // releases and acquires what was written
   int shard;
   const int64_t head0 = list_of(a, p, &shard) * a.H + hg * kHeads;
   float* factor = reinterpret_cast<float*>(sm.plo);   // [C][64]
@@ -1065,13 +1065,14 @@ __device__ __forceinline__ void merge_parts(const MlaFp8Args& a, Smem& sm, uint3
       a.lse2[head0 + h] = all == 0.f ? -INFINITY : top + log2f(all);
   }
   good = !barrier_or(1 + kGroups, active * 32, !good);
-  const int chunks = kDv / 8 / (int)parts;   // of 8 dimensions, 16 bytes out
-  for (int i = threadIdx.x; i < nheads * chunks; i += active * 32) {
-    const int h = i / chunks, k = 2 * ((int)rank * chunks + i - h * chunks);
+  const int groups = kDv / 16 / (int)parts;  // of 16 dimensions; a thread takes 8 of a head
+  for (int i = threadIdx.x; i < 2 * nheads * groups; i += active * 32) {
+    const int gi = (i >> 1) / nheads, h = (i >> 1) - gi * nheads, d16 = (int)rank * groups + gi;
     uint32_t b[4];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const float4* at = reinterpret_cast<const float4*>(slots + h * kDv) + ((k + half) ^ (h & 7));
+      const float4* at = reinterpret_cast<const float4*>(slots) + (d16 * kHeads + h) * 4 +
+                         ((2 * (i & 1) + half) ^ ((h >> 1) & 3));
       float4 u[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c)
@@ -1089,7 +1090,7 @@ __device__ __forceinline__ void merge_parts(const MlaFp8Args& a, Smem& sm, uint3
       b[2 * half + 1] = *reinterpret_cast<const uint32_t*>(&y1);
     }
     if (good)
-      *reinterpret_cast<uint4*>(a.out + (head0 + h) * kDv + k * 4) =
+      *reinterpret_cast<uint4*>(a.out + (head0 + h) * kDv + d16 * 16 + (i & 1) * 8) =
           make_uint4(b[0], b[1], b[2], b[3]);
   }
 }
