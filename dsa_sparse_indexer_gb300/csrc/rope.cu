@@ -12,46 +12,80 @@
 namespace dsa {
 namespace {
 
+template <typename E, int V>
+struct alignas(sizeof(E) * V) Vec {
+  E e[V];
+};
+
 // ---- the table ---------------------------------------------------------------
 //
 // Entry (p, i) is the angle p w_i.  A far position's angle loses its fraction
 // of a turn in fp32, and fp64 arithmetic is slow here, so the angle is an
 // integer: w_i / 2 pi as a 64-bit fraction of a turn (rounded once, on the
 // host), p times that modulo 2^64, the whole turns falling off the top.  Its
-// upper 32 bits, as a signed number, are the angle within half a turn to
-// 2^-32 turns, whatever p.  A thread keeps its pair i and steps its phase by
-// whole positions (one 64-bit addition each).  Bound by its stores, with the
-// sine and cosine close behind: 131072 positions of 64 values (33.5 MB) take
-// 8.4 us, 4.0 TB/s; 4096 of 128 take 2.5 us, which is a launch's latency.
+// upper 32 bits are the angle to 2^-32 turns, whatever p: the nearest quarter turn
+// in whole, and within an eighth of a turn of it a fraction whose sine and
+// cosine are their power series (to x^9 and x^10: the next terms are below 2e-9
+// there).  A thread keeps its pair i and steps its phase by
+// whole positions (one 64-bit addition each); four pairs where 16-byte stores
+// fit.  Bound by its stores, with the arithmetic close behind: 131072 positions
+// of 64 values (33.5 MB) take 6.4 us, 5.3 TB/s (a pair a thread 7.7, and 8.4
+// with sincospif, whose own reduction is not needed here); 62 values, 8.0.  4096
+// positions of 128 take 2.0 us, a launch's latency.
 constexpr int kMaxPairs = 128;
 constexpr int kTableThreads = 256;
-constexpr int kTablePositions = 64;            // positions per block
 
 struct TableArgs {
   uint64_t step[kMaxPairs];                    // 2^64 w_i / (2 pi)
   float* table;
   float amplitude;
-  int max_pos, half, group;                    // group: positions side by side in a block
+  int max_pos, half, group, steps;             // group: positions side by side in a block
 };
 
-__global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const TableArgs a) {
+// Sine and cosine of u 2^-32 turns.
+__device__ __forceinline__ void sincos_turn(uint32_t u, float* s, float* c) {
+  const uint32_t q = (u + 0x20000000u) >> 30;  // quarter turns
+  const float x = (float)(int32_t)(u - (q << 30)) * (6.283185307179586f * 0x1p-32f), y = x * x;
+  float t = fmaf(y, 1.f / 362880.f, -1.f / 5040.f);
+  t = fmaf(y, t, 1.f / 120.f);
+  t = fmaf(y, t, -1.f / 6.f);
+  const float sine = fmaf(x * y, t, x);
+  t = fmaf(y, -1.f / 3628800.f, 1.f / 40320.f);
+  t = fmaf(y, t, -1.f / 720.f);
+  t = fmaf(y, t, 1.f / 24.f);
+  t = fmaf(y, t, -0.5f);
+  const float cosine = fmaf(y, t, 1.f);
+  const bool odd = q & 1u;
+  *s = __uint_as_float(__float_as_uint(odd ? cosine : sine) ^ ((q & 2u) << 30));
+  *c = __uint_as_float(__float_as_uint(odd ? sine : cosine) ^ (((q + 1u) & 2u) << 30));
+}
+
+// V pairs a thread, side by side.
+template <int V>
+__global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_constant__ TableArgs a) {
   __shared__ uint64_t step[kMaxPairs];
   if (threadIdx.x < a.half) step[threadIdx.x] = a.step[threadIdx.x];
   __syncthreads();
-  const int q = threadIdx.x / a.half, i = threadIdx.x - q * a.half;
+  const int each = a.half / V, q = threadIdx.x / each, i = (threadIdx.x - q * each) * V;
   if (q >= a.group) return;
-  const int end = min(a.max_pos - (int)blockIdx.x * kTablePositions, kTablePositions);
-  const int64_t p0 = (int64_t)blockIdx.x * kTablePositions;
-  uint64_t phase = step[i] * (uint64_t)(p0 + q);
-  const uint64_t stride = step[i] * (uint64_t)a.group;
+  const int64_t p0 = (int64_t)blockIdx.x * (a.group * a.steps);
+  const int end = (int)min((int64_t)a.max_pos - p0, (int64_t)a.group * a.steps);
+  uint64_t phase[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) phase[k] = step[i + k] * (uint64_t)(p0 + q);
   float* row = a.table + (p0 + q) * (2 * a.half) + i;
   for (int p = q; p < end; p += a.group) {
-    float s, c;
-    sincospif((float)(int32_t)(uint32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-    row[0] = c * a.amplitude;
-    row[a.half] = s * a.amplitude;
+    Vec<float, V> s, c;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      sincos_turn((uint32_t)(phase[k] >> 32), &s.e[k], &c.e[k]);
+      s.e[k] *= a.amplitude;
+      c.e[k] *= a.amplitude;
+      phase[k] += step[i + k] * (uint64_t)a.group;
+    }
+    *reinterpret_cast<Vec<float, V>*>(row) = c;
+    *reinterpret_cast<Vec<float, V>*>(row + a.half) = s;
     row += (int64_t)a.group * (2 * a.half);
-    phase += stride;
   }
 }
 
@@ -98,11 +132,6 @@ template <typename E> __device__ __forceinline__ E from_float(float v);
 template <> __device__ __forceinline__ float from_float(float v) { return v; }
 template <> __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
-
-template <typename E, int V>
-struct alignas(sizeof(E) * V) Vec {
-  E e[V];
-};
 
 __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   const float x = a, y = b;
@@ -305,10 +334,16 @@ extern "C" dsa_status dsa_rope_table(int max_pos, int rot_dim, double base, int 
   a.amplitude = amplitude;
   a.max_pos = max_pos;
   a.half = rot_dim / 2;
-  a.group = kTableThreads / a.half;
-  const unsigned grid = (unsigned)(((int64_t)max_pos + kTablePositions - 1) / kTablePositions);
+  // 16-byte stores where the rows allow it.
+  const bool wide = a.half % 4 == 0 && (reinterpret_cast<uintptr_t>(table) & 15u) == 0;
+  a.group = kTableThreads / (wide ? a.half / 4 : a.half);
+  // As many positions a thread as leave every SM two blocks: up to 32 entries.
+  a.steps = wide ? 4 : 8;
+  while (a.steps > 1 && (int64_t)a.group * a.steps * 2 * 152 > max_pos) a.steps /= 2;
+  const int64_t positions = (int64_t)a.group * a.steps;
+  const unsigned grid = (unsigned)((max_pos + positions - 1) / positions);
   const cudaError_t e =
-      launch_kernel(rope_table_kernel, dim3(grid), dim3(kTableThreads), 0, stream, 0u, a);
+      launch_kernel(wide ? rope_table_kernel<4> : rope_table_kernel<1>, dim3(grid), dim3(kTableThreads), 0, stream, 0u, a);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 

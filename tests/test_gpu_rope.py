@@ -24,7 +24,8 @@ DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 @pytest.mark.parametrize("max_pos,rot,base,scaling,factor", [
     (1, 2, 10000.0, "ntk", 4.0), (1, 256, 1e6, None, 1.0), (63, 6, 10000.0, "linear", 2.5),
     (65, 64, 10000.0, "yarn", 40.0), (1000, 96, 500000.0, "ntk", 8.0),
-    (4096, 128, 500000.0, "yarn", 1.0), (262147, 64, 10000.0, "yarn", 32.0)])
+    (4096, 128, 500000.0, "yarn", 1.0), (262147, 64, 10000.0, "yarn", 32.0),
+    (70001, 62, 10000.0, "linear", 4.0), (40003, 8, 10000.0, None, 1.0)])
 def test_table(max_pos, rot, base, scaling, factor):
     import dsa_sparse_indexer_gb300 as dsa
     g = G.Guards()
@@ -34,6 +35,14 @@ def test_table(max_pos, rot, base, scaling, factor):
     assert got is out
     want = RO.table(max_pos, rot, base, 1.25, scaling=scaling, factor=factor)
     assert np.abs(out.cpu().numpy() - want).max() <= 4e-7 * 1.25
+
+
+def test_table_without_alignment():
+    import dsa_sparse_indexer_gb300 as dsa
+    held = torch.full((50 * 64 + 2,), 7.0, device="cuda")
+    got = dsa.rope_table(50, 64, out=held[1:-1].view(50, 64))
+    assert torch.equal(got, dsa.rope_table(50, 64))
+    assert float(held[0]) == 7.0 and float(held[-1]) == 7.0
 
 
 def _check(x, pos, cs, got, layout, first, inverse, dtype):
