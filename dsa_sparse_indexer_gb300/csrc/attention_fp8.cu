@@ -219,18 +219,6 @@ __device__ __forceinline__ void proxy_fence() {
 __device__ __forceinline__ void mbar_arrive1(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
 // Named hardware barriers of the softmax's warps, which run the same sequence
 // of them whatever happens: a failed wait does not end their loops, so that no
 // warp is left behind.
@@ -385,9 +373,10 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
                "r"(in ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void landed(uint64_t* bar) {   // this lane's copies, for the MMAs
-  proxy_fence();
-  mbar_arrive1(bar);
+// An arrival once this lane's copies so far have landed; the thread that then
+// issues MMAs on them fences them to the async proxy.
+__device__ __forceinline__ void arrive_landed(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ void gather_tiles(const MlaFp8Args& a, Smem& sm, int p0, int p1) {
@@ -419,33 +408,10 @@ __device__ __forceinline__ void gather_tiles(const MlaFp8Args& a, Smem& sm, int 
     fetch();
     fetch_mine();
   }
-  // Parts issued and not yet handed over, the older first: at most two.
-  uint64_t *older = nullptr, *newer = nullptr;
-  auto drain = [&]() {
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (older) landed(older);
-    if (newer) landed(newer);
-    older = newer = nullptr;
-  };
-  // A part may be filled once the value products of its last tile are done;
-  // where that is still to come, what has been issued is handed over first.
+  // A part may be filled once the value products of its last tile are done.
   auto room = [&](uint64_t* empty, int k) {
-    if (k >= 1 && !__all_sync(kFull, mbar_test(empty, (uint32_t)(k - 1) & 1u))) {
-      drain();
-      ok = wait_or_abort(sm, empty, (uint32_t)(k - 1) & 1u);
-    }
-    if (newer) {
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      landed(older);
-      older = newer;
-      newer = nullptr;
-    }
+    if (k >= 1) ok = wait_or_abort(sm, empty, (uint32_t)(k - 1) & 1u);
     return __all_sync(kFull, ok) != 0;
-  };
-  auto issued = [&](uint64_t* full) {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    if (older) newer = full;
-    else older = full;
   };
   for (int n = 0; cur.valid(p1); ++n) {
     const int st = n & 1, k = n >> 1, left = cur.count - cur.t * kTile - row0;
@@ -481,7 +447,7 @@ __device__ __forceinline__ void gather_tiles(const MlaFp8Args& a, Smem& sm, int 
     };
     if (!room(&sm.emptyA[st], k)) break;
     if (left > 0) copy_pair(0);
-    issued(&sm.fullA[st]);
+    arrive_landed(&sm.fullA[st]);
     if (!room(&sm.emptyB[st], k)) break;
     bad |= in && !(ts == 0.f || (ts >= kMinScale && ts <= kMaxScale));
     sm.tok[st][row0 + lane] = !in ? -1.f : ts > 0.f ? ts : 0.f;
@@ -494,9 +460,11 @@ __device__ __forceinline__ void gather_tiles(const MlaFp8Args& a, Smem& sm, int 
                cache + (int64_t)max(row, 0) * kDqk + kDv - (c & 4) * 16, row >= 0);
       }
     }
-    issued(&sm.fullB[st]);
+    arrive_landed(&sm.fullB[st]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive1(&sm.fullB[st]);   // the scales
   }
-  drain();                                   // none outlives the CTA
+  asm volatile("cp.async.wait_all;" ::: "memory");   // none outlives the CTA
   if (!__all_sync(kFull, ok) && lane == 0 && !aborted(sm)) abort_cta(sm, a.flags);
   if (bad) raise_flag(a.flags, DSA_FLAG_BOUNDS);
 }
@@ -527,10 +495,12 @@ __device__ __forceinline__ bool issue_scores(const MlaFp8Args& a, Smem& sm, uint
     if ((n >= 2 && !wait_or_abort(sm, &sm.sfree[st], parity ^ 1u)) ||
         !wait_or_abort(sm, &sm.fullA[st], parity))
       return false;
+    proxy_fence();
     tc_fence_after();
     block(d, st, 0);
     block(d, st, 1);
     if (!wait_or_abort(sm, &sm.fullB[st], parity)) return false;
+    proxy_fence();
     tc_fence_after();
     block(d, st, 2);
     block(d, st, 3);
@@ -1147,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.fullA[i], 32 * kGatherWarps + kStalledArrivals);   // every gathering lane
-      mbar_init(&sm.fullB[i], 32 * kGatherWarps);
+      mbar_init(&sm.fullB[i], 33 * kGatherWarps);
       mbar_init(&sm.emptyA[i], 1);
       mbar_init(&sm.emptyB[i], 1);
       mbar_init(&sm.sfull[i], 1);
