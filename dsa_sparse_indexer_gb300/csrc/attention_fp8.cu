@@ -10,9 +10,9 @@
 // floats instead: the query (bf16, 8 significant bits) as e4m3 + e4m3 after a
 // power of two per head that brings its largest value to [2^7, 2^8), exact but
 // for values below 2^-10 of that one; a weight as e4m3 plus what that leaves as
-// e5m2 (7 bits and more, down to 2^-17).  Two products with 8-bit operands cost
-// what one with 16-bit ones does.  The scale of a token's block multiplies its
-// scores, and its weight before that is split.
+// e5m2 (to 2^-7 of it; below 2^-9 of the largest to 2^-16 of that one).  Two
+// products with 8-bit operands cost what one with 16-bit ones does.  The scale
+// of a token's block multiplies its scores, and its weight before that is split.
 //
 // A CTA takes 64 heads of one (row, shard), tiles of 128 tokens:
 //  * S^T[token][head]: A = the tile (M = 128 tokens, K-major), B = the query
@@ -30,8 +30,9 @@
 //
 //  warps 0-15  the softmax: a token and 16 heads a thread, the running
 //              reference of a head moving only when a weight would pass its
-//              bound; the outputs; and a row's query in its two parts, the next
-//              one's while this one's last value products run
+//              bound; the outputs (with few heads warps 8-15 write them); and a
+//              row's query in its two parts, the next one's while this one's last
+//              value products run
 //  warps 16-19 gather the selected rows, 32 of each tile a warp, 16-byte
 //              cp.async into the swizzled layouts; a stage is filled and freed
 //              in two parts (dimensions 0-255, the rest), as the value products
@@ -43,7 +44,7 @@
 // clusters of CTAs.
 // Measured, 128 heads: 512 rows of 2048 tokens in 282 us (1.04 PFLOP/s of 16-bit
 // work, 0.55 of a measured bf16 GEMM); 64 rows, 4 shards of 520 tokens in 70 us;
-// 16 heads, 128 rows, 8 shards of 256 tokens in 50 us; a row of 2048 tokens in
+// 16 heads, 128 rows, 8 shards of 256 tokens in 46 us; a row of 2048 tokens in
 // 20.4 us.  Bound by the chain gather, scores, softmax, values over two stages,
 // about 4030 cycles a tile where the MMAs take 2840, and by a pair's end: 6
 // thousand cycles, 13 when a new row's query has to be split.
@@ -78,6 +79,9 @@ constexpr int kThreads = 768;                // six warpgroups; warps 22-23 only
 // Registers a thread of the softmax's four warpgroups, the gathering one and
 // the MMA's: 128 (4 x 88 + 64 + 64) = the 768 x 80 the CTA is launched with.
 constexpr int kRegsSoftmax = 88, kRegsGather = 64, kRegsMma = 64;
+// With few heads: two warpgroups of the softmax, two that write outputs.
+constexpr int kWriter0 = 8, kRegsFew = 112, kRegsWriter = 64;
+static_assert(128 * (2 * kRegsFew + 2 * kRegsWriter + kRegsGather + kRegsMma) <= kThreads * 80, "registers");
 static_assert(128 * (4 * kRegsSoftmax + kRegsGather + kRegsMma) <= kThreads * 80, "registers");
 // Tensor-memory columns.
 constexpr int kOCol = 0, kSCol = 256, kTmemCols = 512;
@@ -113,7 +117,7 @@ struct alignas(1024) Smem {
   int counts[kCounts];                       // of the CTA's first pairs
   int first;                                 // the CTA's first token of its pair (split pairs)
   uint64_t qfull, fullA[kStages], fullB[kStages], emptyA[kStages], emptyB[kStages];
-  uint64_t sfull[2], sfree[2], pfull, pvdone, drain[2];
+  uint64_t sfull[2], sfree[2], pfull, pvdone, ofree, drain[2];
   uint32_t tmem;
   int abort;
 };
@@ -243,6 +247,9 @@ __device__ __forceinline__ bool barrier_or(int id, int threads, bool mine) {
 }
 __device__ __forceinline__ void barrier(int id, int threads) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(int id, int threads) {
+  asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // ---- clusters: a pair split over several CTAs ------------------------------
@@ -521,16 +528,21 @@ __device__ __forceinline__ bool issue_scores(const MlaFp8Args& a, Smem& sm, uint
 }
 
 __device__ __forceinline__ bool issue_values(const MlaFp8Args& a, Smem& sm, uint32_t tmem, int p0,
-                                             int p1) {
+                                             int p1, bool handed) {
   constexpr uint32_t kIdHi = idesc_f8(kHeads, 256, 0, 1, 1), kIdLo = idesc_f8(kHeads, 256, 1, 1, 1);
   const uint64_t lod = smem_desc(smem_u32(sm.plo), 16, 512, 4);
   Cursor cur(a, sm, p0, p1);
+  int pair = -1;                             // pairs begun, less one
   for (int n = 0; cur.valid(p1); ++n) {
     // Groups of 32 tokens that the tile has; the two halves of the dimensions
     // one after the other, so that the first one's blocks free early.
     const int st = n & 1, steps = min(kTile / 32, (cur.count - cur.t * kTile + 31) / 32);
     const uint64_t hid = smem_desc(smem_u32(sm.rope[st]), 16, 512, 4);
     if (!wait_or_abort(sm, &sm.pfull, (uint32_t)n & 1u)) return false;
+    // Where others write a pair's outputs, they have read the last pair's O.
+    if (handed && cur.t == 0 && ++pair > 0 &&
+        !wait_or_abort(sm, &sm.ofree, (uint32_t)(pair - 1) & 1u))
+      return false;
     tc_fence_after();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -594,12 +606,12 @@ __device__ __forceinline__ float split_query(const MlaFp8Args& a, Smem& sm, int 
   const uint4 none = make_uint4(0, 0, 0, 0);
   uint4 v[kEach][2];
   const int ri = lane >> 3;                  // this lane's rope chunk: its head, and place
-  const uint4 rope = gh0 + ri < a.H ? __ldg(src + ri * (kDqk / 8) + kDv / 8 + (lane & 7)) : none;
+  const uint4 rope = gh0 + ri < a.H ? __ldcs(src + ri * (kDqk / 8) + kDv / 8 + (lane & 7)) : none;
 #pragma unroll
   for (int i = 0; i < kEach; ++i)
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      v[i][c] = gh0 + i < a.H ? __ldg(src + i * (kDqk / 8) + c * 32 + lane) : none;
+      v[i][c] = gh0 + i < a.H ? __ldcs(src + i * (kDqk / 8) + c * 32 + lane) : none;
   uint32_t mr = chunk_amax(rope);
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) mr = max(mr, __shfl_xor_sync(kFull, mr, o));
@@ -675,7 +687,113 @@ __device__ __forceinline__ int active_warps(int nheads) {
   return (nheads + kGroupHeads - 1) / kGroupHeads * 4;
 }
 
-template <bool kSplit>
+// Outputs of a pair by warp `quad` of `groups` groups; `of_h` is the factor of
+// head (quad & 1) 32 + lane.  The warp's 32 tensor-memory lanes hold heads
+// (quad & 1) 32 + lane, 64 columns a group.  16 lanes and 32 columns at a time; a
+// thread holds two columns of each 8 of two heads, and swaps with its neighbour
+// so that four threads store 32 contiguous bytes of a head, a whole sector: 4.8
+// thousand cycles a pair of 64 heads, 2.1 of them the stores.  (More with a head
+// a thread and 32-byte stores, and with 16 bytes a thread after two exchanges.
+// From the last stage's space by bulk copies it is 1.3, but the stage then comes
+// back later: the same time in all, and 12 % more where pairs have two tiles.)
+__device__ __forceinline__ void write_outputs(const MlaFp8Args& a, uint32_t lanes, int64_t head0,
+                                              int nheads, int grp, int groups, float of_h,
+                                              bool good) {
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
+  float inv[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) inv[i] = __shfl_sync(kFull, of_h, 8 * i + (lane >> 2));
+  const int j = lane & 3;
+  for (int cg = grp; cg < 4; cg += groups) {
+    __nv_bfloat16* orow = a.out + (head0 + (quad & 1) * 32 + (lane >> 2)) * kDv + (cg >> 1) * 256 +
+                          (quad >> 1) * 128 + (cg & 1) * 64 + (j & 1) * 8 + (j >> 1) * 4;
+#pragma unroll
+    for (int up16 = 0; up16 < 2; ++up16) {
+      if ((quad & 1) * 32 + up16 * 16 >= nheads) break;
+      uint32_t o0[16], o1[16];             // columns 0-31 and 32-63
+      tmem_ld32_of16(lanes + ((uint32_t)up16 << 20) + kOCol + cg * 64, o0);
+      tmem_ld32_of16(lanes + ((uint32_t)up16 << 20) + kOCol + cg * 64 + 32, o1);
+      tmem_wait(o0);
+      tmem_wait(o1);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {        // 32 columns; heads lane / 4, then 8 + lane / 4
+        const int c = (q >> 1) * 32, half = q & 1;
+        const uint32_t(&o)[16] = q < 2 ? o0 : o1;
+        const float f = inv[2 * up16 + half];
+        uint32_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 y =
+              __floats2bfloat162_rn(__uint_as_float(o[4 * i + 2 * half]) * f,
+                                    __uint_as_float(o[4 * i + 2 * half + 1]) * f);
+          b[i] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        const int h = up16 * 16 + half * 8;
+        const bool there = good && (quad & 1) * 32 + h + (lane >> 2) < nheads;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {      // columns 16 k .. + 15: 8-column groups 2 k, 2 k + 1
+          const uint32_t give = j & 1 ? b[2 * k] : b[2 * k + 1];
+          const uint32_t got = __shfl_xor_sync(kFull, give, 1);
+          const uint2 v = j & 1 ? make_uint2(got, b[2 * k + 1]) : make_uint2(b[2 * k], got);
+          if (there) *reinterpret_cast<uint2*>(orow + (int64_t)h * kDv + c + 16 * k) = v;
+        }
+      }
+    }
+  }
+}
+
+// With up to 32 heads (kFew), half of the softmax's warps or more have none:
+// two warpgroups write the outputs, while the softmax goes on with the next
+// pair, with more registers a thread (16 heads, pairs of two to three tiles:
+// 49.5 -> 46.4 us; 32 heads 53.2 -> 48.7; in longer pairs the same).  A pair's
+// sums reach the writers in those parts of the weights' space that belong to no
+// head, alternately in two: the softmax cannot end a pair before the outputs of
+// the one before the last are written, as its first value product waits for
+// them.
+constexpr int kHanded = 32;                  // heads
+__device__ __forceinline__ float* handed_over(Smem& sm, int which, int i) {
+  const int t = i >> 2;                      // 16 bytes of a token's 64, swizzled as the weights are
+  return reinterpret_cast<float*>(sm.plo + t * 64 + (((2 + which) ^ ((t >> 1) & 3)) << 4)) + (i & 3);
+}
+
+__device__ __forceinline__ void write_handed(const MlaFp8Args& a, Smem& sm, uint32_t tmem, int hg,
+                                             int p0, int p1) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3;
+  const int nheads = min(kHeads, a.H - hg * kHeads), active = active_warps(nheads);
+  const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+  bool ok = true;
+  Cursor cur(a, sm, p0, p1);
+  for (int n = 0, pair = 0; cur.valid(p1); ++pair) {
+    const int p = cur.p, which = pair & 1;
+    n += (cur.count + kTile - 1) / kTile;
+    cur.next_pair(a, sm, p0, p1);
+    barrier(2 + kGroups + which, (active + kSoftmaxWarps - kWriter0) * 32);
+    bool good = true;
+    for (int i = 0; i < active; ++i) good = good && *handed_over(sm, which, 9 * kHanded + i) != 0.f;
+    float off = 0.f, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sum += *handed_over(sm, which, i * kHanded + lane);
+      off += *handed_over(sm, which, (4 + i) * kHanded + lane);
+    }
+    const float ref = *handed_over(sm, which, 8 * kHanded + lane);
+    if (!wait_or_abort(sm, &sm.pvdone, (uint32_t)(n - 1) & 1u)) ok = false;
+    good = __all_sync(kFull, good && ok);
+    tc_fence_after();
+    int shard;
+    const int64_t head0 = list_of(a, p, &shard) * a.H + hg * kHeads;
+    if (warp == kWriter0 && lane < nheads && good)
+      a.lse2[head0 + lane] = sum == 0.f ? -INFINITY : ref + log2f(sum);
+    write_outputs(a, lanes, head0, nheads, (warp - kWriter0) >> 2, (kSoftmaxWarps - kWriter0) / 4,
+                  sum == 0.f ? 0.f : 1.f / (sum - off), good);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive1(&sm.ofree);
+  }
+  if (!__all_sync(kFull, ok) && lane == 0 && !aborted(sm)) abort_cta(sm, a.flags);
+}
+
+template <bool kSplit, bool kFew>
 __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm, uint32_t tmem,
                                                   int hg, int p0, int p1) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3, grp = warp >> 2;
@@ -709,14 +827,14 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
     if (lane < 4) sm.fq[4 * warp + lane] = f;
     barrier(1 + kGroups, active * 32);
   }
-  int n = 0;                                 // tiles done
+  int n = 0, which = 0;                      // tiles done; the parity of pairs
 #pragma unroll 1
   while (cur.valid(p1)) {
     const int p = cur.p, ntiles = (cur.count + kTile - 1) / kTile;
     cur.next_pair(a, sm, p0, p1);
     const bool first = cur.valid(p1) && row_of(a, cur.p) != row_of(a, p);   // of its row
     // The last pair's sums have been read, and a new row's factors are there.
-    if (n > 0) barrier(1 + kGroups, active * 32);
+    if (n > 0 && !kFew) barrier(1 + kGroups, active * 32);
     const float4* fq = reinterpret_cast<const float4*>(sm.fq + col0);
     float ref = 0.f;                         // of head `col`
     bool fresh = true;                       // every token so far left out: no reference yet
@@ -867,6 +985,23 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
     // The sums over all tokens: 32 lanes, then the group's four warps, exchanged
     // in the weights' space once the value products have read it.
     const float all = transpose_sum(l), less = transpose_sum(gone);
+    if (kFew) {
+      *handed_over(sm, which, quad * kHanded + col) = all;
+      *handed_over(sm, which, (4 + quad) * kHanded + col) = less;
+      if (quad == 0) *handed_over(sm, which, 8 * kHanded + col) = ref;
+      const bool good = __all_sync(kFull, ok);
+      if (lane == 0) *handed_over(sm, which, 9 * kHanded + warp) = good ? 1.f : 0.f;
+      __threadfence_block();
+      barrier_arrive(2 + kGroups + which, (active + kSoftmaxWarps - kWriter0) * 32);
+      which ^= 1;
+      if (first) {
+        const float factor = split_query(a, sm, row_of(a, cur.p), hg);
+        barrier(1 + kGroups, active * 32);
+        if (lane < 4) sm.fq[4 * warp + lane] = factor;
+        barrier(1 + kGroups, active * 32);
+      }
+      continue;
+    }
     // This row's scores are done: the next row's query takes the place of this
     // one's while the last value products run.
     float factor = 0.f;
@@ -892,54 +1027,7 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
         a.lse2[head0 + h] = sum == 0.f ? -INFINITY : w[8 * kHeads + h] + log2f(sum);
     }
     barrier(1 + kGroups, active * 32);
-    // The warp's 32 tensor-memory lanes hold heads (quad & 1) 32 + lane, 64
-    // columns a group.  16 lanes and 32 columns at a time; a thread holds two
-    // columns of each 8 of two heads, and swaps with its neighbour so that four
-    // threads store 32 contiguous bytes of a head, a whole sector: 3.8 thousand
-    // cycles a pair, beside the next pair's scores.  (5.0 with a head a thread and
-    // 32-byte stores.  From the last stage's space by bulk copies it is 1.3, but
-    // the stage then comes back later: the same time in all, and 12 % more where
-    // pairs have two tiles.)
-    float inv[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) inv[i] = sm.part[0][(quad & 1) * 32 + 8 * i + (lane >> 2)];
-    const int j = lane & 3;
-    for (int cg = grp; cg < 4; cg += active / 4) {
-      __nv_bfloat16* orow = a.out + (head0 + (quad & 1) * 32 + (lane >> 2)) * kDv + (cg >> 1) * 256 +
-                            (quad >> 1) * 128 + (cg & 1) * 64 + (j & 1) * 8 + (j >> 1) * 4;
-#pragma unroll
-      for (int up16 = 0; up16 < 2; ++up16) {
-        if ((quad & 1) * 32 + up16 * 16 >= nheads) break;
-        uint32_t o0[16], o1[16];             // columns 0-31 and 32-63
-        tmem_ld32_of16(lanes + ((uint32_t)up16 << 20) + kOCol + cg * 64, o0);
-        tmem_ld32_of16(lanes + ((uint32_t)up16 << 20) + kOCol + cg * 64 + 32, o1);
-        tmem_wait(o0);
-        tmem_wait(o1);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {        // 32 columns; heads lane / 4, then 8 + lane / 4
-          const int c = (q >> 1) * 32, half = q & 1;
-          const uint32_t(&o)[16] = q < 2 ? o0 : o1;
-          const float f = inv[2 * up16 + half];
-          uint32_t b[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 y =
-                __floats2bfloat162_rn(__uint_as_float(o[4 * i + 2 * half]) * f,
-                                      __uint_as_float(o[4 * i + 2 * half + 1]) * f);
-            b[i] = *reinterpret_cast<const uint32_t*>(&y);
-          }
-          const int h = up16 * 16 + half * 8;
-          const bool there = good && (quad & 1) * 32 + h + (lane >> 2) < nheads;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {      // columns 16 k .. + 15: 8-column groups 2 k, 2 k + 1
-            const uint32_t give = j & 1 ? b[2 * k] : b[2 * k + 1];
-            const uint32_t got = __shfl_xor_sync(kFull, give, 1);
-            const uint2 v = j & 1 ? make_uint2(got, b[2 * k + 1]) : make_uint2(b[2 * k], got);
-            if (there) *reinterpret_cast<uint2*>(orow + (int64_t)h * kDv + c + 16 * k) = v;
-          }
-        }
-      }
-    }
+    write_outputs(a, lanes, head0, nheads, grp, active / 4, sm.part[0][(quad & 1) * 32 + lane], good);
   }
   if (!__all_sync(kFull, ok) && lane == 0 && !aborted(sm)) abort_cta(sm, a.flags);
 }
@@ -1072,7 +1160,7 @@ __device__ __forceinline__ void merge_parts(const MlaFp8Args& a, Smem& sm, uint3
   }
 }
 
-template <bool kSplit>
+template <bool kSplit, bool kFew>
 __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(const MlaFp8Args a) {
   extern __shared__ __align__(1024) unsigned char mla_fp8_smem[];
   Smem& sm = *reinterpret_cast<Smem*>(mla_fp8_smem);
@@ -1133,6 +1221,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
     mbar_init(&sm.qfull, active);
     mbar_init(&sm.pfull, active);
     mbar_init(&sm.pvdone, 1);
+    mbar_init(&sm.ofree, kSoftmaxWarps - kWriter0);
     mbar_init(&sm.drain[0], 1);
     mbar_init(&sm.drain[1], 1);
     sm.abort = 0;
@@ -1143,10 +1232,16 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
 
-  if (warp < kSoftmaxWarps) {
+  if (kFew && warp < kWriter0) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+    if (warp < active) softmax_and_store<kSplit, kFew>(a, sm, tmem, hg, p0, p1);
+  } else if (kFew && warp < kSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWriter));
+    write_handed(a, sm, tmem, hg, p0, p1);
+  } else if (warp < kSoftmaxWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     if (warp < active) {
-      softmax_and_store<kSplit>(a, sm, tmem, hg, p0, p1);
+      softmax_and_store<kSplit, kFew>(a, sm, tmem, hg, p0, p1);
       if (kSplit) merge_parts(a, sm, tmem, hg, p0, sm.counts[0] > 0);
     } else if (kSplit) {
       cluster_sync();                        // the merge's barrier
@@ -1160,7 +1255,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
     if (tid == kMmaWarp * 32)
       drain_mmas(a, sm, &sm.drain[0], issue_scores(a, sm, tmem, p0, p1));
     else if (tid == (kMmaWarp + 1) * 32)
-      drain_mmas(a, sm, &sm.drain[1], issue_values(a, sm, tmem, p0, p1));
+      drain_mmas(a, sm, &sm.drain[1], issue_values(a, sm, tmem, p0, p1, kFew));
     __syncwarp();
     if (kSplit) cluster_sync();
   }
@@ -1223,7 +1318,9 @@ extern "C" dsa_status dsa_sparse_mla_decode_fp8(const uint16_t* q, const uint8_t
   const unsigned parts = work ? (unsigned)split_parts(pairs, hgroups, K) : 1u;
   const int smem = (int)sizeof(Smem);
   const auto kernel =
-      parts > 1 ? sparse_mla_decode_fp8_kernel<true> : sparse_mla_decode_fp8_kernel<false>;
+      parts > 1       ? sparse_mla_decode_fp8_kernel<true, false>
+      : H <= kHanded ? sparse_mla_decode_fp8_kernel<false, true>
+                     : sparse_mla_decode_fp8_kernel<false, false>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return DSA_ERR_CUDA;
   const MlaFp8Args a{reinterpret_cast<const __nv_bfloat16*>(q),

@@ -2,13 +2,19 @@
 the oracle (oracle/kv_fp8.py), dsa_sparse_mla_decode_fp8 with the fp64 softmax
 (oracle/attention.py) over the cache's values, and both in the decode loop.
 
-Attention tolerance, from the arithmetic.  A weight p_j enters the value
-product as two 8-bit floats, the second holding what the first leaves: a
-relative error below 2^-4 2^-3 = 2^-7 (half a step of e4m3 times half a step of
-e5m2), or 2^-17 absolute where that is more, with the largest weight at least
-2^3: 2^-20.  O = sum p v / sum p then moves by at most
-sum p (2^-7 + 2^-20 / p) |v - O| / sum p (first order; 1 % more covers the
-second).  The query enters the scores as two 8-bit floats with an error below
+Attention tolerance, from the arithmetic.  A weight, times its token's scale
+t_j, enters the value product as u_j = p_j t_j in two 8-bit floats, the second
+holding what the first leaves; the largest u is at least 2^3.
+ * u >= 2^-6: e4m3 leaves at most 2^-4 u, of which e5m2 leaves 2^-3: 2^-7 u.
+ * u < 2^-6: e4m3's steps are 2^-9 there and it leaves at most 2^-10 and at most
+   u, of which e5m2 leaves 2^-3: min(2^-13, 2^-3 u); or half of e5m2's least
+   step, 2^-17.
+With m the largest u, an error of 2^-13 is at most 2^-16 m, of 2^-17 2^-20 m, so
+that p_j is off by at most e_j = 2^-7 p_j + min(2^-16 m / t_j, 2^-3 p_j) +
+2^-20 m / t_j.  The normaliser follows these errors: O = sum p v / sum p moves by
+at most sum e |v - O| / sum p (first order; 1 % more covers the second).  It does
+not follow the rounding of u to fp16 before, half a step 2^-11: 2^-11 sum p |v|.
+The query enters the scores as two 8-bit floats with an error below
 2^-18 of its head's largest value, and their sums are fp32 (2^-20 of the sum of
 magnitudes, over 576 products): a score is off by
 d = |scale| (2^-18 max|q| sum|k| + 2^-20 sum|q k|), moving lse2 by d / ln 2 and
@@ -206,14 +212,18 @@ def test_insert_refusals():
 # ---- the attention --------------------------------------------------------------
 
 
-def _tolerance(q, rows, scale, out, lse2):
-    """(out, lse2) bounds of one (shard, row): q [H, 576], rows [n, 576]."""
+def _tolerance(q, rows, scale, out, lse2, t=None):
+    """(out, lse2) bounds of one (shard, row): q [H, 576], rows [n, 576], t [n] the
+    rows' scales (all alike when not given)."""
     x = scale * (q @ rows.T)
     p = np.exp(x - x.max(axis=1, keepdims=True))
     p /= p.sum(axis=1, keepdims=True)
     v = np.abs(rows[None, :, :512] - out[:, None, :])                  # [H, n, 512]
     spread = np.einsum("hn,hnd->hd", p, v)
-    lost = 2.0 ** -20 * v.sum(axis=1)
+    t = np.ones(len(rows)) if t is None else t.astype(np.float64)
+    m = (p * t).max(axis=1, keepdims=True) / t                         # m / t_j
+    lost = np.einsum("hn,hnd->hd", np.minimum(2.0 ** -16 * m, 2.0 ** -3 * p) + 2.0 ** -20 * m, v)
+    lost += 2.0 ** -11 * (p @ np.abs(rows[:, :512]))
     d = abs(scale) * (2.0 ** -18 * np.abs(q).max(axis=1) * np.abs(rows).sum(axis=1).max()
                       + 2.0 ** -20 * (np.abs(q) @ np.abs(rows).T).max(axis=1))
     tol = 2.0 ** -8 * np.abs(out) + 1.01 * ((2.0 ** -7 + 2 * d[:, None]) * spread + lost) + 1e-30
@@ -236,8 +246,9 @@ def _attend(q_bits, codes, scales, slots, counts, scale=SCALE):
             lse2.cpu().numpy().astype(np.float64), int(err.item()))
 
 
-def _check(q_bits, values, slots, counts, scale, out, lse2, pairs=None):
-    """values: [S, n_slots, 576] fp64, or a function of (shard, slots)."""
+def _check(q_bits, values, slots, counts, scale, out, lse2, pairs=None, scales=None):
+    """values: [S, n_slots, 576] fp64, or a function of (shard, slots); scales:
+    [S, blocks], where they are not all alike."""
     q = OC.bf16_to_f64(q_bits)
     S, R = counts.shape
     at = values if callable(values) else (lambda s, j: values[s, j])
@@ -248,7 +259,8 @@ def _check(q_bits, values, slots, counts, scale, out, lse2, pairs=None):
             continue
         rows = at(s, sel)
         want_o, want_l = OA.sparse_mla_decode(q[r], rows, scale, 512)
-        tol_o, tol_l = _tolerance(q[r], rows, scale, want_o, want_l)
+        t = None if scales is None else scales[s, sel // (values.shape[1] // scales.shape[1])]
+        tol_o, tol_l = _tolerance(q[r], rows, scale, want_o, want_l, t)
         off = np.abs(out[s, r] - want_o) / tol_o
         assert (off <= 1).all(), (s, r, off.max(), np.argwhere(off > 1)[:4])
         assert (np.abs(lse2[s, r] - want_l) <= tol_l).all(), (s, r, np.abs(lse2[s, r] - want_l).max())
@@ -277,7 +289,7 @@ def test_random_slot_sets(H, block):
         slots[s, r, :counts[s, r]] = rng.choice(n_slots, counts[s, r], replace=False)
     out, lse2, err = _attend(q, codes, scales, slots, counts)
     assert err == 0
-    _check(q, KF.values(codes, scales), slots, counts, SCALE, out, lse2)
+    _check(q, KF.values(codes, scales), slots, counts, SCALE, out, lse2, scales=scales)
 
 
 @pytest.mark.parametrize("rows,S,K", [(1, 1, 1), (1, 1, 2048), (2, 1, 2048), (1, 3, 777),
@@ -295,7 +307,29 @@ def test_few_and_many_rows(rows, S, K):
     out, lse2, err = _attend(q, codes, scales, slots, counts)
     assert err == 0
     pairs = None if rows * S <= 8 else [(s, r) for s in range(S) for r in rng.integers(0, rows, 4)]
-    _check(q, KF.values(codes, scales), slots, counts, SCALE, out, lse2, pairs)
+    _check(q, KF.values(codes, scales), slots, counts, SCALE, out, lse2, pairs, scales)
+
+
+@pytest.mark.parametrize("H", [1, 16, 17, 32, 33, 48])
+def test_few_heads_many_rows(H):
+    """Many pairs a CTA, with idle softmax warps: lists from none to four tiles,
+    rows with nothing on any shard, one pair between new rows."""
+    rng = np.random.default_rng(H)
+    rows, S, K, n_slots = 250, 3, 400, 4096
+    codes, scales = _cache(rng, S, n_slots, 64, False)
+    q = W.mla_query(rows, H, seed=H)
+    counts = rng.integers(1, K + 1, (S, rows))
+    counts[:, ::3] = rng.integers(0, 130, counts[:, ::3].shape)
+    counts[rng.random((S, rows)) < 0.2] = 0
+    counts[:, 7:9] = 0
+    counts[1:, 40:60] = 0
+    slots = rng.integers(0, n_slots, (S, rows, K))
+    out, lse2, err = _attend(q, codes, scales, slots, counts)
+    assert err == 0
+    pairs = [(s, r) for s in range(S) for r in list(range(0, 12)) + list(range(40, 250, 9))]
+    _check(q, KF.values(codes, scales), slots, counts, SCALE, out, lse2, pairs, scales)
+    again, lse2_again, _ = _attend(q, codes, scales, slots, counts)
+    assert np.array_equal(out, again) and np.array_equal(lse2, lse2_again)
 
 
 @pytest.mark.parametrize("rows,K", [(1, 2048), (3, 700)])

@@ -22,7 +22,8 @@ def stalled_lib():
 
 
 @pytest.mark.parametrize("rows,H,K,split", [(1, 128, 1500, True), (1, 16, 1500, True),
-                                            (3, 128, 400, True), (200, 70, 300, False)])
+                                            (3, 128, 400, True), (200, 70, 300, False),
+                                            (400, 24, 300, False)])
 def test_a_stalled_stage_sets_the_timeout_flag(stalled_lib, rows, H, K, split):
     import torch
 
