@@ -42,10 +42,10 @@
 // pairs in row order, so that a row's shards share the query on chip and a
 // pair's start and end overlap its neighbours' tiles.  Few pairs are split over
 // clusters of CTAs.
-// Measured, 128 heads: 512 rows of 2048 tokens in 282 us (1.04 PFLOP/s of 16-bit
-// work, 0.55 of a measured bf16 GEMM); 64 rows, 4 shards of 520 tokens in 70 us;
-// 16 heads, 128 rows, 8 shards of 256 tokens in 46 us; a row of 2048 tokens in
-// 20.4 us.  Bound by the chain gather, scores, softmax, values over two stages,
+// Measured, 128 heads: 512 rows of 2048 tokens in 275 us (1.06 PFLOP/s of 16-bit
+// work, 0.57 of a measured bf16 GEMM); 64 rows, 4 shards of 520 tokens in 68 us;
+// 16 heads, 128 rows, 8 shards of 256 tokens in 45 us; a row of 2048 tokens in
+// 19.5 us.  Bound by the chain gather, scores, softmax, values over two stages,
 // about 4030 cycles a tile where the MMAs take 2840, and by a pair's end: 6
 // thousand cycles, 13 when a new row's query has to be split.
 // Every wait is bounded; one that runs out raises DSA_FLAG_TIMEOUT and stops
@@ -77,10 +77,12 @@ constexpr int kGroupHeads = kHeads / kGroups;
 constexpr int kGather0 = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + kGatherWarps;
 constexpr int kThreads = 768;                // six warpgroups; warps 22-23 only make up the last
 // Registers a thread of the softmax's four warpgroups, the gathering one and
-// the MMA's: 128 (4 x 88 + 64 + 64) = the 768 x 80 the CTA is launched with.
-constexpr int kRegsSoftmax = 88, kRegsGather = 64, kRegsMma = 64;
+// the MMA's: 128 (4 x 96 + 48 + 48) = the 768 x 80 the CTA is launched with.  A
+// few registers spilled in any role's loop cost 3 to 6 %, so the roles' loops are
+// kept within these.
+constexpr int kRegsSoftmax = 96, kRegsGather = 48, kRegsMma = 48;
 // With few heads: two warpgroups of the softmax, two that write outputs.
-constexpr int kWriter0 = 8, kRegsFew = 112, kRegsWriter = 64;
+constexpr int kWriter0 = 8, kRegsFew = 120, kRegsWriter = 72;
 static_assert(128 * (2 * kRegsFew + 2 * kRegsWriter + kRegsGather + kRegsMma) <= kThreads * 80, "registers");
 static_assert(128 * (4 * kRegsSoftmax + kRegsGather + kRegsMma) <= kThreads * 80, "registers");
 // Tensor-memory columns.
@@ -178,11 +180,12 @@ struct Cursor {
 // swizzle (bits 61-63: 2 = 128-byte, 4 = 64-byte).  K-major: the stride steps
 // between 8-row groups.  MN-major: the stride steps between groups of 8 along
 // K, the leading offset between swizzle atoms along M or N.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride,
-                                              uint32_t swizzle) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lead >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((stride >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) |
-         ((uint64_t)swizzle << 61);
+// In two words: the upper ones are constants.
+__device__ __forceinline__ uint32_t smem_desc(uint32_t addr, uint32_t lead) {
+  return ((addr >> 4) & 0x3FFFu) | (((lead >> 4) & 0x3FFFu) << 16);
+}
+constexpr uint32_t smem_desc_up(uint32_t stride, uint32_t swizzle) {
+  return ((stride >> 4) & 0x3FFFu) | (1u << 14) | (swizzle << 29);
 }
 
 // Instruction descriptor of kind::f8f6f4: D fp32 (bits 4-5 = 1), A's type
@@ -193,21 +196,23 @@ constexpr uint32_t idesc_f8(int m, int n, int a_type, int a_mn, int b_mn) {
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accum) {
+template <uint32_t kA, uint32_t kB, uint32_t kIdesc>
+__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t accum) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accum)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+      "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %6, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(accum), "n"(kA), "n"(kB), "r"(kIdesc)
       : "memory");
 }
 
-__device__ __forceinline__ void mma_f8_ws(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                          uint32_t accum) {
+template <uint32_t kA, uint32_t kB, uint32_t kIdesc>
+__device__ __forceinline__ void mma_f8_ws(uint32_t d, uint32_t a, uint32_t b, uint32_t accum) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.ws.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accum)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+      "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.ws.cta_group::1.kind::f8f6f4 [%0], x, y, %6, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(accum), "n"(kA), "n"(kB), "r"(kIdesc)
       : "memory");
 }
 
@@ -406,22 +411,13 @@ __device__ __forceinline__ void gather_tiles(const MlaFp8Args& a, Smem& sm, int 
   Cursor cur(a, sm, p0, p1);
   const int32_t* slots = a.slots + sm.first;
   int shard = 0;
-  int32_t slot[8];                           // of rows row0 + sub + 4 i, the next tile's
-  auto fetch = [&]() {
-    const int32_t* list = slots + list_of(a, cur.p, &shard) * a.K;
-    const int j0 = cur.t * kTile + row0 + sub;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) slot[i] = j0 + 4 * i < cur.count ? __ldg(list + j0 + 4 * i) : -1;
-  };
   int32_t mine = -1;                         // the slot of row0 + lane, the next tile's
   auto fetch_mine = [&]() {
+    const int32_t* list = slots + list_of(a, cur.p, &shard) * a.K;   // every lane's shard
     const int j = cur.t * kTile + row0 + lane;
-    mine = j < cur.count ? __ldg(slots + list_of(a, cur.p, &shard) * a.K + j) : -1;
+    mine = j < cur.count ? __ldg(list + j) : -1;
   };
-  if (cur.valid(p1)) {
-    fetch();
-    fetch_mine();
-  }
+  if (cur.valid(p1)) fetch_mine();
   // A part may be filled once the value products of its last tile are done.
   auto room = [&](uint64_t* empty, int k) {
     if (k >= 1) ok = wait_or_abort(sm, empty, (uint32_t)(k - 1) & 1u);
@@ -434,21 +430,15 @@ __device__ __forceinline__ void gather_tiles(const MlaFp8Args& a, Smem& sm, int 
     // read whole groups of 32 tokens; a group past the list is not read by any,
     // and its scores are masked: it is not filled.
     int32_t y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool in = slot[i] >= 0 && slot[i] < a.n_slots;
-      y[i] = in ? slot[i] : -1;
-    }
-    // The scale of row0 + lane's token, for the softmax.
     const bool in = mine >= 0 && mine < a.n_slots;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(kFull, in ? mine : -1, 4 * i + sub);
+    // The scale of row0 + lane's token, for the softmax.
     bad |= !in && lane < left;
     float ts = -1.f;
     if (in) ts = __ldg(a.scales + shard * a.n_blocks + fdiv((uint32_t)mine, a.fblock));
     cur.advance(a, sm, p0, p1);
-    if (cur.valid(p1)) {
-      fetch();
-      fetch_mine();
-    }
+    if (cur.valid(p1)) fetch_mine();
     const uint32_t kv = kv0 + (uint32_t)st * (kBlocks * kKvBlock);
     auto copy_pair = [&](int block) {        // blocks `block` and block + 1
 #pragma unroll
@@ -489,13 +479,14 @@ __device__ __forceinline__ void gather_tiles(const MlaFp8Args& a, Smem& sm, int 
 __device__ __forceinline__ bool issue_scores(const MlaFp8Args& a, Smem& sm, uint32_t tmem, int p0,
                                              int p1) {
   constexpr uint32_t kId = idesc_f8(kTile, 2 * kHeads, 0, 0, 0);
-  const uint64_t qd = smem_desc(smem_u32(sm.q[0]), 16, 1024, 2);
-  const uint64_t qrd = smem_desc(smem_u32(sm.qrope), 16, 512, 4);
+  constexpr uint32_t k128 = smem_desc_up(1024, 2), k64 = smem_desc_up(512, 4);
+  const uint32_t qd = smem_desc(smem_u32(sm.q[0]), 16), qrd = smem_desc(smem_u32(sm.qrope), 16);
   auto block = [&](uint32_t d, int st, int b) {
-    const uint64_t kd = smem_desc(smem_u32(sm.kv[st][b]), 16, 1024, 2);
+    const uint32_t kd = smem_desc(smem_u32(sm.kv[st][b]), 16);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      mma_f8(d, kd + k * 2, qd + (uint64_t)(b * (kQBlock >> 4) + k * 2), kId, b + k > 0 ? 1u : 0u);
+      mma_f8<k128, k128, kId>(d, kd + k * 2, qd + (uint32_t)(b * (kQBlock >> 4) + k * 2),
+                              b + k > 0 ? 1u : 0u);
   };
   Cursor cur(a, sm, p0, p1);
   int row = -1, run = -1;                    // the row at hand; rows begun
@@ -518,9 +509,9 @@ __device__ __forceinline__ bool issue_scores(const MlaFp8Args& a, Smem& sm, uint
     tc_fence_after();
     block(d, st, 2);
     block(d, st, 3);
-    const uint64_t rd = smem_desc(smem_u32(sm.rope[st]), 16, 512, 4);
+    const uint32_t rd = smem_desc(smem_u32(sm.rope[st]), 16);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) mma_f8(d, rd + k * 2, qrd + k * 2, kId, 1u);
+    for (int k = 0; k < 2; ++k) mma_f8<k64, k64, kId>(d, rd + k * 2, qrd + k * 2, 1u);
     mma_commit(&sm.sfull[st]);
     cur.advance(a, sm, p0, p1);
   }
@@ -530,14 +521,15 @@ __device__ __forceinline__ bool issue_scores(const MlaFp8Args& a, Smem& sm, uint
 __device__ __forceinline__ bool issue_values(const MlaFp8Args& a, Smem& sm, uint32_t tmem, int p0,
                                              int p1, bool handed) {
   constexpr uint32_t kIdHi = idesc_f8(kHeads, 256, 0, 1, 1), kIdLo = idesc_f8(kHeads, 256, 1, 1, 1);
-  const uint64_t lod = smem_desc(smem_u32(sm.plo), 16, 512, 4);
+  constexpr uint32_t kP = smem_desc_up(512, 4), kV = smem_desc_up(1024, 2);
+  const uint32_t lod = smem_desc(smem_u32(sm.plo), 16);
   Cursor cur(a, sm, p0, p1);
   int pair = -1;                             // pairs begun, less one
   for (int n = 0; cur.valid(p1); ++n) {
     // Groups of 32 tokens that the tile has; the two halves of the dimensions
     // one after the other, so that the first one's blocks free early.
     const int st = n & 1, steps = min(kTile / 32, (cur.count - cur.t * kTile + 31) / 32);
-    const uint64_t hid = smem_desc(smem_u32(sm.rope[st]), 16, 512, 4);
+    const uint32_t hid = smem_desc(smem_u32(sm.rope[st]), 16);
     if (!wait_or_abort(sm, &sm.pfull, (uint32_t)n & 1u)) return false;
     // Where others write a pair's outputs, they have read the last pair's O.
     if (handed && cur.t == 0 && ++pair > 0 &&
@@ -546,12 +538,12 @@ __device__ __forceinline__ bool issue_values(const MlaFp8Args& a, Smem& sm, uint
     tc_fence_after();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const uint64_t vd = smem_desc(smem_u32(sm.kv[st][2 * half]), kKvBlock, 1024, 2);
+      const uint32_t vd = smem_desc(smem_u32(sm.kv[st][2 * half]), kKvBlock);
       const uint32_t d = tmem + kOCol + half * 128;
       for (int k = 0; k < steps; ++k) {
-        const uint64_t v = vd + (uint64_t)(k * (4096 >> 4)), p = (uint64_t)(k * (2048 >> 4));
-        mma_f8_ws(d, lod + p, v, kIdLo, (cur.t > 0 || k > 0) ? 1u : 0u);
-        mma_f8_ws(d, hid + p, v, kIdHi, 1u);
+        const uint32_t v = vd + (uint32_t)(k * (4096 >> 4)), p = (uint32_t)(k * (2048 >> 4));
+        mma_f8_ws<kP, kV, kIdLo>(d, lod + p, v, (cur.t > 0 || k > 0) ? 1u : 0u);
+        mma_f8_ws<kP, kV, kIdHi>(d, hid + p, v, 1u);
       }
       mma_commit(half == 0 ? &sm.emptyA[st] : &sm.emptyB[st]);
     }
