@@ -21,6 +21,9 @@
  * dsa_slot_mapping (the write side of the paged cache: where each shard
  * stores the KV of new tokens) and dsa_sparse_mla_decode (each shard's sparse
  * attention over its compacted slots, whose outputs dsa_lse_combine merges).
+ * Beside them, for long contexts: dsa_rope_table and dsa_rotary_embed (rotary
+ * positions), dsa_kv_cache_insert_fp8 and dsa_sparse_mla_decode_fp8 (the cache
+ * in 8 bits with a scale for each block of slots, and the attention over it).
  *
  * Sharding (PR #46076 report, section 关键源码片段, comment in
  * `_dcp_localize_decode_seq_lens`): global token t lives on shard
