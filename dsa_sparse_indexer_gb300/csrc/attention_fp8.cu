@@ -666,7 +666,7 @@ __device__ __forceinline__ float transpose_max(const float2 (&v)[8]) {
 // need and take the same decisions from it.  O holds head h with dimensions
 // 0-127 of each 256 in lane h, with dimensions 128-255 in lane 64 + h.
 // The sums of a pair, in the weights' space: of each head 4 partial sums of the
-// weights, 4 of what rounding took from them, and the reference.
+// weights, 4 of what rounding took from the larger ones, and the reference.
 __device__ __forceinline__ float head_sum(const float* w, int h, float* off) {
   const float* y = w + h;
   *off = (y[4 * kHeads] + y[5 * kHeads]) + (y[6 * kHeads] + y[7 * kHeads]);
@@ -940,7 +940,11 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
           hi[k] = to_e4m3x2(pw);
           const __half2 rest = __hsub2(pw, of_e4m3x2(hi[k]));
           lo[k] = to_e5m2x2(rest);
-          const float2 lost = __half22float2(__hsub2(rest, of_e5m2x2(lo[k])));
+          // Only a relative loss (to 2^-7) is taken from the normaliser: below
+          // e4m3's normal range, 2^-6, a product may round away whole, however
+          // much of the normaliser its weight is where its scale is small.
+          const __half2 counts = __hge2(pw, __floats2half2_rn(0x1p-6f, 0x1p-6f));
+          const float2 lost = __half22float2(__hmul2(__hsub2(rest, of_e5m2x2(lo[k])), counts));
           gone[e] = ffma2(lost, make_float2(rts, rts), gone[e]);
         }
         phi[i] = hi[0] | (hi[1] << 16);

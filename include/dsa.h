@@ -525,9 +525,10 @@ dsa_status dsa_kv_cache_insert_fp8(const uint16_t* kv_rows, const uint16_t* kpe_
  *                selected row's block is neither 0 nor in [2^-100, 2^100]
  * Scores accumulate in fp32, from the query to 2^-18 of its head's largest
  * value (exactly, above 2^-10 of it); a softmax weight, times its token's
- * scale, enters the value product to 2^-7 of its size, or below 2^-9 of the
- * row's largest to 2^-16 of that one (2^-3 of its own size, if less): the
- * normaliser follows.
+ * scale, enters the value product to 2^-7 of its size, and the normaliser takes
+ * it as it was rounded; a product below 2^-9 of the row's largest enters to
+ * 2^-16 of that one (or an eighth of its own size and 2^-20 of that one, if
+ * less), and the normaliser has the weight itself.
  * A slot outside [0, n_slots) is left out and raises DSA_FLAG_BOUNDS; what
  * the cache holds there or elsewhere cannot reach the result.
  * Errors: rows < 0, K < 1, H < 1, n_slots < 1, block_tokens < 1, n_slots %
