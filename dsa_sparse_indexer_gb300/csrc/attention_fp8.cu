@@ -104,7 +104,7 @@ constexpr uint32_t kStalledArrivals = 1;
 constexpr uint32_t kStalledArrivals = 0;
 #endif
 // Scales for which neither the sums nor the weights leave fp32.
-constexpr float kMinScale = 0x1p-100f, kMaxScale = 0x1p100f;
+constexpr float kMinScale = 0x1p-100f, kMaxScale = 0x1p100f, kLog2MinScale = -100.f;
 
 struct alignas(1024) Smem {
   uint8_t kv[kStages][kBlocks][kKvBlock];    // 131072
@@ -673,6 +673,13 @@ __device__ __forceinline__ float head_sum(const float* w, int h, float* off) {
   return (y[0] + y[kHeads]) + (y[2 * kHeads] + y[3 * kHeads]);
 }
 
+// log2 of a head's sum of weights: the sum's own exponent meets the reference
+// first, so that a large one (all scales 0 or small) costs no bits.
+__device__ __forceinline__ float lse2_of(float ref, float sum) {
+  const int e = min(max((int)(__float_as_uint(sum) >> 23) - 127, -126), 126);
+  return (ref + (float)e) + log2f(sum * pow2(-e));
+}
+
 // Softmax warps with a head; the others leave, and what they would hold (scores,
 // weights and outputs of no head) stays as it is.
 __device__ __forceinline__ int active_warps(int nheads) {
@@ -775,7 +782,7 @@ __device__ __forceinline__ void write_handed(const MlaFp8Args& a, Smem& sm, uint
     int shard;
     const int64_t head0 = list_of(a, p, &shard) * a.H + hg * kHeads;
     if (warp == kWriter0 && lane < nheads && good)
-      a.lse2[head0 + lane] = sum == 0.f ? -INFINITY : ref + log2f(sum);
+      a.lse2[head0 + lane] = sum == 0.f ? -INFINITY : lse2_of(ref, sum);
     write_outputs(a, lanes, head0, nheads, (warp - kWriter0) >> 2, (kSoftmaxWarps - kWriter0) / 4,
                   sum == 0.f ? 0.f : 1.f / (sum - off), good);
     tc_fence_before();
@@ -846,7 +853,9 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
       wait(&sm.fullB[sb], (uint32_t)(n >> 1) & 1u);   // the token's scale is there
       const float held = sm.tok[sb][token], ts = fmaxf(held, 0.f);
       const bool in = held >= 0.f;
-      const float lt = ts > 0.f ? __log2f(ts) : 0.f;
+      // A token of scale 0 has no product whose precision the reference would
+      // serve: it only keeps its weight within fp32, as the least scale does.
+      const float lt = ts > 0.f ? __log2f(ts) : kLog2MinScale;
       wait(&sm.sfull[sb], (uint32_t)(n >> 1) & 1u);
       tc_fence_after();
       // Exponents of 16 heads relative to their references: the query's parts
@@ -1020,7 +1029,7 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
       const float sum = head_sum(w, h, &off);
       sm.part[0][h] = sum == 0.f ? 0.f : 1.f / (sum - off);
       if (h < nheads && good)
-        a.lse2[head0 + h] = sum == 0.f ? -INFINITY : w[8 * kHeads + h] + log2f(sum);
+        a.lse2[head0 + h] = sum == 0.f ? -INFINITY : lse2_of(w[8 * kHeads + h], sum);
     }
     barrier(1 + kGroups, active * 32);
     write_outputs(a, lanes, head0, nheads, grp, active / 4, sm.part[0][(quad & 1) * 32 + lane], good);
@@ -1123,7 +1132,7 @@ __device__ __forceinline__ void merge_parts(const MlaFp8Args& a, Smem& sm, uint3
     for (int c = 0; c < 8; ++c)
       if (c < (int)parts) factor[c * kHeads + h] = ref[c] * inv;
     if (rank == 0 && good)
-      a.lse2[head0 + h] = all == 0.f ? -INFINITY : top + log2f(all);
+      a.lse2[head0 + h] = all == 0.f ? -INFINITY : lse2_of(top, all);
   }
   good = !barrier_or(1 + kGroups, active * 32, !good);
   const int groups = kDv / 16 / (int)parts;  // of 16 dimensions; a thread takes 8 of a head

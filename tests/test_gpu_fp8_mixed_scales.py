@@ -104,3 +104,36 @@ def test_many_tokens_of_small_scale_beside_one_of_a_large_one(rows, H, mass, rat
     order = np.insert(order, 1000, 0)
     assert len(order) == K
     _compare(rows, H, q, codes, scales, block, order)
+
+
+@pytest.mark.parametrize("rows,H", FORMS)
+@pytest.mark.parametrize("size", [2.0 ** -7, 2.0 ** -10, 2.0 ** -40, 2.0 ** -90])
+@pytest.mark.parametrize("lead", [0, 10])
+def test_blocks_of_scale_zero_beside_others(rows, H, size, lead):
+    """Tokens in blocks of scale 0 (score 0, no value) beside tokens of ordinary
+    and small scales with scores about as high, or `lead` binades lower: the
+    others' weights keep their precision."""
+    rng = np.random.default_rng(lead + H)
+    n, block = 2048, 64
+    codes = _codes(rng, n)
+    scales = np.full(n // block, size)
+    scales[::3] = 0.0
+    codes[:, 512:] = 0
+    codes[:, 512] = KF.encode(rng.integers(56, 65, n).astype(np.float64))
+    q = np.zeros(576)
+    q[512] = -lead * np.log(2.0) / (SCALE * 64.0 * size)
+    q[0:512:64] = rng.standard_normal(8) / size / 60
+    _compare(rows, H, q, codes, scales, block, rng.permutation(n)[:1000])
+
+
+@pytest.mark.parametrize("rows,H", FORMS)
+def test_a_list_that_begins_or_ends_with_blocks_of_scale_zero(rows, H):
+    rng = np.random.default_rng(rows)
+    n, block = 1024, 64
+    codes, scales = _codes(rng, n), np.full(n // block, 2.0 ** -30)
+    scales[:5] = 0.0
+    q = rng.standard_normal(576) * 2.0 ** 30 / 60
+    first = rng.permutation(320)
+    for order in (np.concatenate([first, 320 + rng.permutation(500)]),
+                  np.concatenate([320 + rng.permutation(500), first])):
+        _compare(rows, H, q, codes, scales, block, order)
