@@ -103,7 +103,8 @@ constexpr uint32_t kStalledArrivals = 1;
 #else
 constexpr uint32_t kStalledArrivals = 0;
 #endif
-// Scales for which neither the sums nor the weights leave fp32.
+// Scales for which neither the sums nor the weights leave fp32: a weight is at
+// most 2^kGap over the scale, so a list's sum holds 2^18 tokens of the least.
 constexpr float kMinScale = 0x1p-100f, kMaxScale = 0x1p100f, kLog2MinScale = -100.f;
 
 struct alignas(1024) Smem {
@@ -914,7 +915,11 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
                                fmaxf(sm.part[2][col], sm.part[3][col]));
         const bool move = fresh ? mx > -INFINITY : mx > kGap;
         const float up = move ? mx - kTop : 0.f;
-        if (!fresh) alpha = fast_exp2(-up);
+        // The sums take the factor in two steps: before it they may be as far
+        // above 1 as it is below (with scales at both ends of their range).
+        float step = 1.f;
+        if (!fresh) step = fast_exp2(-0.5f * up);
+        alpha = step * step;
         const bool first_tile = fresh;
         fresh = fresh && !__any_sync(kFull, move);
         ref += up;
@@ -923,10 +928,10 @@ __device__ __forceinline__ void softmax_and_store(const MlaFp8Args& a, Smem& sm,
           const float2 d = make_float2(__shfl_sync(kFull, up, 2 * i), __shfl_sync(kFull, up, 2 * i + 1));
           x[i] = fadd2(x[i], make_float2(-d.x, -d.y));
           if (!first_tile) {
-            const float2 f = make_float2(__shfl_sync(kFull, alpha, 2 * i),
-                                         __shfl_sync(kFull, alpha, 2 * i + 1));
-            l[i] = fmul2(l[i], f);
-            gone[i] = fmul2(gone[i], f);
+            const float2 f = make_float2(__shfl_sync(kFull, step, 2 * i),
+                                         __shfl_sync(kFull, step, 2 * i + 1));
+            l[i] = fmul2(fmul2(l[i], f), f);
+            gone[i] = fmul2(fmul2(gone[i], f), f);
           }
         }
         // The maxima have been read before another tile's are written.
@@ -1123,9 +1128,11 @@ __device__ __forceinline__ void merge_parts(const MlaFp8Args& a, Smem& sm, uint3
       if (sum[c] != 0.f) top = fmaxf(top, ref[c]);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      ref[c] = sum[c] != 0.f ? fast_exp2(ref[c] - top) : 0.f;
-      all = fmaf(sum[c], ref[c], all);
-      less = fmaf(off[c], ref[c], less);
+      // (In two steps, as above.)
+      const float step = sum[c] != 0.f ? fast_exp2(0.5f * (ref[c] - top)) : 0.f;
+      all = fmaf(sum[c] * step, step, all);
+      less = fmaf(off[c] * step, step, less);
+      ref[c] = step * step;
     }
     const float inv = all == 0.f ? 0.f : 1.f / (all - less);
 #pragma unroll

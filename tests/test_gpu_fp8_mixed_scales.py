@@ -137,3 +137,17 @@ def test_a_list_that_begins_or_ends_with_blocks_of_scale_zero(rows, H):
     for order in (np.concatenate([first, 320 + rng.permutation(500)]),
                   np.concatenate([320 + rng.permutation(500), first])):
         _compare(rows, H, q, codes, scales, block, order)
+
+
+@pytest.mark.parametrize("rows,H", FORMS)
+@pytest.mark.parametrize("least,most", [(2.0 ** -100, 2.0 ** 100), (2.0 ** -70, 2.0 ** 70), (2.0 ** -100, 2.0 ** 30)])
+@pytest.mark.parametrize("rising", [True, False])
+def test_the_least_and_the_largest_scale_in_one_list(rows, H, least, most, rising):
+    """Tiles (and a split pair's parts) of the least scales, then of the
+    largest, with equal scores: every token counts in the normaliser."""
+    rng = np.random.default_rng(rows + H)
+    n, block = 1024, 64
+    codes = _codes(rng, n)
+    scales = np.full(n // block, least)
+    scales[n // block // 2:] = most
+    _compare(rows, H, np.zeros(576), codes, scales, block, np.arange(n) if rising else np.arange(n)[::-1].copy())
