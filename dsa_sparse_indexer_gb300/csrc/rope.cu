@@ -194,25 +194,20 @@ __global__ void __launch_bounds__(V * sizeof(E) == 16 ? 256 : kMaxWidth / 2) rot
           s[j + i] = sv.e[i] * a.sign;
         }
       }
-    } else {                                 // identity for this token
-      if (u == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);
 #pragma unroll
-      for (int j = 0; j < kPairs; ++j) {
-        c[j] = 1.f;
-        s[j] = 0.f;
-      }
+      for (int k = 0; k < kRows; ++k)
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          E& ea = kVecs == 2 ? v[k][0].e[j] : v[k][0].e[2 * j];
+          E& eb = kVecs == 2 ? v[k][kVecs - 1].e[j] : v[k][0].e[(2 * j + 1) % V];
+          float fa = to_float(ea), fb = to_float(eb);
+          turn(fa, fb, c[j], s[j]);
+          ea = from_float<E>(fa);
+          eb = from_float<E>(fb);
+        }
+    } else if (u == 0) {                     // carried: its bits as they are
+      raise_flag(a.flags, DSA_FLAG_BOUNDS);
     }
-#pragma unroll
-    for (int k = 0; k < kRows; ++k)
-#pragma unroll
-      for (int j = 0; j < kPairs; ++j) {
-        E& ea = kVecs == 2 ? v[k][0].e[j] : v[k][0].e[2 * j];
-        E& eb = kVecs == 2 ? v[k][kVecs - 1].e[j] : v[k][0].e[(2 * j + 1) % V];
-        float fa = to_float(ea), fb = to_float(eb);
-        turn(fa, fb, c[j], s[j]);
-        ea = from_float<E>(fa);
-        eb = from_float<E>(fb);
-      }
   }
   E* dst = static_cast<E*>(a.out) + tok * a.out_token + head * a.out_head + at0;
 #pragma unroll

@@ -460,7 +460,7 @@ dsa_status dsa_rope_table(int max_pos, int rot_dim, double base, int scaling, do
  *              values are not touched); otherwise they must not overlap.
  *   positions  [T] int32; cos_sin_cache [max_pos][rot_dim] fp32
  *   err_flags  DSA_FLAG_BOUNDS if a position is outside [0, max_pos) (that
- *              token is carried unturned).
+ *              token is carried unturned, bit for bit).
  * Errors: negative sizes or strides, D < 1, max_pos < 1, rot_dim odd or < 2,
  *         the turning part outside [0, D), an unknown dtype or layout, null
  *         or misaligned pointers, output rows on one another, out == x with
