@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -218,6 +219,26 @@ __global__ void __launch_bounds__(V * sizeof(E) == 16 ? 256 : kMaxWidth / 2) rot
   }
 }
 
+// No two of the T x H output rows of D elements lie on one another.
+bool rows_apart(int T, int64_t token, int H, int64_t head, int D) {
+  if ((T > 1 && token < D) || (H > 1 && head < D)) return false;
+  if (T == 1 || H == 1) return true;
+  const int64_t near = std::min(token, head), far = std::max(token, head);
+  const int64_t n = token < head ? T : H, m = token < head ? H : T;   // rows `near` and `far` apart
+  if ((far - D) / near >= n - 1) return true;   // one dimension's rows within a step of the other
+  // Row i of the far ones lies `rest` behind row j of the near ones.  j >= i, so
+  // that this takes fewer steps than either dimension has rows.
+  int64_t j = 0, rest = 0;
+  for (int64_t i = 1; i < m; ++i) {
+    j += far / near;
+    rest += far % near;
+    if (rest >= near) rest -= near, ++j;
+    if (j >= n) break;
+    if (rest < D || (near - rest < D && j + 1 < n)) return false;
+  }
+  return true;
+}
+
 template <typename E, int LAYOUT, int V>
 cudaError_t launch_rotary(RotArgs& a, bool in_place, cudaStream_t stream) {
   constexpr int kVecs = LAYOUT == kHalf || V == 1 ? 2 : 1;
@@ -357,8 +378,7 @@ extern "C" dsa_status dsa_rotary_embed(const void* x, int64_t x_token, int64_t x
   if (D > kMaxWidth || (int64_t)T * H > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   if (T == 0 || H == 0) return DSA_OK;
   if (!x || !out || !positions || !cos_sin_cache) return DSA_ERR_INVALID_ARG;
-  // Rows of the output may not land on one another.
-  if ((T > 1 && out_token == 0) || (H > 1 && out_head == 0)) return DSA_ERR_INVALID_ARG;
+  if (!rows_apart(T, out_token, H, out_head, D)) return DSA_ERR_INVALID_ARG;
   const uintptr_t es = dtype == DSA_FP32 ? 3u : 1u;
   if ((reinterpret_cast<uintptr_t>(x) & es) || (reinterpret_cast<uintptr_t>(out) & es) ||
       (reinterpret_cast<uintptr_t>(cos_sin_cache) & 3u))

@@ -455,7 +455,7 @@ dsa_status dsa_rope_table(int max_pos, int rot_dim, double base, int scaling, do
  *   gradient of the rotation).  fp32 arithmetic, one rounding at the store.
  *
  *   x, out     [T][H][D] of dtype, values contiguous, token and head strides in
- *              elements (x's may be 0, out's only for a single token or head).
+ *              elements (x's may be 0; out's rows must lie apart).
  *              out == x with the same strides turns in place (the carried
  *              values are not touched); otherwise they must not overlap.
  *   positions  [T] int32; cos_sin_cache [max_pos][rot_dim] fp32
