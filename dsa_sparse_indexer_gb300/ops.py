@@ -428,7 +428,10 @@ def rotary_embed(x, positions, cos_sin_cache, layout: str = "interleaved", first
 
     layout "interleaved" pairs neighbours, "half" pairs value i with value
     i + rot_dim / 2.  inverse turns back (the rotation's gradient).  out may be
-    x itself (in place), else it must not overlap it."""
+    x itself (in place), else it must not overlap it.  Autograd does not see
+    the call: a tensor that requires grad is refused while gradients are
+    recorded (turn its gradient back with inverse=True), and an out that was
+    saved for a backward pass counts as modified in place."""
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {list(ROPE_LAYOUTS)}, got {layout!r}")
     dtype = x.dtype if isinstance(x, torch.Tensor) else None
@@ -447,11 +450,16 @@ def rotary_embed(x, positions, cos_sin_cache, layout: str = "interleaved", first
     out_token, out_head = _rows_of(out, "out", dtype)
     if out.shape != x.shape:
         raise ValueError("out must have x's shape")
+    if torch.is_grad_enabled() and (x.requires_grad or out.requires_grad):
+        raise ValueError("x and out must not require grad: rotary_embed is not recorded by "
+                         "autograd (call it under torch.no_grad(), with inverse=True on the "
+                         "gradient in the backward pass)")
     context = _together(x, positions, cos_sin_cache, out, err_flags)
     _launch(context, "dsa_rotary_embed", _ptr(x), x_token, x_head, _ptr(positions),
             _ptr(cos_sin_cache), cos_sin_cache.shape[0], cos_sin_cache.shape[1], first, T, H, D,
             ROPE_DTYPES[dtype], ROPE_LAYOUTS[layout], int(bool(inverse)), _ptr(out), out_token,
             out_head, _ptr(err_flags), _raw_stream(x))
+    torch.autograd.graph.increment_version(out)
     return out
 
 
