@@ -478,7 +478,9 @@ def kv_cache_insert_fp8(kv_rows, kpe_rows, slot_mapping, kv_cache, block_scales,
 
     A block whose scale is 0 holds nothing: zero the scales of blocks handed to
     a new sequence.  Scales only grow otherwise, and the rows already in a
-    block move with them.  work: [n_slots + n_blocks] int32 for calls of more
+    block move with them, so no other call may use the blocks that this one
+    writes to while it runs (an attention on another stream, a second insert:
+    not even for other slots of theirs).  work: [n_slots + n_blocks] int32 for calls of more
     than 512 tokens (allocated when not given)."""
     _need(kv_rows, "kv_rows", torch.bfloat16, 2)
     _need(kpe_rows, "kpe_rows", torch.bfloat16, 2)

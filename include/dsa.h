@@ -487,6 +487,11 @@ dsa_status dsa_rotary_embed(const void* x, int64_t x_token, int64_t x_head,
  * becomes the format's NaN).  A scale of 0 (or less, or NaN) means that the
  * block holds nothing yet: zero the scales of blocks handed to a new sequence.
  * A row of a slot that several tokens name is the last one's.
+ * Unlike dsa_kv_cache_insert, which writes its own slots alone, a call rewrites
+ * every row and the scale of each block that it touches: an attention over such
+ * a block, or another insert into it, must not run at the same time, even for
+ * other slots.  Order them by stream or event; calls whose blocks are all
+ * different (other pages, another shard's cache) may overlap.
  *
  *   kv_rows [T][DSA_MLA_DV] bf16, kpe_rows [T][64] bf16: 16-byte aligned
  *   slot_mapping [T] int32; a slot < 0 writes nothing
