@@ -40,7 +40,8 @@ def sources() -> list[str]:
 
 
 def _deps() -> list[str]:
-    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")]
+    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
+                         if f.endswith((".cuh", ".h"))]
     files.append(os.path.join(INCLUDE, "dsa.h"))
     files.append(os.path.abspath(__file__))
     return files

@@ -9,6 +9,7 @@
 #include <cmath>
 
 #include "common.cuh"
+#include "rope_steps.h"
 
 namespace dsa {
 namespace {
@@ -23,8 +24,10 @@ struct alignas(sizeof(E) * V) Vec {
 // Entry (p, i) is the angle p w_i.  A far position's angle loses its fraction
 // of a turn in fp32, and fp64 arithmetic is slow here, so the angle is an
 // integer: w_i / 2 pi as a 64-bit fraction of a turn (rounded once, on the
-// host), p times that modulo 2^64, the whole turns falling off the top.  Its
-// upper 32 bits are the angle to 2^-32 turns, whatever p: the nearest quarter turn
+// host: rope_steps.h), p times that modulo 2^64, the whole turns falling off the
+// top.  Its upper 32 bits are the angle cut to 2^-32 turns, whatever p (an
+// absolute error: the first sines of a slow pair, below 2^-28, have few bits):
+// the nearest quarter turn
 // in whole, and within an eighth of a turn of it a fraction whose sine and
 // cosine are their power series (to x^9 and x^10: the next terms are below 2e-9
 // there).  A thread keeps its pair i and steps its phase by
@@ -34,6 +37,9 @@ struct alignas(sizeof(E) * V) Vec {
 // with sincospif, whose own reduction is not needed here); 62 values, 8.0.  4096
 // positions of 128 take 2.0 us, a launch's latency.
 constexpr int kMaxPairs = 128;
+static_assert((int)DSA_ROPE_NONE == RopeScaling::kNone && (int)DSA_ROPE_LINEAR == RopeScaling::kLinear &&
+                  (int)DSA_ROPE_NTK == RopeScaling::kNtk && (int)DSA_ROPE_YARN == RopeScaling::kYarn,
+              "the scalings' numbers");
 constexpr int kTableThreads = 256;
 
 struct TableArgs {
@@ -324,28 +330,9 @@ extern "C" dsa_status dsa_rope_table(int max_pos, int rot_dim, double base, int 
   if (rot_dim > 2 * kMaxPairs) return DSA_ERR_UNSUPPORTED;
   if (max_pos == 0) return DSA_OK;
   if (!table || (reinterpret_cast<uintptr_t>(table) & 3u)) return DSA_ERR_INVALID_ARG;
-  const double pi = 3.14159265358979323846, d = rot_dim;
-  const double b = scaling == DSA_ROPE_NTK && rot_dim > 2 ? base * std::pow(factor, d / (d - 2.0))
-                                                          : base;
-  // The pair whose wavelength turns `r` times within the trained context.
-  auto pair_of = [&](double r) {
-    return d * std::log(orig_max_pos / (2.0 * pi * r)) / (2.0 * std::log(base));
-  };
-  double low = 0.0, high = 0.0;
-  if (scaling == DSA_ROPE_YARN) {
-    low = std::fmax(std::floor(pair_of(beta_fast)), 0.0);
-    high = std::fmin(std::ceil(pair_of(beta_slow)), d - 1.0);
-  }
   TableArgs a{};
-  for (int i = 0; i < rot_dim / 2; ++i) {
-    double w = std::pow(b, -2.0 * i / d);
-    if (scaling == DSA_ROPE_LINEAR) w /= factor;
-    if (scaling == DSA_ROPE_YARN) {
-      const double ramp = std::fmin(std::fmax((i - low) / std::fmax(high - low, 0.001), 0.0), 1.0);
-      w = w * (1.0 - ramp) + w / factor * ramp;
-    }
-    a.step[i] = (uint64_t)(w / (2.0 * pi) * 0x1p64 + 0.5);
-  }
+  rope_steps(rot_dim, base,
+             {static_cast<RopeScaling::Kind>(scaling), factor, orig_max_pos, beta_fast, beta_slow}, a.step);
   a.table = table;
   a.amplitude = amplitude;
   a.max_pos = max_pos;

@@ -433,8 +433,10 @@ dsa_status dsa_kv_cache_insert(const uint16_t* kv_rows, const uint16_t* kpe_rows
  *                    that turn beta_fast and beta_slow times in orig_max_pos
  *                    positions (floor and ceil of rot_dim ln(orig_max_pos /
  *                    (2 pi beta)) / (2 ln base), kept in [0, rot_dim - 1])
- * Each angle is reduced exactly (modulo a turn, in 64-bit integers), so far
- * positions are as exact as near ones.
+ * Angles are 64-bit fractions of a turn (each w_i's rounded once, to 2^-65
+ * turns) cut to 2^-32 turns, so that far positions are as exact as near ones; the
+ * bound is on the values' absolute error, 4e-7 of the amplitude, so that sines
+ * of about 1e-8 (a slow pair's first positions) have few exact bits.
  * Errors: max_pos < 0, rot_dim odd or < 2, base <= 1, factor < 1, values not
  *         finite, an unknown scaling, YARN with orig_max_pos < 1, beta_slow <= 0
  *         or beta_fast < beta_slow, null or misaligned table -> INVALID_ARG;
