@@ -1281,6 +1281,25 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_decode_fp8_kernel(cons
   }
 }
 
+// Clusters of `parts` CTAs of the split kernel that the device runs at the same
+// time; 0 if that cannot be told.
+int clusters_at_once(unsigned parts, size_t smem) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(parts);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = parts;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  const auto e = cudaOccupancyMaxActiveClusters(&n, sparse_mla_decode_fp8_kernel<true, false>, &cfg);
+  return e == cudaSuccess ? n : 0;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
@@ -1288,9 +1307,13 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 using namespace dsa;
 
-// Few pairs are split, each over a cluster of as many CTAs (at most 8) as keep
-// the SMs busy with four tiles or more a CTA before the last doubling: two
-// tiles cost about what the merge does.
+// Few pairs are split, each over a cluster of at most as many CTAs (up to 8) as
+// the SMs hold, with four tiles or more a CTA before the last doubling: two
+// tiles cost about what the merge does.  A launch takes fewer where that many
+// clusters do not run at once (a cluster lies within a group of SMs, and not
+// every group is a multiple of it: 15 of 8, 36 of 4 and 76 of 2 do), as the ones
+// left over would be a second round: 9 rows of 128 heads and 2048 tokens took
+// 37.6 us over 8, 24.6 over 4; 19 rows 46.8 over 4, 34.7 over 2.
 static int split_parts(int64_t pairs, int64_t hgroups, int K) {
   const int tiles = (K + kTile - 1) / kTile;
   int parts = 1;
@@ -1327,8 +1350,13 @@ extern "C" dsa_status dsa_sparse_mla_decode_fp8(const uint16_t* q, const uint8_t
   if (pairs > INT32_MAX || hgroups > INT32_MAX / kSms) return DSA_ERR_UNSUPPORTED;
   // One CTA an SM: as many groups of pairs as all SMs hold with each head group.
   const int64_t groups = std::min<int64_t>(pairs, std::max<int64_t>(1, kSms / hgroups));
-  const unsigned parts = work ? (unsigned)split_parts(pairs, hgroups, K) : 1u;
+  unsigned parts = work ? (unsigned)split_parts(pairs, hgroups, K) : 1u;
   const int smem = (int)sizeof(Smem);
+  if (parts > 1 &&
+      cudaFuncSetAttribute(sparse_mla_decode_fp8_kernel<true, false>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  while (parts > 1 && pairs * hgroups > clusters_at_once(parts, (size_t)smem)) parts /= 2;   // (0.3 us each)
   const auto kernel =
       parts > 1       ? sparse_mla_decode_fp8_kernel<true, false>
       : H <= kHanded ? sparse_mla_decode_fp8_kernel<false, true>

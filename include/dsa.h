@@ -552,7 +552,7 @@ dsa_status dsa_sparse_mla_decode_fp8(const uint16_t* q, const uint8_t* kv_cache,
                                      float scale, uint16_t* out, float* lse2,
                                      float* work, uint32_t* err_flags, cudaStream_t stream);
 
-/* Bytes of the workspace that dsa_sparse_mla_decode_fp8 uses for these sizes (0: none). */
+/* Bytes of the workspace that dsa_sparse_mla_decode_fp8 may use for these sizes (0: none). */
 int64_t dsa_sparse_mla_decode_fp8_work(int rows, int S, int H, int K);
 
 /*
