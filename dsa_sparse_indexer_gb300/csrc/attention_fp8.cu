@@ -9,10 +9,11 @@
 // is widened in shared memory.  What multiplies them is held in two 8-bit
 // floats instead: the query (bf16, 8 significant bits) as e4m3 + e4m3 after a
 // power of two per head that brings its largest value to [2^7, 2^8), exact but
-// for values below 2^-10 of that one; a weight as e4m3 plus what that leaves as
-// e5m2 (to 2^-7 of it; below 2^-9 of the largest to 2^-16 of that one).  Two
-// products with 8-bit operands cost what one with 16-bit ones does.  The scale
-// of a token's block multiplies its scores, and its weight before that is split.
+// for values below 2^-9 of that one; a weight, times its token's scale, as e4m3
+// plus what that leaves as e5m2 (to 2^-7; below 2^-9 of the largest to 2^-16 of
+// that one).  Two products with 8-bit operands cost what one with 16-bit ones
+// does.  The scale of a token's block multiplies its scores, and its weight
+// before that is split.
 //
 // A CTA takes 64 heads of one (row, shard), tiles of 128 tokens:
 //  * S^T[token][head]: A = the tile (M = 128 tokens, K-major), B = the query

@@ -486,7 +486,8 @@ dsa_status dsa_rotary_embed(const void* x, int64_t x_token, int64_t x_head,
  *   its other rows, if 0 < scale < scale':  code = e4m3(code * (scale / scale'))
  *   its new rows:  code = e4m3(value / scale')
  * with round to nearest even, saturating at +-448 (an infinity too; a NaN
- * becomes the format's NaN).  A scale of 0 (or less, or NaN) means that the
+ * becomes the format's NaN; where scale' is 0, every finite value being 0, the
+ * division is by 1, and infinities stand for 0).  A scale of 0 (or less, or NaN) means that the
  * block holds nothing yet: zero the scales of blocks handed to a new sequence.
  * A row of a slot that several tokens name is the last one's.
  * Unlike dsa_kv_cache_insert, which writes its own slots alone, a call rewrites
@@ -530,8 +531,8 @@ dsa_status dsa_kv_cache_insert_fp8(const uint16_t* kv_rows, const uint16_t* kpe_
  *                same time need their own.
  *   err_flags    as dsa_sparse_mla_decode; DSA_FLAG_BOUNDS also if the scale of a
  *                selected row's block is neither 0 nor in [2^-100, 2^100]
- * Scores accumulate in fp32, from the query to 2^-18 of its head's largest
- * value (exactly, above 2^-10 of it); a softmax weight, times its token's
+ * Scores accumulate in fp32, from the query to 2^-17 of its head's largest
+ * value (exactly, from 2^-9 of it on); a softmax weight, times its token's
  * scale, enters the value product to 2^-7 of its size, and the normaliser takes
  * it as it was rounded; a product below 2^-9 of the row's largest enters to
  * 2^-16 of that one (or an eighth of its own size and 2^-20 of that one, if

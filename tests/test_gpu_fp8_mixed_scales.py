@@ -151,3 +151,16 @@ def test_the_least_and_the_largest_scale_in_one_list(rows, H, least, most, risin
     scales = np.full(n // block, least)
     scales[n // block // 2:] = most
     _compare(rows, H, np.zeros(576), codes, scales, block, np.arange(n) if rising else np.arange(n)[::-1].copy())
+
+
+@pytest.mark.parametrize("rows,H", FORMS)
+def test_query_values_between_the_steps_of_their_second_part(rows, H):
+    """Every value halfway between two steps of its 8-bit parts, beside a
+    largest one of exactly 2^7: the scores' full bound, all on one side."""
+    rng = np.random.default_rng(H)
+    n, block = 512, 64
+    codes = KF.encode(np.abs(rng.standard_normal((n, 576))) * 60)
+    codes[:, 0] = 0
+    q = np.full(576, 0.125 * (1 + 1 / 128))
+    q[0] = 128.0
+    _compare(rows, H, q, codes, np.full(n // block, 2.0 ** -7), block, rng.permutation(n)[:500])
