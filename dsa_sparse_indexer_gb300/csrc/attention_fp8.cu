@@ -43,12 +43,14 @@
 // pairs in row order, so that a row's shards share the query on chip and a
 // pair's start and end overlap its neighbours' tiles.  Few pairs are split over
 // clusters of CTAs.
-// Measured, 128 heads: 512 rows of 2048 tokens in 275 us (1.06 PFLOP/s of 16-bit
-// work, 0.57 of a measured bf16 GEMM); 64 rows, 4 shards of 520 tokens in 68 us;
-// 16 heads, 128 rows, 8 shards of 256 tokens in 45 us; a row of 2048 tokens in
-// 19.5 us.  Bound by the chain gather, scores, softmax, values over two stages,
-// about 4030 cycles a tile where the MMAs take 2840, and by a pair's end: 6
-// thousand cycles, 13 when a new row's query has to be split.
+// Measured, 128 heads: 512 rows of 2048 tokens in 325 us (0.90 PFLOP/s of 16-bit
+// work, 0.48 of a measured bf16 GEMM), 275 with one scale for all blocks, where
+// fewer references move after a list's first tile; 64 rows, 4 shards of 400 to
+// 640 tokens 75 (69); 16 heads, 128 rows, 8 shards of 200 to 312 tokens 53 (52); a
+// row of 2048 tokens 19.2 (18.0).  Bound by the chain gather, scores, softmax,
+// values over two stages, about 4030 cycles a tile where the MMAs take 2840 and no
+// reference moves, and by a pair's end: 6 thousand cycles, 13 when a new row's
+// query has to be split.
 // Every wait is bounded; one that runs out raises DSA_FLAG_TIMEOUT and stops
 // the CTA's roles, which drain their copies and MMAs in flight.
 #include <cuda_bf16.h>
@@ -745,8 +747,8 @@ __device__ __forceinline__ void write_outputs(const MlaFp8Args& a, uint32_t lane
 
 // With up to 32 heads (kFew), half of the softmax's warps or more have none:
 // two warpgroups write the outputs, while the softmax goes on with the next
-// pair, with more registers a thread (16 heads, pairs of two to three tiles:
-// 49.5 -> 46.4 us; 32 heads 53.2 -> 48.7; in longer pairs the same).  A pair's
+// pair, with more registers a thread (one scale for all blocks, 256 tokens a pair,
+// 16 heads: 49.5 -> 46.4 us; 32 heads 53.2 -> 48.7; in longer pairs the same).  A pair's
 // sums reach the writers in those parts of the weights' space that belong to no
 // head, alternately in two: the softmax cannot end a pair before the outputs of
 // the one before the last are written, as its first value product waits for

@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 2) insert_many_kernel(const __grid_c
 // list.  For calls of at least a quarter of the cache's slots, whose untouched
 // blocks are few, and eight tokens a block (or about as many blocks as CTAs fit
 // at a time).  32768 tokens, a tenth left out, into 65536 slots of blocks of
-// 64 (56 MB): in a prompt's order 11.7 us (4.8 TB/s), by the tokens' CTAs
+// 64 (56 MB; replays, in L2): in a prompt's order 11.7 us, by the tokens' CTAs
 // above 14.5; in any order 16.3 and 55.  At the
 // lower bound a prompt's order loses a little (16384 into 65536 of blocks of 64
 // 10.2 us, above 9.4) for what any order gains.  Past the bounds it loses: 8192

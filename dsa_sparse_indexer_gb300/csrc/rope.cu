@@ -27,15 +27,14 @@ struct alignas(sizeof(E) * V) Vec {
 // host: rope_steps.h), p times that modulo 2^64, the whole turns falling off the
 // top.  Its upper 32 bits are the angle cut to 2^-32 turns, whatever p (an
 // absolute error: the first sines of a slow pair, below 2^-28, have few bits):
-// the nearest quarter turn
-// in whole, and within an eighth of a turn of it a fraction whose sine and
-// cosine are their power series (to x^9 and x^10: the next terms are below 2e-9
-// there).  A thread keeps its pair i and steps its phase by
+// the nearest quarter turn in whole, and within an eighth of a turn of it a
+// fraction whose sine and cosine are their power series (to x^9 and x^10: the next
+// terms are below 2e-9 there).  A thread keeps its pair i and steps its phase by
 // whole positions (one 64-bit addition each); four pairs where 16-byte stores
 // fit.  Bound by its stores, with the arithmetic close behind: 131072 positions
-// of 64 values (33.5 MB) take 6.4 us, 5.3 TB/s (a pair a thread 7.7, and 8.4
-// with sincospif, whose own reduction is not needed here); 62 values, 8.0.  4096
-// positions of 128 take 2.0 us, a launch's latency.
+// of 64 values (33.5 MB, in replays into L2) take 6.4 us (a pair a thread 7.7, and
+// 8.4 with sincospif, whose own reduction is not needed here); 62 values, 8.0.
+// 4096 positions of 128 take 2.0 us, a launch's latency.
 constexpr int kMaxPairs = 128;
 static_assert((int)DSA_ROPE_NONE == RopeScaling::kNone && (int)DSA_ROPE_LINEAR == RopeScaling::kLinear &&
                   (int)DSA_ROPE_NTK == RopeScaling::kNtk && (int)DSA_ROPE_YARN == RopeScaling::kYarn,
@@ -107,11 +106,10 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_
 // consecutive heads of a token, all loads in flight at once.  Rows that no
 // 16-byte vectors fit (odd widths, offsets) take vectors of two elements or one.
 // Measured: 4096 tokens of 128 heads of 64 (67 MB in, 67 MB out, strided) in
-// 37 us with every row's token, address and table read found anew, 27.5 so (25
-// in back-to-back replays, 5.3 TB/s); a plain copy of as much takes 23.  64
-// tokens take 2.0 us, a launch's latency.  8192 tokens of 32 heads of 130 (136
-// MB) take 28 us, at odd offsets 36 to 41 for 125 values; a head and an element
-// a thread, 134 and 81.
+// 37 us with every row's token, address and table read found anew, 27.3 so (24.5
+// in replays, 5.5 TB/s); a plain copy of as much takes 23.  64 tokens take 2.0
+// us, a launch's latency.  8192 tokens of 32 heads of 130 (136 MB) take 28 us, at
+// odd offsets 36 to 41 for 125 values; a head and an element a thread, 134 and 81.
 
 enum { kInterleaved = DSA_ROPE_INTERLEAVED, kHalf = DSA_ROPE_HALF };
 constexpr int kMaxWidth = 1024;               // values of a row
