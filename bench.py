@@ -92,7 +92,11 @@ KERNEL_SOURCES = {"shard_topk_pack": ("shard_topk.cu", "fast_select.cuh", "local
                   "sparse_mla_decode": ("attention.cu",),
                   "indexer_logits": ("indexer_logits.cu",),
                   "fused_norm_rope": ("pcp_prefill.cu",),
-                  "kv_cache_insert": ("pcp_prefill.cu",)}
+                  "kv_cache_insert": ("pcp_prefill.cu",),
+                  "rope_table": ("rope.cu", "rope_steps.h"),
+                  "rotary_embed": ("rope.cu",),
+                  "fp8_cache_insert": ("kv_fp8.cu",),
+                  "fp8_mla_decode": ("attention_fp8.cu",)}
 
 
 # ---------------------------------------------------------------------------
