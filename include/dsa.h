@@ -538,7 +538,8 @@ dsa_status dsa_kv_cache_insert_fp8(const uint16_t* kv_rows, const uint16_t* kpe_
  * 2^-16 of that one (or an eighth of its own size and 2^-20 of that one, if
  * less), and the normaliser has the weight itself.  A token whose block has
  * scale 0 has score 0 and adds to the normaliser alone; as the largest product
- * it counts like a token of scale 2^-100.
+ * it counts like a token of scale 2^-100.  Exponents are fp32 sums of a score
+ * and its scale's logarithm: near 2^100 or 2^-100 lse2 is rounded to 2^-17.
  * A slot outside [0, n_slots) is left out and raises DSA_FLAG_BOUNDS; what
  * the cache holds there or elsewhere cannot reach the result.
  * Errors: rows < 0, K < 1, H < 1, n_slots < 1, block_tokens < 1, n_slots %
