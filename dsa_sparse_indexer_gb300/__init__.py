@@ -10,8 +10,9 @@ include/dsa.h (libdsa.so); this package only marshals torch tensors to it.
 """
 from . import _lib
 from .ops import (SUPPORTED_K, convert_index_compact, fused_norm_rope, indexer_fused,
-                  indexer_logits, kv_cache_insert, kv_cache_insert_fp8, lse_combine,
-                  merge_topk_stable, new_error_flags, pack_candidates, rope_table, rotary_embed,
+                  indexer_key_insert, indexer_logits, indexer_query_fp8, kv_cache_insert,
+                  kv_cache_insert_fp8, lse_combine, merge_topk_stable, mla_decode, mla_prefill,
+                  new_error_flags, pack_candidates, rope_table, rotary_embed,
                   shard_topk, shard_topk_pack, slot_mapping, sparse_mla_decode,
                   sparse_mla_decode_fp8)
 from ._lib import DSAError, DSA_FLAG_BOUNDS, DSA_FLAG_TIMEOUT
@@ -20,6 +21,7 @@ __all__ = ["shard_topk", "pack_candidates", "shard_topk_pack", "merge_topk_stabl
            "convert_index_compact", "indexer_fused", "lse_combine", "slot_mapping",
            "sparse_mla_decode", "indexer_logits", "fused_norm_rope", "kv_cache_insert",
            "rope_table", "rotary_embed", "kv_cache_insert_fp8", "sparse_mla_decode_fp8",
+           "mla_prefill", "mla_decode", "indexer_key_insert", "indexer_query_fp8",
            "new_error_flags", "DSAError",
            "DSA_FLAG_BOUNDS", "DSA_FLAG_TIMEOUT", "SUPPORTED_K", "library"]
 

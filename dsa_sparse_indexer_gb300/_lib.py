@@ -46,6 +46,16 @@ SIGNATURES = {
     "dsa_sparse_mla_decode_fp8": ([_p, _p, _p, _i64, _i, _p, _p, _i, _i, _i, _i, ctypes.c_float,
                                    _p, _p, _p, _p, _p], _i),
     "dsa_sparse_mla_decode_fp8_work": ([_i, _i, _i, _i], _i64),
+    "dsa_mla_prefill": ([_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, _i64, _p, _p, _i, _i,
+                         _i, _i, _i, ctypes.c_float, _i, _p, _p, _p, _p, _p], _i),
+    "dsa_mla_prefill_work": ([_i, _i, _i, _i], _i64),
+    "dsa_mla_decode": ([_p, _p, _i64, _p, _i, _i, _i, _p, _p, _p, _i, _i, _i, _i, _i,
+                        ctypes.c_float, _p, _p, _p, _p, _p], _i),
+    "dsa_mla_decode_work": ([_i, _i, _i, _i, _i, _i], _i64),
+    "dsa_indexer_key_insert": ([_p, _i64, _p, _p, ctypes.c_float, _p, _p, _i, _i, _i, _i, _p, _i,
+                                _i, _p, _i64, _p, _p], _i),
+    "dsa_indexer_query_fp8": ([_p, _i64, _i64, _p, ctypes.c_float, _p, _p, _i, _i, _i, _i, _i, _i,
+                               _p, _p, _p, _p], _i),
     "dsa_indexer_steps_noalloc": ([_p, _i64, _i, _i, _i, _i, _p, _p, _p, _i, _i, _i, _p, _p, _p,
                                    _p, _p, _p], _i),
 }

@@ -1,0 +1,774 @@
+// Latent attention in its absorbed form over each shard's whole paged cache,
+// for one token, a chain or a tree of drafted tokens a request (sm_103a).
+//
+// Request q's n rows (tokens) are the last n of the seq_lens[q] tokens in its
+// cache.  Per shard s, row r, head h, over the tokens j of shard s that the row
+// sees: x_j = scale * (q[r][h] . row_j), out = sum_j 2^(x_j log2 e) v_j / sum_j
+// 2^(x_j log2 e), v_j the first 512 entries of row_j, lse2 = log2 sum_j exp(x_j).
+// A row sees every token before the request's n, and of these the ones that its
+// tree mask names, or (no mask) those up to itself.
+//
+// All heads and rows of a request share its keys, so that (row, head) pairs are
+// the rows of one product: blocks of CG * 128 of them, CG CTAs with 128 each
+// (CG = 2: a pair of CTAs issues one product of M = 256 and either holds half of
+// the keys' tile, which halves what a CTA copies).  Outputs of 512 values would
+// fill tensor memory (512 columns): an item takes half of them, and its scores
+// are computed for both halves, 2304 + 1024 cycles of products a tile of 128 keys
+// where 2176 are the least (65 %).
+//  * tensor memory: half an output (256 columns), two score tiles (128 each; the
+//    weights as bf16 pairs in the first half of the same columns);
+//  * shared memory: the block's queries (144 KB) and a ring of 80 KB in blocks of
+//    16 KB / CG: a key tile's nine 64-value column blocks, the values' four
+//    blocks of 32 keys, in the order in which the products take them: keys of
+//    tile j + 2 behind values of tile j, also across items;
+//  * a warp copies (tensor maps, a box per page or 64 keys), one thread (of the
+//    pair's first CTA) issues, four warps run the softmax, a thread a row.
+// The keys may be split into parts that a second kernel joins.
+// The tail of a sequence's last page holds anything: its values are zeroed in
+// shared memory up to the 16 keys that a product step reads, its scores masked.
+// Every wait is bounded and raises DSA_FLAG_TIMEOUT when it runs out.
+#include <algorithm>
+
+#include "split_merge.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kDqk = DSA_MLA_DQK, kDv = DSA_MLA_DV, kHalf = kDv / 2;
+constexpr int kRows = 128;                   // (row, head) pairs of a CTA
+constexpr int kTileK = 128;
+constexpr int kQBlocks = kDqk / 64, kQBlock = kRows * 128, kQBox = 32;
+constexpr int kKBlocks = kDqk / 64, kVBlocks = 4, kVKeys = kTileK / kVBlocks;
+constexpr int kRingBytes = 81920;
+constexpr int kInfo = 8;
+constexpr int kMmaWarp = 4, kLoadWarp = 5, kThreads = 192;
+constexpr int kTmemCols = 512, kOCol = 0;
+__device__ __forceinline__ constexpr uint32_t s_col(uint32_t b) { return 256 + b * 128; }
+#ifdef DSA_TEST_STALLED_COPY
+// The test-only build (never libdsa.so): the ring's first barrier expects one
+// arrival that nothing makes (its copy still lands).
+constexpr uint32_t kStalledArrivals = 1;
+#else
+constexpr uint32_t kStalledArrivals = 0;
+#endif
+
+template <int CG>
+struct Shape {
+  static constexpr int kBlock = 16384 / CG;            // bytes of a ring block
+  static constexpr int kRing = kRingBytes / kBlock;    // 5 or 10
+  static constexpr int kKeys = kTileK / CG;            // keys of a tile that a CTA holds
+  static constexpr int kAtoms = kHalf / CG / 64;       // 64-value columns of its values
+  static constexpr int kAtom = kVKeys * 128;           // bytes of one in a value block
+};
+
+struct alignas(1024) DecodeSmem {
+  uint8_t q[kQBlocks][kQBlock];
+  uint8_t ring[kRingBytes];
+  uint64_t full[10], empty[10], qfull, qempty, sfull[2], pfull[2], pvdone, vtail[2], info[kInfo], drain;
+  uint32_t tail_seq[2];       // ring block of the values that vtail counts
+  uint32_t pages[kInfo];      // valid pages of stream tile j, at j % kInfo: a bit per 16 keys
+  uint32_t tmem;
+  int blocks;                 // row blocks of all requests
+  int abort;
+};
+
+struct DecodeArgs {
+  const int32_t* block_table; // [S][reqs][max_blocks]
+  const int32_t *starts, *lens;
+  const int32_t* mask;        // [rows][words] or null
+  __nv_bfloat16* out;         // [S][rows][H][kDv]
+  float* lse2;                // [S][rows][H]
+  float *part_o, *part_l;     // [splits][S][rows][H][kDv], [splits][S][rows][H]
+  uint32_t* flags;
+  int64_t n_slots;
+  int reqs, max_blocks, block, rows, H, words, splits;
+  int cap;                    // local tokens that a table row names
+  int kbox, vbox;             // keys of a copy
+  float c2;                   // scale * log2(e)
+  ShardMath sm;
+  FastDiv fblock, fH;
+};
+
+struct Item {
+  int req, shard, half, split;
+  int tok0, n;                // the request's rows
+  int row0, rows;             // (row, head) pairs of the block: first of the request, how many
+  int base;                   // tokens before the request's n (may be negative)
+  int nall, nvis, nfree;      // local tokens: in the cache, seen by some row, by every row
+  int t0, t1;                 // key tiles
+  bool bad;                   // a length below zero or past the table
+};
+struct Cursor {
+  int req = 0, before = 0;
+};
+
+__device__ __forceinline__ void rows_of(const DecodeArgs& a, int i, int& first, int& end) {
+  first = min(max(__ldg(a.starts + i), 0), a.rows);
+  end = min(max(__ldg(a.starts + i + 1), first), a.rows);
+}
+
+// Warp-wide: item `index` of blocks * 2 * S * splits: halves and row blocks of a
+// request, which read the same keys, beside one another.
+template <int CG>
+__device__ __forceinline__ Item find_item(const DecodeArgs& a, int blocks, int64_t index, Cursor& c) {
+  const int lane = threadIdx.x & 31;
+  Item it;
+  it.half = (int)(index & 1);
+  const int64_t x = index >> 1;
+  const int y = (int)(x / blocks), qb = (int)(x - (int64_t)y * blocks);
+  it.shard = y / a.splits;
+  it.split = y - it.shard * a.splits;
+  if (qb < c.before) c = Cursor{};
+  int local = 0;
+  for (int at = c.req;; at += 32) {
+    const int i = at + lane;
+    int first = 0, end = 0;
+    if (i < a.reqs) rows_of(a, i, first, end);
+    const int mine = ((end - first) * a.H + CG * kRows - 1) / (CG * kRows);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned past = __ballot_sync(kFull, c.before + incl > qb);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      c.before += __shfl_sync(kFull, incl - mine, l);
+      c.req = at + l;
+      local = qb - c.before;
+      break;
+    }
+    c.before += __shfl_sync(kFull, incl, 31);
+    if (at + 32 >= a.reqs) break;            // not reached: qb < blocks
+  }
+  it.req = c.req;
+  int end;
+  rows_of(a, it.req, it.tok0, end);
+  it.n = end - it.tok0;
+  it.row0 = local * CG * kRows;
+  it.rows = min(CG * kRows, it.n * a.H - it.row0);
+  const int len = max(__ldg(a.lens + it.req), 0);
+  it.base = len - it.n;
+  const int lo = (int)fdiv((uint32_t)it.row0, a.fH);
+  const int hi = (int)fdiv((uint32_t)(it.row0 + it.rows - 1), a.fH);
+  auto local_of = [&](int t) { return min((int)a.sm.local_len((uint32_t)max(t, 0), it.shard), a.cap); };
+  it.bad = __ldg(a.lens + it.req) < 0 || (int)a.sm.local_len((uint32_t)len, it.shard) > a.cap;
+  it.nall = local_of(len);
+  it.nvis = a.mask ? it.nall : local_of(it.base + hi + 1);
+  it.nfree = local_of(a.mask ? it.base : it.base + lo + 1);
+  const int nt = (it.nvis + kTileK - 1) / kTileK, per = (nt + a.splits - 1) / a.splits;
+  it.t0 = min(it.split * per, nt);
+  it.t1 = min(it.t0 + per, nt);
+  return it;
+}
+
+// Steps of 16 keys of tile t's value product, and whether it reads keys behind
+// the sequence's end (zeroed in shared memory by the softmax warps).
+__device__ __forceinline__ int value_steps(const Item& it, int t) {
+  return (min(it.nvis - t * kTileK, kTileK) + 15) / 16;
+}
+__device__ __forceinline__ bool has_tail(const Item& it, int t) {
+  return it.nall - t * kTileK < 16 * value_steps(it, t);
+}
+
+__device__ __forceinline__ uint32_t pair_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The address of the same object in the pair's first CTA.
+__device__ __forceinline__ uint32_t leader_addr(const void* p) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+// A box into this CTA's memory, its bytes counted by `bar` (a shared::cluster address).
+template <int CG>
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                         uint32_t bar) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// ---- the copies ---------------------------------------------------------------
+struct PendingV {              // values of a stream tile whose keys are copied
+  int y, half, shard;          // lane i: row of the cache of its keys 16 i
+  bool tail;
+};
+
+template <int CG>
+__device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem& sm,
+                                           const CUtensorMap* tm_q, const CUtensorMap* tm_k,
+                                           const CUtensorMap* tm_v, int blocks, int64_t items,
+                                           uint32_t rank) {
+  using Sh = Shape<CG>;
+  const int lane = threadIdx.x & 31;
+  const bool leader = rank == 0;
+  Cursor cur;
+  uint32_t seq = 0, j = 0, loads = 0, tails = 0;
+  bool ok = true, bad = false;
+  // Waits for a ring block's space; its barrier then expects the pair's bytes
+  // (or, values with a tail, an arrival alone: they are counted elsewhere).
+  auto open_block = [&](bool bytes) {
+    const uint32_t slot = seq % Sh::kRing, use = seq / Sh::kRing;
+    if (use > 0) ok = __all_sync(kFull, wait_or_abort(&sm.abort, &sm.empty[slot], (use - 1) & 1u));
+    if (ok && leader && lane == 0) {
+      if (bytes) mbar_expect_tx(&sm.full[slot], (uint32_t)(CG * Sh::kBlock));
+      else mbar_arrive1(&sm.full[slot]);
+    }
+    return ok;
+  };
+  auto load_values = [&](const PendingV& p) {
+    uint64_t* vtail = &sm.vtail[tails & 1u];
+    if (p.tail && lane == 0) {
+      sm.tail_seq[tails & 1u] = seq;         // published by the barrier
+      mbar_expect_tx(vtail, (uint32_t)(kVBlocks * Sh::kBlock));
+    }
+    tails += p.tail;
+    for (int b = 0; b < kVBlocks; ++b, ++seq) {
+      if (!open_block(!p.tail)) return;
+      const uint32_t slot = seq % Sh::kRing;
+      uint8_t* dst = sm.ring + slot * Sh::kBlock;
+      const uint32_t bar = p.tail ? smem_u32(vtail)
+                                  : (CG == 1 ? smem_u32(&sm.full[slot]) : leader_addr(&sm.full[slot]));
+      for (int k = 0; k < kVKeys; k += a.vbox) {
+        const int y = __shfl_sync(kFull, p.y, (b * kVKeys + k) >> 4);
+        if (lane < Sh::kAtoms)
+          load_box<CG>(dst + lane * Sh::kAtom + k * 128, tm_v,
+                       p.half * kHalf + ((int)rank * Sh::kAtoms + lane) * 64, y, p.shard, bar);
+      }
+    }
+  };
+  PendingV p0{}, p1{};
+  for (int64_t i = blockIdx.x / CG; ok && i < items; i += gridDim.x / CG) {
+    const Item it = find_item<CG>(a, blocks, i, cur);
+    bad |= it.bad;
+    const int32_t* table = a.block_table + ((int64_t)it.shard * a.reqs + it.req) * a.max_blocks;
+    for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
+      // Where this tile's keys are: lane l (of 8) has its keys 16 l to 16 l + 15.
+      const int key = t * kTileK + (lane & 7) * 16;
+      int y = (int)a.n_slots;                // outside: reads as zero
+      bool in = false;
+      if (key < it.nall) {
+        uint32_t off;
+        const uint32_t col = fdivmod((uint32_t)key, a.fblock, &off);
+        const int64_t at = (int64_t)__ldg(table + col) * a.block + off;
+        in = at >= 0 && at + 16 <= a.n_slots;
+        if (in) y = (int)at;
+        bad |= !in;
+      }
+      const unsigned valid = __ballot_sync(kFull, in) & 0xffu;
+      if (j >= 2) load_values(p0);
+      if (!ok) break;
+      if (t == it.t1 - 1) {                  // the item's queries
+        if (loads > 0) ok = __all_sync(kFull, wait_or_abort(&sm.abort, &sm.qempty, (loads - 1) & 1u));
+        if (!ok) break;
+        ++loads;
+        auto boxes = [&](int r) { return (min(max(it.rows - r * kRows, 0), kRows) + kQBox - 1) / kQBox; };
+        const int mine = boxes((int)rank);
+        if (leader && lane == 0)
+          mbar_expect_tx(&sm.qfull, (uint32_t)((boxes(0) + (CG == 2 ? boxes(1) : 0)) * kQBlocks * kQBox * 128));
+        const uint32_t bar = CG == 1 ? smem_u32(&sm.qfull) : leader_addr(&sm.qfull);
+        if (lane < kQBlocks)
+          for (int b = 0; b < mine; ++b)
+            load_box<CG>(sm.q[lane] + b * kQBox * 128, tm_q, lane * 64,
+                         it.tok0 * a.H + it.row0 + (int)rank * kRows + b * kQBox, 0, bar);
+      }
+      if (lane == 0) {
+        sm.pages[j % kInfo] = valid;
+        mbar_arrive1(&sm.info[j % kInfo]);
+      }
+      for (int b = 0; b < kKBlocks; ++b, ++seq) {
+        if (!open_block(true)) break;
+        const uint32_t slot = seq % Sh::kRing;
+        const uint32_t bar = CG == 1 ? smem_u32(&sm.full[slot]) : leader_addr(&sm.full[slot]);
+        const int boxes = Sh::kKeys / a.kbox, first = (int)rank * Sh::kKeys;
+        const int yk = __shfl_sync(kFull, y, ((first + (lane < boxes ? lane : 0) * a.kbox) >> 4) & 7);
+        if (lane < boxes)
+          load_box<CG>(sm.ring + slot * Sh::kBlock + lane * a.kbox * 128, tm_k, b * 64, yk, it.shard, bar);
+      }
+      p0 = p1;
+      p1 = PendingV{y, it.half, it.shard, has_tail(it, t)};
+    }
+  }
+  if (ok && j >= 2) load_values(p0);
+  if (ok && j >= 1) load_values(p1);
+  if (__any_sync(kFull, bad) && lane == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);
+  if (!ok && lane == 0) {
+    if (!cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
+    // The copies issued land before the CTA ends (a pair's first CTA counts both's).
+    if (leader) {
+      if (loads > 0) mbar_wait(&sm.qfull, (loads - 1) & 1u);
+      for (uint32_t b = seq > Sh::kRing ? seq - Sh::kRing : 0; b < seq; ++b)
+        mbar_wait(&sm.full[b % Sh::kRing], (b / Sh::kRing) & 1u);
+    }
+    for (uint32_t k = tails > 2 ? tails - 2 : 0; k < tails; ++k)
+      mbar_wait(&sm.vtail[k & 1u], (k >> 1) & 1u);
+  }
+  __syncwarp();
+}
+
+// ---- the products: one thread of the (first) CTA -------------------------------
+template <int CG>
+__device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem& sm, uint32_t tmem,
+                                               int blocks, int64_t items) {
+  using Sh = Shape<CG>;
+  constexpr uint32_t kIdS = idesc_f16(CG * kRows, kTileK, true, false);
+  constexpr uint32_t kIdO = idesc_f16(CG * kRows, kHalf, true, true);
+  const int lane = threadIdx.x & 31;
+  const uint32_t ring0 = smem_u32(sm.ring);
+  Cursor cur;
+  uint32_t seq = 0, j = 0, nq = 0;
+  bool ok = true;
+  auto landed = [&]() {
+    ok = wait_or_abort(&sm.abort, &sm.full[seq % Sh::kRing], (seq / Sh::kRing) & 1u);
+    tc_fence_after();
+    return ok;
+  };
+  // Values of stream tile v: `steps` of 16 keys, the item's first or not.
+  auto values = [&](uint32_t v, int steps, bool first) {
+    ok = CG == 1 ? wait_or_abort(&sm.abort, &sm.pfull[v & 1u], (v >> 1) & 1u)
+                 : wait_or_abort_pair(&sm.abort, &sm.pfull[v & 1u], (v >> 1) & 1u);
+    for (int b = 0; ok && b < kVBlocks; ++b, ++seq) {
+      if (!landed()) return;
+      const uint32_t blk = ring0 + (seq % Sh::kRing) * Sh::kBlock;
+      for (int s = 2 * b; s < min(steps, 2 * b + 2); ++s)
+        mma_ts<CG>(tmem + kOCol, tmem + s_col(v & 1u) + s * 8,
+                   smem_desc_sw128(blk + (s & 1) * 2048, Sh::kAtom, 1024), kIdO,
+                   (first && s == 0) ? 0u : 1u);
+      tc_commit<CG>(&sm.empty[seq % Sh::kRing]);
+    }
+    if (ok) tc_commit<CG>(&sm.pvdone);
+  };
+  int steps0 = 0, steps1 = 0;
+  bool first0 = false, first1 = false;
+  for (int64_t i = blockIdx.x / CG; i < items; i += gridDim.x / CG) {
+    const Item it = find_item<CG>(a, blocks, i, cur);
+    if (lane == 0 && ok) {
+      for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
+        if (j >= 2) values(j - 2, steps0, first0);
+        if (!ok) break;
+        if (t == it.t1 - 1) {
+          ok = wait_or_abort(&sm.abort, &sm.qfull, nq & 1u);
+          ++nq;
+        }
+        for (int b = 0; ok && b < kKBlocks; ++b, ++seq) {
+          if (!landed()) break;
+          const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[b]), 16, 1024);
+          const uint64_t kd = smem_desc_sw128(ring0 + (seq % Sh::kRing) * Sh::kBlock, 16, 1024);
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            mma_ss<CG>(tmem + s_col(j & 1u), qd + s * 2, kd + s * 2, kIdS, (b > 0 || s > 0) ? 1u : 0u);
+          tc_commit<CG>(&sm.empty[seq % Sh::kRing]);
+        }
+        if (!ok) break;
+        tc_commit<CG>(&sm.sfull[j & 1u]);
+        if (t == it.t0) tc_commit<CG>(&sm.qempty);
+        steps0 = steps1;
+        first0 = first1;
+        steps1 = value_steps(it, t);
+        first1 = t == it.t1 - 1;
+      }
+    }
+    ok = __shfl_sync(kFull, (int)ok, 0) != 0;
+    if (!ok) break;
+  }
+  if (lane == 0) {
+    if (ok && j >= 2) values(j - 2, steps0, first0);
+    if (ok && j >= 1) values(j - 1, steps1, first1);
+    if (!ok && !cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
+    // Every product issued completes before the tensor memory is freed.
+    tc_commit<CG>(&sm.drain);
+    if (!mbar_wait(&sm.drain, 0)) cta_abort(&sm.abort, a.flags);
+  }
+  __syncwarp();
+}
+
+// Which of the 32 keys from local token `from` on row `tok` (of the request's) sees.
+__device__ __forceinline__ uint32_t seen32(const DecodeArgs& a, const Item& it, int tok, int from) {
+  uint32_t seen = 0;
+  int at = -1;
+  uint32_t word = 0;
+#pragma unroll 1
+  for (int k = 0; k < 32; ++k) {
+    const int l = from + k;
+    if (l >= it.nvis) break;
+    bool see = l < it.nfree;
+    if (!see) {
+      const int i = (int)a.sm.global_id(it.shard, (uint32_t)l) - it.base;   // the request's row
+      if (!a.mask) {
+        see = i <= tok;
+      } else if (i < 0) {
+        see = true;
+      } else if ((i >> 5) < a.words) {
+        if ((i >> 5) != at) {
+          at = i >> 5;
+          word = (uint32_t)__ldg(a.mask + (int64_t)(it.tok0 + tok) * a.words + at);
+        }
+        see = (word >> (i & 31)) & 1u;
+      }
+    }
+    seen |= (uint32_t)see << k;
+  }
+  return seen;
+}
+
+// ---- softmax and outputs --------------------------------------------------------
+template <int CG>
+__device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem& sm, uint32_t tmem,
+                                              int blocks, int64_t items, uint32_t rank) {
+  using Sh = Shape<CG>;
+  const int lane = threadIdx.x & 31, quad = threadIdx.x >> 5;
+  const int r = quad * 32 + lane;
+  const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
+  // A negative scale takes the scores' negatives, 0 their products with it, so
+  // that a masked score is -inf under every scale.
+  const float sign = a.c2 < 0.f ? -1.f : 0.f, c2 = a.c2 == 0.f ? 1.f : fabsf(a.c2);
+  Cursor cur;
+  uint32_t j = 0, tails = 0;                 // tiles and tails so far
+  bool ok = true;
+  for (int64_t i = blockIdx.x / CG; i < items; i += gridDim.x / CG) {
+    const Item it = find_item<CG>(a, blocks, i, cur);
+    const int row = it.row0 + (int)rank * kRows + r;   // of the request's n * H
+    const bool active = (int)rank * kRows + r < it.rows;
+    const int tok = active ? (int)fdiv((uint32_t)row, a.fH) : 0;
+    float m = -INFINITY, l = 0.f;
+    for (int t = it.t1 - 1; t >= it.t0; --t, ++j) {
+      const uint32_t b = j & 1u;
+      ok = wait_or_abort(&sm.abort, &sm.sfull[b], (j >> 1) & 1u) &&
+           wait_or_abort(&sm.abort, &sm.info[j % kInfo], (j / kInfo) & 1u);
+      if (!__all_sync(kFull, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t x[kTileK];
+      tmem_load(trow + s_col(b), x);
+      const uint32_t pages = *reinterpret_cast<volatile uint32_t*>(&sm.pages[j % kInfo]);
+      tmem_wait_ld(x);
+      if (a.c2 <= 0.f) {
+#pragma unroll
+        for (int k = 0; k < kTileK; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * sign);
+      }
+      if (pages != 0xffu || (t + 1) * kTileK > it.nfree) {
+        uint32_t seen[kTileK / 32];
+#pragma unroll
+        for (int c = 0; c < kTileK / 32; ++c) {
+          const uint32_t pg = (pages >> (2 * c)) & 3u;
+          seen[c] = seen32(a, it, tok, t * kTileK + c * 32) &
+                    ((pg & 1u ? 0xffffu : 0u) | (pg & 2u ? 0xffff0000u : 0u));
+        }
+#pragma unroll
+        for (int k = 0; k < kTileK; ++k)
+          if (!((seen[k / 32] >> (k & 31)) & 1u)) x[k] = 0xff800000u;
+      }
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < kTileK; k += 8)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          m4[v] = fmaxf(fmaxf(m4[v], __uint_as_float(x[k + 2 * v])), __uint_as_float(x[k + 2 * v + 1]));
+      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
+      const float mn = mx > m + kRescaleGap ? mx : m;   // m = -inf takes any finite maximum
+      const float alpha = m == -INFINITY ? 1.f : fast_exp2(m - mn);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      m = mn;
+      const float2 c2v = make_float2(c2, c2), nref = make_float2(-ref, -ref);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int c = 0; c < kTileK; c += 32) {
+        uint32_t p[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float2 e = ffma2(make_float2(__uint_as_float(x[c + 2 * k]),
+                                             __uint_as_float(x[c + 2 * k + 1])), c2v, nref);
+          const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
+          p[k] = pack16<true>(e0, e1);
+          sum[k & 1] = fadd2(sum[k & 1], make_float2(e0, e1));
+        }
+        tmem_store(trow + s_col(b) + (uint32_t)(c / 2), p);
+      }
+      l = l * alpha + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
+      if (t < it.t1 - 1) {                   // the previous tile's values are in: O is at rest
+        ok = wait_or_abort(&sm.abort, &sm.pvdone, (j - 1) & 1u);
+        if (!__all_sync(kFull, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (__any_sync(kFull, alpha != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < kHalf; c += 32) {
+            uint32_t o[32];
+            tmem_load(trow + (uint32_t)(kOCol + c), o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_store(trow + (uint32_t)(kOCol + c), o);
+          }
+        }
+      }
+      if (has_tail(it, t)) {                 // values behind the sequence's end: zeros
+        ok = wait_or_abort(&sm.abort, &sm.vtail[tails & 1u], (tails >> 1) & 1u);
+        if (!__all_sync(kFull, ok)) {
+          ok = false;
+          break;
+        }
+        const uint32_t seq = *reinterpret_cast<volatile uint32_t*>(&sm.tail_seq[tails & 1u]);
+        ++tails;
+        const int past = it.nall - t * kTileK, to = 16 * value_steps(it, t);
+        for (int z = r; z < (to - past) * Sh::kAtoms * 8; z += kRows) {
+          const int key = past + z / (Sh::kAtoms * 8), chunk = z % (Sh::kAtoms * 8);
+          uint8_t* blk = sm.ring + ((seq + (uint32_t)(key / kVKeys)) % Sh::kRing) * Sh::kBlock;
+          *reinterpret_cast<uint4*>(blk + (chunk >> 3) * Sh::kAtom + (key % kVKeys) * 128 + (chunk & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();                  // before this warp hands its weights over
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 1) mbar_arrive1(&sm.pfull[b]);
+        else
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                           leader_addr(&sm.pfull[b]))
+                       : "memory");
+      }
+    }
+    const bool some = it.t1 > it.t0;
+    if (ok && some) ok = wait_or_abort(&sm.abort, &sm.pvdone, (j - 1) & 1u);
+    if (!__all_sync(kFull, ok)) {
+      ok = false;
+      break;
+    }
+    if (some) tc_fence_after();
+    const int64_t all = (int64_t)a.rows * a.H;
+    const int64_t to = it.shard * all + (int64_t)it.tok0 * a.H + row;   // [S][rows][H]
+    const int64_t part = (int64_t)it.split * a.sm.S * all + to;
+    if (active && it.half == 0) {
+      const float lse = l == 0.f ? -INFINITY : m + log2f(l);
+      if (a.splits > 1) a.part_l[part] = lse;
+      else a.lse2[to] = lse;
+    }
+    if (!some && a.splits > 1) continue;     // the merge does not read this part
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+    for (int c = 0; c < kHalf; c += 32) {
+      uint32_t o[32];
+      if (some) {
+        tmem_load(trow + (uint32_t)(kOCol + c), o);
+        tmem_wait_ld(o);
+      }
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        o[k] = some && l != 0.f ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
+      if (active && a.splits > 1) {
+        uint4* dst = reinterpret_cast<uint4*>(a.part_o + part * kDv + it.half * kHalf + c);
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+          dst[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+      } else if (active) {
+        uint4* dst = reinterpret_cast<uint4*>(a.out + to * kDv + it.half * kHalf + c);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = pack16<true>(__uint_as_float(o[8 * v + 2 * k]), __uint_as_float(o[8 * v + 2 * k + 1]));
+          dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      __syncwarp();                          // the next columns' load takes the whole warp
+    }
+  }
+  if (!ok && lane == 0 && !cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
+}
+
+template <int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a) {
+  extern __shared__ unsigned char decode_smem_raw[];
+  DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>(
+      (reinterpret_cast<uintptr_t>(decode_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const uint32_t rank = CG == 2 ? pair_rank() : 0u;
+  if (warp == kMmaWarp) {
+    tmem_alloc<CG>(&sm.tmem, kTmemCols);
+  } else if (warp == kLoadWarp) {
+    // Row blocks of all requests; bad bounds are flagged once a call.
+    int blocks = 0;
+    bool bad = false;
+    for (int i = tid & 31; i < a.reqs; i += 32) {
+      int first, end;
+      rows_of(a, i, first, end);
+      bad |= first != a.starts[i] || end != a.starts[i + 1];
+      blocks += ((end - first) * a.H + CG * kRows - 1) / (CG * kRows);
+    }
+    blocks = __reduce_add_sync(kFull, blocks);
+    if (bad && blockIdx.x == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);
+    if ((tid & 31) == 0) sm.blocks = blocks;
+  } else if (tid == 0) {
+    for (int b = 0; b < Shape<CG>::kRing; ++b) {
+      mbar_init(&sm.full[b], 1 + (b == 0 ? kStalledArrivals : 0));
+      mbar_init(&sm.empty[b], 1);
+    }
+    mbar_init(&sm.qfull, 1);
+    mbar_init(&sm.qempty, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.sfull[b], 1);
+      mbar_init(&sm.pfull[b], 4 * CG);       // a warp each, of both CTAs in a pair's first
+      mbar_init(&sm.vtail[b], 1);
+    }
+    for (int b = 0; b < kInfo; ++b) mbar_init(&sm.info[b], 1);
+    mbar_init(&sm.pvdone, 1);
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    mbar_init_fence();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) {                   // the other CTA's barriers are there
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  const int blocks = sm.blocks;
+  const int64_t items = (int64_t)blocks * 2 * a.sm.S * a.splits;
+  if (warp == kLoadWarp) load_tiles<CG>(a, sm, &tm_q, &tm_k, &tm_v, blocks, items, rank);
+  else if (warp < kMmaWarp) softmax_tiles<CG>(a, sm, tmem, blocks, items, rank);
+  else if (rank == 0) issue_products<CG>(a, sm, tmem, blocks, items);
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) {                   // neither CTA's memory goes while the other uses it
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_free<CG>(tmem, kTmemCols);
+  }
+}
+
+constexpr int kSmem = (int)sizeof(DecodeSmem) + 1024;
+
+// How a call is cut: CTAs that share a product, parts of the keys.
+struct Plan {
+  int cg, splits;
+};
+Plan plan_for(int rows, int S, int H, int reqs, int64_t cap) {
+  const int64_t pairs = ((int64_t)rows * H + reqs - 1) / reqs;   // of a request, about
+  Plan p;
+  p.cg = pairs > kRows ? 2 : 1;
+  const int64_t items = (pairs + p.cg * kRows - 1) / (p.cg * kRows) * reqs * 2 * S;
+  const int64_t tiles = (cap + kTileK - 1) / kTileK;
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(device_sms() / p.cg / items, tiles / 2), 64));
+  return p;
+}
+
+template <int CG>
+cudaError_t launch_decode(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                          const DecodeArgs& a, int64_t items, cudaStream_t stream) {
+  const auto kernel = mla_decode_kernel<CG>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  int at_once = device_sms() / CG;
+  if (CG == 2) {                             // pairs that run at once: SM groups may be odd
+    constexpr int kDevices = 64;
+    static int pairs[kDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kDevices) {
+      if (pairs[dev] == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(at_once * CG));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = CG;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        pairs[dev] = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0 ? n : at_once;
+      }
+      at_once = std::min(at_once, pairs[dev]);
+    }
+  }
+  const unsigned grid = (unsigned)(std::min<int64_t>(items, at_once) * CG);
+  return launch_kernel(kernel, dim3(grid), dim3(kThreads), (size_t)kSmem, stream, CG == 2 ? 2u : 0u,
+                       q, k, v, a);
+}
+
+}  // namespace
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" int64_t dsa_mla_decode_work(int rows, int S, int H, int reqs, int max_blocks,
+                                       int block_size) {
+  if (rows < 1 || S < 1 || H < 1 || reqs < 1 || max_blocks < 1 || block_size < 1) return 0;
+  const int parts = plan_for(rows, S, H, reqs, (int64_t)max_blocks * block_size).splits;
+  return parts == 1 ? 0 : (int64_t)parts * S * rows * H * (kDv + 1) * 4;
+}
+
+extern "C" dsa_status dsa_mla_decode(const uint16_t* q, const uint16_t* kv_cache, int64_t n_slots,
+                                     const int32_t* block_table, int reqs, int max_blocks,
+                                     int block_size, const int32_t* query_starts,
+                                     const int32_t* seq_lens, const int32_t* tree_mask,
+                                     int mask_words, int rows, int S, int I, int H, float scale,
+                                     uint16_t* out, float* lse2, float* work, uint32_t* err_flags,
+                                     cudaStream_t stream) {
+  if (rows < 0 || reqs < 0 || H < 1 || max_blocks < 1 || block_size < 1 || n_slots < 1 ||
+      (tree_mask && mask_words < 1) || !(scale == scale) || isinf(scale))
+    return DSA_ERR_INVALID_ARG;
+  if (S < 1 || S > DSA_MAX_SHARDS || I < 1 || (int64_t)I * S > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (block_size != 16 && block_size != 32 && block_size % 64) return DSA_ERR_UNSUPPORTED;
+  if (rows == 0 || reqs == 0) return DSA_OK;
+  if (!q || !kv_cache || !block_table || !query_starts || !seq_lens || !out || !lse2)
+    return DSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(out) || !aligned16(work))
+    return DSA_ERR_INVALID_ARG;
+  const int64_t pairs = (int64_t)rows * H;
+  if (n_slots > INT32_MAX || pairs > ((int64_t)1 << 30) || (int64_t)S * reqs > ((int64_t)1 << 30))
+    return DSA_ERR_UNSUPPORTED;
+  const int64_t cap = std::min<int64_t>((int64_t)max_blocks * block_size, (int64_t)1 << 30);
+  Plan p = plan_for(rows, S, H, reqs, cap);
+  if (!work) p.splits = 1;
+  DecodeArgs a{block_table, query_starts, seq_lens, tree_mask, reinterpret_cast<__nv_bfloat16*>(out),
+               lse2, nullptr, nullptr, err_flags, n_slots, reqs, max_blocks, block_size, rows, H,
+               mask_words, p.splits, (int)cap, std::min(block_size, 64), std::min(block_size, kVKeys),
+               scale * kLog2e, ShardMath(S, I), FastDiv(block_size), FastDiv(H)};
+  if (p.splits > 1) {
+    a.part_o = work;
+    a.part_l = work + (int64_t)p.splits * S * pairs * kDv;
+  }
+  CUtensorMap tq, tk, tv;
+  const uint64_t row = kDqk * 2;
+  if (!encode_map16(&tq, q, true, kDqk, pairs, 1, row, row * pairs, kQBox, 1) ||
+      !encode_map16(&tk, kv_cache, true, kDqk, n_slots, S, row, row * n_slots, a.kbox, 1) ||
+      !encode_map16(&tv, kv_cache, true, kDqk, n_slots, S, row, row * n_slots, a.vbox, 1))
+    return DSA_ERR_CUDA;
+  const int64_t items = (pairs / (p.cg * kRows) + reqs) * 2 * S * p.splits;   // at most
+  const cudaError_t e = p.cg == 2 ? launch_decode<2>(tq, tk, tv, a, items, stream)
+                                  : launch_decode<1>(tq, tk, tv, a, items, stream);
+  if (e != cudaSuccess) return DSA_ERR_CUDA;
+  if (p.splits > 1) {
+    const MergeArgs m{a.part_o, a.part_l, p.splits, S * pairs, query_starts, reqs, rows, H, out, lse2};
+    if (launch_merge<kDv, true>(m, stream) != cudaSuccess) return DSA_ERR_CUDA;
+  }
+  return DSA_OK;
+}

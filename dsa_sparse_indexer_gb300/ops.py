@@ -16,10 +16,12 @@ from . import _lib
 __all__ = ["shard_topk", "pack_candidates", "shard_topk_pack", "merge_topk_stable",
            "convert_index_compact", "indexer_fused", "lse_combine", "slot_mapping",
            "sparse_mla_decode", "rope_table", "rotary_embed", "kv_cache_insert_fp8",
-           "sparse_mla_decode_fp8", "new_error_flags", "SUPPORTED_K", "MLA_DQK", "MLA_DV"]
+           "sparse_mla_decode_fp8", "mla_prefill", "mla_decode", "indexer_key_insert",
+           "indexer_query_fp8", "new_error_flags", "SUPPORTED_K", "MLA_DQK", "MLA_DV"]
 
 SUPPORTED_K = (512, 1024, 2048)
 MLA_DQK, MLA_DV = 576, 512       # DSA_MLA_DQK, DSA_MLA_DV of include/dsa.h
+MLA_DN, MLA_DR, MLA_DVH = 128, 64, 128   # DSA_MLA_DN, DSA_MLA_DR, DSA_MLA_DVH
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -560,3 +562,218 @@ def sparse_mla_decode_fp8(q, kv_cache, block_scales, slots, counts, scale: float
             n_slots, block, _ptr(slots), _ptr(counts), rows, S, H, K, float(scale), _ptr(out),
             _ptr(lse2), _ptr(work), _ptr(err_flags), _raw_stream(q))
     return out, lse2
+
+
+# ---- whole contexts: expanded and absorbed attention; the indexer's operands --
+def _no_grad(*tensors):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError("no tensor may require grad: this call is not recorded by autograd "
+                         "(call it under torch.no_grad())")
+
+
+@functools.lru_cache(maxsize=4096)
+def _mla_prefill_work(device: int, Tq: int, Tk: int, n: int, H: int) -> int:
+    with torch.cuda.device(device):
+        return _lib.load().dsa_mla_prefill_work(Tq, Tk, n, H) // 4
+
+
+def mla_prefill(q, k_nope, k_pe, v, cu_q, cu_k, scale: float, causal: bool = True, out=None,
+                lse2=None, work=None, err_flags=None):
+    """Latent attention in its expanded form over a ragged batch.
+
+    q [Tq, H, 192], k_nope [Tk, H, 128], k_pe [Tk, 64] (one for all heads),
+    v [Tk, H, 128], all bf16 or all fp16, tokens and heads may be strided (views
+    of one projection's output); cu_q, cu_k [n + 1] int32: sequence i has queries
+    cu_q[i] .. cu_q[i + 1] and keys cu_k[i] .. cu_k[i + 1].  causal: the last query
+    sees all keys, each before it one less.  Returns (out [Tq, H, 128] of q's
+    type, lse2 [Tq, H] fp32, base 2): 0 and -inf where a query sees no key; rows of
+    no sequence are left as they are.  Outputs over parts of a context, stacked
+    [parts, Tq, H, 128] and [parts, Tq, H], are lse_combine's input (bf16).
+    work: fp32 workspace of calls with few queries, dsa_mla_prefill_work(Tq, Tk,
+    n, H) bytes (allocated when not given).  Autograd does not see the call."""
+    dtype = q.dtype if isinstance(q, torch.Tensor) else None
+    if dtype is not None and dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"q must be bf16 or fp16, got {dtype}")
+    q_token, q_head = _rows_of(q, "q", dtype)
+    k_token, k_head = _rows_of(k_nope, "k_nope", dtype)
+    pe_token, _ = _rows_of(k_pe, "k_pe", dtype)
+    v_token, v_head = _rows_of(v, "v", dtype)
+    _need(cu_q, "cu_q", torch.int32, 1)
+    _need(cu_k, "cu_k", torch.int32, 1)
+    _flags(err_flags)
+    if q.dim() != 3 or q.shape[2] != MLA_DN + MLA_DR:
+        raise ValueError("q must be [Tq, H, 192]")
+    Tq, H, _ = q.shape
+    Tk = k_pe.shape[0]
+    if tuple(k_nope.shape) != (Tk, H, MLA_DN) or tuple(v.shape) != (Tk, H, MLA_DVH) or \
+            tuple(k_pe.shape) != (Tk, MLA_DR):
+        raise ValueError("k_nope and v must be [Tk, H, 128] and k_pe [Tk, 64]")
+    n = cu_q.shape[0] - 1
+    if n < 0 or cu_k.shape[0] != n + 1:
+        raise ValueError("cu_q and cu_k must have one entry more than there are sequences")
+    if out is None:
+        out = torch.empty((Tq, H, MLA_DVH), dtype=dtype, device=q.device)
+    if lse2 is None:
+        lse2 = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
+    _need(out, "out", dtype, 3)
+    _need(lse2, "lse2", torch.float32, 2)
+    if tuple(out.shape) != (Tq, H, MLA_DVH) or tuple(lse2.shape) != (Tq, H):
+        raise ValueError("out must be [Tq, H, 128] and lse2 [Tq, H]")
+    _no_grad(q, k_nope, k_pe, v, out, lse2)
+    need = _mla_prefill_work(q.get_device(), Tq, Tk, n, H)
+    if work is None and need:
+        work = torch.empty(need, dtype=torch.float32, device=q.device)
+    if work is not None:
+        _need(work, "work", torch.float32, 1)
+        if work.shape[0] < need:
+            raise ValueError(f"work must have {need} entries")
+    context = _together(q, k_nope, k_pe, v, cu_q, cu_k, out, lse2, work, err_flags)
+    _launch(context, "dsa_mla_prefill", _ptr(q), q_token, q_head, _ptr(k_nope), k_token, k_head,
+            _ptr(k_pe), pe_token, _ptr(v), v_token, v_head, _ptr(cu_q), _ptr(cu_k), n, Tq, Tk, H,
+            ROPE_DTYPES[dtype], float(scale), int(bool(causal)), _ptr(out), _ptr(lse2), _ptr(work),
+            _ptr(err_flags), _raw_stream(q))
+    return out, lse2
+
+
+@functools.lru_cache(maxsize=4096)
+def _mla_decode_work(device: int, *sizes: int) -> int:
+    with torch.cuda.device(device):
+        return _lib.load().dsa_mla_decode_work(*sizes) // 4
+
+
+def mla_decode(q, kv_cache, block_table, block_size: int, query_starts, seq_lens, I: int,
+               scale: float, tree_mask=None, out=None, lse2=None, work=None, err_flags=None):
+    """Latent attention in its absorbed form over each shard's whole paged cache.
+
+    q [rows, H, 576] bf16, kv_cache [S, n_slots, 576] bf16, block_table
+    [S, reqs, max_blocks] int32; request r's rows are query_starts[r] ..
+    query_starts[r + 1] ([reqs + 1] int32), the last of its seq_lens[r] tokens
+    ([reqs] int32), whose cache rows are written already.  A row sees all tokens
+    before these rows and, of them, those up to itself, or with tree_mask [rows,
+    words] int32 those whose bit is set (bit i % 32 of word i / 32: the request's
+    row i; its own too, if it is to see itself).  Returns (out [S, rows, H, 512]
+    bf16, lse2 [S, rows, H] fp32, base 2) for lse_combine; rows of no request are
+    left as they are.  work: fp32 workspace of calls with few rows,
+    dsa_mla_decode_work(rows, S, H, reqs, max_blocks, block_size) bytes (allocated
+    when not given).  Autograd does not see the call."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(kv_cache, "kv_cache", torch.bfloat16, 3)
+    _need(block_table, "block_table", torch.int32, 3)
+    _need(query_starts, "query_starts", torch.int32, 1)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _flags(err_flags)
+    rows, H, dqk = q.shape
+    S, n_slots, dqk2 = kv_cache.shape
+    if dqk != MLA_DQK or dqk2 != MLA_DQK:
+        raise ValueError(f"q and kv_cache rows must have {MLA_DQK} entries")
+    _, reqs, max_blocks = block_table.shape
+    if block_table.shape[0] != S:
+        raise ValueError("block_table must be [S, reqs, max_blocks]")
+    if query_starts.shape[0] != reqs + 1 or seq_lens.shape[0] != reqs:
+        raise ValueError("query_starts must have reqs + 1 entries and seq_lens reqs")
+    words = 0
+    if tree_mask is not None:
+        _need(tree_mask, "tree_mask", torch.int32, 2)
+        words = tree_mask.shape[1]
+        if tree_mask.shape[0] != rows or words < 1:
+            raise ValueError("tree_mask must be [rows, words]")
+    if out is None:
+        out = torch.empty((S, rows, H, MLA_DV), dtype=torch.bfloat16, device=q.device)
+    if lse2 is None:
+        lse2 = torch.empty((S, rows, H), dtype=torch.float32, device=q.device)
+    _need(out, "out", torch.bfloat16, 4)
+    _need(lse2, "lse2", torch.float32, 3)
+    if tuple(out.shape) != (S, rows, H, MLA_DV) or tuple(lse2.shape) != (S, rows, H):
+        raise ValueError("out must be [S, rows, H, 512] and lse2 [S, rows, H]")
+    _no_grad(q, kv_cache, out, lse2)
+    need = _mla_decode_work(q.get_device(), rows, S, H, reqs, max_blocks, block_size)
+    if work is None and need:
+        work = torch.empty(need, dtype=torch.float32, device=q.device)
+    if work is not None:
+        _need(work, "work", torch.float32, 1)
+        if work.shape[0] < need:
+            raise ValueError(f"work must have {need} entries")
+    context = _together(q, kv_cache, block_table, query_starts, seq_lens, tree_mask, out, lse2, work,
+                        err_flags)
+    _launch(context, "dsa_mla_decode", _ptr(q), _ptr(kv_cache), n_slots, _ptr(block_table), reqs,
+            max_blocks, block_size, _ptr(query_starts), _ptr(seq_lens), _ptr(tree_mask), words, rows,
+            S, I, H, float(scale), _ptr(out), _ptr(lse2), _ptr(work), _ptr(err_flags),
+            _raw_stream(q))
+    return out, lse2
+
+
+def indexer_key_insert(k, norm_weight, norm_bias, eps: float, positions, cos_sin_cache,
+                       slot_mapping, k_cache, layout: str = "half", first: int = 0,
+                       err_flags=None):
+    """New tokens' indexer keys into the paged key cache of indexer_logits.
+
+    k [T, 128] bf16 (tokens may be strided) is layer-normed (norm_weight [128]
+    fp32, norm_bias the same or None), its values [first, first + rot_dim) turned
+    by the table's row of positions [T] int32 (cos_sin_cache [max_pos, rot_dim]
+    fp32, layouts as rotary_embed), and stored as e4m3 codes at slot_mapping [S, T]
+    int32 (slot_mapping's output; -1: not on that shard) of k_cache
+    [S, n_slots, 128] uint8.  The slots of one shard must differ."""
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {list(ROPE_LAYOUTS)}, got {layout!r}")
+    k_token, _ = _rows_of(k, "k", torch.bfloat16)
+    _need(norm_weight, "norm_weight", torch.float32, 1)
+    if norm_bias is not None:
+        _need(norm_bias, "norm_bias", torch.float32, 1)
+    _need(positions, "positions", torch.int32, 1)
+    _need(cos_sin_cache, "cos_sin_cache", torch.float32, 2)
+    _need(slot_mapping, "slot_mapping", torch.int32, 2)
+    _need(k_cache, "k_cache", torch.uint8, 3)
+    _flags(err_flags)
+    T = positions.shape[0]
+    S, n_slots, dim = k_cache.shape
+    if tuple(k.shape) != (T, IDX_DIM) or dim != IDX_DIM:
+        raise ValueError("k must be [T, 128], T positions, and k_cache [S, n_slots, 128]")
+    if norm_weight.shape[0] != IDX_DIM or (norm_bias is not None and norm_bias.shape[0] != IDX_DIM):
+        raise ValueError("norm_weight and norm_bias must have 128 entries")
+    if tuple(slot_mapping.shape) != (S, T):
+        raise ValueError("slot_mapping must be [S, T]")
+    _no_grad(k, norm_weight, norm_bias)
+    context = _together(k, norm_weight, norm_bias, positions, cos_sin_cache, slot_mapping, k_cache,
+                        err_flags)
+    _launch(context, "dsa_indexer_key_insert", _ptr(k), k_token, _ptr(norm_weight),
+            _ptr(norm_bias), float(eps), _ptr(positions), _ptr(cos_sin_cache),
+            cos_sin_cache.shape[0], cos_sin_cache.shape[1], first, ROPE_LAYOUTS[layout],
+            _ptr(slot_mapping), T, S, _ptr(k_cache), n_slots, _ptr(err_flags), _raw_stream(k))
+    return k_cache
+
+
+def indexer_query_fp8(q, weights, positions, cos_sin_cache, factor: float = 1.0,
+                      layout: str = "half", first: int = 0, q_out=None, weights_out=None,
+                      err_flags=None):
+    """The queries and head weights of indexer_logits: q [T, H, 128] bf16 (tokens
+    and heads may be strided) turned like indexer_key_insert's keys and held as
+    e4m3 codes with a power-of-two scale a head, which goes into weights [T, H]
+    fp32 together with factor.  Returns (q_out [T, H, 128] uint8, weights_out
+    [T, H] fp32)."""
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {list(ROPE_LAYOUTS)}, got {layout!r}")
+    q_token, q_head = _rows_of(q, "q", torch.bfloat16)
+    _need(weights, "weights", torch.float32, 2)
+    _need(positions, "positions", torch.int32, 1)
+    _need(cos_sin_cache, "cos_sin_cache", torch.float32, 2)
+    _flags(err_flags)
+    if q.dim() != 3 or q.shape[2] != IDX_DIM:
+        raise ValueError("q must be [T, H, 128]")
+    T, H, _ = q.shape
+    if tuple(weights.shape) != (T, H) or positions.shape[0] != T:
+        raise ValueError("weights must be [T, H] and positions [T]")
+    if q_out is None:
+        q_out = torch.empty((T, H, IDX_DIM), dtype=torch.uint8, device=q.device)
+    if weights_out is None:
+        weights_out = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    _need(q_out, "q_out", torch.uint8, 3)
+    _need(weights_out, "weights_out", torch.float32, 2)
+    if tuple(q_out.shape) != (T, H, IDX_DIM) or tuple(weights_out.shape) != (T, H):
+        raise ValueError("q_out must be [T, H, 128] and weights_out [T, H]")
+    _no_grad(q, weights, weights_out)
+    context = _together(q, weights, positions, cos_sin_cache, q_out, weights_out, err_flags)
+    _launch(context, "dsa_indexer_query_fp8", _ptr(q), q_token, q_head, _ptr(weights),
+            float(factor), _ptr(positions), _ptr(cos_sin_cache), cos_sin_cache.shape[0],
+            cos_sin_cache.shape[1], first, ROPE_LAYOUTS[layout], T, H, _ptr(q_out),
+            _ptr(weights_out), _ptr(err_flags), _raw_stream(q))
+    return q_out, weights_out

@@ -24,6 +24,9 @@
  * Beside them, for long contexts: dsa_rope_table and dsa_rotary_embed (rotary
  * positions), dsa_kv_cache_insert_fp8 and dsa_sparse_mla_decode_fp8 (the cache
  * in 8 bits with a scale for each block of slots, and the attention over it).
+ * For whole contexts: dsa_mla_prefill (expanded heads) and dsa_mla_decode (over
+ * the paged cache, with trees of drafted tokens); dsa_indexer_key_insert and
+ * dsa_indexer_query_fp8 make the 8-bit operands of dsa_indexer_logits.
  *
  * Sharding (PR #46076 report, section 关键源码片段, comment in
  * `_dcp_localize_decode_seq_lens`): global token t lives on shard
@@ -44,8 +47,8 @@
  *     that exists while the library is loaded).
  *   - Every call is asynchronous on `stream` (0 = legacy default stream) and
  *     enqueues one kernel (dsa_indexer_steps_noalloc: three;
- *     dsa_kv_cache_insert_fp8: one or two); results are
- *     ready when the stream reaches it.
+ *     dsa_kv_cache_insert_fp8, dsa_mla_prefill and dsa_mla_decode: one or
+ *     two); results are ready when the stream reaches it.
  *   - Arguments are checked on the host before anything is enqueued.  A bad
  *     argument returns DSA_ERR_INVALID_ARG or DSA_ERR_UNSUPPORTED and touches
  *     nothing.  rows == 0 returns DSA_OK and enqueues nothing once the scalar
@@ -86,6 +89,11 @@ enum {
  * values in all. */
 #define DSA_MLA_DQK 576
 #define DSA_MLA_DV 512
+/* Expanded latent attention (dsa_mla_prefill): a head's own part of a key, the
+ * rope part that all heads share, and its values. */
+#define DSA_MLA_DN 128
+#define DSA_MLA_DR 64
+#define DSA_MLA_DVH 128
 /* Indexer-logits shape: query heads per token and values per head / key. */
 #define DSA_IDX_HEADS 64
 #define DSA_IDX_DIM 128
@@ -556,6 +564,159 @@ dsa_status dsa_sparse_mla_decode_fp8(const uint16_t* q, const uint8_t* kv_cache,
 
 /* Bytes of the workspace that dsa_sparse_mla_decode_fp8 may use for these sizes (0: none). */
 int64_t dsa_sparse_mla_decode_fp8_work(int rows, int S, int H, int K);
+
+/*
+ * dsa_mla_prefill - latent attention in its expanded form over a ragged batch.
+ * The n sequences' queries lie one behind another: sequence i's are rows
+ * cu_q[i] .. cu_q[i + 1], its keys and values rows cu_k[i] .. cu_k[i + 1].  Query
+ * r of its lq sees all of its lk keys, or with causal != 0 the first lk - lq +
+ * r + 1 of them (its last query is at its last key; a query before its first
+ * key sees none).  Per head h, over the visible keys j:
+ *   x_j = scale * (q[0 .. DSA_MLA_DN) . k_nope_j + q[DSA_MLA_DN ..) . k_pe_j),
+ *   out = sum_j exp(x_j) v_j / sum_j exp(x_j); lse2 = log2 sum_j exp(x_j);
+ * a query that sees no key gets out = 0 and lse2 = -inf.  Outputs over several
+ * parts of a context, stacked, are what dsa_lse_combine merges.
+ *
+ *   q          [Tq][H][DSA_MLA_DN + DSA_MLA_DR] of dtype (DSA_BF16, DSA_FP16)
+ *   k_nope     [Tk][H][DSA_MLA_DN], v [Tk][H][DSA_MLA_DVH], k_pe [Tk][DSA_MLA_DR]
+ *              (one for all heads): all of dtype, values contiguous, 16-byte
+ *              aligned, token and head strides in elements, multiples of 8
+ *              (heads apart by a head's width at least)
+ *   cu_q, cu_k [n + 1] int32, ascending
+ *   out        [Tq][H][DSA_MLA_DVH] of dtype, 16-byte aligned; lse2 [Tq][H] fp32;
+ *              rows of no sequence are left as they are
+ *   work       dsa_mla_prefill_work(Tq, Tk, n, H) bytes, contents arbitrary,
+ *              16-byte aligned, or NULL: the keys of a call with few queries are
+ *              then not split over several CTAs.  Calls that may run at the same
+ *              time need their own.
+ *   err_flags  DSA_FLAG_BOUNDS if a cu_q or cu_k entry is outside its rows or
+ *              below the one before it (taken as the nearest that is not);
+ *              DSA_FLAG_TIMEOUT if a bounded wait ran out (outputs incomplete).
+ * Scores and sums are fp32; a softmax weight enters the value product rounded to
+ * dtype, relative to a maximum of its row within 2^8.  Keys that a query does not
+ * see may hold anything; values of a sequence's own keys are to be finite (a
+ * weight of 0 times an infinity is NaN), what lies outside it may be anything.
+ * Enqueues two kernels when the keys are split, else one.
+ * Errors: negative sizes, H < 1, scale not finite, another dtype, null pointers,
+ *         misalignment, strides -> INVALID_ARG; more than 2^26 blocks of 256
+ *         queries (times heads) -> UNSUPPORTED; tensor-map encoding -> CUDA.
+ */
+dsa_status dsa_mla_prefill(const void* q, int64_t q_token, int64_t q_head, const void* k_nope,
+                           int64_t k_token, int64_t k_head, const void* k_pe, int64_t pe_token,
+                           const void* v, int64_t v_token, int64_t v_head, const int32_t* cu_q,
+                           const int32_t* cu_k, int n, int Tq, int Tk, int H, int dtype,
+                           float scale, int causal, void* out, float* lse2, float* work,
+                           uint32_t* err_flags, cudaStream_t stream);
+
+/* Bytes of the workspace that dsa_mla_prefill may use for these sizes (0: none). */
+int64_t dsa_mla_prefill_work(int Tq, int Tk, int n, int H);
+
+/*
+ * dsa_mla_decode - latent attention in its absorbed form over every shard's whole
+ * paged cache: dsa_sparse_mla_decode's outputs for all of a request's tokens
+ * instead of selected slots, with one row (token) a request or several, chained
+ * or drafted as a tree.
+ *
+ * Request r's rows are query_starts[r] .. query_starts[r + 1], n of them; its
+ * seq_lens[r] = L tokens are in the cache already, the last n of them these rows
+ * (row j at global position L - n + j).  A row sees every token before position
+ * L - n and, of the n, those up to itself (tree_mask NULL) or those whose bit is
+ * set: bit i mod 32 of tree_mask[row][i / 32] for token L - n + i; tokens behind
+ * the mask's words are not seen.  Shard s holds its tokens in order at physical
+ * slots block_table[s][r][l / block_size] * block_size + l % block_size.
+ *
+ *   q            [rows][H][DSA_MLA_DQK] bf16, 16-byte aligned
+ *   kv_cache     [S][n_slots][DSA_MLA_DQK] bf16, 16-byte aligned
+ *   block_table  [S][reqs][max_blocks] int32; query_starts [reqs + 1], seq_lens
+ *                [reqs] int32; tree_mask [rows][mask_words] int32 or NULL
+ *   out          [S][rows][H][DSA_MLA_DV] bf16, 16-byte aligned; lse2 [S][rows][H]
+ *                fp32, base 2: 0 and -inf where a row sees nothing on a shard;
+ *                rows of no request are left as they are
+ *   work         dsa_mla_decode_work(rows, S, H, reqs, max_blocks, block_size)
+ *                bytes, contents arbitrary, 16-byte aligned, or NULL: the tokens
+ *                of a call with few rows are then not split over several CTAs.
+ *                Calls that may run at the same time need their own.
+ *   err_flags    DSA_FLAG_BOUNDS if query_starts is not ascending within the rows
+ *                (entries taken as the nearest that is), a length is negative
+ *                or past the table (cut) or an entry points outside the cache
+ *                (its tokens are left out); DSA_FLAG_TIMEOUT if a bounded wait
+ *                ran out (outputs incomplete).
+ * Scores and sums are fp32; a softmax weight enters the value product as bf16.
+ * Cache rows of a request's own tokens are to be finite (a weight of 0 times an
+ * infinity is NaN); slots behind its last token may hold anything.
+ * Enqueues two kernels when tokens are split, else one.
+ * Errors: negative sizes, H < 1, n_slots < 1, max_blocks < 1, block_size < 1,
+ *         mask_words < 1 with a mask, scale not finite, null pointers,
+ *         misalignment -> INVALID_ARG; S not in [1, 64], I < 1, I*S > INT32_MAX,
+ *         block_size not 16, 32 or a multiple of 64, n_slots > 2^31 - 1, rows * H
+ *         or S * reqs > 2^30 -> UNSUPPORTED; tensor-map encoding -> CUDA.
+ */
+dsa_status dsa_mla_decode(const uint16_t* q, const uint16_t* kv_cache, int64_t n_slots,
+                          const int32_t* block_table, int reqs, int max_blocks, int block_size,
+                          const int32_t* query_starts, const int32_t* seq_lens,
+                          const int32_t* tree_mask, int mask_words, int rows, int S, int I, int H,
+                          float scale, uint16_t* out, float* lse2, float* work,
+                          uint32_t* err_flags, cudaStream_t stream);
+
+/* Bytes of the workspace that dsa_mla_decode may use for these sizes (0: none). */
+int64_t dsa_mla_decode_work(int rows, int S, int H, int reqs, int max_blocks, int block_size);
+
+/*
+ * dsa_indexer_key_insert - new tokens' indexer keys into the paged key cache that
+ * dsa_indexer_logits reads: layer norm, rotation, 8 bits, the token's slot.
+ *   y = (k - mean(k)) / sqrt(var(k) + eps) * norm_weight + norm_bias,
+ *   [first, first + rot_dim) of y turned by the table's row of the token's
+ *   position (as dsa_rotary_embed), code = e4m3(y): fp32 arithmetic, one rounding
+ *   to nearest even, saturating at +-448 (an infinity too; NaN stays NaN).
+ *
+ *   k            [T][DSA_IDX_DIM] bf16, token stride in elements, a multiple of
+ *                8; 16-byte aligned
+ *   norm_weight  [DSA_IDX_DIM] fp32, norm_bias the same or NULL (none); 16-byte
+ *                aligned
+ *   positions    [T] int32; cos_sin_cache [max_pos][rot_dim] fp32
+ *   slot_mapping [S][T] int32, as dsa_slot_mapping writes it: token i goes to slot
+ *                slot_mapping[s][i] of shard s; a slot < 0 writes nothing.  The
+ *                slots of one shard that are not negative must differ.
+ *   k_cache      [S][n_slots][DSA_IDX_DIM] e4m3 codes, 16-byte aligned
+ *   err_flags    DSA_FLAG_BOUNDS if a position is outside [0, max_pos) (that key
+ *                is not turned) or a slot is >= n_slots (skipped)
+ * Errors: T < 0, n_slots < 1, eps negative or not finite, max_pos < 1, rot_dim odd
+ *         or < 2, the turning part outside [0, DSA_IDX_DIM), an unknown layout,
+ *         null pointers, misalignment -> INVALID_ARG; S not in [1, 64] ->
+ *         UNSUPPORTED.
+ */
+dsa_status dsa_indexer_key_insert(const uint16_t* k, int64_t k_token, const float* norm_weight,
+                                  const float* norm_bias, float eps, const int32_t* positions,
+                                  const float* cos_sin_cache, int max_pos, int rot_dim, int first,
+                                  int layout, const int32_t* slot_mapping, int T, int S,
+                                  uint8_t* k_cache, int64_t n_slots, uint32_t* err_flags,
+                                  cudaStream_t stream);
+
+/*
+ * dsa_indexer_query_fp8 - the queries and head weights of dsa_indexer_logits:
+ * each head's values turned as dsa_indexer_key_insert turns keys, held in 8 bits
+ * with a scale of its own that goes into the head's weight (a logit is a weighted
+ * sum of max(0, q . k), so that a positive factor of q may move there):
+ *   s = the smallest power of two >= 2^-126 with max |y| <= 448 s over the head's
+ *       finite values (1 where all are 0),
+ *   q_out = e4m3(y / s) (to nearest even; infinities saturate), weights_out =
+ *   weights * factor * s.
+ *
+ *   q            [T][H][DSA_IDX_DIM] bf16, token and head strides in elements,
+ *                multiples of 8; 16-byte aligned
+ *   weights      [T][H] fp32; factor finite (the logits' scale)
+ *   positions, cos_sin_cache, max_pos, rot_dim, first, layout, err_flags (a
+ *                position out of range): as dsa_indexer_key_insert
+ *   q_out        [T][H][DSA_IDX_DIM] e4m3 codes, 16-byte aligned; weights_out
+ *                [T][H] fp32 (may be weights itself)
+ * Errors: T < 0, H < 1, factor not finite, the rotation's as above, null pointers,
+ *         misalignment -> INVALID_ARG; too many blocks -> UNSUPPORTED.
+ */
+dsa_status dsa_indexer_query_fp8(const uint16_t* q, int64_t q_token, int64_t q_head,
+                                 const float* weights, float factor, const int32_t* positions,
+                                 const float* cos_sin_cache, int max_pos, int rot_dim, int first,
+                                 int layout, int T, int H, uint8_t* q_out, float* weights_out,
+                                 uint32_t* err_flags, cudaStream_t stream);
 
 /*
  * dsa_indexer_steps_noalloc - dsa_shard_topk_pack, dsa_merge_topk_stable and
