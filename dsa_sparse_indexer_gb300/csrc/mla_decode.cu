@@ -172,35 +172,6 @@ __device__ __forceinline__ bool has_tail(const Item& it, int t) {
   return it.nall - t * kTileK < 16 * value_steps(it, t);
 }
 
-__device__ __forceinline__ uint32_t pair_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// The address of the same object in the pair's first CTA.
-__device__ __forceinline__ uint32_t leader_addr(const void* p) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
-  return r;
-}
-// A box into this CTA's memory, its bytes counted by `bar` (a shared::cluster address).
-template <int CG>
-__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int x, int y, int z,
-                                         uint32_t bar) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-
 // ---- the copies ---------------------------------------------------------------
 struct PendingV {              // values of a stream tile whose keys are copied
   int y, half, shard;          // lane i: row of the cache of its keys 16 i
@@ -338,8 +309,7 @@ __device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem& 
   };
   // Values of stream tile v: `steps` of 16 keys, the item's first or not.
   auto values = [&](uint32_t v, int steps, bool first) {
-    ok = CG == 1 ? wait_or_abort(&sm.abort, &sm.pfull[v & 1u], (v >> 1) & 1u)
-                 : wait_or_abort_pair(&sm.abort, &sm.pfull[v & 1u], (v >> 1) & 1u);
+    ok = wait_or_abort(&sm.abort, &sm.pfull[v & 1u], (v >> 1) & 1u);
     for (int b = 0; ok && b < kVBlocks; ++b, ++seq) {
       if (!landed()) return;
       const uint32_t blk = ring0 + (seq % Sh::kRing) * Sh::kBlock;
@@ -458,6 +428,7 @@ __device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem& s
       const uint32_t pages = *reinterpret_cast<volatile uint32_t*>(&sm.pages[j % kInfo]);
       tmem_wait_ld(x);
       if (a.c2 <= 0.f) {
+        keep_branch();
 #pragma unroll
         for (int k = 0; k < kTileK; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * sign);
       }
@@ -534,17 +505,14 @@ __device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem& s
           *reinterpret_cast<uint4*>(blk + (chunk >> 3) * Sh::kAtom + (key % kVKeys) * 128 + (chunk & 7) * 16) =
               make_uint4(0, 0, 0, 0);
         }
-        fence_async_smem();                  // before this warp hands its weights over
+        fence_for_products<CG>();            // before this warp hands its weights over
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if constexpr (CG == 1) mbar_arrive1(&sm.pfull[b]);
-        else
-          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                           leader_addr(&sm.pfull[b]))
-                       : "memory");
+        else mbar_arrive_leader(&sm.pfull[b]);
       }
     }
     const bool some = it.t1 > it.t0;
@@ -640,10 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) {                   // the other CTA's barriers are there
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  }
+  if constexpr (CG == 2) pair_sync();        // the other CTA's barriers are there
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   const int blocks = sm.blocks;
@@ -653,10 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   else if (rank == 0) issue_products<CG>(a, sm, tmem, blocks, items);
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) {                   // neither CTA's memory goes while the other uses it
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  }
+  if constexpr (CG == 2) pair_sync();        // neither CTA's memory goes while the other uses it
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_free<CG>(tmem, kTmemCols);
@@ -685,29 +647,8 @@ cudaError_t launch_decode(const CUtensorMap& q, const CUtensorMap& k, const CUte
   const auto kernel = mla_decode_kernel<CG>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  int at_once = device_sms() / CG;
-  if (CG == 2) {                             // pairs that run at once: SM groups may be odd
-    constexpr int kDevices = 64;
-    static int pairs[kDevices];
-    int dev = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kDevices) {
-      if (pairs[dev] == 0) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(at_once * CG));
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kSmem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = CG;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        pairs[dev] = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0 ? n : at_once;
-      }
-      at_once = std::min(at_once, pairs[dev]);
-    }
-  }
+  static DeviceCount pairs;
+  const int at_once = CG == 1 ? device_sms() : pairs.get(kernel, kThreads, kSmem);
   const unsigned grid = (unsigned)(std::min<int64_t>(items, at_once) * CG);
   return launch_kernel(kernel, dim3(grid), dim3(kThreads), (size_t)kSmem, stream, CG == 2 ? 2u : 0u,
                        q, k, v, a);

@@ -10,6 +10,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cstring>
+
 #include "common.cuh"
 
 namespace dsa {
@@ -30,6 +32,20 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr, uint32_t lbo,
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// The same value in every lane, made known as such: what follows from it stays in
+// uniform registers, and branches on it are the warp's.
+__device__ __forceinline__ int uni(int v) { return __shfl_sync(kFull, v, 0); }
+__device__ __forceinline__ uint32_t uni(uint32_t v) { return __shfl_sync(kFull, v, 0); }
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Instruction descriptor of kind::f16: D fp32 (bits 4-5 = 1), A and B of one
 // type (bits 7-9, 10-12: 0 fp16, 1 bf16), A K-major, B K-major or MN-major (bit
 // 16), N >> 3 (bits 17-22), M >> 4 (bits 24-28).
@@ -37,6 +53,8 @@ constexpr uint32_t idesc_f16(int m, int n, bool bf16, bool b_mn_major) {
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
          ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
+
+constexpr uint32_t kNegateA = 1u << 13;      // descriptor bit: D = or += -A B
 
 // D (tensor memory) = or += A B: A from shared memory (_ss) or tensor memory (_ts).
 template <int CG>
@@ -128,26 +146,200 @@ __device__ __forceinline__ void tmem_wait_st() {
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
+// This thread's writes to shared memory, read next by a product (of a pair: that
+// the first CTA issues).
+template <int CG>
+__device__ __forceinline__ void fence_for_products() {
+  fence_async_smem();
+  if constexpr (CG == 2) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
 __device__ __forceinline__ void mbar_arrive1(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Tensor-map copies global -> shared: a box of [rows][64] 16-bit values.
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
+// A CTA's word that one role sets when a wait of its ran out; the others stop
+// at their next wait.
+__device__ __forceinline__ bool cta_aborted(const int* abort) {
+  return *reinterpret_cast<const volatile int*>(abort) != 0;
 }
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
+__device__ __forceinline__ void cta_abort(int* abort, uint32_t* flags) {
+  raise_flag(flags, DSA_FLAG_TIMEOUT);
+  *reinterpret_cast<volatile int*>(abort) = 1;
+}
+// Bounded wait that also gives up once another role has aborted.
+__device__ __forceinline__ bool wait_or_abort(const int* abort, uint64_t* bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 63 && cta_aborted(abort)) return false;
+  }
+  return false;
+}
+// The same for a converged warp, all lanes alike.  All of them poll: a branch for
+// one lane costs every wait its divergence (8192 queries of 128 heads, expanded:
+// 2992 us with one polling lane, 2180 so).
+__device__ __forceinline__ bool warp_wait(const int* abort, uint64_t* bar, uint32_t parity) {
+  return __all_sync(kFull, wait_or_abort(abort, bar, parity));
+}
+
+// ---- pairs of CTAs ----------------------------------------------------------
+__device__ __forceinline__ uint32_t pair_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The address of the same object in the pair's first CTA.
+__device__ __forceinline__ uint32_t leader_addr(const void* p) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+// A box into this CTA's memory, its bytes counted by `bar` (a shared::cluster address).
+template <int CG>
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                         uint32_t bar) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+// One arrival on the barrier of the pair's first CTA.  What it announces lies in
+// tensor memory (waited for and fenced by tcgen05 instructions): released to the
+// CTA's scope alone.  With .cluster it waits for every memory access of the thread
+// before, and a hand-over of weights took 1400 cycles instead of 150.
+__device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar)) : "memory");
+}
+// Every thread of both CTAs.
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---- items of work, shared out while the kernel runs -------------------------
+// The grid has a cluster of CG CTAs for every item; those that the device has not
+// started yet are cancelled by running ones, which take their items over (cluster
+// launch control), so that CTAs end together whatever their items' lengths, and
+// the next item's first copies run under the last one's end.  One warp of each
+// CTA claims items and works out what they are; the others read that from two
+// slots in shared memory.
+template <typename Item>
+struct WorkSlots {
+  uint4 claimed;              // the launch control's answer (of a pair: to both CTAs)
+  uint64_t answer, ready;     // it has come; both CTAs are ready for the next one
+  uint64_t full[2], empty[2];
+  Item item[2];
+  int last[2];                // nothing here: no more items
+};
+template <typename Item>
+__device__ __forceinline__ void init_slots(WorkSlots<Item>& s, int cg, int readers) {
+  mbar_init(&s.answer, 1);
+  mbar_init(&s.ready, cg);
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&s.full[i], 1);
+    mbar_init(&s.empty[i], readers);
+  }
+}
+
+// The claiming warp.  `find` (warp-wide) says what item `index` < total is.
+template <int CG, typename Item, typename Find>
+__device__ __forceinline__ void share_out(WorkSlots<Item>& s, int* abort, uint32_t* flags,
+                                          int64_t total, uint32_t rank, Find&& find) {
+  const int lane = threadIdx.x & 31;
+  int64_t index = blockIdx.x / CG;
+  uint32_t claims = 0;
+  bool ok = true;
+  for (uint32_t n = 0; ok; ++n) {
+    const uint32_t slot = n & 1u;
+    const bool last = index >= total;
+    Item it{};
+    if (!last) it = find(index);
+    if (n >= 2) ok = warp_wait(abort, &s.empty[slot], ((n >> 1) - 1) & 1u);
+    if (!ok) break;
+    if (lane == 0) {
+      s.item[slot] = it;
+      s.last[slot] = last;
+      mbar_arrive1(&s.full[slot]);
+    }
+    if (last) return;
+    bool got;
+    do {                                     // clusters past the last item are only cancelled
+      if (lane == 0) {
+        mbar_expect_tx(&s.answer, 16);
+        if (CG == 1) mbar_arrive1(&s.ready);
+        else mbar_arrive_leader(&s.ready);
+        if (rank == 0) {
+          ok = wait_or_abort(abort, &s.ready, claims & 1u);
+          if (ok) {
+            if constexpr (CG == 1)
+              asm volatile(
+                  "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+                  " [%0], [%1];" ::"r"(smem_u32(&s.claimed)), "r"(smem_u32(&s.answer))
+                  : "memory");
+            else
+              asm volatile(
+                  "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+                  ".multicast::cluster::all.b128 [%0], [%1];" ::"r"(smem_u32(&s.claimed)),
+                  "r"(smem_u32(&s.answer))
+                  : "memory");
+          }
+        }
+      }
+      ok = __all_sync(kFull, ok) && warp_wait(abort, &s.answer, claims & 1u);
+      ++claims;
+      uint32_t x = 0, yes = 0;
+      if (ok)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 y, z, w;\n\t"
+            "ld.shared.b128 r, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+            "selp.u32 %1, 1, 0, p;\n\t"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, r;\n\t}"
+            : "+r"(x), "=r"(yes)
+            : "r"(smem_u32(&s.claimed))
+            : "memory");
+      got = ok && yes != 0;
+      index = got ? (int64_t)(x / CG) : total;
+      fence_async_smem();                    // read before the next answer is written
+      __syncwarp();
+    } while (got && index >= total);
+  }
+  if (lane == 0 && !cta_aborted(abort)) cta_abort(abort, flags);
+  __syncwarp();
+}
+
+// A reading warp's n-th item; false at the end (or where a wait ran out).
+template <typename Item>
+__device__ __forceinline__ bool next_item(const WorkSlots<Item>& s, const int* abort, uint32_t n,
+                                          bool& ok) {
+  const uint32_t slot = n & 1u;
+  ok = ok && warp_wait(abort, const_cast<uint64_t*>(&s.full[slot]), (n >> 1) & 1u);
+  return ok && !s.last[slot];
+}
+template <typename Item>
+__device__ __forceinline__ bool next_item(const WorkSlots<Item>& s, const int* abort, uint32_t n,
+                                          bool& ok, Item& it) {
+  const bool more = next_item(s, abort, n, ok);
+  if (more) {
+    static_assert(sizeof(Item) % 4 == 0, "an item is words");
+    int w[sizeof(Item) / 4];
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(Item) / 4; ++i) w[i] = uni(reinterpret_cast<const int*>(&s.item[n & 1u])[i]);
+    memcpy(&it, w, sizeof(Item));
+  }
+  return more;
+}
+template <typename Item>
+__device__ __forceinline__ void item_done(WorkSlots<Item>& s, uint32_t n) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive1(&s.empty[n & 1u]);
 }
 
 // Consecutive fp32 columns of this warp's 32 tensor-memory lanes.  A load's
@@ -167,12 +359,26 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
         "=r"(r[o + 25]), "=r"(r[o + 26]), "=r"(r[o + 27]), "=r"(r[o + 28]), "=r"(r[o + 29]),  \
         "=r"(r[o + 30]), "=r"(r[o + 31])                                                     \
       : "r"(taddr + (uint32_t)(o)))
+#define DSA_TC_LD16(o)                                                                        \
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, "  \
+               "%8, %9, %10, %11, %12, %13, %14, %15}, [%16];"                              \
+               : "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]),           \
+                 "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7]),           \
+                 "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]), "=r"(r[o + 11]),         \
+                 "=r"(r[o + 12]), "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15])        \
+               : "r"(taddr + (uint32_t)(o)))
 #define DSA_TC_USE16(o)                                                                     \
   asm volatile(""                                                                           \
                : "+r"(r[o + 0]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]),           \
                  "+r"(r[o + 4]), "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7]),           \
                  "+r"(r[o + 8]), "+r"(r[o + 9]), "+r"(r[o + 10]), "+r"(r[o + 11]),         \
                  "+r"(r[o + 12]), "+r"(r[o + 13]), "+r"(r[o + 14]), "+r"(r[o + 15]))
+#define DSA_TC_ST8(o)                                                                       \
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, "  \
+               "%8};" ::"r"(taddr + (uint32_t)(o)),                                         \
+               "r"(r[o + 0]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]),   \
+               "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])                                  \
+               : "memory")
 #define DSA_TC_ST16(o)                                                                      \
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, " \
                "%8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr + (uint32_t)(o)),  \
@@ -184,9 +390,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
 
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[N]) {
-  static_assert(N % 32 == 0, "columns in steps of 32");
+  static_assert(N == 16 || N % 32 == 0, "16 columns, or steps of 32");
+  if constexpr (N == 16) {
+    DSA_TC_LD16(0);
+  } else {
 #pragma unroll
-  for (int o = 0; o < N; o += 32) DSA_TC_LD32(o);
+    for (int o = 0; o < N; o += 32) DSA_TC_LD32(o);
+  }
 }
 template <int N>
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N]) {
@@ -196,50 +406,56 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N]) {
 }
 template <int N>
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[N]) {
-  static_assert(N % 16 == 0, "columns in steps of 16");
+  static_assert(N == 8 || N % 16 == 0, "8 columns, or steps of 16");
+  if constexpr (N == 8) {
+    DSA_TC_ST8(0);
+  } else {
 #pragma unroll
-  for (int o = 0; o < N; o += 16) DSA_TC_ST16(o);
+    for (int o = 0; o < N; o += 16) DSA_TC_ST16(o);
+  }
+}
+
+// Sixteen lanes as fragments: of 8 fp32 columns a thread has, in registers 4 i to 4
+// i + 3, columns 8 i + 2 (lane % 4) and the next of row lane / 4, then of row lane /
+// 4 + 8; of 4 columns of 16-bit pairs, in registers 2 i and 2 i + 1, column 4 i +
+// lane % 4 of either row: where the same thread's fp32 columns go as pairs.
+__device__ __forceinline__ void tmem_load_frag(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, "
+               "%8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+                 "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_store_frag(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, "
+               "%8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+               "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+               "r"(r[15])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_store_pairs(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, "
+               "%8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 #undef DSA_TC_LD32
+#undef DSA_TC_LD16
 #undef DSA_TC_USE16
+#undef DSA_TC_ST8
 #undef DSA_TC_ST16
 
-// A CTA's word that one role sets when a wait of its ran out; the others stop
-// at their next wait.
-__device__ __forceinline__ bool cta_aborted(const int* abort) {
-  return *reinterpret_cast<const volatile int*>(abort) != 0;
-}
-__device__ __forceinline__ void cta_abort(int* abort, uint32_t* flags) {
-  raise_flag(flags, DSA_FLAG_TIMEOUT);
-  *reinterpret_cast<volatile int*>(abort) = 1;
-}
-// Bounded wait that also gives up once another role has aborted.
-__device__ __forceinline__ bool wait_or_abort(const int* abort, uint64_t* bar, uint32_t parity) {
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (cta_aborted(abort)) return false;
-    if (i > 64) __nanosleep(64);
-  }
-  return false;
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
-// The same for a barrier that the pair's other CTA arrives on too.
-__device__ __forceinline__ bool wait_or_abort_pair(const int* abort, uint64_t* bar, uint32_t parity) {
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if (cta_aborted(abort)) return false;
-    if (i > 64) __nanosleep(64);
-  }
-  return false;
-}
+// In a branch rarely taken: keeps it one (as predicated instructions, a pass of
+// 128 compares and selects cost every tile 300 cycles).
+__device__ __forceinline__ void keep_branch() { asm volatile("" ::: "memory"); }
 
 // 2^x (ex2.approx.ftz.f32: relative error about 2^-22, results below 2^-126
 // flushed to zero; 2^-inf = 0).
@@ -272,6 +488,21 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
       : "=l"(r)
       : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
   return *reinterpret_cast<float2*>(&r);
+}
+
+// Word i of lane j (of four neighbours) and word j of lane i change places.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4], int lane) {
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {         // the lane's bit o against the word's
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!(i & o)) {
+        const uint32_t give = up ? w[i] : w[i + o], got = __shfl_xor_sync(kFull, give, o);
+        if (up) w[i] = got;
+        else w[i + o] = got;
+      }
+  }
 }
 
 // Two values as 16-bit floats in one word, each rounded to nearest even.
@@ -333,5 +564,34 @@ inline int device_sms() {
   }
   return sms[dev];
 }
+
+// Pairs of CTAs of a kernel that a device runs at once (SM groups may be odd, so
+// that this may be less than half of its SMs); looked up once a device.
+struct DeviceCount {
+  static constexpr int kDevices = 64;
+  int count[kDevices] = {};
+  template <typename K>
+  int get(K kernel, int threads, int smem) {
+    int dev = 0;
+    const int half = device_sms() / 2;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return half;
+    if (count[dev] == 0) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)(half * 2));
+      cfg.blockDim = dim3((unsigned)threads);
+      cfg.dynamicSmemBytes = (size_t)smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      const bool known = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
+      count[dev] = known ? (n < half ? n : half) : half;
+    }
+    return count[dev];
+  }
+};
 
 }  // namespace dsa
