@@ -20,7 +20,7 @@
 //  * shared memory: the block's queries (144 KB) and a ring of 80 KB in blocks of
 //    16 KB / CG: a key tile's nine 64-value column blocks, the values' four
 //    blocks of 32 keys, in the order in which the products take them: keys of
-//    tile j + 2 behind values of tile j, also across items;
+//    tile j + 2 behind values of tile j;
 //  * a warp copies (tensor maps, a box per page or 64 keys), one thread (of the
 //    pair's first CTA) issues, four warps run the softmax, a thread a row.
 // The keys may be split into parts that a second kernel joins.
@@ -41,7 +41,9 @@ constexpr int kQBlocks = kDqk / 64, kQBlock = kRows * 128, kQBox = 32;
 constexpr int kKBlocks = kDqk / 64, kVBlocks = 4, kVKeys = kTileK / kVBlocks;
 constexpr int kRingBytes = 81920;
 constexpr int kInfo = 8;
-constexpr int kMmaWarp = 4, kLoadWarp = 5, kThreads = 192;
+// Warps: 8 of the softmax (sub * 4 + quad: rows quad * 32 + sub * 16 to + 15), one
+// issuing products, one copying, one claiming.
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kClaimWarp = 10, kThreads = 352;
 constexpr int kTmemCols = 512, kOCol = 0;
 __device__ __forceinline__ constexpr uint32_t s_col(uint32_t b) { return 256 + b * 128; }
 #ifdef DSA_TEST_STALLED_COPY
@@ -61,9 +63,20 @@ struct Shape {
   static constexpr int kAtom = kVKeys * 128;           // bytes of one in a value block
 };
 
+struct Item {
+  int req, shard, half, split;
+  int tok0, n;                // the request's rows
+  int row0, rows;             // (row, head) pairs of the block: first of the request, how many
+  int base;                   // tokens before the request's n (may be negative)
+  int nall, nvis, nfree;      // local tokens: in the cache, seen by some row, by every row
+  int t0, t1;                 // key tiles
+  int bad;                    // a length below zero or past the table
+};
+
 struct alignas(1024) DecodeSmem {
   uint8_t q[kQBlocks][kQBlock];
   uint8_t ring[kRingBytes];
+  WorkSlots<Item> work;
   uint64_t full[10], empty[10], qfull, qempty, sfull[2], pfull[2], pvdone, vtail[2], info[kInfo], drain;
   uint32_t tail_seq[2];       // ring block of the values that vtail counts
   uint32_t pages[kInfo];      // valid pages of stream tile j, at j % kInfo: a bit per 16 keys
@@ -71,6 +84,8 @@ struct alignas(1024) DecodeSmem {
   int blocks;                 // row blocks of all requests
   int abort;
 };
+
+static_assert(sizeof(DecodeSmem) + 1024 <= 232448, "shared memory of a CTA");
 
 struct DecodeArgs {
   const int32_t* block_table; // [S][reqs][max_blocks]
@@ -84,20 +99,15 @@ struct DecodeArgs {
   int reqs, max_blocks, block, rows, H, words, splits;
   int cap;                    // local tokens that a table row names
   int kbox, vbox;             // keys of a copy
-  float c2;                   // scale * log2(e)
+  // |scale| log2(e), and the score product's descriptor bit that negates A for a
+  // negative scale.  A scale of 0 is taken as 2^-100: finite scores then count
+  // alike, masked ones are -inf as ever.
+  float c2;
+  uint32_t negate;
   ShardMath sm;
   FastDiv fblock, fH;
 };
 
-struct Item {
-  int req, shard, half, split;
-  int tok0, n;                // the request's rows
-  int row0, rows;             // (row, head) pairs of the block: first of the request, how many
-  int base;                   // tokens before the request's n (may be negative)
-  int nall, nvis, nfree;      // local tokens: in the cache, seen by some row, by every row
-  int t0, t1;                 // key tiles
-  bool bad;                   // a length below zero or past the table
-};
 struct Cursor {
   int req = 0, before = 0;
 };
@@ -181,19 +191,18 @@ struct PendingV {              // values of a stream tile whose keys are copied
 template <int CG>
 __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem& sm,
                                            const CUtensorMap* tm_q, const CUtensorMap* tm_k,
-                                           const CUtensorMap* tm_v, int blocks, int64_t items,
-                                           uint32_t rank) {
+                                           const CUtensorMap* tm_v, uint32_t rank) {
   using Sh = Shape<CG>;
   const int lane = threadIdx.x & 31;
   const bool leader = rank == 0;
-  Cursor cur;
+  Item it;
   uint32_t seq = 0, j = 0, loads = 0, tails = 0;
   bool ok = true, bad = false;
   // Waits for a ring block's space; its barrier then expects the pair's bytes
   // (or, values with a tail, an arrival alone: they are counted elsewhere).
   auto open_block = [&](bool bytes) {
     const uint32_t slot = seq % Sh::kRing, use = seq / Sh::kRing;
-    if (use > 0) ok = __all_sync(kFull, wait_or_abort(&sm.abort, &sm.empty[slot], (use - 1) & 1u));
+    if (use > 0) ok = warp_wait(&sm.abort, &sm.empty[slot], (use - 1) & 1u);
     if (ok && leader && lane == 0) {
       if (bytes) mbar_expect_tx(&sm.full[slot], (uint32_t)(CG * Sh::kBlock));
       else mbar_arrive1(&sm.full[slot]);
@@ -222,9 +231,9 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem& sm,
     }
   };
   PendingV p0{}, p1{};
-  for (int64_t i = blockIdx.x / CG; ok && i < items; i += gridDim.x / CG) {
-    const Item it = find_item<CG>(a, blocks, i, cur);
-    bad |= it.bad;
+  for (uint32_t n = 0; next_item(sm.work, &sm.abort, n, ok, it); ++n) {
+    item_done(sm.work, n);
+    bad |= it.bad != 0;
     const int32_t* table = a.block_table + ((int64_t)it.shard * a.reqs + it.req) * a.max_blocks;
     for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
       // Where this tile's keys are: lane l (of 8) has its keys 16 l to 16 l + 15.
@@ -240,10 +249,10 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem& sm,
         bad |= !in;
       }
       const unsigned valid = __ballot_sync(kFull, in) & 0xffu;
-      if (j >= 2) load_values(p0);
+      if (t < it.t1 - 2) load_values(p0);
       if (!ok) break;
       if (t == it.t1 - 1) {                  // the item's queries
-        if (loads > 0) ok = __all_sync(kFull, wait_or_abort(&sm.abort, &sm.qempty, (loads - 1) & 1u));
+        if (loads > 0) ok = warp_wait(&sm.abort, &sm.qempty, (loads - 1) & 1u);
         if (!ok) break;
         ++loads;
         auto boxes = [&](int r) { return (min(max(it.rows - r * kRows, 0), kRows) + kQBox - 1) / kQBox; };
@@ -272,9 +281,9 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem& sm,
       p0 = p1;
       p1 = PendingV{y, it.half, it.shard, has_tail(it, t)};
     }
+    if (ok && it.t1 - it.t0 >= 2) load_values(p0);
+    if (ok && it.t1 - it.t0 >= 1) load_values(p1);
   }
-  if (ok && j >= 2) load_values(p0);
-  if (ok && j >= 1) load_values(p1);
   if (__any_sync(kFull, bad) && lane == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);
   if (!ok && lane == 0) {
     if (!cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
@@ -290,75 +299,93 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem& sm,
   __syncwarp();
 }
 
-// ---- the products: one thread of the (first) CTA -------------------------------
+// ---- the products: a warp of the (first) CTA ------------------------------------
+// It runs along converged and one elected lane issues: inside a branch of one lane
+// the descriptors could not stay in uniform registers.
 template <int CG>
-__device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem& sm, uint32_t tmem,
-                                               int blocks, int64_t items) {
+__device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem& sm, uint32_t tmem) {
   using Sh = Shape<CG>;
-  constexpr uint32_t kIdS = idesc_f16(CG * kRows, kTileK, true, false);
-  constexpr uint32_t kIdO = idesc_f16(CG * kRows, kHalf, true, true);
-  const int lane = threadIdx.x & 31;
-  const uint32_t ring0 = smem_u32(sm.ring);
-  Cursor cur;
-  uint32_t seq = 0, j = 0, nq = 0;
+  const uint32_t id_s = idesc_f16(CG * kRows, kTileK, true, false) | a.negate;
+  constexpr uint32_t id_o = idesc_f16(CG * kRows, kHalf, true, true);
+  constexpr int kStep = Sh::kBlock >> 4;     // a block in a descriptor's address field
+  const uint64_t q0 = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
+  const uint64_t k0 = smem_desc_sw128(smem_u32(sm.ring), 16, 1024);
+  const uint64_t v0 = smem_desc_sw128(smem_u32(sm.ring), Sh::kAtom, 1024);
+  Item it;
+  uint32_t slot = 0, turn = 0, j = 0, nq = 0;   // the ring's next block and its barrier's parity
   bool ok = true;
   auto landed = [&]() {
-    ok = wait_or_abort(&sm.abort, &sm.full[seq % Sh::kRing], (seq / Sh::kRing) & 1u);
+    ok = ok && warp_wait(&sm.abort, &sm.full[slot], turn);
     tc_fence_after();
     return ok;
   };
+  auto next_block = [&]() {
+    if (++slot == Sh::kRing) {
+      slot = 0;
+      turn ^= 1u;
+    }
+  };
   // Values of stream tile v: `steps` of 16 keys, the item's first or not.
   auto values = [&](uint32_t v, int steps, bool first) {
-    ok = wait_or_abort(&sm.abort, &sm.pfull[v & 1u], (v >> 1) & 1u);
-    for (int b = 0; ok && b < kVBlocks; ++b, ++seq) {
+    ok = ok && warp_wait(&sm.abort, &sm.pfull[v & 1u], (v >> 1) & 1u);
+    const uint32_t p = tmem + s_col(v & 1u);
+#pragma unroll 1
+    for (int b = 0; ok && b < kVBlocks; ++b, next_block()) {
       if (!landed()) return;
-      const uint32_t blk = ring0 + (seq % Sh::kRing) * Sh::kBlock;
-      for (int s = 2 * b; s < min(steps, 2 * b + 2); ++s)
-        mma_ts<CG>(tmem + kOCol, tmem + s_col(v & 1u) + s * 8,
-                   smem_desc_sw128(blk + (s & 1) * 2048, Sh::kAtom, 1024), kIdO,
-                   (first && s == 0) ? 0u : 1u);
-      tc_commit<CG>(&sm.empty[seq % Sh::kRing]);
+      const uint64_t vd = v0 + slot * kStep;
+      if (elect_one()) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          if (2 * b + s < steps)
+            mma_ts<CG>(tmem + kOCol, p + (2 * b + s) * 8, vd + s * (2048 >> 4), id_o,
+                       (first && b == 0 && s == 0) ? 0u : 1u);
+        tc_commit<CG>(&sm.empty[slot]);
+        if (b == kVBlocks - 1) tc_commit<CG>(&sm.pvdone);
+      }
+      __syncwarp();
     }
-    if (ok) tc_commit<CG>(&sm.pvdone);
   };
   int steps0 = 0, steps1 = 0;
   bool first0 = false, first1 = false;
-  for (int64_t i = blockIdx.x / CG; i < items; i += gridDim.x / CG) {
-    const Item it = find_item<CG>(a, blocks, i, cur);
-    if (lane == 0 && ok) {
-      for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
-        if (j >= 2) values(j - 2, steps0, first0);
-        if (!ok) break;
-        if (t == it.t1 - 1) {
-          ok = wait_or_abort(&sm.abort, &sm.qfull, nq & 1u);
-          ++nq;
-        }
-        for (int b = 0; ok && b < kKBlocks; ++b, ++seq) {
-          if (!landed()) break;
-          const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[b]), 16, 1024);
-          const uint64_t kd = smem_desc_sw128(ring0 + (seq % Sh::kRing) * Sh::kBlock, 16, 1024);
+  for (uint32_t n = 0; next_item(sm.work, &sm.abort, n, ok, it); ++n) {
+    item_done(sm.work, n);
+    for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
+      if (t < it.t1 - 2) values(j - 2, steps0, first0);
+      if (t == it.t1 - 1) {
+        ok = ok && warp_wait(&sm.abort, &sm.qfull, nq & 1u);
+        ++nq;
+      }
+      const uint32_t d = tmem + s_col(j & 1u);
+#pragma unroll 1
+      for (int b = 0; ok && b < kKBlocks; ++b, next_block()) {
+        if (!landed()) break;
+        const uint64_t qd = q0 + b * (kQBlock >> 4), kd = k0 + slot * kStep;
+        if (elect_one()) {
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            mma_ss<CG>(tmem + s_col(j & 1u), qd + s * 2, kd + s * 2, kIdS, (b > 0 || s > 0) ? 1u : 0u);
-          tc_commit<CG>(&sm.empty[seq % Sh::kRing]);
+            mma_ss<CG>(d, qd + s * 2, kd + s * 2, id_s, (b > 0 || s > 0) ? 1u : 0u);
+          tc_commit<CG>(&sm.empty[slot]);
+          if (b == kKBlocks - 1) {
+            tc_commit<CG>(&sm.sfull[j & 1u]);
+            if (t == it.t0) tc_commit<CG>(&sm.qempty);
+          }
         }
-        if (!ok) break;
-        tc_commit<CG>(&sm.sfull[j & 1u]);
-        if (t == it.t0) tc_commit<CG>(&sm.qempty);
-        steps0 = steps1;
-        first0 = first1;
-        steps1 = value_steps(it, t);
-        first1 = t == it.t1 - 1;
+        __syncwarp();
       }
+      steps0 = steps1;
+      first0 = first1;
+      steps1 = value_steps(it, t);
+      first1 = t == it.t1 - 1;
     }
-    ok = __shfl_sync(kFull, (int)ok, 0) != 0;
-    if (!ok) break;
+    if (ok && it.t1 - it.t0 >= 2) values(j - 2, steps0, first0);
+    if (ok && it.t1 - it.t0 >= 1) values(j - 1, steps1, first1);
   }
-  if (lane == 0) {
-    if (ok && j >= 2) values(j - 2, steps0, first0);
-    if (ok && j >= 1) values(j - 1, steps1, first1);
-    if (!ok && !cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
-    // Every product issued completes before the tensor memory is freed.
+  const int lane = threadIdx.x & 31;
+  if (!ok && lane == 0 && !cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
+  __syncwarp();
+  // Every product issued completes before the tensor memory is freed (a commit
+  // counts the thread's own: elect_one picks the same lane every time).
+  if (elect_one()) {
     tc_commit<CG>(&sm.drain);
     if (!mbar_wait(&sm.drain, 0)) cta_abort(&sm.abort, a.flags);
   }
@@ -395,111 +422,154 @@ __device__ __forceinline__ uint32_t seen32(const DecodeArgs& a, const Item& it, 
 }
 
 // ---- softmax and outputs --------------------------------------------------------
+// A warp has 16 rows, four lanes a row and two rows a lane (tensor memory's
+// fragments).  Warps without a row of the item only keep step.
 template <int CG>
 __device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem& sm, uint32_t tmem,
-                                              int blocks, int64_t items, uint32_t rank) {
+                                              int warp, uint32_t rank) {
   using Sh = Shape<CG>;
-  const int lane = threadIdx.x & 31, quad = threadIdx.x >> 5;
-  const int r = quad * 32 + lane;
-  const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
-  // A negative scale takes the scores' negatives, 0 their products with it, so
-  // that a masked score is -inf under every scale.
-  const float sign = a.c2 < 0.f ? -1.f : 0.f, c2 = a.c2 == 0.f ? 1.f : fabsf(a.c2);
-  Cursor cur;
+  const int lane = threadIdx.x & 31;
+  const int sub = warp >> 2, quad = warp & 3;
+  const int r0 = quad * 32 + sub * 16;       // the warp's first row of the CTA's
+  const int br = (int)rank * kRows + r0 + (lane >> 2);   // the lane's rows of the block: br, br + 8
+  const int col = 2 * (lane & 3);            // its first of 8 columns
+  const uint32_t trow = tmem + ((uint32_t)r0 << 16), t_o = trow + kOCol;
+  // Over the four lanes of a row.
+  auto row_max = [](float v) {
+    v = fmaxf(v, __shfl_xor_sync(kFull, v, 1));
+    return fmaxf(v, __shfl_xor_sync(kFull, v, 2));
+  };
+  auto row_sum = [](float v) {
+    v += __shfl_xor_sync(kFull, v, 1);
+    return v + __shfl_xor_sync(kFull, v, 2);
+  };
   uint32_t j = 0, tails = 0;                 // tiles and tails so far
   bool ok = true;
-  for (int64_t i = blockIdx.x / CG; i < items; i += gridDim.x / CG) {
-    const Item it = find_item<CG>(a, blocks, i, cur);
-    const int row = it.row0 + (int)rank * kRows + r;   // of the request's n * H
-    const bool active = (int)rank * kRows + r < it.rows;
-    const int tok = active ? (int)fdiv((uint32_t)row, a.fH) : 0;
-    float m = -INFINITY, l = 0.f;
-    for (int t = it.t1 - 1; t >= it.t0; --t, ++j) {
+  for (uint32_t n = 0; next_item(sm.work, &sm.abort, n, ok); ++n) {
+    const Item& it = sm.work.item[n & 1u];   // read where it lies
+    const int t0 = uni(it.t0), t1 = uni(it.t1), nall = uni(it.nall), nfree = uni(it.nfree);
+    const bool mine = (int)rank * kRows + r0 < uni(it.rows);
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int t = t1 - 1; t >= t0; --t, ++j) {
       const uint32_t b = j & 1u;
-      ok = wait_or_abort(&sm.abort, &sm.sfull[b], (j >> 1) & 1u) &&
-           wait_or_abort(&sm.abort, &sm.info[j % kInfo], (j / kInfo) & 1u);
-      if (!__all_sync(kFull, ok)) {
-        ok = false;
-        break;
-      }
+      ok = warp_wait(&sm.abort, &sm.sfull[b], (j >> 1) & 1u) &&
+           warp_wait(&sm.abort, &sm.info[j % kInfo], (j / kInfo) & 1u);
+      if (!ok) break;
       tc_fence_after();
-      uint32_t x[kTileK];
-      tmem_load(trow + s_col(b), x);
-      const uint32_t pages = *reinterpret_cast<volatile uint32_t*>(&sm.pages[j % kInfo]);
-      tmem_wait_ld(x);
-      if (a.c2 <= 0.f) {
-        keep_branch();
-#pragma unroll
-        for (int k = 0; k < kTileK; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * sign);
-      }
-      if (pages != 0xffu || (t + 1) * kTileK > it.nfree) {
-        uint32_t seen[kTileK / 32];
-#pragma unroll
-        for (int c = 0; c < kTileK / 32; ++c) {
+      const uint32_t t_s = trow + s_col(b);
+      float alpha[2] = {1.f, 1.f};
+      if (mine) {
+        const uint32_t pages = *reinterpret_cast<volatile uint32_t*>(&sm.pages[j % kInfo]);
+        const bool masked = pages != 0xffu || (t + 1) * kTileK > nfree;
+        uint32_t seen[2] = {kFull, kFull};   // of keys 32 (lane % 4) on, by either row
+        if (masked) {
+          keep_branch();
+          const int c = lane & 3;
           const uint32_t pg = (pages >> (2 * c)) & 3u;
-          seen[c] = seen32(a, it, tok, t * kTileK + c * 32) &
-                    ((pg & 1u ? 0xffffu : 0u) | (pg & 2u ? 0xffff0000u : 0u));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int row = it.row0 + min(br + 8 * k, it.rows - 1);
+            seen[k] = seen32(a, it, (int)fdiv((uint32_t)row, a.fH), t * kTileK + c * 32) &
+                      ((pg & 1u ? 0xffffu : 0u) | (pg & 2u ? 0xffff0000u : 0u));
+          }
+        }
+        auto mask = [&](uint32_t (&x)[16], int c) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t w = __shfl_sync(kFull, seen[k], (lane & ~3) | c) >> col;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (!((w >> (8 * i)) & 1u)) x[4 * i + 2 * k] = 0xff800000u;
+              if (!((w >> (8 * i + 1)) & 1u)) x[4 * i + 2 * k + 1] = 0xff800000u;
+            }
+          }
+        };
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          uint32_t x[2][16];
+          tmem_load_frag(t_s + c * 32, x[0]);
+          tmem_load_frag(t_s + c * 32 + 32, x[1]);
+          tmem_wait_ld(x[0]);
+          tmem_wait_ld(x[1]);
+          if (masked) {
+            keep_branch();
+            mask(x[0], c);
+            mask(x[1], c + 1);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {      // the lane's rows
+            float v[2] = {top[k], -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                v[h] = fmax3(v[h], __uint_as_float(x[h][4 * i + 2 * k]),
+                             __uint_as_float(x[h][4 * i + 2 * k + 1]));
+            top[k] = fmaxf(v[0], v[1]);
+          }
+        }
+        float2 nref[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float mx = row_max(top[k]) * a.c2;
+          const float mn = mx > m[k] + kRescaleGap ? mx : m[k];   // m = -inf takes any finite maximum
+          alpha[k] = m[k] == -INFINITY ? 1.f : fast_exp2(m[k] - mn);
+          const float ref = mn == -INFINITY ? 0.f : mn;
+          nref[k] = make_float2(-ref, -ref);
+          m[k] = mn;
+          l[k] *= alpha[k];
+        }
+        const float2 c2v = make_float2(a.c2, a.c2);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t y[2][16];
+        tmem_load_frag(t_s, y[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t (&x)[16] = y[c & 1];
+          tmem_wait_ld(x);
+          if (c < 3) tmem_load_frag(t_s + (c + 1) * 32, y[(c + 1) & 1]);   // before weights overwrite it
+          if (masked) {
+            keep_branch();
+            mask(x, c);
+          }
+          uint32_t p[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 e = ffma2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                                   c2v, nref[i & 1]);
+            const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
+            p[i] = pack16<true>(e0, e1);
+            sum[i & 1] = fadd2(sum[i & 1], make_float2(e0, e1));
+          }
+          tmem_store_pairs(t_s + c * 16, p);
         }
 #pragma unroll
-        for (int k = 0; k < kTileK; ++k)
-          if (!((seen[k / 32] >> (k & 31)) & 1u)) x[k] = 0xff800000u;
+        for (int k = 0; k < 2; ++k) l[k] += sum[k].x + sum[k].y;
       }
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int k = 0; k < kTileK; k += 8)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          m4[v] = fmaxf(fmaxf(m4[v], __uint_as_float(x[k + 2 * v])), __uint_as_float(x[k + 2 * v + 1]));
-      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
-      const float mn = mx > m + kRescaleGap ? mx : m;   // m = -inf takes any finite maximum
-      const float alpha = m == -INFINITY ? 1.f : fast_exp2(m - mn);
-      const float ref = mn == -INFINITY ? 0.f : mn;
-      m = mn;
-      const float2 c2v = make_float2(c2, c2), nref = make_float2(-ref, -ref);
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int c = 0; c < kTileK; c += 32) {
-        uint32_t p[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float2 e = ffma2(make_float2(__uint_as_float(x[c + 2 * k]),
-                                             __uint_as_float(x[c + 2 * k + 1])), c2v, nref);
-          const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
-          p[k] = pack16<true>(e0, e1);
-          sum[k & 1] = fadd2(sum[k & 1], make_float2(e0, e1));
-        }
-        tmem_store(trow + s_col(b) + (uint32_t)(c / 2), p);
-      }
-      l = l * alpha + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
-      if (t < it.t1 - 1) {                   // the previous tile's values are in: O is at rest
-        ok = wait_or_abort(&sm.abort, &sm.pvdone, (j - 1) & 1u);
-        if (!__all_sync(kFull, ok)) {
-          ok = false;
-          break;
-        }
+      if (t < t1 - 1) {                      // the previous tile's values are in: O is at rest
+        ok = warp_wait(&sm.abort, &sm.pvdone, (j - 1) & 1u);
+        if (!ok) break;
         tc_fence_after();
-        if (__any_sync(kFull, alpha != 1.f)) {
+        if (__any_sync(kFull, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll 1
           for (int c = 0; c < kHalf; c += 32) {
-            uint32_t o[32];
-            tmem_load(trow + (uint32_t)(kOCol + c), o);
+            uint32_t o[16];
+            tmem_load_frag(t_o + (uint32_t)c, o);
             tmem_wait_ld(o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            tmem_store(trow + (uint32_t)(kOCol + c), o);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha[(k >> 1) & 1]);
+            tmem_store_frag(t_o + (uint32_t)c, o);
           }
         }
       }
       if (has_tail(it, t)) {                 // values behind the sequence's end: zeros
-        ok = wait_or_abort(&sm.abort, &sm.vtail[tails & 1u], (tails >> 1) & 1u);
-        if (!__all_sync(kFull, ok)) {
-          ok = false;
-          break;
-        }
+        ok = warp_wait(&sm.abort, &sm.vtail[tails & 1u], (tails >> 1) & 1u);
+        if (!ok) break;
         const uint32_t seq = *reinterpret_cast<volatile uint32_t*>(&sm.tail_seq[tails & 1u]);
         ++tails;
-        const int past = it.nall - t * kTileK, to = 16 * value_steps(it, t);
-        for (int z = r; z < (to - past) * Sh::kAtoms * 8; z += kRows) {
+        const int past = nall - t * kTileK, to = 16 * value_steps(it, t);
+        for (int z = warp * 32 + lane; z < (to - past) * Sh::kAtoms * 8; z += kSoftmaxWarps * 32) {
           const int key = past + z / (Sh::kAtoms * 8), chunk = z % (Sh::kAtoms * 8);
           uint8_t* blk = sm.ring + ((seq + (uint32_t)(key / kVKeys)) % Sh::kRing) * Sh::kBlock;
           *reinterpret_cast<uint4*>(blk + (chunk >> 3) * Sh::kAtom + (key % kVKeys) * 128 + (chunk & 7) * 16) =
@@ -515,51 +585,64 @@ __device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem& s
         else mbar_arrive_leader(&sm.pfull[b]);
       }
     }
-    const bool some = it.t1 > it.t0;
-    if (ok && some) ok = wait_or_abort(&sm.abort, &sm.pvdone, (j - 1) & 1u);
-    if (!__all_sync(kFull, ok)) {
-      ok = false;
-      break;
-    }
+    const bool some = t1 > t0, parts = a.splits > 1;
+    if (ok && some) ok = warp_wait(&sm.abort, &sm.pvdone, (j - 1) & 1u);
+    if (!ok) break;
     if (some) tc_fence_after();
-    const int64_t all = (int64_t)a.rows * a.H;
-    const int64_t to = it.shard * all + (int64_t)it.tok0 * a.H + row;   // [S][rows][H]
-    const int64_t part = (int64_t)it.split * a.sm.S * all + to;
-    if (active && it.half == 0) {
-      const float lse = l == 0.f ? -INFINITY : m + log2f(l);
-      if (a.splits > 1) a.part_l[part] = lse;
-      else a.lse2[to] = lse;
-    }
-    if (!some && a.splits > 1) continue;     // the merge does not read this part
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-    for (int c = 0; c < kHalf; c += 32) {
-      uint32_t o[32];
-      if (some) {
-        tmem_load(trow + (uint32_t)(kOCol + c), o);
-        tmem_wait_ld(o);
+    if (mine) {
+      const int64_t all = (int64_t)a.rows * a.H;
+      const int64_t to = ((int64_t)(parts ? it.split : 0) * a.sm.S + it.shard) * all +
+                         (int64_t)it.tok0 * a.H + it.row0 + br;   // [splits][S][rows][H]
+      bool active[2];
+      float inv[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        l[k] = row_sum(l[k]);
+        active[k] = br + 8 * k < it.rows;
+        inv[k] = l[k] == 0.f ? 0.f : 1.f / l[k];
+        if (active[k] && it.half == 0 && (lane & 3) == 0)
+          (parts ? a.part_l : a.lse2)[to + 8 * k] = l[k] == 0.f ? -INFINITY : m[k] + log2f(l[k]);
       }
+      if (some || !parts) {                  // the merge does not read an empty part
+        const int64_t at = to * kDv + it.half * kHalf;
+#pragma unroll 1
+        for (int c = 0; c < kHalf; c += 32) {
+          uint32_t o[16];
+          if (some) {
+            tmem_load_frag(t_o + (uint32_t)c, o);
+            tmem_wait_ld(o);
+          }
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        o[k] = some && l != 0.f ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
-      if (active && a.splits > 1) {
-        uint4* dst = reinterpret_cast<uint4*>(a.part_o + part * kDv + it.half * kHalf + c);
+          for (int i = 0; i < 16; ++i) {
+            const int k = (i >> 1) & 1;
+            o[i] = some && l[k] != 0.f ? __float_as_uint(__uint_as_float(o[i]) * inv[k]) : 0u;
+          }
 #pragma unroll
-        for (int v = 0; v < 8; ++v)
-          dst[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-      } else if (active) {
-        uint4* dst = reinterpret_cast<uint4*>(a.out + to * kDv + it.half * kHalf + c);
+          for (int k = 0; k < 2; ++k) {
+            if (parts) {
+              if (active[k]) {
+                float* dst = a.part_o + at + 8 * k * kDv + c + col;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          uint32_t w[4];
+                for (int i = 0; i < 4; ++i)
+                  *reinterpret_cast<uint2*>(dst + 8 * i) = make_uint2(o[4 * i + 2 * k], o[4 * i + 2 * k + 1]);
+              }
+            } else {
+              // Pairs of columns 8 i + 2 j in lane j: lane j is to have all of i = j.
+              uint32_t w[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w[k] = pack16<true>(__uint_as_float(o[8 * v + 2 * k]), __uint_as_float(o[8 * v + 2 * k + 1]));
-          dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int i = 0; i < 4; ++i)
+                w[i] = pack16<true>(__uint_as_float(o[4 * i + 2 * k]), __uint_as_float(o[4 * i + 2 * k + 1]));
+              transpose4(w, lane);
+              if (active[k])
+                *reinterpret_cast<uint4*>(a.out + at + 8 * k * kDv + c + 8 * (lane & 3)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          __syncwarp();                      // the next columns' load takes the whole warp
         }
       }
-      __syncwarp();                          // the next columns' load takes the whole warp
     }
+    item_done(sm.work, n);
   }
   if (!ok && lane == 0 && !cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
 }
@@ -571,11 +654,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ unsigned char decode_smem_raw[];
   DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>(
       (reinterpret_cast<uintptr_t>(decode_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = uni(tid >> 5);
   const uint32_t rank = CG == 2 ? pair_rank() : 0u;
   if (warp == kMmaWarp) {
     tmem_alloc<CG>(&sm.tmem, kTmemCols);
-  } else if (warp == kLoadWarp) {
+  } else if (warp == kClaimWarp) {
     // Row blocks of all requests; bad bounds are flagged once a call.
     int blocks = 0;
     bool bad = false;
@@ -597,12 +680,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.qempty, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.sfull[b], 1);
-      mbar_init(&sm.pfull[b], 4 * CG);       // a warp each, of both CTAs in a pair's first
+      mbar_init(&sm.pfull[b], kSoftmaxWarps * CG);   // a warp each, of both CTAs in a pair's first
       mbar_init(&sm.vtail[b], 1);
     }
     for (int b = 0; b < kInfo; ++b) mbar_init(&sm.info[b], 1);
     mbar_init(&sm.pvdone, 1);
     mbar_init(&sm.drain, 1);
+    init_slots(sm.work, CG, kSoftmaxWarps + 1 + (rank == 0 ? 1 : 0));
     sm.abort = 0;
     mbar_init_fence();
   }
@@ -610,12 +694,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if constexpr (CG == 2) pair_sync();        // the other CTA's barriers are there
   tc_fence_after();
-  const uint32_t tmem = sm.tmem;
-  const int blocks = sm.blocks;
-  const int64_t items = (int64_t)blocks * 2 * a.sm.S * a.splits;
-  if (warp == kLoadWarp) load_tiles<CG>(a, sm, &tm_q, &tm_k, &tm_v, blocks, items, rank);
-  else if (warp < kMmaWarp) softmax_tiles<CG>(a, sm, tmem, blocks, items, rank);
-  else if (rank == 0) issue_products<CG>(a, sm, tmem, blocks, items);
+  const uint32_t tmem = uni(sm.tmem);
+  if (warp == kLoadWarp) {
+    load_tiles<CG>(a, sm, &tm_q, &tm_k, &tm_v, rank);
+  } else if (warp < kSoftmaxWarps) {
+    softmax_tiles<CG>(a, sm, tmem, warp, rank);
+  } else if (warp == kClaimWarp) {
+    const int blocks = sm.blocks;
+    Cursor cur;
+    share_out<CG>(sm.work, &sm.abort, a.flags, (int64_t)blocks * 2 * a.sm.S * a.splits, rank,
+                  [&](int64_t i) { return find_item<CG>(a, blocks, i, cur); });
+  } else if (rank == 0) {
+    issue_products<CG>(a, sm, tmem);
+  }
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) pair_sync();        // neither CTA's memory goes while the other uses it
@@ -647,9 +738,8 @@ cudaError_t launch_decode(const CUtensorMap& q, const CUtensorMap& k, const CUte
   const auto kernel = mla_decode_kernel<CG>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  static DeviceCount pairs;
-  const int at_once = CG == 1 ? device_sms() : pairs.get(kernel, kThreads, kSmem);
-  const unsigned grid = (unsigned)(std::min<int64_t>(items, at_once) * CG);
+  // An item a cluster; those that do not start at once are mostly taken over.
+  const unsigned grid = (unsigned)(items * CG);
   return launch_kernel(kernel, dim3(grid), dim3(kThreads), (size_t)kSmem, stream, CG == 2 ? 2u : 0u,
                        q, k, v, a);
 }
@@ -692,7 +782,8 @@ extern "C" dsa_status dsa_mla_decode(const uint16_t* q, const uint16_t* kv_cache
   DecodeArgs a{block_table, query_starts, seq_lens, tree_mask, reinterpret_cast<__nv_bfloat16*>(out),
                lse2, nullptr, nullptr, err_flags, n_slots, reqs, max_blocks, block_size, rows, H,
                mask_words, p.splits, (int)cap, std::min(block_size, 64), std::min(block_size, kVKeys),
-               scale * kLog2e, ShardMath(S, I), FastDiv(block_size), FastDiv(H)};
+               scale == 0.f ? 0x1p-100f : fabsf(scale) * kLog2e, scale < 0.f ? kNegateA : 0u,
+               ShardMath(S, I), FastDiv(block_size), FastDiv(H)};
   if (p.splits > 1) {
     a.part_o = work;
     a.part_l = work + (int64_t)p.splits * S * pairs * kDv;
@@ -704,6 +795,7 @@ extern "C" dsa_status dsa_mla_decode(const uint16_t* q, const uint16_t* kv_cache
       !encode_map16(&tv, kv_cache, true, kDqk, n_slots, S, row, row * n_slots, a.vbox, 1))
     return DSA_ERR_CUDA;
   const int64_t items = (pairs / (p.cg * kRows) + reqs) * 2 * S * p.splits;   // at most
+  if (items * p.cg > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   const cudaError_t e = p.cg == 2 ? launch_decode<2>(tq, tk, tv, a, items, stream)
                                   : launch_decode<1>(tq, tk, tv, a, items, stream);
   if (e != cudaSuccess) return DSA_ERR_CUDA;

@@ -565,33 +565,4 @@ inline int device_sms() {
   return sms[dev];
 }
 
-// Pairs of CTAs of a kernel that a device runs at once (SM groups may be odd, so
-// that this may be less than half of its SMs); looked up once a device.
-struct DeviceCount {
-  static constexpr int kDevices = 64;
-  int count[kDevices] = {};
-  template <typename K>
-  int get(K kernel, int threads, int smem) {
-    int dev = 0;
-    const int half = device_sms() / 2;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return half;
-    if (count[dev] == 0) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3((unsigned)(half * 2));
-      cfg.blockDim = dim3((unsigned)threads);
-      cfg.dynamicSmemBytes = (size_t)smem;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = 2;
-      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      int n = 0;
-      const bool known = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
-      count[dev] = known ? (n < half ? n : half) : half;
-    }
-    return count[dev];
-  }
-};
-
 }  // namespace dsa
