@@ -9,21 +9,25 @@
 // tree mask names, or (no mask) those up to itself.
 //
 // All heads and rows of a request share its keys, so that (row, head) pairs are
-// the rows of one product: blocks of CG * 128 of them, CG CTAs with 128 each
-// (CG = 2: a pair of CTAs issues one product of M = 256 and either holds half of
-// the keys' tile, which halves what a CTA copies).  Outputs of 512 values would
-// fill tensor memory (512 columns): an item takes half of them, and its scores
-// are computed for both halves, 2304 + 1024 cycles of products a tile of 128 keys
-// where 2176 are the least (65 %).
-//  * tensor memory: half an output (256 columns), two score tiles (128 each; the
-//    weights as bf16 pairs in the first half of the same columns);
-//  * shared memory: the block's queries (144 KB) and a ring of 80 KB in blocks of
-//    16 KB / CG: a key tile's nine 64-value column blocks, the values' four
-//    blocks of 32 keys, in the order in which the products take them: keys of
-//    tile j + 2 behind values of tile j;
-//  * a warp copies (tensor maps, a box per page or 64 keys), one thread (of the
-//    pair's first CTA) issues, four warps run the softmax, a thread a row.
-// The keys may be split into parts that a second kernel joins.
+// the rows of one product.  An output of 512 values would fill tensor memory (512
+// columns), so an item takes half of it, and its scores are computed for both
+// halves: 2304 + 1024 cycles of products a tile of 128 keys where 2176 are the
+// least (65 %).  What the rows leave on chip decides how keys are held:
+//  * Pair, more than 128 rows a request: two CTAs with 128 rows each issue one
+//    product of M = 256, and either holds half of the keys' tile and of the values'
+//    columns.  All queries in shared memory (144 KB), two score tiles, and a ring of
+//    80 KB through which a tile's keys pass in three units, its values in two;
+//  * Wide, up to 128: the queries' first 256 dimensions in tensor memory and one
+//    score tile, which makes room for a whole key tile (144 KB), whose value blocks
+//    stay until their product (a pair's halves would read them twice);
+//  * Narrow, up to 32: a product still reads 128 rows of A, but those past 32 may be
+//    anything, here the blocks that follow: the queries take 36 KB, and two score
+//    tiles and two tiles' values fit.
+// The first 256 of an item's output columns, and the last, are its half's value
+// blocks; of a tile's nine 64-value blocks the scores take the other five first.
+// One warp claims items while the kernel runs, one copies (tensor maps, a box per
+// page or 64 keys), one issues products, eight run the softmax.  The keys may be
+// split into parts that a second kernel joins.
 // The tail of a sequence's last page holds anything: its values are zeroed in
 // shared memory up to the 16 keys that a product step reads, its scores masked.
 // Every wait is bounded and raises DSA_FLAG_TIMEOUT when it runs out.
@@ -35,17 +39,16 @@ namespace dsa {
 namespace {
 
 constexpr int kDqk = DSA_MLA_DQK, kDv = DSA_MLA_DV, kHalf = kDv / 2;
-constexpr int kRows = 128;                   // (row, head) pairs of a CTA
+constexpr int kRows = 128;                   // rows of a CTA's product
 constexpr int kTileK = 128;
-constexpr int kQBlocks = kDqk / 64, kQBlock = kRows * 128, kQBox = 32;
-constexpr int kKBlocks = kDqk / 64, kVBlocks = 4, kVKeys = kTileK / kVBlocks;
-constexpr int kRingBytes = 81920;
+constexpr int kBlocks = kDqk / 64;           // 9 blocks of 64 values
+constexpr int kVBlocks = 4, kABlocks = kBlocks - kVBlocks;   // of a half's values; the others
+constexpr int kQBox = 32;                    // rows of a copy of queries
 constexpr int kInfo = 8;
 // Warps: 8 of the softmax (sub * 4 + quad: rows quad * 32 + sub * 16 to + 15), one
 // issuing products, one copying, one claiming.
 constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kClaimWarp = 10, kThreads = 352;
-constexpr int kTmemCols = 512, kOCol = 0;
-__device__ __forceinline__ constexpr uint32_t s_col(uint32_t b) { return 256 + b * 128; }
+constexpr int kTmemCols = 512, kOCol = 0, kQCol = 384;
 #ifdef DSA_TEST_STALLED_COPY
 // The test-only build (never libdsa.so): the ring's first barrier expects one
 // arrival that nothing makes (its copy still lands).
@@ -54,14 +57,30 @@ constexpr uint32_t kStalledArrivals = 1;
 constexpr uint32_t kStalledArrivals = 0;
 #endif
 
-template <int CG>
+enum Mode { kNarrow = 0, kWide = 1, kPair = 2 };
+template <int M>
 struct Shape {
-  static constexpr int kBlock = 16384 / CG;            // bytes of a ring block
-  static constexpr int kRing = kRingBytes / kBlock;    // 5 or 10
-  static constexpr int kKeys = kTileK / CG;            // keys of a tile that a CTA holds
-  static constexpr int kAtoms = kHalf / CG / 64;       // 64-value columns of its values
-  static constexpr int kAtom = kVKeys * 128;           // bytes of one in a value block
+  static constexpr int CG = M == kPair ? 2 : 1;
+  static constexpr int kQRows = M == kNarrow ? 32 : kRows;     // rows of queries that a CTA holds
+  static constexpr int kItemRows = CG * kQRows;
+  static constexpr int kQTm = M == kWide ? 4 : 0;              // query blocks in tensor memory,
+  static constexpr int kQBlock = kQRows * 128;                 // the others in shared memory
+  static constexpr int kQBytes = (kBlocks - kQTm) * kQBlock;
+  static constexpr int kScores = M == kWide ? 1 : 2;           // score tiles
+  static constexpr int kBlock = 16384 / CG;                    // bytes of a key block
+  // Narrow, Wide: blocks that only scores read, tiles of values.
+  static constexpr int kA = M == kNarrow ? 3 : 5, kV = M == kNarrow ? 2 : 1;
+  // Pair: the ring's blocks, keys of a tile that a CTA holds, 64-value columns of
+  // its values, keys of a value block and bytes of a column in it.
+  static constexpr int kRing = 10, kKeys = kTileK / CG, kAtoms = kVBlocks / CG, kVKeys = 32;
+  static constexpr int kAtom = kVKeys * 128;
+  static constexpr int kKvBytes = M == kPair ? kRing * kBlock : (kA + kVBlocks * kV) * kBlock;
+  __device__ static constexpr uint32_t s_col(uint32_t b) { return 256 + b * 128; }
 };
+constexpr int kFullBars = 13, kEmptyBars = 8;   // barriers of key blocks (units)
+constexpr int kV0Full = 5, kV0Empty = 5;     // Narrow, Wide: the first of the values'
+// Pair: blocks of a unit of the ring.
+constexpr uint32_t kKUnit = 3, kVUnit = 2;
 
 struct Item {
   int req, shard, half, split;
@@ -73,21 +92,27 @@ struct Item {
   int bad;                    // a length below zero or past the table
 };
 
+template <int M>
 struct alignas(1024) DecodeSmem {
-  uint8_t q[kQBlocks][kQBlock];
-  uint8_t ring[kRingBytes];
+  uint8_t q[Shape<M>::kQBytes];
+  uint8_t kv[Shape<M>::kKvBytes];            // Narrow, Wide: values of tiles first
   WorkSlots<Item> work;
-  uint64_t full[10], empty[10], qfull, qempty, sfull[2], pfull[2], pvdone, vtail[2], info[kInfo], drain;
-  uint32_t tail_seq[2];       // ring block of the values that vtail counts
+  uint64_t full[kFullBars], empty[kEmptyBars], qfull, qtm, qempty, sfull[2], pfull[2], pvdone, vtail[2],
+      info[kInfo], drain;
+  uint32_t tail_seq[2];       // Pair: ring block of the values that vtail counts
   uint32_t pages[kInfo];      // valid pages of stream tile j, at j % kInfo: a bit per 16 keys
   uint32_t tmem;
   int blocks;                 // row blocks of all requests
   int abort;
 };
-
-static_assert(sizeof(DecodeSmem) + 1024 <= 232448, "shared memory of a CTA");
+static_assert(sizeof(DecodeSmem<kNarrow>) + 1024 <= 232448 && sizeof(DecodeSmem<kWide>) + 1024 <= 232448 &&
+                  sizeof(DecodeSmem<kPair>) + 1024 <= 232448,
+              "shared memory of a CTA");
+static_assert(8 * Shape<kNarrow>::kQBlock + kRows * 128 <= Shape<kNarrow>::kQBytes + Shape<kNarrow>::kKvBytes,
+              "rows past the queries lie in this CTA's memory");
 
 struct DecodeArgs {
+  const __nv_bfloat16* q;     // [rows][H][kDqk]
   const int32_t* block_table; // [S][reqs][max_blocks]
   const int32_t *starts, *lens;
   const int32_t* mask;        // [rows][words] or null
@@ -119,8 +144,9 @@ __device__ __forceinline__ void rows_of(const DecodeArgs& a, int i, int& first, 
 
 // Warp-wide: item `index` of blocks * 2 * S * splits: halves and row blocks of a
 // request, which read the same keys, beside one another.
-template <int CG>
+template <int M>
 __device__ __forceinline__ Item find_item(const DecodeArgs& a, int blocks, int64_t index, Cursor& c) {
+  constexpr int kItemRows = Shape<M>::kItemRows;
   const int lane = threadIdx.x & 31;
   Item it;
   it.half = (int)(index & 1);
@@ -134,7 +160,7 @@ __device__ __forceinline__ Item find_item(const DecodeArgs& a, int blocks, int64
     const int i = at + lane;
     int first = 0, end = 0;
     if (i < a.reqs) rows_of(a, i, first, end);
-    const int mine = ((end - first) * a.H + CG * kRows - 1) / (CG * kRows);
+    const int mine = ((end - first) * a.H + kItemRows - 1) / kItemRows;
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -156,8 +182,8 @@ __device__ __forceinline__ Item find_item(const DecodeArgs& a, int blocks, int64
   int end;
   rows_of(a, it.req, it.tok0, end);
   it.n = end - it.tok0;
-  it.row0 = local * CG * kRows;
-  it.rows = min(CG * kRows, it.n * a.H - it.row0);
+  it.row0 = local * kItemRows;
+  it.rows = min(kItemRows, it.n * a.H - it.row0);
   const int len = max(__ldg(a.lens + it.req), 0);
   it.base = len - it.n;
   const int lo = (int)fdiv((uint32_t)it.row0, a.fH);
@@ -181,120 +207,182 @@ __device__ __forceinline__ int value_steps(const Item& it, int t) {
 __device__ __forceinline__ bool has_tail(const Item& it, int t) {
   return it.nall - t * kTileK < 16 * value_steps(it, t);
 }
+// The i-th block that an item's scores take first, of the nine; its i-th value block.
+__device__ __forceinline__ int block_a(int half, int i) {
+  return half == 0 ? kVBlocks + i : (i < kVBlocks ? i : kBlocks - 1);
+}
+__device__ __forceinline__ int block_v(int half, int i) { return half * kVBlocks + i; }
 
 // ---- the copies ---------------------------------------------------------------
+// A tile's keys 16 l to 16 l + 15 lie in a page: lane l (of 8, repeated) has the
+// page's table entry, then the cache row of the first of them.
+template <int M>
+__device__ __forceinline__ int table_entry(const DecodeArgs& a, const Item& it, int t) {
+  const int key = t * kTileK + (int)(threadIdx.x & 7) * 16;
+  if (t < it.t0 || key >= it.nall) return -1;
+  return __ldg(a.block_table + ((int64_t)it.shard * a.reqs + it.req) * a.max_blocks +
+               fdiv((uint32_t)key, a.fblock));
+}
+
+// Ring of the pair: units are freed in the order in which they were copied.
+struct Ring {
+  uint32_t unit = 0, oldest = 0;             // the next unit; the oldest not known to be free
+  uint32_t end = 0, freed = 0;               // blocks copied and freed so far
+  uint32_t values = 0;                       // bit i: unit oldest + i is one of values
+};
+
 struct PendingV {              // values of a stream tile whose keys are copied
-  int y, half, shard;          // lane i: row of the cache of its keys 16 i
+  int y, half, shard;          // lane l: row of the cache of its keys 16 l
   bool tail;
 };
 
-template <int CG>
-__device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem& sm,
+template <int M>
+__device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& sm,
                                            const CUtensorMap* tm_q, const CUtensorMap* tm_k,
                                            const CUtensorMap* tm_v, uint32_t rank) {
-  using Sh = Shape<CG>;
+  using Sh = Shape<M>;
+  constexpr int CG = Sh::CG;
   const int lane = threadIdx.x & 31;
   const bool leader = rank == 0;
   Item it;
-  uint32_t seq = 0, j = 0, loads = 0, tails = 0;
+  uint32_t j = 0, loads = 0, tails = 0, na = 0;   // tiles, items' queries, tails, score blocks so far
   bool ok = true, bad = false;
-  // Waits for a ring block's space; its barrier then expects the pair's bytes
-  // (or, values with a tail, an arrival alone: they are counted elsewhere).
-  auto open_block = [&](bool bytes) {
-    const uint32_t slot = seq % Sh::kRing, use = seq / Sh::kRing;
-    if (use > 0) ok = warp_wait(&sm.abort, &sm.empty[slot], (use - 1) & 1u);
+  Ring ring;
+  PendingV p0{}, p1{};
+  // Pair: waits for a unit's space; its barrier then expects the pair's bytes (or,
+  // values with a tail, an arrival alone: they are counted elsewhere).
+  auto open_unit = [&](uint32_t blocks, bool bytes) {
+    while (ok && ring.end + blocks - ring.freed > Sh::kRing) {
+      ok = warp_wait(&sm.abort, &sm.empty[ring.oldest % kEmptyBars], (ring.oldest / kEmptyBars) & 1u);
+      ring.freed += ring.values & 1u ? kVUnit : kKUnit;
+      ring.values >>= 1;
+      ++ring.oldest;
+    }
     if (ok && leader && lane == 0) {
-      if (bytes) mbar_expect_tx(&sm.full[slot], (uint32_t)(CG * Sh::kBlock));
-      else mbar_arrive1(&sm.full[slot]);
+      uint64_t* bar = &sm.full[ring.unit % kEmptyBars];
+      if (bytes) mbar_expect_tx(bar, (uint32_t)CG * blocks * Sh::kBlock);
+      else mbar_arrive1(bar);
     }
     return ok;
+  };
+  auto close_unit = [&](uint32_t blocks, bool is_values) {
+    ring.values |= (is_values ? 1u : 0u) << (ring.unit - ring.oldest);
+    ++ring.unit;
+    ring.end += blocks;
   };
   auto load_values = [&](const PendingV& p) {
     uint64_t* vtail = &sm.vtail[tails & 1u];
     if (p.tail && lane == 0) {
-      sm.tail_seq[tails & 1u] = seq;         // published by the barrier
+      sm.tail_seq[tails & 1u] = ring.end;    // published by the barrier
       mbar_expect_tx(vtail, (uint32_t)(kVBlocks * Sh::kBlock));
     }
     tails += p.tail;
-    for (int b = 0; b < kVBlocks; ++b, ++seq) {
-      if (!open_block(!p.tail)) return;
-      const uint32_t slot = seq % Sh::kRing;
-      uint8_t* dst = sm.ring + slot * Sh::kBlock;
-      const uint32_t bar = p.tail ? smem_u32(vtail)
-                                  : (CG == 1 ? smem_u32(&sm.full[slot]) : leader_addr(&sm.full[slot]));
-      for (int k = 0; k < kVKeys; k += a.vbox) {
-        const int y = __shfl_sync(kFull, p.y, (b * kVKeys + k) >> 4);
-        if (lane < Sh::kAtoms)
-          load_box<CG>(dst + lane * Sh::kAtom + k * 128, tm_v,
-                       p.half * kHalf + ((int)rank * Sh::kAtoms + lane) * 64, y, p.shard, bar);
-      }
+    const int boxes = Sh::kVKeys / a.vbox, per = Sh::kAtoms * boxes;   // of a block
+    for (uint32_t b = 0; b < kVBlocks; b += kVUnit) {
+      if (!open_unit(kVUnit, !p.tail)) return;
+      const uint32_t bar = p.tail ? smem_u32(vtail) : leader_addr(&sm.full[ring.unit % kEmptyBars]);
+      const int i = lane / per, atom = lane % per / boxes, key = lane % boxes * a.vbox;
+      const int y = __shfl_sync(kFull, p.y, (((int)b + i) * Sh::kVKeys + key) >> 4 & 7);
+      if (i < (int)kVUnit)
+        load_box<CG>(sm.kv + (ring.end + i) % Sh::kRing * Sh::kBlock + atom * Sh::kAtom + key * 128, tm_v,
+                     p.half * kHalf + ((int)rank * Sh::kAtoms + atom) * 64, y, p.shard, bar);
+      close_unit(kVUnit, true);
     }
   };
-  PendingV p0{}, p1{};
   for (uint32_t n = 0; next_item(sm.work, &sm.abort, n, ok, it); ++n) {
     item_done(sm.work, n);
     bad |= it.bad != 0;
-    const int32_t* table = a.block_table + ((int64_t)it.shard * a.reqs + it.req) * a.max_blocks;
+    int next = table_entry<M>(a, it, it.t1 - 1);
     for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
-      // Where this tile's keys are: lane l (of 8) has its keys 16 l to 16 l + 15.
-      const int key = t * kTileK + (lane & 7) * 16;
+      const int key = t * kTileK + (lane & 7) * 16, entry = next;
+      next = table_entry<M>(a, it, t - 1);   // on its way while this tile is copied
       int y = (int)a.n_slots;                // outside: reads as zero
       bool in = false;
       if (key < it.nall) {
         uint32_t off;
-        const uint32_t col = fdivmod((uint32_t)key, a.fblock, &off);
-        const int64_t at = (int64_t)__ldg(table + col) * a.block + off;
+        fdivmod((uint32_t)key, a.fblock, &off);
+        const int64_t at = (int64_t)entry * a.block + off;
         in = at >= 0 && at + 16 <= a.n_slots;
         if (in) y = (int)at;
         bad |= !in;
       }
       const unsigned valid = __ballot_sync(kFull, in) & 0xffu;
-      if (t < it.t1 - 2) load_values(p0);
+      if (M == kPair && t < it.t1 - 2) load_values(p0);
       if (!ok) break;
       if (t == it.t1 - 1) {                  // the item's queries
         if (loads > 0) ok = warp_wait(&sm.abort, &sm.qempty, (loads - 1) & 1u);
         if (!ok) break;
         ++loads;
-        auto boxes = [&](int r) { return (min(max(it.rows - r * kRows, 0), kRows) + kQBox - 1) / kQBox; };
-        const int mine = boxes((int)rank);
+        constexpr int kN = kBlocks - Sh::kQTm;
+        auto boxes = [&](int r) {
+          return (min(max(it.rows - r * kRows, 0), Sh::kQRows) + kQBox - 1) / kQBox;
+        };
         if (leader && lane == 0)
-          mbar_expect_tx(&sm.qfull, (uint32_t)((boxes(0) + (CG == 2 ? boxes(1) : 0)) * kQBlocks * kQBox * 128));
+          mbar_expect_tx(&sm.qfull, (uint32_t)((boxes(0) + (CG == 2 ? boxes(1) : 0)) * kN * kQBox * 128));
         const uint32_t bar = CG == 1 ? smem_u32(&sm.qfull) : leader_addr(&sm.qfull);
-        if (lane < kQBlocks)
-          for (int b = 0; b < mine; ++b)
-            load_box<CG>(sm.q[lane] + b * kQBox * 128, tm_q, lane * 64,
+        if (lane < kN)
+          for (int b = 0; b < boxes((int)rank); ++b)
+            load_box<CG>(sm.q + lane * Sh::kQBlock + b * kQBox * 128, tm_q, (Sh::kQTm + lane) * 64,
                          it.tok0 * a.H + it.row0 + (int)rank * kRows + b * kQBox, 0, bar);
       }
       if (lane == 0) {
         sm.pages[j % kInfo] = valid;
         mbar_arrive1(&sm.info[j % kInfo]);
       }
-      for (int b = 0; b < kKBlocks; ++b, ++seq) {
-        if (!open_block(true)) break;
-        const uint32_t slot = seq % Sh::kRing;
-        const uint32_t bar = CG == 1 ? smem_u32(&sm.full[slot]) : leader_addr(&sm.full[slot]);
-        const int boxes = Sh::kKeys / a.kbox, first = (int)rank * Sh::kKeys;
-        const int yk = __shfl_sync(kFull, y, ((first + (lane < boxes ? lane : 0) * a.kbox) >> 4) & 7);
-        if (lane < boxes)
-          load_box<CG>(sm.ring + slot * Sh::kBlock + lane * a.kbox * 128, tm_k, b * 64, yk, it.shard, bar);
+      const int boxes = Sh::kKeys / a.kbox;  // of a block: 1 to 8
+      const int i = lane / boxes, first = (int)rank * Sh::kKeys + lane % boxes * a.kbox;
+      const int yk = __shfl_sync(kFull, y, first >> 4 & 7);
+      if constexpr (M == kPair) {
+        for (uint32_t b = 0; b < kBlocks; b += kKUnit) {
+          if (!open_unit(kKUnit, true)) break;
+          const uint32_t bar = leader_addr(&sm.full[ring.unit % kEmptyBars]);
+          if (i < (int)kKUnit)
+            load_box<CG>(sm.kv + (ring.end + i) % Sh::kRing * Sh::kBlock + lane % boxes * a.kbox * 128, tm_k,
+                         ((int)b + i) * 64, yk, it.shard, bar);
+          close_unit(kKUnit, false);
+        }
+        p0 = p1;
+        p1 = PendingV{y, it.half, it.shard, has_tail(it, t)};
+      } else {
+        for (int b = 0; ok && b < kABlocks; ++b, ++na) {
+          const uint32_t slot = na % Sh::kA, use = na / Sh::kA;
+          if (use > 0) ok = warp_wait(&sm.abort, &sm.empty[slot], (use - 1) & 1u);
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(&sm.full[slot], Sh::kBlock);
+          if (lane < boxes)
+            load_box<CG>(sm.kv + (Sh::kV * kVBlocks + slot) * Sh::kBlock + first * 128, tm_k,
+                         block_a(it.half, b) * 64, yk, it.shard, smem_u32(&sm.full[slot]));
+        }
+        const uint32_t vb = j % Sh::kV, use = j / Sh::kV;
+        if (ok && use > 0) ok = warp_wait(&sm.abort, &sm.empty[kV0Empty + vb], (use - 1) & 1u);
+        if (!ok) break;
+        uint64_t* bar = &sm.full[kV0Full + vb * kVBlocks];
+        if (lane < kVBlocks) mbar_expect_tx(bar + lane, Sh::kBlock);
+        if (i < kVBlocks)
+          load_box<CG>(sm.kv + (vb * kVBlocks + i) * Sh::kBlock + first * 128, tm_k,
+                       block_v(it.half, i) * 64, yk, it.shard, smem_u32(bar + i));
       }
-      p0 = p1;
-      p1 = PendingV{y, it.half, it.shard, has_tail(it, t)};
     }
-    if (ok && it.t1 - it.t0 >= 2) load_values(p0);
-    if (ok && it.t1 - it.t0 >= 1) load_values(p1);
+    if (M == kPair && ok && it.t1 - it.t0 >= 2) load_values(p0);
+    if (M == kPair && ok && it.t1 - it.t0 >= 1) load_values(p1);
   }
   if (__any_sync(kFull, bad) && lane == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);
   if (!ok && lane == 0) {
     if (!cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
     // The copies issued land before the CTA ends (a pair's first CTA counts both's).
-    if (leader) {
-      if (loads > 0) mbar_wait(&sm.qfull, (loads - 1) & 1u);
-      for (uint32_t b = seq > Sh::kRing ? seq - Sh::kRing : 0; b < seq; ++b)
-        mbar_wait(&sm.full[b % Sh::kRing], (b / Sh::kRing) & 1u);
+    if (leader && loads > 0) mbar_wait(&sm.qfull, (loads - 1) & 1u);
+    if constexpr (M == kPair) {
+      for (uint32_t u = ring.oldest; leader && u < ring.unit; ++u)
+        mbar_wait(&sm.full[u % kEmptyBars], (u / kEmptyBars) & 1u);
+      for (uint32_t k = tails > 2 ? tails - 2 : 0; k < tails; ++k)
+        mbar_wait(&sm.vtail[k & 1u], (k >> 1) & 1u);
+    } else {
+      for (uint32_t b = na > Sh::kA ? na - Sh::kA : 0; b < na; ++b)
+        mbar_wait(&sm.full[b % Sh::kA], (b / Sh::kA) & 1u);
+      for (uint32_t v = j > Sh::kV ? j - Sh::kV : 0; v < j; ++v)
+        for (int i = 0; i < kVBlocks; ++i)
+          mbar_wait(&sm.full[kV0Full + v % Sh::kV * kVBlocks + i], (v / Sh::kV) & 1u);
     }
-    for (uint32_t k = tails > 2 ? tails - 2 : 0; k < tails; ++k)
-      mbar_wait(&sm.vtail[k & 1u], (k >> 1) & 1u);
   }
   __syncwarp();
 }
@@ -302,83 +390,134 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem& sm,
 // ---- the products: a warp of the (first) CTA ------------------------------------
 // It runs along converged and one elected lane issues: inside a branch of one lane
 // the descriptors could not stay in uniform registers.
-template <int CG>
-__device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem& sm, uint32_t tmem) {
-  using Sh = Shape<CG>;
+template <int M>
+__device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem<M>& sm, uint32_t tmem) {
+  using Sh = Shape<M>;
+  constexpr int CG = Sh::CG;
   const uint32_t id_s = idesc_f16(CG * kRows, kTileK, true, false) | a.negate;
   constexpr uint32_t id_o = idesc_f16(CG * kRows, kHalf, true, true);
   constexpr int kStep = Sh::kBlock >> 4;     // a block in a descriptor's address field
-  const uint64_t q0 = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
-  const uint64_t k0 = smem_desc_sw128(smem_u32(sm.ring), 16, 1024);
-  const uint64_t v0 = smem_desc_sw128(smem_u32(sm.ring), Sh::kAtom, 1024);
+  const uint64_t q0 = smem_desc_sw128(smem_u32(sm.q), 16, 1024);
+  const uint64_t k0 = smem_desc_sw128(smem_u32(sm.kv), 16, 1024);
+  const uint64_t v0 = smem_desc_sw128(smem_u32(sm.kv), M == kPair ? Sh::kAtom : Sh::kBlock, 1024);
   Item it;
-  uint32_t slot = 0, turn = 0, j = 0, nq = 0;   // the ring's next block and its barrier's parity
+  uint32_t j = 0, nq = 0, na = 0;            // tiles, items' queries, score blocks so far
+  uint32_t unit = 0, blk = 0;                // Pair: the ring's next unit and block
   bool ok = true;
-  auto landed = [&]() {
-    ok = ok && warp_wait(&sm.abort, &sm.full[slot], turn);
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    ok = ok && warp_wait(&sm.abort, bar, parity);
     tc_fence_after();
     return ok;
   };
-  auto next_block = [&]() {
-    if (++slot == Sh::kRing) {
-      slot = 0;
-      turn ^= 1u;
+  // Scores with block kb, whose keys' descriptor is kd.
+  auto block_products = [&](uint32_t d, int kb, uint64_t kd, bool first) {
+    if (kb < Sh::kQTm) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        mma_ts<CG>(d, tmem + kQCol + kb * 32 + s * 8, kd + s * 2, id_s, (first && s == 0) ? 0u : 1u);
+    } else {
+      const uint64_t qd = q0 + (uint32_t)(kb - Sh::kQTm) * (Sh::kQBlock >> 4);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        mma_ss<CG>(d, qd + s * 2, kd + s * 2, id_s, (first && s == 0) ? 0u : 1u);
     }
   };
   // Values of stream tile v: `steps` of 16 keys, the item's first or not.
   auto values = [&](uint32_t v, int steps, bool first) {
-    ok = ok && warp_wait(&sm.abort, &sm.pfull[v & 1u], (v >> 1) & 1u);
-    const uint32_t p = tmem + s_col(v & 1u);
+    const uint32_t b = v % Sh::kScores, p = tmem + Sh::s_col(b);
+    if (!wait(&sm.pfull[b], (v / Sh::kScores) & 1u)) return;
+    if constexpr (M == kPair) {
 #pragma unroll 1
-    for (int b = 0; ok && b < kVBlocks; ++b, next_block()) {
-      if (!landed()) return;
-      const uint64_t vd = v0 + slot * kStep;
+      for (uint32_t u = 0; u < kVBlocks / kVUnit; ++u, ++unit, blk = (blk + kVUnit) % Sh::kRing) {
+        if (!wait(&sm.full[unit % kEmptyBars], (unit / kEmptyBars) & 1u)) return;
+        if (elect_one()) {
+#pragma unroll
+          for (uint32_t c = 0; c < kVUnit; ++c) {
+            const uint64_t vd = v0 + (blk + c) % Sh::kRing * kStep;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              const int step = (int)(u * kVUnit + c) * 2 + s;
+              if (step < steps)
+                mma_ts<CG>(tmem + kOCol, p + step * 8, vd + s * (2048 >> 4), id_o,
+                           (first && step == 0) ? 0u : 1u);
+            }
+          }
+          tc_commit<CG>(&sm.empty[unit % kEmptyBars]);
+          if (u == kVBlocks / kVUnit - 1) tc_commit<CG>(&sm.pvdone);
+        }
+        __syncwarp();
+      }
+    } else {
+      const uint64_t vd = v0 + v % Sh::kV * (kVBlocks * kStep);
       if (elect_one()) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-          if (2 * b + s < steps)
-            mma_ts<CG>(tmem + kOCol, p + (2 * b + s) * 8, vd + s * (2048 >> 4), id_o,
-                       (first && b == 0 && s == 0) ? 0u : 1u);
-        tc_commit<CG>(&sm.empty[slot]);
-        if (b == kVBlocks - 1) tc_commit<CG>(&sm.pvdone);
+        for (int s = 0; s < 8; ++s)
+          if (s < steps)
+            mma_ts<CG>(tmem + kOCol, p + s * 8, vd + s * (2048 >> 4), id_o, (first && s == 0) ? 0u : 1u);
+        tc_commit<CG>(&sm.empty[kV0Empty + v % Sh::kV]);
+        tc_commit<CG>(&sm.pvdone);
       }
       __syncwarp();
     }
   };
-  int steps0 = 0, steps1 = 0;
-  bool first0 = false, first1 = false;
   for (uint32_t n = 0; next_item(sm.work, &sm.abort, n, ok, it); ++n) {
     item_done(sm.work, n);
     for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
-      if (t < it.t1 - 2) values(j - 2, steps0, first0);
-      if (t == it.t1 - 1) {
-        ok = ok && warp_wait(&sm.abort, &sm.qfull, nq & 1u);
+      if (M == kPair && t < it.t1 - 2) values(j - 2, value_steps(it, t + 2), t + 2 == it.t1 - 1);
+      if (ok && t == it.t1 - 1) {
+        if (!wait(&sm.qfull, nq & 1u)) break;
+        if (Sh::kQTm > 0 && !wait(&sm.qtm, nq & 1u)) break;
         ++nq;
       }
-      const uint32_t d = tmem + s_col(j & 1u);
+      const uint32_t b = j % Sh::kScores, d = tmem + Sh::s_col(b);
+      auto scores_done = [&]() {
+        tc_commit<CG>(&sm.sfull[b]);
+        if (t == it.t0) tc_commit<CG>(&sm.qempty);
+      };
+      if constexpr (M == kPair) {
 #pragma unroll 1
-      for (int b = 0; ok && b < kKBlocks; ++b, next_block()) {
-        if (!landed()) break;
-        const uint64_t qd = q0 + b * (kQBlock >> 4), kd = k0 + slot * kStep;
-        if (elect_one()) {
+        for (uint32_t u = 0; ok && u < kBlocks / kKUnit; ++u, ++unit, blk = (blk + kKUnit) % Sh::kRing) {
+          if (!wait(&sm.full[unit % kEmptyBars], (unit / kEmptyBars) & 1u)) break;
+          if (elect_one()) {
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
-            mma_ss<CG>(d, qd + s * 2, kd + s * 2, id_s, (b > 0 || s > 0) ? 1u : 0u);
-          tc_commit<CG>(&sm.empty[slot]);
-          if (b == kKBlocks - 1) {
-            tc_commit<CG>(&sm.sfull[j & 1u]);
-            if (t == it.t0) tc_commit<CG>(&sm.qempty);
+            for (uint32_t c = 0; c < kKUnit; ++c)
+              block_products(d, (int)(u * kKUnit + c), k0 + (blk + c) % Sh::kRing * kStep, u == 0 && c == 0);
+            tc_commit<CG>(&sm.empty[unit % kEmptyBars]);
+            if (u == kBlocks / kKUnit - 1) scores_done();
           }
+          __syncwarp();
         }
-        __syncwarp();
+      } else {
+#pragma unroll 1
+        for (int i = 0; ok && i < kABlocks; ++i, ++na) {
+          const uint32_t slot = na % Sh::kA;
+          if (!wait(&sm.full[slot], (na / Sh::kA) & 1u)) break;
+          if (elect_one()) {
+            block_products(d, block_a(it.half, i), k0 + (Sh::kV * kVBlocks + slot) * kStep, i == 0);
+            tc_commit<CG>(&sm.empty[slot]);
+          }
+          __syncwarp();
+        }
+        const uint32_t vb = j % Sh::kV;
+#pragma unroll 1
+        for (int i = 0; ok && i < kVBlocks; ++i) {
+          if (!wait(&sm.full[kV0Full + vb * kVBlocks + i], (j / Sh::kV) & 1u)) break;
+          if (elect_one()) {
+            block_products(d, block_v(it.half, i), k0 + (vb * kVBlocks + i) * kStep, false);
+            if (i == kVBlocks - 1) scores_done();
+          }
+          __syncwarp();
+        }
+        // One score tile: its values at once.  Two: the last tile's, under this
+        // tile's softmax.
+        if (ok && M == kWide) values(j, value_steps(it, t), t == it.t1 - 1);
+        if (ok && M == kNarrow && t < it.t1 - 1) values(j - 1, value_steps(it, t + 1), t + 1 == it.t1 - 1);
       }
-      steps0 = steps1;
-      first0 = first1;
-      steps1 = value_steps(it, t);
-      first1 = t == it.t1 - 1;
     }
-    if (ok && it.t1 - it.t0 >= 2) values(j - 2, steps0, first0);
-    if (ok && it.t1 - it.t0 >= 1) values(j - 1, steps1, first1);
+    if (M == kNarrow && ok && it.t1 > it.t0) values(j - 1, value_steps(it, it.t0), it.t0 == it.t1 - 1);
+    if (M == kPair && ok && it.t1 - it.t0 >= 2)
+      values(j - 2, value_steps(it, it.t0 + 1), it.t0 + 1 == it.t1 - 1);
+    if (M == kPair && ok && it.t1 > it.t0) values(j - 1, value_steps(it, it.t0), it.t0 == it.t1 - 1);
   }
   const int lane = threadIdx.x & 31;
   if (!ok && lane == 0 && !cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
@@ -424,10 +563,11 @@ __device__ __forceinline__ uint32_t seen32(const DecodeArgs& a, const Item& it, 
 // ---- softmax and outputs --------------------------------------------------------
 // A warp has 16 rows, four lanes a row and two rows a lane (tensor memory's
 // fragments).  Warps without a row of the item only keep step.
-template <int CG>
-__device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem& sm, uint32_t tmem,
+template <int M>
+__device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem<M>& sm, uint32_t tmem,
                                               int warp, uint32_t rank) {
-  using Sh = Shape<CG>;
+  using Sh = Shape<M>;
+  constexpr int CG = Sh::CG;
   const int lane = threadIdx.x & 31;
   const int sub = warp >> 2, quad = warp & 3;
   const int r0 = quad * 32 + sub * 16;       // the warp's first row of the CTA's
@@ -450,13 +590,35 @@ __device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem& s
     const int t0 = uni(it.t0), t1 = uni(it.t1), nall = uni(it.nall), nfree = uni(it.nfree);
     const bool mine = (int)rank * kRows + r0 < uni(it.rows);
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    if (M == kWide && t1 > t0) {
+      // The queries' first 256 dimensions into tensor memory, a row a lane (the last
+      // item's scores are through: its outputs were waited for); rows past the
+      // item's repeat its last.
+      const int row = min(quad * 32 + lane, it.rows - 1);
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + ((int64_t)it.tok0 * a.H + it.row0 + row) * kDqk + sub * 128);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = __ldg(src + 4 * c + i);
+          w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+        tmem_store(tmem + ((uint32_t)(quad * 32) << 16) + kQCol + sub * 64 + c * 16, w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(&sm.qtm);
+    }
     for (int t = t1 - 1; t >= t0; --t, ++j) {
-      const uint32_t b = j & 1u;
-      ok = warp_wait(&sm.abort, &sm.sfull[b], (j >> 1) & 1u) &&
+      const uint32_t b = j % Sh::kScores;
+      ok = warp_wait(&sm.abort, &sm.sfull[b], (j / Sh::kScores) & 1u) &&
            warp_wait(&sm.abort, &sm.info[j % kInfo], (j / kInfo) & 1u);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t t_s = trow + s_col(b);
+      const uint32_t t_s = trow + Sh::s_col(b);
       float alpha[2] = {1.f, 1.f};
       if (mine) {
         const uint32_t pages = *reinterpret_cast<volatile uint32_t*>(&sm.pages[j % kInfo]);
@@ -564,16 +726,23 @@ __device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem& s
         }
       }
       if (has_tail(it, t)) {                 // values behind the sequence's end: zeros
-        ok = warp_wait(&sm.abort, &sm.vtail[tails & 1u], (tails >> 1) & 1u);
-        if (!ok) break;
-        const uint32_t seq = *reinterpret_cast<volatile uint32_t*>(&sm.tail_seq[tails & 1u]);
-        ++tails;
+        constexpr int kChunks = Sh::kAtoms * 8;   // 16-byte pieces of a key's values
         const int past = nall - t * kTileK, to = 16 * value_steps(it, t);
-        for (int z = warp * 32 + lane; z < (to - past) * Sh::kAtoms * 8; z += kSoftmaxWarps * 32) {
-          const int key = past + z / (Sh::kAtoms * 8), chunk = z % (Sh::kAtoms * 8);
-          uint8_t* blk = sm.ring + ((seq + (uint32_t)(key / kVKeys)) % Sh::kRing) * Sh::kBlock;
-          *reinterpret_cast<uint4*>(blk + (chunk >> 3) * Sh::kAtom + (key % kVKeys) * 128 + (chunk & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
+        if constexpr (M == kPair) {
+          ok = warp_wait(&sm.abort, &sm.vtail[tails & 1u], (tails >> 1) & 1u);
+          if (!ok) break;
+        }
+        const uint32_t seq = M == kPair ? *reinterpret_cast<volatile uint32_t*>(&sm.tail_seq[tails & 1u]) : 0u;
+        ++tails;
+        for (int z = warp * 32 + lane; z < (to - past) * kChunks; z += kSoftmaxWarps * 32) {
+          const int key = past + z / kChunks, chunk = z % kChunks;
+          uint8_t* at;
+          if constexpr (M == kPair)
+            at = sm.kv + ((seq + (uint32_t)(key / Sh::kVKeys)) % Sh::kRing) * Sh::kBlock +
+                 (chunk >> 3) * Sh::kAtom + (key % Sh::kVKeys) * 128;
+          else
+            at = sm.kv + ((j % Sh::kV) * kVBlocks + (chunk >> 3)) * Sh::kBlock + key * 128;
+          *reinterpret_cast<uint4*>(at + (chunk & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_for_products<CG>();            // before this warp hands its weights over
       }
@@ -647,12 +816,14 @@ __device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem& s
   if (!ok && lane == 0 && !cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
 }
 
-template <int CG>
+template <int M>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a) {
+  using Sh = Shape<M>;
+  constexpr int CG = Sh::CG;
   extern __shared__ unsigned char decode_smem_raw[];
-  DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>(
+  DecodeSmem<M>& sm = *reinterpret_cast<DecodeSmem<M>*>(
       (reinterpret_cast<uintptr_t>(decode_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = uni(tid >> 5);
   const uint32_t rank = CG == 2 ? pair_rank() : 0u;
@@ -666,17 +837,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       int first, end;
       rows_of(a, i, first, end);
       bad |= first != a.starts[i] || end != a.starts[i + 1];
-      blocks += ((end - first) * a.H + CG * kRows - 1) / (CG * kRows);
+      blocks += ((end - first) * a.H + Sh::kItemRows - 1) / Sh::kItemRows;
     }
     blocks = __reduce_add_sync(kFull, blocks);
     if (bad && blockIdx.x == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);
     if ((tid & 31) == 0) sm.blocks = blocks;
   } else if (tid == 0) {
-    for (int b = 0; b < Shape<CG>::kRing; ++b) {
-      mbar_init(&sm.full[b], 1 + (b == 0 ? kStalledArrivals : 0));
-      mbar_init(&sm.empty[b], 1);
-    }
+    for (int b = 0; b < kFullBars; ++b) mbar_init(&sm.full[b], 1 + (b == 0 ? kStalledArrivals : 0));
+    for (int b = 0; b < kEmptyBars; ++b) mbar_init(&sm.empty[b], 1);
     mbar_init(&sm.qfull, 1);
+    mbar_init(&sm.qtm, kSoftmaxWarps);
     mbar_init(&sm.qempty, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.sfull[b], 1);
@@ -696,16 +866,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = uni(sm.tmem);
   if (warp == kLoadWarp) {
-    load_tiles<CG>(a, sm, &tm_q, &tm_k, &tm_v, rank);
+    load_tiles<M>(a, sm, &tm_q, &tm_k, &tm_v, rank);
   } else if (warp < kSoftmaxWarps) {
-    softmax_tiles<CG>(a, sm, tmem, warp, rank);
+    softmax_tiles<M>(a, sm, tmem, warp, rank);
   } else if (warp == kClaimWarp) {
     const int blocks = sm.blocks;
     Cursor cur;
     share_out<CG>(sm.work, &sm.abort, a.flags, (int64_t)blocks * 2 * a.sm.S * a.splits, rank,
-                  [&](int64_t i) { return find_item<CG>(a, blocks, i, cur); });
+                  [&](int64_t i) { return find_item<M>(a, blocks, i, cur); });
   } else if (rank == 0) {
-    issue_products<CG>(a, sm, tmem);
+    issue_products<M>(a, sm, tmem);
   }
   tc_fence_before();
   __syncthreads();
@@ -716,32 +886,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-constexpr int kSmem = (int)sizeof(DecodeSmem) + 1024;
-
-// How a call is cut: CTAs that share a product, parts of the keys.
+// How a call is cut: by the rows of a request (on average), and its keys into parts
+// where items are fewer than CTAs.
 struct Plan {
-  int cg, splits;
+  int mode, item_rows, splits;
 };
 Plan plan_for(int rows, int S, int H, int reqs, int64_t cap) {
-  const int64_t pairs = ((int64_t)rows * H + reqs - 1) / reqs;   // of a request, about
+  const int64_t pairs = ((int64_t)rows * H + reqs - 1) / reqs;
   Plan p;
-  p.cg = pairs > kRows ? 2 : 1;
-  const int64_t items = (pairs + p.cg * kRows - 1) / (p.cg * kRows) * reqs * 2 * S;
-  const int64_t tiles = (cap + kTileK - 1) / kTileK;
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(device_sms() / p.cg / items, tiles / 2), 64));
+  p.mode = pairs > Shape<kWide>::kItemRows ? kPair : pairs > Shape<kNarrow>::kItemRows ? kWide : kNarrow;
+  p.item_rows = p.mode == kPair ? Shape<kPair>::kItemRows : p.mode == kWide ? Shape<kWide>::kItemRows
+                                                                          : Shape<kNarrow>::kItemRows;
+  const int64_t items = (pairs + p.item_rows - 1) / p.item_rows * reqs * 2 * S;
+  const int64_t tiles = (cap + kTileK - 1) / kTileK, ctas = device_sms() / (p.mode == kPair ? 2 : 1);
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(ctas / items, tiles / 2), 64));
   return p;
 }
 
-template <int CG>
+template <int M>
 cudaError_t launch_decode(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                           const DecodeArgs& a, int64_t items, cudaStream_t stream) {
-  const auto kernel = mla_decode_kernel<CG>;
+  const auto kernel = mla_decode_kernel<M>;
+  constexpr int kSmem = (int)sizeof(DecodeSmem<M>) + 1024;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   // An item a cluster; those that do not start at once are mostly taken over.
-  const unsigned grid = (unsigned)(items * CG);
-  return launch_kernel(kernel, dim3(grid), dim3(kThreads), (size_t)kSmem, stream, CG == 2 ? 2u : 0u,
-                       q, k, v, a);
+  const unsigned grid = (unsigned)(items * Shape<M>::CG);
+  return launch_kernel(kernel, dim3(grid), dim3(kThreads), (size_t)kSmem, stream,
+                       Shape<M>::CG == 2 ? 2u : 0u, q, k, v, a);
 }
 
 }  // namespace
@@ -779,9 +951,9 @@ extern "C" dsa_status dsa_mla_decode(const uint16_t* q, const uint16_t* kv_cache
   const int64_t cap = std::min<int64_t>((int64_t)max_blocks * block_size, (int64_t)1 << 30);
   Plan p = plan_for(rows, S, H, reqs, cap);
   if (!work) p.splits = 1;
-  DecodeArgs a{block_table, query_starts, seq_lens, tree_mask, reinterpret_cast<__nv_bfloat16*>(out),
+  DecodeArgs a{reinterpret_cast<const __nv_bfloat16*>(q), block_table, query_starts, seq_lens, tree_mask, reinterpret_cast<__nv_bfloat16*>(out),
                lse2, nullptr, nullptr, err_flags, n_slots, reqs, max_blocks, block_size, rows, H,
-               mask_words, p.splits, (int)cap, std::min(block_size, 64), std::min(block_size, kVKeys),
+               mask_words, p.splits, (int)cap, std::min(block_size, 64), std::min(block_size, (int)Shape<kPair>::kVKeys),
                scale == 0.f ? 0x1p-100f : fabsf(scale) * kLog2e, scale < 0.f ? kNegateA : 0u,
                ShardMath(S, I), FastDiv(block_size), FastDiv(H)};
   if (p.splits > 1) {
@@ -794,10 +966,11 @@ extern "C" dsa_status dsa_mla_decode(const uint16_t* q, const uint16_t* kv_cache
       !encode_map16(&tk, kv_cache, true, kDqk, n_slots, S, row, row * n_slots, a.kbox, 1) ||
       !encode_map16(&tv, kv_cache, true, kDqk, n_slots, S, row, row * n_slots, a.vbox, 1))
     return DSA_ERR_CUDA;
-  const int64_t items = (pairs / (p.cg * kRows) + reqs) * 2 * S * p.splits;   // at most
-  if (items * p.cg > INT32_MAX) return DSA_ERR_UNSUPPORTED;
-  const cudaError_t e = p.cg == 2 ? launch_decode<2>(tq, tk, tv, a, items, stream)
-                                  : launch_decode<1>(tq, tk, tv, a, items, stream);
+  const int64_t items = (pairs / p.item_rows + reqs) * 2 * S * p.splits;   // at most
+  if (items * 2 > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  const auto launch = p.mode == kPair ? launch_decode<kPair> : p.mode == kWide ? launch_decode<kWide>
+                                                                             : launch_decode<kNarrow>;
+  const cudaError_t e = launch(tq, tk, tv, a, items, stream);
   if (e != cudaSuccess) return DSA_ERR_CUDA;
   if (p.splits > 1) {
     const MergeArgs m{a.part_o, a.part_l, p.splits, S * pairs, query_starts, reqs, rows, H, out, lse2};
