@@ -11,18 +11,19 @@
 // All heads and rows of a request share its keys, so that (row, head) pairs are
 // the rows of one product.  An output of 512 values would fill tensor memory (512
 // columns), so an item takes half of it, and its scores are computed for both
-// halves: 2304 + 1024 cycles of products a tile of 128 keys where 2176 are the
-// least (65 %).  What the rows leave on chip decides how keys are held:
+// halves: 2304 + 1024 cycles of products for 128 keys where 2176 are the least (65
+// %).  What the rows leave on chip decides how keys are held:
 //  * Pair, more than 128 rows a request: two CTAs with 128 rows each issue one
-//    product of M = 256, and either holds half of the keys' tile and of the values'
-//    columns.  All queries in shared memory (144 KB), two score tiles, and a ring of
-//    80 KB through which a tile's keys pass in three units, its values in two;
-//  * Wide, up to 128: the queries' first 256 dimensions in tensor memory and one
-//    score tile, which makes room for a whole key tile (144 KB), whose value blocks
-//    stay until their product (a pair's halves would read them twice);
-//  * Narrow, up to 32: a product still reads 128 rows of A, but those past 32 may be
-//    anything, here the blocks that follow: the queries take 36 KB, and two score
-//    tiles and two tiles' values fit.
+//    product of M = 256, and either holds half of the keys' tile (of 128) and of the
+//    values' columns.  All queries in shared memory (144 KB) and a ring of 80 KB
+//    through which a tile's keys pass in three units, its values in two;
+//  * Wide, up to 128: the queries' first 256 dimensions in tensor memory, which
+//    leaves two stages of 72 KB for whole tiles of 64 keys: their value blocks stay
+//    until the value product.  (Scores with N = 64 take 1800 cycles where N = 128
+//    takes 1152 a tile, 4624 for 128 keys; one stage of 128 keys took 5.4 us a tile
+//    against 4.7 for two of these: its values could not be copied ahead.)
+//  * Narrow, up to 32: as Wide, but a product still reads 128 rows of A, and those
+//    past 32 may be anything, here the blocks that follow: the queries take 36 KB.
 // The first 256 of an item's output columns, and the last, are its half's value
 // blocks; of a tile's nine 64-value blocks the scores take the other five first.
 // One warp claims items while the kernel runs, one copies (tensor maps, a box per
@@ -40,7 +41,6 @@ namespace {
 
 constexpr int kDqk = DSA_MLA_DQK, kDv = DSA_MLA_DV, kHalf = kDv / 2;
 constexpr int kRows = 128;                   // rows of a CTA's product
-constexpr int kTileK = 128;
 constexpr int kBlocks = kDqk / 64;           // 9 blocks of 64 values
 constexpr int kVBlocks = 4, kABlocks = kBlocks - kVBlocks;   // of a half's values; the others
 constexpr int kQBox = 32;                    // rows of a copy of queries
@@ -66,19 +66,19 @@ struct Shape {
   static constexpr int kQTm = M == kWide ? 4 : 0;              // query blocks in tensor memory,
   static constexpr int kQBlock = kQRows * 128;                 // the others in shared memory
   static constexpr int kQBytes = (kBlocks - kQTm) * kQBlock;
-  static constexpr int kScores = M == kWide ? 1 : 2;           // score tiles
-  static constexpr int kBlock = 16384 / CG;                    // bytes of a key block
-  // Narrow, Wide: blocks that only scores read, tiles of values.
-  static constexpr int kA = M == kNarrow ? 3 : 5, kV = M == kNarrow ? 2 : 1;
-  // Pair: the ring's blocks, keys of a tile that a CTA holds, 64-value columns of
-  // its values, keys of a value block and bytes of a column in it.
-  static constexpr int kRing = 10, kKeys = kTileK / CG, kAtoms = kVBlocks / CG, kVKeys = 32;
-  static constexpr int kAtom = kVKeys * 128;
-  static constexpr int kKvBytes = M == kPair ? kRing * kBlock : (kA + kVBlocks * kV) * kBlock;
-  __device__ static constexpr uint32_t s_col(uint32_t b) { return 256 + b * 128; }
+  static constexpr int kTile = M == kPair ? 128 : 64;          // keys of a tile
+  static constexpr int kBlock = 8192;                          // bytes of 64 keys' 64 values
+  // Narrow, Wide: stages of a tile's nine blocks, the values' four first.
+  static constexpr int kStages = 2;
+  // Pair: the ring's blocks, 64-value columns of a CTA's values, keys of a value
+  // block and bytes of a column in it.
+  static constexpr int kRing = 10, kAtoms = kVBlocks / CG, kVKeys = 32, kAtom = kVKeys * 128;
+  static constexpr int kKvBytes = (M == kPair ? kRing : kStages * kBlocks) * kBlock;
+  __device__ static constexpr uint32_t s_col(uint32_t b) { return 256 + b * kTile; }
 };
-constexpr int kFullBars = 13, kEmptyBars = 8;   // barriers of key blocks (units)
-constexpr int kV0Full = 5, kV0Empty = 5;     // Narrow, Wide: the first of the values'
+// Barriers of key blocks: a pair's units, or a stage's values (at the stage) and
+// its other blocks (at kStages + the stage).
+constexpr int kUnits = 8;
 // Pair: blocks of a unit of the ring.
 constexpr uint32_t kKUnit = 3, kVUnit = 2;
 
@@ -95,9 +95,9 @@ struct Item {
 template <int M>
 struct alignas(1024) DecodeSmem {
   uint8_t q[Shape<M>::kQBytes];
-  uint8_t kv[Shape<M>::kKvBytes];            // Narrow, Wide: values of tiles first
+  uint8_t kv[Shape<M>::kKvBytes];
   WorkSlots<Item> work;
-  uint64_t full[kFullBars], empty[kEmptyBars], qfull, qtm, qempty, sfull[2], pfull[2], pvdone, vtail[2],
+  uint64_t full[kUnits], empty[kUnits], qfull, qtm, qempty, sfull[2], pfull[2], pvdone, vtail[2],
       info[kInfo], drain;
   uint32_t tail_seq[2];       // Pair: ring block of the values that vtail counts
   uint32_t pages[kInfo];      // valid pages of stream tile j, at j % kInfo: a bit per 16 keys
@@ -193,7 +193,8 @@ __device__ __forceinline__ Item find_item(const DecodeArgs& a, int blocks, int64
   it.nall = local_of(len);
   it.nvis = a.mask ? it.nall : local_of(it.base + hi + 1);
   it.nfree = local_of(a.mask ? it.base : it.base + lo + 1);
-  const int nt = (it.nvis + kTileK - 1) / kTileK, per = (nt + a.splits - 1) / a.splits;
+  constexpr int kTile = Shape<M>::kTile;
+  const int nt = (it.nvis + kTile - 1) / kTile, per = (nt + a.splits - 1) / a.splits;
   it.t0 = min(it.split * per, nt);
   it.t1 = min(it.t0 + per, nt);
   return it;
@@ -201,11 +202,14 @@ __device__ __forceinline__ Item find_item(const DecodeArgs& a, int blocks, int64
 
 // Steps of 16 keys of tile t's value product, and whether it reads keys behind
 // the sequence's end (zeroed in shared memory by the softmax warps).
+template <int M>
 __device__ __forceinline__ int value_steps(const Item& it, int t) {
-  return (min(it.nvis - t * kTileK, kTileK) + 15) / 16;
+  constexpr int kTile = Shape<M>::kTile;
+  return (min(it.nvis - t * kTile, kTile) + 15) / 16;
 }
+template <int M>
 __device__ __forceinline__ bool has_tail(const Item& it, int t) {
-  return it.nall - t * kTileK < 16 * value_steps(it, t);
+  return it.nall - t * Shape<M>::kTile < 16 * value_steps<M>(it, t);
 }
 // The i-th block that an item's scores take first, of the nine; its i-th value block.
 __device__ __forceinline__ int block_a(int half, int i) {
@@ -214,11 +218,12 @@ __device__ __forceinline__ int block_a(int half, int i) {
 __device__ __forceinline__ int block_v(int half, int i) { return half * kVBlocks + i; }
 
 // ---- the copies ---------------------------------------------------------------
-// A tile's keys 16 l to 16 l + 15 lie in a page: lane l (of 8, repeated) has the
-// page's table entry, then the cache row of the first of them.
+// A tile's keys 16 l to 16 l + 15 lie in a page: lane l (of as many as the tile has
+// such pieces, repeated) has the page's table entry, then the first one's cache row.
 template <int M>
 __device__ __forceinline__ int table_entry(const DecodeArgs& a, const Item& it, int t) {
-  const int key = t * kTileK + (int)(threadIdx.x & 7) * 16;
+  constexpr int kTile = Shape<M>::kTile;
+  const int key = t * kTile + (int)(threadIdx.x % (kTile / 16)) * 16;
   if (t < it.t0 || key >= it.nall) return -1;
   return __ldg(a.block_table + ((int64_t)it.shard * a.reqs + it.req) * a.max_blocks +
                fdiv((uint32_t)key, a.fblock));
@@ -245,21 +250,23 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
   const int lane = threadIdx.x & 31;
   const bool leader = rank == 0;
   Item it;
-  uint32_t j = 0, loads = 0, tails = 0, na = 0;   // tiles, items' queries, tails, score blocks so far
+  constexpr int kPieces = Sh::kTile / 16;
+  uint32_t j = 0, loads = 0, tails = 0;      // tiles, items' queries, tails so far
   bool ok = true, bad = false;
+  bool half_tile = false;                    // the last tile's values were not copied
   Ring ring;
   PendingV p0{}, p1{};
   // Pair: waits for a unit's space; its barrier then expects the pair's bytes (or,
   // values with a tail, an arrival alone: they are counted elsewhere).
   auto open_unit = [&](uint32_t blocks, bool bytes) {
     while (ok && ring.end + blocks - ring.freed > Sh::kRing) {
-      ok = warp_wait(&sm.abort, &sm.empty[ring.oldest % kEmptyBars], (ring.oldest / kEmptyBars) & 1u);
+      ok = warp_wait(&sm.abort, &sm.empty[ring.oldest % kUnits], (ring.oldest / kUnits) & 1u);
       ring.freed += ring.values & 1u ? kVUnit : kKUnit;
       ring.values >>= 1;
       ++ring.oldest;
     }
     if (ok && leader && lane == 0) {
-      uint64_t* bar = &sm.full[ring.unit % kEmptyBars];
+      uint64_t* bar = &sm.full[ring.unit % kUnits];
       if (bytes) mbar_expect_tx(bar, (uint32_t)CG * blocks * Sh::kBlock);
       else mbar_arrive1(bar);
     }
@@ -280,7 +287,7 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
     const int boxes = Sh::kVKeys / a.vbox, per = Sh::kAtoms * boxes;   // of a block
     for (uint32_t b = 0; b < kVBlocks; b += kVUnit) {
       if (!open_unit(kVUnit, !p.tail)) return;
-      const uint32_t bar = p.tail ? smem_u32(vtail) : leader_addr(&sm.full[ring.unit % kEmptyBars]);
+      const uint32_t bar = p.tail ? smem_u32(vtail) : leader_addr(&sm.full[ring.unit % kUnits]);
       const int i = lane / per, atom = lane % per / boxes, key = lane % boxes * a.vbox;
       const int y = __shfl_sync(kFull, p.y, (((int)b + i) * Sh::kVKeys + key) >> 4 & 7);
       if (i < (int)kVUnit)
@@ -294,7 +301,7 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
     bad |= it.bad != 0;
     int next = table_entry<M>(a, it, it.t1 - 1);
     for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
-      const int key = t * kTileK + (lane & 7) * 16, entry = next;
+      const int key = t * Sh::kTile + lane % kPieces * 16, entry = next;
       next = table_entry<M>(a, it, t - 1);   // on its way while this tile is copied
       int y = (int)a.n_slots;                // outside: reads as zero
       bool in = false;
@@ -306,7 +313,7 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
         if (in) y = (int)at;
         bad |= !in;
       }
-      const unsigned valid = __ballot_sync(kFull, in) & 0xffu;
+      const unsigned valid = __ballot_sync(kFull, in) & ((1u << kPieces) - 1u);
       if (M == kPair && t < it.t1 - 2) load_values(p0);
       if (!ok) break;
       if (t == it.t1 - 1) {                  // the item's queries
@@ -329,38 +336,41 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
         sm.pages[j % kInfo] = valid;
         mbar_arrive1(&sm.info[j % kInfo]);
       }
-      const int boxes = Sh::kKeys / a.kbox;  // of a block: 1 to 8
-      const int i = lane / boxes, first = (int)rank * Sh::kKeys + lane % boxes * a.kbox;
-      const int yk = __shfl_sync(kFull, y, first >> 4 & 7);
+      const int boxes = 64 / a.kbox;         // of a block: 1 to 4
+      const int i = lane / boxes, first = lane % boxes * a.kbox;
+      const int yk = __shfl_sync(kFull, y, ((int)rank * 64 + first) / 16 % kPieces);
       if constexpr (M == kPair) {
         for (uint32_t b = 0; b < kBlocks; b += kKUnit) {
           if (!open_unit(kKUnit, true)) break;
-          const uint32_t bar = leader_addr(&sm.full[ring.unit % kEmptyBars]);
+          const uint32_t bar = leader_addr(&sm.full[ring.unit % kUnits]);
           if (i < (int)kKUnit)
-            load_box<CG>(sm.kv + (ring.end + i) % Sh::kRing * Sh::kBlock + lane % boxes * a.kbox * 128, tm_k,
+            load_box<CG>(sm.kv + (ring.end + i) % Sh::kRing * Sh::kBlock + first * 128, tm_k,
                          ((int)b + i) * 64, yk, it.shard, bar);
           close_unit(kKUnit, false);
         }
         p0 = p1;
-        p1 = PendingV{y, it.half, it.shard, has_tail(it, t)};
+        p1 = PendingV{y, it.half, it.shard, has_tail<M>(it, t)};
       } else {
-        for (int b = 0; ok && b < kABlocks; ++b, ++na) {
-          const uint32_t slot = na % Sh::kA, use = na / Sh::kA;
-          if (use > 0) ok = warp_wait(&sm.abort, &sm.empty[slot], (use - 1) & 1u);
-          if (!ok) break;
-          if (lane == 0) mbar_expect_tx(&sm.full[slot], Sh::kBlock);
-          if (lane < boxes)
-            load_box<CG>(sm.kv + (Sh::kV * kVBlocks + slot) * Sh::kBlock + first * 128, tm_k,
-                         block_a(it.half, b) * 64, yk, it.shard, smem_u32(&sm.full[slot]));
-        }
-        const uint32_t vb = j % Sh::kV, use = j / Sh::kV;
-        if (ok && use > 0) ok = warp_wait(&sm.abort, &sm.empty[kV0Empty + vb], (use - 1) & 1u);
+        const uint32_t st = j % Sh::kStages, use = j / Sh::kStages;
+        uint8_t* stage = sm.kv + st * kBlocks * Sh::kBlock;
+        if (use > 0) ok = warp_wait(&sm.abort, &sm.empty[Sh::kStages + st], (use - 1) & 1u);
         if (!ok) break;
-        uint64_t* bar = &sm.full[kV0Full + vb * kVBlocks];
-        if (lane < kVBlocks) mbar_expect_tx(bar + lane, Sh::kBlock);
+        uint64_t* bar = &sm.full[Sh::kStages + st];
+        if (lane == 0) mbar_expect_tx(bar, kABlocks * Sh::kBlock);
+        if (i < kABlocks)
+          load_box<CG>(stage + (kVBlocks + i) * Sh::kBlock + first * 128, tm_k, block_a(it.half, i) * 64, yk,
+                       it.shard, smem_u32(bar));
+        if (use > 0) ok = warp_wait(&sm.abort, &sm.empty[st], (use - 1) & 1u);
+        if (!ok) {
+          half_tile = true;
+          ++j;
+          break;
+        }
+        bar = &sm.full[st];
+        if (lane == 0) mbar_expect_tx(bar, kVBlocks * Sh::kBlock);
         if (i < kVBlocks)
-          load_box<CG>(sm.kv + (vb * kVBlocks + i) * Sh::kBlock + first * 128, tm_k,
-                       block_v(it.half, i) * 64, yk, it.shard, smem_u32(bar + i));
+          load_box<CG>(stage + i * Sh::kBlock + first * 128, tm_k, block_v(it.half, i) * 64, yk, it.shard,
+                       smem_u32(bar));
       }
     }
     if (M == kPair && ok && it.t1 - it.t0 >= 2) load_values(p0);
@@ -373,15 +383,14 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
     if (leader && loads > 0) mbar_wait(&sm.qfull, (loads - 1) & 1u);
     if constexpr (M == kPair) {
       for (uint32_t u = ring.oldest; leader && u < ring.unit; ++u)
-        mbar_wait(&sm.full[u % kEmptyBars], (u / kEmptyBars) & 1u);
+        mbar_wait(&sm.full[u % kUnits], (u / kUnits) & 1u);
       for (uint32_t k = tails > 2 ? tails - 2 : 0; k < tails; ++k)
         mbar_wait(&sm.vtail[k & 1u], (k >> 1) & 1u);
     } else {
-      for (uint32_t b = na > Sh::kA ? na - Sh::kA : 0; b < na; ++b)
-        mbar_wait(&sm.full[b % Sh::kA], (b / Sh::kA) & 1u);
-      for (uint32_t v = j > Sh::kV ? j - Sh::kV : 0; v < j; ++v)
-        for (int i = 0; i < kVBlocks; ++i)
-          mbar_wait(&sm.full[kV0Full + v % Sh::kV * kVBlocks + i], (v / Sh::kV) & 1u);
+      for (uint32_t v = j > Sh::kStages ? j - Sh::kStages : 0; v < j; ++v) {
+        mbar_wait(&sm.full[Sh::kStages + v % Sh::kStages], (v / Sh::kStages) & 1u);
+        if (v + 1 < j || !half_tile) mbar_wait(&sm.full[v % Sh::kStages], (v / Sh::kStages) & 1u);
+      }
     }
   }
   __syncwarp();
@@ -394,14 +403,14 @@ template <int M>
 __device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem<M>& sm, uint32_t tmem) {
   using Sh = Shape<M>;
   constexpr int CG = Sh::CG;
-  const uint32_t id_s = idesc_f16(CG * kRows, kTileK, true, false) | a.negate;
+  const uint32_t id_s = idesc_f16(CG * kRows, Sh::kTile, true, false) | a.negate;
   constexpr uint32_t id_o = idesc_f16(CG * kRows, kHalf, true, true);
   constexpr int kStep = Sh::kBlock >> 4;     // a block in a descriptor's address field
   const uint64_t q0 = smem_desc_sw128(smem_u32(sm.q), 16, 1024);
   const uint64_t k0 = smem_desc_sw128(smem_u32(sm.kv), 16, 1024);
   const uint64_t v0 = smem_desc_sw128(smem_u32(sm.kv), M == kPair ? Sh::kAtom : Sh::kBlock, 1024);
   Item it;
-  uint32_t j = 0, nq = 0, na = 0;            // tiles, items' queries, score blocks so far
+  uint32_t j = 0, nq = 0;                    // tiles, items' queries so far
   uint32_t unit = 0, blk = 0;                // Pair: the ring's next unit and block
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -424,12 +433,12 @@ __device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem<M
   };
   // Values of stream tile v: `steps` of 16 keys, the item's first or not.
   auto values = [&](uint32_t v, int steps, bool first) {
-    const uint32_t b = v % Sh::kScores, p = tmem + Sh::s_col(b);
-    if (!wait(&sm.pfull[b], (v / Sh::kScores) & 1u)) return;
+    const uint32_t b = v % 2, p = tmem + Sh::s_col(b);
+    if (!wait(&sm.pfull[b], (v / 2) & 1u)) return;
     if constexpr (M == kPair) {
 #pragma unroll 1
       for (uint32_t u = 0; u < kVBlocks / kVUnit; ++u, ++unit, blk = (blk + kVUnit) % Sh::kRing) {
-        if (!wait(&sm.full[unit % kEmptyBars], (unit / kEmptyBars) & 1u)) return;
+        if (!wait(&sm.full[unit % kUnits], (unit / kUnits) & 1u)) return;
         if (elect_one()) {
 #pragma unroll
           for (uint32_t c = 0; c < kVUnit; ++c) {
@@ -442,19 +451,20 @@ __device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem<M
                            (first && step == 0) ? 0u : 1u);
             }
           }
-          tc_commit<CG>(&sm.empty[unit % kEmptyBars]);
+          tc_commit<CG>(&sm.empty[unit % kUnits]);
           if (u == kVBlocks / kVUnit - 1) tc_commit<CG>(&sm.pvdone);
         }
         __syncwarp();
       }
     } else {
-      const uint64_t vd = v0 + v % Sh::kV * (kVBlocks * kStep);
+      const uint32_t st = v % Sh::kStages;
+      const uint64_t vd = v0 + st * (kBlocks * kStep);
       if (elect_one()) {
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
+        for (int s = 0; s < Sh::kTile / 16; ++s)
           if (s < steps)
             mma_ts<CG>(tmem + kOCol, p + s * 8, vd + s * (2048 >> 4), id_o, (first && s == 0) ? 0u : 1u);
-        tc_commit<CG>(&sm.empty[kV0Empty + v % Sh::kV]);
+        tc_commit<CG>(&sm.empty[st]);
         tc_commit<CG>(&sm.pvdone);
       }
       __syncwarp();
@@ -463,13 +473,13 @@ __device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem<M
   for (uint32_t n = 0; next_item(sm.work, &sm.abort, n, ok, it); ++n) {
     item_done(sm.work, n);
     for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
-      if (M == kPair && t < it.t1 - 2) values(j - 2, value_steps(it, t + 2), t + 2 == it.t1 - 1);
+      if (M == kPair && t < it.t1 - 2) values(j - 2, value_steps<M>(it, t + 2), t + 2 == it.t1 - 1);
       if (ok && t == it.t1 - 1) {
         if (!wait(&sm.qfull, nq & 1u)) break;
         if (Sh::kQTm > 0 && !wait(&sm.qtm, nq & 1u)) break;
         ++nq;
       }
-      const uint32_t b = j % Sh::kScores, d = tmem + Sh::s_col(b);
+      const uint32_t b = j % 2, d = tmem + Sh::s_col(b);
       auto scores_done = [&]() {
         tc_commit<CG>(&sm.sfull[b]);
         if (t == it.t0) tc_commit<CG>(&sm.qempty);
@@ -477,47 +487,42 @@ __device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem<M
       if constexpr (M == kPair) {
 #pragma unroll 1
         for (uint32_t u = 0; ok && u < kBlocks / kKUnit; ++u, ++unit, blk = (blk + kKUnit) % Sh::kRing) {
-          if (!wait(&sm.full[unit % kEmptyBars], (unit / kEmptyBars) & 1u)) break;
+          if (!wait(&sm.full[unit % kUnits], (unit / kUnits) & 1u)) break;
           if (elect_one()) {
 #pragma unroll
             for (uint32_t c = 0; c < kKUnit; ++c)
               block_products(d, (int)(u * kKUnit + c), k0 + (blk + c) % Sh::kRing * kStep, u == 0 && c == 0);
-            tc_commit<CG>(&sm.empty[unit % kEmptyBars]);
+            tc_commit<CG>(&sm.empty[unit % kUnits]);
             if (u == kBlocks / kKUnit - 1) scores_done();
           }
           __syncwarp();
         }
       } else {
+        const uint32_t st = j % Sh::kStages, turn = (j / Sh::kStages) & 1u;
+        const uint64_t kd = k0 + st * (kBlocks * kStep);
+        if (!wait(&sm.full[Sh::kStages + st], turn)) break;
+        if (elect_one()) {
 #pragma unroll 1
-        for (int i = 0; ok && i < kABlocks; ++i, ++na) {
-          const uint32_t slot = na % Sh::kA;
-          if (!wait(&sm.full[slot], (na / Sh::kA) & 1u)) break;
-          if (elect_one()) {
-            block_products(d, block_a(it.half, i), k0 + (Sh::kV * kVBlocks + slot) * kStep, i == 0);
-            tc_commit<CG>(&sm.empty[slot]);
-          }
-          __syncwarp();
+          for (int i = 0; i < kABlocks; ++i)
+            block_products(d, block_a(it.half, i), kd + (kVBlocks + i) * kStep, i == 0);
+          tc_commit<CG>(&sm.empty[Sh::kStages + st]);
         }
-        const uint32_t vb = j % Sh::kV;
+        __syncwarp();
+        if (!wait(&sm.full[st], turn)) break;
+        if (elect_one()) {
 #pragma unroll 1
-        for (int i = 0; ok && i < kVBlocks; ++i) {
-          if (!wait(&sm.full[kV0Full + vb * kVBlocks + i], (j / Sh::kV) & 1u)) break;
-          if (elect_one()) {
-            block_products(d, block_v(it.half, i), k0 + (vb * kVBlocks + i) * kStep, false);
-            if (i == kVBlocks - 1) scores_done();
-          }
-          __syncwarp();
+          for (int i = 0; i < kVBlocks; ++i) block_products(d, block_v(it.half, i), kd + i * kStep, false);
+          scores_done();
         }
-        // One score tile: its values at once.  Two: the last tile's, under this
-        // tile's softmax.
-        if (ok && M == kWide) values(j, value_steps(it, t), t == it.t1 - 1);
-        if (ok && M == kNarrow && t < it.t1 - 1) values(j - 1, value_steps(it, t + 1), t + 1 == it.t1 - 1);
+        __syncwarp();
+        // The last tile's values, under this tile's softmax.
+        if (t < it.t1 - 1) values(j - 1, value_steps<M>(it, t + 1), t + 1 == it.t1 - 1);
       }
     }
-    if (M == kNarrow && ok && it.t1 > it.t0) values(j - 1, value_steps(it, it.t0), it.t0 == it.t1 - 1);
+    if (M != kPair && ok && it.t1 > it.t0) values(j - 1, value_steps<M>(it, it.t0), it.t0 == it.t1 - 1);
     if (M == kPair && ok && it.t1 - it.t0 >= 2)
-      values(j - 2, value_steps(it, it.t0 + 1), it.t0 + 1 == it.t1 - 1);
-    if (M == kPair && ok && it.t1 > it.t0) values(j - 1, value_steps(it, it.t0), it.t0 == it.t1 - 1);
+      values(j - 2, value_steps<M>(it, it.t0 + 1), it.t0 + 1 == it.t1 - 1);
+    if (M == kPair && ok && it.t1 > it.t0) values(j - 1, value_steps<M>(it, it.t0), it.t0 == it.t1 - 1);
   }
   const int lane = threadIdx.x & 31;
   if (!ok && lane == 0 && !cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
@@ -613,8 +618,8 @@ __device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem<M>
       if (lane == 0) mbar_arrive1(&sm.qtm);
     }
     for (int t = t1 - 1; t >= t0; --t, ++j) {
-      const uint32_t b = j % Sh::kScores;
-      ok = warp_wait(&sm.abort, &sm.sfull[b], (j / Sh::kScores) & 1u) &&
+      const uint32_t b = j % 2;
+      ok = warp_wait(&sm.abort, &sm.sfull[b], (j / 2) & 1u) &&
            warp_wait(&sm.abort, &sm.info[j % kInfo], (j / kInfo) & 1u);
       if (!ok) break;
       tc_fence_after();
@@ -622,16 +627,16 @@ __device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem<M>
       float alpha[2] = {1.f, 1.f};
       if (mine) {
         const uint32_t pages = *reinterpret_cast<volatile uint32_t*>(&sm.pages[j % kInfo]);
-        const bool masked = pages != 0xffu || (t + 1) * kTileK > nfree;
+        const bool masked = pages != (1u << (Sh::kTile / 16)) - 1u || (t + 1) * Sh::kTile > nfree;
         uint32_t seen[2] = {kFull, kFull};   // of keys 32 (lane % 4) on, by either row
         if (masked) {
           keep_branch();
-          const int c = lane & 3;
+          const int c = lane & (Sh::kTile / 32 - 1);
           const uint32_t pg = (pages >> (2 * c)) & 3u;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int row = it.row0 + min(br + 8 * k, it.rows - 1);
-            seen[k] = seen32(a, it, (int)fdiv((uint32_t)row, a.fH), t * kTileK + c * 32) &
+            seen[k] = seen32(a, it, (int)fdiv((uint32_t)row, a.fH), t * Sh::kTile + c * 32) &
                       ((pg & 1u ? 0xffffu : 0u) | (pg & 2u ? 0xffff0000u : 0u));
           }
         }
@@ -648,7 +653,7 @@ __device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem<M>
         };
         float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 4; c += 2) {
+        for (int c = 0; c < Sh::kTile / 32; c += 2) {
           uint32_t x[2][16];
           tmem_load_frag(t_s + c * 32, x[0]);
           tmem_load_frag(t_s + c * 32 + 32, x[1]);
@@ -687,10 +692,10 @@ __device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem<M>
         uint32_t y[2][16];
         tmem_load_frag(t_s, y[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < Sh::kTile / 32; ++c) {
           uint32_t (&x)[16] = y[c & 1];
           tmem_wait_ld(x);
-          if (c < 3) tmem_load_frag(t_s + (c + 1) * 32, y[(c + 1) & 1]);   // before weights overwrite it
+          if (c + 1 < Sh::kTile / 32) tmem_load_frag(t_s + (c + 1) * 32, y[(c + 1) & 1]);   // before weights overwrite it
           if (masked) {
             keep_branch();
             mask(x, c);
@@ -725,9 +730,9 @@ __device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem<M>
           }
         }
       }
-      if (has_tail(it, t)) {                 // values behind the sequence's end: zeros
+      if (has_tail<M>(it, t)) {                 // values behind the sequence's end: zeros
         constexpr int kChunks = Sh::kAtoms * 8;   // 16-byte pieces of a key's values
-        const int past = nall - t * kTileK, to = 16 * value_steps(it, t);
+        const int past = nall - t * Sh::kTile, to = 16 * value_steps<M>(it, t);
         if constexpr (M == kPair) {
           ok = warp_wait(&sm.abort, &sm.vtail[tails & 1u], (tails >> 1) & 1u);
           if (!ok) break;
@@ -741,7 +746,7 @@ __device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem<M>
             at = sm.kv + ((seq + (uint32_t)(key / Sh::kVKeys)) % Sh::kRing) * Sh::kBlock +
                  (chunk >> 3) * Sh::kAtom + (key % Sh::kVKeys) * 128;
           else
-            at = sm.kv + ((j % Sh::kV) * kVBlocks + (chunk >> 3)) * Sh::kBlock + key * 128;
+            at = sm.kv + ((j % Sh::kStages) * kBlocks + (chunk >> 3)) * Sh::kBlock + key * 128;
           *reinterpret_cast<uint4*>(at + (chunk & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_for_products<CG>();            // before this warp hands its weights over
@@ -843,8 +848,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (bad && blockIdx.x == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);
     if ((tid & 31) == 0) sm.blocks = blocks;
   } else if (tid == 0) {
-    for (int b = 0; b < kFullBars; ++b) mbar_init(&sm.full[b], 1 + (b == 0 ? kStalledArrivals : 0));
-    for (int b = 0; b < kEmptyBars; ++b) mbar_init(&sm.empty[b], 1);
+    for (int b = 0; b < kUnits; ++b) mbar_init(&sm.full[b], 1 + (b == 0 ? kStalledArrivals : 0));
+    for (int b = 0; b < kUnits; ++b) mbar_init(&sm.empty[b], 1);
     mbar_init(&sm.qfull, 1);
     mbar_init(&sm.qtm, kSoftmaxWarps);
     mbar_init(&sm.qempty, 1);
@@ -898,7 +903,7 @@ Plan plan_for(int rows, int S, int H, int reqs, int64_t cap) {
   p.item_rows = p.mode == kPair ? Shape<kPair>::kItemRows : p.mode == kWide ? Shape<kWide>::kItemRows
                                                                           : Shape<kNarrow>::kItemRows;
   const int64_t items = (pairs + p.item_rows - 1) / p.item_rows * reqs * 2 * S;
-  const int64_t tiles = (cap + kTileK - 1) / kTileK, ctas = device_sms() / (p.mode == kPair ? 2 : 1);
+  const int64_t tiles = (cap + 127) / 128, ctas = device_sms() / (p.mode == kPair ? 2 : 1);
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(ctas / items, tiles / 2), 64));
   return p;
 }
