@@ -7,11 +7,17 @@
 // head's 128 values turned alike, code = e4m3(y / s) with s the smallest power
 // of two with max |y| <= 448 s, and the head's weight times factor * s.
 //
-// Memory-bound: 256 bytes in and 128 out a row.  Sixteen lanes take a row, eight
-// values (16 bytes) each, so that sums and maxima are four shuffles.  A pair's
-// other half may lie in any lane (half layout, odd widths): the rows pass
-// through shared memory as fp32, and every lane turns its own eight values with
-// cosines, sines and partners found once and used for all heads it takes.
+// Memory-bound: 256 bytes in and 128 out a row, and the arithmetic close behind
+// (an issue slot of 16 a value is what the bandwidth leaves).  Sixteen lanes take a
+// row, eight values (16 bytes) each, so that sums and maxima are four shuffles.
+// Where a value's partner lies decides how it is fetched: in the same lane
+// (interleaved pairs at an even offset), in a lane a fixed way off (the half layout
+// at multiples of 8), or anywhere, through shared memory.  A thread finds its cosines
+// and sines once and uses them for all heads it takes.
+// Queries round as the exact values do: a scaled value within fp32's error of a
+// border between two codes, or a largest one near a border between two scales, sends
+// its head through 64 bits (one head in about 300).
+// Measured, replays: MEASURED_QUERY
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -31,38 +37,42 @@ struct TurnArgs {
   uint32_t* flags;
 };
 
+enum Partner { kInLane, kLaneOff, kAnywhere };
+
 // How this lane's eight values turn: y_e = x_e cos_e + x_partner sin_e, partner
-// the other value of the pair (the sine negative for a pair's first).
+// the other value of the pair (the sine negative for a pair's first, 0 where the
+// value is carried).
+template <int P>
 struct Turn {
   float c[kVals], s[kVals];
-  int8_t partner[kVals];
-  bool any;
+  int off;                                   // kLaneOff: the partner's lane
+  int partner[P == kAnywhere ? kVals : 1];   // kAnywhere: its place in the row
 };
 
-__device__ __forceinline__ Turn find_turn(const TurnArgs& a, int token, int lane16) {
-  Turn t;
+template <int P>
+__device__ __forceinline__ Turn<P> find_turn(const TurnArgs& a, int token, int lane16) {
+  Turn<P> t;
   const int pos = __ldg(a.positions + token);
   const bool in = pos >= 0 && pos < a.max_pos;
   if (!in && lane16 == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);
   const float* row = a.table + (int64_t)(in ? pos : 0) * a.rot;
-  const int half = a.rot / 2;
-  t.any = false;
+  const int half = a.rot / 2, i0 = lane16 * kVals - a.first;   // the first value's place among the turning
+  t.off = lane16;
+  if (P == kLaneOff && i0 >= 0 && i0 < a.rot) t.off = lane16 + (i0 < half ? half : -half) / kVals;
 #pragma unroll
   for (int e = 0; e < kVals; ++e) {
-    const int at = lane16 * kVals + e, i = at - a.first;
+    const int i = i0 + e;
     t.c[e] = 1.f;
     t.s[e] = 0.f;
-    t.partner[e] = (int8_t)at;
+    if (P == kAnywhere) t.partner[e] = lane16 * kVals + e;
     if (!in || i < 0 || i >= a.rot) continue;
-    const bool inter = a.layout == DSA_ROPE_INTERLEAVED;
-    const int pair = inter ? i >> 1 : (i < half ? i : i - half);
+    const bool inter = P == kInLane || (P == kAnywhere && a.layout == DSA_ROPE_INTERLEAVED);
     const bool second = inter ? (i & 1) != 0 : i >= half;
-    const int other = inter ? i ^ 1 : (second ? i - half : i + half);
+    const int pair = inter ? i >> 1 : (second ? i - half : i);
     t.c[e] = __ldg(row + pair);
     const float sn = __ldg(row + half + pair);
     t.s[e] = second ? sn : -sn;
-    t.partner[e] = (int8_t)(a.first + other);
-    t.any = true;
+    if (P == kAnywhere) t.partner[e] = a.first + (inter ? i ^ 1 : (second ? i - half : i + half));
   }
   return t;
 }
@@ -84,6 +94,9 @@ __device__ __forceinline__ uint2 codes8(const float (&y)[kVals]) {
                     e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
 }
 
+// In a branch rarely taken: keeps it one.
+__device__ __forceinline__ void keep_branch() { asm volatile("" ::: "memory"); }
+
 // Sum over the 16 lanes of a row.
 __device__ __forceinline__ float sum16(float v) {
 #pragma unroll
@@ -91,17 +104,28 @@ __device__ __forceinline__ float sum16(float v) {
   return v;
 }
 
-// The row's values in shared memory for the others' partners, then this lane's
-// turned.  Rows are of one warp: no barrier of the block.
-__device__ __forceinline__ void turn8(const Turn& t, float* row, int lane16, float (&x)[kVals]) {
-  __syncwarp();
-  *reinterpret_cast<float4*>(row + lane16 * kVals) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4*>(row + lane16 * kVals + 4) = make_float4(x[4], x[5], x[6], x[7]);
-  __syncwarp();
-  if (!t.any) return;
+// Every value's partner.  Rows are of one warp: no barrier of the block.
+template <int P>
+__device__ __forceinline__ void partners(const Turn<P>& t, float* row, int lane16, const float (&x)[kVals],
+                                         float (&p)[kVals]) {
+  if constexpr (P == kInLane) {
 #pragma unroll
-  for (int e = 0; e < kVals; ++e)
-    if (t.partner[e] != lane16 * kVals + e) x[e] = fmaf(x[e], t.c[e], row[t.partner[e]] * t.s[e]);
+    for (int e = 0; e < kVals; ++e) p[e] = x[e ^ 1];
+  } else if constexpr (P == kLaneOff) {
+#pragma unroll
+    for (int e = 0; e < kVals; ++e) p[e] = __shfl_sync(kFull, x[e], t.off, kLanes);
+  } else {
+    __syncwarp();
+    *reinterpret_cast<float4*>(row + lane16 * kVals) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(row + lane16 * kVals + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < kVals; ++e) p[e] = row[t.partner[e]];
+  }
+}
+// A carried value is its bits (a partner that is infinite must not reach it).
+__device__ __forceinline__ float turned(float x, float c, float p, float s) {
+  return s == 0.f ? x * c : fmaf(x, c, p * s);
 }
 
 struct KeyArgs {
@@ -116,15 +140,16 @@ struct KeyArgs {
   uint8_t* cache;                            // [S][n_slots][kDim]
 };
 
+template <int P>
 __global__ void __launch_bounds__(kThreads) indexer_key_kernel(const KeyArgs a) {
-  __shared__ __align__(16) float rows[kRows][kDim];
+  __shared__ __align__(16) float rows[P == kAnywhere ? kRows : 1][kDim];
   const int lane16 = threadIdx.x & (kLanes - 1), r = threadIdx.x / kLanes;
   const int token = blockIdx.x * kRows + r;
   const bool there = token < a.T;
   const int tok = there ? token : a.T - 1;   // the last block's idle lanes: a row not stored
   float x[kVals], w[kVals], b[kVals];
   unpack8(__ldg(reinterpret_cast<const uint4*>(a.k + tok * a.stride) + lane16), x);
-  const Turn t = find_turn(a.turn, tok, lane16);
+  const Turn<P> t = find_turn<P>(a.turn, tok, lane16);
 #pragma unroll
   for (int v = 0; v < 2; ++v) {
     const float4 wv = __ldg(reinterpret_cast<const float4*>(a.weight) + lane16 * 2 + v);
@@ -146,7 +171,10 @@ __global__ void __launch_bounds__(kThreads) indexer_key_kernel(const KeyArgs a) 
   const float inv = 1.f / sqrtf(sum16(q) * (1.f / kDim) + a.eps);
 #pragma unroll
   for (int e = 0; e < kVals; ++e) x[e] = fmaf(x[e] * inv, w[e], b[e]);
-  turn8(t, rows[r], lane16, x);
+  float p[kVals];
+  partners<P>(t, rows[P == kAnywhere ? r : 0], lane16, x, p);
+#pragma unroll
+  for (int e = 0; e < kVals; ++e) x[e] = turned(x[e], t.c[e], p[e], t.s[e]);
   const uint2 code = codes8(x);
   if (!there) return;
   for (int sh = 0; sh < a.S; ++sh) {
@@ -181,9 +209,18 @@ __device__ __forceinline__ float scale_for(F amax) {
   return ldexpf(1.f, max(m > (F)0.875 ? e - 8 : e - 9, -126));
 }
 
-template <int kHeads>
+// Whether z (to be rounded to e4m3) is so close to the middle between two codes that
+// fp32's error may have moved it across: the 20 bits behind the three kept ones; codes
+// below 2^-6 are 2^-9 apart, as those from 2^-6 on.
+__device__ __forceinline__ bool near_middle(float z) {
+  float w = fabsf(z);
+  if (w < 0.015625f) w += 0.015625f;
+  return (__float_as_uint(w) & 0xFFFFFu) - 0x7FFF8u <= 16u;
+}
+
+template <int P, int kHeads>
 __global__ void __launch_bounds__(kThreads) indexer_query_kernel(const QueryArgs a) {
-  __shared__ __align__(16) float rows[kRows][kDim];
+  __shared__ __align__(16) float rows[P == kAnywhere ? kRows : 1][kDim];
   const int lane16 = threadIdx.x & (kLanes - 1), r = threadIdx.x / kLanes;
   const int token = blockIdx.x / a.per_token;
   const int h0 = (blockIdx.x - token * a.per_token) * (kRows * kHeads) + r;
@@ -194,46 +231,81 @@ __global__ void __launch_bounds__(kThreads) indexer_query_kernel(const QueryArgs
     raw[k] = h < a.H ? __ldg(reinterpret_cast<const uint4*>(a.q + token * a.token + h * a.head) + lane16)
                      : make_uint4(0, 0, 0, 0);
   }
-  const Turn t = find_turn(a.turn, token, lane16);
+  const Turn<P> t = find_turn<P>(a.turn, token, lane16);
 #pragma unroll
   for (int k = 0; k < kHeads; ++k) {
     const int h = h0 + k * kRows;
-    float x[kVals];
+    float x[kVals], p[kVals], y[kVals];
     unpack8(raw[k], x);
-    turn8(t, rows[r], lane16, x);
+    partners<P>(t, rows[P == kAnywhere ? r : 0], lane16, x, p);
     float amax = 0.f;
 #pragma unroll
-    for (int e = 0; e < kVals; ++e) amax = fmaxf(amax, isfinite(x[e]) ? fabsf(x[e]) : 0.f);
+    for (int e = 0; e < kVals; ++e) {
+      y[e] = turned(x[e], t.c[e], p[e], t.s[e]);
+      amax = fmaxf(amax, fabsf(y[e]) <= 3.4028235e38f ? fabsf(y[e]) : 0.f);
+    }
 #pragma unroll
     for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
     float scale = scale_for(amax);
-    // A largest value within fp32's error of the border between two scales: found
-    // again in 64 bits, so that the scale is that of the exact values (one head
-    // in a hundred: bf16 values lie on the border itself).
-    const bool near = fabsf(amax / scale - 448.f) < 448.f * 1e-6f || fabsf(amax / scale - 224.f) < 224.f * 1e-6f;
+    float inv = 1.f / scale;                 // exact: a power of two (of 2^-126, 2^126)
+    // A largest value near a border between two scales (on it lie bf16 values), or a
+    // turned one near a middle between two codes (carried ones are exact, and one in
+    // sixteen on a middle): once more in 64 bits.
+    const float top32 = amax * inv;
+    bool near = (fabsf(top32 - 448.f) < 448.f * 1e-6f && top32 != 448.f) || fabsf(top32 - 224.f) < 224.f * 1e-6f;
+#pragma unroll
+    for (int e = 0; e < kVals; ++e) near = near || (t.s[e] != 0.f && near_middle(y[e] * inv));
     if (__any_sync(kFull, near)) {
-      float x0[kVals];
-      unpack8(raw[k], x0);
+      keep_branch();
       double top = 0.0;
 #pragma unroll
       for (int e = 0; e < kVals; ++e) {
-        double y = x0[e];
-        if (t.any && t.partner[e] != lane16 * kVals + e)
-          y = y * (double)t.c[e] + (double)rows[r][t.partner[e]] * (double)t.s[e];
-        if (isfinite(x[e])) top = fmax(top, fabs(y));
+        const double d = t.s[e] == 0.f ? (double)x[e] * t.c[e]
+                                       : fma((double)x[e], (double)t.c[e], (double)p[e] * (double)t.s[e]);
+        if (fabsf(y[e]) <= 3.4028235e38f) top = fmax(top, fabs(d));
       }
 #pragma unroll
       for (int o = 8; o; o >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, o));
       scale = scale_for(top);
-    }
-    if (h >= a.H) continue;
-    const float inv = 1.f / scale;           // exact: a power of two (of 2^-126, 2^126)
+      inv = 1.f / scale;
 #pragma unroll
-    for (int e = 0; e < kVals; ++e) x[e] *= inv;
-    const int64_t row = (int64_t)token * a.H + h;
-    *reinterpret_cast<uint2*>(a.q_out + row * kDim + lane16 * kVals) = codes8(x);
-    if (lane16 == 0) a.w_out[row] = a.weights[row] * a.factor * scale;
+      for (int e = 0; e < kVals; ++e) {
+        const double d = (t.s[e] == 0.f ? (double)x[e] * t.c[e]
+                                        : fma((double)x[e], (double)t.c[e], (double)p[e] * (double)t.s[e])) * inv;
+        // To fp32 with what is cut kept in the last bit, so that the next rounding
+        // sees on which side of a middle it lay.
+        float f = __double2float_rz(d);
+        if ((double)f != d && fabsf(f) <= 3.4028235e38f) f = __uint_as_float(__float_as_uint(f) | 1u);
+        y[e] = f;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kVals; ++e) y[e] *= inv;
+    }
+    if (h < a.H) {
+      const int64_t row = (int64_t)token * a.H + h;
+      *reinterpret_cast<uint2*>(a.q_out + row * kDim + lane16 * kVals) = codes8(y);
+      if (lane16 == 0) a.w_out[row] = a.weights[row] * a.factor * scale;
+    }
   }
+}
+
+// Where a value's partner lies.
+int partner_of(int rot, int first, int layout) {
+  if (layout == DSA_ROPE_INTERLEAVED && first % 2 == 0) return kInLane;
+  if (layout == DSA_ROPE_HALF && first % kVals == 0 && rot % (2 * kVals) == 0) return kLaneOff;
+  return kAnywhere;
+}
+
+template <int P>
+cudaError_t launch_query(QueryArgs& a, bool few, cudaStream_t stream) {
+  // Eight heads a thread share its cosines and sines; with few tokens, two, which
+  // are more blocks.
+  const int heads = kRows * (few ? 2 : 8);
+  a.per_token = (a.H + heads - 1) / heads;
+  const dim3 grid((unsigned)((int64_t)a.T * a.per_token));
+  return few ? launch_kernel(indexer_query_kernel<P, 2>, grid, dim3(kThreads), 0, stream, 0, a)
+             : launch_kernel(indexer_query_kernel<P, 8>, grid, dim3(kThreads), 0, stream, 0, a);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -270,8 +342,11 @@ extern "C" dsa_status dsa_indexer_key_insert(const uint16_t* k, int64_t k_token,
                   {positions, cos_sin_cache, max_pos, rot_dim, first, layout, err_flags},
                   slot_mapping, T, S, n_slots, k_cache};
   const unsigned blocks = (unsigned)(((int64_t)T + kRows - 1) / kRows);
-  return launch_kernel(indexer_key_kernel, dim3(blocks), dim3(kThreads), 0, stream, 0, a) == cudaSuccess
-             ? DSA_OK : DSA_ERR_CUDA;
+  const int part = partner_of(rot_dim, first, layout);
+  const auto kernel = part == kInLane ? indexer_key_kernel<kInLane>
+                      : part == kLaneOff ? indexer_key_kernel<kLaneOff> : indexer_key_kernel<kAnywhere>;
+  return launch_kernel(kernel, dim3(blocks), dim3(kThreads), 0, stream, 0, a) == cudaSuccess ? DSA_OK
+                                                                                            : DSA_ERR_CUDA;
 }
 
 extern "C" dsa_status dsa_indexer_query_fp8(const uint16_t* q, int64_t q_token, int64_t q_head,
@@ -292,11 +367,11 @@ extern "C" dsa_status dsa_indexer_query_fp8(const uint16_t* q, int64_t q_token, 
   QueryArgs a{reinterpret_cast<const __nv_bfloat16*>(q), T > 1 ? q_token : 0, H > 1 ? q_head : 0, weights, factor,
               {positions, cos_sin_cache, max_pos, rot_dim, first, layout, err_flags},
               T, H, 0, q_out, weights_out};
-  constexpr int kHeads = 4;
-  a.per_token = (H + kRows * kHeads - 1) / (kRows * kHeads);
-  const int64_t blocks = (int64_t)T * a.per_token;
-  if (blocks > INT32_MAX) return DSA_ERR_UNSUPPORTED;
-  return launch_kernel(indexer_query_kernel<kHeads>, dim3((unsigned)blocks), dim3(kThreads), 0,
-                       stream, 0, a) == cudaSuccess
-             ? DSA_OK : DSA_ERR_CUDA;
+  if ((int64_t)T * H > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  const int part = partner_of(rot_dim, first, layout);
+  const bool few = (int64_t)T * H < 65536;
+  const cudaError_t e = part == kInLane    ? launch_query<kInLane>(a, few, stream)
+                        : part == kLaneOff ? launch_query<kLaneOff>(a, few, stream)
+                                           : launch_query<kAnywhere>(a, few, stream);
+  return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

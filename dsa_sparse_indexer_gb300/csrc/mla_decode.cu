@@ -16,14 +16,15 @@
 //  * Pair, more than 128 rows a request: two CTAs with 128 rows each issue one
 //    product of M = 256, and either holds half of the keys' tile (of 128) and of the
 //    values' columns.  All queries in shared memory (144 KB) and a ring of 80 KB
-//    through which a tile's keys pass in three units, its values in two;
+//    through which a tile's keys pass in three units, its values in one;
 //  * Wide, up to 128: the queries' first 256 dimensions in tensor memory, which
 //    leaves two stages of 72 KB for whole tiles of 64 keys: their value blocks stay
 //    until the value product.  (Scores with N = 64 take 1800 cycles where N = 128
 //    takes 1152 a tile, 4624 for 128 keys; one stage of 128 keys took 5.4 us a tile
 //    against 4.7 for two of these: its values could not be copied ahead.)
 //  * Narrow, up to 32: as Wide, but a product still reads 128 rows of A, and those
-//    past 32 may be anything, here the blocks that follow: the queries take 36 KB.
+//    past 32 may be anything, here the blocks that follow: the queries take 36 KB,
+//    and two items' fit.
 // The first 256 of an item's output columns, and the last, are its half's value
 // blocks; of a tile's nine 64-value blocks the scores take the other five first.
 // One warp claims items while the kernel runs, one copies (tensor maps, a box per
@@ -66,6 +67,7 @@ struct Shape {
   static constexpr int kQTm = M == kWide ? 4 : 0;              // query blocks in tensor memory,
   static constexpr int kQBlock = kQRows * 128;                 // the others in shared memory
   static constexpr int kQBytes = (kBlocks - kQTm) * kQBlock;
+  static constexpr int kQBufs = M == kNarrow ? 2 : 1;          // items whose queries fit
   static constexpr int kTile = M == kPair ? 128 : 64;          // keys of a tile
   static constexpr int kBlock = 8192;                          // bytes of 64 keys' 64 values
   // Narrow, Wide: stages of a tile's nine blocks, the values' four first.
@@ -80,7 +82,8 @@ struct Shape {
 // its other blocks (at kStages + the stage).
 constexpr int kUnits = 8;
 // Pair: blocks of a unit of the ring.
-constexpr uint32_t kKUnit = 3, kVUnit = 2;
+constexpr uint32_t kKUnit = 3, kVUnit = 4;
+__device__ __forceinline__ uint32_t wrap(uint32_t b) { return b >= 10 ? b - 10 : b; }   // into the ring
 
 struct Item {
   int req, shard, half, split;
@@ -94,12 +97,12 @@ struct Item {
 
 template <int M>
 struct alignas(1024) DecodeSmem {
-  uint8_t q[Shape<M>::kQBytes];
+  uint8_t q[Shape<M>::kQBufs][Shape<M>::kQBytes];
   uint8_t kv[Shape<M>::kKvBytes];
   WorkSlots<Item> work;
-  uint64_t full[kUnits], empty[kUnits], qfull, qtm, qempty, sfull[2], pfull[2], pvdone, vtail[2],
+  uint64_t full[kUnits], empty[kUnits], qfull[2], qtm, qempty[2], sfull[2], pfull[2], pvdone, vtail[2],
       info[kInfo], drain;
-  uint32_t tail_seq[2];       // Pair: ring block of the values that vtail counts
+  uint32_t tail_seq[2];       // Pair: place in the ring of the values that vtail counts
   uint32_t pages[kInfo];      // valid pages of stream tile j, at j % kInfo: a bit per 16 keys
   uint32_t tmem;
   int blocks;                 // row blocks of all requests
@@ -108,7 +111,7 @@ struct alignas(1024) DecodeSmem {
 static_assert(sizeof(DecodeSmem<kNarrow>) + 1024 <= 232448 && sizeof(DecodeSmem<kWide>) + 1024 <= 232448 &&
                   sizeof(DecodeSmem<kPair>) + 1024 <= 232448,
               "shared memory of a CTA");
-static_assert(8 * Shape<kNarrow>::kQBlock + kRows * 128 <= Shape<kNarrow>::kQBytes + Shape<kNarrow>::kKvBytes,
+static_assert(8 * Shape<kNarrow>::kQBlock + kRows * 128 <= Shape<kNarrow>::kKvBytes,
               "rows past the queries lie in this CTA's memory");
 
 struct DecodeArgs {
@@ -232,7 +235,7 @@ __device__ __forceinline__ int table_entry(const DecodeArgs& a, const Item& it, 
 // Ring of the pair: units are freed in the order in which they were copied.
 struct Ring {
   uint32_t unit = 0, oldest = 0;             // the next unit; the oldest not known to be free
-  uint32_t end = 0, freed = 0;               // blocks copied and freed so far
+  uint32_t used = 0, at = 0;                 // blocks not known to be free; the next block's place
   uint32_t values = 0;                       // bit i: unit oldest + i is one of values
 };
 
@@ -259,9 +262,9 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
   // Pair: waits for a unit's space; its barrier then expects the pair's bytes (or,
   // values with a tail, an arrival alone: they are counted elsewhere).
   auto open_unit = [&](uint32_t blocks, bool bytes) {
-    while (ok && ring.end + blocks - ring.freed > Sh::kRing) {
+    while (ok && ring.used + blocks > Sh::kRing) {
       ok = warp_wait(&sm.abort, &sm.empty[ring.oldest % kUnits], (ring.oldest / kUnits) & 1u);
-      ring.freed += ring.values & 1u ? kVUnit : kKUnit;
+      ring.used -= ring.values & 1u ? kVUnit : kKUnit;
       ring.values >>= 1;
       ++ring.oldest;
     }
@@ -275,12 +278,13 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
   auto close_unit = [&](uint32_t blocks, bool is_values) {
     ring.values |= (is_values ? 1u : 0u) << (ring.unit - ring.oldest);
     ++ring.unit;
-    ring.end += blocks;
+    ring.used += blocks;
+    ring.at = wrap(ring.at + blocks);
   };
   auto load_values = [&](const PendingV& p) {
     uint64_t* vtail = &sm.vtail[tails & 1u];
     if (p.tail && lane == 0) {
-      sm.tail_seq[tails & 1u] = ring.end;    // published by the barrier
+      sm.tail_seq[tails & 1u] = ring.at;     // published by the barrier
       mbar_expect_tx(vtail, (uint32_t)(kVBlocks * Sh::kBlock));
     }
     tails += p.tail;
@@ -291,7 +295,7 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
       const int i = lane / per, atom = lane % per / boxes, key = lane % boxes * a.vbox;
       const int y = __shfl_sync(kFull, p.y, (((int)b + i) * Sh::kVKeys + key) >> 4 & 7);
       if (i < (int)kVUnit)
-        load_box<CG>(sm.kv + (ring.end + i) % Sh::kRing * Sh::kBlock + atom * Sh::kAtom + key * 128, tm_v,
+        load_box<CG>(sm.kv + wrap(ring.at + i) * Sh::kBlock + atom * Sh::kAtom + key * 128, tm_v,
                      p.half * kHalf + ((int)rank * Sh::kAtoms + atom) * 64, y, p.shard, bar);
       close_unit(kVUnit, true);
     }
@@ -317,7 +321,8 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
       if (M == kPair && t < it.t1 - 2) load_values(p0);
       if (!ok) break;
       if (t == it.t1 - 1) {                  // the item's queries
-        if (loads > 0) ok = warp_wait(&sm.abort, &sm.qempty, (loads - 1) & 1u);
+        const uint32_t qb = loads % Sh::kQBufs, use = loads / Sh::kQBufs;
+        if (use > 0) ok = warp_wait(&sm.abort, &sm.qempty[qb], (use - 1) & 1u);
         if (!ok) break;
         ++loads;
         constexpr int kN = kBlocks - Sh::kQTm;
@@ -325,11 +330,11 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
           return (min(max(it.rows - r * kRows, 0), Sh::kQRows) + kQBox - 1) / kQBox;
         };
         if (leader && lane == 0)
-          mbar_expect_tx(&sm.qfull, (uint32_t)((boxes(0) + (CG == 2 ? boxes(1) : 0)) * kN * kQBox * 128));
-        const uint32_t bar = CG == 1 ? smem_u32(&sm.qfull) : leader_addr(&sm.qfull);
+          mbar_expect_tx(&sm.qfull[qb], (uint32_t)((boxes(0) + (CG == 2 ? boxes(1) : 0)) * kN * kQBox * 128));
+        const uint32_t bar = CG == 1 ? smem_u32(&sm.qfull[qb]) : leader_addr(&sm.qfull[qb]);
         if (lane < kN)
           for (int b = 0; b < boxes((int)rank); ++b)
-            load_box<CG>(sm.q + lane * Sh::kQBlock + b * kQBox * 128, tm_q, (Sh::kQTm + lane) * 64,
+            load_box<CG>(sm.q[qb] + lane * Sh::kQBlock + b * kQBox * 128, tm_q, (Sh::kQTm + lane) * 64,
                          it.tok0 * a.H + it.row0 + (int)rank * kRows + b * kQBox, 0, bar);
       }
       if (lane == 0) {
@@ -344,7 +349,7 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
           if (!open_unit(kKUnit, true)) break;
           const uint32_t bar = leader_addr(&sm.full[ring.unit % kUnits]);
           if (i < (int)kKUnit)
-            load_box<CG>(sm.kv + (ring.end + i) % Sh::kRing * Sh::kBlock + first * 128, tm_k,
+            load_box<CG>(sm.kv + wrap(ring.at + i) * Sh::kBlock + first * 128, tm_k,
                          ((int)b + i) * 64, yk, it.shard, bar);
           close_unit(kKUnit, false);
         }
@@ -380,7 +385,8 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
   if (!ok && lane == 0) {
     if (!cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
     // The copies issued land before the CTA ends (a pair's first CTA counts both's).
-    if (leader && loads > 0) mbar_wait(&sm.qfull, (loads - 1) & 1u);
+    for (uint32_t k = loads > Sh::kQBufs ? loads - Sh::kQBufs : 0; leader && k < loads; ++k)
+      mbar_wait(&sm.qfull[k % Sh::kQBufs], (k / Sh::kQBufs) & 1u);
     if constexpr (M == kPair) {
       for (uint32_t u = ring.oldest; leader && u < ring.unit; ++u)
         mbar_wait(&sm.full[u % kUnits], (u / kUnits) & 1u);
@@ -406,7 +412,9 @@ __device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem<M
   const uint32_t id_s = idesc_f16(CG * kRows, Sh::kTile, true, false) | a.negate;
   constexpr uint32_t id_o = idesc_f16(CG * kRows, kHalf, true, true);
   constexpr int kStep = Sh::kBlock >> 4;     // a block in a descriptor's address field
-  const uint64_t q0 = smem_desc_sw128(smem_u32(sm.q), 16, 1024);
+  const uint64_t q00 = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
+  uint64_t q0 = q00;                         // of the item's queries
+  uint32_t qb = 0;
   const uint64_t k0 = smem_desc_sw128(smem_u32(sm.kv), 16, 1024);
   const uint64_t v0 = smem_desc_sw128(smem_u32(sm.kv), M == kPair ? Sh::kAtom : Sh::kBlock, 1024);
   Item it;
@@ -437,12 +445,12 @@ __device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem<M
     if (!wait(&sm.pfull[b], (v / 2) & 1u)) return;
     if constexpr (M == kPair) {
 #pragma unroll 1
-      for (uint32_t u = 0; u < kVBlocks / kVUnit; ++u, ++unit, blk = (blk + kVUnit) % Sh::kRing) {
+      for (uint32_t u = 0; u < kVBlocks / kVUnit; ++u, ++unit, blk = wrap(blk + kVUnit)) {
         if (!wait(&sm.full[unit % kUnits], (unit / kUnits) & 1u)) return;
         if (elect_one()) {
 #pragma unroll
           for (uint32_t c = 0; c < kVUnit; ++c) {
-            const uint64_t vd = v0 + (blk + c) % Sh::kRing * kStep;
+            const uint64_t vd = v0 + wrap(blk + c) * kStep;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
               const int step = (int)(u * kVUnit + c) * 2 + s;
@@ -475,23 +483,25 @@ __device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem<M
     for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
       if (M == kPair && t < it.t1 - 2) values(j - 2, value_steps<M>(it, t + 2), t + 2 == it.t1 - 1);
       if (ok && t == it.t1 - 1) {
-        if (!wait(&sm.qfull, nq & 1u)) break;
+        qb = nq % Sh::kQBufs;
+        q0 = q00 + qb * (Sh::kQBytes >> 4);
+        if (!wait(&sm.qfull[qb], (nq / Sh::kQBufs) & 1u)) break;
         if (Sh::kQTm > 0 && !wait(&sm.qtm, nq & 1u)) break;
         ++nq;
       }
       const uint32_t b = j % 2, d = tmem + Sh::s_col(b);
       auto scores_done = [&]() {
         tc_commit<CG>(&sm.sfull[b]);
-        if (t == it.t0) tc_commit<CG>(&sm.qempty);
+        if (t == it.t0) tc_commit<CG>(&sm.qempty[qb]);
       };
       if constexpr (M == kPair) {
 #pragma unroll 1
-        for (uint32_t u = 0; ok && u < kBlocks / kKUnit; ++u, ++unit, blk = (blk + kKUnit) % Sh::kRing) {
+        for (uint32_t u = 0; ok && u < kBlocks / kKUnit; ++u, ++unit, blk = wrap(blk + kKUnit)) {
           if (!wait(&sm.full[unit % kUnits], (unit / kUnits) & 1u)) break;
           if (elect_one()) {
 #pragma unroll
             for (uint32_t c = 0; c < kKUnit; ++c)
-              block_products(d, (int)(u * kKUnit + c), k0 + (blk + c) % Sh::kRing * kStep, u == 0 && c == 0);
+              block_products(d, (int)(u * kKUnit + c), k0 + wrap(blk + c) * kStep, u == 0 && c == 0);
             tc_commit<CG>(&sm.empty[unit % kUnits]);
             if (u == kBlocks / kKUnit - 1) scores_done();
           }
@@ -743,7 +753,7 @@ __device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem<M>
           const int key = past + z / kChunks, chunk = z % kChunks;
           uint8_t* at;
           if constexpr (M == kPair)
-            at = sm.kv + ((seq + (uint32_t)(key / Sh::kVKeys)) % Sh::kRing) * Sh::kBlock +
+            at = sm.kv + wrap(seq + (uint32_t)(key / Sh::kVKeys)) * Sh::kBlock +
                  (chunk >> 3) * Sh::kAtom + (key % Sh::kVKeys) * 128;
           else
             at = sm.kv + ((j % Sh::kStages) * kBlocks + (chunk >> 3)) * Sh::kBlock + key * 128;
@@ -850,10 +860,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (tid == 0) {
     for (int b = 0; b < kUnits; ++b) mbar_init(&sm.full[b], 1 + (b == 0 ? kStalledArrivals : 0));
     for (int b = 0; b < kUnits; ++b) mbar_init(&sm.empty[b], 1);
-    mbar_init(&sm.qfull, 1);
     mbar_init(&sm.qtm, kSoftmaxWarps);
-    mbar_init(&sm.qempty, 1);
     for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.qfull[b], 1);
+      mbar_init(&sm.qempty[b], 1);
       mbar_init(&sm.sfull[b], 1);
       mbar_init(&sm.pfull[b], kSoftmaxWarps * CG);   // a warp each, of both CTAs in a pair's first
       mbar_init(&sm.vtail[b], 1);
@@ -892,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // How a call is cut: by the rows of a request (on average), and its keys into parts
-// where items are fewer than CTAs.
+// where items are few.  Lengths are the device's: the table's width stands for them.
 struct Plan {
   int mode, item_rows, splits;
 };
@@ -903,8 +913,10 @@ Plan plan_for(int rows, int S, int H, int reqs, int64_t cap) {
   p.item_rows = p.mode == kPair ? Shape<kPair>::kItemRows : p.mode == kWide ? Shape<kWide>::kItemRows
                                                                           : Shape<kNarrow>::kItemRows;
   const int64_t items = (pairs + p.item_rows - 1) / p.item_rows * reqs * 2 * S;
+  // 128 keys take a pair about 2.9 us, a CTA alone 3.4; a part has as many at least.
   const int64_t tiles = (cap + 127) / 128, ctas = device_sms() / (p.mode == kPair ? 2 : 1);
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(ctas / items, tiles / 2), 64));
+  p.splits = choose_parts(items, ctas, tiles * (p.mode == kPair ? 2.9 : 3.4) + 4.0, (int64_t)rows * S * H, kDv,
+                          tiles);
   return p;
 }
 

@@ -692,15 +692,14 @@ constexpr int kSmem = (int)sizeof(PrefillSmem) + 1024;
 struct Plan {
   int cg, splits;
 };
-// Parts that an item's keys are split into: as many as SMs are left idle
-// otherwise, but eight key tiles each at least.
 Plan plan_for(int Tq, int Tk, int n, int H) {
   Plan p;
   p.cg = (int64_t)Tq > (int64_t)n * Shape<1>::kBlockQ ? 2 : 1;   // sequences longer than a CTA's block
   const int block = p.cg == 2 ? Shape<2>::kBlockQ : Shape<1>::kBlockQ;
   const int64_t items = std::max<int64_t>(((int64_t)Tq + block - 1) / block, n) * H;
-  const int64_t most = std::min<int64_t>(device_sms() / p.cg / items, Tk / (8 * kTileK));
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, 16));
+  // A key tile takes an item about 1.9 us; a part has four at least.
+  const int64_t tiles = (Tk / n + kTileK - 1) / kTileK;
+  p.splits = choose_parts(items, device_sms() / p.cg, tiles * 1.9 + 5.0, (int64_t)Tq * H, kDv, tiles / 4);
   return p;
 }
 

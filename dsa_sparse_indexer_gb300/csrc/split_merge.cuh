@@ -3,8 +3,10 @@
 // Part p of row i holds O_p (fp32, normalised by its own sum) and l_p, the
 // base-2 log of that sum (-inf: nothing visible, O_p then unwritten and not
 // read): out = sum_p w_p O_p / sum_p w_p and lse2 = M + log2 sum_p w_p with
-// M = max_p l_p, w_p = 2^(l_p - M).  A warp takes a row, its lanes four
-// neighbouring values each of every 128; the parts' loads are independent.
+// M = max_p l_p, w_p = 2^(l_p - M).  A block takes a row: groups of D / 4 threads
+// take every kGroups-th part, a thread four neighbouring values, and add up in
+// shared memory; the parts' loads are independent.  (128 rows of 76 parts, 20 MB: a
+// warp a row with all parts in turn left most SMs idle, 45 us.)
 #pragma once
 
 #include "tcgen05.cuh"
@@ -24,52 +26,79 @@ struct MergeArgs {
   float* lse2;               // [rows]
 };
 
+constexpr int kMergeGroups = 4, kMaxParts = 64;
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) merge_parts_kernel(const MergeArgs a) {
-  constexpr int kV = D / 128;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= a.rows) return;
+__global__ void __launch_bounds__(kMergeGroups * D / 4) merge_parts_kernel(const MergeArgs a) {
+  constexpr int kLanes = D / 4;              // threads of a group
+  __shared__ float weight[kMaxParts];
+  __shared__ float4 sums[kMergeGroups - 1][kLanes];
+  const int64_t row = blockIdx.x;
   const int entry = (int)((row / a.H) % a.per_outer);
   if (entry < __ldg(a.bounds) || entry >= __ldg(a.bounds + a.n)) return;
-  float m = -INFINITY;
-  for (int p = lane; p < a.parts; p += 32) m = fmaxf(m, a.l[p * a.rows + row]);
+  const int tid = threadIdx.x, group = tid / kLanes, at = tid % kLanes;
+  float l = -INFINITY, lse = 0.f;
+  if (tid < 32) {                            // the first warp: weights and their sum
+    float l2 = -INFINITY;
+    if (tid < a.parts) l = a.l[tid * a.rows + row];
+    if (tid + 32 < a.parts) l2 = a.l[(tid + 32) * a.rows + row];
+    float m = fmaxf(l, l2);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-  const float ref = m == -INFINITY ? 0.f : m;
-  float total = 0.f;
-  float4 acc[kV];
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+    const float w = fast_exp2(l - ref), w2 = fast_exp2(l2 - ref);
+    float total = w + w2;
 #pragma unroll
-  for (int v = 0; v < kV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int p = 0; p < a.parts; ++p) {
-    const float w = fast_exp2(a.l[p * a.rows + row] - ref);
-    if (w != 0.f) {
-      const float4* src = reinterpret_cast<const float4*>(a.o + (p * a.rows + row) * D) + lane;
-#pragma unroll
-      for (int v = 0; v < kV; ++v) {
-        const float4 x = src[v * 32];
-        acc[v].x = fmaf(w, x.x, acc[v].x);
-        acc[v].y = fmaf(w, x.y, acc[v].y);
-        acc[v].z = fmaf(w, x.z, acc[v].z);
-        acc[v].w = fmaf(w, x.w, acc[v].w);
-      }
-    }
-    total += w;
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    weight[tid] = w * inv;
+    weight[tid + 32] = w2 * inv;
+    lse = total == 0.f ? -INFINITY : ref + log2f(total);
   }
-  const float inv = total == 0.f ? 0.f : 1.f / total;
-  uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D) + lane;
+  __syncthreads();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = group; p < a.parts; p += kMergeGroups) {
+    const float w = weight[p];
+    if (w != 0.f) {                          // else it may be unwritten
+      const float4 x = __ldg(reinterpret_cast<const float4*>(a.o + (p * a.rows + row) * D) + at);
+      acc.x = fmaf(w, x.x, acc.x);
+      acc.y = fmaf(w, x.y, acc.y);
+      acc.z = fmaf(w, x.z, acc.z);
+      acc.w = fmaf(w, x.w, acc.w);
+    }
+  }
+  if (group > 0) sums[group - 1][at] = acc;
+  __syncthreads();
+  if (group > 0) return;
 #pragma unroll
-  for (int v = 0; v < kV; ++v)
-    dst[v * 32] = make_uint2(pack16<BF16>(acc[v].x * inv, acc[v].y * inv),
-                             pack16<BF16>(acc[v].z * inv, acc[v].w * inv));
-  if (lane == 0) a.lse2[row] = total == 0.f ? -INFINITY : ref + log2f(total);
+  for (int g = 0; g < kMergeGroups - 1; ++g) {
+    const float4 x = sums[g][at];
+    acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+  }
+  reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D)[at] =
+      make_uint2(pack16<BF16>(acc.x, acc.y), pack16<BF16>(acc.z, acc.w));
+  if (tid == 0) a.lse2[row] = lse;
 }
 
 template <int D, bool BF16>
 inline cudaError_t launch_merge(const MergeArgs& a, cudaStream_t stream) {
-  return launch_kernel(merge_parts_kernel<D, BF16>, dim3((unsigned)((a.rows + 7) / 8)), dim3(256), 0,
+  return launch_kernel(merge_parts_kernel<D, BF16>, dim3((unsigned)a.rows), dim3(kMergeGroups * D / 4), 0,
                        stream, 0, a);
+}
+
+// Parts to split each of `items` (of about `item_us` microseconds) into, for `ctas`
+// at a time: the rounds that the parts take, and what writing and reading a
+// part's outputs again costs (rows of 4 D bytes, at 5 TB/s, and a launch).
+inline int choose_parts(int64_t items, int64_t ctas, double item_us, int64_t rows, int D, int64_t most) {
+  if (rows > (1 << 24)) return 1;
+  int best = 1;
+  double least = (double)((items + ctas - 1) / ctas) * item_us;
+  for (int p = 2; p <= (int)(most < kMaxParts ? most : kMaxParts); ++p) {
+    const double us = (double)((items * p + ctas - 1) / ctas) * item_us / p + 4.0 + 1.6e-6 * D * rows * p;
+    if (us < least * 0.97) least = us, best = p;
+  }
+  return best;
 }
 
 }  // namespace dsa

@@ -710,7 +710,7 @@ dsa_status dsa_indexer_key_insert(const uint16_t* k, int64_t k_token, const floa
  *   q_out        [T][H][DSA_IDX_DIM] e4m3 codes, 16-byte aligned; weights_out
  *                [T][H] fp32 (may be weights itself)
  * Errors: T < 0, H < 1, factor not finite, the rotation's as above, null pointers,
- *         misalignment -> INVALID_ARG; too many blocks -> UNSUPPORTED.
+ *         misalignment -> INVALID_ARG; T * H >= 2^31 -> UNSUPPORTED.
  */
 dsa_status dsa_indexer_query_fp8(const uint16_t* q, int64_t q_token, int64_t q_head,
                                  const float* weights, float factor, const int32_t* positions,
