@@ -546,31 +546,31 @@ __device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem<M
   __syncwarp();
 }
 
-// Which of the 32 keys from local token `from` on row `tok` (of the request's) sees.
+// Which of the 32 keys from local token `from` on row `tok` (of the request's) sees:
+// those that all rows see, then the chain's up to itself, or a tree's one by one (as
+// many as are drafted; every key asked for one by one took an item 4 us).
+__device__ __forceinline__ uint32_t first_bits(int n) {
+  return n >= 32 ? kFull : n <= 0 ? 0u : (1u << n) - 1u;
+}
 __device__ __forceinline__ uint32_t seen32(const DecodeArgs& a, const Item& it, int tok, int from) {
-  uint32_t seen = 0;
+  if (!a.mask) {
+    const int own = (int)a.sm.local_len((uint32_t)max(it.base + tok + 1, 0), it.shard);
+    return first_bits(min(own, it.nvis) - from);
+  }
+  uint32_t seen = first_bits(it.nfree - from), word = 0;
   int at = -1;
-  uint32_t word = 0;
 #pragma unroll 1
-  for (int k = 0; k < 32; ++k) {
-    const int l = from + k;
-    if (l >= it.nvis) break;
-    bool see = l < it.nfree;
-    if (!see) {
-      const int i = (int)a.sm.global_id(it.shard, (uint32_t)l) - it.base;   // the request's row
-      if (!a.mask) {
-        see = i <= tok;
-      } else if (i < 0) {
-        see = true;
-      } else if ((i >> 5) < a.words) {
-        if ((i >> 5) != at) {
-          at = i >> 5;
-          word = (uint32_t)__ldg(a.mask + (int64_t)(it.tok0 + tok) * a.words + at);
-        }
-        see = (word >> (i & 31)) & 1u;
+  for (int l = max(from, it.nfree); l < min(from + 32, it.nvis); ++l) {
+    const int i = (int)a.sm.global_id(it.shard, (uint32_t)l) - it.base;   // the request's row
+    bool see = i < 0;
+    if (!see && (i >> 5) < a.words) {
+      if ((i >> 5) != at) {
+        at = i >> 5;
+        word = (uint32_t)__ldg(a.mask + (int64_t)(it.tok0 + tok) * a.words + at);
       }
+      see = (word >> (i & 31)) & 1u;
     }
-    seen |= (uint32_t)see << k;
+    seen |= (uint32_t)see << (l - from);
   }
   return seen;
 }
