@@ -46,6 +46,7 @@ template <int P>
 struct Turn {
   float c[kVals], s[kVals];
   int off;                                   // kLaneOff: the partner's lane
+  bool any;                                  // one of the eight turns (kLaneOff: all or none do)
   int partner[P == kAnywhere ? kVals : 1];   // kAnywhere: its place in the row
 };
 
@@ -58,6 +59,7 @@ __device__ __forceinline__ Turn<P> find_turn(const TurnArgs& a, int token, int l
   const float* row = a.table + (int64_t)(in ? pos : 0) * a.rot;
   const int half = a.rot / 2, i0 = lane16 * kVals - a.first;   // the first value's place among the turning
   t.off = lane16;
+  t.any = in && i0 + kVals > 0 && i0 < a.rot;
   if (P == kLaneOff && i0 >= 0 && i0 < a.rot) t.off = lane16 + (i0 < half ? half : -half) / kVals;
 #pragma unroll
   for (int e = 0; e < kVals; ++e) {
@@ -123,9 +125,12 @@ __device__ __forceinline__ void partners(const Turn<P>& t, float* row, int lane1
     for (int e = 0; e < kVals; ++e) p[e] = row[t.partner[e]];
   }
 }
-// A carried value is its bits (a partner that is infinite must not reach it).
-__device__ __forceinline__ float turned(float x, float c, float p, float s) {
-  return s == 0.f ? x * c : fmaf(x, c, p * s);
+// Value e of the row, turned; a carried one as it is (its partner may be infinite).
+template <int P>
+__device__ __forceinline__ float turned(const Turn<P>& t, int e, float x, float p) {
+  const bool turns = P == kLaneOff ? t.any : t.s[e] != 0.f || t.c[e] != 1.f;
+  const float y = fmaf(x, t.c[e], p * t.s[e]);
+  return turns ? y : x;
 }
 
 struct KeyArgs {
@@ -174,8 +179,8 @@ __global__ void __launch_bounds__(kThreads) indexer_key_kernel(const KeyArgs a) 
   float p[kVals];
   partners<P>(t, rows[P == kAnywhere ? r : 0], lane16, x, p);
 #pragma unroll
-  for (int e = 0; e < kVals; ++e) x[e] = turned(x[e], t.c[e], p[e], t.s[e]);
-  const uint2 code = codes8(x);
+  for (int e = 0; e < kVals; ++e) p[e] = turned<P>(t, e, x[e], p[e]);
+  const uint2 code = codes8(p);
   if (!there) return;
   for (int sh = 0; sh < a.S; ++sh) {
     const int slot = __ldg(a.slots + (int64_t)sh * a.T + token);
@@ -209,13 +214,10 @@ __device__ __forceinline__ float scale_for(F amax) {
   return ldexpf(1.f, max(m > (F)0.875 ? e - 8 : e - 9, -126));
 }
 
-// Whether z (to be rounded to e4m3) is so close to the middle between two codes that
-// fp32's error may have moved it across: the 20 bits behind the three kept ones; codes
-// below 2^-6 are 2^-9 apart, as those from 2^-6 on.
-__device__ __forceinline__ bool near_middle(float z) {
-  float w = fabsf(z);
-  if (w < 0.015625f) w += 0.015625f;
-  return (__float_as_uint(w) & 0xFFFFFu) - 0x7FFF8u <= 16u;
+template <int P>
+__device__ __forceinline__ double exact_turned(const Turn<P>& t, int e, float x, float p) {
+  const bool turns = P == kLaneOff ? t.any : t.s[e] != 0.f || t.c[e] != 1.f;
+  return turns ? fma((double)x, (double)t.c[e], (double)p * (double)t.s[e]) : (double)x;
 }
 
 template <int P, int kHeads>
@@ -238,53 +240,54 @@ __global__ void __launch_bounds__(kThreads) indexer_query_kernel(const QueryArgs
     float x[kVals], p[kVals], y[kVals];
     unpack8(raw[k], x);
     partners<P>(t, rows[P == kAnywhere ? r : 0], lane16, x, p);
-    float amax = 0.f;
+    float amax = 0.f;                        // (of what is no NaN)
 #pragma unroll
     for (int e = 0; e < kVals; ++e) {
-      y[e] = turned(x[e], t.c[e], p[e], t.s[e]);
-      amax = fmaxf(amax, fabsf(y[e]) <= 3.4028235e38f ? fabsf(y[e]) : 0.f);
+      y[e] = turned<P>(t, e, x[e], p[e]);
+      amax = fmaxf(amax, fabsf(y[e]));
     }
 #pragma unroll
     for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
     float scale = scale_for(amax);
-    float inv = 1.f / scale;                 // exact: a power of two (of 2^-126, 2^126)
-    // A largest value near a border between two scales (on it lie bf16 values), or a
-    // turned one near a middle between two codes (carried ones are exact, and one in
-    // sixteen on a middle): once more in 64 bits.
-    const float top32 = amax * inv;
-    bool near = (fabsf(top32 - 448.f) < 448.f * 1e-6f && top32 != 448.f) || fabsf(top32 - 224.f) < 224.f * 1e-6f;
+    const float inv = 1.f / scale;           // exact: a power of two
+    // fp32's error may have moved a turned value across the middle between two codes
+    // if its codes a little further in and out differ (carried values are exact); and
+    // the largest across the border between two scales (on which bf16 values lie), if
+    // it is near.  Those heads, and infinite ones, go once more through 64 bits.
+    const float in = t.any ? inv * (1.f - 0x1p-21f) : inv, out = t.any ? inv * (1.f + 0x1p-21f) : inv;
+    float z[kVals];
 #pragma unroll
-    for (int e = 0; e < kVals; ++e) near = near || (t.s[e] != 0.f && near_middle(y[e] * inv));
+    for (int e = 0; e < kVals; ++e) z[e] = y[e] * in;
+    uint2 code = codes8(z);
+#pragma unroll
+    for (int e = 0; e < kVals; ++e) z[e] = y[e] * out;
+    const uint2 outer = codes8(z);
+    const float top32 = amax * inv;
+    const bool near = code.x != outer.x || code.y != outer.y || !(amax <= 3.4028235e38f) ||
+                      (fabsf(top32 - 448.f) < 448.f * 1e-6f && top32 != 448.f) ||
+                      fabsf(top32 - 224.f) < 224.f * 1e-6f;
     if (__any_sync(kFull, near)) {
       keep_branch();
       double top = 0.0;
 #pragma unroll
-      for (int e = 0; e < kVals; ++e) {
-        const double d = t.s[e] == 0.f ? (double)x[e] * t.c[e]
-                                       : fma((double)x[e], (double)t.c[e], (double)p[e] * (double)t.s[e]);
-        if (fabsf(y[e]) <= 3.4028235e38f) top = fmax(top, fabs(d));
-      }
+      for (int e = 0; e < kVals; ++e)
+        if (fabsf(y[e]) <= 3.4028235e38f) top = fmax(top, fabs(exact_turned<P>(t, e, x[e], p[e])));
 #pragma unroll
       for (int o = 8; o; o >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, o));
       scale = scale_for(top);
-      inv = 1.f / scale;
 #pragma unroll
       for (int e = 0; e < kVals; ++e) {
-        const double d = (t.s[e] == 0.f ? (double)x[e] * t.c[e]
-                                        : fma((double)x[e], (double)t.c[e], (double)p[e] * (double)t.s[e])) * inv;
         // To fp32 with what is cut kept in the last bit, so that the next rounding
         // sees on which side of a middle it lay.
-        float f = __double2float_rz(d);
-        if ((double)f != d && fabsf(f) <= 3.4028235e38f) f = __uint_as_float(__float_as_uint(f) | 1u);
-        y[e] = f;
+        const double d = exact_turned<P>(t, e, x[e], p[e]) / scale;
+        z[e] = __double2float_rz(d);
+        if ((double)z[e] != d && fabsf(z[e]) <= 3.4028235e38f) z[e] = __uint_as_float(__float_as_uint(z[e]) | 1u);
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < kVals; ++e) y[e] *= inv;
+      code = codes8(z);
     }
     if (h < a.H) {
       const int64_t row = (int64_t)token * a.H + h;
-      *reinterpret_cast<uint2*>(a.q_out + row * kDim + lane16 * kVals) = codes8(y);
+      *reinterpret_cast<uint2*>(a.q_out + row * kDim + lane16 * kVals) = code;
       if (lane16 == 0) a.w_out[row] = a.weights[row] * a.factor * scale;
     }
   }
