@@ -204,15 +204,13 @@ struct QueryArgs {
   float* w_out;                              // [T][H]
 };
 
-// The smallest power of two s with amax <= 448 s (448 = 0.875 * 2^9), from 2^-126
-// on; 1 where amax is 0.
-template <typename F>
-__device__ __forceinline__ float scale_for(F amax) {
-  if (!(amax > 0)) return 1.f;
-  int e;
-  const F m = frexp(amax, &e);
-  return ldexpf(1.f, max(m > (F)0.875 ? e - 8 : e - 9, -126));
+// The exponent field of the smallest power of two s with amax <= 448 s (448 = 1.75 *
+// 2^8), from 2^-126 on, from amax's bits; s = 1 where amax is 0.
+__device__ __forceinline__ int scale_exponent(uint32_t amax) {
+  const int e = (int)(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return amax == 0 ? 127 : max(e, 1);
 }
+__device__ __forceinline__ float power(int exponent_field) { return __uint_as_float((uint32_t)exponent_field << 23); }
 
 template <int P>
 __device__ __forceinline__ double exact_turned(const Turn<P>& t, int e, float x, float p) {
@@ -248,8 +246,8 @@ __global__ void __launch_bounds__(kThreads) indexer_query_kernel(const QueryArgs
     }
 #pragma unroll
     for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-    float scale = scale_for(amax);
-    const float inv = 1.f / scale;           // exact: a power of two
+    int field = scale_exponent(__float_as_uint(amax));
+    const float inv = power(254 - field);    // 1 / s
     // fp32's error may have moved a turned value across the middle between two codes
     // if its codes a little further in and out differ (carried values are exact); and
     // the largest across the border between two scales (on which bf16 values lie), if
@@ -262,10 +260,9 @@ __global__ void __launch_bounds__(kThreads) indexer_query_kernel(const QueryArgs
 #pragma unroll
     for (int e = 0; e < kVals; ++e) z[e] = y[e] * out;
     const uint2 outer = codes8(z);
-    const float top32 = amax * inv;
+    const uint32_t part = __float_as_uint(amax) & 0x7FFFFFu;   // next to 1.75, but not on it
     const bool near = code.x != outer.x || code.y != outer.y || !(amax <= 3.4028235e38f) ||
-                      (fabsf(top32 - 448.f) < 448.f * 1e-6f && top32 != 448.f) ||
-                      fabsf(top32 - 224.f) < 224.f * 1e-6f;
+                      (part - 0x5FFFF8u <= 16u && part != 0x600000u);
     if (__any_sync(kFull, near)) {
       keep_branch();
       double top = 0.0;
@@ -274,12 +271,13 @@ __global__ void __launch_bounds__(kThreads) indexer_query_kernel(const QueryArgs
         if (fabsf(y[e]) <= 3.4028235e38f) top = fmax(top, fabs(exact_turned<P>(t, e, x[e], p[e])));
 #pragma unroll
       for (int o = 8; o; o >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, o));
-      scale = scale_for(top);
+      // Rounded up: a value just past the border stays past it.
+      field = scale_exponent(__float_as_uint(__double2float_ru(top)));
 #pragma unroll
       for (int e = 0; e < kVals; ++e) {
         // To fp32 with what is cut kept in the last bit, so that the next rounding
         // sees on which side of a middle it lay.
-        const double d = exact_turned<P>(t, e, x[e], p[e]) / scale;
+        const double d = exact_turned<P>(t, e, x[e], p[e]) * (double)power(254 - field);
         z[e] = __double2float_rz(d);
         if ((double)z[e] != d && fabsf(z[e]) <= 3.4028235e38f) z[e] = __uint_as_float(__float_as_uint(z[e]) | 1u);
       }
@@ -288,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) indexer_query_kernel(const QueryArgs
     if (h < a.H) {
       const int64_t row = (int64_t)token * a.H + h;
       *reinterpret_cast<uint2*>(a.q_out + row * kDim + lane16 * kVals) = code;
-      if (lane16 == 0) a.w_out[row] = a.weights[row] * a.factor * scale;
+      if (lane16 == 0) a.w_out[row] = a.weights[row] * a.factor * power(field);
     }
   }
 }
@@ -302,13 +300,13 @@ int partner_of(int rot, int first, int layout) {
 
 template <int P>
 cudaError_t launch_query(QueryArgs& a, bool few, cudaStream_t stream) {
-  // Eight heads a thread share its cosines and sines; with few tokens, two, which
+  // Four heads a thread share its cosines and sines; with few tokens, two, which
   // are more blocks.
-  const int heads = kRows * (few ? 2 : 8);
+  const int heads = kRows * (few ? 2 : 4);
   a.per_token = (a.H + heads - 1) / heads;
   const dim3 grid((unsigned)((int64_t)a.T * a.per_token));
   return few ? launch_kernel(indexer_query_kernel<P, 2>, grid, dim3(kThreads), 0, stream, 0, a)
-             : launch_kernel(indexer_query_kernel<P, 8>, grid, dim3(kThreads), 0, stream, 0, a);
+             : launch_kernel(indexer_query_kernel<P, 4>, grid, dim3(kThreads), 0, stream, 0, a);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
