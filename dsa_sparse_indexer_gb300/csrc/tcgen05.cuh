@@ -166,9 +166,9 @@ __device__ __forceinline__ void cta_abort(int* abort, uint32_t* flags) {
   raise_flag(flags, DSA_FLAG_TIMEOUT);
   *reinterpret_cast<volatile int*>(abort) = 1;
 }
-// Bounded wait that also gives up once another role has aborted.
+// Bounded wait (a few seconds) that also gives up once another role has aborted.
 __device__ __forceinline__ bool wait_or_abort(const int* abort, uint64_t* bar, uint32_t parity) {
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+  for (uint32_t i = 0; i < kWaitPolls / 4; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 63) == 63 && cta_aborted(abort)) return false;
   }
@@ -342,77 +342,23 @@ __device__ __forceinline__ void item_done(WorkSlots<Item>& s, uint32_t n) {
   if ((threadIdx.x & 31) == 0) mbar_arrive1(&s.empty[n & 1u]);
 }
 
-// Consecutive fp32 columns of this warp's 32 tensor-memory lanes.  A load's
-// registers may be used after tmem_wait_ld of the same array: its empty
-// statements name every register as read and written, so that no use of them
-// is scheduled before the wait.
-#define DSA_TC_LD32(o)                                                                       \
-  asm volatile(                                                                              \
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, " \
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, " \
-      "%28, %29, %30, %31}, [%32];"                                                          \
-      : "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]),       \
-        "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]),       \
-        "=r"(r[o + 10]), "=r"(r[o + 11]), "=r"(r[o + 12]), "=r"(r[o + 13]), "=r"(r[o + 14]),  \
-        "=r"(r[o + 15]), "=r"(r[o + 16]), "=r"(r[o + 17]), "=r"(r[o + 18]), "=r"(r[o + 19]),  \
-        "=r"(r[o + 20]), "=r"(r[o + 21]), "=r"(r[o + 22]), "=r"(r[o + 23]), "=r"(r[o + 24]),  \
-        "=r"(r[o + 25]), "=r"(r[o + 26]), "=r"(r[o + 27]), "=r"(r[o + 28]), "=r"(r[o + 29]),  \
-        "=r"(r[o + 30]), "=r"(r[o + 31])                                                     \
-      : "r"(taddr + (uint32_t)(o)))
-#define DSA_TC_LD16(o)                                                                        \
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, "  \
-               "%8, %9, %10, %11, %12, %13, %14, %15}, [%16];"                              \
-               : "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]),           \
-                 "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7]),           \
-                 "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]), "=r"(r[o + 11]),         \
-                 "=r"(r[o + 12]), "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15])        \
-               : "r"(taddr + (uint32_t)(o)))
-#define DSA_TC_USE16(o)                                                                     \
-  asm volatile(""                                                                           \
-               : "+r"(r[o + 0]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]),           \
-                 "+r"(r[o + 4]), "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7]),           \
-                 "+r"(r[o + 8]), "+r"(r[o + 9]), "+r"(r[o + 10]), "+r"(r[o + 11]),         \
-                 "+r"(r[o + 12]), "+r"(r[o + 13]), "+r"(r[o + 14]), "+r"(r[o + 15]))
-#define DSA_TC_ST8(o)                                                                       \
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, "  \
-               "%8};" ::"r"(taddr + (uint32_t)(o)),                                         \
-               "r"(r[o + 0]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]),   \
-               "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])                                  \
-               : "memory")
-#define DSA_TC_ST16(o)                                                                      \
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, " \
-               "%8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr + (uint32_t)(o)),  \
-               "r"(r[o + 0]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]),   \
-               "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7]), "r"(r[o + 8]), "r"(r[o + 9]),   \
-               "r"(r[o + 10]), "r"(r[o + 11]), "r"(r[o + 12]), "r"(r[o + 13]),              \
-               "r"(r[o + 14]), "r"(r[o + 15])                                               \
-               : "memory")
-
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[N]) {
-  static_assert(N == 16 || N % 32 == 0, "16 columns, or steps of 32");
-  if constexpr (N == 16) {
-    DSA_TC_LD16(0);
-  } else {
-#pragma unroll
-    for (int o = 0; o < N; o += 32) DSA_TC_LD32(o);
-  }
-}
-template <int N>
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N]) {
+// Sixteen registers' uses are not scheduled before the wait for a load of them: empty
+// statements name them as read and written.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int o = 0; o < N; o += 16) DSA_TC_USE16(o);
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
-template <int N>
-__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[N]) {
-  static_assert(N == 8 || N % 16 == 0, "8 columns, or steps of 16");
-  if constexpr (N == 8) {
-    DSA_TC_ST8(0);
-  } else {
-#pragma unroll
-    for (int o = 0; o < N; o += 16) DSA_TC_ST16(o);
-  }
+// Sixteen columns of a warp's 32 lanes, a thread a lane.
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, "
+               "%8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+               "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+               "r"(r[15])
+               : "memory");
 }
 
 // Sixteen lanes as fragments: of 8 fp32 columns a thread has, in registers 4 i to 4
@@ -441,11 +387,6 @@ __device__ __forceinline__ void tmem_store_pairs(uint32_t taddr, const uint32_t 
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-#undef DSA_TC_LD32
-#undef DSA_TC_LD16
-#undef DSA_TC_USE16
-#undef DSA_TC_ST8
-#undef DSA_TC_ST16
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
@@ -465,7 +406,7 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-// Two fused multiply-adds, products or additions in one instruction, each
+// Two fused multiply-adds or additions in one instruction, each
 // rounded as the scalar operation would be.
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   uint64_t r;
@@ -482,14 +423,6 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
       : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
   return *reinterpret_cast<float2*>(&r);
 }
-__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
-  return *reinterpret_cast<float2*>(&r);
-}
-
 // Word i of lane j (of four neighbours) and word j of lane i change places.
 __device__ __forceinline__ void transpose4(uint32_t (&w)[4], int lane) {
 #pragma unroll

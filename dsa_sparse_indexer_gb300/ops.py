@@ -571,6 +571,12 @@ def _no_grad(*tensors):
                          "(call it under torch.no_grad())")
 
 
+def _changed(*outs):
+    """Outputs that the caller gave count as modified in place."""
+    for t in outs:
+        torch.autograd.graph.increment_version(t)
+
+
 @functools.lru_cache(maxsize=4096)
 def _mla_prefill_work(device: int, Tq: int, Tk: int, n: int, H: int) -> int:
     with torch.cuda.device(device):
@@ -632,6 +638,7 @@ def mla_prefill(q, k_nope, k_pe, v, cu_q, cu_k, scale: float, causal: bool = Tru
             _ptr(k_pe), pe_token, _ptr(v), v_token, v_head, _ptr(cu_q), _ptr(cu_k), n, Tq, Tk, H,
             ROPE_DTYPES[dtype], float(scale), int(bool(causal)), _ptr(out), _ptr(lse2), _ptr(work),
             _ptr(err_flags), _raw_stream(q))
+    _changed(out, lse2)
     return out, lse2
 
 
@@ -699,6 +706,7 @@ def mla_decode(q, kv_cache, block_table, block_size: int, query_starts, seq_lens
             max_blocks, block_size, _ptr(query_starts), _ptr(seq_lens), _ptr(tree_mask), words, rows,
             S, I, H, float(scale), _ptr(out), _ptr(lse2), _ptr(work), _ptr(err_flags),
             _raw_stream(q))
+    _changed(out, lse2)
     return out, lse2
 
 
@@ -732,13 +740,14 @@ def indexer_key_insert(k, norm_weight, norm_bias, eps: float, positions, cos_sin
         raise ValueError("norm_weight and norm_bias must have 128 entries")
     if tuple(slot_mapping.shape) != (S, T):
         raise ValueError("slot_mapping must be [S, T]")
-    _no_grad(k, norm_weight, norm_bias)
+    _no_grad(k, norm_weight, norm_bias, cos_sin_cache)
     context = _together(k, norm_weight, norm_bias, positions, cos_sin_cache, slot_mapping, k_cache,
                         err_flags)
     _launch(context, "dsa_indexer_key_insert", _ptr(k), k_token, _ptr(norm_weight),
             _ptr(norm_bias), float(eps), _ptr(positions), _ptr(cos_sin_cache),
             cos_sin_cache.shape[0], cos_sin_cache.shape[1], first, ROPE_LAYOUTS[layout],
             _ptr(slot_mapping), T, S, _ptr(k_cache), n_slots, _ptr(err_flags), _raw_stream(k))
+    _changed(k_cache)
     return k_cache
 
 
@@ -770,10 +779,11 @@ def indexer_query_fp8(q, weights, positions, cos_sin_cache, factor: float = 1.0,
     _need(weights_out, "weights_out", torch.float32, 2)
     if tuple(q_out.shape) != (T, H, IDX_DIM) or tuple(weights_out.shape) != (T, H):
         raise ValueError("q_out must be [T, H, 128] and weights_out [T, H]")
-    _no_grad(q, weights, weights_out)
+    _no_grad(q, weights, weights_out, cos_sin_cache)
     context = _together(q, weights, positions, cos_sin_cache, q_out, weights_out, err_flags)
     _launch(context, "dsa_indexer_query_fp8", _ptr(q), q_token, q_head, _ptr(weights),
             float(factor), _ptr(positions), _ptr(cos_sin_cache), cos_sin_cache.shape[0],
             cos_sin_cache.shape[1], first, ROPE_LAYOUTS[layout], T, H, _ptr(q_out),
             _ptr(weights_out), _ptr(err_flags), _raw_stream(q))
+    _changed(q_out, weights_out)
     return q_out, weights_out

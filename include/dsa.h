@@ -649,7 +649,8 @@ int64_t dsa_mla_prefill_work(int Tq, int Tk, int n, int H);
  *         mask_words < 1 with a mask, scale not finite, null pointers,
  *         misalignment -> INVALID_ARG; S not in [1, 64], I < 1, I*S > INT32_MAX,
  *         block_size not 16, 32 or a multiple of 64, n_slots > 2^31 - 1, rows * H
- *         or S * reqs > 2^30 -> UNSUPPORTED; tensor-map encoding -> CUDA.
+ *         or S * reqs > 2^30, too many CTAs -> UNSUPPORTED; tensor-map encoding
+ *         -> CUDA.
  */
 dsa_status dsa_mla_decode(const uint16_t* q, const uint16_t* kv_cache, int64_t n_slots,
                           const int32_t* block_table, int reqs, int max_blocks, int block_size,

@@ -264,3 +264,48 @@ def test_refusals():
         dsa.mla_decode(*args, float("inf"))
     none = dsa.mla_decode(q[:0], cache, table, block, starts * 0, lens, I, SCALE)
     assert none[0].shape == (1, 0, 4, 512)
+
+
+@pytest.mark.parametrize("H,drafts", [(16, 1), (128, 1), (128, 2)])
+def test_offsets_past_32_bits(H, drafts):
+    """Pages whose rows lie past 2^31 elements of a shard's cache, and of the cache."""
+    import dsa_sparse_indexer_gb300 as dsa
+    n_slots = 64 * 60000
+    cache = torch.empty((2, n_slots, 576), dtype=torch.bfloat16, device="cuda")
+    args = inputs([drafts], [150], H, 2, 1, 64, seed=21)
+    q, near, table, block, starts, lens, I = args
+    far = table + (60000 - int(table.max()) - 1)
+    for s in range(2):
+        for p in table[s, 0].tolist():
+            at = (p + 60000 - int(table.max()) - 1) * 64
+            cache[s, at:at + 64] = near[s, p * 64:p * 64 + 64]
+    a = dsa.mla_decode(q, cache, far.contiguous(), block, starts, lens, I, SCALE)
+    b = dsa.mla_decode(*args, SCALE)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("H,drafts", [(2, [1]), (128, [5, 3])])
+def test_two_streams_and_the_same_twice(H, drafts):
+    """Two calls at once, each with its own outputs and workspace, give what one gives."""
+    import dsa_sparse_indexer_gb300 as dsa
+    args = inputs(drafts, [2500, 900][:len(drafts)], H, 2, 1, 64, seed=23)
+    want = dsa.mla_decode(*args, SCALE)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got.append(dsa.mla_decode(*args, SCALE))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g[0], want[0]) and torch.equal(g[1], want[1]) for g in got)
+
+
+def test_split_tree():
+    """A tree over few rows: its drafts lie in the last of the parts."""
+    import dsa_sparse_indexer_gb300 as dsa
+    from dsa_sparse_indexer_gb300 import _lib
+    args = inputs([33], [3000], 4, 2, 4, 64, seed=25)
+    mask = tree([33], seed=25)
+    assert _lib.load().dsa_mla_decode_work(33, 2, 4, 1, args[2].shape[2], 64) > 0
+    out, lse2 = dsa.mla_decode(*args, SCALE, tree_mask=mask)
+    check(args, SCALE, mask, out, lse2)

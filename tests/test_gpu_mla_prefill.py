@@ -223,3 +223,45 @@ def test_refusals():
         dsa.mla_prefill(q, kn[:, :1].expand(4, 2, 128), pe, v, cu_q, cu_k, SCALE)
     none = dsa.mla_prefill(q[:0], kn, pe, v, cu_q * 0, cu_k, SCALE)
     assert none[0].shape == (0, 2, 128)
+
+
+def test_no_keys_and_many_sequences():
+    import dsa_sparse_indexer_gb300 as dsa
+    q, kv, pe, cu_q, cu_k = inputs([(5, 0), (3, 0)], 2, torch.bfloat16)
+    out, lse2 = dsa.mla_prefill(q, kv[..., :128], pe, kv[..., 128:], cu_q, cu_k, SCALE)
+    assert (out == 0).all() and torch.isneginf(lse2).all()
+    lens = [((7 * i) % 11, (5 * i) % 23) for i in range(100)]
+    q, kv, pe, cu_q, cu_k = inputs(lens, 2, torch.bfloat16, seed=23)
+    out, lse2 = dsa.mla_prefill(q, kv[..., :128], pe, kv[..., 128:], cu_q, cu_k, SCALE)
+    check(q, kv[..., :128], pe, kv[..., 128:], cu_q, cu_k, SCALE, True, out, lse2)
+
+
+def test_offsets_past_32_bits():
+    """Keys and values whose elements lie past 2^31 of their tensors."""
+    import dsa_sparse_indexer_gb300 as dsa
+    far, H = 66000, 128
+    kv = torch.empty((far + 40, H, 256), dtype=torch.bfloat16, device="cuda")
+    q, near, pe, _, _ = inputs([(5, 40)], H, torch.bfloat16, seed=25)
+    kv[far:] = near
+    pes = torch.empty((far + 40, 64), dtype=torch.bfloat16, device="cuda")
+    pes[far:] = pe
+    i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")   # noqa: E731
+    a = dsa.mla_prefill(q, kv[..., :128], pes, kv[..., 128:], i(0, 0, 5), i(0, far, far + 40), SCALE)
+    b = dsa.mla_prefill(q, near[..., :128], pe, near[..., 128:], i(0, 5), i(0, 40), SCALE)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_two_streams_and_the_same_twice():
+    """Two calls at once, each with its own outputs and workspace, give what one gives."""
+    import dsa_sparse_indexer_gb300 as dsa
+    q, kv, pe, cu_q, cu_k = inputs([(40, 3000), (513, 700)], 2, torch.bfloat16, seed=27)
+    args = (q, kv[..., :128], pe, kv[..., 128:], cu_q, cu_k, SCALE)
+    want = dsa.mla_prefill(*args)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got.append(dsa.mla_prefill(*args))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g[0], want[0]) and torch.equal(g[1], want[1]) for g in got)
