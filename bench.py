@@ -96,7 +96,10 @@ KERNEL_SOURCES = {"shard_topk_pack": ("shard_topk.cu", "fast_select.cuh", "local
                   "rope_table": ("rope.cu", "rope_steps.h"),
                   "rotary_embed": ("rope.cu",),
                   "fp8_cache_insert": ("kv_fp8.cu",),
-                  "fp8_mla_decode": ("attention_fp8.cu",)}
+                  "fp8_mla_decode": ("attention_fp8.cu",),
+                  "mla_prefill": ("mla_prefill.cu", "tcgen05.cuh", "split_merge.cuh"),
+                  "mla_decode": ("mla_decode.cu", "tcgen05.cuh", "split_merge.cuh"),
+                  "indexer_query": ("indexer_cache.cu",)}
 
 
 # ---------------------------------------------------------------------------

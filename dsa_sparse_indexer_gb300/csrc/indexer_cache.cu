@@ -15,8 +15,8 @@
 // at multiples of 8), or anywhere, through shared memory.  A thread finds its cosines
 // and sines once and uses them for all heads it takes.
 // Queries round as the exact values do: a scaled value within fp32's error of a
-// border between two codes, or a largest one near a border between two scales, sends
-// its head through 64 bits (one head in about 300).
+// middle between two codes, or a largest one near a border between two scales, sends
+// its head once more through the arithmetic, with its errors.
 // Measured, replays: MEASURED_QUERY
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -154,6 +154,8 @@ __global__ void __launch_bounds__(kThreads) indexer_key_kernel(const KeyArgs a) 
   const int tok = there ? token : a.T - 1;   // the last block's idle lanes: a row not stored
   float x[kVals], w[kVals], b[kVals];
   unpack8(__ldg(reinterpret_cast<const uint4*>(a.k + tok * a.stride) + lane16), x);
+  // The first 16 shards' slots, a lane each, on their way with the rest.
+  const int mine = lane16 < a.S ? __ldg(a.slots + (int64_t)lane16 * a.T + tok) : -1;
   const Turn<P> t = find_turn<P>(a.turn, tok, lane16);
 #pragma unroll
   for (int v = 0; v < 2; ++v) {
@@ -181,10 +183,9 @@ __global__ void __launch_bounds__(kThreads) indexer_key_kernel(const KeyArgs a) 
 #pragma unroll
   for (int e = 0; e < kVals; ++e) p[e] = turned<P>(t, e, x[e], p[e]);
   const uint2 code = codes8(p);
-  if (!there) return;
   for (int sh = 0; sh < a.S; ++sh) {
-    const int slot = __ldg(a.slots + (int64_t)sh * a.T + token);
-    if (slot < 0) continue;
+    const int slot = sh < kLanes ? __shfl_sync(kFull, mine, sh, kLanes) : __ldg(a.slots + (int64_t)sh * a.T + tok);
+    if (!there || slot < 0) continue;
     if (slot >= a.n_slots) {
       if (lane16 == 0) raise_flag(a.turn.flags, DSA_FLAG_BOUNDS);
       continue;
@@ -212,10 +213,26 @@ __device__ __forceinline__ int scale_exponent(uint32_t amax) {
 }
 __device__ __forceinline__ float power(int exponent_field) { return __uint_as_float((uint32_t)exponent_field << 23); }
 
+// Value e turned and rounded to odd: cut to fp32, with the last bit set where
+// anything was cut, so that a further rounding sees on which side of a middle the
+// exact value lay.  The products' and the sum's errors are held in a second fp32
+// (Dekker's and Knuth's error-free transformations), 48 bits in all.  (In fp64 a
+// head took 5 us.)
 template <int P>
-__device__ __forceinline__ double exact_turned(const Turn<P>& t, int e, float x, float p) {
+__device__ __forceinline__ float turned_to_odd(const Turn<P>& t, int e, float x, float p) {
   const bool turns = P == kLaneOff ? t.any : t.s[e] != 0.f || t.c[e] != 1.f;
-  return turns ? fma((double)x, (double)t.c[e], (double)p * (double)t.s[e]) : (double)x;
+  if (!turns) return x;
+  const float a = __fmul_rn(x, t.c[e]), b = __fmul_rn(p, t.s[e]);
+  const float ea = __fmaf_rn(x, t.c[e], -a), eb = __fmaf_rn(p, t.s[e], -b);
+  const float sum = __fadd_rn(a, b), part = __fsub_rn(sum, a);
+  const float es = __fadd_rn(__fsub_rn(a, __fsub_rn(sum, part)), __fsub_rn(b, part));
+  const float low = __fadd_rn(es, __fadd_rn(ea, eb));
+  float z = __fadd_rn(sum, low);
+  const float rest = __fsub_rn(low, __fsub_rn(z, sum));
+  const uint32_t bits = __float_as_uint(z);
+  if (rest != 0.f && z != 0.f && fabsf(z) <= 3.4028235e38f && !(bits & 1u))
+    z = __uint_as_float((rest > 0.f) == (z > 0.f) ? bits + 1u : bits - 1u);
+  return z;
 }
 
 template <int P, int kHeads>
@@ -251,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) indexer_query_kernel(const QueryArgs
     // fp32's error may have moved a turned value across the middle between two codes
     // if its codes a little further in and out differ (carried values are exact); and
     // the largest across the border between two scales (on which bf16 values lie), if
-    // it is near.  Those heads, and infinite ones, go once more through 64 bits.
+    // it is near.  Those heads, and infinite ones, go once more, exactly.
     const float in = t.any ? inv * (1.f - 0x1p-21f) : inv, out = t.any ? inv * (1.f + 0x1p-21f) : inv;
     float z[kVals];
 #pragma unroll
@@ -265,22 +282,17 @@ __global__ void __launch_bounds__(kThreads) indexer_query_kernel(const QueryArgs
                       (part - 0x5FFFF8u <= 16u && part != 0x600000u);
     if (__any_sync(kFull, near)) {
       keep_branch();
-      double top = 0.0;
-#pragma unroll
-      for (int e = 0; e < kVals; ++e)
-        if (fabsf(y[e]) <= 3.4028235e38f) top = fmax(top, fabs(exact_turned<P>(t, e, x[e], p[e])));
-#pragma unroll
-      for (int o = 8; o; o >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, o));
-      // Rounded up: a value just past the border stays past it.
-      field = scale_exponent(__float_as_uint(__double2float_ru(top)));
+      float top = 0.f;
 #pragma unroll
       for (int e = 0; e < kVals; ++e) {
-        // To fp32 with what is cut kept in the last bit, so that the next rounding
-        // sees on which side of a middle it lay.
-        const double d = exact_turned<P>(t, e, x[e], p[e]) * (double)power(254 - field);
-        z[e] = __double2float_rz(d);
-        if ((double)z[e] != d && fabsf(z[e]) <= 3.4028235e38f) z[e] = __uint_as_float(__float_as_uint(z[e]) | 1u);
+        z[e] = turned_to_odd<P>(t, e, x[e], p[e]);
+        if (fabsf(z[e]) <= 3.4028235e38f) top = fmaxf(top, fabsf(z[e]));
       }
+#pragma unroll
+      for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      field = scale_exponent(__float_as_uint(top));
+#pragma unroll
+      for (int e = 0; e < kVals; ++e) z[e] *= power(254 - field);
       code = codes8(z);
     }
     if (h < a.H) {

@@ -32,7 +32,7 @@ def cos_sin(rot, max_pos=300):
 
 
 @pytest.mark.parametrize("layout,rot,first", TURNS)
-@pytest.mark.parametrize("T,S,bias", [(1, 1, True), (7, 4, False), (300, 2, True)])
+@pytest.mark.parametrize("T,S,bias", [(1, 1, True), (7, 4, False), (300, 2, True), (50, 20, False)])
 def test_keys(T, S, bias, layout, rot, first):
     import dsa_sparse_indexer_gb300 as dsa
     g = torch.Generator(device="cuda")
