@@ -466,6 +466,8 @@ __device__ __forceinline__ void softmax_tiles(const PrefillArgs& a, PrefillSmem&
           keep_branch();
           mask(x[0], c);
           mask(x[1], c + 1);
+          tmem_store_frag(t_s + c * 32, x[0]);   // as the weights will read them
+          tmem_store_frag(t_s + c * 32 + 32, x[1]);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {        // the lane's rows
@@ -518,16 +520,13 @@ __device__ __forceinline__ void softmax_tiles(const PrefillArgs& a, PrefillSmem&
       const float2 c2v = make_float2(a.c2, a.c2);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       uint32_t y[2][16];
+      if (masked) tmem_wait_st();
       tmem_load_frag(t_s, y[0]);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t (&x)[16] = y[c & 1];
         tmem_wait_ld(x);
         if (c < 3) tmem_load_frag(t_s + (c + 1) * 32, y[(c + 1) & 1]);   // before weights overwrite it
-        if (masked) {
-          keep_branch();
-          mask(x, c);
-        }
         uint32_t p[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -568,17 +567,24 @@ __device__ __forceinline__ void softmax_tiles(const PrefillArgs& a, PrefillSmem&
         (parts ? a.part_l : a.lse2)[to + k * next] = l[k] == 0.f ? -INFINITY : m[k] + log2f(l[k]);
     }
     if (some || !parts) {                    // the merge does not read an empty part
-#pragma unroll 1
+      // Rows that saw nothing are zeros, whatever their columns hold.
+      const bool seen_all = some && __all_sync(kFull, l[0] != 0.f && l[1] != 0.f);
+      uint32_t y[2][16];
+      if (some) tmem_load_frag(t_o, y[0]);
+#pragma unroll
       for (int c = 0; c < kDv; c += 32) {
-        uint32_t o[16];
+        uint32_t (&o)[16] = y[c / 32 & 1];
         if (some) {
-          tmem_load_frag(t_o + (uint32_t)c, o);
           tmem_wait_ld(o);
+          if (c + 32 < kDv) tmem_load_frag(t_o + (uint32_t)c + 32, y[(c / 32 + 1) & 1]);
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int k = (j >> 1) & 1;
-          o[j] = some && l[k] != 0.f ? __float_as_uint(__uint_as_float(o[j]) * inv[k]) : 0u;
+        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv[(j >> 1) & 1]);
+        if (!seen_all) {
+          keep_branch();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (!some || l[(j >> 1) & 1] == 0.f) o[j] = 0u;
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -590,15 +596,7 @@ __device__ __forceinline__ void softmax_tiles(const PrefillArgs& a, PrefillSmem&
                 *reinterpret_cast<uint2*>(dst + 8 * i) = make_uint2(o[4 * i + 2 * k], o[4 * i + 2 * k + 1]);
             }
           } else {
-            // Pairs of columns 8 i + 2 j in lane j: lane j is to have all of i = j.
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = pack16<BF16>(__uint_as_float(o[4 * i + 2 * k]), __uint_as_float(o[4 * i + 2 * k + 1]));
-            transpose4(w, lane);
-            if (active[k])
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (to + k * next) * kDv + c +
-                                        8 * (lane & 3)) = make_uint4(w[0], w[1], w[2], w[3]);
+            store_row<BF16>(o, k, lane, active[k], static_cast<uint16_t*>(a.out) + (to + k * next) * kDv + c);
           }
         }
         __syncwarp();                        // the next columns' load takes the whole warp

@@ -423,21 +423,6 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
       : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
   return *reinterpret_cast<float2*>(&r);
 }
-// Word i of lane j (of four neighbours) and word j of lane i change places.
-__device__ __forceinline__ void transpose4(uint32_t (&w)[4], int lane) {
-#pragma unroll
-  for (int o = 1; o <= 2; o <<= 1) {         // the lane's bit o against the word's
-    const bool up = (lane & o) != 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (!(i & o)) {
-        const uint32_t give = up ? w[i] : w[i + o], got = __shfl_xor_sync(kFull, give, o);
-        if (up) w[i] = got;
-        else w[i + o] = got;
-      }
-  }
-}
-
 // Two values as 16-bit floats in one word, each rounded to nearest even.
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
@@ -447,6 +432,25 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   } else {
     __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&h);
+  }
+}
+
+// A row's 32 columns as fragments hold them (row k of the lane's two: o[4 i + 2 k],
+// o[4 i + 2 k + 1] are columns 8 i + 2 (lane % 4) and the next), as 16-bit floats to
+// `row`: neighbouring lanes swap words, so that each stores eight bytes and the four
+// lanes of a row whole sectors.
+template <bool BF16>
+__device__ __forceinline__ void store_row(const uint32_t (&o)[16], int k, int lane, bool active, uint16_t* row) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = pack16<BF16>(__uint_as_float(o[4 * i + 2 * k]), __uint_as_float(o[4 * i + 2 * k + 1]));
+  const bool odd = (lane & 1) != 0;          // has i = 1, 3 in the end, an even lane i = 0, 2
+  const uint32_t a = __shfl_xor_sync(kFull, odd ? w[0] : w[1], 1), b = __shfl_xor_sync(kFull, odd ? w[2] : w[3], 1);
+  if (active) {
+    uint16_t* at = row + (odd ? 8 : 0) + (lane & 2 ? 4 : 0);
+    *reinterpret_cast<uint2*>(at) = odd ? make_uint2(a, w[1]) : make_uint2(w[0], a);
+    *reinterpret_cast<uint2*>(at + 16) = odd ? make_uint2(b, w[3]) : make_uint2(w[2], b);
   }
 }
 
