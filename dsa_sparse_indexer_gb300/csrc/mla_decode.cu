@@ -58,25 +58,29 @@ constexpr uint32_t kStalledArrivals = 1;
 constexpr uint32_t kStalledArrivals = 0;
 #endif
 
-enum Mode { kNarrow = 0, kWide = 1, kPair = 2 };
+enum Mode { kNarrow16, kNarrow32, kWide, kPair };
 template <int M>
-struct Shape {
+struct Cut {
   static constexpr int CG = M == kPair ? 2 : 1;
-  static constexpr int kQRows = M == kNarrow ? 32 : kRows;     // rows of queries that a CTA holds
-  static constexpr int kItemRows = CG * kQRows;
+  static constexpr int kItemRows = M == kNarrow16 ? 16 : M == kNarrow32 ? 32 : CG * kRows;
+  static constexpr int kHalves = M == kWide || M == kPair ? 2 : 1;   // items of a row block
+  static constexpr int kTile = M == kWide ? 64 : 128;          // keys of a tile
+  static constexpr int kPieces = kTile / 16;
+};
+template <int M>              // Wide, Pair
+struct Shape : Cut<M> {
+  using Cut<M>::CG;
   static constexpr int kQTm = M == kWide ? 4 : 0;              // query blocks in tensor memory,
-  static constexpr int kQBlock = kQRows * 128;                 // the others in shared memory
+  static constexpr int kQBlock = kRows * 128;                  // the others in shared memory
   static constexpr int kQBytes = (kBlocks - kQTm) * kQBlock;
-  static constexpr int kQBufs = M == kNarrow ? 2 : 1;          // items whose queries fit
-  static constexpr int kTile = M == kPair ? 128 : 64;          // keys of a tile
   static constexpr int kBlock = 8192;                          // bytes of 64 keys' 64 values
-  // Narrow, Wide: stages of a tile's nine blocks, the values' four first.
+  // Wide: stages of a tile's nine blocks, the values' four first.
   static constexpr int kStages = 2;
   // Pair: the ring's blocks, 64-value columns of a CTA's values, keys of a value
   // block and bytes of a column in it.
   static constexpr int kRing = 10, kAtoms = kVBlocks / CG, kVKeys = 32, kAtom = kVKeys * 128;
   static constexpr int kKvBytes = (M == kPair ? kRing : kStages * kBlocks) * kBlock;
-  __device__ static constexpr uint32_t s_col(uint32_t b) { return 256 + b * kTile; }
+  __device__ static constexpr uint32_t s_col(uint32_t b) { return 256 + b * Cut<M>::kTile; }
 };
 // Barriers of key blocks: a pair's units, or a stage's values (at the stage) and
 // its other blocks (at kStages + the stage).
@@ -97,10 +101,10 @@ struct Item {
 
 template <int M>
 struct alignas(1024) DecodeSmem {
-  uint8_t q[Shape<M>::kQBufs][Shape<M>::kQBytes];
+  uint8_t q[Shape<M>::kQBytes];
   uint8_t kv[Shape<M>::kKvBytes];
   WorkSlots<Item> work;
-  uint64_t full[kUnits], empty[kUnits], qfull[2], qtm, qempty[2], sfull[2], pfull[2], pvdone, vtail[2],
+  uint64_t full[kUnits], empty[kUnits], qfull, qtm, qempty, sfull[2], pfull[2], pvdone, vtail[2],
       info[kInfo], drain;
   uint32_t tail_seq[2];       // Pair: place in the ring of the values that vtail counts
   uint32_t pages[kInfo];      // valid pages of stream tile j, at j % kInfo: a bit per 16 keys
@@ -108,11 +112,8 @@ struct alignas(1024) DecodeSmem {
   int blocks;                 // row blocks of all requests
   int abort;
 };
-static_assert(sizeof(DecodeSmem<kNarrow>) + 1024 <= 232448 && sizeof(DecodeSmem<kWide>) + 1024 <= 232448 &&
-                  sizeof(DecodeSmem<kPair>) + 1024 <= 232448,
+static_assert(sizeof(DecodeSmem<kWide>) + 1024 <= 232448 && sizeof(DecodeSmem<kPair>) + 1024 <= 232448,
               "shared memory of a CTA");
-static_assert(8 * Shape<kNarrow>::kQBlock + kRows * 128 <= Shape<kNarrow>::kKvBytes,
-              "rows past the queries lie in this CTA's memory");
 
 struct DecodeArgs {
   const __nv_bfloat16* q;     // [rows][H][kDqk]
@@ -145,15 +146,15 @@ __device__ __forceinline__ void rows_of(const DecodeArgs& a, int i, int& first, 
   end = min(max(__ldg(a.starts + i + 1), first), a.rows);
 }
 
-// Warp-wide: item `index` of blocks * 2 * S * splits: halves and row blocks of a
+// Warp-wide: item `index` of blocks * halves * S * splits: halves and row blocks of a
 // request, which read the same keys, beside one another.
 template <int M>
 __device__ __forceinline__ Item find_item(const DecodeArgs& a, int blocks, int64_t index, Cursor& c) {
-  constexpr int kItemRows = Shape<M>::kItemRows;
+  constexpr int kItemRows = Cut<M>::kItemRows;
   const int lane = threadIdx.x & 31;
   Item it;
-  it.half = (int)(index & 1);
-  const int64_t x = index >> 1;
+  it.half = (int)(index % Cut<M>::kHalves);
+  const int64_t x = index / Cut<M>::kHalves;
   const int y = (int)(x / blocks), qb = (int)(x - (int64_t)y * blocks);
   it.shard = y / a.splits;
   it.split = y - it.shard * a.splits;
@@ -196,23 +197,39 @@ __device__ __forceinline__ Item find_item(const DecodeArgs& a, int blocks, int64
   it.nall = local_of(len);
   it.nvis = a.mask ? it.nall : local_of(it.base + hi + 1);
   it.nfree = local_of(a.mask ? it.base : it.base + lo + 1);
-  constexpr int kTile = Shape<M>::kTile;
+  constexpr int kTile = Cut<M>::kTile;
   const int nt = (it.nvis + kTile - 1) / kTile, per = (nt + a.splits - 1) / a.splits;
   it.t0 = min(it.split * per, nt);
   it.t1 = min(it.t0 + per, nt);
   return it;
 }
 
+// Warp-wide: row blocks of all requests; bad bounds are flagged once a call.
+template <int M>
+__device__ __forceinline__ int count_blocks(const DecodeArgs& a) {
+  constexpr int kItemRows = Cut<M>::kItemRows;
+  int blocks = 0;
+  bool bad = false;
+  for (int i = threadIdx.x & 31; i < a.reqs; i += 32) {
+    int first, end;
+    rows_of(a, i, first, end);
+    bad |= first != a.starts[i] || end != a.starts[i + 1];
+    blocks += ((end - first) * a.H + kItemRows - 1) / kItemRows;
+  }
+  if (bad && blockIdx.x == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);
+  return __reduce_add_sync(kFull, blocks);
+}
+
 // Steps of 16 keys of tile t's value product, and whether it reads keys behind
 // the sequence's end (zeroed in shared memory by the softmax warps).
 template <int M>
 __device__ __forceinline__ int value_steps(const Item& it, int t) {
-  constexpr int kTile = Shape<M>::kTile;
+  constexpr int kTile = Cut<M>::kTile;
   return (min(it.nvis - t * kTile, kTile) + 15) / 16;
 }
 template <int M>
 __device__ __forceinline__ bool has_tail(const Item& it, int t) {
-  return it.nall - t * Shape<M>::kTile < 16 * value_steps<M>(it, t);
+  return it.nall - t * Cut<M>::kTile < 16 * value_steps<M>(it, t);
 }
 // The i-th block that an item's scores take first, of the nine; its i-th value block.
 __device__ __forceinline__ int block_a(int half, int i) {
@@ -225,11 +242,29 @@ __device__ __forceinline__ int block_v(int half, int i) { return half * kVBlocks
 // such pieces, repeated) has the page's table entry, then the first one's cache row.
 template <int M>
 __device__ __forceinline__ int table_entry(const DecodeArgs& a, const Item& it, int t) {
-  constexpr int kTile = Shape<M>::kTile;
-  const int key = t * kTile + (int)(threadIdx.x % (kTile / 16)) * 16;
+  const int key = t * Cut<M>::kTile + (int)(threadIdx.x % Cut<M>::kPieces) * 16;
   if (t < it.t0 || key >= it.nall) return -1;
   return __ldg(a.block_table + ((int64_t)it.shard * a.reqs + it.req) * a.max_blocks +
                fdiv((uint32_t)key, a.fblock));
+}
+// That row, which may be `n_slots` (outside: reads as zero) where there is none;
+// `valid` gets a bit a piece that there is.
+template <int M>
+__device__ __forceinline__ int cache_row(const DecodeArgs& a, const Item& it, int t, int entry, uint32_t& valid,
+                                         bool& bad) {
+  const int key = t * Cut<M>::kTile + (int)(threadIdx.x % Cut<M>::kPieces) * 16;
+  int y = (int)a.n_slots;
+  bool in = false;
+  if (key < it.nall) {
+    uint32_t off;
+    fdivmod((uint32_t)key, a.fblock, &off);
+    const int64_t at = (int64_t)entry * a.block + off;
+    in = at >= 0 && at + 16 <= a.n_slots;
+    if (in) y = (int)at;
+    bad |= !in;
+  }
+  valid = __ballot_sync(kFull, in) & ((1u << Cut<M>::kPieces) - 1u);
+  return y;
 }
 
 // Ring of the pair: units are freed in the order in which they were copied.
@@ -253,7 +288,7 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
   const int lane = threadIdx.x & 31;
   const bool leader = rank == 0;
   Item it;
-  constexpr int kPieces = Sh::kTile / 16;
+  constexpr int kPieces = Sh::kPieces;
   uint32_t j = 0, loads = 0, tails = 0;      // tiles, items' queries, tails so far
   bool ok = true, bad = false;
   bool half_tile = false;                    // the last tile's values were not copied
@@ -305,36 +340,23 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
     bad |= it.bad != 0;
     int next = table_entry<M>(a, it, it.t1 - 1);
     for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
-      const int key = t * Sh::kTile + lane % kPieces * 16, entry = next;
+      uint32_t valid;
+      const int y = cache_row<M>(a, it, t, next, valid, bad);
       next = table_entry<M>(a, it, t - 1);   // on its way while this tile is copied
-      int y = (int)a.n_slots;                // outside: reads as zero
-      bool in = false;
-      if (key < it.nall) {
-        uint32_t off;
-        fdivmod((uint32_t)key, a.fblock, &off);
-        const int64_t at = (int64_t)entry * a.block + off;
-        in = at >= 0 && at + 16 <= a.n_slots;
-        if (in) y = (int)at;
-        bad |= !in;
-      }
-      const unsigned valid = __ballot_sync(kFull, in) & ((1u << kPieces) - 1u);
       if (M == kPair && t < it.t1 - 2) load_values(p0);
       if (!ok) break;
       if (t == it.t1 - 1) {                  // the item's queries
-        const uint32_t qb = loads % Sh::kQBufs, use = loads / Sh::kQBufs;
-        if (use > 0) ok = warp_wait(&sm.abort, &sm.qempty[qb], (use - 1) & 1u);
+        if (loads > 0) ok = warp_wait(&sm.abort, &sm.qempty, (loads - 1) & 1u);
         if (!ok) break;
         ++loads;
         constexpr int kN = kBlocks - Sh::kQTm;
-        auto boxes = [&](int r) {
-          return (min(max(it.rows - r * kRows, 0), Sh::kQRows) + kQBox - 1) / kQBox;
-        };
+        auto boxes = [&](int r) { return (min(max(it.rows - r * kRows, 0), kRows) + kQBox - 1) / kQBox; };
         if (leader && lane == 0)
-          mbar_expect_tx(&sm.qfull[qb], (uint32_t)((boxes(0) + (CG == 2 ? boxes(1) : 0)) * kN * kQBox * 128));
-        const uint32_t bar = CG == 1 ? smem_u32(&sm.qfull[qb]) : leader_addr(&sm.qfull[qb]);
+          mbar_expect_tx(&sm.qfull, (uint32_t)((boxes(0) + (CG == 2 ? boxes(1) : 0)) * kN * kQBox * 128));
+        const uint32_t bar = CG == 1 ? smem_u32(&sm.qfull) : leader_addr(&sm.qfull);
         if (lane < kN)
           for (int b = 0; b < boxes((int)rank); ++b)
-            load_box<CG>(sm.q[qb] + lane * Sh::kQBlock + b * kQBox * 128, tm_q, (Sh::kQTm + lane) * 64,
+            load_box<CG>(sm.q + lane * Sh::kQBlock + b * kQBox * 128, tm_q, (Sh::kQTm + lane) * 64,
                          it.tok0 * a.H + it.row0 + (int)rank * kRows + b * kQBox, 0, bar);
       }
       if (lane == 0) {
@@ -385,8 +407,7 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
   if (!ok && lane == 0) {
     if (!cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
     // The copies issued land before the CTA ends (a pair's first CTA counts both's).
-    for (uint32_t k = loads > Sh::kQBufs ? loads - Sh::kQBufs : 0; leader && k < loads; ++k)
-      mbar_wait(&sm.qfull[k % Sh::kQBufs], (k / Sh::kQBufs) & 1u);
+    if (leader && loads > 0) mbar_wait(&sm.qfull, (loads - 1) & 1u);
     if constexpr (M == kPair) {
       for (uint32_t u = ring.oldest; leader && u < ring.unit; ++u)
         mbar_wait(&sm.full[u % kUnits], (u / kUnits) & 1u);
@@ -412,9 +433,7 @@ __device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem<M
   const uint32_t id_s = idesc_f16(CG * kRows, Sh::kTile, true, false) | a.negate;
   constexpr uint32_t id_o = idesc_f16(CG * kRows, kHalf, true, true);
   constexpr int kStep = Sh::kBlock >> 4;     // a block in a descriptor's address field
-  const uint64_t q00 = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
-  uint64_t q0 = q00;                         // of the item's queries
-  uint32_t qb = 0;
+  const uint64_t q0 = smem_desc_sw128(smem_u32(sm.q), 16, 1024);
   const uint64_t k0 = smem_desc_sw128(smem_u32(sm.kv), 16, 1024);
   const uint64_t v0 = smem_desc_sw128(smem_u32(sm.kv), M == kPair ? Sh::kAtom : Sh::kBlock, 1024);
   Item it;
@@ -483,16 +502,14 @@ __device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem<M
     for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
       if (M == kPair && t < it.t1 - 2) values(j - 2, value_steps<M>(it, t + 2), t + 2 == it.t1 - 1);
       if (ok && t == it.t1 - 1) {
-        qb = nq % Sh::kQBufs;
-        q0 = q00 + qb * (Sh::kQBytes >> 4);
-        if (!wait(&sm.qfull[qb], (nq / Sh::kQBufs) & 1u)) break;
+        if (!wait(&sm.qfull, nq & 1u)) break;
         if (Sh::kQTm > 0 && !wait(&sm.qtm, nq & 1u)) break;
         ++nq;
       }
       const uint32_t b = j % 2, d = tmem + Sh::s_col(b);
       auto scores_done = [&]() {
         tc_commit<CG>(&sm.sfull[b]);
-        if (t == it.t0) tc_commit<CG>(&sm.qempty[qb]);
+        if (t == it.t0) tc_commit<CG>(&sm.qempty);
       };
       if constexpr (M == kPair) {
 #pragma unroll 1
@@ -844,25 +861,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) {
     tmem_alloc<CG>(&sm.tmem, kTmemCols);
   } else if (warp == kClaimWarp) {
-    // Row blocks of all requests; bad bounds are flagged once a call.
-    int blocks = 0;
-    bool bad = false;
-    for (int i = tid & 31; i < a.reqs; i += 32) {
-      int first, end;
-      rows_of(a, i, first, end);
-      bad |= first != a.starts[i] || end != a.starts[i + 1];
-      blocks += ((end - first) * a.H + Sh::kItemRows - 1) / Sh::kItemRows;
-    }
-    blocks = __reduce_add_sync(kFull, blocks);
-    if (bad && blockIdx.x == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);
+    const int blocks = count_blocks<M>(a);
     if ((tid & 31) == 0) sm.blocks = blocks;
   } else if (tid == 0) {
     for (int b = 0; b < kUnits; ++b) mbar_init(&sm.full[b], 1 + (b == 0 ? kStalledArrivals : 0));
     for (int b = 0; b < kUnits; ++b) mbar_init(&sm.empty[b], 1);
     mbar_init(&sm.qtm, kSoftmaxWarps);
+    mbar_init(&sm.qfull, 1);
+    mbar_init(&sm.qempty, 1);
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&sm.qfull[b], 1);
-      mbar_init(&sm.qempty[b], 1);
       mbar_init(&sm.sfull[b], 1);
       mbar_init(&sm.pfull[b], kSoftmaxWarps * CG);   // a warp each, of both CTAs in a pair's first
       mbar_init(&sm.vtail[b], 1);
@@ -900,18 +907,427 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ---- few rows: keys and values as the products' rows ----------------------------
+// S^T = K Q^T (128 keys x N rows) and O^T = V^T P^T (512 values x N rows, four
+// products of 128 values): a step of 16 takes the 32 cycles in which A's 128 rows
+// are read, 2176 cycles for 128 keys where the rows as A would take 9250, and all
+// outputs fit 4 N columns, so that keys are read and scored once.
+//  * tensor memory: scores (N columns; a lane is a key), outputs (4 N; a lane is
+//    one of 128 values);
+//  * shared memory: a tile's 128 keys as four slots of 128 values (32 KB) and one
+//    of the last 64 (16 KB), five and kTails of them; the queries; the weights (a
+//    row's 64 keys to 128 bytes).  Keys stay for the value product, which frees
+//    them slot by slot; the slots left over are filled under the softmax.
+//  * four softmax warps, a thread a key, which exchange maxima and sums through
+//    shared memory; one issuing products, one copying, one claiming.
+// A tile's memory traffic (147 KB, 3.3 us at this SM's share of the bandwidth)
+// bounds it.
+constexpr int kNarrowWarps = 4, kNarrowMma = 4, kNarrowLoad = 5, kNarrowClaim = 6, kNarrowThreads = 224;
+constexpr int kSlots = 5, kSlot = 32768, kSlotBlock = 16384;   // a slot's two blocks: 128 keys' 64 values
+
+template <int M>
+struct alignas(1024) NarrowSmem {
+  static constexpr int N = Cut<M>::kItemRows;
+  static constexpr int kTails = N == 16 ? 2 : 1;
+  uint8_t kv[kSlots][kSlot];
+  uint8_t tail[kTails][kSlotBlock];
+  uint8_t q[kBlocks][N * 128];
+  uint8_t p[2][N * 128];      // the weights of 64 keys each
+  float exchange[2][kNarrowWarps][N];
+  WorkSlots<Item> work;
+  uint64_t full[kSlots], empty[kSlots], tail_full[kTails], tail_empty[kTails], qfull, qempty, sfull, pfull, pvdone,
+      exchanged, info[kInfo], drain;
+  uint32_t pages[kInfo];
+  uint32_t tmem;
+  int blocks;
+  int abort;
+};
+static_assert(sizeof(NarrowSmem<kNarrow16>) + 1024 <= 232448 && sizeof(NarrowSmem<kNarrow32>) + 1024 <= 232448,
+              "shared memory of a CTA");
+
+template <int M>
+__device__ __forceinline__ void narrow_load(const DecodeArgs& a, NarrowSmem<M>& sm, const CUtensorMap* tm_q,
+                                            const CUtensorMap* tm_k) {
+  using Sm = NarrowSmem<M>;
+  constexpr int kTails = Sm::kTails, kPieces = Cut<M>::kPieces;
+  const int lane = threadIdx.x & 31;
+  const int boxes = Cut<M>::kTile / a.kbox, i = lane / boxes, first = lane % boxes * a.kbox;   // 2 to 8 a block
+  Item it;
+  uint32_t j = 0, slot = 0, loads = 0;       // tiles, slots and items' queries so far
+  uint32_t tails = 0;
+  bool ok = true, bad = false;
+  for (uint32_t n = 0; next_item(sm.work, &sm.abort, n, ok, it); ++n) {
+    item_done(sm.work, n);
+    bad |= it.bad != 0;
+    int next = table_entry<M>(a, it, it.t1 - 1);
+    for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
+      uint32_t valid;
+      const int y = cache_row<M>(a, it, t, next, valid, bad);
+      next = table_entry<M>(a, it, t - 1);   // on its way while this tile is copied
+      const int yk = __shfl_sync(kFull, y, first / 16 % kPieces);
+      if (t == it.t1 - 1) {                  // the item's queries
+        if (loads > 0) ok = warp_wait(&sm.abort, &sm.qempty, (loads - 1) & 1u);
+        if (!ok) break;
+        ++loads;
+        if (lane == 0) mbar_expect_tx(&sm.qfull, kBlocks * Sm::N * 128);
+        if (lane < kBlocks)
+          load_box<1>(sm.q[lane], tm_q, lane * 64, it.tok0 * a.H + it.row0, 0, smem_u32(&sm.qfull));
+      }
+      if (lane == 0) {
+        sm.pages[j % kInfo] = valid;
+        mbar_arrive1(&sm.info[j % kInfo]);
+      }
+      const uint32_t at = tails % kTails, use = tails / kTails;
+      if (use > 0) ok = warp_wait(&sm.abort, &sm.tail_empty[at], (use - 1) & 1u);
+      if (!ok) break;
+      ++tails;
+      if (lane == 0) mbar_expect_tx(&sm.tail_full[at], kSlotBlock);
+      if (i < 1)
+        load_box<1>(sm.tail[at] + first * 128, tm_k, (kBlocks - 1) * 64, yk, it.shard, smem_u32(&sm.tail_full[at]));
+      for (int m = 0; m < 4; ++m, ++slot) {
+        const uint32_t k = slot % kSlots, turn = slot / kSlots;
+        if (turn > 0) ok = warp_wait(&sm.abort, &sm.empty[k], (turn - 1) & 1u);
+        if (!ok) break;
+        if (lane == 0) mbar_expect_tx(&sm.full[k], kSlot);
+        if (i < 2)
+          load_box<1>(sm.kv[k] + i * kSlotBlock + first * 128, tm_k, (2 * m + i) * 64, yk, it.shard,
+                      smem_u32(&sm.full[k]));
+      }
+    }
+  }
+  if (__any_sync(kFull, bad) && lane == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);
+  if (!ok && lane == 0) {
+    if (!cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
+    // The copies issued land before the CTA ends.
+    if (loads > 0) mbar_wait(&sm.qfull, (loads - 1) & 1u);
+    for (uint32_t v = tails > kTails ? tails - kTails : 0; v < tails; ++v)
+      mbar_wait(&sm.tail_full[v % kTails], (v / kTails) & 1u);
+    for (uint32_t v = slot > kSlots ? slot - kSlots : 0; v < slot; ++v)
+      mbar_wait(&sm.full[v % kSlots], (v / kSlots) & 1u);
+  }
+  __syncwarp();
+}
+
+template <int M>
+__device__ __forceinline__ void narrow_products(const DecodeArgs& a, NarrowSmem<M>& sm, uint32_t tmem) {
+  using Sm = NarrowSmem<M>;
+  constexpr int N = Sm::N, kTails = Sm::kTails;
+  const uint32_t id_s = idesc_f16(128, N, true, false) | a.negate;
+  constexpr uint32_t id_o = idesc_f16(128, N, true, false) | kAcrossA;
+  const uint64_t q0 = smem_desc_sw128(smem_u32(sm.q), 16, 1024), p0 = smem_desc_sw128(smem_u32(sm.p), 16, 1024);
+  const uint64_t k0 = smem_desc_sw128(smem_u32(sm.kv), 16, 1024), t0 = smem_desc_sw128(smem_u32(sm.tail), 16, 1024);
+  const uint64_t v0 = smem_desc_sw128(smem_u32(sm.kv), kSlotBlock, 1024);
+  constexpr int kRow = N * 128 >> 4;         // a block of queries or weights in an address field
+  Item it;
+  uint32_t j = 0, slot = 0, nq = 0;          // tiles, slots, items' queries so far
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    ok = ok && warp_wait(&sm.abort, bar, parity);
+    tc_fence_after();
+    return ok;
+  };
+  for (uint32_t n = 0; next_item(sm.work, &sm.abort, n, ok, it); ++n) {
+    item_done(sm.work, n);
+    for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
+      if (t == it.t1 - 1 && !wait(&sm.qfull, nq++ & 1u)) break;
+      const uint32_t at = j % kTails;
+      if (!wait(&sm.tail_full[at], (j / kTails) & 1u)) break;
+      if (elect_one()) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          mma_ss<1>(tmem, t0 + at * (kSlotBlock >> 4) + s * 2, q0 + (kBlocks - 1) * kRow + s * 2, id_s, s == 0 ? 0u : 1u);
+        tc_commit<1>(&sm.tail_empty[at]);
+      }
+      __syncwarp();
+      for (int m = 0; m < 4; ++m) {
+        const uint32_t k = (slot + m) % kSlots;
+        if (!wait(&sm.full[k], ((slot + m) / kSlots) & 1u)) break;
+        if (elect_one()) {
+          const uint64_t kd = k0 + k * (kSlot >> 4), qd = q0 + 2 * m * kRow;
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            mma_ss<1>(tmem, kd + (s / 4) * (kSlotBlock >> 4) + (s % 4) * 2, qd + (s / 4) * kRow + (s % 4) * 2, id_s, 1u);
+          if (m == 3) {
+            tc_commit<1>(&sm.sfull);
+            if (t == it.t0) tc_commit<1>(&sm.qempty);
+          }
+        }
+        __syncwarp();
+      }
+      const int steps = value_steps<M>(it, t);
+      if (!ok || !wait(&sm.pfull, j & 1u)) break;
+      if (elect_one()) {
+        const bool first = t == it.t1 - 1;
+#pragma unroll 1
+        for (int m = 0; m < 4; ++m) {
+          const uint32_t k = (slot + m) % kSlots, d = tmem + N + m * N;
+          const uint64_t vd = v0 + k * (kSlot >> 4);
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            if (s < steps)
+              mma_ss<1>(d, vd + s * (2048 >> 4), p0 + (s / 4) * kRow + (s % 4) * 2, id_o, (first && s == 0) ? 0u : 1u);
+          tc_commit<1>(&sm.empty[k]);
+        }
+        tc_commit<1>(&sm.pvdone);
+      }
+      __syncwarp();
+      slot += 4;
+    }
+  }
+  if (!ok && (threadIdx.x & 31) == 0 && !cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
+  __syncwarp();
+  // Every product issued completes before the tensor memory is freed.
+  if (elect_one()) {
+    tc_commit<1>(&sm.drain);
+    if (!mbar_wait(&sm.drain, 0)) cta_abort(&sm.abort, a.flags);
+  }
+  __syncwarp();
+}
+
+template <int M>
+__device__ __forceinline__ void narrow_softmax(const DecodeArgs& a, NarrowSmem<M>& sm, uint32_t tmem, int warp) {
+  constexpr int N = NarrowSmem<M>::N, kTile = Cut<M>::kTile;
+  const int lane = threadIdx.x & 31, key = warp * 32 + lane;   // the thread's key of a tile; value of an output block
+  const uint32_t t_s = tmem + ((uint32_t)(warp * 32) << 16), t_o = t_s + N;
+  uint32_t j = 0, rounds = 0;                // tiles, exchanges so far
+  bool ok = true;
+  // A value a row, one after another, which lane 0 of each warp has written.
+  auto exchange = [&](auto&& write) {
+    float(*buf)[N] = sm.exchange[rounds & 1u];
+    write(buf[warp]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive1(&sm.exchanged);
+    ok = warp_wait(&sm.abort, &sm.exchanged, rounds & 1u);
+    ++rounds;
+    return buf;
+  };
+  auto load_rows = [&](uint32_t at, uint32_t (&x)[N]) {
+#pragma unroll
+    for (int c = 0; c < N; c += 16) tmem_load(at + c, reinterpret_cast<uint32_t(&)[16]>(x[c]));
+#pragma unroll
+    for (int c = 0; c < N; c += 16) tmem_wait_ld(reinterpret_cast<uint32_t(&)[16]>(x[c]));
+  };
+  for (uint32_t n = 0; next_item(sm.work, &sm.abort, n, ok); ++n) {
+    const Item& it = sm.work.item[n & 1u];   // read where it lies
+    const int i0 = uni(it.t0), i1 = uni(it.t1), nall = uni(it.nall), nfree = uni(it.nfree);
+    float m[N], l[N];                        // the same m in every thread; l of the thread's keys
+#pragma unroll
+    for (int r = 0; r < N; ++r) m[r] = -INFINITY, l[r] = 0.f;
+    for (int t = i1 - 1; t >= i0; --t, ++j) {
+      ok = warp_wait(&sm.abort, &sm.sfull, j & 1u) &&
+           warp_wait(&sm.abort, &sm.info[j % kInfo], (j / kInfo) & 1u);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t x[N];
+      load_rows(t_s, x);
+      const uint32_t pages = *reinterpret_cast<volatile uint32_t*>(&sm.pages[j % kInfo]);
+      if (pages != 0xffu || (t + 1) * kTile > nfree) {
+        keep_branch();
+        const int local = t * kTile + key;
+        const bool there = ((pages >> (key >> 4)) & 1u) && local < nall;
+        const int own = !there || local < nfree ? -1 : (int)a.sm.global_id(it.shard, (uint32_t)local) - it.base;
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+          const int tok = (int)fdiv((uint32_t)(it.row0 + min(r, it.rows - 1)), a.fH);
+          bool see = there;
+          if (own >= 0)
+            see = a.mask ? (own >> 5) < a.words &&
+                               ((uint32_t)__ldg(a.mask + (int64_t)(it.tok0 + tok) * a.words + (own >> 5)) >> (own & 31)) & 1u
+                         : own <= tok;
+          if (!see) x[r] = 0xff800000u;
+        }
+      }
+      const auto top = exchange([&](float* mine) {
+        float v[N];
+#pragma unroll
+        for (int r = 0; r < N; ++r) v[r] = warp_max(__uint_as_float(x[r]));
+        if (lane == 0)
+#pragma unroll
+          for (int r = 0; r < N; r += 4)
+            *reinterpret_cast<float4*>(mine + r) = make_float4(v[r], v[r + 1], v[r + 2], v[r + 3]);
+      });
+      if (!ok) break;
+      float alpha[N];
+      bool moved = false;                    // some row's reference: alike in all threads
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        const float mx = fmaxf(fmax3(top[0][r], top[1][r], top[2][r]), top[3][r]) * a.c2;
+        const bool up = mx > m[r] + kRescaleGap;   // m = -inf takes any finite maximum
+        alpha[r] = 1.f;
+        if (up && m[r] != -INFINITY) alpha[r] = fast_exp2(m[r] - mx), moved = true;
+        m[r] = up ? mx : m[r];
+        l[r] *= alpha[r];
+      }
+      if (t < i1 - 1) {                      // the last tile's values are in: weights and outputs are at rest
+        ok = warp_wait(&sm.abort, &sm.pvdone, (j - 1) & 1u);
+        if (!ok) break;
+        tc_fence_after();
+        if (moved) {
+          keep_branch();
+#pragma unroll 1
+          for (int b = 0; b < 4; ++b) {
+            uint32_t o[N];
+            load_rows(t_o + b * N, o);
+#pragma unroll
+            for (int r = 0; r < N; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r]);
+#pragma unroll
+            for (int c = 0; c < N; c += 16) tmem_store(t_o + b * N + c, reinterpret_cast<uint32_t(&)[16]>(o[c]));
+          }
+          tmem_wait_st();
+        }
+      }
+      // The weights, rounded to bf16: row r's 64 keys of half key / 64 in 128 bytes,
+      // its 16-byte pieces swizzled by r % 8.
+      uint8_t* p = sm.p[key >> 6] + (key & 7) * 2;
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        const float ref = m[r] == -INFINITY ? 0.f : m[r];
+        const float e = fast_exp2(fmaf(__uint_as_float(x[r]), a.c2, -ref));
+        l[r] += e;
+        *reinterpret_cast<__nv_bfloat16*>(p + r * 128 + ((((key & 63) >> 3) ^ (r & 7)) << 4)) = __float2bfloat16_rn(e);
+      }
+      if (has_tail<M>(it, t)) {              // values behind the sequence's end: zeros
+        const int past = nall - t * kTile, to = 16 * value_steps<M>(it, t);
+        for (int z = key; z < (to - past) * 64; z += kNarrowWarps * 32) {
+          const int k = past + z / 64, piece = z % 64;   // of 16 bytes
+          uint8_t* block = sm.kv[(4 * j + (piece >> 4)) % kSlots] + ((piece >> 3) & 1) * kSlotBlock;
+          *reinterpret_cast<uint4*>(block + k * 128 + (piece & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      fence_async_smem();                    // read next by products
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(&sm.pfull);
+    }
+    if (!ok) break;
+    const bool some = i1 > i0, parts = a.splits > 1;
+    float inv[N];
+#pragma unroll
+    for (int r = 0; r < N; ++r) inv[r] = 0.f;
+    const int64_t to = ((int64_t)(parts ? it.split : 0) * a.sm.S + it.shard) * a.rows * a.H +
+                       (int64_t)it.tok0 * a.H + it.row0;   // [splits][S][rows][H]
+    float lse = -INFINITY;                   // of row `key`
+    if (some) {
+      const auto sums = exchange([&](float* mine) {
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+          float v = l[r];
+#pragma unroll
+          for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+          if (lane == 0) mine[r] = v;
+        }
+      });
+      if (ok) ok = warp_wait(&sm.abort, &sm.pvdone, (j - 1) & 1u);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        const float sum = (sums[0][r] + sums[1][r]) + (sums[2][r] + sums[3][r]);
+        if (sum != 0.f) {                    // a NaN too
+          inv[r] = 1.f / sum;
+          if (key == r) lse = m[r] + log2f(sum);
+        }
+      }
+    }
+    if (key < it.rows) (parts ? a.part_l : a.lse2)[to + key] = lse;
+    if (some || !parts) {                    // the merge does not read an empty part
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {
+        uint32_t o[N];
+        if (some) load_rows(t_o + b * N, o);
+        const int64_t at = to * kDv + b * 128 + key;
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+          // A row that saw nothing is zeros, whatever its column holds.
+          const float v = inv[r] == 0.f || !some ? 0.f : __uint_as_float(o[r]) * inv[r];
+          if (r >= it.rows) continue;
+          if (parts) a.part_o[at + r * kDv] = v;
+          else a.out[at + r * kDv] = __float2bfloat16_rn(v);
+        }
+        __syncwarp();
+      }
+    }
+    tc_fence_before();
+    item_done(sm.work, n);
+  }
+  if (!ok && lane == 0 && !cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
+}
+
+template <int M>
+__global__ void __launch_bounds__(kNarrowThreads, 1)
+    mla_decode_narrow_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                             const DecodeArgs a) {
+  using Sm = NarrowSmem<M>;
+  constexpr uint32_t kCols = Sm::N == 16 ? 128 : 256;   // 5 N, as a power of two
+  extern __shared__ unsigned char narrow_smem_raw[];
+  Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(narrow_smem_raw) + 1023) &
+                                  ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = uni(tid >> 5);
+  if (warp == kNarrowMma) {
+    tmem_alloc<1>(&sm.tmem, kCols);
+  } else if (warp == kNarrowClaim) {
+    const int blocks = count_blocks<M>(a);
+    if ((tid & 31) == 0) sm.blocks = blocks;
+  } else if (tid == 0) {
+    for (int b = 0; b < kSlots; ++b) {
+      mbar_init(&sm.full[b], 1 + (b == 0 ? kStalledArrivals : 0));
+      mbar_init(&sm.empty[b], 1);
+    }
+    for (int b = 0; b < Sm::kTails; ++b) {
+      mbar_init(&sm.tail_full[b], 1);
+      mbar_init(&sm.tail_empty[b], 1);
+    }
+    mbar_init(&sm.qfull, 1);
+    mbar_init(&sm.qempty, 1);
+    mbar_init(&sm.sfull, 1);
+    mbar_init(&sm.pfull, kNarrowWarps);
+    mbar_init(&sm.pvdone, 1);
+    mbar_init(&sm.exchanged, kNarrowWarps);
+    for (int b = 0; b < kInfo; ++b) mbar_init(&sm.info[b], 1);
+    mbar_init(&sm.drain, 1);
+    init_slots(sm.work, 1, kNarrowWarps + 2);
+    sm.abort = 0;
+    mbar_init_fence();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = uni(sm.tmem);
+  if (warp < kNarrowWarps) {
+    narrow_softmax<M>(a, sm, tmem, warp);
+  } else if (warp == kNarrowLoad) {
+    narrow_load<M>(a, sm, &tm_q, &tm_k);
+  } else if (warp == kNarrowClaim) {
+    const int blocks = sm.blocks;
+    Cursor cur;
+    share_out<1>(sm.work, &sm.abort, a.flags, (int64_t)blocks * a.sm.S * a.splits, 0u,
+                 [&](int64_t i) { return find_item<M>(a, blocks, i, cur); });
+  } else {
+    narrow_products<M>(a, sm, tmem);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kNarrowMma) {
+    tc_fence_after();
+    tmem_free<1>(tmem, kCols);
+  }
+}
+
+
+constexpr int kNarrowMost = 32;
 // How a call is cut: by the rows of a request (on average), and its keys into parts
 // where items are few.  Lengths are the device's: the table's width stands for them.
 struct Plan {
-  int mode, item_rows, splits;
+  int mode, halves, item_rows, splits;
 };
 Plan plan_for(int rows, int S, int H, int reqs, int64_t cap) {
   const int64_t pairs = ((int64_t)rows * H + reqs - 1) / reqs;
   Plan p;
-  p.mode = pairs > Shape<kWide>::kItemRows ? kPair : pairs > Shape<kNarrow>::kItemRows ? kWide : kNarrow;
-  p.item_rows = p.mode == kPair ? Shape<kPair>::kItemRows : p.mode == kWide ? Shape<kWide>::kItemRows
-                                                                          : Shape<kNarrow>::kItemRows;
-  const int64_t items = (pairs + p.item_rows - 1) / p.item_rows * reqs * 2 * S;
+  p.mode = pairs > Cut<kWide>::kItemRows ? kPair : pairs > kNarrowMost ? kWide : pairs > 16 ? kNarrow32 : kNarrow16;
+  p.halves = p.mode == kPair || p.mode == kWide ? 2 : 1;
+  p.item_rows = p.mode == kPair ? Cut<kPair>::kItemRows : p.mode == kWide ? Cut<kWide>::kItemRows
+                : p.mode == kNarrow32 ? Cut<kNarrow32>::kItemRows : Cut<kNarrow16>::kItemRows;
+  const int64_t items = (pairs + p.item_rows - 1) / p.item_rows * reqs * p.halves * S;
   // 128 keys take a pair about 2.9 us, a CTA alone 3.4; a part has as many at least.
   const int64_t tiles = (cap + 127) / 128, ctas = device_sms() / (p.mode == kPair ? 2 : 1);
   p.splits = choose_parts(items, ctas, tiles * (p.mode == kPair ? 2.9 : 3.4) + 4.0, (int64_t)rows * S * H, kDv,
@@ -930,6 +1346,16 @@ cudaError_t launch_decode(const CUtensorMap& q, const CUtensorMap& k, const CUte
   const unsigned grid = (unsigned)(items * Shape<M>::CG);
   return launch_kernel(kernel, dim3(grid), dim3(kThreads), (size_t)kSmem, stream,
                        Shape<M>::CG == 2 ? 2u : 0u, q, k, v, a);
+}
+
+template <int M>
+cudaError_t launch_narrow(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap&, const DecodeArgs& a,
+                          int64_t items, cudaStream_t stream) {
+  const auto kernel = mla_decode_narrow_kernel<M>;
+  constexpr int kSmem = (int)sizeof(NarrowSmem<M>) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kernel, dim3((unsigned)items), dim3(kNarrowThreads), (size_t)kSmem, stream, 0u, q, k, a);
 }
 
 }  // namespace
@@ -978,14 +1404,14 @@ extern "C" dsa_status dsa_mla_decode(const uint16_t* q, const uint16_t* kv_cache
   }
   CUtensorMap tq, tk, tv;
   const uint64_t row = kDqk * 2;
-  if (!encode_map16(&tq, q, true, kDqk, pairs, 1, row, row * pairs, kQBox, 1) ||
+  if (!encode_map16(&tq, q, true, kDqk, pairs, 1, row, row * pairs, std::min(p.item_rows, kQBox), 1) ||
       !encode_map16(&tk, kv_cache, true, kDqk, n_slots, S, row, row * n_slots, a.kbox, 1) ||
       !encode_map16(&tv, kv_cache, true, kDqk, n_slots, S, row, row * n_slots, a.vbox, 1))
     return DSA_ERR_CUDA;
-  const int64_t items = (pairs / p.item_rows + reqs) * 2 * S * p.splits;   // at most
+  const int64_t items = (pairs / p.item_rows + reqs) * p.halves * S * p.splits;   // at most
   if (items * 2 > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   const auto launch = p.mode == kPair ? launch_decode<kPair> : p.mode == kWide ? launch_decode<kWide>
-                                                                             : launch_decode<kNarrow>;
+                      : p.mode == kNarrow32 ? launch_narrow<kNarrow32> : launch_narrow<kNarrow16>;
   const cudaError_t e = launch(tq, tk, tv, a, items, stream);
   if (e != cudaSuccess) return DSA_ERR_CUDA;
   if (p.splits > 1) {

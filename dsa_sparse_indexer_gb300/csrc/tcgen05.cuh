@@ -55,6 +55,7 @@ constexpr uint32_t idesc_f16(int m, int n, bool bf16, bool b_mn_major) {
 }
 
 constexpr uint32_t kNegateA = 1u << 13;      // descriptor bit: D = or += -A B
+constexpr uint32_t kAcrossA = 1u << 15;      // descriptor bit: A MN-major
 
 // D (tensor memory) = or += A B: A from shared memory (_ss) or tensor memory (_ts).
 template <int CG>
@@ -352,6 +353,14 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
                  "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 // Sixteen columns of a warp's 32 lanes, a thread a lane.
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, "
+               "%8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+                 "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, "
                "%8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
@@ -386,6 +395,13 @@ __device__ __forceinline__ void tmem_store_pairs(uint32_t taddr, const uint32_t 
                "%8};" ::"r"(taddr),
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+// The largest of a warp's values that is no NaN.
+__device__ __forceinline__ float warp_max(float v) {
+  float d;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
+  return d;
 }
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
