@@ -912,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // products of 128 values): a step of 16 takes the 32 cycles in which A's 128 rows
 // are read, 2176 cycles for 128 keys where the rows as A would take 9250, and all
 // outputs fit 4 N columns, so that keys are read and scored once.
-//  * tensor memory: scores (N columns; a lane is a key), outputs (4 N; a lane is
+//  * tensor memory: two tiles' scores (N columns each; a lane is a key), outputs (4 N; a lane is
 //    one of 128 values);
 //  * shared memory: a tile's 128 keys as four slots of 128 values (32 KB) and one
 //    of the last 64 (16 KB), five and kTails of them; the queries; the weights (a
@@ -935,7 +935,7 @@ struct alignas(1024) NarrowSmem {
   uint8_t p[2][N * 128];      // the weights of 64 keys each
   float exchange[2][kNarrowWarps][N];
   WorkSlots<Item> work;
-  uint64_t full[kSlots], empty[kSlots], tail_full[kTails], tail_empty[kTails], qfull, qempty, sfull, pfull, pvdone,
+  uint64_t full[kSlots], empty[kSlots], tail_full[kTails], tail_empty[kTails], qfull, qempty, sfull[2], pfull, pvdone,
       exchanged, info[kInfo], drain;
   uint32_t pages[kInfo];
   uint32_t tmem;
@@ -1019,48 +1019,54 @@ __device__ __forceinline__ void narrow_products(const DecodeArgs& a, NarrowSmem<
   const uint64_t v0 = smem_desc_sw128(smem_u32(sm.kv), kSlotBlock, 1024);
   constexpr int kRow = N * 128 >> 4;         // a block of queries or weights in an address field
   Item it;
-  uint32_t j = 0, slot = 0, nq = 0;          // tiles, slots, items' queries so far
+  uint32_t j = 0, nq = 0;                    // tiles, items' queries so far
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     ok = ok && warp_wait(&sm.abort, bar, parity);
     tc_fence_after();
     return ok;
   };
-  for (uint32_t n = 0; next_item(sm.work, &sm.abort, n, ok, it); ++n) {
-    item_done(sm.work, n);
-    for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
-      if (t == it.t1 - 1 && !wait(&sm.qfull, nq++ & 1u)) break;
-      const uint32_t at = j % kTails;
-      if (!wait(&sm.tail_full[at], (j / kTails) & 1u)) break;
+  // Scores of stream tile v with its slot m, the tile's last 64 dimensions before the first.
+  auto scores = [&](uint32_t v, int m) {
+    const uint32_t d = tmem + (v & 1u) * N, at = v % kTails, u = 4 * v + m, k = u % kSlots;
+    if (m == 0) {
+      if (!wait(&sm.tail_full[at], (v / kTails) & 1u)) return;
       if (elect_one()) {
 #pragma unroll
         for (int s = 0; s < 4; ++s)
-          mma_ss<1>(tmem, t0 + at * (kSlotBlock >> 4) + s * 2, q0 + (kBlocks - 1) * kRow + s * 2, id_s, s == 0 ? 0u : 1u);
+          mma_ss<1>(d, t0 + at * (kSlotBlock >> 4) + s * 2, q0 + (kBlocks - 1) * kRow + s * 2, id_s, s == 0 ? 0u : 1u);
         tc_commit<1>(&sm.tail_empty[at]);
       }
       __syncwarp();
-      for (int m = 0; m < 4; ++m) {
-        const uint32_t k = (slot + m) % kSlots;
-        if (!wait(&sm.full[k], ((slot + m) / kSlots) & 1u)) break;
-        if (elect_one()) {
-          const uint64_t kd = k0 + k * (kSlot >> 4), qd = q0 + 2 * m * kRow;
+    }
+    if (!wait(&sm.full[k], (u / kSlots) & 1u)) return;
+    if (elect_one()) {
+      const uint64_t kd = k0 + k * (kSlot >> 4), qd = q0 + 2 * m * kRow;
 #pragma unroll
-          for (int s = 0; s < 8; ++s)
-            mma_ss<1>(tmem, kd + (s / 4) * (kSlotBlock >> 4) + (s % 4) * 2, qd + (s / 4) * kRow + (s % 4) * 2, id_s, 1u);
-          if (m == 3) {
-            tc_commit<1>(&sm.sfull);
-            if (t == it.t0) tc_commit<1>(&sm.qempty);
-          }
-        }
-        __syncwarp();
+      for (int s = 0; s < 8; ++s)
+        mma_ss<1>(d, kd + (s / 4) * (kSlotBlock >> 4) + (s % 4) * 2, qd + (s / 4) * kRow + (s % 4) * 2, id_s, 1u);
+    }
+    __syncwarp();
+  };
+  for (uint32_t n = 0; next_item(sm.work, &sm.abort, n, ok, it); ++n) {
+    item_done(sm.work, n);
+    for (int t = it.t1 - 1; ok && t >= it.t0; --t, ++j) {
+      const bool first = t == it.t1 - 1, last = t == it.t0;
+      if (first && wait(&sm.qfull, nq++ & 1u)) scores(j, 0);
+      for (int m = 1; ok && m < 4; ++m) scores(j, m);
+      if (!ok) break;
+      if (elect_one()) {
+        tc_commit<1>(&sm.sfull[j & 1u]);
+        if (last) tc_commit<1>(&sm.qempty);
       }
+      __syncwarp();
+      if (!last) scores(j + 1, 0);           // what the slots have room for, under this tile's softmax
       const int steps = value_steps<M>(it, t);
       if (!ok || !wait(&sm.pfull, j & 1u)) break;
       if (elect_one()) {
-        const bool first = t == it.t1 - 1;
 #pragma unroll 1
-        for (int m = 0; m < 4; ++m) {
-          const uint32_t k = (slot + m) % kSlots, d = tmem + N + m * N;
+        for (uint32_t m = 0; m < 4; ++m) {
+          const uint32_t k = (4 * j + m) % kSlots, d = tmem + 2 * N + m * N;
           const uint64_t vd = v0 + k * (kSlot >> 4);
 #pragma unroll
           for (int s = 0; s < 8; ++s)
@@ -1071,7 +1077,6 @@ __device__ __forceinline__ void narrow_products(const DecodeArgs& a, NarrowSmem<
         tc_commit<1>(&sm.pvdone);
       }
       __syncwarp();
-      slot += 4;
     }
   }
   if (!ok && (threadIdx.x & 31) == 0 && !cta_aborted(&sm.abort)) cta_abort(&sm.abort, a.flags);
@@ -1088,7 +1093,7 @@ template <int M>
 __device__ __forceinline__ void narrow_softmax(const DecodeArgs& a, NarrowSmem<M>& sm, uint32_t tmem, int warp) {
   constexpr int N = NarrowSmem<M>::N, kTile = Cut<M>::kTile;
   const int lane = threadIdx.x & 31, key = warp * 32 + lane;   // the thread's key of a tile; value of an output block
-  const uint32_t t_s = tmem + ((uint32_t)(warp * 32) << 16), t_o = t_s + N;
+  const uint32_t t_s = tmem + ((uint32_t)(warp * 32) << 16), t_o = t_s + 2 * N;
   uint32_t j = 0, rounds = 0;                // tiles, exchanges so far
   bool ok = true;
   // A value a row, one after another, which lane 0 of each warp has written.
@@ -1110,16 +1115,17 @@ __device__ __forceinline__ void narrow_softmax(const DecodeArgs& a, NarrowSmem<M
   for (uint32_t n = 0; next_item(sm.work, &sm.abort, n, ok); ++n) {
     const Item& it = sm.work.item[n & 1u];   // read where it lies
     const int i0 = uni(it.t0), i1 = uni(it.t1), nall = uni(it.nall), nfree = uni(it.nfree);
+    const int row0 = uni(it.row0), rows = uni(it.rows), tok0 = uni(it.tok0);
     float m[N], l[N];                        // the same m in every thread; l of the thread's keys
 #pragma unroll
     for (int r = 0; r < N; ++r) m[r] = -INFINITY, l[r] = 0.f;
     for (int t = i1 - 1; t >= i0; --t, ++j) {
-      ok = warp_wait(&sm.abort, &sm.sfull, j & 1u) &&
+      ok = warp_wait(&sm.abort, &sm.sfull[j & 1u], (j >> 1) & 1u) &&
            warp_wait(&sm.abort, &sm.info[j % kInfo], (j / kInfo) & 1u);
       if (!ok) break;
       tc_fence_after();
       uint32_t x[N];
-      load_rows(t_s, x);
+      load_rows(t_s + (j & 1u) * N, x);
       const uint32_t pages = *reinterpret_cast<volatile uint32_t*>(&sm.pages[j % kInfo]);
       if (pages != 0xffu || (t + 1) * kTile > nfree) {
         keep_branch();
@@ -1128,11 +1134,11 @@ __device__ __forceinline__ void narrow_softmax(const DecodeArgs& a, NarrowSmem<M
         const int own = !there || local < nfree ? -1 : (int)a.sm.global_id(it.shard, (uint32_t)local) - it.base;
 #pragma unroll
         for (int r = 0; r < N; ++r) {
-          const int tok = (int)fdiv((uint32_t)(it.row0 + min(r, it.rows - 1)), a.fH);
+          const int tok = (int)fdiv((uint32_t)(row0 + min(r, rows - 1)), a.fH);
           bool see = there;
           if (own >= 0)
             see = a.mask ? (own >> 5) < a.words &&
-                               ((uint32_t)__ldg(a.mask + (int64_t)(it.tok0 + tok) * a.words + (own >> 5)) >> (own & 31)) & 1u
+                               ((uint32_t)__ldg(a.mask + (int64_t)(tok0 + tok) * a.words + (own >> 5)) >> (own & 31)) & 1u
                          : own <= tok;
           if (!see) x[r] = 0xff800000u;
         }
@@ -1147,23 +1153,45 @@ __device__ __forceinline__ void narrow_softmax(const DecodeArgs& a, NarrowSmem<M
             *reinterpret_cast<float4*>(mine + r) = make_float4(v[r], v[r + 1], v[r + 2], v[r + 3]);
       });
       if (!ok) break;
-      float alpha[N];
-      bool moved = false;                    // some row's reference: alike in all threads
+      // Rows r to r + 3: the tile's maxima, scaled.
+      auto maxima = [&](int r, float (&mx)[4]) {
+        float4 w[kNarrowWarps];
 #pragma unroll
-      for (int r = 0; r < N; ++r) {
-        const float mx = fmaxf(fmax3(top[0][r], top[1][r], top[2][r]), top[3][r]) * a.c2;
-        const bool up = mx > m[r] + kRescaleGap;   // m = -inf takes any finite maximum
-        alpha[r] = 1.f;
-        if (up && m[r] != -INFINITY) alpha[r] = fast_exp2(m[r] - mx), moved = true;
-        m[r] = up ? mx : m[r];
-        l[r] *= alpha[r];
+        for (int k = 0; k < kNarrowWarps; ++k) w[k] = *reinterpret_cast<const float4*>(&top[k][r]);
+        mx[0] = fmaxf(fmax3(w[0].x, w[1].x, w[2].x), w[3].x) * a.c2;
+        mx[1] = fmaxf(fmax3(w[0].y, w[1].y, w[2].y), w[3].y) * a.c2;
+        mx[2] = fmaxf(fmax3(w[0].z, w[1].z, w[2].z), w[3].z) * a.c2;
+        mx[3] = fmaxf(fmax3(w[0].w, w[1].w, w[2].w), w[3].w) * a.c2;
+      };
+      bool up = false;                       // some row's maximum is above its reference: alike in all threads
+#pragma unroll
+      for (int r = 0; r < N; r += 4) {
+        float mx[4];
+        maxima(r, mx);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) up |= mx[e] > m[r + e] + kRescaleGap;   // m = -inf takes any finite maximum
       }
       if (t < i1 - 1) {                      // the last tile's values are in: weights and outputs are at rest
         ok = warp_wait(&sm.abort, &sm.pvdone, (j - 1) & 1u);
         if (!ok) break;
         tc_fence_after();
-        if (moved) {
-          keep_branch();
+      }
+      if (up) {
+        keep_branch();
+        float alpha[N];
+#pragma unroll
+        for (int r = 0; r < N; r += 4) {
+          float mx[4];
+          maxima(r, mx);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float old = m[r + e];
+            if (mx[e] > old + kRescaleGap) m[r + e] = mx[e];
+            alpha[r + e] = old == -INFINITY ? 1.f : fast_exp2(old - m[r + e]);
+            l[r + e] *= alpha[r + e];
+          }
+        }
+        if (t < i1 - 1) {
 #pragma unroll 1
           for (int b = 0; b < 4; ++b) {
             uint32_t o[N];
@@ -1205,7 +1233,7 @@ __device__ __forceinline__ void narrow_softmax(const DecodeArgs& a, NarrowSmem<M
 #pragma unroll
     for (int r = 0; r < N; ++r) inv[r] = 0.f;
     const int64_t to = ((int64_t)(parts ? it.split : 0) * a.sm.S + it.shard) * a.rows * a.H +
-                       (int64_t)it.tok0 * a.H + it.row0;   // [splits][S][rows][H]
+                       (int64_t)tok0 * a.H + row0;   // [splits][S][rows][H]
     float lse = -INFINITY;                   // of row `key`
     if (some) {
       const auto sums = exchange([&](float* mine) {
@@ -1229,20 +1257,24 @@ __device__ __forceinline__ void narrow_softmax(const DecodeArgs& a, NarrowSmem<M
         }
       }
     }
-    if (key < it.rows) (parts ? a.part_l : a.lse2)[to + key] = lse;
+    if (key < rows) (parts ? a.part_l : a.lse2)[to + key] = lse;
     if (some || !parts) {                    // the merge does not read an empty part
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {
         uint32_t o[N];
         if (some) load_rows(t_o + b * N, o);
         const int64_t at = to * kDv + b * 128 + key;
+        float v[N];                          // a row that saw nothing is zeros, whatever its column holds
 #pragma unroll
-        for (int r = 0; r < N; ++r) {
-          // A row that saw nothing is zeros, whatever its column holds.
-          const float v = inv[r] == 0.f || !some ? 0.f : __uint_as_float(o[r]) * inv[r];
-          if (r >= it.rows) continue;
-          if (parts) a.part_o[at + r * kDv] = v;
-          else a.out[at + r * kDv] = __float2bfloat16_rn(v);
+        for (int r = 0; r < N; ++r) v[r] = inv[r] == 0.f || !some ? 0.f : __uint_as_float(o[r]) * inv[r];
+        if (parts) {
+#pragma unroll
+          for (int r = 0; r < N; ++r)
+            if (r < rows) a.part_o[at + r * kDv] = v[r];
+        } else {
+#pragma unroll
+          for (int r = 0; r < N; ++r)
+            if (r < rows) a.out[at + r * kDv] = __float2bfloat16_rn(v[r]);
         }
         __syncwarp();
       }
@@ -1258,7 +1290,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     mla_decode_narrow_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                              const DecodeArgs a) {
   using Sm = NarrowSmem<M>;
-  constexpr uint32_t kCols = Sm::N == 16 ? 128 : 256;   // 5 N, as a power of two
+  constexpr uint32_t kCols = Sm::N == 16 ? 128 : 256;   // 6 N, as a power of two
   extern __shared__ unsigned char narrow_smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(narrow_smem_raw) + 1023) &
                                   ~static_cast<uintptr_t>(1023));
@@ -1279,7 +1311,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     }
     mbar_init(&sm.qfull, 1);
     mbar_init(&sm.qempty, 1);
-    mbar_init(&sm.sfull, 1);
+    for (int b = 0; b < 2; ++b) mbar_init(&sm.sfull[b], 1);
     mbar_init(&sm.pfull, kNarrowWarps);
     mbar_init(&sm.pvdone, 1);
     mbar_init(&sm.exchanged, kNarrowWarps);
