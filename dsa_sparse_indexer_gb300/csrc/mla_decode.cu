@@ -1132,16 +1132,20 @@ __device__ __forceinline__ void narrow_softmax(const DecodeArgs& a, NarrowSmem<M
         const int local = t * kTile + key;
         const bool there = ((pages >> (key >> 4)) & 1u) && local < nall;
         const int own = !there || local < nfree ? -1 : (int)a.sm.global_id(it.shard, (uint32_t)local) - it.base;
+        if (__any_sync(kFull, own >= 0)) {
+          keep_branch();
 #pragma unroll
-        for (int r = 0; r < N; ++r) {
-          const int tok = (int)fdiv((uint32_t)(row0 + min(r, rows - 1)), a.fH);
-          bool see = there;
-          if (own >= 0)
-            see = a.mask ? (own >> 5) < a.words &&
-                               ((uint32_t)__ldg(a.mask + (int64_t)(tok0 + tok) * a.words + (own >> 5)) >> (own & 31)) & 1u
-                         : own <= tok;
-          if (!see) x[r] = 0xff800000u;
+          for (int r = 0; r < N; ++r) {
+            const int tok = (int)fdiv((uint32_t)(row0 + min(r, rows - 1)), a.fH);
+            bool see = own <= tok;
+            if (own >= 0 && a.mask)
+              see = (own >> 5) < a.words &&
+                    ((uint32_t)__ldg(a.mask + (int64_t)(tok0 + tok) * a.words + (own >> 5)) >> (own & 31)) & 1u;
+            if (!see) x[r] = 0xff800000u;
+          }
         }
+#pragma unroll
+        for (int r = 0; r < N; ++r) x[r] = there ? x[r] : 0xff800000u;
       }
       const auto top = exchange([&](float* mine) {
         float v[N];
@@ -1229,12 +1233,9 @@ __device__ __forceinline__ void narrow_softmax(const DecodeArgs& a, NarrowSmem<M
     }
     if (!ok) break;
     const bool some = i1 > i0, parts = a.splits > 1;
-    float inv[N];
-#pragma unroll
-    for (int r = 0; r < N; ++r) inv[r] = 0.f;
     const int64_t to = ((int64_t)(parts ? it.split : 0) * a.sm.S + it.shard) * a.rows * a.H +
                        (int64_t)tok0 * a.H + row0;   // [splits][S][rows][H]
-    float lse = -INFINITY;                   // of row `key`
+    float scale = 0.f, lse = -INFINITY;      // row lane's: 1 / its sum
     if (some) {
       const auto sums = exchange([&](float* mine) {
 #pragma unroll
@@ -1248,33 +1249,51 @@ __device__ __forceinline__ void narrow_softmax(const DecodeArgs& a, NarrowSmem<M
       if (ok) ok = warp_wait(&sm.abort, &sm.pvdone, (j - 1) & 1u);
       if (!ok) break;
       tc_fence_after();
-#pragma unroll
-      for (int r = 0; r < N; ++r) {
-        const float sum = (sums[0][r] + sums[1][r]) + (sums[2][r] + sums[3][r]);
+      if (lane < N) {
+        const float sum = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
         if (sum != 0.f) {                    // a NaN too
-          inv[r] = 1.f / sum;
-          if (key == r) lse = m[r] + log2f(sum);
+          scale = 1.f / sum;
+          lse = log2f(sum);
         }
       }
+      __syncwarp();
+#pragma unroll
+      for (int r = 0; r < N; ++r)
+        if (lane == r) lse += m[r] == -INFINITY ? 0.f : m[r];   // (-inf: no sum either)
     }
-    if (key < rows) (parts ? a.part_l : a.lse2)[to + key] = lse;
+    if (warp == 0 && lane < rows) (parts ? a.part_l : a.lse2)[to + lane] = lse;
     if (some || !parts) {                    // the merge does not read an empty part
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {
         uint32_t o[N];
         if (some) load_rows(t_o + b * N, o);
-        const int64_t at = to * kDv + b * 128 + key;
-        float v[N];                          // a row that saw nothing is zeros, whatever its column holds
 #pragma unroll
-        for (int r = 0; r < N; ++r) v[r] = inv[r] == 0.f || !some ? 0.f : __uint_as_float(o[r]) * inv[r];
+        for (int r = 0; r < N; ++r) {        // a row that saw nothing is zeros, whatever its column holds
+          const float inv = __shfl_sync(kFull, scale, r);
+          o[r] = inv == 0.f || !some ? 0u : __float_as_uint(__uint_as_float(o[r]) * inv);
+        }
         if (parts) {
+          float* at = a.part_o + to * kDv + b * 128 + key;
 #pragma unroll
           for (int r = 0; r < N; ++r)
-            if (r < rows) a.part_o[at + r * kDv] = v[r];
+            if (r < rows) at[r * kDv] = __uint_as_float(o[r]);
         } else {
+          // Lanes swap until each has four neighbouring values of every fourth row.
+          const bool odd = (lane & 1) != 0, high = (lane & 2) != 0;
+          uint16_t* at = reinterpret_cast<uint16_t*>(a.out) + to * kDv + b * 128 + (key & ~3);
 #pragma unroll
-          for (int r = 0; r < N; ++r)
-            if (r < rows) a.out[at + r * kDv] = __float2bfloat16_rn(v[r]);
+          for (int r = 0; r < N; r += 4) {
+            uint32_t w[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float x0 = __uint_as_float(o[r + 2 * h]), x1 = __uint_as_float(o[r + 2 * h + 1]);
+              const float x = __shfl_xor_sync(kFull, odd ? x0 : x1, 1);
+              w[h] = odd ? pack16<true>(x, x1) : pack16<true>(x0, x);
+            }
+            const uint32_t x = __shfl_xor_sync(kFull, high ? w[0] : w[1], 2);
+            const int row = r + (lane & 3);
+            if (row < rows) *reinterpret_cast<uint2*>(at + row * kDv) = high ? make_uint2(x, w[1]) : make_uint2(w[0], x);
+          }
         }
         __syncwarp();
       }
