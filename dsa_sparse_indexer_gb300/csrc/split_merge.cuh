@@ -26,7 +26,7 @@ struct MergeArgs {
   float* lse2;               // [rows]
 };
 
-constexpr int kMergeGroups = 4, kMaxParts = 64;
+constexpr int kMergeGroups = 4, kMaxParts = 128;
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kMergeGroups * D / 4) merge_parts_kernel(const MergeArgs a) {
@@ -37,22 +37,25 @@ __global__ void __launch_bounds__(kMergeGroups * D / 4) merge_parts_kernel(const
   const int entry = (int)((row / a.H) % a.per_outer);
   if (entry < __ldg(a.bounds) || entry >= __ldg(a.bounds + a.n)) return;
   const int tid = threadIdx.x, group = tid / kLanes, at = tid % kLanes;
-  float l = -INFINITY, lse = 0.f;
+  float lse = 0.f;
   if (tid < 32) {                            // the first warp: weights and their sum
-    float l2 = -INFINITY;
-    if (tid < a.parts) l = a.l[tid * a.rows + row];
-    if (tid + 32 < a.parts) l2 = a.l[(tid + 32) * a.rows + row];
-    float m = fmaxf(l, l2);
+    float l[kMaxParts / 32], m = -INFINITY, total = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxParts / 32; ++k) {
+      const int p = tid + 32 * k;
+      l[k] = p < a.parts ? a.l[p * a.rows + row] : -INFINITY;
+      m = fmaxf(m, l[k]);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
     const float ref = m == -INFINITY ? 0.f : m;
-    const float w = fast_exp2(l - ref), w2 = fast_exp2(l2 - ref);
-    float total = w + w2;
+#pragma unroll
+    for (int k = 0; k < kMaxParts / 32; ++k) total += l[k] = fast_exp2(l[k] - ref);
 #pragma unroll
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
     const float inv = total == 0.f ? 0.f : 1.f / total;
-    weight[tid] = w * inv;
-    weight[tid + 32] = w2 * inv;
+#pragma unroll
+    for (int k = 0; k < kMaxParts / 32; ++k) weight[tid + 32 * k] = l[k] * inv;
     lse = total == 0.f ? -INFINITY : ref + log2f(total);
   }
   __syncthreads();
