@@ -9,27 +9,30 @@
 // tree mask names, or (no mask) those up to itself.
 //
 // All heads and rows of a request share its keys, so that (row, head) pairs are
-// the rows of one product.  An output of 512 values would fill tensor memory (512
-// columns), so an item takes half of it, and its scores are computed for both
-// halves: 2304 + 1024 cycles of products for 128 keys where 2176 are the least (65
-// %).  What the rows leave on chip decides how keys are held:
+// the rows of one product.  Where they are many, an output of 512 values would fill
+// tensor memory (512 columns), so an item takes half of it, and its scores are
+// computed for both halves: 2304 + 1024 cycles of products for 128 keys where 2176
+// are the least (65 %).  What the rows leave on chip decides how keys are held:
 //  * Pair, more than 128 rows a request: two CTAs with 128 rows each issue one
 //    product of M = 256, and either holds half of the keys' tile (of 128) and of the
 //    values' columns.  All queries in shared memory (144 KB) and a ring of 80 KB
 //    through which a tile's keys pass in three units, its values in one;
-//  * Wide, up to 128: the queries' first 256 dimensions in tensor memory, which
+//  * Wide, 33 to 128: the queries' first 256 dimensions in tensor memory, which
 //    leaves two stages of 72 KB for whole tiles of 64 keys: their value blocks stay
 //    until the value product.  (Scores with N = 64 take 1800 cycles where N = 128
 //    takes 1152 a tile, 4624 for 128 keys; one stage of 128 keys took 5.4 us a tile
 //    against 4.7 for two of these: its values could not be copied ahead.)
-//  * Narrow, up to 32: as Wide, but a product still reads 128 rows of A, and those
-//    past 32 may be anything, here the blocks that follow: the queries take 36 KB,
-//    and two items' fit.
+//  * Narrow, up to 32: keys and values as the products' rows, see there.
 // The first 256 of an item's output columns, and the last, are its half's value
 // blocks; of a tile's nine 64-value blocks the scores take the other five first.
 // One warp claims items while the kernel runs, one copies (tensor maps, a box per
 // page or 64 keys), one issues products, eight run the softmax.  The keys may be
 // split into parts that a second kernel joins.
+// Measured, 64 requests of 8192 to 16384 tokens on 4 shards, 128 heads: one token
+// 394 us (219 GFLOP, 949 MB; scores of both halves and the 64-key tiles' products
+// take 2.2 us of the 4.7 a tile and half), a tree of eight 1450 us (1.05 PFLOP/s of
+// the work, 1.6 of what is issued: tensor pipes 68 % busy); one sequence of 32768,
+// one token, 29 us.
 // The tail of a sequence's last page holds anything: its values are zeroed in
 // shared memory up to the 16 keys that a product step reads, its scores masked.
 // Every wait is bounded and raises DSA_FLAG_TIMEOUT when it runs out.
@@ -909,19 +912,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- few rows: keys and values as the products' rows ----------------------------
 // S^T = K Q^T (128 keys x N rows) and O^T = V^T P^T (512 values x N rows, four
-// products of 128 values): a step of 16 takes the 32 cycles in which A's 128 rows
-// are read, 2176 cycles for 128 keys where the rows as A would take 9250, and all
-// outputs fit 4 N columns, so that keys are read and scored once.
-//  * tensor memory: two tiles' scores (N columns each; a lane is a key), outputs (4 N; a lane is
-//    one of 128 values);
+// products of 128 values): all outputs fit 4 N columns, so that keys are read and
+// scored once.  A step of 16 takes 60 cycles here and 82 with values (their rows lie
+// across), whatever N up to 32, 4800 cycles for 128 keys where the rows as A would
+// take 9250 for both halves.
+//  * tensor memory: two tiles' scores (N columns each; a lane is a key), outputs
+//    (4 N; a lane is one of 128 values);
 //  * shared memory: a tile's 128 keys as four slots of 128 values (32 KB) and one
 //    of the last 64 (16 KB), five and kTails of them; the queries; the weights (a
 //    row's 64 keys to 128 bytes).  Keys stay for the value product, which frees
-//    them slot by slot; the slots left over are filled under the softmax.
+//    them slot by slot; what the slots have room for of the next tile is scored
+//    under the softmax.
 //  * four softmax warps, a thread a key, which exchange maxima and sums through
 //    shared memory; one issuing products, one copying, one claiming.
-// A tile's memory traffic (147 KB, 3.3 us at this SM's share of the bandwidth)
-// bounds it.
+// Measured, 128 requests of 2048 to 8192 tokens on 8 shards, 16 heads: 168 us, 4.6
+// TB/s; a tile takes 6100 cycles (the products' 4800 and the softmax's part that
+// they do not cover), 147 KB in 3.2 us of this SM's share.
 constexpr int kNarrowWarps = 4, kNarrowMma = 4, kNarrowLoad = 5, kNarrowClaim = 6, kNarrowThreads = 224;
 constexpr int kSlots = 5, kSlot = 32768, kSlotBlock = 16384;   // a slot's two blocks: 128 keys' 64 values
 
@@ -1368,6 +1374,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
 constexpr int kNarrowMost = 32;
 // How a call is cut: by the rows of a request (on average), and its keys into parts
 // where items are few.  Lengths are the device's: the table's width stands for them.
+// Rows of 64 requests, 8192 to 16384 tokens on 4 shards, in us: Narrow of 16 against
+// 32 rows an item 201 / 227 (16 rows); Narrow against Wide 201 / 354 (16), 238 / 376
+// (32), two items of it 397 / 392 (48), 413 / 410 (64), three 519 / 385 (96); Wide
+// against Pair 584 / 492 (256), 1020 / 784 (512).
 struct Plan {
   int mode, halves, item_rows, splits;
 };
@@ -1379,7 +1389,8 @@ Plan plan_for(int rows, int S, int H, int reqs, int64_t cap) {
   p.item_rows = p.mode == kPair ? Cut<kPair>::kItemRows : p.mode == kWide ? Cut<kWide>::kItemRows
                 : p.mode == kNarrow32 ? Cut<kNarrow32>::kItemRows : Cut<kNarrow16>::kItemRows;
   const int64_t items = (pairs + p.item_rows - 1) / p.item_rows * reqs * p.halves * S;
-  // 128 keys take a pair about 2.9 us, a CTA alone 3.4; a part has as many at least.
+  // 128 keys take a pair about 2.9 us (a half), a CTA alone 3.2 to 4.7; a part has as
+  // many at least.
   const int64_t tiles = (cap + 127) / 128, ctas = device_sms() / (p.mode == kPair ? 2 : 1);
   p.splits = choose_parts(items, ctas, tiles * (p.mode == kPair ? 2.9 : 3.4) + 4.0, (int64_t)rows * S * H, kDv,
                           tiles);

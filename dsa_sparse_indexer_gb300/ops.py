@@ -573,8 +573,17 @@ def _no_grad(*tensors):
 
 def _changed(*outs):
     """Outputs that the caller gave count as modified in place."""
-    for t in outs:
-        torch.autograd.graph.increment_version(t)
+    torch.autograd.graph.increment_version(outs)
+
+
+def _output(out, name: str, shape, dtype, device):
+    """The caller's output, checked, or a new one (is it the caller's?)."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device), False
+    _need(out, name, dtype, len(shape))
+    if out.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(out.shape)}")
+    return out, True
 
 
 @functools.lru_cache(maxsize=4096)
@@ -617,14 +626,8 @@ def mla_prefill(q, k_nope, k_pe, v, cu_q, cu_k, scale: float, causal: bool = Tru
     n = cu_q.shape[0] - 1
     if n < 0 or cu_k.shape[0] != n + 1:
         raise ValueError("cu_q and cu_k must have one entry more than there are sequences")
-    if out is None:
-        out = torch.empty((Tq, H, MLA_DVH), dtype=dtype, device=q.device)
-    if lse2 is None:
-        lse2 = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
-    _need(out, "out", dtype, 3)
-    _need(lse2, "lse2", torch.float32, 2)
-    if tuple(out.shape) != (Tq, H, MLA_DVH) or tuple(lse2.shape) != (Tq, H):
-        raise ValueError("out must be [Tq, H, 128] and lse2 [Tq, H]")
+    out, given = _output(out, "out", (Tq, H, MLA_DVH), dtype, q.device)
+    lse2, given2 = _output(lse2, "lse2", (Tq, H), torch.float32, q.device)
     _no_grad(q, k_nope, k_pe, v, out, lse2)
     need = _mla_prefill_work(q.get_device(), Tq, Tk, n, H)
     if work is None and need:
@@ -638,7 +641,8 @@ def mla_prefill(q, k_nope, k_pe, v, cu_q, cu_k, scale: float, causal: bool = Tru
             _ptr(k_pe), pe_token, _ptr(v), v_token, v_head, _ptr(cu_q), _ptr(cu_k), n, Tq, Tk, H,
             ROPE_DTYPES[dtype], float(scale), int(bool(causal)), _ptr(out), _ptr(lse2), _ptr(work),
             _ptr(err_flags), _raw_stream(q))
-    _changed(out, lse2)
+    if given or given2:
+        _changed(out, lse2)
     return out, lse2
 
 
@@ -684,14 +688,8 @@ def mla_decode(q, kv_cache, block_table, block_size: int, query_starts, seq_lens
         words = tree_mask.shape[1]
         if tree_mask.shape[0] != rows or words < 1:
             raise ValueError("tree_mask must be [rows, words]")
-    if out is None:
-        out = torch.empty((S, rows, H, MLA_DV), dtype=torch.bfloat16, device=q.device)
-    if lse2 is None:
-        lse2 = torch.empty((S, rows, H), dtype=torch.float32, device=q.device)
-    _need(out, "out", torch.bfloat16, 4)
-    _need(lse2, "lse2", torch.float32, 3)
-    if tuple(out.shape) != (S, rows, H, MLA_DV) or tuple(lse2.shape) != (S, rows, H):
-        raise ValueError("out must be [S, rows, H, 512] and lse2 [S, rows, H]")
+    out, given = _output(out, "out", (S, rows, H, MLA_DV), torch.bfloat16, q.device)
+    lse2, given2 = _output(lse2, "lse2", (S, rows, H), torch.float32, q.device)
     _no_grad(q, kv_cache, out, lse2)
     need = _mla_decode_work(q.get_device(), rows, S, H, reqs, max_blocks, block_size)
     if work is None and need:
@@ -706,7 +704,8 @@ def mla_decode(q, kv_cache, block_table, block_size: int, query_starts, seq_lens
             max_blocks, block_size, _ptr(query_starts), _ptr(seq_lens), _ptr(tree_mask), words, rows,
             S, I, H, float(scale), _ptr(out), _ptr(lse2), _ptr(work), _ptr(err_flags),
             _raw_stream(q))
-    _changed(out, lse2)
+    if given or given2:
+        _changed(out, lse2)
     return out, lse2
 
 
@@ -771,19 +770,14 @@ def indexer_query_fp8(q, weights, positions, cos_sin_cache, factor: float = 1.0,
     T, H, _ = q.shape
     if tuple(weights.shape) != (T, H) or positions.shape[0] != T:
         raise ValueError("weights must be [T, H] and positions [T]")
-    if q_out is None:
-        q_out = torch.empty((T, H, IDX_DIM), dtype=torch.uint8, device=q.device)
-    if weights_out is None:
-        weights_out = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    _need(q_out, "q_out", torch.uint8, 3)
-    _need(weights_out, "weights_out", torch.float32, 2)
-    if tuple(q_out.shape) != (T, H, IDX_DIM) or tuple(weights_out.shape) != (T, H):
-        raise ValueError("q_out must be [T, H, 128] and weights_out [T, H]")
+    q_out, given = _output(q_out, "q_out", (T, H, IDX_DIM), torch.uint8, q.device)
+    weights_out, given2 = _output(weights_out, "weights_out", (T, H), torch.float32, q.device)
     _no_grad(q, weights, weights_out, cos_sin_cache)
     context = _together(q, weights, positions, cos_sin_cache, q_out, weights_out, err_flags)
     _launch(context, "dsa_indexer_query_fp8", _ptr(q), q_token, q_head, _ptr(weights),
             float(factor), _ptr(positions), _ptr(cos_sin_cache), cos_sin_cache.shape[0],
             cos_sin_cache.shape[1], first, ROPE_LAYOUTS[layout], T, H, _ptr(q_out),
             _ptr(weights_out), _ptr(err_flags), _raw_stream(q))
-    _changed(q_out, weights_out)
+    if given or given2:
+        _changed(q_out, weights_out)
     return q_out, weights_out

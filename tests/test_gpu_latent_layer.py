@@ -105,3 +105,38 @@ def test_indexer_selects_over_its_cache():
                                torch.tensor([T], dtype=torch.int32, device="cuda"), I, SCALE)
     assert (l2 - d2).abs().max() <= 2e-3
     assert (sparse.float() - dense.float()).abs().max() <= 4 * 2.0 ** -8 * L["cache"].float().abs().max()
+
+
+def test_inference_mode_and_versions():
+    """Outputs that the caller gave count as changed; tensors made under
+    inference_mode, which have no version, are taken as well."""
+    import dsa_sparse_indexer_gb300 as dsa
+    T, heads = 3, 2
+
+    def run(given):
+        q, kv = torch.zeros(T, heads, 192, device="cuda").half(), torch.zeros(T, heads, 256, device="cuda").half()
+        cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+        o, l2 = torch.ones(T, heads, 128, device="cuda").half(), torch.ones(T, heads, device="cuda")
+        dsa.mla_prefill(q, kv[..., :128], torch.zeros(T, 64, device="cuda").half(), kv[..., 128:], cu, cu, 1.0,
+                        out=o if given else None, lse2=l2 if given else None)
+        cache = torch.zeros(1, 64, 576, device="cuda").bfloat16()
+        o2 = torch.ones(1, T, heads, 512, device="cuda").bfloat16()
+        dsa.mla_decode(torch.zeros(T, heads, 576, device="cuda").bfloat16(), cache,
+                       torch.zeros(1, 1, 1, dtype=torch.int32, device="cuda"), 64, cu,
+                       torch.tensor([T], dtype=torch.int32, device="cuda"), 1, 1.0, out=o2 if given else None)
+        cs, pos = dsa.rope_table(8, 64), torch.arange(T, dtype=torch.int32, device="cuda")
+        keys = torch.zeros(1, 64, 128, dtype=torch.uint8, device="cuda")
+        dsa.indexer_key_insert(torch.zeros(T, 128, device="cuda").bfloat16(), torch.ones(128, device="cuda"), None, 1e-6,
+                               pos, cs, pos.view(1, T), keys)
+        w = torch.ones(T, heads, device="cuda")
+        dsa.indexer_query_fp8(torch.zeros(T, heads, 128, device="cuda").bfloat16(), w, pos, cs,
+                              weights_out=w if given else None)
+        torch.cuda.synchronize()
+        return o, l2, o2, keys, w
+
+    for given in (False, True):
+        with torch.inference_mode():
+            run(given)
+    before = [t._version for t in run(False)]
+    after = [t._version for t in run(True)]
+    assert [b - a for a, b in zip(before, after)] == [1, 1, 1, 0, 1] and before[3] > 0
