@@ -29,7 +29,7 @@
 // page or 64 keys), one issues products, eight run the softmax.  The keys may be
 // split into parts that a second kernel joins.
 // Measured, 64 requests of 8192 to 16384 tokens on 4 shards, 128 heads: one token
-// 394 us (219 GFLOP, 949 MB; scores of both halves and the 64-key tiles' products
+// 360 us (219 GFLOP, 949 MB; scores of both halves and the 64-key tiles' products
 // take 2.2 us of the 4.7 a tile and half), a tree of eight 1450 us (1.05 PFLOP/s of
 // the work, 1.6 of what is issued: tensor pipes 68 % busy); one sequence of 32768,
 // one token, 29 us.
@@ -110,6 +110,7 @@ struct alignas(1024) DecodeSmem {
   uint64_t full[kUnits], empty[kUnits], qfull, qtm, qempty, sfull[2], pfull[2], pvdone, vtail[2],
       info[kInfo], drain;
   uint32_t tail_seq[2];       // Pair: place in the ring of the values that vtail counts
+  Order order;
   uint32_t pages[kInfo];      // valid pages of stream tile j, at j % kInfo: a bit per 16 keys
   uint32_t tmem;
   int blocks;                 // row blocks of all requests
@@ -129,6 +130,7 @@ struct DecodeArgs {
   uint32_t* flags;
   int64_t n_slots;
   int reqs, max_blocks, block, rows, H, words, splits;
+  int ordered;                // items in the requests' order by length
   int cap;                    // local tokens that a table row names
   int kbox, vbox;             // keys of a copy
   // |scale| log2(e), and the score product's descriptor bit that negates A for a
@@ -141,7 +143,7 @@ struct DecodeArgs {
 };
 
 struct Cursor {
-  int req = 0, before = 0;
+  int req = 0, before = 0;    // the request's place in the order, row blocks before it
 };
 
 __device__ __forceinline__ void rows_of(const DecodeArgs& a, int i, int& first, int& end) {
@@ -152,7 +154,8 @@ __device__ __forceinline__ void rows_of(const DecodeArgs& a, int i, int& first, 
 // Warp-wide: item `index` of blocks * halves * S * splits: halves and row blocks of a
 // request, which read the same keys, beside one another.
 template <int M>
-__device__ __forceinline__ Item find_item(const DecodeArgs& a, int blocks, int64_t index, Cursor& c) {
+__device__ __forceinline__ Item find_item(const DecodeArgs& a, const Order& order, int blocks, int64_t index,
+                                          Cursor& c) {
   constexpr int kItemRows = Cut<M>::kItemRows;
   const int lane = threadIdx.x & 31;
   Item it;
@@ -166,7 +169,7 @@ __device__ __forceinline__ Item find_item(const DecodeArgs& a, int blocks, int64
   for (int at = c.req;; at += 32) {
     const int i = at + lane;
     int first = 0, end = 0;
-    if (i < a.reqs) rows_of(a, i, first, end);
+    if (i < a.reqs) rows_of(a, in_order(order, a.ordered, i), first, end);
     const int mine = ((end - first) * a.H + kItemRows - 1) / kItemRows;
     int incl = mine;
 #pragma unroll
@@ -185,7 +188,7 @@ __device__ __forceinline__ Item find_item(const DecodeArgs& a, int blocks, int64
     c.before += __shfl_sync(kFull, incl, 31);
     if (at + 32 >= a.reqs) break;            // not reached: qb < blocks
   }
-  it.req = c.req;
+  it.req = in_order(order, a.ordered, c.req);
   int end;
   rows_of(a, it.req, it.tok0, end);
   it.n = end - it.tok0;
@@ -884,6 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.abort = 0;
     mbar_init_fence();
   }
+  if (a.ordered) longest_first(sm.order, a.reqs, tid, [&](int i) { return __ldg(a.lens + i); });
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) pair_sync();        // the other CTA's barriers are there
@@ -897,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int blocks = sm.blocks;
     Cursor cur;
     share_out<CG>(sm.work, &sm.abort, a.flags, (int64_t)blocks * 2 * a.sm.S * a.splits, rank,
-                  [&](int64_t i) { return find_item<M>(a, blocks, i, cur); });
+                  [&](int64_t i) { return find_item<M>(a, sm.order, blocks, i, cur); });
   } else if (rank == 0) {
     issue_products<M>(a, sm, tmem);
   }
@@ -925,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 //    under the softmax.
 //  * four softmax warps, a thread a key, which exchange maxima and sums through
 //    shared memory; one issuing products, one copying, one claiming.
-// Measured, 128 requests of 2048 to 8192 tokens on 8 shards, 16 heads: 168 us, 4.6
+// Measured, 128 requests of 2048 to 8192 tokens on 8 shards, 16 heads: 163 us, 4.7
 // TB/s; a tile takes 6100 cycles (the products' 4800 and the softmax's part that
 // they do not cover), 147 KB in 3.2 us of this SM's share.
 constexpr int kNarrowWarps = 4, kNarrowMma = 4, kNarrowLoad = 5, kNarrowClaim = 6, kNarrowThreads = 224;
@@ -944,6 +948,7 @@ struct alignas(1024) NarrowSmem {
   uint64_t full[kSlots], empty[kSlots], tail_full[kTails], tail_empty[kTails], qfull, qempty, sfull[2], pfull, pvdone,
       exchanged, info[kInfo], drain;
   uint32_t pages[kInfo];
+  Order order;
   uint32_t tmem;
   int blocks;
   int abort;
@@ -1346,6 +1351,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     sm.abort = 0;
     mbar_init_fence();
   }
+  if (a.ordered) longest_first(sm.order, a.reqs, tid, [&](int i) { return __ldg(a.lens + i); });
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1358,7 +1364,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     const int blocks = sm.blocks;
     Cursor cur;
     share_out<1>(sm.work, &sm.abort, a.flags, (int64_t)blocks * a.sm.S * a.splits, 0u,
-                 [&](int64_t i) { return find_item<M>(a, blocks, i, cur); });
+                 [&](int64_t i) { return find_item<M>(a, sm.order, blocks, i, cur); });
   } else {
     narrow_products<M>(a, sm, tmem);
   }
@@ -1379,7 +1385,7 @@ constexpr int kNarrowMost = 32;
 // (32), two items of it 397 / 392 (48), 413 / 410 (64), three 519 / 385 (96); Wide
 // against Pair 584 / 492 (256), 1020 / 784 (512).
 struct Plan {
-  int mode, halves, item_rows, splits;
+  int mode, halves, item_rows, splits, ordered;
 };
 Plan plan_for(int rows, int S, int H, int reqs, int64_t cap) {
   const int64_t pairs = ((int64_t)rows * H + reqs - 1) / reqs;
@@ -1394,6 +1400,7 @@ Plan plan_for(int rows, int S, int H, int reqs, int64_t cap) {
   const int64_t tiles = (cap + 127) / 128, ctas = device_sms() / (p.mode == kPair ? 2 : 1);
   p.splits = choose_parts(items, ctas, tiles * (p.mode == kPair ? 2.9 : 3.4) + 4.0, (int64_t)rows * S * H, kDv,
                           tiles);
+  p.ordered = order_pays(reqs, items * p.splits, ctas);
   return p;
 }
 
@@ -1457,7 +1464,7 @@ extern "C" dsa_status dsa_mla_decode(const uint16_t* q, const uint16_t* kv_cache
   if (!work) p.splits = 1;
   DecodeArgs a{reinterpret_cast<const __nv_bfloat16*>(q), block_table, query_starts, seq_lens, tree_mask, reinterpret_cast<__nv_bfloat16*>(out),
                lse2, nullptr, nullptr, err_flags, n_slots, reqs, max_blocks, block_size, rows, H,
-               mask_words, p.splits, (int)cap, std::min(block_size, 64), std::min(block_size, (int)Shape<kPair>::kVKeys),
+               mask_words, p.splits, p.ordered, (int)cap, std::min(block_size, 64), std::min(block_size, (int)Shape<kPair>::kVKeys),
                scale == 0.f ? 0x1p-100f : fabsf(scale) * kLog2e, scale < 0.f ? kNegateA : 0u,
                ShardMath(S, I), FastDiv(block_size), FastDiv(H)};
   if (p.splits > 1) {

@@ -28,7 +28,7 @@
 // Measured, one sequence of 8192, 128 heads, causal: 1720 us, 1.60 PFLOP/s of the
 // 1.96 that a library product reaches; 3753 with one CTA an item, a warp issuing
 // for both query tiles and a thread a row in the softmax.  16 heads, 500 queries of
-// 16384 keys: 78 to 82 us, 1.0 PFLOP/s (items of uneven length on 76 pairs).
+// 16384 keys: 79 us, 1.05 PFLOP/s, its keys in parts.
 #include <algorithm>
 
 #include "split_merge.cuh"
@@ -91,6 +91,7 @@ struct alignas(1024) PrefillSmem {
   WorkSlots<Item> work;
   uint64_t qfull[2], qempty[2], full[kUnits], empty[kUnits], sfull[2], phalf[2], pfull[2], ofull[2], vtail[2],
       drain[2];
+  Order order;
   uint32_t tmem;
   int blocks;                                // query blocks of all sequences
   int abort;
@@ -103,7 +104,7 @@ struct PrefillArgs {
   float* lse2;                // [Tq][H]
   float *part_o, *part_l;     // [splits][Tq][H][kDv], [splits][Tq][H]
   uint32_t* flags;
-  int n, Tq, Tk, H, group, splits, causal;
+  int n, Tq, Tk, H, group, splits, causal, ordered;   // items in the sequences' order by length
   // |scale| log2(e), and the score product's descriptor bit that negates A for a
   // negative scale.  A scale of 0 is taken as 2^-100: finite scores then count
   // alike, masked ones are -inf as ever.
@@ -120,15 +121,15 @@ __device__ __forceinline__ void bounds_of(const int32_t* cu, int i, int T, int& 
 __device__ __forceinline__ int end_of(const Item& it, int g) { return g == 0 ? it.end[0] : it.end[1]; }
 
 struct Cursor {               // where the last item's sequence was found
-  int seq = 0, before = 0;    // query blocks before it
+  int seq = 0, before = 0;    // its place in the order, query blocks before it
 };
 
 // Warp-wide: item `index` of a.H * blocks * splits.  Heads go in groups whose
 // keys and values stay in L2 together; within one, a sequence's longest blocks
 // (its last) come first, so that the CTAs, which claim items, end alike.
 template <int CG>
-__device__ __forceinline__ Item find_item(const PrefillArgs& a, int blocks, int64_t index,
-                                          Cursor& c) {
+__device__ __forceinline__ Item find_item(const PrefillArgs& a, const Order& order, int blocks,
+                                          int64_t index, Cursor& c) {
   constexpr int kGroup = Shape<CG>::kGroup, kBlockQ = Shape<CG>::kBlockQ;
   const int lane = threadIdx.x & 31;
   Item it;
@@ -145,7 +146,7 @@ __device__ __forceinline__ Item find_item(const PrefillArgs& a, int blocks, int6
   for (int base = c.seq;; base += 32) {
     const int i = base + lane;
     int first = 0, end = 0;
-    if (i < a.n) bounds_of(a.cu_q, i, a.Tq, first, end);
+    if (i < a.n) bounds_of(a.cu_q, in_order(order, a.ordered, i), a.Tq, first, end);
     const int mine = (end - first + kBlockQ - 1) / kBlockQ;
     int incl = mine;
 #pragma unroll
@@ -166,8 +167,9 @@ __device__ __forceinline__ Item find_item(const PrefillArgs& a, int blocks, int6
     if (base + 32 >= a.n) break;             // not reached: qb < blocks
   }
   int q0, q1, k0, k1;
-  bounds_of(a.cu_q, c.seq, a.Tq, q0, q1);
-  bounds_of(a.cu_k, c.seq, a.Tk, k0, k1);
+  const int seq = in_order(order, a.ordered, c.seq);
+  bounds_of(a.cu_q, seq, a.Tq, q0, q1);
+  bounds_of(a.cu_k, seq, a.Tk, k0, k1);
   const int at = (nb - 1 - local) * kBlockQ;
   it.row0 = q0 + at;
   it.rows = min(kBlockQ, q1 - it.row0);
@@ -655,6 +657,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.abort = 0;
     mbar_init_fence();
   }
+  if (a.ordered)
+    longest_first(sm.order, a.n, tid, [&](int i) { return __ldg(a.cu_k + i + 1) - __ldg(a.cu_k + i); });
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) pair_sync();        // the other CTA's barriers are there
@@ -668,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int blocks = sm.blocks;
       Cursor cur;
       share_out<CG>(sm.work, &sm.abort, a.flags, (int64_t)blocks * a.H * a.splits, rank,
-                    [&](int64_t i) { return find_item<CG>(a, blocks, i, cur); });
+                    [&](int64_t i) { return find_item<CG>(a, sm.order, blocks, i, cur); });
     } else if (rank == 0) {
       issue_products<CG, BF16>(a, sm, tmem, warp - kMmaWarp);
     }
@@ -692,7 +696,7 @@ constexpr int kSmem = (int)sizeof(PrefillSmem) + 1024;
 // 2214; 4096, 32 heads 281 / 358; 2048, 128 heads 167 / 204; eight of 1024, 32 heads
 // 127 / 132; 16 of 512 (just a pair's item) 91 / 88.
 struct Plan {
-  int cg, splits;
+  int cg, splits, ordered;
 };
 Plan plan_for(int Tq, int Tk, int n, int H) {
   Plan p;
@@ -702,6 +706,7 @@ Plan plan_for(int Tq, int Tk, int n, int H) {
   // A key tile takes an item about 1.9 us; a part has four at least.
   const int64_t tiles = (Tk / n + kTileK - 1) / kTileK;
   p.splits = choose_parts(items, device_sms() / p.cg, tiles * 1.9 + 5.0, (int64_t)Tq * H, kDv, tiles / 4);
+  p.ordered = order_pays(n, items * p.splits, device_sms() / p.cg);
   return p;
 }
 
@@ -776,7 +781,7 @@ extern "C" dsa_status dsa_mla_prefill(const void* q, int64_t q_token, int64_t q_
   // Heads whose keys and values (512 bytes a token and head) fit half of L2.
   const int64_t fit = ((int64_t)48 << 20) / (512 * (int64_t)std::max(Tk, 1));
   PrefillArgs a{cu_q, cu_k, out, lse2, nullptr, nullptr, err_flags, n, Tq, Tk, H,
-                (int)std::max<int64_t>(1, std::min<int64_t>(fit, H)), splits, causal != 0,
+                (int)std::max<int64_t>(1, std::min<int64_t>(fit, H)), splits, causal != 0, p.ordered,
                 scale == 0.f ? 0x1p-100f : fabsf(scale) * kLog2e, scale < 0.f ? kNegateA : 0u};
   if (splits > 1) {
     a.part_o = work;

@@ -309,3 +309,18 @@ def test_split_tree():
     assert _lib.load().dsa_mla_decode_work(33, 2, 4, 1, args[2].shape[2], 64) > 0
     out, lse2 = dsa.mla_decode(*args, SCALE, tree_mask=mask)
     check(args, SCALE, mask, out, lse2)
+
+
+@pytest.mark.parametrize("reqs,H", [(33, 40), (128, 2), (129, 2)])
+def test_requests_in_any_order(reqs, H):
+    """Requests are taken longest first, up to 128 of them: lengths with repeats,
+    none ascending or descending, some empty."""
+    import dsa_sparse_indexer_gb300 as dsa
+    rng = np.random.default_rng(reqs)
+    drafts = [int(x) for x in rng.integers(0, 3, reqs)]
+    lens = [int(x) for x in rng.integers(0, 200, reqs)]
+    args = inputs(drafts, lens, H, 2, 1, 16, seed=reqs)
+    err = dsa.new_error_flags("cuda")
+    out, lse2 = dsa.mla_decode(*args, SCALE, err_flags=err)
+    assert int(err) == 0
+    check(args, SCALE, None, out, lse2)

@@ -265,3 +265,19 @@ def test_two_streams_and_the_same_twice():
             got.append(dsa.mla_prefill(*args))
     torch.cuda.synchronize()
     assert all(torch.equal(g[0], want[0]) and torch.equal(g[1], want[1]) for g in got)
+
+
+@pytest.mark.parametrize("n", [33, 128, 129])
+def test_sequences_in_any_order(n):
+    """Sequences are taken longest first, up to 128 of them: lengths with repeats,
+    none ascending or descending, some empty."""
+    rng = np.random.default_rng(n)
+    lens = [(int(a), int(b)) for a, b in zip(rng.integers(0, 3, n), rng.integers(0, 200, n))]
+    lens[n // 2] = (40, 300)
+    import dsa_sparse_indexer_gb300 as dsa
+    q, kv, pe, cu_q, cu_k = inputs(lens, 2, torch.bfloat16, seed=n)
+    kn, v = kv[..., :128], kv[..., 128:]
+    err = dsa.new_error_flags("cuda")
+    out, lse2 = dsa.mla_prefill(q, kn, pe, v, cu_q, cu_k, SCALE, err_flags=err)
+    assert int(err) == 0
+    check(q, kn, pe, v, cu_q, cu_k, SCALE, True, out, lse2)
