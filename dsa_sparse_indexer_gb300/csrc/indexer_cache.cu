@@ -19,7 +19,7 @@
 // its head once more through the arithmetic, with its errors.
 // Measured: 64 keys into 4 shards 4.3 us, 32768 keys 12.4 us and 131072 35.7 (86 MB,
 // 2.4 TB/s: the issue slots of norm, rotation and stores); the queries of 64 tokens,
-// 64 heads 6.3 us, of 4096 tokens 43 us (104 MB, 2.4 TB/s: the issue slots of
+// 64 heads 6.3 us, of 4096 tokens 39 us (104 MB, 2.7 TB/s: the issue slots of
 // rotation, scale and rounding).  Two or four keys a thread, its weights read once:
 // 32768 keys 10.7 and 13.3 us where one takes 10.0, back to back.
 #include <cuda_bf16.h>
@@ -239,8 +239,11 @@ __device__ __forceinline__ float turned_to_odd(const Turn<P>& t, int e, float x,
   return z;
 }
 
+// Nine blocks an SM (56 registers) hide more of a row's latency than the seven that
+// 72 registers leave: 4096 tokens of 64 heads 39.1 us against 43.7; ten 42.9.  (Some
+// of the half layout's spill, at the second pass.)
 template <int P, int kHeads>
-__global__ void __launch_bounds__(kThreads) indexer_query_kernel(const QueryArgs a) {
+__global__ void __launch_bounds__(kThreads, kHeads == 4 && P != kAnywhere ? 9 : 1) indexer_query_kernel(const QueryArgs a) {
   __shared__ __align__(16) float rows[P == kAnywhere ? kRows : 1][kDim];
   const int lane16 = threadIdx.x & (kLanes - 1), r = threadIdx.x / kLanes;
   const int token = blockIdx.x / a.per_token;
