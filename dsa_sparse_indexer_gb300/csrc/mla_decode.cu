@@ -1404,6 +1404,11 @@ Plan plan_for(int rows, int S, int H, int reqs, int64_t cap) {
   return p;
 }
 
+// Local tokens that a table row names, as far as the kernels count.
+int64_t table_tokens(int max_blocks, int block_size) {
+  return std::min<int64_t>((int64_t)max_blocks * block_size, (int64_t)1 << 30);
+}
+
 template <int M>
 cudaError_t launch_decode(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                           const DecodeArgs& a, int64_t items, cudaStream_t stream) {
@@ -1435,7 +1440,7 @@ using namespace dsa;
 extern "C" int64_t dsa_mla_decode_work(int rows, int S, int H, int reqs, int max_blocks,
                                        int block_size) {
   if (rows < 1 || S < 1 || H < 1 || reqs < 1 || max_blocks < 1 || block_size < 1) return 0;
-  const int parts = plan_for(rows, S, H, reqs, (int64_t)max_blocks * block_size).splits;
+  const int parts = plan_for(rows, S, H, reqs, table_tokens(max_blocks, block_size)).splits;
   return parts == 1 ? 0 : (int64_t)parts * S * rows * H * (kDv + 1) * 4;
 }
 
@@ -1459,7 +1464,7 @@ extern "C" dsa_status dsa_mla_decode(const uint16_t* q, const uint16_t* kv_cache
   const int64_t pairs = (int64_t)rows * H;
   if (n_slots > INT32_MAX || pairs > ((int64_t)1 << 30) || (int64_t)S * reqs > ((int64_t)1 << 30))
     return DSA_ERR_UNSUPPORTED;
-  const int64_t cap = std::min<int64_t>((int64_t)max_blocks * block_size, (int64_t)1 << 30);
+  const int64_t cap = table_tokens(max_blocks, block_size);
   Plan p = plan_for(rows, S, H, reqs, cap);
   if (!work) p.splits = 1;
   DecodeArgs a{reinterpret_cast<const __nv_bfloat16*>(q), block_table, query_starts, seq_lens, tree_mask, reinterpret_cast<__nv_bfloat16*>(out),

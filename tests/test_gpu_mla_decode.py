@@ -324,3 +324,27 @@ def test_requests_in_any_order(reqs, H):
     out, lse2 = dsa.mla_decode(*args, SCALE, err_flags=err)
     assert int(err) == 0
     check(args, SCALE, None, out, lse2)
+
+
+UNEVEN = [([20, 1, 0, 1, 1, 1], [300, 5, 9, 1, 140, 128], 4, 16), ([30, 1, 1, 1], [31, 700, 129, 64], 3, 64),
+          ([1, 70, 1, 1, 1, 1, 1, 1], [900, 70, 1, 2, 300, 17, 128, 256], 2, 32)]
+
+
+@pytest.mark.parametrize("with_tree", [False, True])
+@pytest.mark.parametrize("drafts,lens,H,block", UNEVEN)
+def test_few_rows_and_one_request_of_many(drafts, lens, H, block, with_tree):
+    """Few rows a request on average, one with several blocks of them."""
+    test_parity(drafts, lens, H, 2, 1, block, with_tree)
+
+
+def test_split_tokens_of_32_rows():
+    """Two tokens of 16 heads and one of 32, many tokens in parts."""
+    import dsa_sparse_indexer_gb300 as dsa
+    from dsa_sparse_indexer_gb300 import _lib
+    for H, drafts in ((16, [2]), (32, [1])):
+        args = inputs(drafts, [5000], H, 1, 1, 64, seed=H)
+        rows, table = args[0].shape[0], args[2]
+        need = _lib.load().dsa_mla_decode_work(rows, 1, H, 1, table.shape[2], 64)
+        assert need > 0
+        out, lse2 = dsa.mla_decode(*args, SCALE)
+        check(args, SCALE, None, out, lse2)
