@@ -37,6 +37,7 @@
 // shared memory up to the 16 keys that a product step reads, its scores masked.
 // Every wait is bounded and raises DSA_FLAG_TIMEOUT when it runs out.
 #include <algorithm>
+#include <numeric>
 
 #include "split_merge.cuh"
 
@@ -1482,7 +1483,10 @@ extern "C" dsa_status dsa_mla_decode(const uint16_t* q, const uint16_t* kv_cache
       !encode_map16(&tk, kv_cache, true, kDqk, n_slots, S, row, row * n_slots, a.kbox, 1) ||
       !encode_map16(&tv, kv_cache, true, kDqk, n_slots, S, row, row * n_slots, a.vbox, 1))
     return DSA_ERR_CUDA;
-  const int64_t items = (pairs / p.item_rows + reqs) * p.halves * S * p.splits;   // at most
+  // At most: a request's pairs are a multiple of H, so that its last block has a
+  // common divisor at least.  (Clusters without an item have to be cancelled too.)
+  const int64_t blocks = (pairs + (int64_t)reqs * (p.item_rows - std::gcd(H, p.item_rows))) / p.item_rows;
+  const int64_t items = blocks * p.halves * S * p.splits;
   if (items * 2 > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   const auto launch = p.mode == kPair ? launch_decode<kPair> : p.mode == kWide ? launch_decode<kWide>
                       : p.mode == kNarrow32 ? launch_narrow<kNarrow32> : launch_narrow<kNarrow16>;

@@ -717,7 +717,7 @@ cudaError_t launch_prefill(const CUtensorMap& q, const CUtensorMap& k, const CUt
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   // An item a cluster; those that do not start at once are mostly taken over.
-  const int64_t most = ((int64_t)a.Tq / Shape<CG>::kBlockQ + a.n) * a.H * a.splits;
+  const int64_t most = ((int64_t)a.Tq + (int64_t)a.n * (Shape<CG>::kBlockQ - 1)) / Shape<CG>::kBlockQ * a.H * a.splits;
   const unsigned grid = (unsigned)(most * CG);
   return launch_kernel(kernel, dim3(grid), dim3(kThreads), (size_t)kSmem, stream, CG == 2 ? 2u : 0u,
                        q, k, pe, v, a);

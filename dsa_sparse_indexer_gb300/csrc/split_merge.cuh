@@ -3,10 +3,11 @@
 // Part p of row i holds O_p (fp32, normalised by its own sum) and l_p, the
 // base-2 log of that sum (-inf: nothing visible, O_p then unwritten and not
 // read): out = sum_p w_p O_p / sum_p w_p and lse2 = M + log2 sum_p w_p with
-// M = max_p l_p, w_p = 2^(l_p - M).  A block takes a row: groups of D / 4 threads
-// take every kGroups-th part, a thread four neighbouring values, and add up in
-// shared memory; the parts' loads are independent.  (128 rows of 76 parts, 20 MB: a
-// warp a row with all parts in turn left most SMs idle, 45 us.)
+// M = max_p l_p, w_p = 2^(l_p - M).  A block takes a row or, with many parts, a
+// quarter of it: groups of threads take every kGroups-th part, a thread four
+// neighbouring values, and add up in shared memory; the parts' loads are
+// independent.  (128 rows of 76 parts, 20 MB: a warp a row with all parts in turn
+// left most SMs idle, 45 us.)
 #pragma once
 
 #include "tcgen05.cuh"
@@ -26,17 +27,24 @@ struct MergeArgs {
   float* lse2;               // [rows]
 };
 
-constexpr int kMergeGroups = 4, kMaxParts = 128;
+constexpr int kMaxParts = 128;
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kMergeGroups * D / 4) merge_parts_kernel(const MergeArgs a) {
-  constexpr int kLanes = D / 4;              // threads of a group
+template <int D, int kGroups>
+struct MergeCut {
+  static constexpr int kLanes = D / 4 < 512 / kGroups ? D / 4 : 512 / kGroups;   // threads of a group
+  static constexpr int kBlocks = D / 4 / kLanes;                                 // blocks of a row
+};
+
+template <int D, bool BF16, int kGroups>
+__global__ void __launch_bounds__(kGroups * MergeCut<D, kGroups>::kLanes) merge_parts_kernel(const MergeArgs a) {
+  constexpr int kLanes = MergeCut<D, kGroups>::kLanes, kBlocks = MergeCut<D, kGroups>::kBlocks;
   __shared__ float weight[kMaxParts];
-  __shared__ float4 sums[kMergeGroups - 1][kLanes];
-  const int64_t row = blockIdx.x;
+  __shared__ float4 sums[kGroups - 1][kLanes];
+  const int64_t row = blockIdx.x / kBlocks;
   const int entry = (int)((row / a.H) % a.per_outer);
   if (entry < __ldg(a.bounds) || entry >= __ldg(a.bounds + a.n)) return;
-  const int tid = threadIdx.x, group = tid / kLanes, at = tid % kLanes;
+  const int tid = threadIdx.x, group = tid / kLanes;
+  const int at = (int)(blockIdx.x % kBlocks) * kLanes + tid % kLanes;
   float lse = 0.f;
   if (tid < 32) {                            // the first warp: weights and their sum
     float l[kMaxParts / 32], m = -INFINITY, total = 0.f;
@@ -61,7 +69,7 @@ __global__ void __launch_bounds__(kMergeGroups * D / 4) merge_parts_kernel(const
   __syncthreads();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int p = group; p < a.parts; p += kMergeGroups) {
+  for (int p = group; p < a.parts; p += kGroups) {
     const float w = weight[p];
     if (w != 0.f) {                          // else it may be unwritten
       const float4 x = __ldg(reinterpret_cast<const float4*>(a.o + (p * a.rows + row) * D) + at);
@@ -71,23 +79,32 @@ __global__ void __launch_bounds__(kMergeGroups * D / 4) merge_parts_kernel(const
       acc.w = fmaf(w, x.w, acc.w);
     }
   }
-  if (group > 0) sums[group - 1][at] = acc;
+  if (group > 0) sums[group - 1][tid % kLanes] = acc;
   __syncthreads();
   if (group > 0) return;
 #pragma unroll
-  for (int g = 0; g < kMergeGroups - 1; ++g) {
-    const float4 x = sums[g][at];
+  for (int g = 0; g < kGroups - 1; ++g) {
+    const float4 x = sums[g][tid];
     acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
   }
   reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D)[at] =
       make_uint2(pack16<BF16>(acc.x, acc.y), pack16<BF16>(acc.z, acc.w));
-  if (tid == 0) a.lse2[row] = lse;
+  if (at == 0) a.lse2[row] = lse;
 }
 
+template <int D, bool BF16, int kGroups>
+inline cudaError_t launch_merge_by(const MergeArgs& a, cudaStream_t stream) {
+  using Cut = MergeCut<D, kGroups>;
+  return launch_kernel(merge_parts_kernel<D, BF16, kGroups>, dim3((unsigned)(a.rows * Cut::kBlocks)),
+                       dim3(kGroups * Cut::kLanes), 0, stream, 0, a);
+}
 template <int D, bool BF16>
 inline cudaError_t launch_merge(const MergeArgs& a, cudaStream_t stream) {
-  return launch_kernel(merge_parts_kernel<D, BF16>, dim3((unsigned)a.rows), dim3(kMergeGroups * D / 4), 0,
-                       stream, 0, a);
+  // Many parts of few rows, 16 groups against four, whole calls in us: 16 rows of 128
+  // parts 24.6 / 27.1, 128 of 76 31.2 / 33.0; but 256 rows of 38 parts 31.2 / 29.5 and
+  // 5856 of three 231 / 181.
+  return a.parts > 16 && a.rows <= 152 ? launch_merge_by<D, BF16, 16>(a, stream)
+                                       : launch_merge_by<D, BF16, 4>(a, stream);
 }
 
 // Parts to split each of `items` (of about `item_us` microseconds) into, for `ctas`
