@@ -32,7 +32,7 @@
 // 360 us (219 GFLOP, 949 MB; scores of both halves and the 64-key tiles' products
 // take 2.2 us of the 4.7 a tile and half), a tree of eight 1450 us (1.05 PFLOP/s of
 // the work, 1.6 of what is issued: tensor pipes 68 % busy); one sequence of 32768,
-// one token, 29 us.
+// one token, 28 us.
 // The tail of a sequence's last page holds anything: its values are zeroed in
 // shared memory up to the 16 keys that a product step reads, its scores masked.
 // Every wait is bounded and raises DSA_FLAG_TIMEOUT when it runs out.
