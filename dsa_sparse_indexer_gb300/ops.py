@@ -566,9 +566,11 @@ def sparse_mla_decode_fp8(q, kv_cache, block_scales, slots, counts, scale: float
 
 # ---- whole contexts: expanded and absorbed attention; the indexer's operands --
 def _no_grad(*tensors):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError("no tensor may require grad: this call is not recorded by autograd "
-                         "(call it under torch.no_grad())")
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("no tensor may require grad: this call is not recorded by autograd "
+                                 "(call it under torch.no_grad())")
 
 
 def _changed(*outs):
@@ -620,8 +622,7 @@ def mla_prefill(q, k_nope, k_pe, v, cu_q, cu_k, scale: float, causal: bool = Tru
         raise ValueError("q must be [Tq, H, 192]")
     Tq, H, _ = q.shape
     Tk = k_pe.shape[0]
-    if tuple(k_nope.shape) != (Tk, H, MLA_DN) or tuple(v.shape) != (Tk, H, MLA_DVH) or \
-            tuple(k_pe.shape) != (Tk, MLA_DR):
+    if k_nope.shape != (Tk, H, MLA_DN) or v.shape != (Tk, H, MLA_DVH) or k_pe.shape != (Tk, MLA_DR):
         raise ValueError("k_nope and v must be [Tk, H, 128] and k_pe [Tk, 64]")
     n = cu_q.shape[0] - 1
     if n < 0 or cu_k.shape[0] != n + 1:
@@ -733,11 +734,11 @@ def indexer_key_insert(k, norm_weight, norm_bias, eps: float, positions, cos_sin
     _flags(err_flags)
     T = positions.shape[0]
     S, n_slots, dim = k_cache.shape
-    if tuple(k.shape) != (T, IDX_DIM) or dim != IDX_DIM:
+    if k.shape != (T, IDX_DIM) or dim != IDX_DIM:
         raise ValueError("k must be [T, 128], T positions, and k_cache [S, n_slots, 128]")
     if norm_weight.shape[0] != IDX_DIM or (norm_bias is not None and norm_bias.shape[0] != IDX_DIM):
         raise ValueError("norm_weight and norm_bias must have 128 entries")
-    if tuple(slot_mapping.shape) != (S, T):
+    if slot_mapping.shape != (S, T):
         raise ValueError("slot_mapping must be [S, T]")
     _no_grad(k, norm_weight, norm_bias, cos_sin_cache)
     context = _together(k, norm_weight, norm_bias, positions, cos_sin_cache, slot_mapping, k_cache,
@@ -768,7 +769,7 @@ def indexer_query_fp8(q, weights, positions, cos_sin_cache, factor: float = 1.0,
     if q.dim() != 3 or q.shape[2] != IDX_DIM:
         raise ValueError("q must be [T, H, 128]")
     T, H, _ = q.shape
-    if tuple(weights.shape) != (T, H) or positions.shape[0] != T:
+    if weights.shape != (T, H) or positions.shape[0] != T:
         raise ValueError("weights must be [T, H] and positions [T]")
     q_out, given = _output(q_out, "q_out", (T, H, IDX_DIM), torch.uint8, q.device)
     weights_out, given2 = _output(weights_out, "weights_out", (T, H), torch.float32, q.device)
