@@ -16,7 +16,8 @@
 // and sines once and uses them for all heads it takes.
 // Queries round as the exact values do: a scaled value within fp32's error of a
 // middle between two codes, or a largest one near a border between two scales, sends
-// its head once more through the arithmetic, with its errors.
+// its head once more through the arithmetic, with its errors.  Infinities saturate;
+// a value that turns past fp32's range is finite all the same.
 // Measured: 64 keys into 4 shards 4.3 us, 32768 keys 12.4 us and 131072 35.7 (86 MB,
 // 2.4 TB/s: the issue slots of norm, rotation and stores); the queries of 64 tokens,
 // 64 heads 6.3 us, of 4096 tokens 39 us (104 MB, 2.7 TB/s: the issue slots of
@@ -209,6 +210,8 @@ struct QueryArgs {
   float* w_out;                              // [T][H]
 };
 
+constexpr float kLargest = 3.4028235e38f;    // fp32's largest finite value
+
 // The exponent field of the smallest power of two s with amax <= 448 s (448 = 1.75 *
 // 2^8), from 2^-126 on, from amax's bits; s = 1 where amax is 0.
 __device__ __forceinline__ int scale_exponent(uint32_t amax) {
@@ -221,7 +224,8 @@ __device__ __forceinline__ float power(int exponent_field) { return __uint_as_fl
 // anything was cut, so that a further rounding sees on which side of a middle the
 // exact value lay.  The products' and the sum's errors are held in a second fp32
 // (Dekker's and Knuth's error-free transformations), 48 bits in all.  (In fp64 a
-// head took 5 us.)
+// head took 5 us.)  An infinite sum, of infinite values or past fp32's range, is itself
+// (its errors would be NaN).
 template <int P>
 __device__ __forceinline__ float turned_to_odd(const Turn<P>& t, int e, float x, float p) {
   const bool turns = P == kLaneOff ? t.any : t.s[e] != 0.f || t.c[e] != 1.f;
@@ -229,12 +233,13 @@ __device__ __forceinline__ float turned_to_odd(const Turn<P>& t, int e, float x,
   const float a = __fmul_rn(x, t.c[e]), b = __fmul_rn(p, t.s[e]);
   const float ea = __fmaf_rn(x, t.c[e], -a), eb = __fmaf_rn(p, t.s[e], -b);
   const float sum = __fadd_rn(a, b), part = __fsub_rn(sum, a);
+  if (!(fabsf(sum) <= kLargest)) return sum;
   const float es = __fadd_rn(__fsub_rn(a, __fsub_rn(sum, part)), __fsub_rn(b, part));
   const float low = __fadd_rn(es, __fadd_rn(ea, eb));
   float z = __fadd_rn(sum, low);
   const float rest = __fsub_rn(low, __fsub_rn(z, sum));
   const uint32_t bits = __float_as_uint(z);
-  if (rest != 0.f && z != 0.f && fabsf(z) <= 3.4028235e38f && !(bits & 1u))
+  if (rest != 0.f && z != 0.f && fabsf(z) <= kLargest && !(bits & 1u))
     z = __uint_as_float((rest > 0.f) == (z > 0.f) ? bits + 1u : bits - 1u);
   return z;
 }
@@ -285,21 +290,36 @@ __global__ void __launch_bounds__(kThreads, kHeads == 4 && P != kAnywhere ? 9 : 
     for (int e = 0; e < kVals; ++e) z[e] = y[e] * out;
     const uint2 outer = codes8(z);
     const uint32_t part = __float_as_uint(amax) & 0x7FFFFFu;   // next to 1.75, but not on it
-    const bool near = code.x != outer.x || code.y != outer.y || !(amax <= 3.4028235e38f) ||
+    const bool near = code.x != outer.x || code.y != outer.y || !(amax <= kLargest) ||
                       (part - 0x5FFFF8u <= 16u && part != 0x600000u);
     if (__any_sync(kFull, near)) {
       keep_branch();
-      float top = 0.f;
+      // Finite values may turn past fp32's range (by a factor of |cos| + |sin|): their
+      // heads go 2^16 smaller, in which their largest finite values lose nothing.
+      float pre = 1.f, top = 0.f;
+      bool past = false;
 #pragma unroll
       for (int e = 0; e < kVals; ++e) {
         z[e] = turned_to_odd<P>(t, e, x[e], p[e]);
-        if (fabsf(z[e]) <= 3.4028235e38f) top = fmaxf(top, fabsf(z[e]));
+        past |= !(fabsf(z[e]) <= kLargest) && fabsf(x[e]) <= kLargest && fabsf(p[e]) <= kLargest;
       }
+      const unsigned past_rows = __ballot_sync(kFull, past);
+      if (past_rows) {
+        keep_branch();
+        if (past_rows & (0xffffu << (threadIdx.x & kLanes))) pre = 0x1p-16f;
+#pragma unroll
+        for (int e = 0; e < kVals; ++e) z[e] = turned_to_odd<P>(t, e, x[e] * pre, p[e] * pre);
+      }
+      const float most = pre == 1.f ? kLargest : 448.f * 0x1p111f;   // what the largest s reaches, 448 * 2^127
+#pragma unroll
+      for (int e = 0; e < kVals; ++e)
+        if (fabsf(z[e]) <= most) top = fmaxf(top, fabsf(z[e]));
 #pragma unroll
       for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
       field = scale_exponent(__float_as_uint(top));
 #pragma unroll
       for (int e = 0; e < kVals; ++e) z[e] *= power(254 - field);
+      if (pre != 1.f) field += 16;
       code = codes8(z);
     }
     if (h < a.H) {
