@@ -14,10 +14,10 @@
 // (interleaved pairs at an even offset), in a lane a fixed way off (the half layout
 // at multiples of 8), or anywhere, through shared memory.  A thread finds its cosines
 // and sines once and uses them for all heads it takes.
-// Queries round as the exact values do: a scaled value within fp32's error of a
-// middle between two codes, or a largest one near a border between two scales, sends
-// its head once more through the arithmetic, with its errors.  Infinities saturate;
-// a value that turns past fp32's range is finite all the same.
+// Queries round as the exact values do: a scaled value within the arithmetic's error
+// of a middle between two codes, a largest one near a border between two scales, or a
+// head below 2^-60, sends its head once more through the arithmetic, with its errors.
+// Infinities saturate; a value that turns past fp32's range is finite all the same.
 // Measured: 64 keys into 4 shards 4.3 us, 32768 keys 12.4 us and 131072 35.7 (86 MB,
 // 2.4 TB/s: the issue slots of norm, rotation and stores); the queries of 64 tokens,
 // 64 heads 6.3 us, of 4096 tokens 39 us (104 MB, 2.7 TB/s: the issue slots of
@@ -138,6 +138,19 @@ __device__ __forceinline__ float turned(const Turn<P>& t, int e, float x, float 
   return turns ? y : x;
 }
 
+// The same without the first product's rounding: within 2^-23 of itself and 2^-48 of
+// the product of the exact value, however much of the products cancels (2^-24 of the
+// product alone may be any part of what they leave).  `y` is the value before, which
+// shows an infinity where this is NaN.
+template <int P>
+__device__ __forceinline__ float turned_close(const Turn<P>& t, int e, float x, float p, float& y) {
+  const bool turns = P == kLaneOff ? t.any : t.s[e] != 0.f || t.c[e] != 1.f;
+  const float b = __fmul_rn(p, t.s[e]);
+  const float v = __fmaf_rn(x, t.c[e], b);
+  y = turns ? v : x;
+  return turns ? __fsub_rn(v, __fmaf_rn(-p, t.s[e], b)) : x;
+}
+
 struct KeyArgs {
   const __nv_bfloat16* k;
   int64_t stride;
@@ -236,7 +249,7 @@ __device__ __forceinline__ float turned_to_odd(const Turn<P>& t, int e, float x,
   if (!(fabsf(sum) <= kLargest)) return sum;
   const float es = __fadd_rn(__fsub_rn(a, __fsub_rn(sum, part)), __fsub_rn(b, part));
   const float low = __fadd_rn(es, __fadd_rn(ea, eb));
-  float z = __fadd_rn(sum, low);
+  float z = low == 0.f ? sum : __fadd_rn(sum, low);   // (-0 stays)
   const float rest = __fsub_rn(low, __fsub_rn(z, sum));
   const uint32_t bits = __float_as_uint(z);
   if (rest != 0.f && z != 0.f && fabsf(z) <= kLargest && !(bits & 1u))
@@ -267,20 +280,24 @@ __global__ void __launch_bounds__(kThreads, kHeads == 4 && P != kAnywhere ? 9 : 
     float x[kVals], p[kVals], y[kVals];
     unpack8(raw[k], x);
     partners<P>(t, rows[P == kAnywhere ? r : 0], lane16, x, p);
-    float amax = 0.f;                        // (of what is no NaN)
+    float own = 0.f;                         // the lane's largest (of what is no NaN)
 #pragma unroll
     for (int e = 0; e < kVals; ++e) {
-      y[e] = turned<P>(t, e, x[e], p[e]);
-      amax = fmaxf(amax, fabsf(y[e]));
+      float v;
+      y[e] = turned_close<P>(t, e, x[e], p[e], v);
+      own = fmaxf(own, fabsf(v));
     }
+    float amax = own;
 #pragma unroll
     for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
     int field = scale_exponent(__float_as_uint(amax));
     const float inv = power(254 - field);    // 1 / s
-    // fp32's error may have moved a turned value across the middle between two codes
-    // if its codes a little further in and out differ (carried values are exact); and
-    // the largest across the border between two scales (on which bf16 values lie), if
-    // it is near.  Those heads, and infinite ones, go once more, exactly.
+    // The error may have moved a turned value across the middle between two codes if its
+    // codes 2^-21 of it further in and out differ (carried values are exact); and the
+    // lane's largest across the border between two scales if it is near: its error is 2.1
+    // units of its last place at most, as a product is no larger than the pair, and that
+    // no more than sqrt(2) times the head's largest.  Those heads, infinite ones, and
+    // those whose errors may be subnormal go once more, exactly.
     const float in = t.any ? inv * (1.f - 0x1p-21f) : inv, out = t.any ? inv * (1.f + 0x1p-21f) : inv;
     float z[kVals];
 #pragma unroll
@@ -289,37 +306,41 @@ __global__ void __launch_bounds__(kThreads, kHeads == 4 && P != kAnywhere ? 9 : 
 #pragma unroll
     for (int e = 0; e < kVals; ++e) z[e] = y[e] * out;
     const uint2 outer = codes8(z);
-    const uint32_t part = __float_as_uint(amax) & 0x7FFFFFu;   // next to 1.75, but not on it
+    const uint32_t border = (__float_as_uint(amax) & 0x7F800000u) | 0x600000u;
     const bool near = code.x != outer.x || code.y != outer.y || !(amax <= kLargest) ||
-                      (part - 0x5FFFF8u <= 16u && part != 0x600000u);
+                      (t.any && (__float_as_uint(own) - (border - 8u) <= 16u || (amax < 0x1p-60f && amax > 0.f)));
     if (__any_sync(kFull, near)) {
       keep_branch();
-      // Finite values may turn past fp32's range (by a factor of |cos| + |sin|): their
-      // heads go 2^16 smaller, in which their largest finite values lose nothing.
-      float pre = 1.f, top = 0.f;
-      bool past = false;
+      // Finite values may turn past fp32's range (by a factor of |cos| + |sin|; where these
+      // are below 64, to values that a scale reaches), and errors below it: such heads go
+      // once more 2^16 smaller, where their largest values lose nothing, or 2^64 larger.
+      float top;
+      int down = 0;                          // by 2^down smaller
+#pragma unroll 1
+      for (int trip = 0;; ++trip) {
+        const float pre = power(127 - down);
+        const float most = down > 0 ? 448.f * 0x1p111f : kLargest;   // what the largest s reaches, 448 * 2^127
+        bool past = false;
+        top = 0.f;
 #pragma unroll
-      for (int e = 0; e < kVals; ++e) {
-        z[e] = turned_to_odd<P>(t, e, x[e], p[e]);
-        past |= !(fabsf(z[e]) <= kLargest) && fabsf(x[e]) <= kLargest && fabsf(p[e]) <= kLargest;
+        for (int e = 0; e < kVals; ++e) {
+          // (An infinite value stays: larger, the finite one beside it may be so too.)
+          if (trip == 0 || down >= 0 || fabsf(z[e]) <= kLargest)
+            z[e] = turned_to_odd<P>(t, e, x[e] * pre, p[e] * pre);
+          past |= !(fabsf(z[e]) <= kLargest) && fabsf(x[e]) <= kLargest && fabsf(p[e]) <= kLargest &&
+                  fabsf(t.c[e]) <= 64.f && fabsf(t.s[e]) <= 64.f;
+          if (fabsf(z[e]) <= most) top = fmaxf(top, fabsf(z[e]));
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        if (trip > 0) break;
+        const unsigned past_rows = __ballot_sync(kFull, past);
+        down = past_rows & (0xffffu << (threadIdx.x & kLanes)) ? 16 : top < 0x1p-60f ? -64 : 0;
+        if (!__any_sync(kFull, down != 0)) break;
       }
-      const unsigned past_rows = __ballot_sync(kFull, past);
-      if (past_rows) {
-        keep_branch();
-        if (past_rows & (0xffffu << (threadIdx.x & kLanes))) pre = 0x1p-16f;
+      field = top == 0.f ? 127 : max(scale_exponent(__float_as_uint(top)) + down, 1);
 #pragma unroll
-        for (int e = 0; e < kVals; ++e) z[e] = turned_to_odd<P>(t, e, x[e] * pre, p[e] * pre);
-      }
-      const float most = pre == 1.f ? kLargest : 448.f * 0x1p111f;   // what the largest s reaches, 448 * 2^127
-#pragma unroll
-      for (int e = 0; e < kVals; ++e)
-        if (fabsf(z[e]) <= most) top = fmaxf(top, fabsf(z[e]));
-#pragma unroll
-      for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-      field = scale_exponent(__float_as_uint(top));
-#pragma unroll
-      for (int e = 0; e < kVals; ++e) z[e] *= power(254 - field);
-      if (pre != 1.f) field += 16;
+      for (int e = 0; e < kVals; ++e) z[e] *= power(254 - field + down);
       code = codes8(z);
     }
     if (h < a.H) {

@@ -699,10 +699,10 @@ dsa_status dsa_indexer_key_insert(const uint16_t* k, int64_t k_token, const floa
  * with a scale of its own that goes into the head's weight (a logit is a weighted
  * sum of max(0, q . k), so that a positive factor of q may move there):
  *   s = the smallest power of two >= 2^-126 with max |y| <= 448 s over the head's
- *       finite values (1 where all are 0; values past 448 * 2^127, which no s
- *       reaches, count as infinite),
- *   q_out = e4m3(y / s) (to nearest even; infinities saturate), weights_out =
- *   weights * factor * s.
+ *       finite values (1 where all are 0; a value past fp32's range is finite where
+ *       the table's entries are at most 64 in size, else it counts as infinite),
+ *   q_out = e4m3(y / s) (the exact value's rounding, to nearest even; infinities
+ *   saturate), weights_out = weights * factor * s.
  *
  *   q            [T][H][DSA_IDX_DIM] bf16, token and head strides in elements,
  *                multiples of 8; 16-byte aligned
