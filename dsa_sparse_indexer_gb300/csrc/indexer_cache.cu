@@ -20,7 +20,7 @@
 // Infinities saturate; a value that turns past fp32's range is finite all the same.
 // Measured: 64 keys into 4 shards 4.3 us, 32768 keys 12.4 us and 131072 35.7 (86 MB,
 // 2.4 TB/s: the issue slots of norm, rotation and stores); the queries of 64 tokens,
-// 64 heads 6.3 us, of 4096 tokens 39 us (104 MB, 2.7 TB/s: the issue slots of
+// 64 heads 6.3 us, of 4096 tokens 40 us (104 MB, 2.6 TB/s: the issue slots of
 // rotation, scale and rounding).  Two or four keys a thread, its weights read once:
 // 32768 keys 10.7 and 13.3 us where one takes 10.0, back to back.
 #include <cuda_bf16.h>
@@ -100,9 +100,6 @@ __device__ __forceinline__ uint2 codes8(const float (&y)[kVals]) {
   return make_uint2(e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16),
                     e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
 }
-
-// In a branch rarely taken: keeps it one.
-__device__ __forceinline__ void keep_branch() { asm volatile("" ::: "memory"); }
 
 // Sum over the 16 lanes of a row.
 __device__ __forceinline__ float sum16(float v) {
@@ -258,8 +255,7 @@ __device__ __forceinline__ float turned_to_odd(const Turn<P>& t, int e, float x,
 }
 
 // Nine blocks an SM (56 registers) hide more of a row's latency than the seven that
-// 72 registers leave: 4096 tokens of 64 heads 39.1 us against 43.7; ten 42.9.  (Some
-// of the half layout's spill, at the second pass.)
+// 72 registers leave: 4096 tokens of 64 heads 39.1 us against 43.7; ten 42.9.
 template <int P, int kHeads>
 __global__ void __launch_bounds__(kThreads, kHeads == 4 && P != kAnywhere ? 9 : 1) indexer_query_kernel(const QueryArgs a) {
   __shared__ __align__(16) float rows[P == kAnywhere ? kRows : 1][kDim];
@@ -274,6 +270,12 @@ __global__ void __launch_bounds__(kThreads, kHeads == 4 && P != kAnywhere ? 9 : 
                      : make_uint4(0, 0, 0, 0);
   }
   const Turn<P> t = find_turn<P>(a.turn, token, lane16);
+  auto store = [&](int h, uint2 code, int field) {
+    const int64_t row = (int64_t)token * a.H + h;
+    *reinterpret_cast<uint2*>(a.q_out + row * kDim + lane16 * kVals) = code;
+    if (lane16 == 0) a.w_out[row] = a.weights[row] * a.factor * power(field);
+  };
+  uint32_t again = 0;                        // bit k: the warp's k-th two heads go once more
 #pragma unroll
   for (int k = 0; k < kHeads; ++k) {
     const int h = h0 + k * kRows;
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, kHeads == 4 && P != kAnywhere ? 9 : 
     float amax = own;
 #pragma unroll
     for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-    int field = scale_exponent(__float_as_uint(amax));
+    const int field = scale_exponent(__float_as_uint(amax));
     const float inv = power(254 - field);    // 1 / s
     // The error may have moved a turned value across the middle between two codes if its
     // codes 2^-21 of it further in and out differ (carried values are exact); and the
@@ -302,52 +304,56 @@ __global__ void __launch_bounds__(kThreads, kHeads == 4 && P != kAnywhere ? 9 : 
     float z[kVals];
 #pragma unroll
     for (int e = 0; e < kVals; ++e) z[e] = y[e] * in;
-    uint2 code = codes8(z);
+    const uint2 code = codes8(z);
 #pragma unroll
     for (int e = 0; e < kVals; ++e) z[e] = y[e] * out;
     const uint2 outer = codes8(z);
     const uint32_t border = (__float_as_uint(amax) & 0x7F800000u) | 0x600000u;
     const bool near = code.x != outer.x || code.y != outer.y || !(amax <= kLargest) ||
                       (t.any && (__float_as_uint(own) - (border - 8u) <= 16u || (amax < 0x1p-60f && amax > 0.f)));
-    if (__any_sync(kFull, near)) {
-      keep_branch();
-      // Finite values may turn past fp32's range (by a factor of |cos| + |sin|; where these
-      // are below 64, to values that a scale reaches), and errors below it: such heads go
-      // once more 2^16 smaller, where their largest values lose nothing, or 2^64 larger.
-      float top;
-      int down = 0;                          // by 2^down smaller
+    if (__any_sync(kFull, near)) again |= 1u << k;
+    else if (h < a.H) store(h, code, field);
+  }
+  // Behind the others, read again: inlined above, the second pass's registers cost every
+  // head (4096 tokens of 64 heads 43.7 us against 40.0).
 #pragma unroll 1
-      for (int trip = 0;; ++trip) {
-        const float pre = power(127 - down);
-        const float most = down > 0 ? 448.f * 0x1p111f : kLargest;   // what the largest s reaches, 448 * 2^127
-        bool past = false;
-        top = 0.f;
+  for (; again; again &= again - 1) {
+    const int h = h0 + (__ffs(again) - 1) * kRows;
+    float x[kVals], p[kVals], z[kVals];
+    unpack8(h < a.H ? __ldg(reinterpret_cast<const uint4*>(a.q + token * a.token + h * a.head) + lane16)
+                    : make_uint4(0, 0, 0, 0), x);
+    partners<P>(t, rows[P == kAnywhere ? r : 0], lane16, x, p);
+    // Finite values may turn past fp32's range (by a factor of |cos| + |sin|; where these
+    // are below 64, to values that a scale reaches), and errors below it: such heads go
+    // once more 2^16 smaller, where their largest values lose nothing, or 2^64 larger.
+    float top;
+    int down = 0;                            // by 2^down smaller
+#pragma unroll 1
+    for (int trip = 0;; ++trip) {
+      const float pre = power(127 - down);
+      const float most = down > 0 ? 448.f * 0x1p111f : kLargest;   // what the largest s reaches, 448 * 2^127
+      bool past = false;
+      top = 0.f;
 #pragma unroll
-        for (int e = 0; e < kVals; ++e) {
-          // (An infinite value stays: larger, the finite one beside it may be so too.)
-          if (trip == 0 || down >= 0 || fabsf(z[e]) <= kLargest)
-            z[e] = turned_to_odd<P>(t, e, x[e] * pre, p[e] * pre);
-          past |= !(fabsf(z[e]) <= kLargest) && fabsf(x[e]) <= kLargest && fabsf(p[e]) <= kLargest &&
-                  fabsf(t.c[e]) <= 64.f && fabsf(t.s[e]) <= 64.f;
-          if (fabsf(z[e]) <= most) top = fmaxf(top, fabsf(z[e]));
-        }
-#pragma unroll
-        for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-        if (trip > 0) break;
-        const unsigned past_rows = __ballot_sync(kFull, past);
-        down = past_rows & (0xffffu << (threadIdx.x & kLanes)) ? 16 : top < 0x1p-60f ? -64 : 0;
-        if (!__any_sync(kFull, down != 0)) break;
+      for (int e = 0; e < kVals; ++e) {
+        // (An infinite value stays: larger, the finite one beside it may be so too.)
+        if (trip == 0 || down >= 0 || fabsf(z[e]) <= kLargest)
+          z[e] = turned_to_odd<P>(t, e, x[e] * pre, p[e] * pre);
+        past |= !(fabsf(z[e]) <= kLargest) && fabsf(x[e]) <= kLargest && fabsf(p[e]) <= kLargest &&
+                fabsf(t.c[e]) <= 64.f && fabsf(t.s[e]) <= 64.f;
+        if (fabsf(z[e]) <= most) top = fmaxf(top, fabsf(z[e]));
       }
-      field = top == 0.f ? 127 : max(scale_exponent(__float_as_uint(top)) + down, 1);
 #pragma unroll
-      for (int e = 0; e < kVals; ++e) z[e] *= power(254 - field + down);
-      code = codes8(z);
+      for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      if (trip > 0) break;
+      const unsigned past_rows = __ballot_sync(kFull, past);
+      down = past_rows & (0xffffu << (threadIdx.x & kLanes)) ? 16 : top < 0x1p-60f ? -64 : 0;
+      if (!__any_sync(kFull, down != 0)) break;
     }
-    if (h < a.H) {
-      const int64_t row = (int64_t)token * a.H + h;
-      *reinterpret_cast<uint2*>(a.q_out + row * kDim + lane16 * kVals) = code;
-      if (lane16 == 0) a.w_out[row] = a.weights[row] * a.factor * power(field);
-    }
+    const int field = top == 0.f ? 127 : max(scale_exponent(__float_as_uint(top)) + down, 1);
+#pragma unroll
+    for (int e = 0; e < kVals; ++e) z[e] *= power(254 - field + down);
+    if (h < a.H) store(h, codes8(z), field);
   }
 }
 
