@@ -50,6 +50,7 @@ constexpr int kBlocks = kDqk / 64;           // 9 blocks of 64 values
 constexpr int kVBlocks = 4, kABlocks = kBlocks - kVBlocks;   // of a half's values; the others
 constexpr int kQBox = 32;                    // rows of a copy of queries
 constexpr int kInfo = 8;
+constexpr int kCut = 8;                      // bit of a tile's first piece of 16 keys that is there in part
 // Warps: 8 of the softmax (sub * 4 + quad: rows quad * 32 + sub * 16 to + 15), one
 // issuing products, one copying, one claiming.
 constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kClaimWarp = 10, kThreads = 352;
@@ -112,7 +113,7 @@ struct alignas(1024) DecodeSmem {
       info[kInfo], drain;
   uint32_t tail_seq[2];       // Pair: place in the ring of the values that vtail counts
   Order order;
-  uint32_t pages[kInfo];      // valid pages of stream tile j, at j % kInfo: a bit per 16 keys
+  uint32_t pages[kInfo];      // pages of stream tile j, at j % kInfo: cache_row's bits, one per 16 keys
   uint32_t tmem;
   int blocks;                 // row blocks of all requests
   int abort;
@@ -255,22 +256,25 @@ __device__ __forceinline__ int table_entry(const DecodeArgs& a, const Item& it, 
                fdiv((uint32_t)key, a.fblock));
 }
 // That row, which may be `n_slots` (outside: reads as zero) where there is none;
-// `valid` gets a bit a piece that there is.
+// `valid` gets a bit a piece that there is, and at kCut one a piece that the cache's
+// end cuts: pieces start at multiples of 16, so that n_slots % 16 slots are left of it.
 template <int M>
 __device__ __forceinline__ int cache_row(const DecodeArgs& a, const Item& it, int t, int entry, uint32_t& valid,
                                          bool& bad) {
   const int key = t * Cut<M>::kTile + (int)(threadIdx.x % Cut<M>::kPieces) * 16;
   int y = (int)a.n_slots;
-  bool in = false;
+  bool in = false, cut = false;
   if (key < it.nall) {
     uint32_t off;
     fdivmod((uint32_t)key, a.fblock, &off);
     const int64_t at = (int64_t)entry * a.block + off;
     in = at >= 0 && at + 16 <= a.n_slots;
-    if (in) y = (int)at;
-    bad |= !in;
+    cut = at >= 0 && !in && at < a.n_slots;
+    if (in || cut) y = (int)at;
+    bad |= at < 0 || at + min(16, it.nall - key) > a.n_slots;
   }
-  valid = __ballot_sync(kFull, in) & ((1u << Cut<M>::kPieces) - 1u);
+  constexpr unsigned kAll = (1u << Cut<M>::kPieces) - 1u;
+  valid = (__ballot_sync(kFull, in) & kAll) | (__ballot_sync(kFull, cut) & kAll) << kCut;
   return y;
 }
 
@@ -576,6 +580,10 @@ __device__ __forceinline__ void issue_products(const DecodeArgs& a, DecodeSmem<M
 __device__ __forceinline__ uint32_t first_bits(int n) {
   return n >= 32 ? kFull : n <= 0 ? 0u : (1u << n) - 1u;
 }
+// Of a tile's 16 keys `piece`, those that the cache holds.
+__device__ __forceinline__ uint32_t piece_bits(const DecodeArgs& a, uint32_t pages, int piece) {
+  return (pages >> piece) & 1u ? 0xffffu : (pages >> (kCut + piece)) & 1u ? first_bits((int)a.n_slots & 15) : 0u;
+}
 __device__ __forceinline__ uint32_t seen32(const DecodeArgs& a, const Item& it, int tok, int from) {
   if (!a.mask) {
     const int own = (int)a.sm.local_len((uint32_t)max(it.base + tok + 1, 0), it.shard);
@@ -666,12 +674,11 @@ __device__ __forceinline__ void softmax_tiles(const DecodeArgs& a, DecodeSmem<M>
         if (masked) {
           keep_branch();
           const int c = lane & (Sh::kTile / 32 - 1);
-          const uint32_t pg = (pages >> (2 * c)) & 3u;
+          const uint32_t there = piece_bits(a, pages, 2 * c) | piece_bits(a, pages, 2 * c + 1) << 16;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int row = it.row0 + min(br + 8 * k, it.rows - 1);
-            seen[k] = seen32(a, it, (int)fdiv((uint32_t)row, a.fH), t * Sh::kTile + c * 32) &
-                      ((pg & 1u ? 0xffffu : 0u) | (pg & 2u ? 0xffff0000u : 0u));
+            seen[k] = seen32(a, it, (int)fdiv((uint32_t)row, a.fH), t * Sh::kTile + c * 32) & there;
           }
         }
         auto mask = [&](uint32_t (&x)[16], int c) {
@@ -1142,7 +1149,7 @@ __device__ __forceinline__ void narrow_softmax(const DecodeArgs& a, NarrowSmem<M
       if (pages != 0xffu || (t + 1) * kTile > nfree) {
         keep_branch();
         const int local = t * kTile + key;
-        const bool there = ((pages >> (key >> 4)) & 1u) && local < nall;
+        const bool there = ((piece_bits(a, pages, key >> 4) >> (key & 15)) & 1u) && local < nall;
         const int own = !there || local < nfree ? -1 : (int)a.sm.global_id(it.shard, (uint32_t)local) - it.base;
         if (__any_sync(kFull, own >= 0)) {
           keep_branch();

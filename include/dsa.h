@@ -638,9 +638,9 @@ int64_t dsa_mla_prefill_work(int Tq, int Tk, int n, int H);
  *                Calls that may run at the same time need their own.
  *   err_flags    DSA_FLAG_BOUNDS if query_starts is not ascending within the rows
  *                (entries taken as the nearest that is), a length is negative
- *                or past the table (cut) or an entry points outside the cache
- *                (its tokens are left out); DSA_FLAG_TIMEOUT if a bounded wait
- *                ran out (outputs incomplete).
+ *                or past the table (cut) or a token's slot is outside the cache
+ *                (it is left out; n_slots need be no multiple of block_size);
+ *                DSA_FLAG_TIMEOUT if a bounded wait ran out (outputs incomplete).
  * Scores and sums are fp32; a softmax weight enters the value product as bf16.
  * Cache rows of a request's own tokens are to be finite (a weight of 0 times an
  * infinity is NaN); slots behind its last token may hold anything.
