@@ -175,7 +175,13 @@ __device__ __forceinline__ bool wait_or_abort(const int* abort, uint64_t* bar, u
   }
   return false;
 }
-// The same for a converged warp, all lanes alike.  All of them poll: a branch for
+// The same for what lands before a CTA may end: it waits on when others have aborted.
+__device__ __forceinline__ bool wait_landed(uint64_t* bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kWaitPolls / 4; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+// wait_or_abort for a converged warp, all lanes alike.  All of them poll: a branch for
 // one lane costs every wait its divergence (8192 queries of 128 heads, expanded:
 // 2992 us with one polling lane, 2180 so).
 __device__ __forceinline__ bool warp_wait(const int* abort, uint64_t* bar, uint32_t parity) {
@@ -293,7 +299,13 @@ __device__ __forceinline__ void share_out(WorkSlots<Item>& s, int* abort, uint32
           }
         }
       }
-      ok = __all_sync(kFull, ok) && warp_wait(abort, &s.answer, claims & 1u);
+      const bool asked = __shfl_sync(kFull, (int)ok, 0) != 0;
+      ok = asked && warp_wait(abort, &s.answer, claims & 1u);
+      // An answer under way is not left to land in memory of the CTA that comes next.  (A
+      // pair's second CTA does not know whether the first has asked: at worst it waits
+      // until the bound.)
+      if (!ok && asked) wait_landed(&s.answer, claims & 1u);
+      __syncwarp();
       ++claims;
       uint32_t x = 0, yes = 0;
       if (ok)
