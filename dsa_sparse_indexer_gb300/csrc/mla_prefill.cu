@@ -682,7 +682,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) pair_sync();        // neither CTA's memory goes while the other uses it
+  if constexpr (CG == 2) {
+    // The products' arrivals come to both CTAs: the second sees the last of them too.
+    for (int g = 0; rank == 1 && warp == kMmaWarp && g < 2; ++g)
+      if (!wait_landed(&sm.drain[g], 0)) raise_flag(a.flags, DSA_FLAG_TIMEOUT);
+    __syncwarp();
+    pair_sync();                             // neither CTA's memory goes while the other uses it
+  }
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_free<CG>(tmem, kTmemCols);
