@@ -1410,7 +1410,7 @@ Plan plan_for(int rows, int S, int H, int reqs, int64_t cap) {
   const int64_t items = (pairs + p.item_rows - 1) / p.item_rows * reqs * p.halves * S;
   // 128 keys take a pair about 2.9 us (a half), a CTA alone 3.2 to 4.7; a part has as
   // many at least.
-  const int64_t tiles = (cap + 127) / 128, ctas = device_sms() / (p.mode == kPair ? 2 : 1);
+  const int64_t tiles = (cap + 127) / 128, ctas = kSms / (p.mode == kPair ? 2 : 1);
   p.splits = choose_parts(items, ctas, tiles * (p.mode == kPair ? 2.9 : 3.4) + 4.0, (int64_t)rows * S * H, kDv,
                           tiles);
   p.ordered = order_pays(reqs, items * p.splits, ctas);

@@ -711,8 +711,8 @@ Plan plan_for(int Tq, int Tk, int n, int H) {
   const int64_t items = std::max<int64_t>(((int64_t)Tq + block - 1) / block, n) * H;
   // A key tile takes an item about 1.9 us; a part has four at least.
   const int64_t tiles = (Tk / n + kTileK - 1) / kTileK;
-  p.splits = choose_parts(items, device_sms() / p.cg, tiles * 1.9 + 5.0, (int64_t)Tq * H, kDv, tiles / 4);
-  p.ordered = order_pays(n, items * p.splits, device_sms() / p.cg);
+  p.splits = choose_parts(items, kSms / p.cg, tiles * 1.9 + 5.0, (int64_t)Tq * H, kDv, tiles / 4);
+  p.ordered = order_pays(n, items * p.splits, kSms / p.cg);
   return p;
 }
 

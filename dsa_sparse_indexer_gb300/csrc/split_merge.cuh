@@ -103,7 +103,7 @@ inline cudaError_t launch_merge(const MergeArgs& a, cudaStream_t stream) {
   // Many parts of few rows, 16 groups against four, whole calls in us: 16 rows of 128
   // parts 24.6 / 27.1, 128 of 76 31.2 / 33.0; but 256 rows of 38 parts 31.2 / 29.5 and
   // 5856 of three 231 / 181.
-  return a.parts > 16 && a.rows <= 152 ? launch_merge_by<D, BF16, 16>(a, stream)
+  return a.parts > 16 && a.rows <= kSms ? launch_merge_by<D, BF16, 16>(a, stream)
                                        : launch_merge_by<D, BF16, 4>(a, stream);
 }
 

@@ -17,6 +17,9 @@
 namespace dsa {
 
 constexpr float kLog2e = 1.4426950408889634f;
+// SMs of a GB300, for which calls are cut.  (A constant: the size of a workspace and the
+// launch that uses it go by the same number, whatever device is current at either.)
+constexpr int kSms = 152;
 // A softmax's reference moves when a tile's maximum exceeds it by this much in
 // binades: weights stay below 2^8, and accumulators are rescaled rarely.
 constexpr float kRescaleGap = 8.f;
@@ -543,20 +546,6 @@ inline bool encode_map16(CUtensorMap* map, const void* base, bool bf16, uint64_t
             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// SMs of the current device (looked up once a device; 152 where that fails).
-inline int device_sms() {
-  constexpr int kDevices = 64;
-  static int sms[kDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 152;
-  if (sms[dev] == 0) {
-    int n = 0;
-    sms[dev] = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0
-                   ? n : 152;
-  }
-  return sms[dev];
 }
 
 }  // namespace dsa

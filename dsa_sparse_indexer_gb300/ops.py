@@ -589,9 +589,8 @@ def _output(out, name: str, shape, dtype, device):
 
 
 @functools.lru_cache(maxsize=4096)
-def _mla_prefill_work(device: int, Tq: int, Tk: int, n: int, H: int) -> int:
-    with torch.cuda.device(device):
-        return _lib.load().dsa_mla_prefill_work(Tq, Tk, n, H) // 4
+def _mla_prefill_work(Tq: int, Tk: int, n: int, H: int) -> int:
+    return _lib.load().dsa_mla_prefill_work(Tq, Tk, n, H) // 4
 
 
 def mla_prefill(q, k_nope, k_pe, v, cu_q, cu_k, scale: float, causal: bool = True, out=None,
@@ -630,7 +629,7 @@ def mla_prefill(q, k_nope, k_pe, v, cu_q, cu_k, scale: float, causal: bool = Tru
     out, given = _output(out, "out", (Tq, H, MLA_DVH), dtype, q.device)
     lse2, given2 = _output(lse2, "lse2", (Tq, H), torch.float32, q.device)
     _no_grad(q, k_nope, k_pe, v, out, lse2)
-    need = _mla_prefill_work(q.get_device(), Tq, Tk, n, H)
+    need = _mla_prefill_work(Tq, Tk, n, H)
     if work is None and need:
         work = torch.empty(need, dtype=torch.float32, device=q.device)
     if work is not None:
@@ -648,9 +647,8 @@ def mla_prefill(q, k_nope, k_pe, v, cu_q, cu_k, scale: float, causal: bool = Tru
 
 
 @functools.lru_cache(maxsize=4096)
-def _mla_decode_work(device: int, *sizes: int) -> int:
-    with torch.cuda.device(device):
-        return _lib.load().dsa_mla_decode_work(*sizes) // 4
+def _mla_decode_work(*sizes: int) -> int:
+    return _lib.load().dsa_mla_decode_work(*sizes) // 4
 
 
 def mla_decode(q, kv_cache, block_table, block_size: int, query_starts, seq_lens, I: int,
@@ -692,7 +690,7 @@ def mla_decode(q, kv_cache, block_table, block_size: int, query_starts, seq_lens
     out, given = _output(out, "out", (S, rows, H, MLA_DV), torch.bfloat16, q.device)
     lse2, given2 = _output(lse2, "lse2", (S, rows, H), torch.float32, q.device)
     _no_grad(q, kv_cache, out, lse2)
-    need = _mla_decode_work(q.get_device(), rows, S, H, reqs, max_blocks, block_size)
+    need = _mla_decode_work(rows, S, H, reqs, max_blocks, block_size)
     if work is None and need:
         work = torch.empty(need, dtype=torch.float32, device=q.device)
     if work is not None:
