@@ -22,8 +22,9 @@
 //    run its softmax: maximum, weights relative to a reference that moves when
 //    exceeded by 2^8, their sum, the outputs.
 // The weights' sum is of the fp32 weights; a weight enters the value product
-// rounded to 16 bits (2^-8 of itself at most in bf16, 2^-11 in fp16), the
-// reference's own weight is 1 and exact.
+// rounded to 16 bits: by 2^-8 of itself at most in bf16; in fp16, whose weights are
+// 2^7 larger so that few are subnormal, by 2^-11 of itself or 2^-32 of the
+// reference's weight.  That is 1 or 2^7, and exact.
 // Every wait is bounded and raises DSA_FLAG_TIMEOUT when it runs out.
 // Measured, one sequence of 8192, 128 heads, causal: 1720 us, 1.60 PFLOP/s of the
 // 1.96 that a library product reaches; 3753 with one CTA an item, a warp issuing
@@ -400,6 +401,10 @@ __device__ __forceinline__ void issue_products(const PrefillArgs& a, PrefillSmem
 // memory's fragments): twice the warps of a thread a row, so that the chain scores -
 // weights - value product, which a tile waits for, is half as long, and a row's
 // maximum still needs no more than shuffles.
+// In binades: weights go up to kRescaleGap above the reference's (fp16: 2^15 of 65504).
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 7.f;
+
 template <int CG, bool BF16>
 __device__ __forceinline__ void softmax_tiles(const PrefillArgs& a, PrefillSmem& sm, uint32_t tmem,
                                               int warp, uint32_t rank) {
@@ -436,7 +441,7 @@ __device__ __forceinline__ void softmax_tiles(const PrefillArgs& a, PrefillSmem&
     const Item& it = sm.work.item[n & 1u];
     const int end = uni(end_of(it, g)), t0 = uni(it.t0), lk = uni(it.lk);
     const int seen = a.causal ? it.shift + br + 1 : lk;   // by the first row (causal: 8 more by the second)
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // references (less the lift), sums
     for (int t = end - 1; t >= t0; --t, ++ns) {
       ok = warp_wait(&sm.abort, &sm.sfull[g], ns & 1u);
       if (!ok) break;
@@ -488,7 +493,8 @@ __device__ __forceinline__ void softmax_tiles(const PrefillArgs& a, PrefillSmem&
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const float mx = row_max(top[k]) * a.c2;
-        const float mn = mx > m[k] + kRescaleGap ? mx : m[k];   // m = -inf takes any finite maximum
+        // m = -inf takes any finite maximum.
+        const float mn = mx > m[k] + (kRescaleGap + kLift<BF16>) ? mx - kLift<BF16> : m[k];
         alpha[k] = m[k] == -INFINITY ? 1.f : fast_exp2(m[k] - mn);
         const float ref = mn == -INFINITY ? 0.f : mn;
         nref[k] = make_float2(-ref, -ref);

@@ -593,9 +593,10 @@ int64_t dsa_sparse_mla_decode_fp8_work(int rows, int S, int H, int K);
  *              below the one before it (taken as the nearest that is not);
  *              DSA_FLAG_TIMEOUT if a bounded wait ran out (outputs incomplete).
  * Scores and sums are fp32; a softmax weight enters the value product rounded to
- * dtype, relative to a maximum of its row within 2^8.  Keys that a query does not
- * see may hold anything; values of a sequence's own keys are to be finite (a
- * weight of 0 times an infinity is NaN), what lies outside it may be anything.
+ * dtype (in fp16 to 2^-11 of itself or 2^-32 of the row's largest, whichever is
+ * more).  Keys that a query does not see may hold anything; values of a sequence's
+ * own keys are to be finite (a weight of 0 times an infinity is NaN), what lies
+ * outside it may be anything.
  * Enqueues two kernels when the keys are split, else one.
  * Errors: negative sizes, H < 1, scale not finite, another dtype, null pointers,
  *         misalignment, strides -> INVALID_ARG; more than 2^26 blocks of 256
