@@ -116,6 +116,7 @@ struct alignas(1024) DecodeSmem {
   uint32_t pages[kInfo];      // pages of stream tile j, at j % kInfo: cache_row's bits, one per 16 keys
   uint32_t tmem;
   int blocks;                 // row blocks of all requests
+  int bad;                    // query_starts is not ascending inside the rows
   int abort;
 };
 static_assert(sizeof(DecodeSmem<kWide>) + 1024 <= 232448 && sizeof(DecodeSmem<kPair>) + 1024 <= 232448,
@@ -148,16 +149,11 @@ struct Cursor {
   int req = 0, before = 0;    // the request's place in the order, row blocks before it
 };
 
-__device__ __forceinline__ void rows_of(const DecodeArgs& a, int i, int& first, int& end) {
-  first = min(max(__ldg(a.starts + i), 0), a.rows);
-  end = min(max(__ldg(a.starts + i + 1), first), a.rows);
-}
-
 // Warp-wide: item `index` of blocks * halves * S * splits: halves and row blocks of a
 // request, which read the same keys, beside one another.
 template <int M>
-__device__ __forceinline__ Item find_item(const DecodeArgs& a, const Order& order, int blocks, int64_t index,
-                                          Cursor& c) {
+__device__ __forceinline__ Item find_item(const DecodeArgs& a, const Order& order, int blocks, bool bad,
+                                          int64_t index, Cursor& c) {
   constexpr int kItemRows = Cut<M>::kItemRows;
   const int lane = threadIdx.x & 31;
   Item it;
@@ -171,7 +167,7 @@ __device__ __forceinline__ Item find_item(const DecodeArgs& a, const Order& orde
   for (int at = c.req;; at += 32) {
     const int i = at + lane;
     int first = 0, end = 0;
-    if (i < a.reqs) rows_of(a, in_order(order, a.ordered, i), first, end);
+    if (i < a.reqs) bounds_of(a.starts, in_order(order, a.ordered, i), a.rows, bad, first, end);
     const int mine = ((end - first) * a.H + kItemRows - 1) / kItemRows;
     int incl = mine;
 #pragma unroll
@@ -192,7 +188,7 @@ __device__ __forceinline__ Item find_item(const DecodeArgs& a, const Order& orde
   }
   it.req = in_order(order, a.ordered, c.req);
   int end;
-  rows_of(a, it.req, it.tok0, end);
+  bounds_of(a.starts, it.req, a.rows, bad, it.tok0, end);
   it.n = end - it.tok0;
   it.row0 = local * kItemRows;
   it.rows = min(kItemRows, it.n * a.H - it.row0);
@@ -210,22 +206,6 @@ __device__ __forceinline__ Item find_item(const DecodeArgs& a, const Order& orde
   it.t0 = min(it.split * per, nt);
   it.t1 = min(it.t0 + per, nt);
   return it;
-}
-
-// Warp-wide: row blocks of all requests; bad bounds are flagged once a call.
-template <int M>
-__device__ __forceinline__ int count_blocks(const DecodeArgs& a) {
-  constexpr int kItemRows = Cut<M>::kItemRows;
-  int blocks = 0;
-  bool bad = false;
-  for (int i = threadIdx.x & 31; i < a.reqs; i += 32) {
-    int first, end;
-    rows_of(a, i, first, end);
-    bad |= first != a.starts[i] || end != a.starts[i + 1];
-    blocks += ((end - first) * a.H + kItemRows - 1) / kItemRows;
-  }
-  if (bad && blockIdx.x == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);
-  return __reduce_add_sync(kFull, blocks);
 }
 
 // Steps of 16 keys of tile t's value product, and whether it reads keys behind
@@ -875,8 +855,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) {
     tmem_alloc<CG>(&sm.tmem, kTmemCols);
   } else if (warp == kClaimWarp) {
-    const int blocks = count_blocks<M>(a);
-    if ((tid & 31) == 0) sm.blocks = blocks;
+    bool bad;
+    const int blocks = count_blocks(a.starts, a.rows, nullptr, 0, a.reqs, a.H, Cut<M>::kItemRows, a.flags, bad);
+    if ((tid & 31) == 0) sm.blocks = blocks, sm.bad = bad;
   } else if (tid == 0) {
     for (int b = 0; b < kUnits; ++b) mbar_init(&sm.full[b], 1 + (b == 0 ? kStalledArrivals : 0));
     for (int b = 0; b < kUnits; ++b) mbar_init(&sm.empty[b], 1);
@@ -907,9 +888,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     softmax_tiles<M>(a, sm, tmem, warp, rank);
   } else if (warp == kClaimWarp) {
     const int blocks = sm.blocks;
+    const bool bad = sm.bad != 0;
     Cursor cur;
     share_out<CG>(sm.work, &sm.abort, a.flags, (int64_t)blocks * 2 * a.sm.S * a.splits, rank,
-                  [&](int64_t i) { return find_item<M>(a, sm.order, blocks, i, cur); });
+                  [&](int64_t i) { return find_item<M>(a, sm.order, blocks, bad, i, cur); });
   } else if (rank == 0) {
     issue_products<M>(a, sm, tmem);
   }
@@ -963,7 +945,7 @@ struct alignas(1024) NarrowSmem {
   uint32_t pages[kInfo];
   Order order;
   uint32_t tmem;
-  int blocks;
+  int blocks, bad;
   int abort;
 };
 static_assert(sizeof(NarrowSmem<kNarrow16>) + 1024 <= 232448 && sizeof(NarrowSmem<kNarrow32>) + 1024 <= 232448,
@@ -1341,8 +1323,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   if (warp == kNarrowMma) {
     tmem_alloc<1>(&sm.tmem, kCols);
   } else if (warp == kNarrowClaim) {
-    const int blocks = count_blocks<M>(a);
-    if ((tid & 31) == 0) sm.blocks = blocks;
+    bool bad;
+    const int blocks = count_blocks(a.starts, a.rows, nullptr, 0, a.reqs, a.H, Cut<M>::kItemRows, a.flags, bad);
+    if ((tid & 31) == 0) sm.blocks = blocks, sm.bad = bad;
   } else if (tid == 0) {
     for (int b = 0; b < kSlots; ++b) {
       mbar_init(&sm.full[b], 1 + (b == 0 ? kStalledArrivals : 0));
@@ -1375,9 +1358,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     narrow_load<M>(a, sm, &tm_q, &tm_k);
   } else if (warp == kNarrowClaim) {
     const int blocks = sm.blocks;
+    const bool bad = sm.bad != 0;
     Cursor cur;
     share_out<1>(sm.work, &sm.abort, a.flags, (int64_t)blocks * a.sm.S * a.splits, 0u,
-                 [&](int64_t i) { return find_item<M>(a, sm.order, blocks, i, cur); });
+                 [&](int64_t i) { return find_item<M>(a, sm.order, blocks, bad, i, cur); });
   } else {
     narrow_products<M>(a, sm, tmem);
   }

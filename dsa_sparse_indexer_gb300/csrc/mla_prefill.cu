@@ -95,6 +95,7 @@ struct alignas(1024) PrefillSmem {
   Order order;
   uint32_t tmem;
   int blocks;                                // query blocks of all sequences
+  int bad;                                   // cu_q or cu_k is not ascending inside its rows
   int abort;
 };
 static_assert(sizeof(PrefillSmem) + 1024 <= 232448, "shared memory of a CTA");
@@ -113,12 +114,6 @@ struct PrefillArgs {
   uint32_t negate;
 };
 
-// Sequence i's rows of an array of T rows, kept inside it.
-__device__ __forceinline__ void bounds_of(const int32_t* cu, int i, int T, int& first, int& end) {
-  first = min(max(__ldg(cu + i), 0), T);
-  end = min(max(__ldg(cu + i + 1), first), T);
-}
-
 __device__ __forceinline__ int end_of(const Item& it, int g) { return g == 0 ? it.end[0] : it.end[1]; }
 
 struct Cursor {               // where the last item's sequence was found
@@ -129,7 +124,7 @@ struct Cursor {               // where the last item's sequence was found
 // keys and values stay in L2 together; within one, a sequence's longest blocks
 // (its last) come first, so that the CTAs, which claim items, end alike.
 template <int CG>
-__device__ __forceinline__ Item find_item(const PrefillArgs& a, const Order& order, int blocks,
+__device__ __forceinline__ Item find_item(const PrefillArgs& a, const Order& order, int blocks, bool bad,
                                           int64_t index, Cursor& c) {
   constexpr int kGroup = Shape<CG>::kGroup, kBlockQ = Shape<CG>::kBlockQ;
   const int lane = threadIdx.x & 31;
@@ -147,7 +142,7 @@ __device__ __forceinline__ Item find_item(const PrefillArgs& a, const Order& ord
   for (int base = c.seq;; base += 32) {
     const int i = base + lane;
     int first = 0, end = 0;
-    if (i < a.n) bounds_of(a.cu_q, in_order(order, a.ordered, i), a.Tq, first, end);
+    if (i < a.n) bounds_of(a.cu_q, in_order(order, a.ordered, i), a.Tq, bad, first, end);
     const int mine = (end - first + kBlockQ - 1) / kBlockQ;
     int incl = mine;
 #pragma unroll
@@ -169,8 +164,8 @@ __device__ __forceinline__ Item find_item(const PrefillArgs& a, const Order& ord
   }
   int q0, q1, k0, k1;
   const int seq = in_order(order, a.ordered, c.seq);
-  bounds_of(a.cu_q, seq, a.Tq, q0, q1);
-  bounds_of(a.cu_k, seq, a.Tk, k0, k1);
+  bounds_of(a.cu_q, seq, a.Tq, bad, q0, q1);
+  bounds_of(a.cu_k, seq, a.Tk, bad, k0, k1);
   const int at = (nb - 1 - local) * kBlockQ;
   it.row0 = q0 + at;
   it.rows = min(kBlockQ, q1 - it.row0);
@@ -630,20 +625,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) {
     tmem_alloc<CG>(&sm.tmem, kTmemCols);
   } else if (warp == kClaimWarp) {
-    // Query blocks of all sequences; bad bounds are flagged once a call.
-    const int lane = tid & 31;
-    int blocks = 0;
-    bool bad = false;
-    for (int i = lane; i < a.n; i += 32) {
-      int q0, q1, k0, k1;
-      bounds_of(a.cu_q, i, a.Tq, q0, q1);
-      bounds_of(a.cu_k, i, a.Tk, k0, k1);
-      bad |= q0 != a.cu_q[i] || q1 != a.cu_q[i + 1] || k0 != a.cu_k[i] || k1 != a.cu_k[i + 1];
-      blocks += (q1 - q0 + Sh::kBlockQ - 1) / Sh::kBlockQ;
-    }
-    blocks = __reduce_add_sync(kFull, blocks);
-    if (bad && blockIdx.x == 0) raise_flag(a.flags, DSA_FLAG_BOUNDS);
-    if (lane == 0) sm.blocks = blocks;
+    bool bad;
+    const int blocks = count_blocks(a.cu_q, a.Tq, a.cu_k, a.Tk, a.n, 1, Sh::kBlockQ, a.flags, bad);
+    if ((tid & 31) == 0) sm.blocks = blocks, sm.bad = bad;
   } else if (tid == 0) {
     for (int g = 0; g < 2; ++g) {
       mbar_init(&sm.qfull[g], 1);
@@ -676,9 +660,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_tiles<CG>(a, sm, &tm_q, &tm_k, &tm_pe, &tm_v, rank);
     } else if (warp == kClaimWarp) {
       const int blocks = sm.blocks;
+      const bool bad = sm.bad != 0;
       Cursor cur;
       share_out<CG>(sm.work, &sm.abort, a.flags, (int64_t)blocks * a.H * a.splits, rank,
-                    [&](int64_t i) { return find_item<CG>(a, sm.order, blocks, i, cur); });
+                    [&](int64_t i) { return find_item<CG>(a, sm.order, blocks, bad, i, cur); });
     } else if (rank == 0) {
       issue_products<CG, BF16>(a, sm, tmem, warp - kMmaWarp);
     }

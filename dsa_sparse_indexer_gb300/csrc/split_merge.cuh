@@ -19,8 +19,8 @@ struct MergeArgs {
   const float* l;            // [parts][rows]
   int parts;
   int64_t rows;              // outer * per_outer * H
-  // Rows of entries outside [bounds[0], bounds[n]) are left as they are; entry
-  // = row / H mod per_outer.
+  // Rows of entries below bounds[0], or not below any, are left as they are; entry = row
+  // / H mod per_outer.
   const int32_t* bounds;
   int n, per_outer, H;
   void* out;                 // [rows][D], 16-bit floats
@@ -42,8 +42,13 @@ __global__ void __launch_bounds__(kGroups * MergeCut<D, kGroups>::kLanes) merge_
   __shared__ float4 sums[kGroups - 1][kLanes];
   const int64_t row = blockIdx.x / kBlocks;
   const int entry = (int)((row / a.H) % a.per_outer);
-  if (entry < __ldg(a.bounds) || entry >= __ldg(a.bounds + a.n)) return;
   const int tid = threadIdx.x, group = tid / kLanes;
+  if (entry < __ldg(a.bounds)) return;
+  if (entry >= __ldg(a.bounds + a.n)) {      // of no sequence, unless bounds descend
+    bool below = false;
+    for (int i = tid; i < a.n; i += blockDim.x) below |= __ldg(a.bounds + i) > entry;
+    if (!__syncthreads_or(below)) return;
+  }
   const int at = (int)(blockIdx.x % kBlocks) * kLanes + tid % kLanes;
   float lse = 0.f;
   if (tid < 32) {                            // the first warp: weights and their sum

@@ -387,6 +387,45 @@ __device__ __forceinline__ void item_done(WorkSlots<Item>& s, uint32_t n) {
   if ((threadIdx.x & 31) == 0) mbar_arrive1(&s.empty[n & 1u]);
 }
 
+// Entries i and i + 1 of ascending bounds cu[0 .. n] of T rows; of others (`bad`) each
+// taken as the nearest inside the rows that is not below one before it, so that no row
+// is in two sequences.
+__device__ __forceinline__ void bounds_of(const int32_t* cu, int i, int T, bool bad, int& first, int& end) {
+  first = min(max(__ldg(cu + i), 0), T);
+  if (bad)
+    for (int j = 0; j < i; ++j) first = max(first, min(__ldg(cu + j), T));
+  end = min(max(__ldg(cu + i + 1), first), T);
+}
+// Warp-wide: how many blocks of up to `size` the rows of n sequences make, `times` of
+// them a row; whether bounds (cu's, or those of `more`) are bad, flagged once a call.
+__device__ __forceinline__ int count_blocks(const int32_t* cu, int T, const int32_t* more, int T_more, int n,
+                                            int times, int size, uint32_t* flags, bool& bad) {
+  const int lane = threadIdx.x & 31;
+  int blocks = 0;
+  bad = false;
+  for (int i = lane; i < n; i += 32) {
+    int first, end;
+    bounds_of(cu, i, T, false, first, end);
+    bad |= first != __ldg(cu + i) || end != __ldg(cu + i + 1);
+    blocks += ((end - first) * times + size - 1) / size;
+    if (more) {
+      bounds_of(more, i, T_more, false, first, end);
+      bad |= first != __ldg(more + i) || end != __ldg(more + i + 1);
+    }
+  }
+  bad = __any_sync(kFull, bad);
+  if (bad) {
+    if (blockIdx.x == 0 && lane == 0) raise_flag(flags, DSA_FLAG_BOUNDS);
+    blocks = 0;
+    for (int i = lane; i < n; i += 32) {
+      int first, end;
+      bounds_of(cu, i, T, true, first, end);
+      blocks += ((end - first) * times + size - 1) / size;
+    }
+  }
+  return __reduce_add_sync(kFull, blocks);
+}
+
 // Sixteen registers' uses are not scheduled before the wait for a load of them: empty
 // statements name them as read and written.
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
