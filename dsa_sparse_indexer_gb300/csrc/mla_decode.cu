@@ -411,6 +411,9 @@ __device__ __forceinline__ void load_tiles(const DecodeArgs& a, DecodeSmem<M>& s
       }
     }
   }
+  // The products' arrivals come to both CTAs of a pair: the second, which waits for few
+  // of them, sees the last before it ends.
+  if (CG == 2 && !leader) wait_landed(&sm.drain, 0);
   __syncwarp();
 }
 
@@ -897,12 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) {
-    // The products' arrivals come to both CTAs: the second sees the last of them too.
-    if (rank == 1 && warp == kMmaWarp && !wait_landed(&sm.drain, 0)) raise_flag(a.flags, DSA_FLAG_TIMEOUT);
-    __syncwarp();
-    pair_sync();                             // neither CTA's memory goes while the other uses it
-  }
+  if constexpr (CG == 2) pair_sync();        // neither CTA's memory goes while the other uses it
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_free<CG>(tmem, kTmemCols);

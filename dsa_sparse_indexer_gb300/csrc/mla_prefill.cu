@@ -295,6 +295,12 @@ __device__ __forceinline__ void load_tiles(const PrefillArgs& a, PrefillSmem& sm
     for (uint32_t k = tails > 2 ? tails - 2 : 0; k < tails; ++k)
       mbar_wait(&sm.vtail[k & 1u], (k >> 1) & 1u);
   }
+  // The products' arrivals come to both CTAs of a pair: the second, which waits for few
+  // of them, sees the last before it ends.
+  if (CG == 2 && rank == 1) {
+    wait_landed(&sm.drain[0], 0);
+    wait_landed(&sm.drain[1], 0);
+  }
   __syncwarp();
 }
 
@@ -673,13 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) {
-    // The products' arrivals come to both CTAs: the second sees the last of them too.
-    for (int g = 0; rank == 1 && warp == kMmaWarp && g < 2; ++g)
-      if (!wait_landed(&sm.drain[g], 0)) raise_flag(a.flags, DSA_FLAG_TIMEOUT);
-    __syncwarp();
-    pair_sync();                             // neither CTA's memory goes while the other uses it
-  }
+  if constexpr (CG == 2) pair_sync();        // neither CTA's memory goes while the other uses it
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_free<CG>(tmem, kTmemCols);
