@@ -27,6 +27,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "regions.h"
 
 namespace dsa {
 namespace {
@@ -406,6 +407,11 @@ extern "C" dsa_status dsa_indexer_key_insert(const uint16_t* k, int64_t k_token,
       !aligned(k_cache, 16) || !aligned(positions, 4) || !aligned(cos_sin_cache, 4) ||
       !aligned(slot_mapping, 4) || (T > 1 && (k_token < 0 || k_token % 8)))
     return DSA_ERR_INVALID_ARG;
+  if (!apart({bytes_of(k_cache, S * n_slots * kDim)},
+             {rows_of(k, T, k_token, 1, 0, kDim, 2), bytes_of(norm_weight, kDim * 4), bytes_of(norm_bias, kDim * 4),
+              bytes_of(positions, (int64_t)T * 4), bytes_of(cos_sin_cache, (int64_t)max_pos * rot_dim * 4),
+              bytes_of(slot_mapping, (int64_t)S * T * 4)}))
+    return DSA_ERR_INVALID_ARG;
   const KeyArgs a{reinterpret_cast<const __nv_bfloat16*>(k), T > 1 ? k_token : 0, norm_weight, norm_bias, eps,
                   {positions, cos_sin_cache, max_pos, rot_dim, first, layout, err_flags},
                   slot_mapping, T, S, n_slots, k_cache};
@@ -435,9 +441,15 @@ extern "C" dsa_status dsa_indexer_query_fp8(const uint16_t* q, int64_t q_token, 
   QueryArgs a{reinterpret_cast<const __nv_bfloat16*>(q), T > 1 ? q_token : 0, H > 1 ? q_head : 0, weights, factor,
               {positions, cos_sin_cache, max_pos, rot_dim, first, layout, err_flags},
               T, H, 0, q_out, weights_out};
-  if ((int64_t)T * H > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  const int64_t heads = (int64_t)T * H;
+  if (heads > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  const Region w = weights_out == weights ? Region{} : bytes_of(weights, heads * 4);   // in place, or apart
+  if (!apart({bytes_of(q_out, heads * kDim), bytes_of(weights_out, heads * 4)},
+             {rows_of(q, T, q_token, H, q_head, kDim, 2), w, bytes_of(positions, (int64_t)T * 4),
+              bytes_of(cos_sin_cache, (int64_t)max_pos * rot_dim * 4)}))
+    return DSA_ERR_INVALID_ARG;
   const int part = partner_of(rot_dim, first, layout);
-  const bool few = (int64_t)T * H < 65536;
+  const bool few = heads < 65536;
   const cudaError_t e = part == kInLane    ? launch_query<kInLane>(a, few, stream)
                         : part == kLaneOff ? launch_query<kLaneOff>(a, few, stream)
                                            : launch_query<kAnywhere>(a, few, stream);

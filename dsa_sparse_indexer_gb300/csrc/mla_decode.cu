@@ -39,6 +39,7 @@
 #include <algorithm>
 #include <numeric>
 
+#include "regions.h"
 #include "split_merge.cuh"
 
 namespace dsa {
@@ -1462,6 +1463,13 @@ extern "C" dsa_status dsa_mla_decode(const uint16_t* q, const uint16_t* kv_cache
   const int64_t cap = table_tokens(max_blocks, block_size);
   Plan p = plan_for(rows, S, H, reqs, cap);
   if (!work) p.splits = 1;
+  const int64_t outs = S * pairs;
+  if (!apart({bytes_of(out, outs * kDv * 2), bytes_of(lse2, outs * 4),
+              bytes_of(p.splits > 1 ? work : nullptr, p.splits * outs * (kDv + 1) * 4)},
+             {bytes_of(q, pairs * kDqk * 2), bytes_of(kv_cache, S * n_slots * kDqk * 2),
+              bytes_of(block_table, (int64_t)S * reqs * max_blocks * 4), bytes_of(query_starts, ((int64_t)reqs + 1) * 4),
+              bytes_of(seq_lens, (int64_t)reqs * 4), bytes_of(tree_mask, (int64_t)rows * mask_words * 4)}))
+    return DSA_ERR_INVALID_ARG;
   DecodeArgs a{reinterpret_cast<const __nv_bfloat16*>(q), block_table, query_starts, seq_lens, tree_mask, reinterpret_cast<__nv_bfloat16*>(out),
                lse2, nullptr, nullptr, err_flags, n_slots, reqs, max_blocks, block_size, rows, H,
                mask_words, p.splits, p.ordered, (int)cap, std::min(block_size, 64), std::min(block_size, (int)Shape<kPair>::kVKeys),

@@ -32,6 +32,7 @@
 // 16384 keys: 79 us, 1.05 PFLOP/s, its keys in parts.
 #include <algorithm>
 
+#include "regions.h"
 #include "split_merge.cuh"
 
 namespace dsa {
@@ -756,6 +757,15 @@ extern "C" dsa_status dsa_mla_prefill(const void* q, int64_t q_token, int64_t q_
       !strides_fit(pe_token, kDr, Tk, 1, kDr) || !strides_fit(v_token, v_head, Tk, H, kDv))
     return DSA_ERR_INVALID_ARG;
   if (((int64_t)Tq / Shape<1>::kBlockQ + n) * H > ((int64_t)1 << 26)) return DSA_ERR_UNSUPPORTED;
+  const Plan p = plan_for(Tq, Tk, n, H);
+  const int splits = work ? p.splits : 1;
+  const int64_t all = (int64_t)Tq * H;
+  if (!apart({bytes_of(out, all * kDv * 2), bytes_of(lse2, all * 4),
+              bytes_of(splits > 1 ? work : nullptr, splits * all * (kDv + 1) * 4)},
+             {rows_of(q, Tq, q_token, H, q_head, kDn + kDr, 2), rows_of(k_nope, Tk, k_token, H, k_head, kDn, 2),
+              rows_of(k_pe, Tk, pe_token, 1, 0, kDr, 2), rows_of(v, Tk, v_token, H, v_head, kDv, 2),
+              bytes_of(cu_q, ((int64_t)n + 1) * 4), bytes_of(cu_k, ((int64_t)n + 1) * 4)}))
+    return DSA_ERR_INVALID_ARG;
   const bool bf16 = dtype == DSA_BF16;
   if (Tk == 0) k_nope = k_pe = v = q;        // never read
   // A dimension of one row has no stride of its own.
@@ -765,7 +775,6 @@ extern "C" dsa_status dsa_mla_prefill(const void* q, int64_t q_token, int64_t q_
     const uint64_t ts = T > 1 ? (uint64_t)token * 2 : hs * heads;
     return encode_map16(m, p, bf16, width, heads, std::max(T, 1), hs, ts, 1, rows);
   };
-  const Plan p = plan_for(Tq, Tk, n, H);
   const uint32_t keys = (uint32_t)(kTileK / p.cg);
   CUtensorMap tm_q, tm_k, tm_pe, tm_v;
   if (!map(&tm_q, q, kDn + kDr, H, Tq, q_token, q_head, kTileQ) ||
@@ -774,7 +783,6 @@ extern "C" dsa_status dsa_mla_prefill(const void* q, int64_t q_token, int64_t q_
                     (uint64_t)(Tk > 1 ? pe_token : kDr) * 2 * std::max(Tk, 1), keys, 1) ||
       !map(&tm_v, v, kDv, H, Tk, v_token, v_head, kVKeys))
     return DSA_ERR_CUDA;
-  const int splits = work ? p.splits : 1;
   // Heads whose keys and values (512 bytes a token and head) fit half of L2.
   const int64_t fit = ((int64_t)48 << 20) / (512 * (int64_t)std::max(Tk, 1));
   PrefillArgs a{cu_q, cu_k, out, lse2, nullptr, nullptr, err_flags, n, Tq, Tk, H,

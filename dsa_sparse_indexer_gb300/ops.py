@@ -606,7 +606,8 @@ def mla_prefill(q, k_nope, k_pe, v, cu_q, cu_k, scale: float, causal: bool = Tru
     no sequence are left as they are.  Outputs over parts of a context, stacked
     [parts, Tq, H, 128] and [parts, Tq, H], are lse_combine's input (bf16).
     work: fp32 workspace of calls with few queries, dsa_mla_prefill_work(Tq, Tk,
-    n, H) bytes (allocated when not given).  Autograd does not see the call."""
+    n, H) bytes (allocated when not given).  Outputs that overlap an input are
+    refused.  Autograd does not see the call."""
     dtype = q.dtype if isinstance(q, torch.Tensor) else None
     if dtype is not None and dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"q must be bf16 or fp16, got {dtype}")
@@ -665,7 +666,8 @@ def mla_decode(q, kv_cache, block_table, block_size: int, query_starts, seq_lens
     bf16, lse2 [S, rows, H] fp32, base 2) for lse_combine; rows of no request are
     left as they are.  work: fp32 workspace of calls with few rows,
     dsa_mla_decode_work(rows, S, H, reqs, max_blocks, block_size) bytes (allocated
-    when not given).  Autograd does not see the call."""
+    when not given).  Outputs that overlap an input are refused.  Autograd does
+    not see the call."""
     _need(q, "q", torch.bfloat16, 3)
     _need(kv_cache, "kv_cache", torch.bfloat16, 3)
     _need(block_table, "block_table", torch.int32, 3)
@@ -756,7 +758,7 @@ def indexer_query_fp8(q, weights, positions, cos_sin_cache, factor: float = 1.0,
     and heads may be strided) turned like indexer_key_insert's keys and held as
     e4m3 codes with a power-of-two scale a head, which goes into weights [T, H]
     fp32 together with factor.  Returns (q_out [T, H, 128] uint8, weights_out
-    [T, H] fp32)."""
+    [T, H] fp32), which must not overlap the inputs; weights_out may be weights."""
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {list(ROPE_LAYOUTS)}, got {layout!r}")
     q_token, q_head = _rows_of(q, "q", torch.bfloat16)

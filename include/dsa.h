@@ -599,7 +599,8 @@ int64_t dsa_sparse_mla_decode_fp8_work(int rows, int S, int H, int K);
  * outside it may be anything.
  * Enqueues two kernels when the keys are split, else one.
  * Errors: negative sizes, H < 1, scale not finite, another dtype, null pointers,
- *         misalignment, strides -> INVALID_ARG; more than 2^26 blocks of 256
+ *         misalignment, strides, outputs or a workspace in use that overlap one
+ *         another or an input (the span of its rows) -> INVALID_ARG; more than 2^26 blocks of 256
  *         queries (times heads) -> UNSUPPORTED; tensor-map encoding -> CUDA.
  */
 dsa_status dsa_mla_prefill(const void* q, int64_t q_token, int64_t q_head, const void* k_nope,
@@ -648,7 +649,8 @@ int64_t dsa_mla_prefill_work(int Tq, int Tk, int n, int H);
  * Enqueues two kernels when tokens are split, else one.
  * Errors: negative sizes, H < 1, n_slots < 1, max_blocks < 1, block_size < 1,
  *         mask_words < 1 with a mask, scale not finite, null pointers,
- *         misalignment -> INVALID_ARG; S not in [1, 64], I < 1, I*S > INT32_MAX,
+ *         misalignment, outputs or a workspace in use that overlap one another
+ *         or an input -> INVALID_ARG; S not in [1, 64], I < 1, I*S > INT32_MAX,
  *         block_size not 16, 32 or a multiple of 64, n_slots > 2^31 - 1, rows * H
  *         or S * reqs > 2^30, too many CTAs -> UNSUPPORTED; tensor-map encoding
  *         -> CUDA.
@@ -684,8 +686,8 @@ int64_t dsa_mla_decode_work(int rows, int S, int H, int reqs, int max_blocks, in
  *                is not turned) or a slot is >= n_slots (skipped)
  * Errors: T < 0, n_slots < 1, eps negative or not finite, max_pos < 1, rot_dim odd
  *         or < 2, the turning part outside [0, DSA_IDX_DIM), an unknown layout,
- *         null pointers, misalignment -> INVALID_ARG; S not in [1, 64] ->
- *         UNSUPPORTED.
+ *         null pointers, misalignment, a cache that overlaps another argument ->
+ *         INVALID_ARG; S not in [1, 64] -> UNSUPPORTED.
  */
 dsa_status dsa_indexer_key_insert(const uint16_t* k, int64_t k_token, const float* norm_weight,
                                   const float* norm_bias, float eps, const int32_t* positions,
@@ -713,7 +715,8 @@ dsa_status dsa_indexer_key_insert(const uint16_t* k, int64_t k_token, const floa
  *   q_out        [T][H][DSA_IDX_DIM] e4m3 codes, 16-byte aligned; weights_out
  *                [T][H] fp32 (may be weights itself)
  * Errors: T < 0, H < 1, factor not finite, the rotation's as above, null pointers,
- *         misalignment -> INVALID_ARG; T * H >= 2^31 -> UNSUPPORTED.
+ *         misalignment, outputs that overlap one another or an input (but for
+ *         weights_out on weights) -> INVALID_ARG; T * H >= 2^31 -> UNSUPPORTED.
  */
 dsa_status dsa_indexer_query_fp8(const uint16_t* q, int64_t q_token, int64_t q_head,
                                  const float* weights, float factor, const int32_t* positions,
