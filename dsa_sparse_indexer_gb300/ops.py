@@ -10,6 +10,7 @@ from __future__ import annotations
 import functools
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 
@@ -456,6 +457,7 @@ def rotary_embed(x, positions, cos_sin_cache, layout: str = "interleaved", first
         raise ValueError("x and out must not require grad: rotary_embed is not recorded by "
                          "autograd (call it under torch.no_grad(), with inverse=True on the "
                          "gradient in the backward pass)")
+    _no_grad(x, out)
     context = _together(x, positions, cos_sin_cache, out, err_flags)
     _launch(context, "dsa_rotary_embed", _ptr(x), x_token, x_head, _ptr(positions),
             _ptr(cos_sin_cache), cos_sin_cache.shape[0], cos_sin_cache.shape[1], first, T, H, D,
@@ -571,6 +573,10 @@ def _no_grad(*tensors):
             if t is not None and t.requires_grad:
                 raise ValueError("no tensor may require grad: this call is not recorded by autograd "
                                  "(call it under torch.no_grad())")
+    if forward_ad._current_level >= 0:           # within a forward_ad.dual_level
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError("no tensor may carry a tangent: this call has no forward derivative")
 
 
 def _changed(*outs):
