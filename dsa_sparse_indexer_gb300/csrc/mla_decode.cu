@@ -30,9 +30,9 @@
 // split into parts that a second kernel joins.
 // Measured, 64 requests of 8192 to 16384 tokens on 4 shards, 128 heads: one token
 // 360 us (219 GFLOP, 949 MB; scores of both halves and the 64-key tiles' products
-// take 2.2 us of the 4.7 a tile and half), a tree of eight 1450 us (1.05 PFLOP/s of
-// the work, 1.6 of what is issued: tensor pipes 68 % busy); one sequence of 32768,
-// one token, 28 us.
+// take 2.2 us of the 4.7 a tile and half), a tree of eight 1465 us after a pause (1.05
+// PFLOP/s of the work, 1.6 of what is issued: tensor pipes 68 % busy) and 1550 to 1590
+// one after another, at the power limit; one sequence of 32768, one token, 32 us.
 // The tail of a sequence's last page holds anything: its values are zeroed in
 // shared memory up to the 16 keys that a product step reads, its scores masked.
 // Every wait is bounded and raises DSA_FLAG_TIMEOUT when it runs out.
@@ -1375,7 +1375,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
 
 constexpr int kNarrowMost = 32;
 // How a call is cut: by the rows of a request (on average), and its keys into parts
-// where items are few.  Lengths are the device's: the table's width stands for them.
+// where items are few.  Lengths are the device's: the table's width stands for them, and
+// one wider than the sequences makes parts that are not needed: the 64 requests below
+// with 128 heads 354 us, 472 with a table of 65536 tokens or more (two parts); 64 of
+// 2000 tokens on one shard 63, 138 with one of 32768 or more (seven).
 // Rows of 64 requests, 8192 to 16384 tokens on 4 shards, in us: Narrow of 16 against
 // 32 rows an item 201 / 227 (16 rows); Narrow against Wide 201 / 354 (16), 238 / 376
 // (32), two items of it 397 / 392 (48), 413 / 410 (64), three 519 / 385 (96); Wide

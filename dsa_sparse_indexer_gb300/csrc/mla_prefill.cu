@@ -26,10 +26,11 @@
 // 2^7 larger so that few are subnormal, by 2^-11 of itself or 2^-32 of the
 // reference's weight.  That is 1 or 2^7, and exact.
 // Every wait is bounded and raises DSA_FLAG_TIMEOUT when it runs out.
-// Measured, one sequence of 8192, 128 heads, causal: 1720 us, 1.60 PFLOP/s of the
-// 1.96 that a library product reaches; 3753 with one CTA an item, a warp issuing
-// for both query tiles and a thread a row in the softmax.  16 heads, 500 queries of
-// 16384 keys: 79 us, 1.05 PFLOP/s, its keys in parts.
+// Measured, one sequence of 8192, 128 heads, causal: 1740 us after a pause (2070 MHz),
+// 1.58 PFLOP/s of the 1.96 that a library product reaches, 1840 to 1900 one after
+// another at the power limit (1867 to 1912 MHz); 3753 with one CTA an item, a warp
+// issuing for both query tiles and a thread a row in the softmax.  16 heads, 500
+// queries of 16384 keys: 80 us, 1.03 PFLOP/s, its keys in parts.
 #include <algorithm>
 
 #include "regions.h"
@@ -693,6 +694,9 @@ constexpr int kSmem = (int)sizeof(PrefillSmem) + 1024;
 // Pairs against single CTAs, in us: one sequence of 8192 queries, 128 heads 1712 /
 // 2214; 4096, 32 heads 281 / 358; 2048, 128 heads 167 / 204; eight of 1024, 32 heads
 // 127 / 132; 16 of 512 (just a pair's item) 91 / 88.
+// Bounds are the device's: means stand for them, in which empty sequences count.  A
+// chunk of 500 queries of 16384 keys, 16 heads, is cut for 78 us alone; in a batch of
+// eight or more whose others are empty, as single CTAs without parts, for 333.
 struct Plan {
   int cg, splits, ordered;
 };
