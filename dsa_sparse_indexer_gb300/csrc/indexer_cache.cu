@@ -53,8 +53,14 @@ struct Turn {
   float c[kVals], s[kVals];
   int off;                                   // kLaneOff: the partner's lane
   bool any;                                  // one of the eight turns (kLaneOff: all or none do)
+  uint32_t turning;                          // the others: bit e, value e turns
   int partner[P == kAnywhere ? kVals : 1];   // kAnywhere: its place in the row
 };
+
+template <int P>
+__device__ __forceinline__ bool turns_at(const Turn<P>& t, int e) {
+  return P == kLaneOff ? t.any : (t.turning >> e) & 1u;
+}
 
 template <int P>
 __device__ __forceinline__ Turn<P> find_turn(const TurnArgs& a, int token, int lane16) {
@@ -66,6 +72,7 @@ __device__ __forceinline__ Turn<P> find_turn(const TurnArgs& a, int token, int l
   const int half = a.rot / 2, i0 = lane16 * kVals - a.first;   // the first value's place among the turning
   t.off = lane16;
   t.any = in && i0 + kVals > 0 && i0 < a.rot;
+  t.turning = 0u;
   if (P == kLaneOff && i0 >= 0 && i0 < a.rot) t.off = lane16 + (i0 < half ? half : -half) / kVals;
 #pragma unroll
   for (int e = 0; e < kVals; ++e) {
@@ -74,6 +81,7 @@ __device__ __forceinline__ Turn<P> find_turn(const TurnArgs& a, int token, int l
     t.s[e] = 0.f;
     if (P == kAnywhere) t.partner[e] = lane16 * kVals + e;
     if (!in || i < 0 || i >= a.rot) continue;
+    t.turning |= 1u << e;
     const bool inter = P == kInLane || (P == kAnywhere && a.layout == DSA_ROPE_INTERLEAVED);
     const bool second = inter ? (i & 1) != 0 : i >= half;
     const int pair = inter ? i >> 1 : (second ? i - half : i);
@@ -131,7 +139,7 @@ __device__ __forceinline__ void partners(const Turn<P>& t, float* row, int lane1
 // Value e of the row, turned; a carried one as it is (its partner may be infinite).
 template <int P>
 __device__ __forceinline__ float turned(const Turn<P>& t, int e, float x, float p) {
-  const bool turns = P == kLaneOff ? t.any : t.s[e] != 0.f || t.c[e] != 1.f;
+  const bool turns = turns_at(t, e);
   const float y = fmaf(x, t.c[e], p * t.s[e]);
   return turns ? y : x;
 }
@@ -142,7 +150,7 @@ __device__ __forceinline__ float turned(const Turn<P>& t, int e, float x, float 
 // shows an infinity where this is NaN.
 template <int P>
 __device__ __forceinline__ float turned_close(const Turn<P>& t, int e, float x, float p, float& y) {
-  const bool turns = P == kLaneOff ? t.any : t.s[e] != 0.f || t.c[e] != 1.f;
+  const bool turns = turns_at(t, e);
   const float b = __fmul_rn(p, t.s[e]);
   const float v = __fmaf_rn(x, t.c[e], b);
   y = turns ? v : x;
@@ -239,7 +247,7 @@ __device__ __forceinline__ float power(int exponent_field) { return __uint_as_fl
 // (its errors would be NaN).
 template <int P>
 __device__ __forceinline__ float turned_to_odd(const Turn<P>& t, int e, float x, float p) {
-  const bool turns = P == kLaneOff ? t.any : t.s[e] != 0.f || t.c[e] != 1.f;
+  const bool turns = turns_at(t, e);
   if (!turns) return x;
   const float a = __fmul_rn(x, t.c[e]), b = __fmul_rn(p, t.s[e]);
   const float ea = __fmaf_rn(x, t.c[e], -a), eb = __fmaf_rn(p, t.s[e], -b);

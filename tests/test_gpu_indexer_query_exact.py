@@ -147,3 +147,14 @@ def test_a_chunk_of_heads():
         q = bf16(rng.standard_normal((1024, 64, 128)))
         w = rng.standard_normal((1024, 64)).astype(np.float32)
         check(q, np.arange(start, start + 1024), table, "half", 0, w)
+
+
+@pytest.mark.parametrize("layout,rot,first", TURNS)
+def test_infinities_at_position_0(layout, rot, first):
+    """Position 0 turns by the table's row like any other: beside an infinity a value
+    times a sine of 0 is NaN in every layout, and no part of the scale."""
+    table = RO.table(3, rot, 1e4).astype(np.float32)
+    a, b = pairs_of(layout, rot, first)[-1]
+    q = bf16(np.random.default_rng(5).standard_normal((3, 4, 128)))
+    q[:, 0, a], q[:, 1, b], q[:, 2, b], q[:, 2, a], q[:, 3, 17] = INF, -INF, INF, 1000.0, INF
+    check(q, [0, 1, 0], table, layout, first)
