@@ -612,8 +612,9 @@ def mla_prefill(q, k_nope, k_pe, v, cu_q, cu_k, scale: float, causal: bool = Tru
     no sequence are left as they are.  Outputs over parts of a context, stacked
     [parts, Tq, H, 128] and [parts, Tq, H], are lse_combine's input (bf16).
     work: fp32 workspace of calls with few queries, dsa_mla_prefill_work(Tq, Tk,
-    n, H) bytes (allocated when not given).  Outputs that overlap an input are
-    refused.  Autograd does not see the call."""
+    n, H) bytes (allocated when not given).  The call is cut by the sequences' mean
+    sizes: leave empty ones out where they are many.  Outputs that overlap an input
+    are refused.  Autograd does not see the call."""
     dtype = q.dtype if isinstance(q, torch.Tensor) else None
     if dtype is not None and dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"q must be bf16 or fp16, got {dtype}")
@@ -672,8 +673,9 @@ def mla_decode(q, kv_cache, block_table, block_size: int, query_starts, seq_lens
     bf16, lse2 [S, rows, H] fp32, base 2) for lse_combine; rows of no request are
     left as they are.  work: fp32 workspace of calls with few rows,
     dsa_mla_decode_work(rows, S, H, reqs, max_blocks, block_size) bytes (allocated
-    when not given).  Outputs that overlap an input are refused.  Autograd does
-    not see the call."""
+    when not given).  The call is cut by the table's width: give it no more
+    columns than the sequences need.  Outputs that overlap an input are refused.
+    Autograd does not see the call."""
     _need(q, "q", torch.bfloat16, 3)
     _need(kv_cache, "kv_cache", torch.bfloat16, 3)
     _need(block_table, "block_table", torch.int32, 3)

@@ -597,7 +597,9 @@ int64_t dsa_sparse_mla_decode_fp8_work(int rows, int S, int H, int K);
  * more).  Keys that a query does not see may hold anything; values of a sequence's
  * own keys are to be finite (a weight of 0 times an infinity is NaN), what lies
  * outside it may be anything.
- * Enqueues two kernels when the keys are split, else one.
+ * Enqueues two kernels when the keys are split, else one.  A call is cut into CTAs
+ * by the means of Tq and Tk over n (the bounds are the device's): empty sequences
+ * in n cost time where they are many.
  * Errors: negative sizes, H < 1, scale not finite, another dtype, null pointers,
  *         misalignment, strides, outputs or a workspace in use that overlap one
  *         another or an input (the span of its rows) -> INVALID_ARG; more than 2^26 blocks of 256
@@ -646,7 +648,9 @@ int64_t dsa_mla_prefill_work(int Tq, int Tk, int n, int H);
  * Scores and sums are fp32; a softmax weight enters the value product as bf16.
  * Cache rows of a request's own tokens are to be finite (a weight of 0 times an
  * infinity is NaN); slots behind its last token may hold anything.
- * Enqueues two kernels when tokens are split, else one.
+ * Enqueues two kernels when tokens are split, else one.  A call is cut into CTAs by
+ * max_blocks (the lengths are the device's): a table several times as wide as its
+ * sequences need costs time, and workspace, where requests are few.
  * Errors: negative sizes, H < 1, n_slots < 1, max_blocks < 1, block_size < 1,
  *         mask_words < 1 with a mask, scale not finite, null pointers,
  *         misalignment, outputs or a workspace in use that overlap one another
